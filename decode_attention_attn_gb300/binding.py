@@ -23,6 +23,7 @@ ERRORS = {0: "DA_OK", -1: "DA_ERR_INVALID_ARG", -2: "DA_ERR_UNSUPPORTED",
 DA_ERR_RANGE_TOO_WIDE = -9
 MAX_HIST_BINS = 32768
 DTYPE_CODES = {"f32": DA_F32, "f16": DA_F16, "bf16": DA_BF16}
+ROPE_CODES = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "by_index": 4}
 MODE_CODES = {"sync": DA_SOFTMAX_SYNC, "unified": DA_SOFTMAX_UNIFIED,
               "unified_local": DA_SOFTMAX_UNIFIED_LOCAL}
 
@@ -109,6 +110,83 @@ class da_run_args(ctypes.Structure):
     ]
 
 
+class da_rope_config(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int),
+        ("rotary_dim", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+        ("scaling", ctypes.c_int),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("original_max_position", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+        ("attn_factor", ctypes.c_double),
+    ]
+
+
+class da_rope_args(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("dtype", ctypes.c_int),
+        ("rows", ctypes.c_int),
+        ("heads", ctypes.c_int),
+        ("x_row_stride", ctypes.c_int64),
+        ("x_head_stride", ctypes.c_int64),
+        ("out_row_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("positions", ctypes.c_void_p),
+        ("transpose", ctypes.c_int),
+        ("cuda_stream", ctypes.c_void_p),
+    ]
+
+
+class da_kv_write_args(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_row_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_row_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("rows", ctypes.c_int),
+        ("k_cache", ctypes.c_void_p),
+        ("v_cache", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("row_offsets", ctypes.c_void_p),
+        ("start", ctypes.c_void_p),
+        ("rope", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("q", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("q_row_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("q_out_row_stride", ctypes.c_int64),
+        ("q_out_head_stride", ctypes.c_int64),
+        ("amax", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("cuda_stream", ctypes.c_void_p),
+    ]
+
+
+class da_kv_read_args(ctypes.Structure):
+    _fields_ = [
+        ("k_cache", ctypes.c_void_p),
+        ("v_cache", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("row_offsets", ctypes.c_void_p),
+        ("start", ctypes.c_void_p),
+        ("rows", ctypes.c_int),
+        ("k_out", ctypes.c_void_p),
+        ("v_out", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("cuda_stream", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 P = ctypes.c_void_p
 
@@ -144,6 +222,13 @@ def lib():
         L.decode_attn_choose_phi.argtypes = [ctypes.POINTER(ctypes.c_ulonglong), ctypes.c_int,
                                              ctypes.c_float, ctypes.c_float, ctypes.c_double,
                                              ctypes.c_float, F, F, F]
+        L.decode_attn_rope_create.argtypes = [ctypes.POINTER(da_rope_config), ctypes.POINTER(P)]
+        L.decode_attn_rope_frequencies.argtypes = [P, ctypes.POINTER(ctypes.c_double)]
+        L.decode_attn_rope_apply.argtypes = [P, ctypes.POINTER(da_rope_args)]
+        L.decode_attn_kv_write.argtypes = [P, ctypes.POINTER(da_kv_write_args)]
+        L.decode_attn_kv_read.argtypes = [P, ctypes.POINTER(da_kv_read_args)]
+        L.decode_attn_rope_destroy.argtypes = [P]
+        L.decode_attn_rope_destroy.restype = None
         L.decode_attn_destroy.argtypes = [P]
         L.decode_attn_destroy.restype = None
         L.decode_attn_strerror.argtypes = [ctypes.c_int]
@@ -154,6 +239,8 @@ def lib():
                      "decode_attn_check_status",
                      "decode_attn_debug_gather", "decode_attn_logit_histogram",
                      "decode_attn_choose_phi",
+                     "decode_attn_rope_create", "decode_attn_rope_frequencies",
+                     "decode_attn_rope_apply", "decode_attn_kv_write", "decode_attn_kv_read",
                      "decode_attn_abi_version"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -274,6 +361,36 @@ def decode_attn_choose_phi(counts, lo: float, hi: float, coverage: float = 0.999
     return phi.value, x_lo.value, x_hi.value, rc == 0
 
 
+def decode_attn_rope_create(config: da_rope_config):
+    rope = P()
+    _check(lib().decode_attn_rope_create(ctypes.byref(config), ctypes.byref(rope)),
+           "decode_attn_rope_create")
+    return rope
+
+
+def decode_attn_rope_frequencies(rope, pairs: int) -> list:
+    """The scaled frequencies (radians per position) of the handle's rotary_dim / 2 pairs."""
+    theta = (ctypes.c_double * pairs)()
+    _check(lib().decode_attn_rope_frequencies(rope, theta), "decode_attn_rope_frequencies")
+    return list(theta)
+
+
+def decode_attn_rope_apply(rope, args: da_rope_args):
+    _check(lib().decode_attn_rope_apply(rope, ctypes.byref(args)), "decode_attn_rope_apply")
+
+
+def decode_attn_rope_destroy(rope):
+    lib().decode_attn_rope_destroy(rope)
+
+
+def decode_attn_kv_write(plan, args: da_kv_write_args):
+    _check(lib().decode_attn_kv_write(plan, ctypes.byref(args)), "decode_attn_kv_write")
+
+
+def decode_attn_kv_read(plan, args: da_kv_read_args):
+    _check(lib().decode_attn_kv_read(plan, ctypes.byref(args)), "decode_attn_kv_read")
+
+
 def decode_attn_destroy(plan):
     lib().decode_attn_destroy(plan)
 
@@ -359,3 +476,236 @@ class DecodeAttention:
         if want_stats:
             return out, out_lse, row_flags, st
         return out, out_lse, row_flags
+
+
+def _device_of(**tensors):
+    """The one CUDA device of the given tensors (None entries are passed over)."""
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    return device
+
+
+def _rows_tensor(name, t, dtype, heads, d):
+    """A [rows, heads, d] tensor whose heads are contiguous (rows and heads may be strided)."""
+    if t.dtype != dtype or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or \
+            (t.stride(2) != 1 and t.numel()):
+        raise ValueError(f"{name} must be a [rows, {heads}, {d}] tensor of {dtype} whose last "
+                         "dimension is contiguous")
+
+
+def _int32(name, t, numel):
+    import torch
+    if t.dtype != torch.int32 or t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {numel} elements")
+
+
+def _stream_of(device, stream):
+    """The stream to enqueue on (the device's current one unless given), and whether the call must
+    first make that device current."""
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    return s.cuda_stream or None, torch.cuda.current_device() != device.index
+
+
+def _call(device, switch, fn, *args):
+    if not switch:
+        return fn(*args)
+    import torch
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+class Rope:
+    """A rotary embedding: its frequencies, scaled for long contexts by `scaling` ("none", "linear",
+    "ntk", "by_parts", "by_index"; see da_rope_scaling), and its layout.
+
+    apply() rotates a [rows, heads, head_dim] tensor; KVCacheIO.write() takes the handle to rotate
+    q and k on their way into the cache."""
+
+    def __init__(self, head_dim: int, rotary_dim: Optional[int] = None, interleaved: bool = False,
+                 base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original_max_position: float = 0.0, low: float = 1.0, high: float = 32.0,
+                 attn_factor: float = 1.0):
+        if scaling not in ROPE_CODES:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_CODES)}")
+        self.head_dim = head_dim
+        self.rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        self.handle = decode_attn_rope_create(da_rope_config(
+            head_dim, self.rotary_dim, int(bool(interleaved)), ROPE_CODES[scaling], base, factor,
+            original_max_position, low, high, attn_factor))
+        from .workloads import TORCH_DTYPES
+        self._codes = {TORCH_DTYPES[k]: v for k, v in DTYPE_CODES.items()}
+
+    def __del__(self):
+        handle = getattr(self, "handle", None)
+        if handle is not None and _lib is not None:
+            decode_attn_rope_destroy(handle)
+            self.handle = None
+
+    def frequencies(self) -> list:
+        return decode_attn_rope_frequencies(self.handle, self.rotary_dim // 2)
+
+    def apply(self, x, positions, out=None, transpose: bool = False, stream=None):
+        """Rows of x (fp32, fp16 or bf16; rows and heads may be strided) rotated by `positions`
+        (int32 [rows]), into `out` (x itself: in place). transpose: the transposed map, which takes
+        the gradient of the output to the gradient of x."""
+        import torch
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if x.dtype not in self._codes:
+            raise ValueError("x must be fp32, fp16 or bf16")
+        device = _device_of(x=x, positions=positions, out=out)
+        if x.dim() != 3:
+            raise ValueError("x must be a [rows, heads, head_dim] tensor")
+        rows, heads = x.shape[0], x.shape[1]
+        _rows_tensor("x", x, x.dtype, heads, self.head_dim)
+        _rows_tensor("out", out, x.dtype, heads, self.head_dim)
+        if out.shape[0] != rows:
+            raise ValueError("out must have as many rows as x")
+        _int32("positions", positions, rows)
+        if rows == 0 or heads == 0:
+            return out
+        s, switch = _stream_of(device, stream)
+        xs, os_ = x.stride(), out.stride()
+        args = da_rope_args(x.data_ptr(), out.data_ptr(), self._codes[x.dtype], rows, heads, xs[0],
+                            xs[1], os_[0], os_[1], positions.data_ptr(), int(bool(transpose)), s)
+        _call(device, switch, decode_attn_rope_apply, self.handle, args)
+        return out
+
+
+class KVCacheIO:
+    """Writes rows of K and V into a cache of the problem's shape and storage, and reads them back.
+
+    The rows of a step lie one after another, sequence by sequence: row_offsets (int32
+    [batch + 1]) says which rows are whose, start (int32 [batch]) the cache position of each
+    sequence's first row. With findings=True (or the problem's validate) the device records rows
+    without a place in the cache, which check_status() reports."""
+
+    def __init__(self, problem: da_problem, findings: bool = False, device=None):
+        import torch
+        self.problem = problem
+        self.plan, self.workspace_bytes = decode_attn_plan(problem, 0)
+        from .workloads import TORCH_DTYPES
+        names = {v: k for k, v in DTYPE_CODES.items()}
+        self._dtype = TORCH_DTYPES[names[problem.qkv_dtype]]
+        self._kv_ok = (torch.uint8, torch.float8_e4m3fn) if problem.kv_fp8 else (self._dtype,)
+        self.workspace = None
+        if findings or problem.validate:
+            device = torch.device(device) if device is not None else torch.device("cuda")
+            self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=device)
+
+    def __del__(self):
+        plan = getattr(self, "plan", None)
+        if plan is not None and _lib is not None:
+            decode_attn_destroy(plan)
+            self.plan = None
+
+    def _common(self, k_cache, v_cache, block_table, row_offsets, start):
+        pr = self.problem
+        shape = (pr.num_physical_blocks, pr.page_size, pr.num_kv_heads, pr.head_dim) if pr.paged \
+            else (pr.batch, pr.max_seq_len, pr.num_kv_heads, pr.head_dim)
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if t is not None and (t.dtype not in self._kv_ok or tuple(t.shape) != shape or
+                                  not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {shape} tensor of {self._kv_ok}")
+        if (block_table is None) == bool(pr.paged):
+            raise ValueError("a paged cache takes a block_table, a contiguous one none")
+        if block_table is not None:
+            _int32("block_table", block_table, pr.batch * pr.max_blocks_per_seq)
+        _int32("row_offsets", row_offsets, pr.batch + 1)
+        _int32("start", start, pr.batch)
+
+    def _workspace(self):
+        return (None, 0) if self.workspace is None else (self.workspace.data_ptr(),
+                                                         self.workspace_bytes)
+
+    def write(self, k, v, k_cache, v_cache, block_table, row_offsets, start, rope=None,
+              positions=None, q=None, q_out=None, amax=None, stream=None):
+        """Write the rows of k and v ([rows, H_kv, d], strided rows and heads allowed); with `rope`
+        rotate k, and q into q_out (allocated when None, q itself: in place). `positions`: rotary
+        positions other than the cache positions. `amax`: a float32 [2] tensor that takes the
+        running largest |k| and |v|. Returns q_out (None without q)."""
+        import torch
+        pr = self.problem
+        self._common(k_cache, v_cache, block_table, row_offsets, start)
+        if k_cache is None or v_cache is None:
+            raise ValueError("k_cache and v_cache must both be given")
+        rows = k.shape[0]
+        _rows_tensor("k", k, self._dtype, pr.num_kv_heads, pr.head_dim)
+        _rows_tensor("v", v, self._dtype, pr.num_kv_heads, pr.head_dim)
+        if q is not None:
+            _rows_tensor("q", q, self._dtype, pr.num_q_heads, pr.head_dim)
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            _rows_tensor("q_out", q_out, self._dtype, pr.num_q_heads, pr.head_dim)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if any(t is not None and t.shape[0] != rows for t in (v, q, q_out)):
+            raise ValueError("k, v, q and q_out must have as many rows")
+        if positions is not None:
+            _int32("positions", positions, rows)
+        if rope is None and (q is not None or positions is not None):
+            raise ValueError("q and positions need a rope")
+        if amax is not None and (amax.dtype != torch.float32 or amax.numel() != 2 or
+                                 not amax.is_contiguous()):
+            raise ValueError("amax must be a contiguous float32 tensor of 2 elements")
+        device = _device_of(k=k, v=v, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                            row_offsets=row_offsets, start=start, positions=positions, q=q,
+                            q_out=q_out, amax=amax, workspace=self.workspace)
+        if rows == 0:
+            return q_out
+        s, switch = _stream_of(device, stream)
+        ks, vs = k.stride(), v.stride()
+        qs, qos = (q.stride(), q_out.stride()) if q is not None else ((0, 0), (0, 0))
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        args = da_kv_write_args(k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], rows,
+                                k_cache.data_ptr(), v_cache.data_ptr(), ptr(block_table),
+                                row_offsets.data_ptr(), start.data_ptr(),
+                                None if rope is None else rope.handle, ptr(positions), ptr(q),
+                                ptr(q_out), qs[0], qs[1], qos[0], qos[1], ptr(amax),
+                                *self._workspace(), s)
+        _call(device, switch, decode_attn_kv_write, self.plan, args)
+        return q_out
+
+    def read(self, k_cache, v_cache, block_table, row_offsets, start, k_out, v_out, stream=None):
+        """Fill k_out and v_out (contiguous [rows, H_kv, d]; either may be None, its cache too) with
+        the rows' K and V. Returns (k_out, v_out)."""
+        pr = self.problem
+        self._common(k_cache, v_cache, block_table, row_offsets, start)
+        outs = [t for t in (k_out, v_out) if t is not None]
+        if not outs or (k_out is None) != (k_cache is None) or \
+                (v_out is None) != (v_cache is None) or outs[0].shape != outs[-1].shape:
+            raise ValueError("give k_out with k_cache, v_out with v_cache, or all four")
+        for t in outs:
+            _rows_tensor("k_out / v_out", t, self._dtype, pr.num_kv_heads, pr.head_dim)
+            if not t.is_contiguous():
+                raise ValueError("k_out and v_out must be contiguous")
+        device = _device_of(k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                            row_offsets=row_offsets, start=start, k_out=k_out, v_out=v_out,
+                            workspace=self.workspace)
+        rows = outs[0].shape[0]
+        if rows == 0:
+            return k_out, v_out
+        s, switch = _stream_of(device, stream)
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        args = da_kv_read_args(ptr(k_cache), ptr(v_cache), ptr(block_table),
+                               row_offsets.data_ptr(), start.data_ptr(), rows, ptr(k_out),
+                               ptr(v_out), *self._workspace(), s)
+        _call(device, switch, decode_attn_kv_read, self.plan, args)
+        return k_out, v_out
+
+    def check_status(self, stream=None):
+        """Synchronise, then raise the first finding recorded since the last call."""
+        if self.workspace is None:
+            raise ValueError("made without findings")
+        s, switch = _stream_of(self.workspace.device, stream)
+        _call(self.workspace.device, switch, decode_attn_check_status, self.plan,
+              self.workspace.data_ptr(), s)

@@ -4,8 +4,6 @@
 // of the phi calibration pass.
 #include "decode_attn.h"
 
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -18,6 +16,7 @@
 
 #include "da_device.cuh"
 #include "da_mma.cuh"
+#include "da_plan.h"
 #include "da_scratch_cache.h"
 
 namespace da {
@@ -452,25 +451,7 @@ const void* histogram_kernel_for(int D, int G) {
 
 using namespace da;
 
-struct da_plan {
-  da_problem prob;
-  int num_sms;
-  int group, es, unit, box_tokens, capacity, n_groups, piece_units;
-  int kv_es;                    // K / V bytes per element (1: FP8 E4M3 cache; else es)
-  int hp;                       // KV heads per split-kernel group (2: packed FP8 pairs)
-  int sgroup;                   // query heads per split-kernel group (group * hp)
-  int policy, num_splits;       // the plan's default split choice
-  int narrow;                   // the device schedule's arithmetic fits 32 bits
-  int grid;                     // balanced grid (or the default uniform grid)
-  int recompute_splits, max_splits;
-  int stages, batch_smem;
-  size_t smem_bytes;
-  long long slots;
-  size_t off_counters, off_list, off_list_state, off_status, off_stats;
-  size_t off_part_flags, off_part_l, off_part_o, zero_bytes, ws_bytes;
-};
-
-namespace {
+namespace da {
 
 thread_local std::string g_cuda_error;
 
@@ -479,7 +460,9 @@ int cuda_fail(cudaError_t e, const char* what) {
   return DA_ERR_CUDA;
 }
 
-size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+}  // namespace da
+
+namespace {
 
 // Grid for `items` equal uniform-split items: the fewest CTAs that still give every CTA the
 // smallest possible number of items (512 items on 152 SMs: 128 CTAs of 4 rather than a mix
@@ -490,11 +473,11 @@ int uniform_grid(long long items, int sms) {
   return (int)((items + per - 1) / per);
 }
 
-int elem_size(int dt) { return dt == DA_F32 ? 4 : 2; }
-
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace
+
+namespace da {
 
 int validate_problem(const da_problem& p) {
   if (p.batch < 1 || p.num_q_heads < 1 || p.num_kv_heads < 1) return DA_ERR_INVALID_ARG;
@@ -534,6 +517,10 @@ int validate_problem(const da_problem& p) {
   return DA_OK;
 }
 
+}  // namespace da
+
+namespace {
+
 const void* kernel_for(const da_plan& pl, int mode) {
   if (pl.prob.kv_fp8) return kernel_fp8(pl.prob.head_dim, pl.sgroup, mode, pl.hp);
   switch (pl.prob.qkv_dtype) {
@@ -572,6 +559,10 @@ int ensure_smem_attr(const void* fn, size_t smem) {
   return DA_OK;
 }
 
+}  // namespace
+
+namespace da {
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -585,6 +576,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+}  // namespace da
+
+namespace {
 
 // [tokens, Hkv, D] view of a K or V cache; one box = box_tokens rows of one KV head. The
 // bf16 tensor-core kernels read the tile with ldmatrix and need the 128-byte swizzle, whose
@@ -643,6 +638,10 @@ int make_kv_map(const da_plan& pl, const void* base, bool swizzled, int hp,
   return DA_OK;
 }
 
+}  // namespace
+
+namespace da {
+
 void fill_common(const da_plan& pl, Params& k, const int32_t* block_table,
                  const int32_t* seq_lens, void* ws) {
   const da_problem& p = pl.prob;
@@ -691,7 +690,7 @@ int status_to_error(int s) {
   return DA_OK;
 }
 
-}  // namespace
+}  // namespace da
 
 extern "C" {
 

@@ -1,0 +1,673 @@
+// da_cache.cu -- the operators around a step: rotary positions, the quantising write of new
+// rows into the cache (rotary fused in), and the read of rows back out of it.
+//
+// All three are bound by memory: every row element is read once and written once, and the
+// arithmetic (two products and an add per element, a conversion) is small beside it. At a decode
+// step's size (one row a sequence) the time is the launch and a chain of dependent loads.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <type_traits>
+
+#include "da_plan.h"
+
+using namespace da;
+
+struct da_rope {
+  da_rope_config cfg;
+  double theta[128];        // radians per position
+  unsigned long long turn[128];   // turns per position, 0.64 fixed point (mod 1)
+};
+
+namespace {
+
+constexpr int kRowThreads = 128;
+constexpr int kMaxPairs = 128;   // rotary_dim / 2 <= 128
+
+// ---- rows kernel: rotary and the quantising write ------------------------------------------
+struct RowParams {
+  Params cache;                 // layout of the cache, block table, status
+  const void* q;                // [rows, hq, d] or null
+  const void* k;                // [rows, hkv, d] or null (plain rotary)
+  const void* v;
+  void* q_out;
+  void* k_cache;
+  void* v_cache;
+  long long q_rs, q_hs, k_rs, k_hs, v_rs, v_hs, qo_rs, qo_hs;   // strides, elements
+  const int32_t* row_offsets;   // null: plain rotary, every row has a position of its own
+  const int32_t* start;
+  const int32_t* positions;     // null: the cache positions
+  float* amax;
+  int rows, hq, hkv;
+  int units, head_lanes;        // a head is `units` lanes wide; head_lanes heads a block pass
+  int rotary, interleaved, transpose;
+  float m;                      // attn_factor
+  float k_inv, v_inv;           // 1 / scale of an FP8 cache
+  unsigned long long turn[kMaxPairs];
+};
+
+// The sequence whose rows hold row r: the last b with offsets[b] <= r, or -1 where r lies
+// before the first row or behind the last one.
+__device__ __forceinline__ int find_sequence(const int32_t* offsets, int batch, int r) {
+  int lo = 0, hi = batch;   // offsets[lo] <= r < offsets[hi], once both ends are checked
+  if (r < __ldg(offsets) || r >= __ldg(offsets + batch)) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(offsets + mid) <= r) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Where row r goes: its cache position (pos) and cache row (z; -1: none, recorded).
+// Returns false for a row of no sequence.
+__device__ __forceinline__ bool locate_row(const Params& c, const int32_t* offsets,
+                                           const int32_t* start, int r, int& pos, int& z) {
+  const int b = find_sequence(offsets, c.batch, r);
+  if (b < 0) return false;
+  const long long t = (long long)__ldg(start + b) + (r - __ldg(offsets + b));
+  pos = (int)t;
+  z = -1;
+  if (t < 0 || t >= c.capacity) {
+    if (c.status) atomicOr(c.status, kStatusBadSeqLen);
+    return true;
+  }
+  const int entry =
+      c.paged ? __ldg(c.block_table + (long long)b * c.max_blocks + pos / c.page_size) : 0;
+  z = token_row(c, b, pos, entry);
+  if (z < 0 && c.status) atomicOr(c.status, kStatusBadBlockTable);
+  return true;
+}
+
+// VEC elements of T as a lane holds them: 16 bytes (VEC = 16 / sizeof(T)), or one element.
+template <typename T, int VEC>
+struct RowVec {
+  using Raw = uint4;
+  __device__ __forceinline__ static void to_f32(const Raw& r, float* f) {
+    Elem<T>::to_f32(r, f);
+  }
+};
+template <typename T>
+struct RowVec<T, 1> {
+  using Raw = T;
+  __device__ __forceinline__ static void to_f32(const Raw& r, float* f) {
+    if constexpr (std::is_same<T, float>::value) f[0] = r;
+    else if constexpr (std::is_same<T, __half>::value) f[0] = __half2float(r);
+    else f[0] = __bfloat162float(r);
+  }
+};
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+// Two E4M3 codes, nearest even, |x| > 448 to +-448; `a` in the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float a, float b) {
+  uint32_t u;
+  asm("{\n\t.reg .b16 c;\n\tcvt.rn.satfinite.e4m3x2.f32 c, %2, %1;\n\tcvt.u32.u16 %0, c;\n\t}"
+      : "=r"(u)
+      : "f"(a), "f"(b));
+  return u;
+}
+
+// VEC floats stored as VEC elements of C at dst[at].
+template <typename C, int VEC>
+__device__ __forceinline__ void store_vec(C* dst, long long at, const float* f) {
+  if constexpr (std::is_same<C, fp8e4m3>::value) {
+    uint8_t* d8 = reinterpret_cast<uint8_t*>(dst) + at;
+    if constexpr (VEC == 1) {
+      *d8 = (uint8_t)pack_e4m3x2(f[0], 0.f);
+    } else {
+      static_assert(VEC == 8, "FP8 caches have 16-bit rows");
+      uint2 w;
+      w.x = pack_e4m3x2(f[0], f[1]) | pack_e4m3x2(f[2], f[3]) << 16;
+      w.y = pack_e4m3x2(f[4], f[5]) | pack_e4m3x2(f[6], f[7]) << 16;
+      *reinterpret_cast<uint2*>(d8) = w;
+    }
+  } else if constexpr (std::is_same<C, float>::value) {
+    if constexpr (VEC == 1) dst[at] = f[0];
+    else *reinterpret_cast<float4*>(dst + at) = make_float4(f[0], f[1], f[2], f[3]);
+  } else if constexpr (VEC == 1) {
+    if constexpr (std::is_same<C, __half>::value) dst[at] = __float2half_rn(f[0]);
+    else dst[at] = __float2bfloat16_rn(f[0]);
+  } else {
+    uint4 w;
+    w.x = pack2(f[0], f[1], C());
+    w.y = pack2(f[2], f[3], C());
+    w.z = pack2(f[4], f[5], C());
+    w.w = pack2(f[6], f[7], C());
+    *reinterpret_cast<uint4*>(dst + at) = w;
+  }
+}
+
+// One block per row (and slice of its heads). A head of d elements is d / (2 VEC) units; a unit is
+// two vectors of VEC elements, so VEC rotated pairs: with half pairs the vectors at u VEC and
+// u VEC + rotary / 2, else 2 VEC neighbours (also where nothing is rotated). A thread keeps one
+// unit position u, whose cosines and sines it holds in registers, and walks over heads.
+//
+// The angle of position t is t * turn mod 1 in 64-bit fixed point: exact for any 32-bit t, with
+// no 64-bit float arithmetic (an fp32 angle at t = 10^6 would be off by 0.06). Its top 32 bits,
+// as a signed half-turn count, go through sincospif.
+//
+// The first heads' vectors are loaded before the row's place in the cache is looked up, so that the
+// lookup chain (offsets, start, table) and the loads run side by side.
+template <typename T, typename C, int VEC>
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowParams p) {
+  __shared__ float s_cos[kMaxPairs], s_sin[kMaxPairs];
+  __shared__ int s_info[3];   // member, position, cache row
+  using V = RowVec<T, VEC>;
+  using Raw = typename V::Raw;
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const int u = tid % p.units, lane_head = tid / p.units;
+  const int heads = p.hq + 2 * p.hkv;
+  const int step = p.head_lanes * gridDim.y;
+  const int d = p.units * 2 * VEC;
+  const bool turned = u * 2 * VEC < p.rotary;
+  const int a0 = turned && !p.interleaved ? u * VEC : u * 2 * VEC;
+  const int b0 = turned && !p.interleaved ? a0 + p.rotary / 2 : a0 + VEC;
+  int h = lane_head < p.head_lanes ? lane_head + p.head_lanes * blockIdx.y : heads;
+
+  auto source = [&](int hh) -> const T* {
+    if (hh < p.hq) return static_cast<const T*>(p.q) + row * p.q_rs + hh * p.q_hs;
+    hh -= p.hq;
+    if (hh < p.hkv) return static_cast<const T*>(p.k) + row * p.k_rs + hh * p.k_hs;
+    return static_cast<const T*>(p.v) + row * p.v_rs + (hh - p.hkv) * p.v_hs;
+  };
+  Raw ra{}, rb{};
+  if (h < heads) {
+    const T* x = source(h);
+    ra = *reinterpret_cast<const Raw*>(x + a0);
+    rb = *reinterpret_cast<const Raw*>(x + b0);
+  }
+
+  if (tid == 0) {
+    int pos = 0, z = -1;
+    bool member = true;
+    if (p.row_offsets) member = locate_row(p.cache, p.row_offsets, p.start, row, pos, z);
+    if (member && p.positions) pos = __ldg(p.positions + row);
+    s_info[0] = member;
+    s_info[1] = pos;
+    s_info[2] = z;
+  }
+  __syncthreads();
+  if (!s_info[0]) return;
+  const long long z = s_info[2];
+  float cs[VEC], sn[VEC];
+  if (p.rotary) {
+    const long long pos = s_info[1];
+    for (int i = tid; i < p.rotary / 2; i += kRowThreads) {
+      const unsigned long long a = (unsigned long long)pos * p.turn[i];
+      float s, c;
+      sincospif((float)(int)(unsigned)(a >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
+      s_cos[i] = c * p.m;
+      s_sin[i] = (p.transpose ? -s : s) * p.m;
+    }
+    __syncthreads();
+    if (turned) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        cs[i] = s_cos[u * VEC + i];
+        sn[i] = s_sin[u * VEC + i];
+      }
+    }
+  }
+
+  float most_k = 0.f, most_v = 0.f;
+  while (h < heads) {
+    const int cur = h;
+    const Raw xa = ra, xb = rb;
+    h += step;
+    if (h < heads) {
+      const T* x = source(h);
+      ra = *reinterpret_cast<const Raw*>(x + a0);
+      rb = *reinterpret_cast<const Raw*>(x + b0);
+    }
+    const bool is_q = cur < p.hq, is_k = !is_q && cur < p.hq + p.hkv;
+    if (!is_q && z < 0) continue;   // no place in the cache
+    const bool rot = turned && (is_q || is_k);
+    const int kvh = is_k ? cur - p.hq : cur - p.hq - p.hkv;
+    const long long at = is_q ? row * p.qo_rs + cur * p.qo_hs
+                              : (z * p.hkv + kvh) * (long long)d;
+    // elements that pass unchanged move as they are
+    if (!rot && !p.amax && (is_q || std::is_same<T, C>::value)) {
+      T* dst = static_cast<T*>(is_q ? p.q_out : is_k ? p.k_cache : p.v_cache) + at;
+      *reinterpret_cast<Raw*>(dst + a0) = xa;
+      *reinterpret_cast<Raw*>(dst + b0) = xb;
+      continue;
+    }
+    float e[2 * VEC];
+    V::to_f32(xa, e);
+    V::to_f32(xb, e + VEC);
+    if (rot) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        if (p.interleaved) {
+          const float a = e[2 * i], b = e[2 * i + 1];
+          e[2 * i] = a * cs[i] - b * sn[i];
+          e[2 * i + 1] = b * cs[i] + a * sn[i];
+        } else {
+          const float a = e[i], b = e[VEC + i];
+          e[i] = a * cs[i] - b * sn[i];
+          e[VEC + i] = b * cs[i] + a * sn[i];
+        }
+      }
+    }
+    if (is_q) {
+      T* dst = static_cast<T*>(p.q_out);
+      store_vec<T, VEC>(dst, at + a0, e);
+      store_vec<T, VEC>(dst, at + b0, e + VEC);
+      continue;
+    }
+    if (p.amax) {
+      float& most = is_k ? most_k : most_v;
+#pragma unroll
+      for (int i = 0; i < 2 * VEC; ++i) most = fmaxf(most, fabsf(e[i]));   // NaN passes over
+    }
+    if constexpr (std::is_same<C, fp8e4m3>::value) {
+      const float inv = is_k ? p.k_inv : p.v_inv;
+#pragma unroll
+      for (int i = 0; i < 2 * VEC; ++i) e[i] *= inv;
+    }
+    C* dst = static_cast<C*>(is_k ? p.k_cache : p.v_cache);
+    store_vec<C, VEC>(dst, at + a0, e);
+    store_vec<C, VEC>(dst, at + b0, e + VEC);
+  }
+  if (p.amax) {
+    __syncwarp();
+    for (int o = 16; o > 0; o >>= 1) {
+      most_k = fmaxf(most_k, __shfl_xor_sync(0xffffffffu, most_k, o));
+      most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, o));
+    }
+    // non-negative floats order as their bits; a maximum does not depend on order
+    if ((tid & 31) == 0) {
+      if (most_k > 0.f) atomicMax(reinterpret_cast<int*>(p.amax), __float_as_int(most_k));
+      if (most_v > 0.f) atomicMax(reinterpret_cast<int*>(p.amax) + 1, __float_as_int(most_v));
+    }
+  }
+}
+
+template <typename T, typename C>
+const void* rows_kernel_for(bool vec) {
+  return vec ? reinterpret_cast<const void*>(&rows_kernel<T, C, 16 / (int)sizeof(T)>)
+             : reinterpret_cast<const void*>(&rows_kernel<T, C, 1>);
+}
+
+// Whether a row tensor can move 16 bytes a lane.
+bool vector_ok(const void* p, long long rs, long long hs, int es) {
+  return !p || (aligned(p, 16) && rs * es % 16 == 0 && hs * es % 16 == 0);
+}
+
+int launch_rows(RowParams& p, int head_dim, int es, bool vec, const void* fn,
+                cudaStream_t stream) {
+  const int v = vec ? 16 / es : 1;
+  p.units = head_dim / (2 * v);
+  p.head_lanes = kRowThreads / p.units;
+  const int heads = p.hq + 2 * p.hkv;
+  // A block per row; where rows are few, a row's heads are spread over more blocks (at least one
+  // pass of heads each), up to two blocks an SM.
+  const int passes = (heads + p.head_lanes - 1) / p.head_lanes;
+  int slices = 1;
+  while (slices < passes && (long long)p.rows * slices < 2 * 152) ++slices;
+  void* args[1] = {&p};
+  const cudaError_t e = cudaLaunchKernel(fn, dim3((unsigned)p.rows, (unsigned)slices),
+                                         dim3(kRowThreads), args, 0, stream);
+  return e == cudaSuccess ? DA_OK : cuda_fail(e, "launching the rows kernel");
+}
+
+void set_rope(RowParams& p, const da_rope* rope) {
+  if (!rope) return;
+  p.rotary = rope->cfg.rotary_dim;
+  p.interleaved = rope->cfg.interleaved;
+  p.m = (float)rope->cfg.attn_factor;
+  std::memcpy(p.turn, rope->turn, sizeof p.turn);
+}
+
+// ---- read kernel ----------------------------------------------------------------------------
+struct ReadParams {
+  Params cache;
+  const void* src[2];           // the caches read (K, V, or one of them)
+  void* dst[2];
+  float scale[2];
+  const int32_t* row_offsets;
+  const int32_t* start;
+  int rows;
+  int chunks;                   // 16-byte chunks of a cache row of one tensor
+  int row_items;                // chunks * tensors
+  unsigned row_magic, chunk_magic;   // ceil(2^32 / row_items), ceil(2^32 / chunks)
+  long long items;              // rows * row_items
+};
+
+constexpr int kReadThreads = 256;
+
+// The step's rows as one line of items (row, tensor, 16-byte chunk of the cache row). A warp takes
+// 32 * PER neighbouring items, PER a lane with all their loads in flight; its lanes look up the
+// rows these touch, one row a lane, and pass the cache rows on by shuffles. They are at most 32: a
+// row of 8 items divides the 256 of PER = 8, one of 9 and more spans at most 30 rows, and shorter
+// ones (4 items: one tensor, one head of 64 codes) take PER = 2.
+template <typename T, typename C, int PER>
+__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
+  constexpr bool kFp8 = std::is_same<C, fp8e4m3>::value;
+  const int lane = threadIdx.x & 31;
+  const long long i0 =
+      ((long long)blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5)) * (32 * PER);
+  if (i0 >= p.items) return;   // the whole warp
+  const int row0 = (int)(i0 / p.row_items);
+  const int off0 = (int)(i0 - (long long)row0 * p.row_items);
+  // rows row0 + lane: -2 none or of no sequence, -1 no place, else the cache row
+  int z = -2;
+  if (lane * p.row_items < off0 + 32 * PER && row0 + lane < p.rows) {
+    int pos;
+    if (!locate_row(p.cache, p.row_offsets, p.start, row0 + lane, pos, z)) z = -2;
+  }
+  uint4 c[PER];
+  int zr[PER], dr[PER], ch[PER];
+  unsigned t[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const unsigned i = (unsigned)(off0 + k * 32 + lane);
+    dr[k] = (int)__umulhi(i, p.row_magic);                    // i / row_items
+    const unsigned in_row = i - (unsigned)dr[k] * p.row_items;
+    t[k] = __umulhi(in_row, p.chunk_magic);                   // 0: the first tensor, 1: the second
+    ch[k] = (int)(in_row - t[k] * p.chunks);
+    zr[k] = __shfl_sync(0xffffffffu, z, dr[k] & 31);
+    c[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (zr[k] >= 0)
+      c[k] = __ldg(reinterpret_cast<const uint4*>(p.src[t[k] & 1]) +
+                   (long long)zr[k] * p.chunks + ch[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    if (zr[k] == -2) continue;
+    const long long at = (long long)(row0 + dr[k]) * p.chunks + ch[k];
+    if constexpr (!kFp8) {
+      static_cast<uint4*>(p.dst[t[k] & 1])[at] = c[k];
+    } else {
+      const float s = p.scale[t[k] & 1];
+      const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t lo, hi;
+        e4m3x4_to_f16x2(w[j], lo, hi);
+        __half2 h;
+        memcpy(&h, &lo, 4);
+        const float2 f = __half22float2(h);
+        memcpy(&h, &hi, 4);
+        const float2 g = __half22float2(h);
+        o[2 * j] = pack2(f.x * s, f.y * s, T());
+        o[2 * j + 1] = pack2(g.x * s, g.y * s, T());
+      }
+      uint4* d = static_cast<uint4*>(p.dst[t[k] & 1]) + 2 * at;
+      d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+template <typename T, typename C>
+const void* read_kernel_for(int per) {
+  return per == 2   ? reinterpret_cast<const void*>(&read_kernel<T, C, 2>)
+         : per == 4 ? reinterpret_cast<const void*>(&read_kernel<T, C, 4>)
+                    : reinterpret_cast<const void*>(&read_kernel<T, C, 8>);
+}
+
+// Checks that the write and the read share; the status word when a workspace is given.
+int common_checks(const da_plan& pl, const int32_t* block_table, const int32_t* row_offsets,
+                  const int32_t* start, int rows, const void* workspace, size_t workspace_bytes) {
+  if (rows < 0 || !row_offsets || !start) return DA_ERR_INVALID_ARG;
+  if (pl.prob.paged ? !block_table : block_table != nullptr) return DA_ERR_INVALID_ARG;
+  if (!aligned(row_offsets, 4) || !aligned(start, 4) || (block_table && !aligned(block_table, 4)))
+    return DA_ERR_INVALID_ARG;
+  if (workspace ? !aligned(workspace, 256) : pl.prob.validate != 0) return DA_ERR_INVALID_ARG;
+  if (workspace && workspace_bytes < pl.ws_bytes) return DA_ERR_WORKSPACE_TOO_SMALL;
+  return DA_OK;
+}
+
+int clear_status(const da_plan& pl, void* workspace, cudaStream_t stream) {
+  if (!pl.prob.validate) return DA_OK;
+  const cudaError_t e = cudaMemsetAsync(static_cast<char*>(workspace) + pl.off_status, 0, 4, stream);
+  return e == cudaSuccess ? DA_OK : cuda_fail(e, "cudaMemsetAsync(status)");
+}
+
+}  // namespace
+
+extern "C" {
+
+int decode_attn_rope_create(const da_rope_config* config, da_rope** rope_out) {
+  if (!config || !rope_out) return DA_ERR_INVALID_ARG;
+  *rope_out = nullptr;
+  const da_rope_config& c = *config;
+  if (c.head_dim < 2 || c.head_dim > 2 * kMaxPairs || c.head_dim % 2) return DA_ERR_UNSUPPORTED;
+  if (c.rotary_dim < 2 || c.rotary_dim > c.head_dim || c.rotary_dim % 2) return DA_ERR_UNSUPPORTED;
+  if (c.interleaved != 0 && c.interleaved != 1) return DA_ERR_INVALID_ARG;
+  if (!std::isfinite(c.base) || !(c.base > 1.0) || !std::isfinite(c.attn_factor))
+    return DA_ERR_INVALID_ARG;
+  const bool ramp = c.scaling == DA_ROPE_BY_PARTS || c.scaling == DA_ROPE_BY_INDEX;
+  if (c.scaling < DA_ROPE_NONE || c.scaling > DA_ROPE_BY_INDEX) return DA_ERR_INVALID_ARG;
+  if (c.scaling != DA_ROPE_NONE && (!std::isfinite(c.factor) || !(c.factor > 0.0)))
+    return DA_ERR_INVALID_ARG;
+  if (ramp && (!std::isfinite(c.original_max_position) || !(c.original_max_position > 0.0) ||
+               !std::isfinite(c.low) || !std::isfinite(c.high) || !(c.low > 0.0) ||
+               !(c.low < c.high)))
+    return DA_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925286766559;
+  const int n = c.rotary_dim;
+  double base = c.base;
+  if (c.scaling == DA_ROPE_NTK && n > 2) base *= std::pow(c.factor, (double)n / (n - 2));
+  if (!std::isfinite(base) || !(base > 0.0)) return DA_ERR_INVALID_ARG;
+  double first = 0.0, last = 0.0;
+  if (c.scaling == DA_ROPE_BY_INDEX) {
+    auto at = [&](double turns) {
+      return n * std::log(c.original_max_position / (turns * two_pi)) / (2.0 * std::log(c.base));
+    };
+    first = std::max(std::floor(at(c.high)), 0.0);
+    last = std::min(std::ceil(at(c.low)), (double)n - 1.0);
+  }
+  da_rope* r = new (std::nothrow) da_rope();
+  if (!r) return DA_ERR_INVALID_ARG;
+  r->cfg = c;
+  for (int i = 0; i < n / 2; ++i) {
+    double theta = std::pow(base, -2.0 * i / n);
+    double keep = 1.0;
+    if (c.scaling == DA_ROPE_LINEAR) keep = 0.0;
+    if (c.scaling == DA_ROPE_BY_PARTS) {
+      const double turns = c.original_max_position * theta / two_pi;
+      keep = std::min(std::max((turns - c.low) / (c.high - c.low), 0.0), 1.0);
+    }
+    if (c.scaling == DA_ROPE_BY_INDEX)
+      keep = 1.0 - std::min(std::max((i - first) / std::max(last - first, 0.001), 0.0), 1.0);
+    if (keep < 1.0) theta = theta / c.factor * (1.0 - keep) + theta * keep;
+    if (!std::isfinite(theta)) {
+      delete r;
+      return DA_ERR_INVALID_ARG;
+    }
+    r->theta[i] = theta;
+    // whole turns per position leave every integer position where it is
+    const double turns = theta / two_pi;
+    const double frac = turns - std::floor(turns);
+    // 64 fraction bits in two halves, each exact in a double
+    const double hi = std::floor(frac * 4294967296.0);
+    const double lo = std::floor((frac * 4294967296.0 - hi) * 4294967296.0 + 0.5);
+    r->turn[i] = ((unsigned long long)hi << 32) + (unsigned long long)lo;
+  }
+  *rope_out = r;
+  return DA_OK;
+}
+
+int decode_attn_rope_frequencies(const da_rope* rope, double* theta) {
+  if (!rope || !theta) return DA_ERR_INVALID_ARG;
+  std::memcpy(theta, rope->theta, sizeof(double) * (rope->cfg.rotary_dim / 2));
+  return DA_OK;
+}
+
+void decode_attn_rope_destroy(da_rope* rope) { delete rope; }
+
+int decode_attn_rope_apply(const da_rope* rope, const da_rope_args* args) {
+  if (!rope || !args) return DA_ERR_INVALID_ARG;
+  const da_rope_args& a = *args;
+  if (a.rows < 0 || a.heads < 1 || (a.transpose != 0 && a.transpose != 1))
+    return DA_ERR_INVALID_ARG;
+  if (a.dtype < DA_F32 || a.dtype > DA_BF16) return DA_ERR_UNSUPPORTED;
+  if (a.rows == 0) return DA_OK;
+  const int es = elem_size(a.dtype);
+  if (!a.x || !a.out || !a.positions || !aligned(a.x, es) || !aligned(a.out, es) ||
+      !aligned(a.positions, 4))
+    return DA_ERR_INVALID_ARG;
+  if (a.x == a.out && (a.x_row_stride != a.out_row_stride || a.x_head_stride != a.out_head_stride))
+    return DA_ERR_INVALID_ARG;
+  RowParams p;
+  std::memset(&p, 0, sizeof p);
+  set_rope(p, rope);
+  p.q = a.x;
+  p.q_out = a.out;
+  p.q_rs = a.x_row_stride;
+  p.q_hs = a.x_head_stride;
+  p.qo_rs = a.out_row_stride;
+  p.qo_hs = a.out_head_stride;
+  p.positions = a.positions;
+  p.rows = a.rows;
+  p.hq = a.heads;
+  p.transpose = a.transpose;
+  const int pair = 32 / es;   // elements of one unit
+  const bool vec = rope->cfg.head_dim % pair == 0 && rope->cfg.rotary_dim % pair == 0 &&
+                   vector_ok(a.x, a.x_row_stride, a.x_head_stride, es) &&
+                   vector_ok(a.out, a.out_row_stride, a.out_head_stride, es);
+  const void* fn = a.dtype == DA_F32   ? rows_kernel_for<float, float>(vec)
+                   : a.dtype == DA_F16 ? rows_kernel_for<__half, __half>(vec)
+                                       : rows_kernel_for<__nv_bfloat16, __nv_bfloat16>(vec);
+  return launch_rows(p, rope->cfg.head_dim, es, vec, fn, static_cast<cudaStream_t>(a.cuda_stream));
+}
+
+int decode_attn_kv_write(const da_plan* plan, const da_kv_write_args* args) {
+  if (!plan || !args) return DA_ERR_INVALID_ARG;
+  const da_plan& pl = *plan;
+  const da_kv_write_args& a = *args;
+  const da_problem& pr = pl.prob;
+  int rc = common_checks(pl, a.block_table, a.row_offsets, a.start, a.rows, a.workspace,
+                         a.workspace_bytes);
+  if (rc != DA_OK) return rc;
+  if (!a.rope && (a.positions || a.q || a.q_out)) return DA_ERR_INVALID_ARG;
+  if ((a.q == nullptr) != (a.q_out == nullptr) && a.rows > 0) return DA_ERR_INVALID_ARG;
+  if (a.rope && a.rope->cfg.head_dim != pr.head_dim) return DA_ERR_INVALID_ARG;
+  if (a.rows == 0) return DA_OK;
+  const int es = pl.es;
+  if (!a.k || !a.v || !a.k_cache || !a.v_cache || !aligned(a.k, es) || !aligned(a.v, es) ||
+      !aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) || !aligned(a.positions, 4) ||
+      !aligned(a.q, es) || !aligned(a.q_out, es) || !aligned(a.amax, 4))
+    return DA_ERR_INVALID_ARG;
+  if (a.q && a.q == a.q_out &&
+      (a.q_row_stride != a.q_out_row_stride || a.q_head_stride != a.q_out_head_stride))
+    return DA_ERR_INVALID_ARG;
+  RowParams p;
+  std::memset(&p, 0, sizeof p);
+  fill_common(pl, p.cache, a.block_table, nullptr, a.workspace);
+  set_rope(p, a.rope);
+  p.q = a.q;
+  p.q_out = a.q_out;
+  p.k = a.k;
+  p.v = a.v;
+  p.k_cache = a.k_cache;
+  p.v_cache = a.v_cache;
+  p.q_rs = a.q_row_stride;
+  p.q_hs = a.q_head_stride;
+  p.qo_rs = a.q_out_row_stride;
+  p.qo_hs = a.q_out_head_stride;
+  p.k_rs = a.k_row_stride;
+  p.k_hs = a.k_head_stride;
+  p.v_rs = a.v_row_stride;
+  p.v_hs = a.v_head_stride;
+  p.row_offsets = a.row_offsets;
+  p.start = a.start;
+  p.positions = a.positions;
+  p.amax = a.amax;
+  p.rows = a.rows;
+  p.hq = a.q ? pr.num_q_heads : 0;
+  p.hkv = pr.num_kv_heads;
+  if (pr.kv_fp8) {
+    p.k_inv = (float)(1.0 / (double)pr.k_scale);
+    p.v_inv = (float)(1.0 / (double)pr.v_scale);
+    if (!std::isfinite(p.k_inv) || !std::isfinite(p.v_inv)) return DA_ERR_INVALID_ARG;
+  }
+  const bool vec = (!a.rope || a.rope->cfg.rotary_dim % (32 / es) == 0) &&
+                   vector_ok(a.q, a.q_row_stride, a.q_head_stride, es) &&
+                   vector_ok(a.q_out, a.q_out_row_stride, a.q_out_head_stride, es) &&
+                   vector_ok(a.k, a.k_row_stride, a.k_head_stride, es) &&
+                   vector_ok(a.v, a.v_row_stride, a.v_head_stride, es);
+  const void* fn = pr.kv_fp8                ? rows_kernel_for<__nv_bfloat16, fp8e4m3>(vec)
+                   : pr.qkv_dtype == DA_F32 ? rows_kernel_for<float, float>(vec)
+                   : pr.qkv_dtype == DA_F16 ? rows_kernel_for<__half, __half>(vec)
+                                            : rows_kernel_for<__nv_bfloat16, __nv_bfloat16>(vec);
+  cudaStream_t stream = static_cast<cudaStream_t>(a.cuda_stream);
+  rc = clear_status(pl, a.workspace, stream);
+  if (rc == DA_OK) rc = launch_rows(p, pr.head_dim, es, vec, fn, stream);
+  if (rc == DA_OK && pr.validate) rc = decode_attn_check_status(plan, a.workspace, stream);
+  return rc;
+}
+
+int decode_attn_kv_read(const da_plan* plan, const da_kv_read_args* args) {
+  if (!plan || !args) return DA_ERR_INVALID_ARG;
+  const da_plan& pl = *plan;
+  const da_kv_read_args& a = *args;
+  const da_problem& pr = pl.prob;
+  int rc = common_checks(pl, a.block_table, a.row_offsets, a.start, a.rows, a.workspace,
+                         a.workspace_bytes);
+  if (rc != DA_OK) return rc;
+  if (a.rows == 0) return DA_OK;
+  if ((a.k_out == nullptr) != (a.k_cache == nullptr) ||
+      (a.v_out == nullptr) != (a.v_cache == nullptr) || (!a.k_out && !a.v_out))
+    return DA_ERR_INVALID_ARG;
+  if (!aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) || !aligned(a.k_out, 16) ||
+      !aligned(a.v_out, 16))
+    return DA_ERR_INVALID_ARG;
+  ReadParams p;
+  std::memset(&p, 0, sizeof p);
+  fill_common(pl, p.cache, a.block_table, nullptr, a.workspace);
+  int nt = 0;
+  if (a.k_out) {
+    p.src[nt] = a.k_cache;
+    p.dst[nt] = a.k_out;
+    p.scale[nt++] = pr.k_scale;
+  }
+  if (a.v_out) {
+    p.src[nt] = a.v_cache;
+    p.dst[nt] = a.v_out;
+    p.scale[nt++] = pr.v_scale;
+  }
+  p.row_offsets = a.row_offsets;
+  p.start = a.start;
+  p.rows = a.rows;
+  p.chunks = pr.num_kv_heads * pr.head_dim * pl.kv_es / 16;
+  p.row_items = p.chunks * nt;
+  // i / n = umulhi(i, ceil(2^32 / n)) for i n < 2^32: here i < row_items + 256 and n = row_items,
+  // or i < row_items and n = chunks, which caps row_items at 2^15
+  if (p.row_items > (1 << 15)) return DA_ERR_UNSUPPORTED;
+  p.row_magic = (unsigned)(((1ull << 32) + p.row_items - 1) / p.row_items);
+  p.chunk_magic = (unsigned)(((1ull << 32) + p.chunks - 1) / p.chunks);
+  p.items = (long long)p.rows * p.row_items;
+  // items a lane: more loads in flight where there are enough items to fill the GPU's warps
+  const int per = p.row_items < 8 ? 2 : p.items >= (1ll << 21) ? 8 : 4;
+  const long long per_block = (long long)kReadThreads * per;
+  const long long blocks = (p.items + per_block - 1) / per_block;
+  if (blocks >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
+  const void* fn = pr.kv_fp8                ? read_kernel_for<__nv_bfloat16, fp8e4m3>(per)
+                   : pr.qkv_dtype == DA_F32 ? read_kernel_for<float, float>(per)
+                                            : read_kernel_for<__half, __half>(per);   // moved as bits
+  cudaStream_t stream = static_cast<cudaStream_t>(a.cuda_stream);
+  rc = clear_status(pl, a.workspace, stream);
+  if (rc != DA_OK) return rc;
+  void* kargs[1] = {&p};
+  const cudaError_t e = cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(kReadThreads), kargs, 0,
+                                         stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the read kernel");
+  return pr.validate ? decode_attn_check_status(plan, a.workspace, stream) : DA_OK;
+}
+
+}  // extern "C"

@@ -1,5 +1,7 @@
 /*
- * decode_attn.h -- C ABI of the GB300 (sm_103a) single-query decode-attention library.
+ * decode_attn.h -- C ABI of the GB300 (sm_103a) decode-attention library: single-query decode
+ * attention over a KV cache, attention for trees of drafted tokens over the same cache, and the
+ * operators that fill and read it (rotary positions, quantising writes, reads).
  *
  * Computes, for every sequence b and query head h of a decode step,
  *     o[b,h] = softmax(scale * q[b,h] . K_b^T) V_b          (natural exp)
@@ -360,6 +362,172 @@ int decode_attn_logit_histogram(const da_plan* plan, const void* q, const void* 
 int decode_attn_choose_phi(const unsigned long long* counts, int nbins, float lo, float hi,
                            double coverage, float max_width, float* phi, float* x_lo,
                            float* x_hi);
+
+/* ---- The rows around a step: rotary positions, writing the cache, reading it back ---------
+ * A step's new rows are laid out one after another, sequence by sequence:
+ *   row_offsets device int32 [batch + 1], non-decreasing: rows row_offsets[b] ..
+ *               row_offsets[b + 1] - 1 belong to sequence b (none where they are equal). Rows
+ *               before the first and behind the last sequence belong to none (a padded batch).
+ *   start       device int32 [batch]: the cache position of sequence b's first row, >= 0; row r
+ *               of sequence b stands for position start[b] + r - row_offsets[b]. To append to a
+ *               cache that holds n tokens of b, start[b] = n.
+ *   rows        the number of rows of the row tensors; row_offsets may reach past it, those rows
+ *               do not exist. rows = 0: the call returns DA_OK and enqueues nothing.
+ * Row tensors are [rows, heads, d]; where strides are taken, they count elements, between rows
+ * and between heads, and the d elements of a head are contiguous. */
+
+/* How a rotary embedding's frequencies theta_i = base^(-2 i / rotary_dim), i < rotary_dim / 2,
+ * are scaled for contexts longer than those a model was trained on, s = factor,
+ * L0 = original_max_position, rho_i = L0 theta_i / (2 pi) (turns over the original context):
+ * DA_ROPE_NONE      as they are.
+ * DA_ROPE_LINEAR    theta_i / s (position interpolation).
+ * DA_ROPE_NTK       base replaced by base * s^(rotary_dim / (rotary_dim - 2)).
+ * DA_ROPE_BY_PARTS  theta_i (keep + (1 - keep) / s), keep = clamp((rho_i - low) / (high - low),
+ *                   0, 1): what turns more than `high` times is kept, less than `low` times
+ *                   interpolated ("YaRN: Efficient Context Window Extension of Large Language
+ *                   Models", "NTK-by-parts").
+ * DA_ROPE_BY_INDEX  the same mix with a ramp that is linear in i: keep = 1 - clamp((i - first) /
+ *                   max(last - first, 0.001), 0, 1), first = max(floor(at(high)), 0), last =
+ *                   min(ceil(at(low)), rotary_dim - 1), at(n) = rotary_dim ln(L0 / (2 pi n)) /
+ *                   (2 ln base), the index whose frequency turns n times. */
+typedef enum {
+  DA_ROPE_NONE = 0,
+  DA_ROPE_LINEAR = 1,
+  DA_ROPE_NTK = 2,
+  DA_ROPE_BY_PARTS = 3,
+  DA_ROPE_BY_INDEX = 4
+} da_rope_scaling;
+
+typedef struct {
+  int head_dim;              /* d: even, 2 to 256 */
+  int rotary_dim;            /* even, 2 to head_dim: elements [0, rotary_dim) of a head are rotated,
+                                the rest pass unchanged */
+  int interleaved;           /* 0: element i pairs with i + rotary_dim / 2; 1: 2 i with 2 i + 1 */
+  da_rope_scaling scaling;
+  double base;               /* > 1, finite */
+  double factor;             /* s > 0, finite; every scaling but NONE */
+  double original_max_position; /* L0 > 0; BY_PARTS, BY_INDEX */
+  double low, high;          /* 0 < low < high; BY_PARTS, BY_INDEX */
+  double attn_factor;        /* m, finite: both elements of a rotated pair are multiplied by m */
+} da_rope_config;
+
+typedef struct da_rope da_rope;   /* opaque, host-owned, immutable after creation */
+
+/* Compute the frequencies. Host only, touches no device. Owns: *rope_out (free with
+ * decode_attn_rope_destroy). Errors: INVALID_ARG, UNSUPPORTED (head_dim or rotary_dim). */
+int decode_attn_rope_create(const da_rope_config* config, da_rope** rope_out);
+
+/* Copy the scaled frequencies (radians per position) into theta[rotary_dim / 2].
+ * Errors: INVALID_ARG. */
+int decode_attn_rope_frequencies(const da_rope* rope, double* theta);
+
+void decode_attn_rope_destroy(da_rope* rope);
+
+/* Rotate rows: for every row r, head h and pair (a, b) with angle phi = positions[r] theta_i,
+ *   out_a = m (x_a cos phi - x_b sin phi),  out_b = m (x_b cos phi + x_a sin phi);
+ * transpose = 1: sin phi is negated, which is the transposed map, so the gradient with respect to
+ * x of a forward call given the gradient with respect to its output (and, with m = 1, its
+ * inverse). phi is reduced exactly in 64-bit fixed point whatever the position; the arithmetic is
+ * fp32, rounded once to the storage type.
+ *   x, out      device, [rows, heads, head_dim] of `dtype` with the given strides (elements;
+ *               heads of a row and rows must not overlap in out). out may be x with equal
+ *               strides (in place); any other overlap is not allowed.
+ *   positions   device int32 [rows]; negative positions rotate backwards.
+ * Aligned to 16 bytes, with strides that are multiples of 16 bytes and rotary_dim and head_dim
+ * multiples of 32 bytes, rows move 16 bytes a lane; any other case takes one pair a lane.
+ * Enqueued on cuda_stream. Errors: INVALID_ARG, UNSUPPORTED (dtype), CUDA. */
+typedef struct {
+  const void* x;
+  void* out;
+  da_dtype dtype;
+  int rows;
+  int heads;
+  int64_t x_row_stride, x_head_stride;
+  int64_t out_row_stride, out_head_stride;
+  const int32_t* positions;
+  int transpose;
+  void* cuda_stream;
+} da_rope_args;
+
+int decode_attn_rope_apply(const da_rope* rope, const da_rope_args* args);
+
+/* Write a step's K and V rows into the cache, in the layout and storage of the plan's problem,
+ * and, with `rope`, rotate q and k on the way, all in one launch.
+ *   plan: any plan of the problem shape; its softmax mode and split choice are not used.
+ *   k, v        device, [rows, H_kv, d] in qkv_dtype with the given strides (parts of one
+ *               projection's rows, for instance).
+ *   k_cache,    device, as for decode_attn_run. A 16-bit or fp32 cache takes the values as
+ *   v_cache     they are (a rotated k rounded once to nearest even). An FP8 cache takes E4M3
+ *               codes of x * (1 / k_scale) or x * (1 / v_scale) in fp32, rounded to nearest
+ *               even, values beyond +-448 to +-448, NaN to the NaN code; a rotated k is not
+ *               rounded to qkv_dtype in between.
+ *   block_table as for decode_attn_run. Rows of two sequences must not fall on the same token
+ *               of the pool (of two rows written to one token, either may stay, in parts).
+ *   rope        nullable. With it k is rotated by its row's position, and q, when given, is
+ *               rotated into q_out: [rows, H_q, d] in qkv_dtype, both with strides; q_out may be
+ *               q with equal strides. Without it q and q_out must be NULL. rope's head_dim must
+ *               be the plan's.
+ *   positions   nullable device int32 [rows]: the rotary positions where they are not the cache
+ *               positions (drafted trees: a node's depth). Needs rope.
+ *   amax        nullable device float [2]: amax[0] = max(amax[0], |k| as written before scaling),
+ *               amax[1] likewise for v; initialise to 0. From them an FP8 cache's scales are
+ *               chosen (amax / 448). NaNs are passed over; the result does not depend on order.
+ *   workspace   nullable, the plan's workspace: device findings are recorded in its status word
+ *               (decode_attn_check_status). Required when the problem's validate is set: the call
+ *               then synchronises and returns them.
+ * A row whose position lies outside [0, capacity) (BAD_SEQ_LEN) or on a block-table entry outside
+ * the pool (BAD_BLOCK_TABLE) is not written; its q is still rotated. Rows of no sequence leave
+ * the cache and q_out as they were. Enqueued on cuda_stream.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA; with validate the findings. */
+typedef struct {
+  const void* k;
+  const void* v;
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+  int rows;
+  void* k_cache;
+  void* v_cache;
+  const int32_t* block_table;
+  const int32_t* row_offsets;
+  const int32_t* start;
+  const da_rope* rope;
+  const int32_t* positions;
+  const void* q;
+  void* q_out;
+  int64_t q_row_stride, q_head_stride;
+  int64_t q_out_row_stride, q_out_head_stride;
+  float* amax;
+  void* workspace;
+  size_t workspace_bytes;
+  void* cuda_stream;
+} da_kv_write_args;
+
+int decode_attn_kv_write(const da_plan* plan, const da_kv_write_args* args);
+
+/* Read rows back from the cache: k_out[r], v_out[r] = the K and V of row r's position, codes of an
+ * FP8 cache times k_scale or v_scale, rounded once to qkv_dtype (to nearest even).
+ *   k_out, v_out  device, [rows, H_kv, d] contiguous, qkv_dtype, 16-byte aligned; either may be
+ *                 NULL (not both), and its cache then too.
+ * Rows at a position outside [0, capacity) or on a bad block-table entry read as zeros and are
+ * recorded as in decode_attn_kv_write; rows of no sequence are left as they were.
+ * Writing rows read from an FP8 cache back with the same scales reproduces their codes (a NaN
+ * code's sign excepted) as long as the products are normal numbers of qkv_dtype. Enqueued on
+ * cuda_stream. Errors: as kv_write. */
+typedef struct {
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_table;
+  const int32_t* row_offsets;
+  const int32_t* start;
+  int rows;
+  void* k_out;
+  void* v_out;
+  void* workspace;
+  size_t workspace_bytes;
+  void* cuda_stream;
+} da_kv_read_args;
+
+int decode_attn_kv_read(const da_plan* plan, const da_kv_read_args* args);
 
 void decode_attn_destroy(da_plan* plan);
 

@@ -22,6 +22,7 @@ ERRORS = {0: "DA_OK", -1: "DA_ERR_INVALID_ARG", -2: "DA_ERR_UNSUPPORTED",
           -9: "DA_ERR_RANGE_TOO_WIDE"}
 DA_ERR_RANGE_TOO_WIDE = -9
 MAX_HIST_BINS = 32768
+MAX_TREE = 64
 DTYPE_CODES = {"f32": DA_F32, "f16": DA_F16, "bf16": DA_BF16}
 ROPE_CODES = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "by_index": 4}
 MODE_CODES = {"sync": DA_SOFTMAX_SYNC, "unified": DA_SOFTMAX_UNIFIED,
@@ -187,6 +188,38 @@ class da_kv_read_args(ctypes.Structure):
     ]
 
 
+class da_tree_plan_info(ctypes.Structure):
+    _fields_ = [
+        ("grid_ctas", ctypes.c_int),
+        ("row_tiles", ctypes.c_int),
+        ("tile_rows", ctypes.c_int),
+        ("tile_tokens", ctypes.c_int),
+        ("stages", ctypes.c_int),
+        ("max_tree", ctypes.c_int),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("smem_bytes", ctypes.c_size_t),
+    ]
+
+
+class da_tree_args(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("k_cache", ctypes.c_void_p),
+        ("v_cache", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("row_offsets", ctypes.c_void_p),
+        ("ctx_lens", ctypes.c_void_p),
+        ("tree_mask", ctypes.c_void_p),
+        ("rows", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("out", ctypes.c_void_p),
+        ("out_lse", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("cuda_stream", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 P = ctypes.c_void_p
 
@@ -227,6 +260,14 @@ def lib():
         L.decode_attn_rope_apply.argtypes = [P, ctypes.POINTER(da_rope_args)]
         L.decode_attn_kv_write.argtypes = [P, ctypes.POINTER(da_kv_write_args)]
         L.decode_attn_kv_read.argtypes = [P, ctypes.POINTER(da_kv_read_args)]
+        L.decode_attn_tree_plan.argtypes = [ctypes.POINTER(da_problem), ctypes.c_int,
+                                            ctypes.POINTER(P), ctypes.POINTER(ctypes.c_size_t)]
+        L.decode_attn_tree_plan_info.argtypes = [P, ctypes.POINTER(da_tree_plan_info)]
+        L.decode_attn_tree_workspace_init.argtypes = [P, P, ctypes.c_size_t, P]
+        L.decode_attn_tree_run.argtypes = [P, ctypes.POINTER(da_tree_args)]
+        L.decode_attn_tree_check_status.argtypes = [P, P, P]
+        L.decode_attn_tree_destroy.argtypes = [P]
+        L.decode_attn_tree_destroy.restype = None
         L.decode_attn_rope_destroy.argtypes = [P]
         L.decode_attn_rope_destroy.restype = None
         L.decode_attn_destroy.argtypes = [P]
@@ -241,7 +282,9 @@ def lib():
                      "decode_attn_choose_phi",
                      "decode_attn_rope_create", "decode_attn_rope_frequencies",
                      "decode_attn_rope_apply", "decode_attn_kv_write", "decode_attn_kv_read",
-                     "decode_attn_abi_version"):
+                     "decode_attn_tree_plan", "decode_attn_tree_plan_info",
+                     "decode_attn_tree_workspace_init", "decode_attn_tree_run",
+                     "decode_attn_tree_check_status", "decode_attn_abi_version"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -389,6 +432,40 @@ def decode_attn_kv_write(plan, args: da_kv_write_args):
 
 def decode_attn_kv_read(plan, args: da_kv_read_args):
     _check(lib().decode_attn_kv_read(plan, ctypes.byref(args)), "decode_attn_kv_read")
+
+
+def decode_attn_tree_plan(problem: da_problem, max_tree: int):
+    """Returns (tree plan handle, workspace bytes)."""
+    plan = P()
+    ws = ctypes.c_size_t()
+    _check(lib().decode_attn_tree_plan(ctypes.byref(problem), max_tree, ctypes.byref(plan),
+                                       ctypes.byref(ws)), "decode_attn_tree_plan")
+    return plan, ws.value
+
+
+def decode_attn_tree_plan_info(plan) -> da_tree_plan_info:
+    info = da_tree_plan_info()
+    _check(lib().decode_attn_tree_plan_info(plan, ctypes.byref(info)),
+           "decode_attn_tree_plan_info")
+    return info
+
+
+def decode_attn_tree_workspace_init(plan, workspace: int, workspace_bytes: int, stream: int = 0):
+    _check(lib().decode_attn_tree_workspace_init(plan, workspace, workspace_bytes, stream or None),
+           "decode_attn_tree_workspace_init")
+
+
+def decode_attn_tree_run(plan, args: da_tree_args):
+    _check(lib().decode_attn_tree_run(plan, ctypes.byref(args)), "decode_attn_tree_run")
+
+
+def decode_attn_tree_check_status(plan, workspace: int, stream: int = 0):
+    _check(lib().decode_attn_tree_check_status(plan, workspace, stream or None),
+           "decode_attn_tree_check_status")
+
+
+def decode_attn_tree_destroy(plan):
+    lib().decode_attn_tree_destroy(plan)
 
 
 def decode_attn_destroy(plan):
@@ -581,6 +658,21 @@ class Rope:
         return out
 
 
+def _cache_args(pr, kv_ok, k_cache, v_cache, block_table, row_offsets, start):
+    """Checks of the cache, its block table and a step's row layout."""
+    shape = (pr.num_physical_blocks, pr.page_size, pr.num_kv_heads, pr.head_dim) if pr.paged \
+        else (pr.batch, pr.max_seq_len, pr.num_kv_heads, pr.head_dim)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t is not None and (t.dtype not in kv_ok or t.shape != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {shape} tensor of {kv_ok}")
+    if (block_table is None) == bool(pr.paged):
+        raise ValueError("a paged cache takes a block_table, a contiguous one none")
+    if block_table is not None:
+        _int32("block_table", block_table, pr.batch * pr.max_blocks_per_seq)
+    _int32("row_offsets", row_offsets, pr.batch + 1)
+    _int32("the sequences' lengths", start, pr.batch)
+
+
 class KVCacheIO:
     """Writes rows of K and V into a cache of the problem's shape and storage, and reads them back.
 
@@ -608,21 +700,6 @@ class KVCacheIO:
             decode_attn_destroy(plan)
             self.plan = None
 
-    def _common(self, k_cache, v_cache, block_table, row_offsets, start):
-        pr = self.problem
-        shape = (pr.num_physical_blocks, pr.page_size, pr.num_kv_heads, pr.head_dim) if pr.paged \
-            else (pr.batch, pr.max_seq_len, pr.num_kv_heads, pr.head_dim)
-        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-            if t is not None and (t.dtype not in self._kv_ok or tuple(t.shape) != shape or
-                                  not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous {shape} tensor of {self._kv_ok}")
-        if (block_table is None) == bool(pr.paged):
-            raise ValueError("a paged cache takes a block_table, a contiguous one none")
-        if block_table is not None:
-            _int32("block_table", block_table, pr.batch * pr.max_blocks_per_seq)
-        _int32("row_offsets", row_offsets, pr.batch + 1)
-        _int32("start", start, pr.batch)
-
     def _workspace(self):
         return (None, 0) if self.workspace is None else (self.workspace.data_ptr(),
                                                          self.workspace_bytes)
@@ -635,7 +712,7 @@ class KVCacheIO:
         running largest |k| and |v|. Returns q_out (None without q)."""
         import torch
         pr = self.problem
-        self._common(k_cache, v_cache, block_table, row_offsets, start)
+        _cache_args(pr, self._kv_ok, k_cache, v_cache, block_table, row_offsets, start)
         if k_cache is None or v_cache is None:
             raise ValueError("k_cache and v_cache must both be given")
         rows = k.shape[0]
@@ -679,7 +756,7 @@ class KVCacheIO:
         """Fill k_out and v_out (contiguous [rows, H_kv, d]; either may be None, its cache too) with
         the rows' K and V. Returns (k_out, v_out)."""
         pr = self.problem
-        self._common(k_cache, v_cache, block_table, row_offsets, start)
+        _cache_args(pr, self._kv_ok, k_cache, v_cache, block_table, row_offsets, start)
         outs = [t for t in (k_out, v_out) if t is not None]
         if not outs or (k_out is None) != (k_cache is None) or \
                 (v_out is None) != (v_cache is None) or outs[0].shape != outs[-1].shape:
@@ -708,4 +785,79 @@ class KVCacheIO:
             raise ValueError("made without findings")
         s, switch = _stream_of(self.workspace.device, stream)
         _call(self.workspace.device, switch, decode_attn_check_status, self.plan,
+              self.workspace.data_ptr(), s)
+
+
+class TreeAttention:
+    """Attention of drafted tokens over a cache that already holds their K and V, one tree (or
+    chain) of up to max_tree tokens a sequence: a plan plus its workspace. Two runs of one object
+    must not overlap on the GPU."""
+
+    def __init__(self, problem: da_problem, max_tree: int = MAX_TREE, device=None):
+        import torch
+        self.problem = problem
+        self.plan, self.workspace_bytes = decode_attn_tree_plan(problem, max_tree)
+        self.info = decode_attn_tree_plan_info(self.plan)
+        from .workloads import TORCH_DTYPES
+        names = {v: k for k, v in DTYPE_CODES.items()}
+        self._dtype = TORCH_DTYPES[names[problem.qkv_dtype]]
+        self._out_dtype = TORCH_DTYPES[names[problem.out_dtype]]
+        self._kv_ok = (torch.uint8, torch.float8_e4m3fn) if problem.kv_fp8 else (self._dtype,)
+        self.device = torch.device(device) if device is not None else torch.device("cuda")
+        # a zero-filled workspace needs no decode_attn_tree_workspace_init call
+        self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+
+    def __del__(self):
+        plan = getattr(self, "plan", None)
+        if plan is not None and _lib is not None:
+            decode_attn_tree_destroy(plan)
+            self.plan = None
+
+    def run(self, q, k_cache, v_cache, block_table, row_offsets, ctx_lens, tree_mask, scale: float,
+            out=None, out_lse=None, stream=None):
+        """q [rows, H_q, d]: the drafted tokens' queries, sequence by sequence (row_offsets); their K
+        and V lie in the cache from position ctx_lens[b] on. tree_mask: int64 (or uint64) [rows],
+        bit j of a row's word set iff it attends to its sequence's drafted token j; None: a chain.
+        Returns (out, lse)."""
+        import torch
+        pr = self.problem
+        H, d = pr.num_q_heads, pr.head_dim
+        _cache_args(pr, self._kv_ok, k_cache, v_cache, block_table, row_offsets, ctx_lens)
+        if k_cache is None or v_cache is None:
+            raise ValueError("k_cache and v_cache must both be given")
+        _rows_tensor("q", q, self._dtype, H, d)
+        rows = q.shape[0]
+        if out is None:
+            out = torch.empty((rows, H, d), dtype=self._out_dtype, device=q.device)
+        if out_lse is None:
+            out_lse = torch.empty((rows, H), dtype=torch.float32, device=q.device)
+        _rows_tensor("out", out, self._out_dtype, H, d)
+        if not q.is_contiguous() or not out.is_contiguous() or out.shape[0] != rows:
+            raise ValueError("q and out must be contiguous, with as many rows")
+        if out_lse.dtype != torch.float32 or out_lse.shape != (rows, H) or \
+                not out_lse.is_contiguous():
+            raise ValueError("out_lse must be a contiguous float32 [rows, H_q] tensor")
+        if tree_mask is not None and (tree_mask.dtype not in (torch.int64, torch.uint64) or
+                                      tree_mask.shape != (rows,) or
+                                      not tree_mask.is_contiguous()):
+            raise ValueError("tree_mask must be a contiguous int64 [rows] tensor")
+        device = _device_of(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                            row_offsets=row_offsets, ctx_lens=ctx_lens, tree_mask=tree_mask,
+                            out=out, out_lse=out_lse, workspace=self.workspace)
+        if rows == 0:
+            return out, out_lse
+        s, switch = _stream_of(device, stream)
+        args = da_tree_args(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                            None if block_table is None else block_table.data_ptr(),
+                            row_offsets.data_ptr(), ctx_lens.data_ptr(),
+                            None if tree_mask is None else tree_mask.data_ptr(), rows, scale,
+                            out.data_ptr(), out_lse.data_ptr(), self.workspace.data_ptr(),
+                            self.workspace_bytes, s)
+        _call(device, switch, decode_attn_tree_run, self.plan, args)
+        return out, out_lse
+
+    def check_status(self, stream=None):
+        """Synchronise, then raise the first finding recorded since the last call."""
+        s, switch = _stream_of(self.workspace.device, stream)
+        _call(self.workspace.device, switch, decode_attn_tree_check_status, self.plan,
               self.workspace.data_ptr(), s)

@@ -1,0 +1,512 @@
+// da_tree.cu -- attention for trees of drafted tokens over a cache: the fp32 kernel, the merge of
+// partials, and the host side of decode_attn_tree_*.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <map>
+#include <mutex>
+#include <new>
+#include <type_traits>
+
+#include "da_plan.h"
+#include "da_tree.cuh"
+
+using namespace da;
+
+struct da_tree_plan {
+  da_problem prob;
+  da_plan cache;                // the problem's cache layout (decode_attn_plan's fields)
+  int max_tree, num_sms;
+  int tile_rows, tile_tokens, max_row_tiles;
+  int grid, stages;
+  size_t smem_bytes;
+  size_t off_status, off_head, off_info, off_part_l, off_part_o, ws_bytes;
+};
+
+namespace {
+
+// ---- CUDA-core kernel -----------------------------------------------------------------------
+constexpr int kCoreRows = 32;      // query rows per tile
+constexpr int kCoreTokens = 64;    // KV tokens per tile
+constexpr int kCoreThreads = 256;
+
+template <int D>
+struct CoreSmem {
+  static constexpr int kStride = D + 4;        // rows 16 bytes apart mod 128: no bank conflicts
+  float q[kCoreRows * kStride];
+  float k[kCoreTokens * kStride];
+  float v[kCoreTokens * D];
+  float p[kCoreRows * (kCoreTokens + 4)];
+  unsigned long long odd;                      // drafted tokens whose V has a value not finite
+  TreeScratch sched;
+};
+
+// A 32 x 64 tile of logits by 256 threads: thread (ty, tx) holds rows 2 ty, 2 ty + 1 and tokens tx
+// + 16 j; then the same rows of O, columns 4 tx + 64 j. fp32 throughout. K and V rows past the
+// sequence's end or on bad pages are zero in shared memory.
+template <typename T, int D>
+__global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_constant__ TreeParams p,
+                                                                 const void* __restrict__ kc,
+                                                                 const void* __restrict__ vc) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  using Smem = CoreSmem<D>;
+  using Q = typename QOf<T>::type;
+  Smem& sm = *reinterpret_cast<Smem*>(raw);
+  constexpr int QS = Smem::kStride, PS = kCoreTokens + 4;
+  constexpr int NC = D / 64;                   // float4 columns of O per row
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int G = p.group;
+  const TreeShare sh = tree_schedule<kCoreThreads>(p, sm.sched);
+  TreeWalk w(p, sh);
+  bool first_piece = true;
+  while (w.next(p, sh)) {
+    if (first_piece && tid == 0 && sh.row_tile == 0)
+      p.info[sh.owner] = make_int4(w.b, w.kvh, w.t0, w.s.tiles);
+    first_piece = false;
+    const int R = w.s.T * G, r0 = sh.row_tile * kCoreRows;
+    if (r0 >= R) continue;
+    __syncthreads();
+    if (tid == 0) sm.odd = 0;
+    for (int i = tid; i < kCoreRows * D; i += kCoreThreads) {
+      const int r = i / D, d = i % D, rr = r0 + r;
+      float x = 0.f;
+      if (rr < R) {
+        const Q* q = static_cast<const Q*>(p.q) +
+                     ((long long)(w.s.row0 + rr / G) * p.c.hq + w.kvh * G + rr % G) * D + d;
+        if constexpr (std::is_same<Q, float>::value) x = *q;
+        else if constexpr (std::is_same<Q, __half>::value) x = __half2float(*q);
+        else x = __bfloat162float(*q);
+      }
+      sm.q[r * QS + d] = x;
+    }
+    unsigned long long word[2];
+    int mine[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      const int rr = r0 + 2 * ty + a;
+      mine[a] = rr < R ? rr : -1;
+      const int i = rr / G;
+      word[a] = rr < R ? tree_word(p, w.s.row0 + i, i, w.s.T) : 0ull;
+    }
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[2][NC][4] = {};
+    for (int kt = w.t0; kt < w.t1; ++kt) {
+      __syncthreads();
+      // K and V tile: 16-byte chunks of a cache row; a quarter of the block takes a row at a time
+      constexpr int EPC = std::is_same<T, fp8e4m3>::value ? 16 : 16 / (int)sizeof(Q);
+      constexpr int CH = D / EPC;
+      for (int i = tid; i < kCoreTokens * CH; i += kCoreThreads) {
+        const int j = i / CH, c = i % CH;
+        const int t = kt * kCoreTokens + j;
+        int z = -1;
+        if (t < w.s.n) {
+          const int entry = p.c.paged ? __ldg(p.c.block_table + (long long)w.b * p.c.max_blocks +
+                                              t / p.c.page_size)
+                                      : 0;
+          z = token_row(p.c, w.b, t, entry);
+          if (z < 0) atomicOr(p.c.status, kStatusBadBlockTable);
+        }
+        uint4 ck = make_uint4(0u, 0u, 0u, 0u), cv = ck;
+        if (z >= 0) {
+          const long long at = ((long long)z * p.c.hkv + w.kvh) * CH + c;
+          ck = __ldg(reinterpret_cast<const uint4*>(kc) + at);
+          cv = __ldg(reinterpret_cast<const uint4*>(vc) + at);
+        }
+        float fk[EPC], fv[EPC];
+        if constexpr (std::is_same<T, fp8e4m3>::value) {
+          const uint32_t wk[4] = {ck.x, ck.y, ck.z, ck.w}, wv[4] = {cv.x, cv.y, cv.z, cv.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t hk = e4m3x2_to_f16x2(wk[e / 2] >> (e % 2 * 16));
+            const uint32_t hv = e4m3x2_to_f16x2(wv[e / 2] >> (e % 2 * 16));
+            __half2 h;
+            memcpy(&h, &hk, 4);
+            const float2 a = __half22float2(h);
+            memcpy(&h, &hv, 4);
+            const float2 b = __half22float2(h);
+            fk[2 * e] = a.x;
+            fk[2 * e + 1] = a.y;
+            fv[2 * e] = b.x;
+            fv[2 * e + 1] = b.y;
+          }
+        } else {
+          Elem<T>::to_f32(ck, fk);
+          Elem<T>::to_f32(cv, fv);
+        }
+        if (t >= w.s.ctx) {
+          // a drafted token may be hidden from some rows: its infinities and NaN must not reach
+          // them as 0 * inf; they are set aside and added to the rows that see the token
+          bool odd = false;
+#pragma unroll
+          for (int e = 0; e < EPC; ++e)
+            if (!isfinite(fv[e])) {
+              odd = true;
+              fv[e] = 0.f;
+            }
+          if (odd) atomicOr(&sm.odd, 1ull << ((t - w.s.ctx) & 63));
+        }
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) {
+          sm.k[j * QS + c * EPC + e] = fk[e];
+          sm.v[j * D + c * EPC + e] = fv[e];
+        }
+      }
+      __syncthreads();
+      float s[2][4] = {};
+      const float4* q0 = reinterpret_cast<const float4*>(sm.q + (2 * ty) * QS);
+      const float4* q1 = reinterpret_cast<const float4*>(sm.q + (2 * ty + 1) * QS);
+#pragma unroll 4
+      for (int c = 0; c < D / 4; ++c) {
+        const float4 a = q0[c], b = q1[c];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 k = reinterpret_cast<const float4*>(sm.k + (tx + 16 * j) * QS)[c];
+          s[0][j] += a.x * k.x + a.y * k.y + a.z * k.z + a.w * k.w;
+          s[1][j] += b.x * k.x + b.y * k.y + b.z * k.z + b.w * k.w;
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        float mx = m[a];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = kt * kCoreTokens + tx + 16 * j;
+          const bool seen = t < w.s.ctx || (t < w.s.n && (word[a] >> (t - w.s.ctx) & 1ull));
+          s[a][j] = seen ? s[a][j] * p.qscale : -INFINITY;
+          mx = fmaxf(mx, s[a][j]);
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const float f = exp2f(m[a] - ref);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = exp2f(s[a][j] - ref);
+          sum += e;
+          sm.p[(2 * ty + a) * PS + tx + 16 * j] = e;
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        l[a] = l[a] * f + sum;
+        m[a] = mx;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[a][c][e] *= f;
+      }
+      __syncwarp();   // a row's 16 threads are in one warp
+#pragma unroll 2
+      for (int t = 0; t < kCoreTokens; t += 4) {
+        const float4 pa = *reinterpret_cast<const float4*>(sm.p + (2 * ty) * PS + t);
+        const float4 pb = *reinterpret_cast<const float4*>(sm.p + (2 * ty + 1) * PS + t);
+        const float a4[4] = {pa.x, pa.y, pa.z, pa.w}, b4[4] = {pb.x, pb.y, pb.z, pb.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float4 v = reinterpret_cast<const float4*>(sm.v + (t + e) * D)[tx + 16 * c];
+            o[0][c][0] += a4[e] * v.x;
+            o[0][c][1] += a4[e] * v.y;
+            o[0][c][2] += a4[e] * v.z;
+            o[0][c][3] += a4[e] * v.w;
+            o[1][c][0] += b4[e] * v.x;
+            o[1][c][1] += b4[e] * v.y;
+            o[1][c][2] += b4[e] * v.z;
+            o[1][c][3] += b4[e] * v.w;
+          }
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      if (mine[a] < 0) continue;
+      for (unsigned long long rest = sm.odd & word[a]; rest; rest &= rest - 1) {   // rare
+        const int t = w.s.ctx + __ffsll((long long)rest) - 1;
+        const int entry = p.c.paged ? __ldg(p.c.block_table + (long long)w.b * p.c.max_blocks +
+                                            t / p.c.page_size)
+                                    : 0;
+        const int z = token_row(p.c, w.b, t, entry);
+        for (int c = 0; c < NC; ++c)
+          for (int e = 0; e < 4; ++e) {
+            const long long at = ((long long)z * p.c.hkv + w.kvh) * D + (tx + 16 * c) * 4 + e;
+            float v;
+            if constexpr (std::is_same<T, fp8e4m3>::value) {
+              const uint32_t hv = e4m3x2_to_f16x2(static_cast<const uint8_t*>(vc)[at]);
+              __half h;
+              memcpy(&h, &hv, 2);
+              v = __half2float(h);
+            } else if constexpr (std::is_same<T, float>::value) {
+              v = static_cast<const float*>(vc)[at];
+            } else if constexpr (std::is_same<T, __half>::value) {
+              v = __half2float(static_cast<const __half*>(vc)[at]);
+            } else {
+              v = __bfloat162float(static_cast<const __nv_bfloat16*>(vc)[at]);
+            }
+            if (!isfinite(v)) o[a][c][e] += v;
+          }
+      }
+      const float inv = l[a] == 0.f ? 0.f : 1.f / l[a];
+      const float L = l[a] == 0.f ? -INFINITY : m[a] + log2f(l[a]);
+      if (w.whole) {
+        const int i = mine[a] / G, h = w.kvh * G + mine[a] % G;
+        const long long row = (long long)(w.s.row0 + i) * p.c.hq + h;
+        for (int c = 0; c < NC; ++c)
+          for (int e = 0; e < 4; ++e)
+            store_out(p.out, row * D + (tx + 16 * c) * 4 + e, p.c.out_dtype,
+                      o[a][c][e] * inv * p.v_scale);
+        if (p.out_lse && tx == 0) p.out_lse[row] = L * 0.69314718055994531f;
+      } else {
+        const long long at =
+            tree_slot(sh.owner, w.head, sh.row_tile, sh.row_tiles) * kCoreRows + 2 * ty + a;
+        for (int c = 0; c < NC; ++c)
+          for (int e = 0; e < 4; ++e)
+            p.part_o[at * D + (tx + 16 * c) * 4 + e] = o[a][c][e] * inv;
+        if (tx == 0) p.part_l[at] = L;
+      }
+    }
+  }
+  pdl_launch_dependents();
+}
+
+// ---- merge ----------------------------------------------------------------------------------
+// o = sum_s 2^(L_s - L) o_s, L = log2 sum_s 2^(L_s). Block (x, y): the group whose units cross the
+// start of owner x + 1's share, if x is the first owner it has units with; rows y * 8 .. + 7, a
+// warp a row, D / 32 columns a lane. A programmatic dependent of the attention kernel.
+constexpr int kMergeWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(
+    const __grid_constant__ TreeParams p) {
+  pdl_wait();
+  const long long W = p.head[0], P = p.head[1];
+  const int R = (int)p.head[2];
+  const int next = blockIdx.x + 1;
+  if (next >= P) return;
+  const int4 g = p.info[next];                 // the first piece of the next owner
+  const long long at = tree_share_begin(next, W, P);
+  const long long gs = at - g.z, ge = gs + g.w;   // the group's units
+  if (g.z == 0) return;                        // it starts there: nothing crosses
+  const int o1 = (int)tree_owner(gs, W, P), o2 = (int)tree_owner(ge - 1, W, P);
+  if (o1 != (int)blockIdx.x) return;           // another block's
+  const TreeSeq s = tree_seq(p, g.x);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kMergeWarps + warp;
+  if (r >= s.T * p.group) return;
+  const int rt = r / p.tile_rows, rr = r % p.tile_rows;
+  auto place = [&](int o) {
+    const bool head = o > o1 || gs == tree_share_begin(o1, W, P);
+    return tree_slot(o, head, rt, R) * p.tile_rows + rr;
+  };
+  float top = -INFINITY;
+  for (int o = o1 + lane; o <= o2; o += 32) top = fmaxf(top, p.part_l[place(o)]);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  // a NaN among the L's passes the maximum over; it comes back through the weights
+  const float ref = top == -INFINITY ? 0.f : top;
+  constexpr int C = D / 32;
+  float acc[C] = {};
+  float sum = 0.f;
+#pragma unroll 4
+  for (int o = o1; o <= o2; ++o) {
+    const long long a = place(o);
+    const float wgt = exp2f(p.part_l[a] - ref);
+    const float* src = p.part_o + a * D + lane * C;
+    float v[C];
+    if constexpr (C == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      v[0] = x.x; v[1] = x.y;
+    }
+    sum += wgt;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] += wgt * v[c];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int i = r / p.group, h = g.y * p.group + r % p.group;
+  const long long row = (long long)(s.row0 + i) * p.c.hq + h;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    store_out(p.out, row * D + lane * C + c, p.c.out_dtype, acc[c] * inv * p.v_scale);
+  if (p.out_lse && lane == 0)
+    p.out_lse[row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+}
+
+template <typename T>
+const void* core_kernel_for(int D) {
+  return D == 64 ? reinterpret_cast<const void*>(&tree_core_kernel<T, 64>)
+                 : reinterpret_cast<const void*>(&tree_core_kernel<T, 128>);
+}
+
+const void* core_kernel(const da_problem& p) {
+  if (p.kv_fp8) return core_kernel_for<fp8e4m3>(p.head_dim);
+  if (p.qkv_dtype == DA_F32) return core_kernel_for<float>(p.head_dim);
+  if (p.qkv_dtype == DA_F16) return core_kernel_for<__half>(p.head_dim);
+  return core_kernel_for<__nv_bfloat16>(p.head_dim);
+}
+
+}  // namespace
+
+extern "C" {
+
+int decode_attn_tree_plan(const da_problem* problem, int max_tree, da_tree_plan** plan_out,
+                          size_t* workspace_bytes_out) {
+  if (!problem || !plan_out) return DA_ERR_INVALID_ARG;
+  *plan_out = nullptr;
+  if (max_tree < 1 || max_tree > DECODE_ATTN_MAX_TREE) return DA_ERR_INVALID_ARG;
+  if (problem->mode != DA_SOFTMAX_SYNC) {
+    const int v = validate_problem(*problem);
+    return v != DA_OK ? v : DA_ERR_UNSUPPORTED;
+  }
+  if (problem->debug_stall_stage != 0) return DA_ERR_INVALID_ARG;
+  da_plan* cache = nullptr;
+  const int rc = decode_attn_plan(problem, 0, &cache, nullptr);
+  if (rc != DA_OK) return rc;
+  da_tree_plan* pl = new (std::nothrow) da_tree_plan();
+  if (!pl) {
+    decode_attn_destroy(cache);
+    return DA_ERR_INVALID_ARG;
+  }
+  pl->cache = *cache;
+  decode_attn_destroy(cache);
+  pl->prob = *problem;
+  const da_problem& p = pl->prob;
+  pl->max_tree = max_tree;
+  pl->num_sms = pl->cache.num_sms;
+  pl->tile_rows = kCoreRows;
+  pl->tile_tokens = kCoreTokens;
+  pl->stages = 0;
+  pl->smem_bytes = p.head_dim == 64 ? sizeof(CoreSmem<64>) : sizeof(CoreSmem<128>);
+  pl->max_row_tiles = (max_tree * pl->cache.group + pl->tile_rows - 1) / pl->tile_rows;
+  const long long units = (long long)p.batch * p.num_kv_heads *
+                          ((pl->cache.capacity + pl->tile_tokens - 1) / pl->tile_tokens);
+  pl->grid = (int)std::min<long long>(
+      std::max(2 * pl->num_sms, pl->max_row_tiles), units * pl->max_row_tiles);
+  const size_t slots = 2ull * pl->grid;   // two an owner and row tile; owners x row tiles <= grid
+  size_t off = 0;
+  pl->off_status = off;
+  pl->off_head = off + 16;
+  off = align256(off + 64);
+  pl->off_info = off;
+  off = align256(off + (size_t)pl->grid * 16);
+  pl->off_part_l = off;
+  off = align256(off + slots * pl->tile_rows * 4);
+  pl->off_part_o = off;
+  off = align256(off + slots * pl->tile_rows * p.head_dim * 4);
+  pl->ws_bytes = off;
+  *plan_out = pl;
+  if (workspace_bytes_out) *workspace_bytes_out = pl->ws_bytes;
+  return DA_OK;
+}
+
+int decode_attn_tree_plan_info(const da_tree_plan* plan, da_tree_plan_info* info) {
+  if (!plan || !info) return DA_ERR_INVALID_ARG;
+  info->grid_ctas = plan->grid;
+  info->row_tiles = plan->max_row_tiles;
+  info->tile_rows = plan->tile_rows;
+  info->tile_tokens = plan->tile_tokens;
+  info->stages = plan->stages;
+  info->max_tree = plan->max_tree;
+  info->workspace_bytes = plan->ws_bytes;
+  info->smem_bytes = plan->smem_bytes;
+  return DA_OK;
+}
+
+void decode_attn_tree_destroy(da_tree_plan* plan) { delete plan; }
+
+int decode_attn_tree_workspace_init(const da_tree_plan* plan, void* workspace,
+                                    size_t workspace_bytes, void* cuda_stream) {
+  if (!plan || !workspace || !aligned(workspace, 256)) return DA_ERR_INVALID_ARG;
+  if (workspace_bytes < plan->ws_bytes) return DA_ERR_WORKSPACE_TOO_SMALL;
+  const cudaError_t e = cudaMemsetAsync(static_cast<char*>(workspace) + plan->off_status, 0, 4,
+                                        static_cast<cudaStream_t>(cuda_stream));
+  return e == cudaSuccess ? DA_OK : cuda_fail(e, "cudaMemsetAsync(tree workspace)");
+}
+
+int decode_attn_tree_check_status(const da_tree_plan* plan, void* workspace, void* cuda_stream) {
+  if (!plan || !workspace) return DA_ERR_INVALID_ARG;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  char* ws = static_cast<char*>(workspace);
+  int32_t st = 0;
+  cudaError_t e = cudaMemcpyAsync(&st, ws + plan->off_status, 4, cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e == cudaSuccess) e = cudaMemsetAsync(ws + plan->off_status, 0, 4, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "reading the device status");
+  return status_to_error(st);
+}
+
+int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
+  if (!plan || !args) return DA_ERR_INVALID_ARG;
+  const da_tree_plan& pl = *plan;
+  const da_tree_args& a = *args;
+  const da_problem& pr = pl.prob;
+  if (a.rows < 0 || !a.row_offsets || !a.ctx_lens || !a.workspace || !std::isfinite(a.scale))
+    return DA_ERR_INVALID_ARG;
+  if (pr.paged ? !a.block_table : a.block_table != nullptr) return DA_ERR_INVALID_ARG;
+  if (!aligned(a.row_offsets, 4) || !aligned(a.ctx_lens, 4) || !aligned(a.block_table, 4) ||
+      !aligned(a.workspace, 256) || !aligned(a.tree_mask, 8) || !aligned(a.out_lse, 4))
+    return DA_ERR_INVALID_ARG;
+  if (a.workspace_bytes < pl.ws_bytes) return DA_ERR_WORKSPACE_TOO_SMALL;
+  if (a.rows == 0) return DA_OK;
+  if (!a.q || !a.k_cache || !a.v_cache || !a.out || !aligned(a.q, 16) || !aligned(a.k_cache, 16) ||
+      !aligned(a.v_cache, 16) || !aligned(a.out, 16))
+    return DA_ERR_INVALID_ARG;
+  TreeParams p;
+  std::memset(&p, 0, sizeof p);
+  fill_common(pl.cache, p.c, a.block_table, nullptr, nullptr);
+  char* ws = static_cast<char*>(a.workspace);
+  p.c.status = reinterpret_cast<int32_t*>(ws + pl.off_status);
+  p.head = reinterpret_cast<long long*>(ws + pl.off_head);
+  p.info = reinterpret_cast<int4*>(ws + pl.off_info);
+  p.part_l = reinterpret_cast<float*>(ws + pl.off_part_l);
+  p.part_o = reinterpret_cast<float*>(ws + pl.off_part_o);
+  p.q = a.q;
+  p.row_offsets = a.row_offsets;
+  p.ctx_lens = a.ctx_lens;
+  p.mask = reinterpret_cast<const unsigned long long*>(a.tree_mask);
+  p.out = a.out;
+  p.out_lse = a.out_lse;
+  p.rows = a.rows;
+  p.max_tree = pl.max_tree;
+  p.group = pl.cache.group;
+  p.tile_rows = pl.tile_rows;
+  p.tile_tokens = pl.tile_tokens;
+  p.max_row_tiles = pl.max_row_tiles;
+  p.qscale = (float)((double)a.scale * 1.4426950408889634 * (pr.kv_fp8 ? (double)pr.k_scale : 1.0));
+  p.v_scale = pr.kv_fp8 ? pr.v_scale : 1.f;
+  cudaStream_t stream = static_cast<cudaStream_t>(a.cuda_stream);
+  cudaError_t e;
+  if (pr.validate) {
+    e = cudaMemsetAsync(ws + pl.off_status, 0, 4, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(status)");
+  }
+  const void* fn = core_kernel(pr);
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pl.smem_bytes);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(tree kernel)");
+  const void* kc = a.k_cache;
+  const void* vc = a.v_cache;
+  void* kargs[3] = {&p, &kc, &vc};
+  e = cudaLaunchKernel(fn, dim3((unsigned)pl.grid), dim3(kCoreThreads), kargs, pl.smem_bytes, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the tree kernel");
+  if (pl.grid > 1) {
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(pl.grid - 1),
+                       (unsigned)((pl.max_tree * pl.cache.group + kMergeWarps - 1) / kMergeWarps));
+    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    void* margs[1] = {&p};
+    const void* mf = pr.head_dim == 64 ? reinterpret_cast<const void*>(&tree_merge_kernel<64>)
+                                       : reinterpret_cast<const void*>(&tree_merge_kernel<128>);
+    e = cudaLaunchKernelExC(&cfg, mf, margs);
+    if (e != cudaSuccess) return cuda_fail(e, "launching the merge kernel");
+  }
+  return pr.validate ? decode_attn_tree_check_status(plan, a.workspace, a.cuda_stream) : DA_OK;
+}
+
+}  // extern "C"

@@ -529,6 +529,86 @@ typedef struct {
 
 int decode_attn_kv_read(const da_plan* plan, const da_kv_read_args* args);
 
+/* ---- Attention for a tree of drafted tokens ------------------------------------------------
+ * Verification of drafted tokens: sequence b holds ctx_lens[b] tokens, and T_b drafted tokens'
+ * K and V follow them in the cache, at positions ctx_lens[b] + j, j < T_b (decode_attn_kv_write
+ * with start = ctx_lens puts them there). Every drafted token i has H_q queries, which attend to
+ * the whole context and to the drafted tokens that tree_mask names:
+ *     o[i,h] = softmax over t in S_i of (scale q[i,h] . k_t) applied to v_t,
+ *     S_i = [0, ctx_lens[b]) and { ctx_lens[b] + j : bit j of tree_mask[i], j < T_b },
+ * with the GQA mapping of decode_attn_run. Rows are laid out by row_offsets as above, T_b =
+ * row_offsets[b + 1] - row_offsets[b] <= max_tree. */
+
+#define DECODE_ATTN_MAX_TREE 64
+
+typedef struct da_tree_plan da_tree_plan;   /* opaque, host-owned, immutable after creation */
+
+typedef struct {
+  int grid_ctas;            /* CTAs of the attention launch */
+  int row_tiles;            /* tiles of query rows (T * G rows of one KV head) a sequence takes */
+  int tile_rows;            /* query rows per tile */
+  int tile_tokens;          /* KV tokens per tile */
+  int stages;               /* K or V tiles in flight (0: the fp32 kernel, which has no ring) */
+  int max_tree;
+  size_t workspace_bytes;
+  size_t smem_bytes;
+} da_tree_plan_info;
+
+/* Plan for the problem's cache and up to max_tree (1 to DECODE_ATTN_MAX_TREE) drafted tokens a
+ * sequence. problem->mode must be DA_SOFTMAX_SYNC (a unified maximum has no counterpart here:
+ * UNSUPPORTED); debug_stall_stage must be 0. Errors: as decode_attn_plan. */
+int decode_attn_tree_plan(const da_problem* problem, int max_tree, da_tree_plan** plan_out,
+                          size_t* workspace_bytes_out);
+
+int decode_attn_tree_plan_info(const da_tree_plan* plan, da_tree_plan_info* info);
+
+/* Clear a new workspace's status word (a zero-filled allocation needs no call). Enqueued on
+ * cuda_stream. Errors: INVALID_ARG, WORKSPACE_TOO_SMALL, CUDA. */
+int decode_attn_tree_workspace_init(const da_tree_plan* plan, void* workspace,
+                                    size_t workspace_bytes, void* cuda_stream);
+
+/* Run one verification step.
+ *   q           device, [rows, H_q, d] in qkv_dtype, contiguous, 16-byte aligned.
+ *   k_cache, v_cache, block_table, scale: as for decode_attn_run.
+ *   row_offsets, ctx_lens: device int32 [batch + 1] and [batch]. ctx_lens[b] + T_b above the
+ *               capacity, T_b above max_tree or a negative length is recorded (BAD_SEQ_LEN) and
+ *               clamped; rows past the clamped T_b are left as they were.
+ *   tree_mask   nullable device uint64 [rows]: bit j of row i's word is set iff drafted token i
+ *               attends to drafted token j of its sequence (its own bit too, where it should
+ *               see itself). Bits at or past T_b are ignored. NULL: a chain, j <= i.
+ *   out         device, [rows, H_q, d] in out_dtype, 16-byte aligned. A row that attends to
+ *               nothing (no context, mask 0) gets 0. out must not overlap q.
+ *   out_lse     nullable device float [rows, H_q]: natural-log log-sum-exp (-inf: nothing).
+ *   workspace   device, 256-byte aligned, at least the plan's workspace_bytes.
+ * Masked drafted tokens and cache slots past a sequence's end add nothing, whatever they hold
+ * (NaN and infinities included). Rows of no sequence are left as they were. Results do not depend
+ * on launch order. Enqueued on cuda_stream; with the problem's validate set the call
+ * synchronises and returns the device's findings.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA, and the findings. */
+typedef struct {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_table;
+  const int32_t* row_offsets;
+  const int32_t* ctx_lens;
+  const uint64_t* tree_mask;
+  int rows;
+  float scale;
+  void* out;
+  float* out_lse;
+  void* workspace;
+  size_t workspace_bytes;
+  void* cuda_stream;
+} da_tree_args;
+
+int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args);
+
+/* decode_attn_check_status for a tree plan's workspace. */
+int decode_attn_tree_check_status(const da_tree_plan* plan, void* workspace, void* cuda_stream);
+
+void decode_attn_tree_destroy(da_tree_plan* plan);
+
 void decode_attn_destroy(da_plan* plan);
 
 const char* decode_attn_strerror(int code);

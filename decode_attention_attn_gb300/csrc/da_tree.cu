@@ -3,13 +3,15 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
-#include <map>
 #include <mutex>
 #include <new>
+#include <set>
+#include <string>
 #include <type_traits>
+#include <utility>
 
 #include "da_plan.h"
-#include "da_tree.cuh"
+#include "da_tree_mma.cuh"
 
 using namespace da;
 
@@ -25,7 +27,7 @@ struct da_tree_plan {
 
 namespace {
 
-// ---- CUDA-core kernel -----------------------------------------------------------------------
+// ---- fp32 caches: CUDA cores ------------------------------------------------------------------
 constexpr int kCoreRows = 32;      // query rows per tile
 constexpr int kCoreTokens = 64;    // KV tokens per tile
 constexpr int kCoreThreads = 256;
@@ -44,13 +46,12 @@ struct CoreSmem {
 // A 32 x 64 tile of logits by 256 threads: thread (ty, tx) holds rows 2 ty, 2 ty + 1 and tokens tx
 // + 16 j; then the same rows of O, columns 4 tx + 64 j. fp32 throughout. K and V rows past the
 // sequence's end or on bad pages are zero in shared memory.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_constant__ TreeParams p,
                                                                  const void* __restrict__ kc,
                                                                  const void* __restrict__ vc) {
   extern __shared__ __align__(16) uint8_t raw[];
   using Smem = CoreSmem<D>;
-  using Q = typename QOf<T>::type;
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   constexpr int QS = Smem::kStride, PS = kCoreTokens + 4;
   constexpr int NC = D / 64;                   // float4 columns of O per row
@@ -71,11 +72,8 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
       const int r = i / D, d = i % D, rr = r0 + r;
       float x = 0.f;
       if (rr < R) {
-        const Q* q = static_cast<const Q*>(p.q) +
-                     ((long long)(w.s.row0 + rr / G) * p.c.hq + w.kvh * G + rr % G) * D + d;
-        if constexpr (std::is_same<Q, float>::value) x = *q;
-        else if constexpr (std::is_same<Q, __half>::value) x = __half2float(*q);
-        else x = __bfloat162float(*q);
+        x = __ldg(static_cast<const float*>(p.q) +
+                  ((long long)(w.s.row0 + rr / G) * p.c.hq + w.kvh * G + rr % G) * D + d);
       }
       sm.q[r * QS + d] = x;
     }
@@ -93,7 +91,7 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
     for (int kt = w.t0; kt < w.t1; ++kt) {
       __syncthreads();
       // K and V tile: 16-byte chunks of a cache row; a quarter of the block takes a row at a time
-      constexpr int EPC = std::is_same<T, fp8e4m3>::value ? 16 : 16 / (int)sizeof(Q);
+      constexpr int EPC = 4;
       constexpr int CH = D / EPC;
       for (int i = tid; i < kCoreTokens * CH; i += kCoreThreads) {
         const int j = i / CH, c = i % CH;
@@ -113,26 +111,8 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
           cv = __ldg(reinterpret_cast<const uint4*>(vc) + at);
         }
         float fk[EPC], fv[EPC];
-        if constexpr (std::is_same<T, fp8e4m3>::value) {
-          const uint32_t wk[4] = {ck.x, ck.y, ck.z, ck.w}, wv[4] = {cv.x, cv.y, cv.z, cv.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t hk = e4m3x2_to_f16x2(wk[e / 2] >> (e % 2 * 16));
-            const uint32_t hv = e4m3x2_to_f16x2(wv[e / 2] >> (e % 2 * 16));
-            __half2 h;
-            memcpy(&h, &hk, 4);
-            const float2 a = __half22float2(h);
-            memcpy(&h, &hv, 4);
-            const float2 b = __half22float2(h);
-            fk[2 * e] = a.x;
-            fk[2 * e + 1] = a.y;
-            fv[2 * e] = b.x;
-            fv[2 * e + 1] = b.y;
-          }
-        } else {
-          Elem<T>::to_f32(ck, fk);
-          Elem<T>::to_f32(cv, fv);
-        }
+        Elem<float>::to_f32(ck, fk);
+        Elem<float>::to_f32(cv, fv);
         if (t >= w.s.ctx) {
           // a drafted token may be hidden from some rows: its infinities and NaN must not reach
           // them as 0 * inf; they are set aside and added to the rows that see the token
@@ -229,19 +209,7 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
         for (int c = 0; c < NC; ++c)
           for (int e = 0; e < 4; ++e) {
             const long long at = ((long long)z * p.c.hkv + w.kvh) * D + (tx + 16 * c) * 4 + e;
-            float v;
-            if constexpr (std::is_same<T, fp8e4m3>::value) {
-              const uint32_t hv = e4m3x2_to_f16x2(static_cast<const uint8_t*>(vc)[at]);
-              __half h;
-              memcpy(&h, &hv, 2);
-              v = __half2float(h);
-            } else if constexpr (std::is_same<T, float>::value) {
-              v = static_cast<const float*>(vc)[at];
-            } else if constexpr (std::is_same<T, __half>::value) {
-              v = __half2float(static_cast<const __half*>(vc)[at]);
-            } else {
-              v = __bfloat162float(static_cast<const __nv_bfloat16*>(vc)[at]);
-            }
+            const float v = static_cast<const float*>(vc)[at];
             if (!isfinite(v)) o[a][c][e] += v;
           }
       }
@@ -333,17 +301,75 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(
     p.out_lse[row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
 }
 
-template <typename T>
-const void* core_kernel_for(int D) {
-  return D == 64 ? reinterpret_cast<const void*>(&tree_core_kernel<T, 64>)
-                 : reinterpret_cast<const void*>(&tree_core_kernel<T, 128>);
+const void* core_kernel(int D) {
+  return D == 64 ? reinterpret_cast<const void*>(&tree_core_kernel<64>)
+                 : reinterpret_cast<const void*>(&tree_core_kernel<128>);
 }
 
-const void* core_kernel(const da_problem& p) {
-  if (p.kv_fp8) return core_kernel_for<fp8e4m3>(p.head_dim);
-  if (p.qkv_dtype == DA_F32) return core_kernel_for<float>(p.head_dim);
-  if (p.qkv_dtype == DA_F16) return core_kernel_for<__half>(p.head_dim);
-  return core_kernel_for<__nv_bfloat16>(p.head_dim);
+bool uses_mma(const da_problem& p) { return p.kv_fp8 || p.qkv_dtype != DA_F32; }
+
+// The kernel's shared-memory limit, raised once per device and kernel.
+int raise_smem(const void* fn, size_t smem) {
+  static std::mutex mu;
+  static std::set<std::pair<int, const void*>> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  std::lock_guard<std::mutex> lk(mu);
+  if (done.count({dev, fn})) return DA_OK;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(tree kernel)");
+  done.insert({dev, fn});
+  return DA_OK;
+}
+
+int encode(CUtensorMap* map, int es, int rank, const void* base, const cuuint64_t* dims,
+           const cuuint64_t* strides, const cuuint32_t* box, bool swizzle,
+           CUtensorMapL2promotion promote) {
+  auto fn = encode_fn();
+  if (!fn) {
+    g_cuda_error = "cuTensorMapEncodeTiled is not available from the driver";
+    return DA_ERR_CUDA;
+  }
+  const cuuint32_t ones[5] = {1u, 1u, 1u, 1u, 1u};
+  const CUresult r =
+      fn(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+         (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+         promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    g_cuda_error = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
+    return DA_ERR_CUDA;
+  }
+  return DA_OK;
+}
+
+// [tokens, Hkv, D] cache, one box = `box` tokens of one KV head: 16-bit caches in blocks of 64
+// elements (view [Hkv, D / 64, tokens, 64], 128-byte swizzle), FP8 caches as rows of codes.
+int kv_map(const da_tree_plan& pl, const void* base, int box, CUtensorMap* map) {
+  const da_problem& p = pl.prob;
+  const cuuint64_t tokens = p.paged ? (cuuint64_t)p.num_physical_blocks * p.page_size
+                                    : (cuuint64_t)p.batch * p.max_seq_len;
+  const cuuint64_t D = p.head_dim, H = p.num_kv_heads;
+  if (p.kv_fp8) {
+    const cuuint64_t dims[3] = {D, tokens, H}, strides[2] = {H * D, D};
+    const cuuint32_t b[3] = {(cuuint32_t)D, (cuuint32_t)box, 1u};
+    return encode(map, 1, 3, base, dims, strides, b, false,
+                  D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
+  }
+  const cuuint64_t dims[4] = {64, tokens, D / 64, H}, strides[3] = {H * D * 2, 128, D * 2};
+  const cuuint32_t b[4] = {64u, (cuuint32_t)box, 1u, 1u};
+  return encode(map, 2, 4, base, dims, strides, b, true,
+                D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+}
+
+// [rows, Hq, D] q, one box = the G heads of a KV head of 128 / G drafted tokens, one 64-element block.
+int q_map(const da_tree_plan& pl, const void* base, int rows, CUtensorMap* map) {
+  const cuuint64_t D = pl.prob.head_dim, H = pl.prob.num_q_heads;
+  const cuuint32_t G = (cuuint32_t)pl.cache.group;
+  const cuuint64_t dims[4] = {64, H, (cuuint64_t)rows, D / 64}, strides[3] = {D * 2, H * D * 2, 128};
+  const cuuint32_t b[4] = {64u, G, (cuuint32_t)kTreeRows / G, 1u};
+  return encode(map, 2, 4, base, dims, strides, b, true, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
 }  // namespace
@@ -374,15 +400,25 @@ int decode_attn_tree_plan(const da_problem* problem, int max_tree, da_tree_plan*
   const da_problem& p = pl->prob;
   pl->max_tree = max_tree;
   pl->num_sms = pl->cache.num_sms;
-  pl->tile_rows = kCoreRows;
-  pl->tile_tokens = kCoreTokens;
-  pl->stages = 0;
-  pl->smem_bytes = p.head_dim == 64 ? sizeof(CoreSmem<64>) : sizeof(CoreSmem<128>);
+  const bool mma = uses_mma(p);
+  if (mma) {
+    const TreeLayout L = tree_layout(p.head_dim, p.kv_fp8 != 0);
+    pl->tile_rows = kTreeRows;
+    pl->tile_tokens = kTreeTokens;
+    pl->stages = p.kv_fp8 ? 2 * L.raw : L.nk + L.nv;
+    pl->smem_bytes = L.total;
+  } else {
+    pl->tile_rows = kCoreRows;
+    pl->tile_tokens = kCoreTokens;
+    pl->stages = 0;
+    pl->smem_bytes = p.head_dim == 64 ? sizeof(CoreSmem<64>) : sizeof(CoreSmem<128>);
+  }
   pl->max_row_tiles = (max_tree * pl->cache.group + pl->tile_rows - 1) / pl->tile_rows;
   const long long units = (long long)p.batch * p.num_kv_heads *
                           ((pl->cache.capacity + pl->tile_tokens - 1) / pl->tile_tokens);
   pl->grid = (int)std::min<long long>(
-      std::max(2 * pl->num_sms, pl->max_row_tiles), units * pl->max_row_tiles);
+      std::max(mma ? pl->num_sms : 2 * pl->num_sms, pl->max_row_tiles),
+      units * pl->max_row_tiles);
   const size_t slots = 2ull * pl->grid;   // two an owner and row tile; owners x row tiles <= grid
   size_t off = 0;
   pl->off_status = off;
@@ -481,13 +517,33 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
     e = cudaMemsetAsync(ws + pl.off_status, 0, 4, stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(status)");
   }
-  const void* fn = core_kernel(pr);
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pl.smem_bytes);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(tree kernel)");
-  const void* kc = a.k_cache;
-  const void* vc = a.v_cache;
-  void* kargs[3] = {&p, &kc, &vc};
-  e = cudaLaunchKernel(fn, dim3((unsigned)pl.grid), dim3(kCoreThreads), kargs, pl.smem_bytes, stream);
+  if (uses_mma(pr)) {
+    // P as two parts: always for bf16 and f16 caches; for FP8 caches, whose P is f16, where the
+    // output is fp32
+    const void* fn = tree_mma_kernel(pr.qkv_dtype, pr.kv_fp8 != 0, pr.head_dim,
+                                     !pr.kv_fp8 || pr.out_dtype == DA_F32);
+    if (!fn) return DA_ERR_UNSUPPORTED;
+    p.c.box_tokens = pr.paged ? std::min(pr.page_size, kTreeTokens) : kTreeTokens;
+    CUtensorMap tmq, tmk, tmv;
+    int rc = q_map(pl, a.q, a.rows, &tmq);
+    if (rc == DA_OK) rc = kv_map(pl, a.k_cache, p.c.box_tokens, &tmk);
+    if (rc == DA_OK) rc = kv_map(pl, a.v_cache, p.c.box_tokens, &tmv);
+    if (rc == DA_OK) rc = raise_smem(fn, pl.smem_bytes);
+    if (rc != DA_OK) return rc;
+    const void* vc = a.v_cache;
+    void* kargs[5] = {&p, &tmq, &tmk, &tmv, &vc};
+    e = cudaLaunchKernel(fn, dim3((unsigned)pl.grid), dim3((unsigned)tree_threads(pr.kv_fp8 != 0)),
+                         kargs, pl.smem_bytes, stream);
+  } else {
+    const void* fn = core_kernel(pr.head_dim);
+    const int rc = raise_smem(fn, pl.smem_bytes);
+    if (rc != DA_OK) return rc;
+    const void* kc = a.k_cache;
+    const void* vc = a.v_cache;
+    void* kargs[3] = {&p, &kc, &vc};
+    e = cudaLaunchKernel(fn, dim3((unsigned)pl.grid), dim3(kCoreThreads), kargs, pl.smem_bytes,
+                         stream);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "launching the tree kernel");
   if (pl.grid > 1) {
     cudaLaunchAttribute pdl[1];

@@ -187,6 +187,7 @@ struct TreeWalk {
   __device__ __forceinline__ bool next(const TreeParams& p, const TreeShare& sh) {
     if (u >= sh.u1) return false;
     while (u >= base + (long long)s.tiles * p.c.hkv) {
+      if (b + 1 >= p.c.batch) return false;   // (lengths that changed under way)
       base += (long long)s.tiles * p.c.hkv;
       s = tree_seq(p, ++b);
     }

@@ -246,15 +246,14 @@ template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(
     const __grid_constant__ TreeParams p) {
   pdl_wait();
-  const long long W = p.head[0], P = p.head[1];
-  const int R = (int)p.head[2];
+  const int W = p.head[0], P = p.head[1], R = p.head[2];
   const int next = blockIdx.x + 1;
   if (next >= P) return;
   const int4 g = p.info[next];                 // the first piece of the next owner
-  const long long at = tree_share_begin(next, W, P);
-  const long long gs = at - g.z, ge = gs + g.w;   // the group's units
+  const int at = tree_share_begin(next, W, P);
+  const int gs = at - g.z, ge = gs + g.w;      // the group's units
   if (g.z == 0) return;                        // it starts there: nothing crosses
-  const int o1 = (int)tree_owner(gs, W, P), o2 = (int)tree_owner(ge - 1, W, P);
+  const int o1 = tree_owner(gs, W, P), o2 = tree_owner(ge - 1, W, P);
   if (o1 != (int)blockIdx.x) return;           // another block's
   const TreeSeq s = tree_seq(p, g.x);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -308,8 +307,9 @@ const void* core_kernel(int D) {
 
 bool uses_mma(const da_problem& p) { return p.kv_fp8 || p.qkv_dtype != DA_F32; }
 
-// The kernel's shared-memory limit, raised once per device and kernel.
-int raise_smem(const void* fn, size_t smem) {
+// The kernel's shared-memory limit, raised once per device and kernel. regs: the registers that the
+// kernel must have been compiled to (its register split draws on them), or 0.
+int raise_smem(const void* fn, size_t smem, int regs) {
   static std::mutex mu;
   static std::set<std::pair<int, const void*>> done;
   int dev = 0;
@@ -319,6 +319,16 @@ int raise_smem(const void* fn, size_t smem) {
   if (done.count({dev, fn})) return DA_OK;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(tree kernel)");
+  if (regs) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, fn);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
+    if (fa.numRegs != regs) {
+      g_cuda_error = "tree kernel built with " + std::to_string(fa.numRegs) +
+                     " registers per thread; the register split needs " + std::to_string(regs);
+      return DA_ERR_CUDA;
+    }
+  }
   done.insert({dev, fn});
   return DA_OK;
 }
@@ -344,8 +354,9 @@ int encode(CUtensorMap* map, int es, int rank, const void* base, const cuuint64_
   return DA_OK;
 }
 
-// [tokens, Hkv, D] cache, one box = `box` tokens of one KV head: 16-bit caches in blocks of 64
-// elements (view [Hkv, D / 64, tokens, 64], 128-byte swizzle), FP8 caches as rows of codes.
+// [tokens, Hkv, D] cache, one box = `box` tokens of one KV head. FP8 caches: rows of codes. 16-bit
+// caches in 128-byte-swizzled blocks of 64 elements: contiguous ones as [Hkv, D / 64, tokens, 64], a
+// box one block of 128 tokens; paged ones as [Hkv, tokens / 8, D / 64, 8, 64], a box whole rows.
 int kv_map(const da_tree_plan& pl, const void* base, int box, CUtensorMap* map) {
   const da_problem& p = pl.prob;
   const cuuint64_t tokens = p.paged ? (cuuint64_t)p.num_physical_blocks * p.page_size
@@ -357,10 +368,17 @@ int kv_map(const da_tree_plan& pl, const void* base, int box, CUtensorMap* map) 
     return encode(map, 1, 3, base, dims, strides, b, false,
                   D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
   }
+  const auto promote =
+      D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+  if (p.paged) {   // pages hold at least 8 tokens
+    const cuuint64_t dims[5] = {64, 8, D / 64, tokens / 8, H};
+    const cuuint64_t strides[4] = {H * D * 2, 128, H * D * 16, D * 2};
+    const cuuint32_t b[5] = {64u, 8u, (cuuint32_t)D / 64, (cuuint32_t)box / 8, 1u};
+    return encode(map, 2, 5, base, dims, strides, b, true, promote);
+  }
   const cuuint64_t dims[4] = {64, tokens, D / 64, H}, strides[3] = {H * D * 2, 128, D * 2};
   const cuuint32_t b[4] = {64u, (cuuint32_t)box, 1u, 1u};
-  return encode(map, 2, 4, base, dims, strides, b, true,
-                D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+  return encode(map, 2, 4, base, dims, strides, b, true, promote);
 }
 
 // [rows, Hq, D] q, one box = the G heads of a KV head of 128 / G drafted tokens, one 64-element block.
@@ -416,6 +434,10 @@ int decode_attn_tree_plan(const da_problem* problem, int max_tree, da_tree_plan*
   pl->max_row_tiles = (max_tree * pl->cache.group + pl->tile_rows - 1) / pl->tile_rows;
   const long long units = (long long)p.batch * p.num_kv_heads *
                           ((pl->cache.capacity + pl->tile_tokens - 1) / pl->tile_tokens);
+  if (units >= (1ll << 31)) {   // the device schedule's 32-bit units
+    delete pl;
+    return DA_ERR_UNSUPPORTED;
+  }
   pl->grid = (int)std::min<long long>(
       std::max(mma ? pl->num_sms : 2 * pl->num_sms, pl->max_row_tiles),
       units * pl->max_row_tiles);
@@ -493,7 +515,7 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
   fill_common(pl.cache, p.c, a.block_table, nullptr, nullptr);
   char* ws = static_cast<char*>(a.workspace);
   p.c.status = reinterpret_cast<int32_t*>(ws + pl.off_status);
-  p.head = reinterpret_cast<long long*>(ws + pl.off_head);
+  p.head = reinterpret_cast<int*>(ws + pl.off_head);
   p.info = reinterpret_cast<int4*>(ws + pl.off_info);
   p.part_l = reinterpret_cast<float*>(ws + pl.off_part_l);
   p.part_o = reinterpret_cast<float*>(ws + pl.off_part_o);
@@ -523,12 +545,14 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
     const void* fn = tree_mma_kernel(pr.qkv_dtype, pr.kv_fp8 != 0, pr.head_dim,
                                      !pr.kv_fp8 || pr.out_dtype == DA_F32);
     if (!fn) return DA_ERR_UNSUPPORTED;
-    p.c.box_tokens = pr.paged ? std::min(pr.page_size, kTreeTokens) : kTreeTokens;
+    // FP8 tiles are loaded by the warps that convert them, 32 rows each
+    const int most = pr.kv_fp8 ? kTreeTokens / kTreeConvertWarps : kTreeTokens;
+    p.c.box_tokens = pr.paged ? std::min(pr.page_size, most) : most;
     CUtensorMap tmq, tmk, tmv;
     int rc = q_map(pl, a.q, a.rows, &tmq);
     if (rc == DA_OK) rc = kv_map(pl, a.k_cache, p.c.box_tokens, &tmk);
     if (rc == DA_OK) rc = kv_map(pl, a.v_cache, p.c.box_tokens, &tmv);
-    if (rc == DA_OK) rc = raise_smem(fn, pl.smem_bytes);
+    if (rc == DA_OK) rc = raise_smem(fn, pl.smem_bytes, tree_launch_regs(pr.kv_fp8 != 0));
     if (rc != DA_OK) return rc;
     const void* vc = a.v_cache;
     void* kargs[5] = {&p, &tmq, &tmk, &tmv, &vc};
@@ -536,7 +560,7 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
                          kargs, pl.smem_bytes, stream);
   } else {
     const void* fn = core_kernel(pr.head_dim);
-    const int rc = raise_smem(fn, pl.smem_bytes);
+    const int rc = raise_smem(fn, pl.smem_bytes, 0);
     if (rc != DA_OK) return rc;
     const void* kc = a.k_cache;
     const void* vc = a.v_cache;

@@ -25,7 +25,7 @@ struct TreeParams {
   const unsigned long long* mask;   // [rows] or null (a chain)
   void* out;
   float* out_lse;
-  long long* head;              // workspace: [0] units W, [1] owners P, [2] row tiles R
+  int* head;                    // workspace: [0] units W, [1] owners P, [2] row tiles R
   int4* info;                   // [owners]: b, kvh, first unit's offset in its group, group tiles
   float* part_o;                // [2 owners][R][tile rows][d], 2 P R <= 2 CTAs
   float* part_l;                // [2 owners][R][tile rows]
@@ -71,27 +71,26 @@ __device__ __forceinline__ unsigned long long tree_word(const TreeParams& p, int
 }
 
 // A CTA's part of the schedule.
+// (units fit 32 bits: the plan refuses problems whose units might not)
 struct TreeShare {
-  long long u0, u1;    // units
-  long long base;      // first unit of sequence b0
+  int u0, u1;          // units
+  int base;            // first unit of sequence b0
   int b0;              // the sequence that u0 lies in
   int row_tile, row_tiles, owner, owners;
-  long long units;
 };
 
 struct TreeScratch {   // shared memory of tree_schedule
-  long long warp_sum[32];
+  int warp_sum[32];
   int warp_max[32];
-  long long base;
-  int b0;
+  int base, b0;
 };
 
-__device__ __forceinline__ long long tree_share_begin(long long o, long long W, long long P) {
-  return o * W / P;
+__device__ __forceinline__ int tree_share_begin(int o, int W, int P) {
+  return (int)((long long)o * W / P);
 }
 // The owner of unit u: the o with o W / P <= u < (o + 1) W / P (floor divisions).
-__device__ __forceinline__ long long tree_owner(long long u, long long W, long long P) {
-  return ((u + 1) * P - 1) / W;
+__device__ __forceinline__ int tree_owner(int u, int W, int P) {
+  return (int)((((long long)u + 1) * P - 1) / W);
 }
 
 // Every thread of the CTA calls this (NT threads). Each takes a run of sequences; a block scan of
@@ -102,8 +101,7 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.c.batch + NT - 1) / NT;
   const int first = min(tid * per, p.c.batch), last = min(first + per, p.c.batch);
-  long long sum = 0;
-  int most = 1;
+  int sum = 0, most = 1;
   bool bad = false;
   for (int b = first; b < last; ++b) {
     const TreeSeq s = tree_seq(p, b);
@@ -112,10 +110,10 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
     bad |= s.bad;
   }
   if (bad && blockIdx.x == 0) atomicOr(p.c.status, kStatusBadSeqLen);
-  long long inc = sum;
+  int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+    const int up = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += up;
   }
 #pragma unroll
@@ -123,29 +121,28 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
   if (lane == 31) sc.warp_sum[warp] = inc;
   if (lane == 0) sc.warp_max[warp] = most;
   __syncthreads();
-  long long before = 0, total = 0;
+  int before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     if (w < warp) before += sc.warp_sum[w];
     total += sc.warp_sum[w];
     most = max(most, sc.warp_max[w]);
   }
-  const long long pre = before + inc - sum;
+  const int pre = before + inc - sum, units = total * p.c.hkv;
   TreeShare sh;
-  sh.units = total * p.c.hkv;
   sh.row_tiles = min(most, p.max_row_tiles);
-  sh.owners = (int)max(1ll, min((long long)gridDim.x / sh.row_tiles, sh.units));
+  sh.owners = max(1, min((int)gridDim.x / sh.row_tiles, units));
   sh.owner = blockIdx.x / sh.row_tiles;
   sh.row_tile = blockIdx.x % sh.row_tiles;
-  if (sh.units == 0 || sh.owner >= sh.owners) {
+  if (units == 0 || sh.owner >= sh.owners) {
     sh.u0 = sh.u1 = 0;
     sh.b0 = 0;
     sh.base = 0;
   } else {
-    sh.u0 = tree_share_begin(sh.owner, sh.units, sh.owners);
-    sh.u1 = tree_share_begin(sh.owner + 1, sh.units, sh.owners);
+    sh.u0 = tree_share_begin(sh.owner, units, sh.owners);
+    sh.u1 = tree_share_begin(sh.owner + 1, units, sh.owners);
     if (pre * p.c.hkv <= sh.u0 && sh.u0 < (pre + sum) * p.c.hkv) {   // exactly one thread
-      long long at = pre;
+      int at = pre;
       for (int b = first; b < last; ++b) {
         const int t = tree_seq(p, b).tiles;
         if (sh.u0 < (at + t) * p.c.hkv) {
@@ -163,7 +160,7 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
     sh.base = sc.base;
   }
   if (tid == 0 && blockIdx.x == 0) {
-    p.head[0] = sh.units;
+    p.head[0] = units;
     p.head[1] = sh.owners;
     p.head[2] = sh.row_tiles;
   }
@@ -172,8 +169,8 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
 
 // Walks a share's pieces: units of one (sequence, KV head).
 struct TreeWalk {
-  long long u;     // next unit
-  long long base;  // first unit of sequence b
+  int u;           // next unit
+  int base;        // first unit of sequence b
   int b;
   TreeSeq s;
   // the current piece
@@ -186,15 +183,15 @@ struct TreeWalk {
   }
   __device__ __forceinline__ bool next(const TreeParams& p, const TreeShare& sh) {
     if (u >= sh.u1) return false;
-    while (u >= base + (long long)s.tiles * p.c.hkv) {
+    while (u >= base + s.tiles * p.c.hkv) {
       if (b + 1 >= p.c.batch) return false;   // (lengths that changed under way)
-      base += (long long)s.tiles * p.c.hkv;
+      base += s.tiles * p.c.hkv;
       s = tree_seq(p, ++b);
     }
-    const int off = (int)(u - base);
+    const int off = u - base;
     kvh = off / s.tiles;
     t0 = off - kvh * s.tiles;
-    t1 = (int)min((long long)s.tiles, t0 + (sh.u1 - u));
+    t1 = min(s.tiles, t0 + (sh.u1 - u));
     whole = t0 == 0 && t1 == s.tiles;
     head = u == sh.u0;
     u += t1 - t0;

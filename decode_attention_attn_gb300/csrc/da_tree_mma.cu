@@ -31,9 +31,21 @@ namespace {
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;      // two S / P buffers of 128 columns
 constexpr uint32_t kColO = 256;    // O: D columns
+constexpr uint32_t kColQ = 384;    // FP8: two q tiles of D / 2 columns
 constexpr float kRescale = 8.f;    // log2: P <= 2^8 before the reference moves
 
-// ---- tcgen05 -----------------------------------------------------------------------------
+// ---- TMA and tcgen05 -----------------------------------------------------------------------------
+// 5-D tiled TMA load (a cache's [heads, tokens / 8, d / 64, 8, 64] view).
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                            int y, int z, int w, int v, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v),
+      "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                    smem_u32(slot)),
@@ -61,6 +73,15 @@ __device__ __forceinline__ void tmem_wait_ld() {
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// The thread of a converged warp that issues for it (the whole warp walks the issue loops, so that
+// descriptors stay in uniform registers).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
 }
 // D[tmem] (+)= A[smem] B[smem]
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
@@ -106,12 +127,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
-// Shared-memory operand descriptor, 128-byte swizzle: `lead` is the distance between 64-element
-// blocks along the contiguous dimension (used where that is M or N), 1024 bytes that between
-// 8-row groups.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 |
-         (uint64_t)(1024u >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// Shared-memory operand descriptor, 128-byte swizzle: `block` is the distance between 64-element
+// blocks along the contiguous dimension (read where that is M or N), `group` that between 8-row
+// groups.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t block, uint32_t group) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(block >> 4) << 16 |
+         (uint64_t)(group >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 // fp32 accumulator, M = 128, N, 16-bit operands (bf16 or f16); trans_b: B's N is contiguous.
 __host__ __device__ constexpr uint32_t mma_desc(bool bf16, int n, bool trans_b) {
@@ -121,6 +142,14 @@ __host__ __device__ constexpr uint32_t mma_desc(bool bf16, int n, bool trans_b) 
 
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Tiles that other CTAs read too (more row tiles) are left in L2.
+__device__ __forceinline__ uint64_t kv_policy(int row_tiles) {
+  if (row_tiles == 1) return make_evict_first_policy();
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
 }
 
 // A pipeline wait that gives up, for every warp of the CTA, when one of them ran out of time: from
@@ -216,6 +245,40 @@ __device__ __forceinline__ unsigned long long visible(int off, unsigned long lon
   return off > -64 ? word >> -off : 0ull;
 }
 
+// Adds what drafted tokens' V rows hold that is not finite (`odd`, tokens a row attends to) to this
+// half of the row's stored result: the infinities and NaN that were taken out before the product. Rare.
+template <typename T, int D>
+__device__ __noinline__ void add_odd(const TreeParams& p, int b, int ctx, int kvh,
+                                     unsigned long long odd, const void* v_cache, int half, void* dst,
+                                     long long row, int out_type) {
+  constexpr bool kFp8 = std::is_same<T, fp8e4m3>::value;
+#pragma unroll 1
+  for (int col = half * (D / 2); col < (half + 1) * (D / 2); ++col) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (unsigned long long rest = odd; rest; rest &= rest - 1) {
+      const int t = ctx + __ffsll((long long)rest) - 1;
+      const int entry = p.c.paged ? __ldg(p.c.block_table + (long long)b * p.c.max_blocks +
+                                          t / p.c.page_size)
+                                  : 0;
+      const long long at = ((long long)token_row(p.c, b, t, entry) * p.c.hkv + kvh) * D + col;
+      float v;
+      if constexpr (kFp8)
+        v = unpack_pair<__half>(e4m3x2_to_f16x2(static_cast<const uint8_t*>(v_cache)[at])).x;
+      else
+        v = unpack_pair<typename MmaOf<T>::type>(static_cast<const uint16_t*>(v_cache)[at]).x;
+      if (!isfinite(v)) sum += v;
+    }
+    if (isfinite(sum)) continue;
+    const long long i = row * D + col;
+    float o;
+    if (out_type == kOutF32) o = static_cast<const float*>(dst)[i];
+    else if (out_type == kOutF16) o = __half2float(static_cast<const __half*>(dst)[i]);
+    else o = __bfloat162float(static_cast<const __nv_bfloat16*>(dst)[i]);
+    store_out(dst, i, out_type, o + sum);
+  }
+}
+
 template <typename T, int D, bool kSplit>
 __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value), 1)
     tree_mma_kernel_t(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tmq,
@@ -228,7 +291,6 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   constexpr uint32_t kTile = tree_tile_bytes(D);
   constexpr uint32_t kCode = 128u * D;
   constexpr int CH = D / 64;                 // 64-element blocks of a row
-  constexpr int kBoxes = kFp8 ? 1 : CH;      // TMA boxes per run of tokens
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L.bar_off);
   uint64_t* k_full = bar;                 // the 16-bit tiles that the MMAs read
@@ -240,12 +302,10 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   uint64_t* s_full = q_empty + L.nq;      // S of a buffer done
   uint64_t* p_full = s_full + 2;          // P of a buffer written, O rescaled
   uint64_t* o_full = p_full + 2;          // O += P V done, tiles in turn
-  uint64_t* rk_full = o_full + 2;         // FP8: tiles of codes
-  uint64_t* rk_empty = rk_full + L.raw;
-  uint64_t* rv_full = rk_empty + L.raw;
-  uint64_t* rv_empty = rv_full + L.raw;
-  uint64_t* drained = rv_empty + L.raw;
-  static_assert(2 * L.nk + 2 * L.nv + 2 * L.nq + 7 + 4 * L.raw <= 48, "");
+  uint64_t* drained = o_full + 2;
+  uint64_t* rk_full = drained + 2;        // FP8: tiles of codes, a barrier for each warp's rows
+  uint64_t* rv_full = rk_full + L.raw * kTreeConvertWarps;
+  static_assert(2 * L.nk + 2 * L.nv + 2 * L.nq + 8 + 2 * L.raw * kTreeConvertWarps <= 64, "");
   float* exch = reinterpret_cast<float*>(smem + L.exch_off);
   signed char* qexp = reinterpret_cast<signed char*>(smem + L.qexp_off);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L.misc_off);
@@ -266,7 +326,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
       mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < L.nq; ++i) {
-      mbar_init(&q_full[i], 1);
+      mbar_init(&q_full[i], kFp8 ? kTreeConvertWarps : 1);
       mbar_init(&q_empty[i], kFp8 ? 1 + kTreeSoftmaxWarps : 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -274,13 +334,9 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
       mbar_init(&p_full[i], kTreeSoftmaxWarps);
       mbar_init(&o_full[i], 1);
     }
-    mbar_init(drained, 1);
-    for (int i = 0; i < L.raw; ++i) {
-      mbar_init(&rk_full[i], 1);
-      mbar_init(&rk_empty[i], kTreeConvertWarps);
-      mbar_init(&rv_full[i], 1);
-      mbar_init(&rv_empty[i], kTreeConvertWarps);
-    }
+    mbar_init(&drained[0], 1);
+    mbar_init(&drained[1], 1);
+    for (int i = 0; i < 2 * L.raw * kTreeConvertWarps; ++i) mbar_init(&rk_full[i], 1);
     // the swizzled tiles need a 1 KB boundary; elsewhere nothing may run
     *abort_flag = (smem_u32(smem) & 1023u) ? 1 : 0;
     if (*abort_flag) atomicOr(p.c.status, kStatusTimeout);
@@ -292,11 +348,18 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // K and V tiles: distance between 64-element blocks and between 8-row groups
+  const bool paired = !kFp8 && p.c.paged;
+  const uint32_t blk_bytes = paired ? 1024u : 16384u, grp_bytes = paired ? CH * 1024u : 1024u;
   Waiter wait{abort_flag, p.c.status, kWaitLimitNs, *abort_flag != 0};
-  Cursor c(p, sh);
+  if (warp < kTreeSoftmaxWarps)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(tree_softmax_regs(D, kFp8)));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(tree_other_regs(D, kFp8)));
 
   if (warp < kTreeSoftmaxWarps) {
     // ---- softmax -----------------------------------------------------------------------
+    Cursor c(p, sh);
     const int half = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)quarter << 21);   // TMEM lane quarter * 32
@@ -326,8 +389,8 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
       const uint32_t s_addr = lane_addr + kColS + (uint32_t)buf * 128u;
       const int tok0 = c.kt * kTreeTokens;
       const bool tail = tok0 + kTreeTokens > c.w.s.ctx;   // drafted tokens or the end in this tile
-      // O of tile it - 2 (complete: S of this tile was issued after it), so that every phase of the
-      // two barriers is waited for in turn and a parity names one phase
+      // O of tile it - 2: complete, as S of this tile waited for it; waiting for every phase of the
+      // two barriers in turn makes a parity name one phase
       if (it >= 2) wait(&o_full[buf], ((it - 2) >> 1) & 1);
       wait(&s_full[buf], (it >> 1) & 1);
       tc_fence_after();
@@ -368,7 +431,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
           // O so far, relative to the new reference: this half's columns
           wait(&o_full[buf ^ 1], ((it - 1) >> 1) & 1);
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int cc = 0; cc < D / 64; ++cc) {
             uint32_t o[32];
             const uint32_t a = lane_addr + kColO + half * (D / 2) + cc * 32;
@@ -414,9 +477,9 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
         wait(&v_full[vs], (it / L.nv) & 1);
         const int valid = min(kTreeTokens, c.w.s.n - tok0);
         const int t = tid & 127, end = (valid + 15) / 16 * 16;
-        uint4* vrow = reinterpret_cast<uint4*>(smem + L.v_off + vs * kTile + t * 128);
+        uint8_t* vrow = smem + L.v_off + vs * kTile + (t >> 3) * grp_bytes + (t & 7) * 128;
         for (int blk = tid >> 7; blk < CH; blk += 2) {
-          uint4* v4 = vrow + blk * (128 * 128 / 16);
+          uint4* v4 = reinterpret_cast<uint4*>(vrow + blk * blk_bytes);
           if (t >= valid && t < end) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) v4[(k + t) & 7] = make_uint4(0u, 0u, 0u, 0u);
@@ -473,32 +536,13 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
             if (!c.w.whole) p.part_l[prow] = lg;
             else if (p.out_lse) p.out_lse[orow] = lg * 0.69314718055994531f;
           }
-#pragma unroll
+#pragma unroll 1
           for (int cc = 0; cc < D / 64; ++cc) {
             const int col = half * (D / 2) + cc * 32;
             float o[32];
             tmem_ld32(lane_addr + kColO + col, reinterpret_cast<uint32_t*>(o));
             tmem_wait_ld();
             if (r >= R) continue;
-            for (unsigned long long rest = strange; rest; rest &= rest - 1) {   // rare
-              const int t = c.w.s.ctx + __ffsll((long long)rest) - 1;
-              const int entry = p.c.paged ? __ldg(p.c.block_table +
-                                                  (long long)c.w.b * p.c.max_blocks + t / p.c.page_size)
-                                          : 0;
-              const long long at =
-                  ((long long)token_row(p.c, c.w.b, t, entry) * p.c.hkv + c.w.kvh) * D + col;
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                float v;
-                if constexpr (kFp8) {
-                  const uint32_t hv = e4m3x2_to_f16x2(static_cast<const uint8_t*>(v_cache)[at + k]);
-                  v = unpack_pair<__half>(hv).x;
-                } else {
-                  v = unpack_pair<M>(static_cast<const uint16_t*>(v_cache)[at + k]).x;
-                }
-                if (!isfinite(v)) o[k] += v;
-              }
-            }
             if (!c.w.whole) {
               float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + col);
 #pragma unroll
@@ -529,6 +573,10 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
               }
             }
           }
+          if (strange && r < R)
+            add_odd<T, D>(p, c.w.b, c.w.s.ctx, c.w.kvh, strange, v_cache, half,
+                          c.w.whole ? p.out : p.part_o, c.w.whole ? orow : prow,
+                          c.w.whole ? p.c.out_dtype : (int)kOutF32);
         }
         // every warp has read `odd`; clear it for the next piece
         named_bar_sync(5, kTreeSoftmaxWarps * 32);
@@ -537,240 +585,324 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
       }
       ++it;
     }
-  } else if (warp == kTreeSoftmaxWarps || warp == kTreeSoftmaxWarps + 1) {
-    // ---- K (V) producer ------------------------------------------------------------------
-    const bool is_v = warp != kTreeSoftmaxWarps;
-    const CUtensorMap* tm = is_v ? &tmv : &tmk;
-    uint64_t* full = kFp8 ? (is_v ? rv_full : rk_full) : (is_v ? v_full : k_full);
-    uint64_t* empty = kFp8 ? (is_v ? rv_empty : rk_empty) : (is_v ? v_empty : k_empty);
-    const uint32_t slots = kFp8 ? L.raw : (is_v ? L.nv : L.nk);
-    const uint32_t base = kFp8 ? (is_v ? L.rawv_off : L.rawk_off) : (is_v ? L.v_off : L.k_off);
-    constexpr uint32_t kSlot = kFp8 ? kCode : kTile;
-    constexpr uint32_t kRow = kFp8 ? (uint32_t)D : 128u;   // bytes of a token in a box
-    const int box = p.c.box_tokens;
-    if (lane == 0) prefetch_tensormap(tm);
-    uint64_t pol;
-    if (sh.row_tiles > 1)   // other CTAs read the same tiles: leave them in L2
-      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-    else
-      pol = make_evict_first_policy();
-    // the cache row that lane's box starts at: -2 past the end, -1 on a bad page
-    auto lookup = [&](int kt) {
-      const int t = kt * kTreeTokens + (lane / kBoxes) * box;
-      if ((lane / kBoxes) * box >= kTreeTokens || t >= c.w.s.n) return -2;
-      const int entry =
-          p.c.paged ? __ldg(p.c.block_table + (long long)c.w.b * p.c.max_blocks + t / p.c.page_size)
-                    : 0;
-      return token_row(p.c, c.w.b, t, entry);
-    };
-    const int past = p.c.paged ? p.c.num_blocks * p.c.page_size : p.c.batch * p.c.max_seq_len;
-    uint32_t it = 0, issued = 0;
-    int z = -2;
-    while (c.advance(p, sh)) {
-      if (c.first()) z = lookup(c.kt);
-      const int z_next = c.last() ? -2 : lookup(c.kt + 1);   // in flight during the wait
-      const uint32_t slot = it % slots;
-      wait(&empty[slot], ((it / slots) & 1) ^ 1);
-      if (!wait.dead) {
-        const int boxes = __popc(__ballot_sync(0xffffffffu, z != -2));
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(boxes * box) * kRow);
-        __syncwarp();
-        if (z != -2) {
-          if (z < 0) atomicOr(p.c.status, kStatusBadBlockTable);
-          const int row0 = z < 0 ? past : z;   // past the pool: zeros
-          uint8_t* dst = smem + base + slot * kSlot + (uint32_t)((lane / kBoxes) * box) * kRow;
-          if constexpr (kFp8) {
-            tma_load_3d(dst, tm, &full[slot], 0, row0, c.w.kvh, pol);
-          } else {
-            const int blk = lane % kBoxes;
-            tma_load_4d(dst + blk * (128 * 128), tm, &full[slot], 0, row0, blk, c.w.kvh, pol);
+  } else if (warp < kTreeSoftmaxWarps + 2) {
+    if constexpr (!kFp8) {
+      // ---- loaders: K with q, and V ------------------------------------------------------
+      Cursor c(p, sh);
+      const bool is_v = warp != kTreeSoftmaxWarps;
+      const CUtensorMap* tm = is_v ? &tmv : &tmk;
+      uint64_t* full = is_v ? v_full : k_full;
+      uint64_t* empty = is_v ? v_empty : k_empty;
+      const uint32_t slots = is_v ? L.nv : L.nk;
+      uint8_t* const ring = smem + (is_v ? L.v_off : L.k_off);
+      if (lane == 0) prefetch_tensormap(tm);
+      const uint64_t pol = kv_policy(sh.row_tiles);
+      // Paged: lane i loads the i-th run of `box` tokens, whole rows. Contiguous: lane i loads block i.
+      const int box = p.c.box_tokens;
+      auto lookup = [&](int kt) {   // lane's cache row; -2: nothing to load, -1: a bad page
+        const int t = kt * kTreeTokens + (p.c.paged ? lane * box : 0);
+        if (p.c.paged ? lane * box >= kTreeTokens || t >= c.w.s.n : lane >= CH) return -2;
+        const int entry =
+            p.c.paged ? __ldg(p.c.block_table + (long long)c.w.b * p.c.max_blocks + t / p.c.page_size)
+                      : 0;
+        return token_row(p.c, c.w.b, t, entry);
+      };
+      const uint32_t lane_off = p.c.paged ? (uint32_t)(lane * box / 8) * grp_bytes : lane * blk_bytes;
+      const uint32_t lane_bytes = (uint32_t)box * 128u * (p.c.paged ? CH : 1);
+      uint32_t slot = 0, par = 1, it = 0, issued = 0;
+      int z = -2, loaded = 0;
+      while (c.advance(p, sh)) {
+        if (c.first()) {
+          z = lookup(c.kt);
+          if (!is_v) {
+            const int qb = c.piece & 1;
+            const int i0 = sh.row_tile * (kTreeRows / p.group);   // the tile's first drafted token
+            wait(&q_empty[qb], ((c.piece >> 1) & 1) ^ 1);
+            if (!wait.dead) {
+              if (lane == 0) mbar_arrive_expect_tx(&q_full[qb], kTile);
+              __syncwarp();
+              if (lane < CH)
+                tma_load_4d(smem + L.q_off + qb * kTile + lane * (128 * 128), &tmq, &q_full[qb], 0,
+                            c.w.kvh * p.group, c.w.s.row0 + i0, lane, pol);
+              ++loaded;
+            }
           }
         }
-        issued = it + 1;
+        const int z_next = c.last() ? -2 : lookup(c.kt + 1);   // in flight during the wait
+        wait(&empty[slot], par);
+        if (!wait.dead) {
+          const int boxes = __popc(__ballot_sync(0xffffffffu, z != -2));
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], boxes * lane_bytes);
+          __syncwarp();
+          if (z != -2) {
+            uint8_t* dst = ring + slot * kTile + lane_off;
+            if (p.c.paged) {
+              if (z < 0) atomicOr(p.c.status, kStatusBadBlockTable);
+              // a bad page: past the pool, zeros
+              const int group = z < 0 ? p.c.num_blocks * (p.c.page_size / 8) : z / 8;
+              tma_load_5d(dst, tm, &full[slot], 0, 0, 0, group, c.w.kvh, pol);
+            } else {
+              tma_load_4d(dst, tm, &full[slot], 0, z, lane, c.w.kvh, pol);
+            }
+          }
+          issued = it + 1;
+        }
+        __syncwarp();
+        if (++slot == slots) slot = 0, par ^= 1;
+        z = z_next;
+        ++it;
       }
-      __syncwarp();
-      z = z_next;
-      ++it;
+      // never leave with copies in flight
+      for (uint32_t k = issued > slots ? issued - slots : 0; k < issued; ++k)
+        mbar_wait(&full[k % slots], (k / slots) & 1, kWaitLimitNs);
+      for (int k = loaded > L.nq ? loaded - L.nq : 0; k < loaded; ++k)
+        mbar_wait(&q_full[k & 1], (k >> 1) & 1, kWaitLimitNs);
     }
-    // never leave with copies in flight
-    for (uint32_t k = issued > slots ? issued - slots : 0; k < issued; ++k)
-      mbar_wait(&full[k % slots], (k / slots) & 1, kWaitLimitNs);
   } else if (warp == kTreeSoftmaxWarps + 2) {
-    // ---- MMA issuer ------------------------------------------------------------------------
+    // ---- S = Q K^T issuer ------------------------------------------------------------------
+    Cursor c(p, sh);
     constexpr bool kBf16 = std::is_same<M, __nv_bfloat16>::value;
     constexpr uint32_t kDescS = mma_desc(kBf16, kTreeTokens, false);
-    constexpr uint32_t kDescO = mma_desc(kBf16, D, true);
-    const uint32_t q_base = smem_u32(smem + L.q_off), k_base = smem_u32(smem + L.k_off);
-    const uint32_t v_base = smem_u32(smem + L.v_off);
-    Cursor d(p, sh);      // S runs a tile ahead of O
-    uint32_t is = 0, io = 0;
-    auto issue_s = [&]() {
-      const uint32_t slot = is % L.nk, qb = d.piece & 1;
-      if (d.first()) wait(&q_full[qb], (d.piece >> 1) & 1);
-      wait(&k_full[slot], (is / L.nk) & 1);
-      tc_fence_after();
-      if (!wait.dead && lane == 0) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (uint32_t)(k / 4) * 16384u + (uint32_t)(k % 4) * 32u;
-          mma_ss(tmem + kColS + (is & 1) * 128u, tile_desc(q_base + qb * kTile + off, 16),
-                 tile_desc(k_base + slot * kTile + off, 16), kDescS, k != 0);
-        }
-        tc_commit(&k_empty[slot]);
-        if (d.last()) tc_commit(&q_empty[qb]);
-        tc_commit(&s_full[is & 1]);
-      }
-      __syncwarp();
-      ++is;
-    };
-    bool more = d.advance(p, sh);
-    if (more) issue_s();
-    while (c.advance(p, sh)) {
-      more = d.advance(p, sh);
-      if (more) issue_s();
-      const uint32_t slot = io % L.nv, buf = io & 1;
-      wait(&v_full[slot], (io / L.nv) & 1);
-      wait(&p_full[buf], (io >> 1) & 1);
-      tc_fence_after();
-      if (!wait.dead && lane == 0) {
-        const int steps = (min(kTreeTokens, c.w.s.n - c.kt * kTreeTokens) + 15) / 16;
-        const uint32_t pa = tmem + kColS + buf * 128u;
-#pragma unroll 1
-        for (int part = 0; part < (kSplit ? 2 : 1); ++part)
-#pragma unroll 1
-          for (int k = 0; k < steps; ++k)
-            mma_ts(tmem + kColO, pa + part * 64u + k * 8u,
-                   tile_desc(v_base + slot * kTile + k * 2048u, 16384), kDescO,
-                   !c.first() || k != 0 || part != 0);
-        tc_commit(&v_empty[slot]);
-        tc_commit(&o_full[buf]);
-      }
-      __syncwarp();
-      ++io;
-    }
-    // nothing leaves before the last MMA has completed (after a timeout too)
-    if (lane == 0) tc_commit(drained);
-    __syncwarp();
-    mbar_wait(drained, 0, kWaitLimitNs);
-  } else if (warp == kTreeSoftmaxWarps + 3) {
-    // ---- q producer --------------------------------------------------------------------------
-    int loaded = 0;
+    // descriptors of the first tiles; an address step of b bytes adds b / 16 to them
+    const uint64_t q_desc = tile_desc(smem_u32(smem + L.q_off), 16, 1024);
+    const uint64_t k_desc = tile_desc(smem_u32(smem + L.k_off), 16, grp_bytes);
+    const bool issuer = elect_one();
+    uint32_t it = 0, k_slot = 0, k_par = 0;
     // the merge reads the first piece of every owner, whether this row tile has rows in it or not
     {
       TreeWalk w(p, sh);
-      if (w.next(p, sh) && sh.row_tile == 0 && lane == 0)
+      if (w.next(p, sh) && sh.row_tile == 0 && issuer)
         p.info[sh.owner] = make_int4(w.b, w.kvh, w.t0, w.s.tiles);
     }
     while (c.advance(p, sh)) {
-      if (!c.first()) {
-        c.kt = c.w.t1 - 1;   // the rest of the piece
-        continue;
-      }
-      const int qb = c.piece & 1;
-      const int i0 = sh.row_tile * (kTreeRows / p.group);   // the tile's first drafted token
-      wait(&q_empty[qb], ((c.piece >> 1) & 1) ^ 1);
-      if (!wait.dead) {
-        if constexpr (!kFp8) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&q_full[qb], kTile);
-            for (int blk = 0; blk < CH; ++blk)
-              tma_load_4d(smem + L.q_off + qb * kTile + blk * (128 * 128), &tmq, &q_full[qb], 0,
-                          c.w.kvh * p.group, c.w.s.row0 + i0, blk, make_evict_first_policy());
-          }
-          ++loaded;
-        } else {
-          // D / 8 lanes a row, 8 elements each: q as f16 times a power of two per row, so that its
-          // largest element lies in [2^14, 2^15)
-          constexpr int LR = D / 8, RW = 32 / LR;
-          const int sub = lane / LR, e = lane % LR, R = c.w.s.T * p.group;
-#pragma unroll 4
-          for (int r8 = 0; r8 < kTreeRows; r8 += RW) {
-            const int rr = r8 + sub, r = sh.row_tile * kTreeRows + rr;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (r < R)
-              v = __ldg(reinterpret_cast<const uint4*>(
-                            static_cast<const __nv_bfloat16*>(p.q) +
-                            ((long long)(c.w.s.row0 + r / p.group) * p.c.hq + c.w.kvh * p.group +
-                             r % p.group) * D) + e);
-            float f[8];
-            Elem<__nv_bfloat16>::to_f32(v, f);
-            float big = 0.f;
+      const uint32_t qb = c.piece & 1, buf = it & 1;
+      const bool last = c.last();
+      if (c.first()) wait(&q_full[qb], (c.piece >> 1) & 1);
+      // the buffer's P has been used (its O is done); the softmax read its S before that
+      if (it >= 2) wait(&o_full[buf], ((it - 2) >> 1) & 1);
+      wait(&k_full[k_slot], k_par);
+      tc_fence_after();
+      if (!wait.dead && issuer) {
+        const uint64_t kd = k_desc + k_slot * (kTile >> 4);
+        const uint32_t s_col = tmem + kColS + buf * 128u;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f[k]));
-#pragma unroll
-            for (int o = LR / 2; o > 0; o >>= 1)
-              big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-            // 2^(14 - exponent of the largest), within what an int8 holds; 1 for a row of zeros
-            int s = big > 0.f && big < INFINITY ? 14 - ((int)(__float_as_uint(big) >> 23) - 127) : 0;
-            s = min(max(s, -112), 126);
-            const float mul = __uint_as_float((uint32_t)(s + 127) << 23);
-            uint4 w;
-            w.x = pack_pair<__half>(f[0] * mul, f[1] * mul);
-            w.y = pack_pair<__half>(f[2] * mul, f[3] * mul);
-            w.z = pack_pair<__half>(f[4] * mul, f[5] * mul);
-            w.w = pack_pair<__half>(f[6] * mul, f[7] * mul);
-            *reinterpret_cast<uint4*>(smem + L.q_off + qb * kTile + (e / 8) * (128 * 128) + rr * 128 +
-                                      (((e & 7) ^ (rr & 7)) << 4)) = w;
-            if (e == 0) qexp[qb * 128 + rr] = (signed char)-s;
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t kk = kd + (uint32_t)(k / 4) * (blk_bytes >> 4) + (uint32_t)(k % 4) * 2u;
+          if constexpr (kFp8) {
+            mma_ts(s_col, tmem + kColQ + qb * (D / 2) + k * 8u, kk, kDescS, k != 0);
+          } else {
+            const uint32_t off = (uint32_t)(k / 4) * (16384u >> 4) + (uint32_t)(k % 4) * 2u;
+            mma_ss(s_col, q_desc + qb * (kTile >> 4) + off, kk, kDescS, k != 0);
           }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&q_full[qb]);
         }
+        tc_commit(&s_full[buf]);
+        tc_commit(&k_empty[k_slot]);
+        if (last) tc_commit(&q_empty[qb]);
       }
       __syncwarp();
+      if (++k_slot == L.nk) k_slot = 0, k_par ^= 1;
+      ++it;
     }
-    if constexpr (!kFp8)
-      for (int k = loaded > L.nq ? loaded - L.nq : 0; k < loaded; ++k)
-        mbar_wait(&q_full[k & 1], (k >> 1) & 1, kWaitLimitNs);
-  } else if constexpr (kFp8) {
-    // ---- FP8: codes to f16 tiles ------------------------------------------------------------
-    const int cw = warp - (kTreeSoftmaxWarps + 4);
-    auto convert = [&](uint32_t n, uint64_t* rfull, uint64_t* rempty, uint32_t raw_off,
-                       uint64_t* full, uint64_t* empty, uint32_t off, uint32_t slots) {
-      const uint32_t rs = n % L.raw, ds = n % slots;
-      wait(&rfull[rs], (n / L.raw) & 1);
-      wait(&empty[ds], ((n / slots) & 1) ^ 1);
-      if (!wait.dead) {
-        constexpr int LR = D / 16, RW = 32 / LR;   // lanes a row (16 codes each), rows a pass
-        const int seg = lane % LR, sub = lane / LR;
-        const uint8_t* src = smem + raw_off + rs * kCode + cw * 32 * D + lane * 16;
-        uint8_t* dst = smem + off + ds * kTile + (seg / 4) * (128 * 128);
-        const int k0 = (seg & 3) * 2, flip = seg >> 2;   // the upper block's lanes store in the other
-                                                         // order: 8 lanes then hit 8 different chunks
-#pragma unroll
-        for (int g = 0; g < 32; g += RW) {
-          const int t = cw * 32 + g + sub;
-          const uint4 v = *reinterpret_cast<const uint4*>(src + g * D);
-          uint4 a, b;
-          e4m3x4_to_f16x2(v.x, a.x, a.y);
-          e4m3x4_to_f16x2(v.y, a.z, a.w);
-          e4m3x4_to_f16x2(v.z, b.x, b.y);
-          e4m3x4_to_f16x2(v.w, b.z, b.w);
-          uint8_t* d = dst + t * 128;
-          *reinterpret_cast<uint4*>(d + (((k0 + flip) ^ (t & 7)) << 4)) = flip ? b : a;
-          *reinterpret_cast<uint4*>(d + (((k0 + 1 - flip) ^ (t & 7)) << 4)) = flip ? a : b;
-        }
-        fence_async_smem();
-      }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&rempty[rs]);
-        mbar_arrive(&full[ds]);
-      }
-    };
-    // in the order the MMAs take them: K 0, K 1, V 0, K 2, V 1, ...
-    uint32_t nk = 0, nv = 0;
+    if (issuer) tc_commit(&drained[0]);   // nothing leaves before the last MMA has completed
+    mbar_wait(&drained[0], 0, kWaitLimitNs);
+  } else if (warp == kTreeSoftmaxWarps + 3) {
+    // ---- O += P V issuer -------------------------------------------------------------------
+    Cursor c(p, sh);
+    constexpr bool kBf16 = std::is_same<M, __nv_bfloat16>::value;
+    constexpr uint32_t kDescO = mma_desc(kBf16, D, true);
+    const uint64_t v_desc = tile_desc(smem_u32(smem + L.v_off), blk_bytes, grp_bytes);
+    const uint32_t v_step = 2u * grp_bytes >> 4;   // 16 tokens
+    const bool issuer = elect_one();
+    uint32_t it = 0, v_slot = 0, v_par = 0;
     while (c.advance(p, sh)) {
-      convert(nk, rk_full, rk_empty, L.rawk_off, k_full, k_empty, L.k_off, L.nk);
-      ++nk;
-      if (nk >= 2) {
-        convert(nv, rv_full, rv_empty, L.rawv_off, v_full, v_empty, L.v_off, L.nv);
-        ++nv;
+      const uint32_t buf = it & 1;
+      const uint64_t vd = v_desc + v_slot * (kTile >> 4);
+      const uint32_t pa = tmem + kColS + buf * 128u, oc = tmem + kColO;
+      const int valid = c.w.s.n - c.kt * kTreeTokens;
+      const bool fresh = c.first();
+      wait(&v_full[v_slot], v_par);
+      wait(&p_full[buf], (it >> 1) & 1);
+      tc_fence_after();
+      if (!wait.dead && issuer) {
+        if (valid >= kTreeTokens) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ts(oc, pa + k * 8u, vd + k * v_step, kDescO, k != 0 || !fresh);
+          if constexpr (kSplit) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_ts(oc, pa + 64u + k * 8u, vd + k * v_step, kDescO, true);
+          }
+        } else {   // the sequence ends in this tile
+          const int steps = (valid + 15) / 16;
+#pragma unroll 1
+          for (int k = 0; k < steps; ++k) {
+            mma_ts(oc, pa + k * 8u, vd + k * v_step, kDescO, k != 0 || !fresh);
+            if constexpr (kSplit) mma_ts(oc, pa + 64u + k * 8u, vd + k * v_step, kDescO, true);
+          }
+        }
+        tc_commit(&o_full[buf]);
+        tc_commit(&v_empty[v_slot]);
+      }
+      __syncwarp();
+      if (++v_slot == L.nv) v_slot = 0, v_par ^= 1;
+      ++it;
+    }
+    if (issuer) tc_commit(&drained[1]);
+    mbar_wait(&drained[1], 0, kWaitLimitNs);
+  } else if constexpr (kFp8) {
+    // ---- FP8: loads of codes, conversion to f16 tiles, q -----------------------------------
+    // A warp loads and converts the same 32 rows of every tile, so that codes need no barrier between
+    // warps: it refills its part of a slot as soon as it has read it.
+    Cursor c(p, sh), ld(p, sh);
+    const int cw = warp - (kTreeSoftmaxWarps + 4);
+    const int box = p.c.box_tokens;   // 8 to 32
+    struct Load {
+      int z, kvh;    // lane's cache row (-2: none, -1: a bad page); kvh < 0: no more tiles
+    };
+    auto next_load = [&]() {
+      Load a{-2, -1};
+      if (!ld.advance(p, sh)) return a;
+      a.kvh = ld.w.kvh;
+      const int t = ld.kt * kTreeTokens + cw * 32 + lane * box;
+      if (lane * box < 32 && t < ld.w.s.n) {
+        const int entry =
+            p.c.paged ? __ldg(p.c.block_table + (long long)ld.w.b * p.c.max_blocks + t / p.c.page_size)
+                      : 0;
+        a.z = token_row(p.c, ld.w.b, t, entry);
+      }
+      return a;
+    };
+    auto issue = [&](const Load& a, const CUtensorMap* tm, uint64_t* full, uint32_t off, uint32_t slot) {
+      if (wait.dead) return;
+      uint64_t* b = &full[slot * kTreeConvertWarps + cw];
+      const int boxes = __popc(__ballot_sync(0xffffffffu, a.z != -2));
+      if (lane == 0) mbar_arrive_expect_tx(b, (uint32_t)(boxes * box) * D);
+      __syncwarp();
+      if (a.z != -2) {
+        if (a.z < 0) atomicOr(p.c.status, kStatusBadBlockTable);
+        const uint64_t pol = kv_policy(sh.row_tiles);
+        tma_load_3d(smem + off + slot * kCode + (uint32_t)(cw * 32 + lane * box) * D, tm, b, 0,
+                    a.z < 0 ? p.c.num_blocks * p.c.page_size : a.z, a.kvh, pol);   // bad: past the pool
+      }
+      __syncwarp();
+    };
+    auto convert = [&](uint64_t* rfull, uint32_t raw_off, uint32_t rs, uint32_t rpar, uint64_t* full,
+                       uint64_t* empty, uint32_t off, uint32_t ds, uint32_t dpar) {
+      wait(&rfull[rs * kTreeConvertWarps + cw], rpar);
+      wait(&empty[ds], dpar);
+      constexpr int LR = D / 16, RW = 32 / LR;   // lanes a row (16 codes each), rows a pass
+      const int seg = lane % LR, sub = lane / LR;
+      const uint8_t* src = smem + raw_off + rs * kCode + cw * 32 * D + lane * 16;
+      uint8_t* dst = smem + off + ds * kTile + (seg / 4) * 16384 + (cw * 32 + sub) * 128;
+      const int k0 = (seg & 3) * 2, flip = seg >> 2;   // the upper block's lanes store in the other
+                                                       // order: 8 lanes then hit 8 different chunks
+#pragma unroll
+      for (int g = 0; g < 32; g += 4 * RW) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(src + (g + j * RW) * D);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t7 = (g + j * RW + sub) & 7;
+          uint4 a, b;
+          e4m3x4_to_f16x2(v[j].x, a.x, a.y);
+          e4m3x4_to_f16x2(v[j].y, a.z, a.w);
+          e4m3x4_to_f16x2(v[j].z, b.x, b.y);
+          e4m3x4_to_f16x2(v[j].w, b.z, b.w);
+          uint8_t* d = dst + (g + j * RW) * 128;
+          *reinterpret_cast<uint4*>(d + (((k0 + flip) ^ t7) << 4)) = flip ? b : a;
+          *reinterpret_cast<uint4*>(d + (((k0 + 1 - flip) ^ t7) << 4)) = flip ? a : b;
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[ds]);
+    };
+    // tile n converts K n, loads K n + raw, converts V n - 1 and loads V n - 1 + raw
+    uint32_t n = 0, rk = 0, rk_par = 0, loads = 0;
+    Load nxt{-2, -1}, old{-2, -1};
+    for (uint32_t i = 0; i < (uint32_t)L.raw; ++i) {
+      const Load a = next_load();
+      if (a.kvh < 0) break;
+      issue(a, &tmk, rk_full, L.rawk_off, i);
+      issue(a, &tmv, rv_full, L.rawv_off, i);
+      ++loads;
+    }
+    nxt = next_load();
+    auto convert_v = [&](uint32_t i, uint32_t rv, uint32_t rv_par) {
+      convert(rv_full, L.rawv_off, rv, rv_par, v_full, v_empty, L.v_off, i & 1, ((i >> 1) & 1) ^ 1);
+      if (old.kvh >= 0) issue(old, &tmv, rv_full, L.rawv_off, rv);
+    };
+    while (c.advance(p, sh)) {
+      if (c.first()) {
+        // q: a thread's row as f16 times a power of two, so that its largest element lies in
+        // [2^14, 2^15), into TMEM
+        const int qb = c.piece & 1, rr = cw * 32 + lane, r = sh.row_tile * kTreeRows + rr;
+        wait(&q_empty[qb], ((c.piece >> 1) & 1) ^ 1);
+        tc_fence_after();
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(p.q) +
+            ((long long)(c.w.s.row0 + r / p.group) * p.c.hq + c.w.kvh * p.group + r % p.group) * D);
+        const bool have = r < c.w.s.T * p.group;
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+        float big = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < D / 8; ++j) {
+          const uint4 v = have ? __ldg(src + j) : none;
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_pair<__nv_bfloat16>(u[e]);
+            big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+        // 2^(14 - exponent of the largest), within what an int8 holds; 1 for a row of zeros
+        int s = big > 0.f && big < INFINITY ? 14 - ((int)(__float_as_uint(big) >> 23) - 127) : 0;
+        s = min(max(s, -112), 126);
+        const float mul = __uint_as_float((uint32_t)(s + 127) << 23);
+        const uint32_t q_addr = tmem + ((uint32_t)cw << 21) + kColQ + qb * (D / 2);
+#pragma unroll 1
+        for (int j = 0; j < D / 64; ++j) {
+          uint32_t w[32];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint4 v = have ? __ldg(src + j * 8 + k) : none;
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack_pair<__nv_bfloat16>(u[e]);
+              w[4 * k + e] = pack_pair<__half>(f.x * mul, f.y * mul);
+            }
+          }
+          tmem_st32(q_addr + j * 32, w);
+        }
+        qexp[qb * 128 + rr] = (signed char)-s;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[qb]);
+      }
+      // in the order that the MMAs take them: K 0, K 1, V 0, K 2, V 1, ...
+      convert(rk_full, L.rawk_off, rk, rk_par, k_full, k_empty, L.k_off, n & 1, ((n >> 1) & 1) ^ 1);
+      if (nxt.kvh >= 0) {
+        issue(nxt, &tmk, rk_full, L.rawk_off, rk);
+        ++loads;
+      }
+      const uint32_t rv = rk ? rk - 1 : L.raw - 1, rv_par = rk ? rk_par : rk_par ^ 1;
+      if (n >= 1) convert_v(n - 1, rv, rv_par);
+      old = nxt;
+      nxt = next_load();
+      if (++rk == (uint32_t)L.raw) rk = 0, rk_par ^= 1;
+      ++n;
+    }
+    if (n) convert_v(n - 1, rk ? rk - 1 : L.raw - 1, rk ? rk_par : rk_par ^ 1);
+    if (wait.dead) {   // never leave with copies in flight (otherwise each was waited for)
+      for (uint32_t k = loads > L.raw ? loads - L.raw : 0; k < loads; ++k) {
+        mbar_wait(&rk_full[k % L.raw * kTreeConvertWarps + cw], (k / L.raw) & 1, kWaitLimitNs);
+        mbar_wait(&rv_full[k % L.raw * kTreeConvertWarps + cw], (k / L.raw) & 1, kWaitLimitNs);
       }
     }
-    for (; nv < nk; ++nv)
-      convert(nv, rv_full, rv_empty, L.rawv_off, v_full, v_empty, L.v_off, L.nv);
   }
   __syncwarp();
   tc_fence_before();

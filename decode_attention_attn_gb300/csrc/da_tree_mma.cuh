@@ -8,20 +8,43 @@ namespace da {
 constexpr int kTreeRows = 128;       // query rows per tile: the M of tcgen05.mma
 constexpr int kTreeTokens = 128;     // KV tokens per tile
 
-// Warps: 8 softmax, K producer, V producer, MMA issuer, q producer, and for FP8 caches 4 that
-// convert codes to f16 tiles.
+// Warps: 8 softmax, then two loaders (16-bit caches: K with q, and V), the issuer of S, the issuer
+// of O, and for FP8 caches 4 that load codes and convert them to f16 tiles.
 constexpr int kTreeSoftmaxWarps = 8;
 constexpr int kTreeConvertWarps = 4;
 __host__ __device__ constexpr int tree_threads(bool fp8) {
   return (kTreeSoftmaxWarps + 4 + (fp8 ? kTreeConvertWarps : 0)) * 32;
 }
 
-// A 16-bit tile of 128 rows (tokens or query rows) is D / 64 blocks of [128 rows][128 bytes], rows
-// swizzled in groups of 8 (1 KB), as the TMA's 128-byte swizzle writes them and tcgen05.mma reads them.
+// Registers: compiled (and launched) with tree_launch_regs a thread; the softmax warps then take more
+// from the others. A spilled register costs an L2 round trip here, with all of L1 in use as shared
+// memory: at 128 registers for everyone the FP8 kernel spent most of its time on spills.
+__host__ __device__ constexpr int tree_launch_regs(bool fp8) { return fp8 ? 128 : 168; }
+__host__ __device__ constexpr int tree_softmax_regs(int D, bool fp8) {
+  return !fp8 ? 208 : D == 128 ? 152 : 168;
+}
+__host__ __device__ constexpr int tree_other_regs(int D, bool fp8) {
+  return fp8 && D == 128 ? 104 : 88;
+}
+__host__ __device__ constexpr bool tree_regs_fit(int D, bool fp8) {
+  return kTreeSoftmaxWarps * tree_softmax_regs(D, fp8) +
+             (tree_threads(fp8) / 32 - kTreeSoftmaxWarps) * tree_other_regs(D, fp8) ==
+         tree_threads(fp8) / 32 * tree_launch_regs(fp8);
+}
+static_assert(tree_regs_fit(64, false) && tree_regs_fit(128, false) && tree_regs_fit(64, true) &&
+                  tree_regs_fit(128, true),
+              "the register split must fit the launch allocation");
+
+// A 16-bit tile of 128 rows (tokens or query rows) of D elements in shared memory, as tcgen05.mma
+// reads it with the 128-byte swizzle: groups of 8 rows x 64 elements (1 KB), rows of 128 bytes. The
+// groups of a 64-element block follow one another and the blocks too (q, contiguous caches, converted
+// codes); a paged cache's tiles hold the D / 64 blocks of an 8-row group side by side, so that one TMA
+// box brings whole rows of a page (half as many boxes: the loader's issue rate, about 100 cycles a box,
+// is what 16-token pages run into).
 __host__ __device__ constexpr uint32_t tree_tile_bytes(int D) { return 128u * D * 2u; }
 
 struct TreeLayout {
-  int nk, nv, nq;        // 16-bit K, V and q tiles
+  int nk, nv, nq;        // 16-bit K and V tiles; q tiles (16-bit caches: shared memory, FP8: TMEM)
   int raw;               // FP8: tiles of codes, for K and for V each
   uint32_t q_off, k_off, v_off, rawk_off, rawv_off, bar_off, exch_off, qexp_off, misc_off, total;
 };
@@ -29,19 +52,12 @@ __host__ __device__ constexpr TreeLayout tree_layout(int D, bool fp8) {
   TreeLayout L{};
   const uint32_t tile = tree_tile_bytes(D), code = 128u * D;
   L.nq = 2;
-  if (!fp8) {
-    // 160 KB (D = 128: 64 KB of K and V ahead of the softmax on average) or 144 KB
-    L.nk = D == 128 ? 2 : 4;
-    L.nv = D == 128 ? 3 : 5;
-    L.raw = 0;
-  } else {
-    L.nk = 2;
-    L.nv = D == 128 ? 1 : 2;
-    L.raw = D == 128 ? 2 : 4;
-  }
+  L.nk = fp8 || D == 128 ? 2 : 4;
+  L.nv = fp8 ? 2 : D == 128 ? 3 : 5;
+  L.raw = !fp8 ? 0 : D == 128 ? 3 : 4;
   uint32_t off = 0;
   L.q_off = off;
-  off += L.nq * tile;
+  if (!fp8) off += L.nq * tile;
   L.k_off = off;
   off += L.nk * tile;
   L.v_off = off;
@@ -51,22 +67,21 @@ __host__ __device__ constexpr TreeLayout tree_layout(int D, bool fp8) {
   L.rawv_off = off;
   off += L.raw * code;
   L.bar_off = off;
-  off += 48 * 8;
+  off += 64 * 8;
   L.exch_off = off;           // row maxima of the two column halves, two tiles; scratch of the schedule
   off += 2 * 2 * 128 * 4;
   L.qexp_off = off;           // FP8: q's power of two per row
   off += 2 * 128;
   L.misc_off = off;           // TMEM address, abort flag, odd-token word
   off += 32;
-  L.total = off;
+  // more than half of an SM's shared memory: one CTA an SM, so each has the SM's whole TMEM
+  L.total = off > 120u * 1024 ? off : 120u * 1024;
   return L;
 }
 static_assert(tree_layout(128, false).total <= kSmemLimit, "");
 static_assert(tree_layout(128, true).total <= kSmemLimit, "");
 static_assert(tree_layout(64, false).total <= kSmemLimit, "");
 static_assert(tree_layout(64, true).total <= kSmemLimit, "");
-// more than half of an SM's shared memory: one CTA an SM, so each has the SM's whole TMEM
-static_assert(tree_layout(64, false).total > 116736 && tree_layout(64, true).total > 116736, "");
 static_assert(sizeof(TreeScratch) <= 2 * 2 * 128 * 4, "the schedule's scratch lies in the exchange");
 
 // The kernel of a cache type (da_dtype, or FP8), head_dim and output; null: not built.

@@ -334,7 +334,7 @@ int raise_smem(const void* fn, size_t smem, int regs) {
 }
 
 int encode(CUtensorMap* map, int es, int rank, const void* base, const cuuint64_t* dims,
-           const cuuint64_t* strides, const cuuint32_t* box, bool swizzle,
+           const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle,
            CUtensorMapL2promotion promote) {
   auto fn = encode_fn();
   if (!fn) {
@@ -345,8 +345,7 @@ int encode(CUtensorMap* map, int es, int rank, const void* base, const cuuint64_
   const CUresult r =
       fn(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
          (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-         promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     g_cuda_error = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
     return DA_ERR_CUDA;
@@ -354,7 +353,8 @@ int encode(CUtensorMap* map, int es, int rank, const void* base, const cuuint64_
   return DA_OK;
 }
 
-// [tokens, Hkv, D] cache, one box = `box` tokens of one KV head. FP8 caches: rows of codes. 16-bit
+// [tokens, Hkv, D] cache, one box = `box` tokens of one KV head. FP8 caches: rows of codes, swizzled
+// as wide as they are. 16-bit
 // caches in 128-byte-swizzled blocks of 64 elements: contiguous ones as [Hkv, D / 64, tokens, 64], a
 // box one block of 128 tokens; paged ones as [Hkv, tokens / 8, D / 64, 8, 64], a box whole rows.
 int kv_map(const da_tree_plan& pl, const void* base, int box, CUtensorMap* map) {
@@ -365,7 +365,8 @@ int kv_map(const da_tree_plan& pl, const void* base, int box, CUtensorMap* map) 
   if (p.kv_fp8) {
     const cuuint64_t dims[3] = {D, tokens, H}, strides[2] = {H * D, D};
     const cuuint32_t b[3] = {(cuuint32_t)D, (cuuint32_t)box, 1u};
-    return encode(map, 1, 3, base, dims, strides, b, false,
+    return encode(map, 1, 3, base, dims, strides, b,
+                  D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
   }
   const auto promote =
@@ -374,11 +375,11 @@ int kv_map(const da_tree_plan& pl, const void* base, int box, CUtensorMap* map) 
     const cuuint64_t dims[5] = {64, 8, D / 64, tokens / 8, H};
     const cuuint64_t strides[4] = {H * D * 2, 128, H * D * 16, D * 2};
     const cuuint32_t b[5] = {64u, 8u, (cuuint32_t)D / 64, (cuuint32_t)box / 8, 1u};
-    return encode(map, 2, 5, base, dims, strides, b, true, promote);
+    return encode(map, 2, 5, base, dims, strides, b, CU_TENSOR_MAP_SWIZZLE_128B, promote);
   }
   const cuuint64_t dims[4] = {64, tokens, D / 64, H}, strides[3] = {H * D * 2, 128, D * 2};
   const cuuint32_t b[4] = {64u, (cuuint32_t)box, 1u, 1u};
-  return encode(map, 2, 4, base, dims, strides, b, true, promote);
+  return encode(map, 2, 4, base, dims, strides, b, CU_TENSOR_MAP_SWIZZLE_128B, promote);
 }
 
 // [rows, Hq, D] q, one box = the G heads of a KV head of 128 / G drafted tokens, one 64-element block.
@@ -387,7 +388,8 @@ int q_map(const da_tree_plan& pl, const void* base, int rows, CUtensorMap* map) 
   const cuuint32_t G = (cuuint32_t)pl.cache.group;
   const cuuint64_t dims[4] = {64, H, (cuuint64_t)rows, D / 64}, strides[3] = {D * 2, H * D * 2, 128};
   const cuuint32_t b[4] = {64u, G, (cuuint32_t)kTreeRows / G, 1u};
-  return encode(map, 2, 4, base, dims, strides, b, true, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+  return encode(map, 2, 4, base, dims, strides, b, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
 }  // namespace
@@ -545,14 +547,12 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
     const void* fn = tree_mma_kernel(pr.qkv_dtype, pr.kv_fp8 != 0, pr.head_dim,
                                      !pr.kv_fp8 || pr.out_dtype == DA_F32);
     if (!fn) return DA_ERR_UNSUPPORTED;
-    // FP8 tiles are loaded by the warps that convert them, 32 rows each
-    const int most = pr.kv_fp8 ? kTreeTokens / kTreeConvertWarps : kTreeTokens;
-    p.c.box_tokens = pr.paged ? std::min(pr.page_size, most) : most;
+    p.c.box_tokens = pr.paged ? std::min(pr.page_size, kTreeTokens) : kTreeTokens;
     CUtensorMap tmq, tmk, tmv;
     int rc = q_map(pl, a.q, a.rows, &tmq);
     if (rc == DA_OK) rc = kv_map(pl, a.k_cache, p.c.box_tokens, &tmk);
     if (rc == DA_OK) rc = kv_map(pl, a.v_cache, p.c.box_tokens, &tmv);
-    if (rc == DA_OK) rc = raise_smem(fn, pl.smem_bytes, tree_launch_regs(pr.kv_fp8 != 0));
+    if (rc == DA_OK) rc = raise_smem(fn, pl.smem_bytes, pr.kv_fp8 ? tree_launch_regs(true) : 0);
     if (rc != DA_OK) return rc;
     const void* vc = a.v_cache;
     void* kargs[5] = {&p, &tmq, &tmk, &tmv, &vc};

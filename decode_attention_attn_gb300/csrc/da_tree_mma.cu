@@ -127,6 +127,31 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 // Shared-memory operand descriptor, 128-byte swizzle: `block` is the distance between 64-element
 // blocks along the contiguous dimension (read where that is M or N), `group` that between 8-row
 // groups.
@@ -138,6 +163,12 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t block, uin
 __host__ __device__ constexpr uint32_t mma_desc(bool bf16, int n, bool trans_b) {
   return 1u << 4 | (bf16 ? 1u : 0u) << 7 | (bf16 ? 1u : 0u) << 10 | (trans_b ? 1u : 0u) << 16 |
          (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+
+__device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 __device__ __forceinline__ void fence_async_smem() {
@@ -152,6 +183,42 @@ __device__ __forceinline__ uint64_t kv_policy(int row_tiles) {
   return pol;
 }
 
+// mbar_try_wait that may sleep up to 1 us before it answers no: a poll that spins takes issue slots from
+// the softmax.
+__device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Barrier `id` of n threads that tells whether any of them has v set.
+__device__ __forceinline__ bool bar_any(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
 // A pipeline wait that gives up, for every warp of the CTA, when one of them ran out of time: from
 // then on nothing waits, no copy or MMA is issued, and every warp walks to its end (through all the
 // CTA's barriers).
@@ -163,12 +230,12 @@ struct Waiter {
   // warp-uniform
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
     if (dead) return;
-    bool ok = mbar_try_wait(bar, parity);
+    bool ok = mbar_sleep_wait(bar, parity);
     if (!__all_sync(0xffffffffu, ok)) {
       const unsigned long long t0 = global_timer_ns();
       while (!ok) {
 #pragma unroll 1
-        for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+        for (int i = 0; i < 64 && !ok; ++i) ok = mbar_sleep_wait(bar, parity);
         if (ok || *reinterpret_cast<volatile int*>(abort_flag)) break;
         if (global_timer_ns() - t0 > limit) {
           atomicOr(status, kStatusTimeout);
@@ -237,23 +304,24 @@ __device__ __forceinline__ float2 unpack_pair(uint32_t u) {
   }
 }
 
-// Columns c < 64 of a half tile that a row attends to: its context (t < ctx) and its drafted tokens'
-// bits; `off` = ctx minus the half tile's first token.
-__device__ __forceinline__ unsigned long long visible(int off, unsigned long long word) {
-  if (off >= 64) return ~0ull;
-  if (off > 0) return ((1ull << off) - 1ull) | word << off;
-  return off > -64 ? word >> -off : 0ull;
+// Columns c < 32 of a quarter tile that a row attends to: its context (t < ctx) and its drafted tokens'
+// bits; `off` = ctx minus the quarter's first token.
+__device__ __forceinline__ uint32_t visible(int off, unsigned long long word) {
+  if (off >= 32) return ~0u;
+  if (off > 0) return ((1u << off) - 1u) | (uint32_t)word << off;
+  return off > -64 ? (uint32_t)(word >> -off) : 0u;
 }
 
-// Adds what drafted tokens' V rows hold that is not finite (`odd`, tokens a row attends to) to this
-// half of the row's stored result: the infinities and NaN that were taken out before the product. Rare.
+// Adds what drafted tokens' V rows hold that is not finite (`odd`, tokens a row attends to) to 32
+// columns of the row's stored result: the infinities and NaN that were taken out before the product.
+// Rare.
 template <typename T, int D>
 __device__ __noinline__ void add_odd(const TreeParams& p, int b, int ctx, int kvh,
-                                     unsigned long long odd, const void* v_cache, int half, void* dst,
+                                     unsigned long long odd, const void* v_cache, int col0, void* dst,
                                      long long row, int out_type) {
   constexpr bool kFp8 = std::is_same<T, fp8e4m3>::value;
 #pragma unroll 1
-  for (int col = half * (D / 2); col < (half + 1) * (D / 2); ++col) {
+  for (int col = col0; col < col0 + 32; ++col) {
     float sum = 0.f;
 #pragma unroll 1
     for (unsigned long long rest = odd; rest; rest &= rest - 1) {
@@ -303,9 +371,11 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   uint64_t* p_full = s_full + 2;          // P of a buffer written, O rescaled
   uint64_t* o_full = p_full + 2;          // O += P V done, tiles in turn
   uint64_t* drained = o_full + 2;
-  uint64_t* rk_full = drained + 2;        // FP8: tiles of codes, a barrier for each warp's rows
-  uint64_t* rv_full = rk_full + L.raw * kTreeConvertWarps;
-  static_assert(2 * L.nk + 2 * L.nv + 2 * L.nq + 8 + 2 * L.raw * kTreeConvertWarps <= 64, "");
+  uint64_t* rk_full = drained + 2;        // FP8: tiles of codes
+  uint64_t* rk_empty = rk_full + L.raw;
+  uint64_t* rv_full = rk_empty + L.raw;
+  uint64_t* rv_empty = rv_full + L.raw;
+  static_assert(2 * L.nk + 2 * L.nv + 2 * L.nq + 8 + 4 * L.raw <= 40, "");
   float* exch = reinterpret_cast<float*>(smem + L.exch_off);
   signed char* qexp = reinterpret_cast<signed char*>(smem + L.qexp_off);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L.misc_off);
@@ -314,8 +384,13 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const TreeShare sh = tree_schedule<kThreadsT>(p, *reinterpret_cast<TreeScratch*>(exch));
-  if (sh.u1 <= sh.u0) return;   // the whole CTA
+  // the share lies in shared memory: it is looked at once a piece, and registers are short
+  TreeShare& sh = *reinterpret_cast<TreeShare*>(smem + L.misc_off + 16);
+  {
+    const TreeShare mine = tree_schedule<kThreadsT>(p, *reinterpret_cast<TreeScratch*>(exch));
+    if (mine.u1 <= mine.u0) return;   // the whole CTA
+    if (tid == 0) sh = mine;
+  }
   if (tid == 0) {
     for (int i = 0; i < L.nk; ++i) {
       mbar_init(&k_full[i], kFp8 ? kTreeConvertWarps : 1);
@@ -336,7 +411,12 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
     }
     mbar_init(&drained[0], 1);
     mbar_init(&drained[1], 1);
-    for (int i = 0; i < 2 * L.raw * kTreeConvertWarps; ++i) mbar_init(&rk_full[i], 1);
+    for (int i = 0; i < L.raw; ++i) {
+      mbar_init(&rk_full[i], 1);
+      mbar_init(&rk_empty[i], kTreeConvertWarps);
+      mbar_init(&rv_full[i], 1);
+      mbar_init(&rv_empty[i], kTreeConvertWarps);
+    }
     // the swizzled tiles need a 1 KB boundary; elsewhere nothing may run
     *abort_flag = (smem_u32(smem) & 1023u) ? 1 : 0;
     if (*abort_flag) atomicOr(p.c.status, kStatusTimeout);
@@ -352,29 +432,33 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   const bool paired = !kFp8 && p.c.paged;
   const uint32_t blk_bytes = paired ? 1024u : 16384u, grp_bytes = paired ? CH * 1024u : 1024u;
   Waiter wait{abort_flag, p.c.status, kWaitLimitNs, *abort_flag != 0};
-  if (warp < kTreeSoftmaxWarps)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(tree_softmax_regs(D, kFp8)));
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(tree_other_regs(D, kFp8)));
+  if constexpr (kFp8) {
+    if (warp < kTreeSoftmaxWarps)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(tree_softmax_regs(true)));
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(tree_other_regs(true)));
+  }
 
   if (warp < kTreeSoftmaxWarps) {
     // ---- softmax -----------------------------------------------------------------------
     Cursor c(p, sh);
-    const int half = warp >> 2, quarter = warp & 3;
+    const int quarter = warp & 3, cq = warp >> 2;      // 32 rows, 32 of S's 128 columns
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)quarter << 21);   // TMEM lane quarter * 32
+    float* ex = exch + row;
     uint32_t it = 0;
     float m = -INFINITY, l = 0.f, factor = p.qscale;
     bool active = false;
     int r = 0;
     unsigned long long word = 0;
     while (c.advance(p, sh)) {
-      const int R = c.w.s.T * p.group;
       if (c.first()) {
+        const int R = c.w.s.T * p.group;
         r = sh.row_tile * kTreeRows + row;
         active = sh.row_tile * kTreeRows + quarter * 32 < R;   // this warp has rows
         const int i = r / p.group;
         word = r < R ? tree_word(p, c.w.s.row0 + i, i, c.w.s.T) : 0ull;
+        if (r >= R) r = -1;
         m = -INFINITY;
         l = 0.f;
         if constexpr (kFp8) {
@@ -386,88 +470,121 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
         }
       }
       const int buf = it & 1;
-      const uint32_t s_addr = lane_addr + kColS + (uint32_t)buf * 128u;
+      const uint32_t s_addr = lane_addr + kColS + (uint32_t)buf * 128u + cq * 32u;
       const int tok0 = c.kt * kTreeTokens;
       const bool tail = tok0 + kTreeTokens > c.w.s.ctx;   // drafted tokens or the end in this tile
-      // O of tile it - 2: complete, as S of this tile waited for it; waiting for every phase of the
-      // two barriers in turn makes a parity name one phase
-      if (it >= 2) wait(&o_full[buf], ((it - 2) >> 1) & 1);
+      // S of this tile was issued after O of tile it - 2 had completed, so that a parity of o_full
+      // names one phase below
       wait(&s_full[buf], (it >> 1) & 1);
       tc_fence_after();
       if (active) {
-        float x[64];
-        tmem_ld32(s_addr + half * 64, reinterpret_cast<uint32_t*>(x));
-        tmem_ld32(s_addr + half * 64 + 32, reinterpret_cast<uint32_t*>(x) + 32);
-        tmem_wait_ld();
-        const f32x2 f2 = f2_pack(factor, factor);
+        // The exchange of row maxima between the four warps of a row is skipped while no row exceeds
+        // its reference by more than kRescale: one barrier that reduces a predicate instead of two and
+        // a round trip through shared memory.
+        auto tile = [&](auto tail_c) {
+          constexpr bool kTail = decltype(tail_c)::value;
+          uint32_t vis = ~0u;
+          if constexpr (kTail) vis = visible(c.w.s.ctx - tok0 - cq * 32, word);
+          float top;   // largest logit of the 32 columns (-inf: none seen)
+          {
+            float x[32];
+            tmem_ld32(s_addr, reinterpret_cast<uint32_t*>(x));
+            tmem_wait_ld();
+            const float none = p.qscale >= 0.f ? -INFINITY : INFINITY;
+            if constexpr (kTail) {
 #pragma unroll
-        for (int k = 0; k < 64; k += 2) f2_unpack(f2_mul(f2_pack(x[k], x[k + 1]), f2), x[k], x[k + 1]);
-        if (tail) {
-          const unsigned long long vis = visible(c.w.s.ctx - tok0 - half * 64, word);
+              for (int k = 0; k < 32; ++k)
+                if (!(vis >> k & 1u)) x[k] = none;
+            }
+            float mx[2] = {x[0], x[1]};
+            if (p.qscale >= 0.f) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (!((k < 32 ? (uint32_t)vis : (uint32_t)(vis >> 32)) >> (k & 31) & 1u)) x[k] = -INFINITY;
-        }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
+              for (int k = 2; k < 32; k += 2) mx[k >> 1 & 1] = max3(mx[k >> 1 & 1], x[k], x[k + 1]);
+              mx[0] = fmaxf(mx[0], mx[1]);
+            } else {
 #pragma unroll
-        for (int k = 4; k < 64; ++k) mx[k & 3] = fmaxf(mx[k & 3], x[k]);
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // the other half's maximum; P may be written over S once both have read it
-        float* ex = exch + buf * 256;
-        ex[half * 128 + row] = top;
-        named_bar_sync(1 + quarter, 64);
-        top = fmaxf(top, ex[(half ^ 1) * 128 + row]);
-        bool move = false;
-        float f = 1.f;
-        if (c.first()) {
-          m = top;
-        } else if (top > m + kRescale) {
-          f = fast_exp2(m - top);
-          m = top;
-          l *= f;
-          move = true;
-        }
-        if (__any_sync(0xffffffffu, move)) {
-          // O so far, relative to the new reference: this half's columns
-          wait(&o_full[buf ^ 1], ((it - 1) >> 1) & 1);
-          tc_fence_after();
-#pragma unroll 1
-          for (int cc = 0; cc < D / 64; ++cc) {
-            uint32_t o[32];
-            const uint32_t a = lane_addr + kColO + half * (D / 2) + cc * 32;
-            tmem_ld32(a, o);
+              for (int k = 2; k < 32; k += 2) mx[k >> 1 & 1] = min3(mx[k >> 1 & 1], x[k], x[k + 1]);
+              mx[0] = fminf(mx[0], mx[1]);
+            }
+            top = mx[0] == none ? -INFINITY : mx[0] * factor;
+          }
+          const bool fresh = c.first();
+          if (bar_any(1 + quarter, 128, fresh || top > m + kRescale)) {
+            ex[cq * 128] = top;
+            named_bar_sync(1 + quarter, 128);
+            top = fmaxf(fmaxf(ex[0], ex[128]), fmaxf(ex[256], ex[384]));
+            bool move = false;
+            float f = 1.f;
+            if (fresh) {
+              m = top;
+            } else if (top > m + kRescale) {
+              f = fast_exp2(m - top);
+              m = top;
+              l *= f;
+              move = true;
+            }
+            if (__any_sync(0xffffffffu, move)) {
+              // O so far, relative to the new reference: 32 columns a warp
+              wait(&o_full[buf ^ 1], ((it - 1) >> 1) & 1);
+              tc_fence_after();
+              if (cq * 32 < D) {
+                uint32_t o[32];
+                const uint32_t a = lane_addr + kColO + cq * 32;
+                tmem_ld32(a, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st32(a, o);
+                tmem_wait_st();
+              }
+            }
+          }
+          // P over the columns of S that it comes from (S is read once more: registers are short), 8
+          // columns of hi and 8 of lo for every 16 tokens
+          const float ref = m == -INFINITY ? 0.f : m;
+          const f32x2 f2 = f2_pack(factor, factor), neg = f2_pack(-ref, -ref);
+          f32x2 sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x[16];
+            uint32_t pk[16];
+            tmem_ld16(s_addr + h * 16, reinterpret_cast<uint32_t*>(x));
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st32(a, o);
+            for (int k = 0; k < 16; k += 2) {
+              f32x2 d = neg;
+              f2_fma(d, f2_pack(x[k], x[k + 1]), f2);
+              float a, b;
+              f2_unpack(d, a, b);
+              if constexpr (kTail) {
+                if (!(vis >> (h * 16 + k) & 1u)) a = -INFINITY;
+                if (!(vis >> (h * 16 + k + 1) & 1u)) b = -INFINITY;
+              }
+              a = fast_exp2(a);
+              b = fast_exp2(b);
+              const f32x2 e = f2_pack(a, b);
+              sum[k >> 1 & 1] = f2_add(sum[k >> 1 & 1], e);
+              const uint32_t hi = pack_pair<M>(a, b);
+              pk[k / 2] = hi;
+              if constexpr (kSplit) {
+                const float2 hf = unpack_pair<M>(hi);
+                float da, db;
+                f2_unpack(f2_add(e, f2_pack(-hf.x, -hf.y)), da, db);
+                pk[8 + k / 2] = pack_pair<M>(da, db);
+              }
+            }
+            if constexpr (kSplit) tmem_st16(s_addr + h * 16, pk);
+            else tmem_st8(s_addr + h * 16, pk);
+          }
+          {
+            float a, b;
+            f2_unpack(f2_add(sum[0], sum[1]), a, b);
+            l += a + b;
           }
           tmem_wait_st();
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
-        const f32x2 neg = f2_pack(-ref, -ref);
-        uint32_t hi[32];
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < 64; k += 2) {
-          float a, b;
-          f32x2 d = f2_pack(x[k], x[k + 1]);
-          asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(neg));
-          f2_unpack(d, a, b);
-          a = fast_exp2(a);
-          b = fast_exp2(b);
-          sum[k & 2] += a;
-          sum[(k & 2) + 1] += b;
-          const uint32_t h = pack_pair<M>(a, b);
-          hi[k / 2] = h;
-          if constexpr (kSplit) {
-            const float2 hf = unpack_pair<M>(h);
-            x[k / 2] = __uint_as_float(pack_pair<M>(a - hf.x, b - hf.y));
-          }
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st32(s_addr + half * 32, hi);
-        if constexpr (kSplit) tmem_st32(s_addr + 64 + half * 32, reinterpret_cast<uint32_t*>(x));
-        tmem_wait_st();
+        };
+        if (tail) tile(std::true_type{});
+        else tile(std::false_type{});
       }
       if (tail) {
         // V rows that the MMA reads past the sequence's end are cleared, and values that are not
@@ -476,10 +593,10 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
         const uint32_t vs = it % L.nv;
         wait(&v_full[vs], (it / L.nv) & 1);
         const int valid = min(kTreeTokens, c.w.s.n - tok0);
-        const int t = tid & 127, end = (valid + 15) / 16 * 16;
-        uint8_t* vrow = smem + L.v_off + vs * kTile + (t >> 3) * grp_bytes + (t & 7) * 128;
-        for (int blk = tid >> 7; blk < CH; blk += 2) {
-          uint4* v4 = reinterpret_cast<uint4*>(vrow + blk * blk_bytes);
+        const int t = tid & 127, end = (valid + 15) / 16 * 16, blk = tid >> 7;
+        if (blk < CH) {
+          uint4* v4 = reinterpret_cast<uint4*>(smem + L.v_off + vs * kTile + (t >> 3) * grp_bytes +
+                                               (t & 7) * 128 + blk * blk_bytes);
           if (t >= valid && t < end) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) v4[(k + t) & 7] = make_uint4(0u, 0u, 0u, 0u);
@@ -488,7 +605,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
             bool found = false;
 #pragma unroll 1
             for (int k = 0; k < 8; ++k) {
-              uint4 v = v4[(k + t) & 7];
+              const uint4 v = v4[(k + t) & 7];
               uint32_t w[4] = {v.x, v.y, v.z, v.w};
               bool here = false;
 #pragma unroll
@@ -520,45 +637,38 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
         wait(&o_full[buf], (it >> 1) & 1);
         tc_fence_after();
         if (active) {
-          float* ex = exch + (buf ^ 1) * 256;
-          named_bar_sync(1 + quarter, 64);   // the other half has read its maximum of the tile before
-          ex[half * 128 + row] = l;
-          named_bar_sync(1 + quarter, 64);
-          const float total = l + ex[(half ^ 1) * 128 + row];
+          named_bar_sync(1 + quarter, 128);   // all have read the maxima
+          ex[cq * 128] = l;
+          named_bar_sync(1 + quarter, 128);
+          const float total = (ex[0] + ex[128]) + (ex[256] + ex[384]);
           const float inv = total == 0.f ? 0.f : 1.f / total;
-          const float lg = total == 0.f ? -INFINITY : m + log2f(total);
           const unsigned long long strange = *odd & word;
-          const int i = r / p.group, h = c.w.kvh * p.group + r % p.group;
-          const long long orow = (long long)(c.w.s.row0 + i) * p.c.hq + h;
-          const long long prow =
-              tree_slot(sh.owner, c.w.head, sh.row_tile, sh.row_tiles) * kTreeRows + row;
-          if (half == 0 && r < R) {
-            if (!c.w.whole) p.part_l[prow] = lg;
-            else if (p.out_lse) p.out_lse[orow] = lg * 0.69314718055994531f;
+          const int col = cq * 32;
+          const bool whole = c.w.whole;
+          // the row of out (and lse), or of the partials
+          const long long at =
+              whole ? (long long)(c.w.s.row0 + r / p.group) * p.c.hq + c.w.kvh * p.group + r % p.group
+                    : tree_slot(sh.owner, c.w.head, sh.row_tile, sh.row_tiles) * kTreeRows + row;
+          if (cq == 0 && r >= 0) {
+            const float lg = total == 0.f ? -INFINITY : m + log2f(total);
+            if (!whole) p.part_l[at] = lg;
+            else if (p.out_lse) p.out_lse[at] = lg * 0.69314718055994531f;
           }
-#pragma unroll 1
-          for (int cc = 0; cc < D / 64; ++cc) {
-            const int col = half * (D / 2) + cc * 32;
+          if (col < D) {
             float o[32];
             tmem_ld32(lane_addr + kColO + col, reinterpret_cast<uint32_t*>(o));
             tmem_wait_ld();
-            if (r >= R) continue;
-            if (!c.w.whole) {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + col);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv,
-                                     o[4 * k + 3] * inv);
-            } else {
-              const float g = inv * p.v_scale;
-              if (p.c.out_dtype == kOutF32) {
-                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow * D + col);
+            if (r >= 0) {
+              const float g = whole ? inv * p.v_scale : inv;
+              if (!whole || p.c.out_dtype == kOutF32) {
+                float4* dst = reinterpret_cast<float4*>(
+                    (whole ? static_cast<float*>(p.out) : p.part_o) + at * D + col);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                   dst[k] = make_float4(o[4 * k] * g, o[4 * k + 1] * g, o[4 * k + 2] * g,
                                        o[4 * k + 3] * g);
               } else {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow * D + col);
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + col);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   uint32_t w[4];
@@ -571,12 +681,11 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
                   dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
               }
+              if (strange)
+                add_odd<T, D>(p, c.w.b, c.w.s.ctx, c.w.kvh, strange, v_cache, col,
+                              whole ? p.out : p.part_o, at, whole ? p.c.out_dtype : (int)kOutF32);
             }
           }
-          if (strange && r < R)
-            add_odd<T, D>(p, c.w.b, c.w.s.ctx, c.w.kvh, strange, v_cache, half,
-                          c.w.whole ? p.out : p.part_o, c.w.whole ? orow : prow,
-                          c.w.whole ? p.c.out_dtype : (int)kOutF32);
         }
         // every warp has read `odd`; clear it for the next piece
         named_bar_sync(5, kTreeSoftmaxWarps * 32);
@@ -586,78 +695,79 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
       ++it;
     }
   } else if (warp < kTreeSoftmaxWarps + 2) {
-    if constexpr (!kFp8) {
-      // ---- loaders: K with q, and V ------------------------------------------------------
-      Cursor c(p, sh);
-      const bool is_v = warp != kTreeSoftmaxWarps;
-      const CUtensorMap* tm = is_v ? &tmv : &tmk;
-      uint64_t* full = is_v ? v_full : k_full;
-      uint64_t* empty = is_v ? v_empty : k_empty;
-      const uint32_t slots = is_v ? L.nv : L.nk;
-      uint8_t* const ring = smem + (is_v ? L.v_off : L.k_off);
-      if (lane == 0) prefetch_tensormap(tm);
-      const uint64_t pol = kv_policy(sh.row_tiles);
-      // Paged: lane i loads the i-th run of `box` tokens, whole rows. Contiguous: lane i loads block i.
-      const int box = p.c.box_tokens;
-      auto lookup = [&](int kt) {   // lane's cache row; -2: nothing to load, -1: a bad page
-        const int t = kt * kTreeTokens + (p.c.paged ? lane * box : 0);
-        if (p.c.paged ? lane * box >= kTreeTokens || t >= c.w.s.n : lane >= CH) return -2;
-        const int entry =
-            p.c.paged ? __ldg(p.c.block_table + (long long)c.w.b * p.c.max_blocks + t / p.c.page_size)
-                      : 0;
-        return token_row(p.c, c.w.b, t, entry);
-      };
-      const uint32_t lane_off = p.c.paged ? (uint32_t)(lane * box / 8) * grp_bytes : lane * blk_bytes;
-      const uint32_t lane_bytes = (uint32_t)box * 128u * (p.c.paged ? CH : 1);
-      uint32_t slot = 0, par = 1, it = 0, issued = 0;
-      int z = -2, loaded = 0;
-      while (c.advance(p, sh)) {
-        if (c.first()) {
-          z = lookup(c.kt);
-          if (!is_v) {
-            const int qb = c.piece & 1;
-            const int i0 = sh.row_tile * (kTreeRows / p.group);   // the tile's first drafted token
-            wait(&q_empty[qb], ((c.piece >> 1) & 1) ^ 1);
-            if (!wait.dead) {
-              if (lane == 0) mbar_arrive_expect_tx(&q_full[qb], kTile);
-              __syncwarp();
-              if (lane < CH)
-                tma_load_4d(smem + L.q_off + qb * kTile + lane * (128 * 128), &tmq, &q_full[qb], 0,
-                            c.w.kvh * p.group, c.w.s.row0 + i0, lane, pol);
-              ++loaded;
-            }
+    // ---- loaders: K (with q, for 16-bit caches) and V ------------------------------------------
+    Cursor c(p, sh);
+    const bool is_v = warp != kTreeSoftmaxWarps;
+    const CUtensorMap* tm = is_v ? &tmv : &tmk;
+    uint64_t* full = kFp8 ? (is_v ? rv_full : rk_full) : (is_v ? v_full : k_full);
+    uint64_t* empty = kFp8 ? (is_v ? rv_empty : rk_empty) : (is_v ? v_empty : k_empty);
+    const uint32_t slots = kFp8 ? L.raw : is_v ? L.nv : L.nk;
+    uint8_t* const ring = smem + (kFp8 ? (is_v ? L.rawv_off : L.rawk_off) : (is_v ? L.v_off : L.k_off));
+    constexpr uint32_t kSlot = kFp8 ? kCode : kTile;
+    if (lane == 0) prefetch_tensormap(tm);
+    const uint64_t pol = kv_policy(sh.row_tiles);
+    // Paged (and FP8) caches: lane i loads the i-th run of `box` tokens, whole rows. Contiguous 16-bit
+    // caches: lane i loads block i of all tokens.
+    const bool rows = kFp8 || p.c.paged;
+    const int box = p.c.box_tokens;
+    auto lookup = [&](int kt) {   // lane's cache row; -2: nothing to load, -1: a bad page
+      const int t = kt * kTreeTokens + (rows ? lane * box : 0);
+      if (rows ? lane * box >= kTreeTokens || t >= c.w.s.n : lane >= CH) return -2;
+      const int entry =
+          p.c.paged ? __ldg(p.c.block_table + (long long)c.w.b * p.c.max_blocks + t / p.c.page_size)
+                    : 0;
+      return token_row(p.c, c.w.b, t, entry);
+    };
+    const uint32_t lane_off = kFp8   ? (uint32_t)(lane * box) * D
+                              : rows ? (uint32_t)(lane * box / 8) * grp_bytes
+                                     : lane * blk_bytes;
+    const uint32_t lane_bytes = (uint32_t)box * (kFp8 ? D : rows ? CH * 128 : 128);
+    uint32_t slot = 0, par = 1, it = 0, issued = 0;
+    int z = -2, loaded = 0;
+    while (c.advance(p, sh)) {
+      if (c.first()) {
+        z = lookup(c.kt);
+        if (!kFp8 && !is_v) {
+          const int qb = c.piece & 1;
+          const int i0 = sh.row_tile * (kTreeRows / p.group);   // the tile's first drafted token
+          wait(&q_empty[qb], ((c.piece >> 1) & 1) ^ 1);
+          if (!wait.dead) {
+            if (lane == 0) mbar_arrive_expect_tx(&q_full[qb], kTile);
+            __syncwarp();
+            if (lane < CH)
+              tma_load_4d(smem + L.q_off + qb * kTile + lane * (128 * 128), &tmq, &q_full[qb], 0,
+                          c.w.kvh * p.group, c.w.s.row0 + i0, lane, pol);
+            ++loaded;
           }
         }
-        const int z_next = c.last() ? -2 : lookup(c.kt + 1);   // in flight during the wait
-        wait(&empty[slot], par);
-        if (!wait.dead) {
-          const int boxes = __popc(__ballot_sync(0xffffffffu, z != -2));
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], boxes * lane_bytes);
-          __syncwarp();
-          if (z != -2) {
-            uint8_t* dst = ring + slot * kTile + lane_off;
-            if (p.c.paged) {
-              if (z < 0) atomicOr(p.c.status, kStatusBadBlockTable);
-              // a bad page: past the pool, zeros
-              const int group = z < 0 ? p.c.num_blocks * (p.c.page_size / 8) : z / 8;
-              tma_load_5d(dst, tm, &full[slot], 0, 0, 0, group, c.w.kvh, pol);
-            } else {
-              tma_load_4d(dst, tm, &full[slot], 0, z, lane, c.w.kvh, pol);
-            }
-          }
-          issued = it + 1;
-        }
-        __syncwarp();
-        if (++slot == slots) slot = 0, par ^= 1;
-        z = z_next;
-        ++it;
       }
-      // never leave with copies in flight
-      for (uint32_t k = issued > slots ? issued - slots : 0; k < issued; ++k)
-        mbar_wait(&full[k % slots], (k / slots) & 1, kWaitLimitNs);
-      for (int k = loaded > L.nq ? loaded - L.nq : 0; k < loaded; ++k)
-        mbar_wait(&q_full[k & 1], (k >> 1) & 1, kWaitLimitNs);
+      const int z_next = c.last() ? -2 : lookup(c.kt + 1);   // in flight during the wait
+      wait(&empty[slot], par);
+      if (!wait.dead) {
+        const int boxes = __popc(__ballot_sync(0xffffffffu, z != -2));
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], boxes * lane_bytes);
+        __syncwarp();
+        if (z != -2) {
+          uint8_t* dst = ring + slot * kSlot + lane_off;
+          // a bad page: past the pool, zeros
+          if (z < 0) atomicOr(p.c.status, kStatusBadBlockTable);
+          const int at = z < 0 ? p.c.num_blocks * p.c.page_size : z;
+          if constexpr (kFp8) tma_load_3d(dst, tm, &full[slot], 0, at, c.w.kvh, pol);
+          else if (rows) tma_load_5d(dst, tm, &full[slot], 0, 0, 0, at / 8, c.w.kvh, pol);
+          else tma_load_4d(dst, tm, &full[slot], 0, at, lane, c.w.kvh, pol);
+        }
+        issued = it + 1;
+      }
+      __syncwarp();
+      if (++slot == slots) slot = 0, par ^= 1;
+      z = z_next;
+      ++it;
     }
+    // never leave with copies in flight
+    for (uint32_t k = issued > slots ? issued - slots : 0; k < issued; ++k)
+      mbar_wait(&full[k % slots], (k / slots) & 1, kWaitLimitNs);
+    for (int k = loaded > L.nq ? loaded - L.nq : 0; k < loaded; ++k)
+      mbar_wait(&q_full[k & 1], (k >> 1) & 1, kWaitLimitNs);
   } else if (warp == kTreeSoftmaxWarps + 2) {
     // ---- S = Q K^T issuer ------------------------------------------------------------------
     Cursor c(p, sh);
@@ -711,7 +821,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
     constexpr bool kBf16 = std::is_same<M, __nv_bfloat16>::value;
     constexpr uint32_t kDescO = mma_desc(kBf16, D, true);
     const uint64_t v_desc = tile_desc(smem_u32(smem + L.v_off), blk_bytes, grp_bytes);
-    const uint32_t v_step = 2u * grp_bytes >> 4;   // 16 tokens
+    const uint32_t v_step = 2u * grp_bytes >> 4;   // 16 tokens; their P: 8 columns of hi, 8 of lo
     const bool issuer = elect_one();
     uint32_t it = 0, v_slot = 0, v_par = 0;
     while (c.advance(p, sh)) {
@@ -727,18 +837,18 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
         if (valid >= kTreeTokens) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_ts(oc, pa + k * 8u, vd + k * v_step, kDescO, k != 0 || !fresh);
+            mma_ts(oc, pa + k * 16u, vd + k * v_step, kDescO, k != 0 || !fresh);
           if constexpr (kSplit) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_ts(oc, pa + 64u + k * 8u, vd + k * v_step, kDescO, true);
+              mma_ts(oc, pa + 8u + k * 16u, vd + k * v_step, kDescO, true);
           }
         } else {   // the sequence ends in this tile
           const int steps = (valid + 15) / 16;
 #pragma unroll 1
           for (int k = 0; k < steps; ++k) {
-            mma_ts(oc, pa + k * 8u, vd + k * v_step, kDescO, k != 0 || !fresh);
-            if constexpr (kSplit) mma_ts(oc, pa + 64u + k * 8u, vd + k * v_step, kDescO, true);
+            mma_ts(oc, pa + k * 16u, vd + k * v_step, kDescO, k != 0 || !fresh);
+            if constexpr (kSplit) mma_ts(oc, pa + 8u + k * 16u, vd + k * v_step, kDescO, true);
           }
         }
         tc_commit(&o_full[buf]);
@@ -751,89 +861,67 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
     if (issuer) tc_commit(&drained[1]);
     mbar_wait(&drained[1], 0, kWaitLimitNs);
   } else if constexpr (kFp8) {
-    // ---- FP8: loads of codes, conversion to f16 tiles, q -----------------------------------
-    // A warp loads and converts the same 32 rows of every tile, so that codes need no barrier between
-    // warps: it refills its part of a slot as soon as it has read it.
-    Cursor c(p, sh), ld(p, sh);
+    // ---- FP8: codes to f16 tiles, q ----------------------------------------------------------
+    Cursor c(p, sh);
     const int cw = warp - (kTreeSoftmaxWarps + 4);
-    const int box = p.c.box_tokens;   // 8 to 32
-    struct Load {
-      int z, kvh;    // lane's cache row (-2: none, -1: a bad page); kvh < 0: no more tiles
-    };
-    auto next_load = [&]() {
-      Load a{-2, -1};
-      if (!ld.advance(p, sh)) return a;
-      a.kvh = ld.w.kvh;
-      const int t = ld.kt * kTreeTokens + cw * 32 + lane * box;
-      if (lane * box < 32 && t < ld.w.s.n) {
-        const int entry =
-            p.c.paged ? __ldg(p.c.block_table + (long long)ld.w.b * p.c.max_blocks + t / p.c.page_size)
-                      : 0;
-        a.z = token_row(p.c, ld.w.b, t, entry);
-      }
-      return a;
-    };
-    auto issue = [&](const Load& a, const CUtensorMap* tm, uint64_t* full, uint32_t off, uint32_t slot) {
-      if (wait.dead) return;
-      uint64_t* b = &full[slot * kTreeConvertWarps + cw];
-      const int boxes = __popc(__ballot_sync(0xffffffffu, a.z != -2));
-      if (lane == 0) mbar_arrive_expect_tx(b, (uint32_t)(boxes * box) * D);
-      __syncwarp();
-      if (a.z != -2) {
-        if (a.z < 0) atomicOr(p.c.status, kStatusBadBlockTable);
-        const uint64_t pol = kv_policy(sh.row_tiles);
-        tma_load_3d(smem + off + slot * kCode + (uint32_t)(cw * 32 + lane * box) * D, tm, b, 0,
-                    a.z < 0 ? p.c.num_blocks * p.c.page_size : a.z, a.kvh, pol);   // bad: past the pool
-      }
-      __syncwarp();
-    };
-    auto convert = [&](uint64_t* rfull, uint32_t raw_off, uint32_t rs, uint32_t rpar, uint64_t* full,
-                       uint64_t* empty, uint32_t off, uint32_t ds, uint32_t dpar) {
-      wait(&rfull[rs * kTreeConvertWarps + cw], rpar);
-      wait(&empty[ds], dpar);
-      constexpr int LR = D / 16, RW = 32 / LR;   // lanes a row (16 codes each), rows a pass
-      const int seg = lane % LR, sub = lane / LR;
-      const uint8_t* src = smem + raw_off + rs * kCode + cw * 32 * D + lane * 16;
-      uint8_t* dst = smem + off + ds * kTile + (seg / 4) * 16384 + (cw * 32 + sub) * 128;
-      const int k0 = (seg & 3) * 2, flip = seg >> 2;   // the upper block's lanes store in the other
-                                                       // order: 8 lanes then hit 8 different chunks
+    // A warp converts 32 rows of a tile. 8 lanes take the same 16 codes of 8 rows, so that with both
+    // tiles swizzled (the codes' by the TMA: 16-byte chunk ^= row % 8, or ^= row / 2 % 4 where a row is
+    // 64 bytes) neither its loads nor its stores meet a bank twice.
+    const int r7 = lane & 7, sg = lane >> 3;
+    const uint32_t src0 = (uint32_t)(cw * 32 + r7) * D + ((D == 128 ? sg ^ r7 : sg ^ (r7 >> 1)) << 4);
+    const uint32_t dst0 = (uint32_t)(cw * 32 + r7) * 128 + (((sg * 2) ^ r7) << 4);
+    auto convert = [&](uint32_t from, uint32_t to) {   // 32 rows of a tile of codes to those of an f16 tile
+      const uint8_t* src = smem + from + src0;
+      uint8_t* dst = smem + to + dst0;
 #pragma unroll
-      for (int g = 0; g < 32; g += 4 * RW) {
+      for (int h = 0; h < CH; ++h) {
         uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(src + (g + j * RW) * D);
+        for (int g = 0; g < 4; ++g)   // segment sg + 4 h: 64 bytes on, within the swizzle
+          v[g] = *reinterpret_cast<const uint4*>(
+              reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(src) ^ (h * 64)) + g * 8 * D);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t7 = (g + j * RW + sub) & 7;
+        for (int g = 0; g < 4; ++g) {
           uint4 a, b;
-          e4m3x4_to_f16x2(v[j].x, a.x, a.y);
-          e4m3x4_to_f16x2(v[j].y, a.z, a.w);
-          e4m3x4_to_f16x2(v[j].z, b.x, b.y);
-          e4m3x4_to_f16x2(v[j].w, b.z, b.w);
-          uint8_t* d = dst + (g + j * RW) * 128;
-          *reinterpret_cast<uint4*>(d + (((k0 + flip) ^ t7) << 4)) = flip ? b : a;
-          *reinterpret_cast<uint4*>(d + (((k0 + 1 - flip) ^ t7) << 4)) = flip ? a : b;
+          e4m3x4_to_f16x2(v[g].x, a.x, a.y);
+          e4m3x4_to_f16x2(v[g].y, a.z, a.w);
+          e4m3x4_to_f16x2(v[g].z, b.x, b.y);
+          e4m3x4_to_f16x2(v[g].w, b.z, b.w);
+          uint8_t* d = dst + h * 16384 + g * 1024;
+          *reinterpret_cast<uint4*>(d) = a;
+          *reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(d) ^ 16) = b;
         }
+      }
+    };
+    // K of tile n and V of tile n - 1, which the MMAs take at about the same time, in one pass: the
+    // waits, the fence and the arrivals cost more than a tile's conversion.
+    auto pass = [&](bool k, bool v, uint32_t n, uint32_t rk, uint32_t rk_par) {
+      const uint32_t i = n - 1, rv = rk ? rk - 1 : L.raw - 1, rv_par = rk ? rk_par : rk_par ^ 1;
+      if (k) {
+        wait(&rk_full[rk], rk_par);
+        wait(&k_empty[n & 1], ((n >> 1) & 1) ^ 1);
+        convert(L.rawk_off + rk * kCode, L.k_off + (n & 1) * kTile);
+      }
+      if (v) {
+        wait(&rv_full[rv], rv_par);
+        wait(&v_empty[i & 1], ((i >> 1) & 1) ^ 1);
+        convert(L.rawv_off + rv * kCode, L.v_off + (i & 1) * kTile);
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[ds]);
+      if (lane == 0) {
+        if (k) {
+          mbar_arrive(&k_full[n & 1]);
+          mbar_arrive(&rk_empty[rk]);
+        }
+        if (v) {
+          mbar_arrive(&v_full[i & 1]);
+          mbar_arrive(&rv_empty[rv]);
+        }
+      }
     };
-    // tile n converts K n, loads K n + raw, converts V n - 1 and loads V n - 1 + raw
-    uint32_t n = 0, rk = 0, rk_par = 0, loads = 0;
-    Load nxt{-2, -1}, old{-2, -1};
-    for (uint32_t i = 0; i < (uint32_t)L.raw; ++i) {
-      const Load a = next_load();
-      if (a.kvh < 0) break;
-      issue(a, &tmk, rk_full, L.rawk_off, i);
-      issue(a, &tmv, rv_full, L.rawv_off, i);
-      ++loads;
-    }
-    nxt = next_load();
-    auto convert_v = [&](uint32_t i, uint32_t rv, uint32_t rv_par) {
-      convert(rv_full, L.rawv_off, rv, rv_par, v_full, v_empty, L.v_off, i & 1, ((i >> 1) & 1) ^ 1);
-      if (old.kvh >= 0) issue(old, &tmv, rv_full, L.rawv_off, rv);
-    };
+    static_assert(!kFp8 || (L.nk == 2 && L.nv == 2), "");
+    uint32_t n = 0, rk = 0, rk_par = 0;
     while (c.advance(p, sh)) {
       if (c.first()) {
         // q: a thread's row as f16 times a power of two, so that its largest element lies in
@@ -883,26 +971,11 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[qb]);
       }
-      // in the order that the MMAs take them: K 0, K 1, V 0, K 2, V 1, ...
-      convert(rk_full, L.rawk_off, rk, rk_par, k_full, k_empty, L.k_off, n & 1, ((n >> 1) & 1) ^ 1);
-      if (nxt.kvh >= 0) {
-        issue(nxt, &tmk, rk_full, L.rawk_off, rk);
-        ++loads;
-      }
-      const uint32_t rv = rk ? rk - 1 : L.raw - 1, rv_par = rk ? rk_par : rk_par ^ 1;
-      if (n >= 1) convert_v(n - 1, rv, rv_par);
-      old = nxt;
-      nxt = next_load();
+      pass(true, n >= 1, n, rk, rk_par);
       if (++rk == (uint32_t)L.raw) rk = 0, rk_par ^= 1;
       ++n;
     }
-    if (n) convert_v(n - 1, rk ? rk - 1 : L.raw - 1, rk ? rk_par : rk_par ^ 1);
-    if (wait.dead) {   // never leave with copies in flight (otherwise each was waited for)
-      for (uint32_t k = loads > L.raw ? loads - L.raw : 0; k < loads; ++k) {
-        mbar_wait(&rk_full[k % L.raw * kTreeConvertWarps + cw], (k / L.raw) & 1, kWaitLimitNs);
-        mbar_wait(&rv_full[k % L.raw * kTreeConvertWarps + cw], (k / L.raw) & 1, kWaitLimitNs);
-      }
-    }
+    if (n) pass(false, true, n, rk, rk_par);
   }
   __syncwarp();
   tc_fence_before();

@@ -8,31 +8,27 @@ namespace da {
 constexpr int kTreeRows = 128;       // query rows per tile: the M of tcgen05.mma
 constexpr int kTreeTokens = 128;     // KV tokens per tile
 
-// Warps: 8 softmax, then two loaders (16-bit caches: K with q, and V), the issuer of S, the issuer
-// of O, and for FP8 caches 4 that load codes and convert them to f16 tiles.
-constexpr int kTreeSoftmaxWarps = 8;
+// Warps: 16 softmax (a thread has 32 columns of one row's S), then the loaders of K (with q, for 16-bit
+// caches) and of V, the issuer of S, the issuer of O, and for FP8 caches 4 that convert codes to f16
+// tiles (and q).
+constexpr int kTreeSoftmaxWarps = 16;
 constexpr int kTreeConvertWarps = 4;
 __host__ __device__ constexpr int tree_threads(bool fp8) {
   return (kTreeSoftmaxWarps + 4 + (fp8 ? kTreeConvertWarps : 0)) * 32;
 }
 
-// Registers: compiled (and launched) with tree_launch_regs a thread; the softmax warps then take more
-// from the others. A spilled register costs an L2 round trip here, with all of L1 in use as shared
+// Registers: compiled (and launched) with tree_launch_regs a thread; in the FP8 kernel the softmax warps
+// then give some to the others. A spilled register costs an L2 round trip here, with all of L1 in use as shared
 // memory: at 128 registers for everyone the FP8 kernel spent most of its time on spills.
-__host__ __device__ constexpr int tree_launch_regs(bool fp8) { return fp8 ? 128 : 168; }
-__host__ __device__ constexpr int tree_softmax_regs(int D, bool fp8) {
-  return !fp8 ? 208 : D == 128 ? 152 : 168;
-}
-__host__ __device__ constexpr int tree_other_regs(int D, bool fp8) {
-  return fp8 && D == 128 ? 104 : 88;
-}
-__host__ __device__ constexpr bool tree_regs_fit(int D, bool fp8) {
-  return kTreeSoftmaxWarps * tree_softmax_regs(D, fp8) +
-             (tree_threads(fp8) / 32 - kTreeSoftmaxWarps) * tree_other_regs(D, fp8) ==
+__host__ __device__ constexpr int tree_launch_regs(bool fp8) { return fp8 ? 80 : 96; }
+__host__ __device__ constexpr int tree_softmax_regs(bool fp8) { return fp8 ? 72 : 96; }
+__host__ __device__ constexpr int tree_other_regs(bool fp8) { return 96; }
+__host__ __device__ constexpr bool tree_regs_fit(bool fp8) {
+  return kTreeSoftmaxWarps * tree_softmax_regs(fp8) +
+             (tree_threads(fp8) / 32 - kTreeSoftmaxWarps) * tree_other_regs(fp8) <=
          tree_threads(fp8) / 32 * tree_launch_regs(fp8);
 }
-static_assert(tree_regs_fit(64, false) && tree_regs_fit(128, false) && tree_regs_fit(64, true) &&
-                  tree_regs_fit(128, true),
+static_assert(tree_regs_fit(false) && tree_regs_fit(true),
               "the register split must fit the launch allocation");
 
 // A 16-bit tile of 128 rows (tokens or query rows) of D elements in shared memory, as tcgen05.mma
@@ -67,13 +63,13 @@ __host__ __device__ constexpr TreeLayout tree_layout(int D, bool fp8) {
   L.rawv_off = off;
   off += L.raw * code;
   L.bar_off = off;
-  off += 64 * 8;
-  L.exch_off = off;           // row maxima of the two column halves, two tiles; scratch of the schedule
-  off += 2 * 2 * 128 * 4;
+  off += 40 * 8;
+  L.exch_off = off;           // row maxima of the four column quarters; scratch of the schedule
+  off += 4 * 128 * 4;
   L.qexp_off = off;           // FP8: q's power of two per row
   off += 2 * 128;
-  L.misc_off = off;           // TMEM address, abort flag, odd-token word
-  off += 32;
+  L.misc_off = off;           // TMEM address, abort flag, odd-token word, the CTA's share
+  off += 16 + sizeof(TreeShare);
   // more than half of an SM's shared memory: one CTA an SM, so each has the SM's whole TMEM
   L.total = off > 120u * 1024 ? off : 120u * 1024;
   return L;
@@ -82,7 +78,7 @@ static_assert(tree_layout(128, false).total <= kSmemLimit, "");
 static_assert(tree_layout(128, true).total <= kSmemLimit, "");
 static_assert(tree_layout(64, false).total <= kSmemLimit, "");
 static_assert(tree_layout(64, true).total <= kSmemLimit, "");
-static_assert(sizeof(TreeScratch) <= 2 * 2 * 128 * 4, "the schedule's scratch lies in the exchange");
+static_assert(sizeof(TreeScratch) <= 4 * 128 * 4, "the schedule's scratch lies in the exchange");
 
 // The kernel of a cache type (da_dtype, or FP8), head_dim and output; null: not built.
 // split: P enters as the sum of two 16-bit parts.

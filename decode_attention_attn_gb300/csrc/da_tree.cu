@@ -58,11 +58,11 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int G = p.group;
   const TreeShare sh = tree_schedule<kCoreThreads>(p, sm.sched);
+  pdl_launch_dependents();   // the merge's launch runs beside this kernel; it waits for its end
   TreeWalk w(p, sh);
   bool first_piece = true;
   while (w.next(p, sh)) {
-    if (first_piece && tid == 0 && sh.row_tile == 0)
-      p.info[sh.owner] = make_int4(w.b, w.kvh, w.t0, w.s.tiles);
+    if (first_piece && tid == 0 && sh.row_tile == 0 && sh.head == 0) tree_record(p, sh, w);
     first_piece = false;
     const int R = w.s.T * G, r0 = sh.row_tile * kCoreRows;
     if (r0 >= R) continue;
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
       const int rr = r0 + 2 * ty + a;
       mine[a] = rr < R ? rr : -1;
       const int i = rr / G;
-      word[a] = rr < R ? tree_word(p, w.s.row0 + i, i, w.s.T) : 0ull;
+      word[a] = rr < R ? tree_clip(p, p.mask ? __ldg(p.mask + w.s.row0 + i) : 0ull, i, w.s.T) : 0ull;
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float o[2][NC][4] = {};
@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
         if (p.out_lse && tx == 0) p.out_lse[row] = L * 0.69314718055994531f;
       } else {
         const long long at =
-            tree_slot(sh.owner, w.head, sh.row_tile, sh.row_tiles) * kCoreRows + 2 * ty + a;
+            tree_slot(sh.owner, w.head, sh.row_tiles * sh.heads,
+                      sh.head * sh.row_tiles + sh.row_tile) * kCoreRows + 2 * ty + a;
         for (int c = 0; c < NC; ++c)
           for (int e = 0; e < 4; ++e)
             p.part_o[at * D + (tx + 16 * c) * 4 + e] = o[a][c][e] * inv;
@@ -233,39 +234,42 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
       }
     }
   }
-  pdl_launch_dependents();
 }
 
 // ---- merge ----------------------------------------------------------------------------------
 // o = sum_s 2^(L_s - L) o_s, L = log2 sum_s 2^(L_s). Block (x, y): the group whose units cross the
-// start of owner x + 1's share, if x is the first owner it has units with; rows y * 8 .. + 7, a
-// warp a row, D / 32 columns a lane. A programmatic dependent of the attention kernel.
+// start of CTA x's share, if the owner before it is the first that has units of the group; CTA x's head and
+// row tile, rows y * 8 .. + 7 of it, a warp a row, D / 32 columns a lane. A programmatic dependent of the
+// attention kernel. Bound by its chain of loads (record, L's, partials: L2 round trips), so that
+// partials are read 8 at a time.
 constexpr int kMergeWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(
     const __grid_constant__ TreeParams p) {
   pdl_wait();
-  const int W = p.head[0], P = p.head[1], R = p.head[2];
-  const int next = blockIdx.x + 1;
-  if (next >= P) return;
-  const int4 g = p.info[next];                 // the first piece of the next owner
+  const int4 head = *p.head;
+  const int W = head.x, P = head.y, R = head.z, lanes = head.z * head.w;
+  const int next = blockIdx.x / lanes, sub = blockIdx.x % lanes;
+  if (next == 0 || next >= P) return;
+  const int4 g = p.info[2 * next], s = p.info[2 * next + 1];
+  if (g.y == 0) return;                        // its first group starts there: no crossing
   const int at = tree_share_begin(next, W, P);
-  const int gs = at - g.z, ge = gs + g.w;      // the group's units
-  if (g.z == 0) return;                        // it starts there: nothing crosses
+  const int gs = at - g.y, ge = gs + g.z;      // the group's units
   const int o1 = tree_owner(gs, W, P), o2 = tree_owner(ge - 1, W, P);
-  if (o1 != (int)blockIdx.x) return;           // another block's
-  const TreeSeq s = tree_seq(p, g.x);
+  if (o1 != next - 1) return;                  // another block's
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.y * kMergeWarps + warp;
-  if (r >= s.T * p.group) return;
-  const int rt = r / p.tile_rows, rr = r % p.tile_rows;
-  auto place = [&](int o) {
-    const bool head = o > o1 || gs == tree_share_begin(o1, W, P);
-    return tree_slot(o, head, rt, R) * p.tile_rows + rr;
+  const int rr = blockIdx.y * kMergeWarps + warp, r = sub % R * p.tile_rows + rr;
+  if (r >= s.y * p.group) return;
+  // partial j of the group: owner o1 + j's first piece, or o1's last
+  const bool whole_first = gs == tree_share_begin(o1, W, P);
+  const int n = o2 - o1 + 1;
+  const float* const part_o = p.part_o + (long long)rr * D + lane * (D / 32);
+  auto slot = [&](int j) {
+    return tree_slot(o1 + j, j > 0 || whole_first, lanes, sub) * p.tile_rows;
   };
   float top = -INFINITY;
-  for (int o = o1 + lane; o <= o2; o += 32) top = fmaxf(top, p.part_l[place(o)]);
+  for (int j = lane; j < n; j += 32) top = fmaxf(top, p.part_l[slot(j) + rr]);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
   // a NaN among the L's passes the maximum over; it comes back through the weights
@@ -273,26 +277,29 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(
   constexpr int C = D / 32;
   float acc[C] = {};
   float sum = 0.f;
-#pragma unroll 4
-  for (int o = o1; o <= o2; ++o) {
-    const long long a = place(o);
-    const float wgt = exp2f(p.part_l[a] - ref);
-    const float* src = p.part_o + a * D + lane * C;
-    float v[C];
-    if constexpr (C == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(src);
-      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(src);
-      v[0] = x.x; v[1] = x.y;
-    }
-    sum += wgt;
+  for (int j0 = 0; j0 < n; j0 += 32) {
+    const float wl = j0 + lane < n ? exp2f(p.part_l[slot(j0 + lane) + rr] - ref) : 0.f;
+    const int m = min(32, n - j0);
+#pragma unroll 8
+    for (int j = 0; j < m; ++j) {
+      const float wgt = __shfl_sync(0xffffffffu, wl, j);
+      const float* src = part_o + slot(j0 + j) * D;
+      float v[C];
+      if constexpr (C == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        v[0] = x.x; v[1] = x.y;
+      }
+      sum += wgt;
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] += wgt * v[c];
+      for (int c = 0; c < C; ++c) acc[c] += wgt * v[c];
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int i = r / p.group, h = g.y * p.group + r % p.group;
-  const long long row = (long long)(s.row0 + i) * p.c.hq + h;
+  const int i = r / p.group, h = (g.x * head.w + sub / R) * p.group + r % p.group;
+  const long long row = (long long)(s.x + i) * p.c.hq + h;
 #pragma unroll
   for (int c = 0; c < C; ++c)
     store_out(p.out, row * D + lane * C + c, p.c.out_dtype, acc[c] * inv * p.v_scale);
@@ -449,7 +456,7 @@ int decode_attn_tree_plan(const da_problem* problem, int max_tree, da_tree_plan*
   pl->off_head = off + 16;
   off = align256(off + 64);
   pl->off_info = off;
-  off = align256(off + (size_t)pl->grid * 16);
+  off = align256(off + (size_t)pl->grid * 32);
   pl->off_part_l = off;
   off = align256(off + slots * pl->tile_rows * 4);
   pl->off_part_o = off;
@@ -517,7 +524,7 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
   fill_common(pl.cache, p.c, a.block_table, nullptr, nullptr);
   char* ws = static_cast<char*>(a.workspace);
   p.c.status = reinterpret_cast<int32_t*>(ws + pl.off_status);
-  p.head = reinterpret_cast<int*>(ws + pl.off_head);
+  p.head = reinterpret_cast<int4*>(ws + pl.off_head);
   p.info = reinterpret_cast<int4*>(ws + pl.off_info);
   p.part_l = reinterpret_cast<float*>(ws + pl.off_part_l);
   p.part_o = reinterpret_cast<float*>(ws + pl.off_part_o);
@@ -552,7 +559,7 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
     int rc = q_map(pl, a.q, a.rows, &tmq);
     if (rc == DA_OK) rc = kv_map(pl, a.k_cache, p.c.box_tokens, &tmk);
     if (rc == DA_OK) rc = kv_map(pl, a.v_cache, p.c.box_tokens, &tmv);
-    if (rc == DA_OK) rc = raise_smem(fn, pl.smem_bytes, pr.kv_fp8 ? tree_launch_regs(true) : 0);
+    if (rc == DA_OK) rc = raise_smem(fn, pl.smem_bytes, tree_launch_regs(pr.kv_fp8 != 0));
     if (rc != DA_OK) return rc;
     const void* vc = a.v_cache;
     void* kargs[5] = {&p, &tmq, &tmk, &tmv, &vc};
@@ -574,8 +581,8 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(pl.grid - 1),
-                       (unsigned)((pl.max_tree * pl.cache.group + kMergeWarps - 1) / kMergeWarps));
+    const int rows = std::min(pl.tile_rows, pl.max_tree * pl.cache.group);
+    cfg.gridDim = dim3((unsigned)pl.grid, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps));
     cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cfg.attrs = pdl;

@@ -3,14 +3,16 @@
 //
 // Work. The query heads of a KV head and the drafted tokens of a sequence are rows of one matrix:
 // row r = i G + g is head g of drafted token i, so one read of a KV head serves T G rows. Rows are
-// cut into row tiles, a sequence's tokens into KV tiles. The units of the schedule are the KV tiles
-// of every (sequence, KV head), in that order; owner o of P takes units [o W / P, (o + 1) W / P).
-// With R row tiles (the most that any sequence has) an owner is R CTAs that walk the same
-// units, one row tile each, at about the same time, so that the second read of a KV tile hits L2.
+// cut into row tiles, a sequence's tokens into KV tiles, the KV heads into blocks of `heads` heads. The
+// units of the schedule are the KV tiles of every (sequence, block of heads), in that order; owner o of P
+// takes units [o W / P, (o + 1) W / P). An owner is R x heads CTAs, for each of R row tiles (the most
+// that any sequence has) and each head of a block, that walk the same units at about the same time: the
+// second row tile's read of a KV tile then hits L2, and a token's rows of several heads, which lie side by
+// side in the cache, are read together.
 //
-// A (sequence, KV head) whose units lie with one owner is finished by it. One that spans owners
-// leaves a partial with each (normalised rows and their log2 LSE), which the merge kernel joins: of
-// an owner's pieces only the first and the last can be partial, so two slots an owner hold them.
+// A group, a (sequence, block of heads), whose units lie with one owner is finished by it. One that
+// spans owners leaves a partial with each (normalised rows and their log2 LSE), which the merge kernel
+// joins: of a CTA's pieces only the first and the last can be partial, so two slots a CTA hold them.
 #pragma once
 
 #include "da_device.cuh"
@@ -25,10 +27,11 @@ struct TreeParams {
   const unsigned long long* mask;   // [rows] or null (a chain)
   void* out;
   float* out_lse;
-  int* head;                    // workspace: [0] units W, [1] owners P, [2] row tiles R
-  int4* info;                   // [owners]: b, kvh, first unit's offset in its group, group tiles
-  float* part_o;                // [2 owners][R][tile rows][d], 2 P R <= 2 CTAs
-  float* part_l;                // [2 owners][R][tile rows]
+  int4* head;                   // workspace: units W, owners P, row tiles R, heads
+  int4* info;                   // [owners][2]: {block of heads, first unit's offset in its group, the
+                                // group's tiles, 0}, {first row, drafted tokens, 0, 0} of its first piece
+  float* part_o;                // [owners][2][heads][R][tile rows][d]: 2 slots a CTA
+  float* part_l;                // [owners][2][heads][R][tile rows]
   int rows, max_tree, group;
   int tile_rows, tile_tokens;
   int max_row_tiles;            // R's bound, from max_tree
@@ -44,11 +47,18 @@ struct TreeSeq {
   bool bad;
 };
 
-// Sequence b's rows and lengths, clamped to what exists.
-__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
+struct TreeRaw {   // a sequence's row range and length as they stand in memory
+  int lo, hi, ctx;
+};
+__device__ __forceinline__ TreeRaw tree_raw(const TreeParams& p, int b) {
+  return {__ldg(p.row_offsets + b), __ldg(p.row_offsets + b + 1), __ldg(p.ctx_lens + b)};
+}
+
+// A sequence's rows and lengths, clamped to what exists.
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, const TreeRaw& raw) {
   TreeSeq s;
-  const int lo = __ldg(p.row_offsets + b), hi = __ldg(p.row_offsets + b + 1);
-  int ctx = __ldg(p.ctx_lens + b);
+  const int lo = raw.lo, hi = raw.hi;
+  int ctx = raw.ctx;
   s.row0 = min(max(lo, 0), p.rows);
   int T = min(max(hi, s.row0), p.rows) - s.row0;
   s.bad = ctx < 0 || T > p.max_tree || lo < 0;
@@ -63,11 +73,15 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   return s;
 }
 
-// The drafted tokens that row `row` (drafted token i of T) attends to.
-__device__ __forceinline__ unsigned long long tree_word(const TreeParams& p, int row, int i,
-                                                        int T) {
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
+  return tree_seq(p, tree_raw(p, b));
+}
+
+// The drafted tokens that drafted token i of T attends to, from its mask word (no mask: a chain).
+__device__ __forceinline__ unsigned long long tree_clip(const TreeParams& p, unsigned long long word,
+                                                        int i, int T) {
   const unsigned long long all = T >= 64 ? ~0ull : (1ull << T) - 1ull;
-  return (p.mask ? __ldg(p.mask + row) : (2ull << i) - 1ull) & all;
+  return (p.mask ? word : (2ull << i) - 1ull) & all;
 }
 
 // A CTA's part of the schedule.
@@ -76,7 +90,7 @@ struct TreeShare {
   int u0, u1;          // units
   int base;            // first unit of sequence b0
   int b0;              // the sequence that u0 lies in
-  int row_tile, row_tiles, owner, owners;
+  int row_tile, row_tiles, head, heads, owner, owners;
 };
 
 struct TreeScratch {   // shared memory of tree_schedule
@@ -91,6 +105,13 @@ __device__ __forceinline__ int tree_share_begin(int o, int W, int P) {
 // The owner of unit u: the o with o W / P <= u < (o + 1) W / P (floor divisions).
 __device__ __forceinline__ int tree_owner(int u, int W, int P) {
   return (int)((((long long)u + 1) * P - 1) / W);
+}
+
+// Heads that an owner takes side by side: as many as leave at most 5 % of the CTAs without an owner.
+__device__ __forceinline__ int tree_heads(int ctas, int row_tiles, int hkv) {
+  for (int h = hkv; h > 1; --h)
+    if (hkv % h == 0 && ctas / (row_tiles * h) * (row_tiles * h) * 20 >= ctas * 19) return h;
+  return 1;
 }
 
 // Every thread of the CTA calls this (NT threads). Each takes a run of sequences; a block scan of
@@ -128,12 +149,15 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
     total += sc.warp_sum[w];
     most = max(most, sc.warp_max[w]);
   }
-  const int pre = before + inc - sum, units = total * p.c.hkv;
   TreeShare sh;
   sh.row_tiles = min(most, p.max_row_tiles);
-  sh.owners = max(1, min((int)gridDim.x / sh.row_tiles, units));
-  sh.owner = blockIdx.x / sh.row_tiles;
+  sh.heads = tree_heads(gridDim.x, sh.row_tiles, p.c.hkv);
+  const int blocks = p.c.hkv / sh.heads, lanes = sh.row_tiles * sh.heads;
+  const int pre = before + inc - sum, units = total * blocks;
+  sh.owners = max(1, min((int)gridDim.x / lanes, units));
+  sh.owner = blockIdx.x / lanes;
   sh.row_tile = blockIdx.x % sh.row_tiles;
+  sh.head = blockIdx.x % lanes / sh.row_tiles;
   if (units == 0 || sh.owner >= sh.owners) {
     sh.u0 = sh.u1 = 0;
     sh.b0 = 0;
@@ -141,13 +165,13 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
   } else {
     sh.u0 = tree_share_begin(sh.owner, units, sh.owners);
     sh.u1 = tree_share_begin(sh.owner + 1, units, sh.owners);
-    if (pre * p.c.hkv <= sh.u0 && sh.u0 < (pre + sum) * p.c.hkv) {   // exactly one thread
+    if (pre * blocks <= sh.u0 && sh.u0 < (pre + sum) * blocks) {   // exactly one thread
       int at = pre;
       for (int b = first; b < last; ++b) {
         const int t = tree_seq(p, b).tiles;
-        if (sh.u0 < (at + t) * p.c.hkv) {
+        if (sh.u0 < (at + t) * blocks) {
           sc.b0 = b;
-          sc.base = at * p.c.hkv;
+          sc.base = at * blocks;
           break;
         }
         at += t;
@@ -159,20 +183,19 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
     sh.b0 = sc.b0;
     sh.base = sc.base;
   }
-  if (tid == 0 && blockIdx.x == 0) {
-    p.head[0] = units;
-    p.head[1] = sh.owners;
-    p.head[2] = sh.row_tiles;
-  }
+  if (tid == 0 && blockIdx.x == 0) *p.head = make_int4(units, sh.owners, sh.row_tiles, sh.heads);
   return sh;
 }
 
-// Walks a share's pieces: units of one (sequence, KV head).
+// Walks a share's pieces: units of one group. The next sequence's lengths are loaded
+// when a sequence is entered, a piece before they are needed: at a piece's end every role of the
+// tensor-core kernel would otherwise wait for memory in turn.
 struct TreeWalk {
   int u;           // next unit
   int base;        // first unit of sequence b
   int b;
   TreeSeq s;
+  TreeRaw ahead;   // of sequence b + 1
   // the current piece
   int kvh, t0, t1;      // KV tiles [t0, t1) of the sequence
   bool whole, head;     // covers all tiles; starts at the share's first unit
@@ -180,17 +203,22 @@ struct TreeWalk {
   __device__ __forceinline__ TreeWalk(const TreeParams& p, const TreeShare& sh)
       : u(sh.u0), base(sh.base), b(sh.b0) {
     if (sh.u1 > sh.u0) s = tree_seq(p, b);
+    ahead = tree_raw(p, min(b + 1, p.c.batch - 1));
   }
   __device__ __forceinline__ bool next(const TreeParams& p, const TreeShare& sh) {
     if (u >= sh.u1) return false;
-    while (u >= base + s.tiles * p.c.hkv) {
+    const int blocks = p.c.hkv / sh.heads;
+    while (u >= base + s.tiles * blocks) {
       if (b + 1 >= p.c.batch) return false;   // (lengths that changed under way)
-      base += s.tiles * p.c.hkv;
-      s = tree_seq(p, ++b);
+      base += s.tiles * blocks;
+      ++b;
+      s = tree_seq(p, ahead);
+      ahead = tree_raw(p, min(b + 1, p.c.batch - 1));
     }
     const int off = u - base;
-    kvh = off / s.tiles;
-    t0 = off - kvh * s.tiles;
+    const int block = off / s.tiles;
+    kvh = block * sh.heads + sh.head;
+    t0 = off - block * s.tiles;
     t1 = min(s.tiles, t0 + (sh.u1 - u));
     whole = t0 == 0 && t1 == s.tiles;
     head = u == sh.u0;
@@ -199,10 +227,17 @@ struct TreeWalk {
   }
 };
 
-// Slot of a partial: [2 owners][row tiles].
-__device__ __forceinline__ long long tree_slot(int owner, bool head, int row_tile, int row_tiles) {
-  return ((long long)owner * 2 + (head ? 0 : 1)) * row_tiles + row_tile;
+// What the merge has to know of an owner's first piece, in one place: it finds its work in one round
+// trip to memory.
+__device__ __forceinline__ void tree_record(const TreeParams& p, const TreeShare& sh,
+                                            const TreeWalk& w) {
+  p.info[2 * sh.owner] = make_int4(w.kvh / sh.heads, w.t0, w.s.tiles, 0);
+  p.info[2 * sh.owner + 1] = make_int4(w.s.row0, w.s.T, 0, 0);
 }
 
+// Slot of a partial: [owners][2][heads][row tiles]; `lane` = head * row tiles + row tile.
+__device__ __forceinline__ long long tree_slot(int owner, bool head, int lanes, int lane) {
+  return ((long long)owner * 2 + (head ? 0 : 1)) * lanes + lane;
+}
 
 }  // namespace da

@@ -29,9 +29,10 @@ namespace da {
 namespace {
 
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0;      // two S / P buffers of 128 columns
-constexpr uint32_t kColO = 256;    // O: D columns
+constexpr uint32_t kColO = 0;      // O: D columns
+constexpr uint32_t kColS = 128;    // S / P buffers of 128 columns: 3, or 2 and
 constexpr uint32_t kColQ = 384;    // FP8: two q tiles of D / 2 columns
+__host__ __device__ constexpr uint32_t s_buffers(bool fp8) { return fp8 ? 2 : 3; }
 constexpr float kRescale = 8.f;    // log2: P <= 2^8 before the reference moves
 
 // ---- TMA and tcgen05 -----------------------------------------------------------------------------
@@ -70,6 +71,19 @@ __device__ __forceinline__ void tc_fence_after() {
 }
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// After the wait, `x` may be used: nothing that reads it can move above.
+template <int N>
+__device__ __forceinline__ void tmem_ready(float (&x)[N]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int k = 0; k < N; ++k) asm volatile("" : "+f"(x[k]));
+}
+template <int N>
+__device__ __forceinline__ void tmem_ready(uint32_t (&x)[N]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int k = 0; k < N; ++k) asm volatile("" : "+r"(x[k]));
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -127,28 +141,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
-}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
       "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
 
@@ -183,20 +181,9 @@ __device__ __forceinline__ uint64_t kv_policy(int row_tiles) {
   return pol;
 }
 
-// mbar_try_wait that may sleep up to 1 us before it answers no: a poll that spins takes issue slots from
-// the softmax.
-__device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -207,16 +194,8 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// Barrier `id` of n threads that tells whether any of them has v set.
-__device__ __forceinline__ bool bar_any(int id, int n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(n), "r"((uint32_t)v)
-      : "memory");
-  return r != 0;
+__device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
 // A pipeline wait that gives up, for every warp of the CTA, when one of them ran out of time: from
@@ -230,12 +209,12 @@ struct Waiter {
   // warp-uniform
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
     if (dead) return;
-    bool ok = mbar_sleep_wait(bar, parity);
+    bool ok = mbar_try_wait(bar, parity);
     if (!__all_sync(0xffffffffu, ok)) {
       const unsigned long long t0 = global_timer_ns();
       while (!ok) {
 #pragma unroll 1
-        for (int i = 0; i < 64 && !ok; ++i) ok = mbar_sleep_wait(bar, parity);
+        for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
         if (ok || *reinterpret_cast<volatile int*>(abort_flag)) break;
         if (global_timer_ns() - t0 > limit) {
           atomicOr(status, kStatusTimeout);
@@ -270,6 +249,18 @@ struct Cursor {
   }
   __device__ __forceinline__ bool first() const { return kt == w.t0; }
   __device__ __forceinline__ bool last() const { return kt + 1 == w.t1; }
+};
+
+// The S / P buffer of a tile, and the parity of its barriers' phase.
+template <uint32_t N>
+struct TileSlot {
+  uint32_t buf = 0, par = 0;
+  __device__ __forceinline__ void next() {
+    if (++buf == N) buf = 0, par ^= 1;
+  }
+  // those of the tile before
+  __device__ __forceinline__ uint32_t before() const { return buf ? buf - 1 : N - 1; }
+  __device__ __forceinline__ uint32_t before_par() const { return buf ? par : par ^ 1; }
 };
 
 template <typename T>
@@ -359,6 +350,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   constexpr uint32_t kTile = tree_tile_bytes(D);
   constexpr uint32_t kCode = 128u * D;
   constexpr int CH = D / 64;                 // 64-element blocks of a row
+  constexpr uint32_t NS = s_buffers(kFp8);
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L.bar_off);
   uint64_t* k_full = bar;                 // the 16-bit tiles that the MMAs read
@@ -368,14 +360,14 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   uint64_t* q_full = v_empty + L.nv;
   uint64_t* q_empty = q_full + L.nq;
   uint64_t* s_full = q_empty + L.nq;      // S of a buffer done
-  uint64_t* p_full = s_full + 2;          // P of a buffer written, O rescaled
-  uint64_t* o_full = p_full + 2;          // O += P V done, tiles in turn
-  uint64_t* drained = o_full + 2;
+  uint64_t* p_full = s_full + NS;         // P of a buffer written, O rescaled
+  uint64_t* o_full = p_full + NS;         // O += P V of a buffer done
+  uint64_t* drained = o_full + NS;
   uint64_t* rk_full = drained + 2;        // FP8: tiles of codes
   uint64_t* rk_empty = rk_full + L.raw;
   uint64_t* rv_full = rk_empty + L.raw;
   uint64_t* rv_empty = rv_full + L.raw;
-  static_assert(2 * L.nk + 2 * L.nv + 2 * L.nq + 8 + 4 * L.raw <= 40, "");
+  static_assert(2 * L.nk + 2 * L.nv + 2 * L.nq + 3 * NS + 2 + 4 * L.raw <= 40, "");
   float* exch = reinterpret_cast<float*>(smem + L.exch_off);
   signed char* qexp = reinterpret_cast<signed char*>(smem + L.qexp_off);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L.misc_off);
@@ -384,10 +376,16 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (tid == 0) {   // first use of a map would wait for its fetch
+    if (!kFp8) prefetch_tensormap(&tmq);
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
+  }
   // the share lies in shared memory: it is looked at once a piece, and registers are short
   TreeShare& sh = *reinterpret_cast<TreeShare*>(smem + L.misc_off + 16);
   {
     const TreeShare mine = tree_schedule<kThreadsT>(p, *reinterpret_cast<TreeScratch*>(exch));
+    pdl_launch_dependents();   // the merge's launch runs beside this kernel; it waits for its end
     if (mine.u1 <= mine.u0) return;   // the whole CTA
     if (tid == 0) sh = mine;
   }
@@ -404,9 +402,9 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
       mbar_init(&q_full[i], kFp8 ? kTreeConvertWarps : 1);
       mbar_init(&q_empty[i], kFp8 ? 1 + kTreeSoftmaxWarps : 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < (int)NS; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kTreeSoftmaxWarps);
+      mbar_init(&p_full[i], kTreeSoftmaxWarps / 2);
       mbar_init(&o_full[i], 1);
     }
     mbar_init(&drained[0], 1);
@@ -432,33 +430,40 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   const bool paired = !kFp8 && p.c.paged;
   const uint32_t blk_bytes = paired ? 1024u : 16384u, grp_bytes = paired ? CH * 1024u : 1024u;
   Waiter wait{abort_flag, p.c.status, kWaitLimitNs, *abort_flag != 0};
-  if constexpr (kFp8) {
-    if (warp < kTreeSoftmaxWarps)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(tree_softmax_regs(true)));
-    else
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(tree_other_regs(true)));
-  }
-
+  if (warp < kTreeSoftmaxWarps)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(tree_softmax_regs(kFp8, kSplit)));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(tree_other_regs(kFp8, kSplit)));
   if (warp < kTreeSoftmaxWarps) {
     // ---- softmax -----------------------------------------------------------------------
+    // Team `team` (4 warps, a thread a row) takes the tiles it = team, team + 2, ...; while it
+    // exponentiates one the other team reads the next. Both weigh against one reference per row, m in
+    // shared memory, which belongs to O: before a tile's weights are formed its team learns that the tile
+    // before has settled m (a barrier between the two warps of 32 rows, `settled`), moves it where the
+    // tile exceeds it by more than kRescale, and passes on. Row sums are kept per team, relative to the
+    // reference its thread saw last.
     Cursor c(p, sh);
-    const int quarter = warp & 3, cq = warp >> 2;      // 32 rows, 32 of S's 128 columns
+    const int team = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)quarter << 21);   // TMEM lane quarter * 32
-    float* ex = exch + row;
+    const int settled = 1 + quarter * 2;                           // + the settling team
     uint32_t it = 0;
+    TileSlot<NS> sl;
     float m = -INFINITY, l = 0.f, factor = p.qscale;
-    bool active = false;
+    bool active = false, due = false, masked = false;
     int r = 0;
     unsigned long long word = 0;
     while (c.advance(p, sh)) {
+      float* const m_row = exch + (c.piece & 1) * 128 + row;
       if (c.first()) {
         const int R = c.w.s.T * p.group;
         r = sh.row_tile * kTreeRows + row;
         active = sh.row_tile * kTreeRows + quarter * 32 < R;   // this warp has rows
         const int i = r / p.group;
-        word = r < R ? tree_word(p, c.w.s.row0 + i, i, c.w.s.T) : 0ull;
+        // (the mask's word is on its way until a drafted token's tile needs it)
+        word = r < R && p.mask ? __ldg(p.mask + c.w.s.row0 + i) : 0ull;
         if (r >= R) r = -1;
+        masked = false;
         m = -INFINITY;
         l = 0.f;
         if constexpr (kFp8) {
@@ -469,230 +474,261 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
           if (lane == 0) mbar_arrive(&q_empty[qb]);
         }
       }
-      const int buf = it & 1;
-      const uint32_t s_addr = lane_addr + kColS + (uint32_t)buf * 128u + cq * 32u;
-      const int tok0 = c.kt * kTreeTokens;
-      const bool tail = tok0 + kTreeTokens > c.w.s.ctx;   // drafted tokens or the end in this tile
-      // S of this tile was issued after O of tile it - 2 had completed, so that a parity of o_full
-      // names one phase below
-      wait(&s_full[buf], (it >> 1) & 1);
-      tc_fence_after();
-      if (active) {
-        // The exchange of row maxima between the four warps of a row is skipped while no row exceeds
-        // its reference by more than kRescale: one barrier that reduces a predicate instead of two and
-        // a round trip through shared memory.
-        auto tile = [&](auto tail_c) {
-          constexpr bool kTail = decltype(tail_c)::value;
-          uint32_t vis = ~0u;
-          if constexpr (kTail) vis = visible(c.w.s.ctx - tok0 - cq * 32, word);
-          float top;   // largest logit of the 32 columns (-inf: none seen)
-          {
-            float x[32];
-            tmem_ld32(s_addr, reinterpret_cast<uint32_t*>(x));
-            tmem_wait_ld();
+      if ((it & 1) == team) {
+        const uint32_t s_addr = lane_addr + kColS + sl.buf * 128u;
+        const int tok0 = c.kt * kTreeTokens;
+        const bool tail = tok0 + kTreeTokens > c.w.s.ctx;   // drafted tokens or the end in this tile
+        if (tail && !masked) {
+          word = r < 0 ? 0ull : tree_clip(p, word, r / p.group, c.w.s.T);
+          masked = true;
+        }
+        wait(&s_full[sl.buf], sl.par);
+        tc_fence_after();
+        if (active) {
+          auto tile = [&](auto tail_c) {
+            constexpr bool kTail = decltype(tail_c)::value;
+            // largest logit of the row's 128 columns (-inf: none seen)
             const float none = p.qscale >= 0.f ? -INFINITY : INFINITY;
-            if constexpr (kTail) {
+            float top = none;
+#pragma unroll 1
+            for (int q2 = 0; q2 < 2; ++q2) {
+              float x[64];
+              tmem_ld32(s_addr + q2 * 64, reinterpret_cast<uint32_t*>(x));
+              tmem_ld32(s_addr + q2 * 64 + 32, reinterpret_cast<uint32_t*>(x) + 32);
+              tmem_ready(x);
+              if constexpr (kTail) {
+                const uint32_t v0 = visible(c.w.s.ctx - tok0 - q2 * 64, word);
+                const uint32_t v1 = visible(c.w.s.ctx - tok0 - q2 * 64 - 32, word);
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!(vis >> k & 1u)) x[k] = none;
+                for (int k = 0; k < 64; ++k)
+                  if (!((k < 32 ? v0 : v1) >> (k & 31) & 1u)) x[k] = none;
+              }
+              float mx[4] = {top, x[0], x[1], x[2]};
+              if (p.qscale >= 0.f) {
+#pragma unroll
+                for (int k = 3; k < 63; k += 2)
+                  mx[k >> 1 & 3] = max3(mx[k >> 1 & 3], x[k], x[k + 1]);
+                top = max3(max3(mx[0], mx[1], mx[2]), mx[3], x[63]);
+              } else {
+#pragma unroll
+                for (int k = 3; k < 63; k += 2)
+                  mx[k >> 1 & 3] = min3(mx[k >> 1 & 3], x[k], x[k + 1]);
+                top = min3(min3(mx[0], mx[1], mx[2]), mx[3], x[63]);
+              }
             }
-            float mx[2] = {x[0], x[1]};
-            if (p.qscale >= 0.f) {
+            top = top == none ? -INFINITY : top * factor;
+            if (due) named_bar_sync(settled + (team ^ 1), 64);   // the tile before has settled m
+            float now = top;
+            if (!c.first()) {
+              now = *m_row;
+              if (now != m) {   // the other team moved it, or this is the team's first tile of the piece
+                l *= fast_exp2(m - now);
+                if (l != l) l = m == -INFINITY ? 0.f : l;
+                m = now;
+              }
+              float f = 1.f;
+              if (top > now + kRescale) {
+                f = fast_exp2(now - top);
+                now = top;
+                l *= f;
+                *m_row = now;
+              }
+              if (__any_sync(0xffffffffu, f != 1.f)) {
+                // O so far, relative to the new reference
+                // (S of this tile waited for O of the tile NS before it, so the parity names one phase)
+                wait(&o_full[sl.before()], sl.before_par());
+                tc_fence_after();
+#pragma unroll 1
+                for (int cc = 0; cc < D; cc += 32) {
+                  uint32_t o[32];
+                  tmem_ld32(lane_addr + kColO + cc, o);
+                  tmem_ready(o);
 #pragma unroll
-              for (int k = 2; k < 32; k += 2) mx[k >> 1 & 1] = max3(mx[k >> 1 & 1], x[k], x[k + 1]);
-              mx[0] = fmaxf(mx[0], mx[1]);
-            } else {
-#pragma unroll
-              for (int k = 2; k < 32; k += 2) mx[k >> 1 & 1] = min3(mx[k >> 1 & 1], x[k], x[k + 1]);
-              mx[0] = fminf(mx[0], mx[1]);
-            }
-            top = mx[0] == none ? -INFINITY : mx[0] * factor;
-          }
-          const bool fresh = c.first();
-          if (bar_any(1 + quarter, 128, fresh || top > m + kRescale)) {
-            ex[cq * 128] = top;
-            named_bar_sync(1 + quarter, 128);
-            top = fmaxf(fmaxf(ex[0], ex[128]), fmaxf(ex[256], ex[384]));
-            bool move = false;
-            float f = 1.f;
-            if (fresh) {
-              m = top;
-            } else if (top > m + kRescale) {
-              f = fast_exp2(m - top);
-              m = top;
-              l *= f;
-              move = true;
-            }
-            if (__any_sync(0xffffffffu, move)) {
-              // O so far, relative to the new reference: 32 columns a warp
-              wait(&o_full[buf ^ 1], ((it - 1) >> 1) & 1);
-              tc_fence_after();
-              if (cq * 32 < D) {
-                uint32_t o[32];
-                const uint32_t a = lane_addr + kColO + cq * 32;
-                tmem_ld32(a, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                tmem_st32(a, o);
+                  for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                  tmem_st32(lane_addr + kColO + cc, o);
+                }
                 tmem_wait_st();
               }
+            } else {
+              *m_row = now;
             }
-          }
-          // P over the columns of S that it comes from (S is read once more: registers are short), 8
-          // columns of hi and 8 of lo for every 16 tokens
-          const float ref = m == -INFINITY ? 0.f : m;
-          const f32x2 f2 = f2_pack(factor, factor), neg = f2_pack(-ref, -ref);
-          f32x2 sum[2] = {0ull, 0ull};
+            m = now;
+            named_bar_arrive(settled + team, 64);
+            // P over the columns of S that it comes from (S is read once more): for every 32 tokens 16
+            // columns of hi, 16 of lo
+            const float ref = m == -INFINITY ? 0.f : m;
+            const f32x2 f2 = f2_pack(factor, factor), neg = f2_pack(-ref, -ref);
+            f32x2 sum[2] = {0ull, 0ull};
+            auto weigh = [&](float* x, int h) {
+              uint32_t pk[kSplit ? 32 : 16];
+              uint32_t vis = ~0u;
+              if constexpr (kTail) vis = visible(c.w.s.ctx - tok0 - h * 32, word);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x[16];
-            uint32_t pk[16];
-            tmem_ld16(s_addr + h * 16, reinterpret_cast<uint32_t*>(x));
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              f32x2 d = neg;
-              f2_fma(d, f2_pack(x[k], x[k + 1]), f2);
-              float a, b;
-              f2_unpack(d, a, b);
-              if constexpr (kTail) {
-                if (!(vis >> (h * 16 + k) & 1u)) a = -INFINITY;
-                if (!(vis >> (h * 16 + k + 1) & 1u)) b = -INFINITY;
+              for (int k = 0; k < 32; k += 2) {
+                f32x2 d = neg;
+                f2_fma(d, f2_pack(x[k], x[k + 1]), f2);
+                float a, b;
+                f2_unpack(d, a, b);
+                if constexpr (kTail) {
+                  if (!(vis >> k & 1u)) a = -INFINITY;
+                  if (!(vis >> (k + 1) & 1u)) b = -INFINITY;
+                }
+                a = fast_exp2(a);
+                b = fast_exp2(b);
+                const f32x2 e = f2_pack(a, b);
+                sum[k >> 1 & 1] = f2_add(sum[k >> 1 & 1], e);
+                const uint32_t hi = pack_pair<M>(a, b);
+                pk[k / 2] = hi;
+                if constexpr (kSplit) {
+                  const float2 hf = unpack_pair<M>(hi);
+                  float da, db;
+                  f2_unpack(f2_add(e, f2_pack(-hf.x, -hf.y)), da, db);
+                  pk[16 + k / 2] = pack_pair<M>(da, db);
+                }
               }
-              a = fast_exp2(a);
-              b = fast_exp2(b);
-              const f32x2 e = f2_pack(a, b);
-              sum[k >> 1 & 1] = f2_add(sum[k >> 1 & 1], e);
-              const uint32_t hi = pack_pair<M>(a, b);
-              pk[k / 2] = hi;
-              if constexpr (kSplit) {
-                const float2 hf = unpack_pair<M>(hi);
-                float da, db;
-                f2_unpack(f2_add(e, f2_pack(-hf.x, -hf.y)), da, db);
-                pk[8 + k / 2] = pack_pair<M>(da, db);
-              }
+              if constexpr (kSplit) tmem_st32(s_addr + h * 32, pk);
+              else tmem_st16(s_addr + h * 32, pk);
+            };
+            float xa[32], xb[32];   // the next 32 columns are on their way while these are weighed
+            tmem_ld32(s_addr, reinterpret_cast<uint32_t*>(xa));
+            tmem_ready(xa);
+#pragma unroll 1
+            for (int h = 0; h < 4; h += 2) {
+              tmem_ld32(s_addr + (h + 1) * 32, reinterpret_cast<uint32_t*>(xb));
+              weigh(xa, h);
+              tmem_ready(xb);
+              if (h == 0) tmem_ld32(s_addr + 64, reinterpret_cast<uint32_t*>(xa));
+              weigh(xb, h + 1);
+              tmem_ready(xa);
             }
-            if constexpr (kSplit) tmem_st16(s_addr + h * 16, pk);
-            else tmem_st8(s_addr + h * 16, pk);
-          }
-          {
             float a, b;
             f2_unpack(f2_add(sum[0], sum[1]), a, b);
             l += a + b;
-          }
-          tmem_wait_st();
-        };
-        if (tail) tile(std::true_type{});
-        else tile(std::false_type{});
-      }
-      if (tail) {
-        // V rows that the MMA reads past the sequence's end are cleared, and values that are not
-        // finite are taken out of drafted tokens' rows (0 * inf would reach rows that the token is
-        // hidden from) and added to the rows that see them below.
-        const uint32_t vs = it % L.nv;
-        wait(&v_full[vs], (it / L.nv) & 1);
-        const int valid = min(kTreeTokens, c.w.s.n - tok0);
-        const int t = tid & 127, end = (valid + 15) / 16 * 16, blk = tid >> 7;
-        if (blk < CH) {
-          uint4* v4 = reinterpret_cast<uint4*>(smem + L.v_off + vs * kTile + (t >> 3) * grp_bytes +
-                                               (t & 7) * 128 + blk * blk_bytes);
-          if (t >= valid && t < end) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v4[(k + t) & 7] = make_uint4(0u, 0u, 0u, 0u);
-          } else if (t < valid && tok0 + t >= c.w.s.ctx) {
-            constexpr uint32_t kInf = std::is_same<M, __half>::value ? 0x7c00u : 0x7f80u;
-            bool found = false;
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k) {
-              const uint4 v = v4[(k + t) & 7];
-              uint32_t w[4] = {v.x, v.y, v.z, v.w};
-              bool here = false;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((w[e] & kInf) == kInf) {
-                  w[e] &= 0xffff0000u;
-                  here = true;
-                }
-                if ((w[e] >> 16 & kInf) == kInf) {
-                  w[e] &= 0xffffu;
-                  here = true;
-                }
-              }
-              if (here) v4[(k + t) & 7] = make_uint4(w[0], w[1], w[2], w[3]);
-              found |= here;
-            }
-            if (found) atomicOr(odd, 1ull << (tok0 + t - c.w.s.ctx));
-          }
+            tmem_wait_st();
+          };
+          if (tail) tile(std::true_type{});
+          else tile(std::false_type{});
+        } else {
+          if (due) named_bar_sync(settled + (team ^ 1), 64);
+          named_bar_arrive(settled + team, 64);
         }
-        fence_async_smem();
+        due = false;
+        if (tail) {
+          // V rows that the MMA reads past the sequence's end are cleared, and values that are not
+          // finite are taken out of drafted tokens' rows (0 * inf would reach rows that the token is
+          // hidden from) and added to the rows that see them below.
+          const uint32_t vs = it % L.nv;
+          wait(&v_full[vs], (it / L.nv) & 1);
+          const int valid = min(kTreeTokens, c.w.s.n - tok0);
+          const int end = (valid + 15) / 16 * 16, from = max(c.w.s.ctx - tok0, 0);
+          constexpr uint32_t kInf = std::is_same<M, __half>::value ? 0x7c00u : 0x7f80u;
+          // 16-byte chunks of rows from .. end - 1, a chunk a thread
+#pragma unroll 1
+          for (int i = tid & 127; i < (end - from) * (8 * CH); i += 128) {
+            const int t = from + i / (8 * CH), k = i % (8 * CH);
+            uint4* at = reinterpret_cast<uint4*>(smem + L.v_off + vs * kTile + (t >> 3) * grp_bytes +
+                                                 (t & 7) * 128 + (k >> 3) * blk_bytes + (k & 7) * 16);
+            if (t >= valid) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+            const uint4 v = *at;
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            bool here = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool lo = (w[e] & kInf) == kInf, hi = (w[e] >> 16 & kInf) == kInf;
+              here |= lo | hi;
+              w[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+            }
+            if (here) {
+              *at = make_uint4(w[0], w[1], w[2], w[3]);
+              atomicOr(odd, 1ull << (tok0 + t - c.w.s.ctx));
+            }
+          }
+          fence_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[sl.buf]);
+      } else {
+        due = true;   // the other team settles m with this tile: learnt at the next one, or below
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[buf]);
 
       if (c.last()) {
-        // ---- a piece's end: normalise and store ----------------------------------------
-        if (it >= 1) wait(&o_full[buf ^ 1], ((it - 1) >> 1) & 1);
-        wait(&o_full[buf], (it >> 1) & 1);
+        // ---- a piece's end: normalise and store, half of the columns a team ----------------
+        wait(&s_full[sl.buf], sl.par);   // (O of this buffer's tile before is done: the next phase is its)
+        wait(&o_full[sl.buf], sl.par);
         tc_fence_after();
+        if (due) named_bar_sync(settled + (team ^ 1), 64);
+        due = false;
         if (active) {
-          named_bar_sync(1 + quarter, 128);   // all have read the maxima
-          ex[cq * 128] = l;
-          named_bar_sync(1 + quarter, 128);
-          const float total = (ex[0] + ex[128]) + (ex[256] + ex[384]);
+          // the final reference, settled by the last tile
+          const float last = *m_row;
+          if (last != m) {
+            l *= fast_exp2(m - last);
+            if (l != l) l = m == -INFINITY ? 0.f : l;
+            m = last;
+          }
+          float* const l_row = exch + 256 + row;
+          l_row[team * 128] = l;
+          named_bar_sync(9 + quarter, 64);
+          const float total = l_row[0] + l_row[128];
           const float inv = total == 0.f ? 0.f : 1.f / total;
-          const unsigned long long strange = *odd & word;
-          const int col = cq * 32;
+          unsigned long long strange = *odd;
+          if (strange && r >= 0)
+            strange &= masked ? word : tree_clip(p, word, r / p.group, c.w.s.T);
           const bool whole = c.w.whole;
           // the row of out (and lse), or of the partials
           const long long at =
               whole ? (long long)(c.w.s.row0 + r / p.group) * p.c.hq + c.w.kvh * p.group + r % p.group
-                    : tree_slot(sh.owner, c.w.head, sh.row_tile, sh.row_tiles) * kTreeRows + row;
-          if (cq == 0 && r >= 0) {
+                    : tree_slot(sh.owner, c.w.head, sh.row_tiles * sh.heads,
+                              sh.head * sh.row_tiles + sh.row_tile) * kTreeRows + row;
+          if (team == 0 && r >= 0) {
             const float lg = total == 0.f ? -INFINITY : m + log2f(total);
             if (!whole) p.part_l[at] = lg;
             else if (p.out_lse) p.out_lse[at] = lg * 0.69314718055994531f;
           }
-          if (col < D) {
+          const float g = whole ? inv * p.v_scale : inv;
+#pragma unroll 1
+          for (int col = team * (D / 2); col < (team + 1) * (D / 2); col += 32) {
             float o[32];
             tmem_ld32(lane_addr + kColO + col, reinterpret_cast<uint32_t*>(o));
-            tmem_wait_ld();
-            if (r >= 0) {
-              const float g = whole ? inv * p.v_scale : inv;
-              if (!whole || p.c.out_dtype == kOutF32) {
-                float4* dst = reinterpret_cast<float4*>(
-                    (whole ? static_cast<float*>(p.out) : p.part_o) + at * D + col);
+            tmem_ready(o);
+            if (r < 0) continue;
+            if (!whole || p.c.out_dtype == kOutF32) {
+              float4* dst = reinterpret_cast<float4*>(
+                  (whole ? static_cast<float*>(p.out) : p.part_o) + at * D + col);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  dst[k] = make_float4(o[4 * k] * g, o[4 * k + 1] * g, o[4 * k + 2] * g,
-                                       o[4 * k + 3] * g);
-              } else {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + col);
+              for (int k = 0; k < 8; ++k)
+                dst[k] = make_float4(o[4 * k] * g, o[4 * k + 1] * g, o[4 * k + 2] * g, o[4 * k + 3] * g);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + col);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  uint32_t w[4];
+              for (int k = 0; k < 4; ++k) {
+                uint32_t w[4];
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const float a = o[8 * k + 2 * e] * g, b = o[8 * k + 2 * e + 1] * g;
-                    w[e] = p.c.out_dtype == kOutF16 ? pack_pair<__half>(a, b)
-                                                    : pack_pair<__nv_bfloat16>(a, b);
-                  }
-                  dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int e = 0; e < 4; ++e) {
+                  const float a = o[8 * k + 2 * e] * g, b = o[8 * k + 2 * e + 1] * g;
+                  w[e] = p.c.out_dtype == kOutF16 ? pack_pair<__half>(a, b)
+                                                  : pack_pair<__nv_bfloat16>(a, b);
                 }
+                dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
               }
-              if (strange)
-                add_odd<T, D>(p, c.w.b, c.w.s.ctx, c.w.kvh, strange, v_cache, col,
-                              whole ? p.out : p.part_o, at, whole ? p.c.out_dtype : (int)kOutF32);
             }
+            if (strange)   // (r >= 0)
+              add_odd<T, D>(p, c.w.b, c.w.s.ctx, c.w.kvh, strange, v_cache, col,
+                            whole ? p.out : p.part_o, at, whole ? p.c.out_dtype : (int)kOutF32);
           }
+          tc_fence_before();
         }
-        // every warp has read `odd`; clear it for the next piece
-        named_bar_sync(5, kTreeSoftmaxWarps * 32);
+        // O and `odd` have been read by everyone: the next piece may write them
+        named_bar_sync(13, kTreeSoftmaxWarps * 32);
         if (tid == 0) *odd = 0;
-        named_bar_sync(5, kTreeSoftmaxWarps * 32);
+        named_bar_sync(13, kTreeSoftmaxWarps * 32);
       }
       ++it;
+      sl.next();
     }
   } else if (warp < kTreeSoftmaxWarps + 2) {
     // ---- loaders: K (with q, for 16-bit caches) and V ------------------------------------------
@@ -704,14 +740,14 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
     const uint32_t slots = kFp8 ? L.raw : is_v ? L.nv : L.nk;
     uint8_t* const ring = smem + (kFp8 ? (is_v ? L.rawv_off : L.rawk_off) : (is_v ? L.v_off : L.k_off));
     constexpr uint32_t kSlot = kFp8 ? kCode : kTile;
-    if (lane == 0) prefetch_tensormap(tm);
     const uint64_t pol = kv_policy(sh.row_tiles);
     // Paged (and FP8) caches: lane i loads the i-th run of `box` tokens, whole rows. Contiguous 16-bit
     // caches: lane i loads block i of all tokens.
     const bool rows = kFp8 || p.c.paged;
     const int box = p.c.box_tokens;
-    auto lookup = [&](int kt) {   // lane's cache row; -2: nothing to load, -1: a bad page
-      const int t = kt * kTreeTokens + (rows ? lane * box : 0);
+    // lane's cache row of the cursor's tile; -2: nothing to load, -1: a bad page
+    auto lookup = [&]() {
+      const int t = c.kt * kTreeTokens + (rows ? lane * box : 0);
       if (rows ? lane * box >= kTreeTokens || t >= c.w.s.n : lane >= CH) return -2;
       const int entry =
           p.c.paged ? __ldg(p.c.block_table + (long long)c.w.b * p.c.max_blocks + t / p.c.page_size)
@@ -723,44 +759,46 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
                                      : lane * blk_bytes;
     const uint32_t lane_bytes = (uint32_t)box * (kFp8 ? D : rows ? CH * 128 : 128);
     uint32_t slot = 0, par = 1, it = 0, issued = 0;
-    int z = -2, loaded = 0;
-    while (c.advance(p, sh)) {
-      if (c.first()) {
-        z = lookup(c.kt);
-        if (!kFp8 && !is_v) {
-          const int qb = c.piece & 1;
-          const int i0 = sh.row_tile * (kTreeRows / p.group);   // the tile's first drafted token
-          wait(&q_empty[qb], ((c.piece >> 1) & 1) ^ 1);
-          if (!wait.dead) {
-            if (lane == 0) mbar_arrive_expect_tx(&q_full[qb], kTile);
-            __syncwarp();
-            if (lane < CH)
-              tma_load_4d(smem + L.q_off + qb * kTile + lane * (128 * 128), &tmq, &q_full[qb], 0,
-                          c.w.kvh * p.group, c.w.s.row0 + i0, lane, pol);
-            ++loaded;
-          }
+    int loaded = 0;
+    // the cursor is a tile ahead of the loads, so that its page lookups are on their way meanwhile
+    bool more = c.advance(p, sh);
+    int z = more ? lookup() : -2;
+    while (more) {
+      const int kvh = c.w.kvh, row0 = c.w.s.row0, piece = c.piece, z_now = z;
+      const bool first = c.first();
+      more = c.advance(p, sh);
+      z = more ? lookup() : -2;
+      if (!kFp8 && !is_v && first) {
+        const int qb = piece & 1;
+        const int i0 = sh.row_tile * (kTreeRows / p.group);   // the tile's first drafted token
+        wait(&q_empty[qb], ((piece >> 1) & 1) ^ 1);
+        if (!wait.dead) {
+          if (lane == 0) mbar_arrive_expect_tx(&q_full[qb], kTile);
+          __syncwarp();
+          if (lane < CH)
+            tma_load_4d(smem + L.q_off + qb * kTile + lane * (128 * 128), &tmq, &q_full[qb], 0,
+                        kvh * p.group, row0 + i0, lane, pol);
+          ++loaded;
         }
       }
-      const int z_next = c.last() ? -2 : lookup(c.kt + 1);   // in flight during the wait
       wait(&empty[slot], par);
       if (!wait.dead) {
-        const int boxes = __popc(__ballot_sync(0xffffffffu, z != -2));
+        const int boxes = __popc(__ballot_sync(0xffffffffu, z_now != -2));
         if (lane == 0) mbar_arrive_expect_tx(&full[slot], boxes * lane_bytes);
         __syncwarp();
-        if (z != -2) {
+        if (z_now != -2) {
           uint8_t* dst = ring + slot * kSlot + lane_off;
           // a bad page: past the pool, zeros
-          if (z < 0) atomicOr(p.c.status, kStatusBadBlockTable);
-          const int at = z < 0 ? p.c.num_blocks * p.c.page_size : z;
-          if constexpr (kFp8) tma_load_3d(dst, tm, &full[slot], 0, at, c.w.kvh, pol);
-          else if (rows) tma_load_5d(dst, tm, &full[slot], 0, 0, 0, at / 8, c.w.kvh, pol);
-          else tma_load_4d(dst, tm, &full[slot], 0, at, lane, c.w.kvh, pol);
+          if (z_now < 0) atomicOr(p.c.status, kStatusBadBlockTable);
+          const int at = z_now < 0 ? p.c.num_blocks * p.c.page_size : z_now;
+          if constexpr (kFp8) tma_load_3d(dst, tm, &full[slot], 0, at, kvh, pol);
+          else if (rows) tma_load_5d(dst, tm, &full[slot], 0, 0, 0, at / 8, kvh, pol);
+          else tma_load_4d(dst, tm, &full[slot], 0, at, lane, kvh, pol);
         }
         issued = it + 1;
       }
       __syncwarp();
       if (++slot == slots) slot = 0, par ^= 1;
-      z = z_next;
       ++it;
     }
     // never leave with copies in flight
@@ -778,18 +816,18 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
     const uint64_t k_desc = tile_desc(smem_u32(smem + L.k_off), 16, grp_bytes);
     const bool issuer = elect_one();
     uint32_t it = 0, k_slot = 0, k_par = 0;
+    TileSlot<NS> sl;
     // the merge reads the first piece of every owner, whether this row tile has rows in it or not
     {
       TreeWalk w(p, sh);
-      if (w.next(p, sh) && sh.row_tile == 0 && issuer)
-        p.info[sh.owner] = make_int4(w.b, w.kvh, w.t0, w.s.tiles);
+      if (w.next(p, sh) && sh.row_tile == 0 && sh.head == 0 && issuer) tree_record(p, sh, w);
     }
     while (c.advance(p, sh)) {
-      const uint32_t qb = c.piece & 1, buf = it & 1;
+      const uint32_t qb = c.piece & 1, buf = sl.buf;
       const bool last = c.last();
       if (c.first()) wait(&q_full[qb], (c.piece >> 1) & 1);
       // the buffer's P has been used (its O is done); the softmax read its S before that
-      if (it >= 2) wait(&o_full[buf], ((it - 2) >> 1) & 1);
+      if (it >= NS) wait(&o_full[buf], sl.par ^ 1);
       wait(&k_full[k_slot], k_par);
       tc_fence_after();
       if (!wait.dead && issuer) {
@@ -812,6 +850,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
       __syncwarp();
       if (++k_slot == L.nk) k_slot = 0, k_par ^= 1;
       ++it;
+      sl.next();
     }
     if (issuer) tc_commit(&drained[0]);   // nothing leaves before the last MMA has completed
     mbar_wait(&drained[0], 0, kWaitLimitNs);
@@ -821,34 +860,37 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
     constexpr bool kBf16 = std::is_same<M, __nv_bfloat16>::value;
     constexpr uint32_t kDescO = mma_desc(kBf16, D, true);
     const uint64_t v_desc = tile_desc(smem_u32(smem + L.v_off), blk_bytes, grp_bytes);
-    const uint32_t v_step = 2u * grp_bytes >> 4;   // 16 tokens; their P: 8 columns of hi, 8 of lo
+    const uint32_t v_step = 2u * grp_bytes >> 4;   // 16 tokens
+    // P's columns of 16 tokens (hi): every 32 tokens' P lies over their S, lo 16 columns behind hi
+    auto p_col = [](int k) { return (uint32_t)(k >> 1) * 32u + (uint32_t)(k & 1) * 8u; };
     const bool issuer = elect_one();
-    uint32_t it = 0, v_slot = 0, v_par = 0;
+    uint32_t v_slot = 0, v_par = 0;
+    TileSlot<NS> sl;
     while (c.advance(p, sh)) {
-      const uint32_t buf = it & 1;
+      const uint32_t buf = sl.buf;
       const uint64_t vd = v_desc + v_slot * (kTile >> 4);
       const uint32_t pa = tmem + kColS + buf * 128u, oc = tmem + kColO;
       const int valid = c.w.s.n - c.kt * kTreeTokens;
       const bool fresh = c.first();
       wait(&v_full[v_slot], v_par);
-      wait(&p_full[buf], (it >> 1) & 1);
+      wait(&p_full[buf], sl.par);
       tc_fence_after();
       if (!wait.dead && issuer) {
         if (valid >= kTreeTokens) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_ts(oc, pa + k * 16u, vd + k * v_step, kDescO, k != 0 || !fresh);
+            mma_ts(oc, pa + p_col(k), vd + k * v_step, kDescO, k != 0 || !fresh);
           if constexpr (kSplit) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_ts(oc, pa + 8u + k * 16u, vd + k * v_step, kDescO, true);
+              mma_ts(oc, pa + 16u + p_col(k), vd + k * v_step, kDescO, true);
           }
         } else {   // the sequence ends in this tile
           const int steps = (valid + 15) / 16;
 #pragma unroll 1
           for (int k = 0; k < steps; ++k) {
-            mma_ts(oc, pa + k * 16u, vd + k * v_step, kDescO, k != 0 || !fresh);
-            if constexpr (kSplit) mma_ts(oc, pa + 8u + k * 16u, vd + k * v_step, kDescO, true);
+            mma_ts(oc, pa + p_col(k), vd + k * v_step, kDescO, k != 0 || !fresh);
+            if constexpr (kSplit) mma_ts(oc, pa + 16u + p_col(k), vd + k * v_step, kDescO, true);
           }
         }
         tc_commit(&o_full[buf]);
@@ -856,7 +898,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
       }
       __syncwarp();
       if (++v_slot == L.nv) v_slot = 0, v_par ^= 1;
-      ++it;
+      sl.next();
     }
     if (issuer) tc_commit(&drained[1]);
     mbar_wait(&drained[1], 0, kWaitLimitNs);
@@ -924,6 +966,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
     uint32_t n = 0, rk = 0, rk_par = 0;
     while (c.advance(p, sh)) {
       if (c.first()) {
+        if (n) pass(false, true, n, rk, rk_par);   // the piece before is done with first
         // q: a thread's row as f16 times a power of two, so that its largest element lies in
         // [2^14, 2^15), into TMEM
         const int qb = c.piece & 1, rr = cw * 32 + lane, r = sh.row_tile * kTreeRows + rr;
@@ -933,16 +976,28 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
             static_cast<const __nv_bfloat16*>(p.q) +
             ((long long)(c.w.s.row0 + r / p.group) * p.c.hq + c.w.kvh * p.group + r % p.group) * D);
         const bool have = r < c.w.s.T * p.group;
+        if (have) {   // its lines, and those of the next KV head's heads, which mostly come next
+          const bool next = c.w.kvh + 1 < p.c.hkv;
+          for (int j = 0; j < D / 8; j += 8) {
+            prefetch_l2(src + j);
+            if (next) prefetch_l2(src + p.group * (D / 8) + j);
+          }
+        }
         const uint4 none = make_uint4(0u, 0u, 0u, 0u);
         float big = 0.f;
-#pragma unroll 4
-        for (int j = 0; j < D / 8; ++j) {
-          const uint4 v = have ? __ldg(src + j) : none;
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 1
+        for (int j = 0; j < D / 64; ++j) {   // a 128-byte line at a time: registers are short
+          uint4 v[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack_pair<__nv_bfloat16>(u[e]);
-            big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+          for (int k = 0; k < 8; ++k) v[k] = have ? __ldg(src + j * 8 + k) : none;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack_pair<__nv_bfloat16>(u[e]);
+              big = max3(big, fabsf(f.x), fabsf(f.y));
+            }
           }
         }
         // 2^(14 - exponent of the largest), within what an int8 holds; 1 for a row of zeros
@@ -970,8 +1025,10 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[qb]);
+        pass(true, false, n, rk, rk_par);
+      } else {
+        pass(true, true, n, rk, rk_par);
       }
-      pass(true, n >= 1, n, rk, rk_par);
       if (++rk == (uint32_t)L.raw) rk = 0, rk_par ^= 1;
       ++n;
     }
@@ -982,7 +1039,6 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   __syncthreads();
   tc_fence_after();
   if (warp == kTreeSoftmaxWarps + 2) tmem_free(tmem, kTmemCols);
-  pdl_launch_dependents();
 }
 
 template <typename T, bool kSplit>

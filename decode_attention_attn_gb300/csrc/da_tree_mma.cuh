@@ -8,27 +8,30 @@ namespace da {
 constexpr int kTreeRows = 128;       // query rows per tile: the M of tcgen05.mma
 constexpr int kTreeTokens = 128;     // KV tokens per tile
 
-// Warps: 16 softmax (a thread has 32 columns of one row's S), then the loaders of K (with q, for 16-bit
-// caches) and of V, the issuer of S, the issuer of O, and for FP8 caches 4 that convert codes to f16
-// tiles (and q).
-constexpr int kTreeSoftmaxWarps = 16;
+// Warps: 8 softmax (two teams of 4 that take the KV tiles in turn, a thread a row), then the loaders of K
+// (with q, for 16-bit caches) and of V, the issuer of S, the issuer of O, and for FP8 caches 4 that
+// convert codes to f16 tiles (and q). No register may spill: with all of L1 in use as shared memory a
+// spilled one costs an L2 round trip.
+constexpr int kTreeSoftmaxWarps = 8;
 constexpr int kTreeConvertWarps = 4;
 __host__ __device__ constexpr int tree_threads(bool fp8) {
   return (kTreeSoftmaxWarps + 4 + (fp8 ? kTreeConvertWarps : 0)) * 32;
 }
 
-// Registers: compiled (and launched) with tree_launch_regs a thread; in the FP8 kernel the softmax warps
-// then give some to the others. A spilled register costs an L2 round trip here, with all of L1 in use as shared
-// memory: at 128 registers for everyone the FP8 kernel spent most of its time on spills.
-__host__ __device__ constexpr int tree_launch_regs(bool fp8) { return fp8 ? 80 : 96; }
-__host__ __device__ constexpr int tree_softmax_regs(bool fp8) { return fp8 ? 72 : 96; }
-__host__ __device__ constexpr int tree_other_regs(bool fp8) { return 96; }
-__host__ __device__ constexpr bool tree_regs_fit(bool fp8) {
-  return kTreeSoftmaxWarps * tree_softmax_regs(fp8) +
-             (tree_threads(fp8) / 32 - kTreeSoftmaxWarps) * tree_other_regs(fp8) <=
+// The softmax warps take registers from the others; all are launched with tree_launch_regs.
+__host__ __device__ constexpr int tree_launch_regs(bool fp8) { return fp8 ? 128 : 168; }
+__host__ __device__ constexpr int tree_softmax_regs(bool fp8, bool split) {
+  return !fp8 ? 192 : split ? 168 : 152;
+}
+__host__ __device__ constexpr int tree_other_regs(bool fp8, bool split) {
+  return !fp8 ? 120 : split ? 88 : 104;
+}
+__host__ __device__ constexpr bool tree_regs_fit(bool fp8, bool split) {
+  return kTreeSoftmaxWarps * tree_softmax_regs(fp8, split) +
+             (tree_threads(fp8) / 32 - kTreeSoftmaxWarps) * tree_other_regs(fp8, split) <=
          tree_threads(fp8) / 32 * tree_launch_regs(fp8);
 }
-static_assert(tree_regs_fit(false) && tree_regs_fit(true),
+static_assert(tree_regs_fit(false, true) && tree_regs_fit(true, true) && tree_regs_fit(true, false),
               "the register split must fit the launch allocation");
 
 // A 16-bit tile of 128 rows (tokens or query rows) of D elements in shared memory, as tcgen05.mma
@@ -64,7 +67,7 @@ __host__ __device__ constexpr TreeLayout tree_layout(int D, bool fp8) {
   off += L.raw * code;
   L.bar_off = off;
   off += 40 * 8;
-  L.exch_off = off;           // row maxima of the four column quarters; scratch of the schedule
+  L.exch_off = off;           // row references of two pieces, row sums of the two teams
   off += 4 * 128 * 4;
   L.qexp_off = off;           // FP8: q's power of two per row
   off += 2 * 128;
@@ -78,7 +81,7 @@ static_assert(tree_layout(128, false).total <= kSmemLimit, "");
 static_assert(tree_layout(128, true).total <= kSmemLimit, "");
 static_assert(tree_layout(64, false).total <= kSmemLimit, "");
 static_assert(tree_layout(64, true).total <= kSmemLimit, "");
-static_assert(sizeof(TreeScratch) <= 4 * 128 * 4, "the schedule's scratch lies in the exchange");
+static_assert(sizeof(TreeScratch) <= 4 * 128 * 4, "the schedule's scratch lies there first");
 
 // The kernel of a cache type (da_dtype, or FP8), head_dim and output; null: not built.
 // split: P enters as the sum of two 16-bit parts.

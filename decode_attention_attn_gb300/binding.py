@@ -555,27 +555,31 @@ class DecodeAttention:
         return out, out_lse, row_flags
 
 
-def _device_of(**tensors):
-    """The one CUDA device of the given tensors (None entries are passed over)."""
-    device = None
-    for name, t in tensors.items():
+def _device_index(names: str, *tensors) -> int:
+    """The index of the one CUDA device that the tensors (named in `names`; None is passed over) are on."""
+    index = None
+    for i, t in enumerate(tensors):
         if t is None:
             continue
-        if t.device.type != "cuda":
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-    return device
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{names.split()[i]} must be a CUDA tensor")
+        if index is None:
+            index = d
+        elif d != index:
+            raise ValueError(f"{names.split()[i]} is on cuda:{d}, other tensors on cuda:{index}")
+    return index
 
 
 def _rows_tensor(name, t, dtype, heads, d):
-    """A [rows, heads, d] tensor whose heads are contiguous (rows and heads may be strided)."""
-    if t.dtype != dtype or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or \
-            (t.stride(2) != 1 and t.numel()):
-        raise ValueError(f"{name} must be a [rows, {heads}, {d}] tensor of {dtype} whose last "
-                         "dimension is contiguous")
+    """A [rows, heads, d] tensor whose heads are contiguous (rows and heads may be strided). Returns its
+    row and head strides."""
+    if t.dtype != dtype or t.dim() != 3 or t.shape[1:] != (heads, d):
+        raise ValueError(f"{name} must be a [rows, {heads}, {d}] tensor of {dtype}")
+    row, head, one = t.stride()
+    if one != 1 and t.numel():
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return row, head
 
 
 def _int32(name, t, numel):
@@ -584,20 +588,24 @@ def _int32(name, t, numel):
         raise ValueError(f"{name} must be a contiguous int32 tensor of {numel} elements")
 
 
-def _stream_of(device, stream):
-    """The stream to enqueue on (the device's current one unless given), and whether the call must
-    first make that device current."""
+def _launch(fn, handle, args, index, stream):
+    """Call fn on the given stream (the device's current one unless given), with the tensors' device
+    current."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream or None, torch.cuda.current_device() != device.index
+    if stream is not None:
+        s = stream.cuda_stream
+    else:
+        s = torch._C._cuda_getCurrentRawStream(index)   # current_stream() without its objects
+    args.cuda_stream = s or None
+    if torch._C._cuda_getDevice() == index:
+        fn(handle, args)
+    else:
+        with torch.cuda.device(index):
+            fn(handle, args)
 
 
-def _call(device, switch, fn, *args):
-    if not switch:
-        return fn(*args)
-    import torch
-    with torch.cuda.device(device):
-        return fn(*args)
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 class Rope:
@@ -634,43 +642,57 @@ class Rope:
         """Rows of x (fp32, fp16 or bf16; rows and heads may be strided) rotated by `positions`
         (int32 [rows]), into `out` (x itself: in place). transpose: the transposed map, which takes
         the gradient of the output to the gradient of x."""
-        import torch
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if x.dtype not in self._codes:
+        code = self._codes.get(x.dtype)
+        if code is None:
             raise ValueError("x must be fp32, fp16 or bf16")
-        device = _device_of(x=x, positions=positions, out=out)
         if x.dim() != 3:
             raise ValueError("x must be a [rows, heads, head_dim] tensor")
+        if out is None:
+            import torch
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         rows, heads = x.shape[0], x.shape[1]
-        _rows_tensor("x", x, x.dtype, heads, self.head_dim)
-        _rows_tensor("out", out, x.dtype, heads, self.head_dim)
+        x_row, x_head = _rows_tensor("x", x, x.dtype, heads, self.head_dim)
+        out_row, out_head = _rows_tensor("out", out, x.dtype, heads, self.head_dim)
         if out.shape[0] != rows:
             raise ValueError("out must have as many rows as x")
         _int32("positions", positions, rows)
+        index = _device_index("x positions out", x, positions, out)
         if rows == 0 or heads == 0:
             return out
-        s, switch = _stream_of(device, stream)
-        xs, os_ = x.stride(), out.stride()
-        args = da_rope_args(x.data_ptr(), out.data_ptr(), self._codes[x.dtype], rows, heads, xs[0],
-                            xs[1], os_[0], os_[1], positions.data_ptr(), int(bool(transpose)), s)
-        _call(device, switch, decode_attn_rope_apply, self.handle, args)
+        args = da_rope_args(x.data_ptr(), out.data_ptr(), code, rows, heads, x_row, x_head, out_row,
+                            out_head, positions.data_ptr(), int(bool(transpose)))
+        _launch(decode_attn_rope_apply, self.handle, args, index, stream)
         return out
 
 
-def _cache_args(pr, kv_ok, k_cache, v_cache, block_table, row_offsets, start):
-    """Checks of the cache, its block table and a step's row layout."""
-    shape = (pr.num_physical_blocks, pr.page_size, pr.num_kv_heads, pr.head_dim) if pr.paged \
-        else (pr.batch, pr.max_seq_len, pr.num_kv_heads, pr.head_dim)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t is not None and (t.dtype not in kv_ok or t.shape != shape or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {shape} tensor of {kv_ok}")
-    if (block_table is None) == bool(pr.paged):
-        raise ValueError("a paged cache takes a block_table, a contiguous one none")
-    if block_table is not None:
-        _int32("block_table", block_table, pr.batch * pr.max_blocks_per_seq)
-    _int32("row_offsets", row_offsets, pr.batch + 1)
-    _int32("the sequences' lengths", start, pr.batch)
+class _Cache:
+    """What a problem says of its cache, and the checks of a call's cache, block table and row layout."""
+
+    def __init__(self, pr: da_problem):
+        import torch
+        from .workloads import TORCH_DTYPES
+        names = {v: k for k, v in DTYPE_CODES.items()}
+        self.dtype, self.out_dtype = TORCH_DTYPES[names[pr.qkv_dtype]], TORCH_DTYPES[names[pr.out_dtype]]
+        self.kv_dtypes = (torch.uint8, torch.float8_e4m3fn) if pr.kv_fp8 else (self.dtype,)
+        self.batch, self.hq, self.hkv, self.d = (pr.batch, pr.num_q_heads, pr.num_kv_heads,
+                                                 pr.head_dim)
+        self.paged = bool(pr.paged)
+        self.table = pr.batch * pr.max_blocks_per_seq
+        self.shape = ((pr.num_physical_blocks, pr.page_size, self.hkv, self.d) if self.paged else
+                      (pr.batch, pr.max_seq_len, self.hkv, self.d))
+
+    def check(self, k_cache, v_cache, block_table, row_offsets, start):
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if t is not None and (t.dtype not in self.kv_dtypes or t.shape != self.shape or
+                                  not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {self.shape} tensor of "
+                                 f"{self.kv_dtypes}")
+        if (block_table is None) == self.paged:
+            raise ValueError("a paged cache takes a block_table, a contiguous one none")
+        if block_table is not None:
+            _int32("block_table", block_table, self.table)
+        _int32("row_offsets", row_offsets, self.batch + 1)
+        _int32("the sequences' lengths", start, self.batch)
 
 
 class KVCacheIO:
@@ -682,15 +704,12 @@ class KVCacheIO:
     without a place in the cache, which check_status() reports."""
 
     def __init__(self, problem: da_problem, findings: bool = False, device=None):
-        import torch
         self.problem = problem
         self.plan, self.workspace_bytes = decode_attn_plan(problem, 0)
-        from .workloads import TORCH_DTYPES
-        names = {v: k for k, v in DTYPE_CODES.items()}
-        self._dtype = TORCH_DTYPES[names[problem.qkv_dtype]]
-        self._kv_ok = (torch.uint8, torch.float8_e4m3fn) if problem.kv_fp8 else (self._dtype,)
+        self._cache = _Cache(problem)
         self.workspace = None
         if findings or problem.validate:
+            import torch
             device = torch.device(device) if device is not None else torch.device("cuda")
             self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=device)
 
@@ -700,10 +719,6 @@ class KVCacheIO:
             decode_attn_destroy(plan)
             self.plan = None
 
-    def _workspace(self):
-        return (None, 0) if self.workspace is None else (self.workspace.data_ptr(),
-                                                         self.workspace_bytes)
-
     def write(self, k, v, k_cache, v_cache, block_table, row_offsets, start, rope=None,
               positions=None, q=None, q_out=None, amax=None, stream=None):
         """Write the rows of k and v ([rows, H_kv, d], strided rows and heads allowed); with `rope`
@@ -711,22 +726,25 @@ class KVCacheIO:
         positions other than the cache positions. `amax`: a float32 [2] tensor that takes the
         running largest |k| and |v|. Returns q_out (None without q)."""
         import torch
-        pr = self.problem
-        _cache_args(pr, self._kv_ok, k_cache, v_cache, block_table, row_offsets, start)
+        c = self._cache
+        c.check(k_cache, v_cache, block_table, row_offsets, start)
         if k_cache is None or v_cache is None:
             raise ValueError("k_cache and v_cache must both be given")
         rows = k.shape[0]
-        _rows_tensor("k", k, self._dtype, pr.num_kv_heads, pr.head_dim)
-        _rows_tensor("v", v, self._dtype, pr.num_kv_heads, pr.head_dim)
+        k_row, k_head = _rows_tensor("k", k, c.dtype, c.hkv, c.d)
+        v_row, v_head = _rows_tensor("v", v, c.dtype, c.hkv, c.d)
+        q_row = q_head = out_row = out_head = 0
         if q is not None:
-            _rows_tensor("q", q, self._dtype, pr.num_q_heads, pr.head_dim)
+            q_row, q_head = _rows_tensor("q", q, c.dtype, c.hq, c.d)
             if q_out is None:
                 q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            _rows_tensor("q_out", q_out, self._dtype, pr.num_q_heads, pr.head_dim)
+            out_row, out_head = _rows_tensor("q_out", q_out, c.dtype, c.hq, c.d)
+            if q.shape[0] != rows or q_out.shape[0] != rows:
+                raise ValueError("q and q_out must have as many rows as k")
         elif q_out is not None:
             raise ValueError("q_out without q")
-        if any(t is not None and t.shape[0] != rows for t in (v, q, q_out)):
-            raise ValueError("k, v, q and q_out must have as many rows")
+        if v.shape[0] != rows:
+            raise ValueError("v must have as many rows as k")
         if positions is not None:
             _int32("positions", positions, rows)
         if rope is None and (q is not None or positions is not None):
@@ -734,58 +752,57 @@ class KVCacheIO:
         if amax is not None and (amax.dtype != torch.float32 or amax.numel() != 2 or
                                  not amax.is_contiguous()):
             raise ValueError("amax must be a contiguous float32 tensor of 2 elements")
-        device = _device_of(k=k, v=v, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                            row_offsets=row_offsets, start=start, positions=positions, q=q,
-                            q_out=q_out, amax=amax, workspace=self.workspace)
+        index = _device_index("k v k_cache v_cache block_table row_offsets start positions q q_out amax "
+                              "workspace", k, v, k_cache, v_cache, block_table, row_offsets, start,
+                              positions, q, q_out, amax, self.workspace)
         if rows == 0:
             return q_out
-        s, switch = _stream_of(device, stream)
-        ks, vs = k.stride(), v.stride()
-        qs, qos = (q.stride(), q_out.stride()) if q is not None else ((0, 0), (0, 0))
-        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        args = da_kv_write_args(k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], rows,
-                                k_cache.data_ptr(), v_cache.data_ptr(), ptr(block_table),
+        args = da_kv_write_args(k.data_ptr(), v.data_ptr(), k_row, k_head, v_row, v_head, rows,
+                                k_cache.data_ptr(), v_cache.data_ptr(), _address(block_table),
                                 row_offsets.data_ptr(), start.data_ptr(),
-                                None if rope is None else rope.handle, ptr(positions), ptr(q),
-                                ptr(q_out), qs[0], qs[1], qos[0], qos[1], ptr(amax),
-                                *self._workspace(), s)
-        _call(device, switch, decode_attn_kv_write, self.plan, args)
+                                None if rope is None else rope.handle, _address(positions),
+                                _address(q), _address(q_out), q_row, q_head, out_row, out_head,
+                                _address(amax), _address(self.workspace), self.workspace_bytes)
+        _launch(decode_attn_kv_write, self.plan, args, index, stream)
         return q_out
 
     def read(self, k_cache, v_cache, block_table, row_offsets, start, k_out, v_out, stream=None):
         """Fill k_out and v_out (contiguous [rows, H_kv, d]; either may be None, its cache too) with
         the rows' K and V. Returns (k_out, v_out)."""
-        pr = self.problem
-        _cache_args(pr, self._kv_ok, k_cache, v_cache, block_table, row_offsets, start)
+        c = self._cache
+        c.check(k_cache, v_cache, block_table, row_offsets, start)
         outs = [t for t in (k_out, v_out) if t is not None]
         if not outs or (k_out is None) != (k_cache is None) or \
                 (v_out is None) != (v_cache is None) or outs[0].shape != outs[-1].shape:
             raise ValueError("give k_out with k_cache, v_out with v_cache, or all four")
         for t in outs:
-            _rows_tensor("k_out / v_out", t, self._dtype, pr.num_kv_heads, pr.head_dim)
+            _rows_tensor("k_out / v_out", t, c.dtype, c.hkv, c.d)
             if not t.is_contiguous():
                 raise ValueError("k_out and v_out must be contiguous")
-        device = _device_of(k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                            row_offsets=row_offsets, start=start, k_out=k_out, v_out=v_out,
-                            workspace=self.workspace)
+        index = _device_index("k_cache v_cache block_table row_offsets start k_out v_out workspace",
+                              k_cache, v_cache, block_table, row_offsets, start, k_out, v_out,
+                              self.workspace)
         rows = outs[0].shape[0]
         if rows == 0:
             return k_out, v_out
-        s, switch = _stream_of(device, stream)
-        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        args = da_kv_read_args(ptr(k_cache), ptr(v_cache), ptr(block_table),
-                               row_offsets.data_ptr(), start.data_ptr(), rows, ptr(k_out),
-                               ptr(v_out), *self._workspace(), s)
-        _call(device, switch, decode_attn_kv_read, self.plan, args)
+        args = da_kv_read_args(_address(k_cache), _address(v_cache), _address(block_table),
+                               row_offsets.data_ptr(), start.data_ptr(), rows, _address(k_out),
+                               _address(v_out), _address(self.workspace), self.workspace_bytes)
+        _launch(decode_attn_kv_read, self.plan, args, index, stream)
         return k_out, v_out
 
     def check_status(self, stream=None):
         """Synchronise, then raise the first finding recorded since the last call."""
         if self.workspace is None:
             raise ValueError("made without findings")
-        s, switch = _stream_of(self.workspace.device, stream)
-        _call(self.workspace.device, switch, decode_attn_check_status, self.plan,
-              self.workspace.data_ptr(), s)
+        _check_workspace(decode_attn_check_status, self.plan, self.workspace, stream)
+
+
+def _check_workspace(fn, plan, workspace, stream):
+    import torch
+    with torch.cuda.device(workspace.device):
+        s = stream if stream is not None else torch.cuda.current_stream()
+        fn(plan, workspace.data_ptr(), s.cuda_stream)
 
 
 class TreeAttention:
@@ -798,14 +815,11 @@ class TreeAttention:
         self.problem = problem
         self.plan, self.workspace_bytes = decode_attn_tree_plan(problem, max_tree)
         self.info = decode_attn_tree_plan_info(self.plan)
-        from .workloads import TORCH_DTYPES
-        names = {v: k for k, v in DTYPE_CODES.items()}
-        self._dtype = TORCH_DTYPES[names[problem.qkv_dtype]]
-        self._out_dtype = TORCH_DTYPES[names[problem.out_dtype]]
-        self._kv_ok = (torch.uint8, torch.float8_e4m3fn) if problem.kv_fp8 else (self._dtype,)
+        self._cache = _Cache(problem)
         self.device = torch.device(device) if device is not None else torch.device("cuda")
         # a zero-filled workspace needs no decode_attn_tree_workspace_init call
         self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+        self._address = self.workspace.data_ptr()
 
     def __del__(self):
         plan = getattr(self, "plan", None)
@@ -820,44 +834,38 @@ class TreeAttention:
         bit j of a row's word set iff it attends to its sequence's drafted token j; None: a chain.
         Returns (out, lse)."""
         import torch
-        pr = self.problem
-        H, d = pr.num_q_heads, pr.head_dim
-        _cache_args(pr, self._kv_ok, k_cache, v_cache, block_table, row_offsets, ctx_lens)
+        c = self._cache
+        c.check(k_cache, v_cache, block_table, row_offsets, ctx_lens)
         if k_cache is None or v_cache is None:
             raise ValueError("k_cache and v_cache must both be given")
-        _rows_tensor("q", q, self._dtype, H, d)
+        _rows_tensor("q", q, c.dtype, c.hq, c.d)
         rows = q.shape[0]
         if out is None:
-            out = torch.empty((rows, H, d), dtype=self._out_dtype, device=q.device)
+            out = torch.empty(q.shape, dtype=c.out_dtype, device=q.device)
         if out_lse is None:
-            out_lse = torch.empty((rows, H), dtype=torch.float32, device=q.device)
-        _rows_tensor("out", out, self._out_dtype, H, d)
+            out_lse = torch.empty((rows, c.hq), dtype=torch.float32, device=q.device)
+        _rows_tensor("out", out, c.out_dtype, c.hq, c.d)
         if not q.is_contiguous() or not out.is_contiguous() or out.shape[0] != rows:
             raise ValueError("q and out must be contiguous, with as many rows")
-        if out_lse.dtype != torch.float32 or out_lse.shape != (rows, H) or \
+        if out_lse.dtype != torch.float32 or out_lse.shape != (rows, c.hq) or \
                 not out_lse.is_contiguous():
             raise ValueError("out_lse must be a contiguous float32 [rows, H_q] tensor")
         if tree_mask is not None and (tree_mask.dtype not in (torch.int64, torch.uint64) or
                                       tree_mask.shape != (rows,) or
                                       not tree_mask.is_contiguous()):
             raise ValueError("tree_mask must be a contiguous int64 [rows] tensor")
-        device = _device_of(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                            row_offsets=row_offsets, ctx_lens=ctx_lens, tree_mask=tree_mask,
-                            out=out, out_lse=out_lse, workspace=self.workspace)
+        index = _device_index("q k_cache v_cache block_table row_offsets ctx_lens tree_mask out out_lse "
+                              "workspace", q, k_cache, v_cache, block_table, row_offsets, ctx_lens,
+                              tree_mask, out, out_lse, self.workspace)
         if rows == 0:
             return out, out_lse
-        s, switch = _stream_of(device, stream)
         args = da_tree_args(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                            None if block_table is None else block_table.data_ptr(),
-                            row_offsets.data_ptr(), ctx_lens.data_ptr(),
-                            None if tree_mask is None else tree_mask.data_ptr(), rows, scale,
-                            out.data_ptr(), out_lse.data_ptr(), self.workspace.data_ptr(),
-                            self.workspace_bytes, s)
-        _call(device, switch, decode_attn_tree_run, self.plan, args)
+                            _address(block_table), row_offsets.data_ptr(), ctx_lens.data_ptr(),
+                            _address(tree_mask), rows, scale, out.data_ptr(), out_lse.data_ptr(),
+                            self._address, self.workspace_bytes)
+        _launch(decode_attn_tree_run, self.plan, args, index, stream)
         return out, out_lse
 
     def check_status(self, stream=None):
         """Synchronise, then raise the first finding recorded since the last call."""
-        s, switch = _stream_of(self.workspace.device, stream)
-        _call(self.workspace.device, switch, decode_attn_tree_check_status, self.plan,
-              self.workspace.data_ptr(), s)
+        _check_workspace(decode_attn_tree_check_status, self.plan, self.workspace, stream)

@@ -20,7 +20,8 @@ struct da_tree_plan {
   da_plan cache;                // the problem's cache layout (decode_attn_plan's fields)
   int max_tree, num_sms;
   int tile_rows, tile_tokens, max_row_tiles;
-  int grid, stages;
+  int grid, stages, narrow;
+  unsigned char heads[kTreeMaxRowTiles + 1];
   size_t smem_bytes;
   size_t off_status, off_head, off_info, off_part_l, off_part_o, ws_bytes;
 };
@@ -254,15 +255,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(
   if (next == 0 || next >= P) return;
   const int4 g = p.info[2 * next], s = p.info[2 * next + 1];
   if (g.y == 0) return;                        // its first group starts there: no crossing
-  const int at = tree_share_begin(next, W, P);
+  const int at = tree_share_begin(next, W, P, p.narrow);
   const int gs = at - g.y, ge = gs + g.z;      // the group's units
-  const int o1 = tree_owner(gs, W, P), o2 = tree_owner(ge - 1, W, P);
+  const int o1 = tree_owner(gs, W, P, p.narrow), o2 = tree_owner(ge - 1, W, P, p.narrow);
   if (o1 != next - 1) return;                  // another block's
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rr = blockIdx.y * kMergeWarps + warp, r = sub % R * p.tile_rows + rr;
   if (r >= s.y * p.group) return;
   // partial j of the group: owner o1 + j's first piece, or o1's last
-  const bool whole_first = gs == tree_share_begin(o1, W, P);
+  const bool whole_first = gs == tree_share_begin(o1, W, P, p.narrow);
   const int n = o2 - o1 + 1;
   const float* const part_o = p.part_o + (long long)rr * D + lane * (D / 32);
   auto slot = [&](int j) {
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int i = r / p.group, h = (g.x * head.w + sub / R) * p.group + r % p.group;
+  const int i = r / p.group, h = (g.x + sub / R) * p.group + r % p.group;
   const long long row = (long long)(s.x + i) * p.c.hq + h;
 #pragma unroll
   for (int c = 0; c < C; ++c)
@@ -450,6 +451,9 @@ int decode_attn_tree_plan(const da_problem* problem, int max_tree, da_tree_plan*
   pl->grid = (int)std::min<long long>(
       std::max(mma ? pl->num_sms : 2 * pl->num_sms, pl->max_row_tiles),
       units * pl->max_row_tiles);
+  pl->narrow = (units + 1) * pl->grid < (1ll << 31) ? 1 : 0;
+  for (int r = 1; r <= pl->max_row_tiles; ++r)
+    pl->heads[r] = (unsigned char)tree_heads(pl->grid, r, p.num_kv_heads);
   const size_t slots = 2ull * pl->grid;   // two an owner and row tile; owners x row tiles <= grid
   size_t off = 0;
   pl->off_status = off;
@@ -540,6 +544,8 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
   p.tile_rows = pl.tile_rows;
   p.tile_tokens = pl.tile_tokens;
   p.max_row_tiles = pl.max_row_tiles;
+  p.narrow = pl.narrow;
+  std::memcpy(p.heads, pl.heads, sizeof p.heads);
   p.qscale = (float)((double)a.scale * 1.4426950408889634 * (pr.kv_fp8 ? (double)pr.k_scale : 1.0));
   p.v_scale = pr.kv_fp8 ? pr.v_scale : 1.f;
   cudaStream_t stream = static_cast<cudaStream_t>(a.cuda_stream);

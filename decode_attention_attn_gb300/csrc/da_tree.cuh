@@ -19,6 +19,8 @@
 
 namespace da {
 
+constexpr int kTreeMaxRowTiles = 16;   // 64 drafted tokens x 8 heads in tiles of 32 rows
+
 struct TreeParams {
   Params c;                     // cache layout, block table, status (seq_lens unused)
   const void* q;                // [rows, hq, d]
@@ -28,13 +30,15 @@ struct TreeParams {
   void* out;
   float* out_lse;
   int4* head;                   // workspace: units W, owners P, row tiles R, heads
-  int4* info;                   // [owners][2]: {block of heads, first unit's offset in its group, the
+  int4* info;                   // [owners][2]: {first head of its block, first unit's offset in its group, the
                                 // group's tiles, 0}, {first row, drafted tokens, 0, 0} of its first piece
   float* part_o;                // [owners][2][heads][R][tile rows][d]: 2 slots a CTA
   float* part_l;                // [owners][2][heads][R][tile rows]
   int rows, max_tree, group;
   int tile_rows, tile_tokens;
   int max_row_tiles;            // R's bound, from max_tree
+  int narrow;                   // owners x units fits 32 bits: short divisions
+  unsigned char heads[kTreeMaxRowTiles + 1];   // heads side by side, by R (tree_heads)
   float qscale, v_scale;
 };
 
@@ -91,26 +95,31 @@ struct TreeShare {
   int base;            // first unit of sequence b0
   int b0;              // the sequence that u0 lies in
   int row_tile, row_tiles, head, heads, owner, owners;
+  int blocks;          // blocks of heads
+  TreeRaw raw, ahead;  // sequences b0 and b0 + 1
 };
 
 struct TreeScratch {   // shared memory of tree_schedule
   int warp_sum[32];
   int warp_max[32];
   int base, b0;
+  TreeRaw raw, ahead;
 };
 
-__device__ __forceinline__ int tree_share_begin(int o, int W, int P) {
-  return (int)((long long)o * W / P);
+__device__ __forceinline__ int tree_share_begin(int o, int W, int P, int narrow) {
+  return narrow ? (int)((unsigned)o * (unsigned)W / (unsigned)P) : (int)((long long)o * W / P);
 }
 // The owner of unit u: the o with o W / P <= u < (o + 1) W / P (floor divisions).
-__device__ __forceinline__ int tree_owner(int u, int W, int P) {
-  return (int)((((long long)u + 1) * P - 1) / W);
+__device__ __forceinline__ int tree_owner(int u, int W, int P, int narrow) {
+  return narrow ? (int)((((unsigned)u + 1u) * (unsigned)P - 1u) / (unsigned)W)
+                : (int)((((long long)u + 1) * P - 1) / W);
 }
 
 // Heads that an owner takes side by side: as many as leave at most 5 % of the CTAs without an owner.
-__device__ __forceinline__ int tree_heads(int ctas, int row_tiles, int hkv) {
+inline int tree_heads(int ctas, int row_tiles, int hkv) {
   for (int h = hkv; h > 1; --h)
-    if (hkv % h == 0 && ctas / (row_tiles * h) * (row_tiles * h) * 20 >= ctas * 19) return h;
+    if (h < 256 && hkv % h == 0 && ctas / (row_tiles * h) * (row_tiles * h) * 20 >= ctas * 19)
+      return h;
   return 1;
 }
 
@@ -151,27 +160,32 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
   }
   TreeShare sh;
   sh.row_tiles = min(most, p.max_row_tiles);
-  sh.heads = tree_heads(gridDim.x, sh.row_tiles, p.c.hkv);
-  const int blocks = p.c.hkv / sh.heads, lanes = sh.row_tiles * sh.heads;
+  sh.heads = p.heads[sh.row_tiles];
+  const unsigned lanes = sh.row_tiles * sh.heads;
+  const int blocks = (unsigned)p.c.hkv / (unsigned)sh.heads;
   const int pre = before + inc - sum, units = total * blocks;
-  sh.owners = max(1, min((int)gridDim.x / lanes, units));
+  sh.blocks = blocks;
+  sh.owners = max(1, min((int)(gridDim.x / lanes), units));
   sh.owner = blockIdx.x / lanes;
-  sh.row_tile = blockIdx.x % sh.row_tiles;
-  sh.head = blockIdx.x % lanes / sh.row_tiles;
+  sh.head = (blockIdx.x - sh.owner * lanes) / (unsigned)sh.row_tiles;
+  sh.row_tile = blockIdx.x - sh.owner * lanes - sh.head * sh.row_tiles;
   if (units == 0 || sh.owner >= sh.owners) {
     sh.u0 = sh.u1 = 0;
     sh.b0 = 0;
     sh.base = 0;
   } else {
-    sh.u0 = tree_share_begin(sh.owner, units, sh.owners);
-    sh.u1 = tree_share_begin(sh.owner + 1, units, sh.owners);
+    sh.u0 = tree_share_begin(sh.owner, units, sh.owners, p.narrow);
+    sh.u1 = tree_share_begin(sh.owner + 1, units, sh.owners, p.narrow);
     if (pre * blocks <= sh.u0 && sh.u0 < (pre + sum) * blocks) {   // exactly one thread
       int at = pre;
       for (int b = first; b < last; ++b) {
-        const int t = tree_seq(p, b).tiles;
+        const TreeRaw raw = tree_raw(p, b);
+        const int t = tree_seq(p, raw).tiles;
         if (sh.u0 < (at + t) * blocks) {
           sc.b0 = b;
           sc.base = at * blocks;
+          sc.raw = raw;
+          sc.ahead = tree_raw(p, min(b + 1, p.c.batch - 1));
           break;
         }
         at += t;
@@ -182,6 +196,8 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
   if (sh.u1 > sh.u0) {
     sh.b0 = sc.b0;
     sh.base = sc.base;
+    sh.raw = sc.raw;
+    sh.ahead = sc.ahead;
   }
   if (tid == 0 && blockIdx.x == 0) *p.head = make_int4(units, sh.owners, sh.row_tiles, sh.heads);
   return sh;
@@ -202,12 +218,14 @@ struct TreeWalk {
 
   __device__ __forceinline__ TreeWalk(const TreeParams& p, const TreeShare& sh)
       : u(sh.u0), base(sh.base), b(sh.b0) {
-    if (sh.u1 > sh.u0) s = tree_seq(p, b);
-    ahead = tree_raw(p, min(b + 1, p.c.batch - 1));
+    if (sh.u1 > sh.u0) {
+      s = tree_seq(p, sh.raw);
+      ahead = sh.ahead;
+    }
   }
   __device__ __forceinline__ bool next(const TreeParams& p, const TreeShare& sh) {
     if (u >= sh.u1) return false;
-    const int blocks = p.c.hkv / sh.heads;
+    const int blocks = sh.blocks;
     while (u >= base + s.tiles * blocks) {
       if (b + 1 >= p.c.batch) return false;   // (lengths that changed under way)
       base += s.tiles * blocks;
@@ -216,7 +234,7 @@ struct TreeWalk {
       ahead = tree_raw(p, min(b + 1, p.c.batch - 1));
     }
     const int off = u - base;
-    const int block = off / s.tiles;
+    const int block = (unsigned)off / (unsigned)s.tiles;
     kvh = block * sh.heads + sh.head;
     t0 = off - block * s.tiles;
     t1 = min(s.tiles, t0 + (sh.u1 - u));
@@ -231,7 +249,7 @@ struct TreeWalk {
 // trip to memory.
 __device__ __forceinline__ void tree_record(const TreeParams& p, const TreeShare& sh,
                                             const TreeWalk& w) {
-  p.info[2 * sh.owner] = make_int4(w.kvh / sh.heads, w.t0, w.s.tiles, 0);
+  p.info[2 * sh.owner] = make_int4(w.kvh - sh.head, w.t0, w.s.tiles, 0);
   p.info[2 * sh.owner + 1] = make_int4(w.s.row0, w.s.T, 0, 0);
 }
 

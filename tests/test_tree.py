@@ -83,7 +83,7 @@ def reference(lay, q, kc, vc, words, scale):
 def run(lay, q, kc, vc, words, scale, max_tree=None, fill=5.0, obj=None):
     t = obj or binding.TreeAttention(lay.problem, max_tree or max(max(lay.new), 1))
     out = torch.full((lay.rows, lay.hq, lay.d), fill, device="cuda",
-                     dtype=t._out_dtype)
+                     dtype=t._cache.out_dtype)
     lse = torch.full((lay.rows, lay.hq), fill, device="cuda")
     t.run(q.cuda(), kc.cuda(), vc.cuda(), lay.table.cuda() if lay.page else None, lay.row_offsets.cuda(),
           lay.start.cuda(), None if words is None else words.cuda(), scale, out=out, out_lse=lse)

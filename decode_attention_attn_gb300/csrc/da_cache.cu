@@ -41,11 +41,26 @@ struct RowParams {
   float* amax;
   int rows, hq, hkv;
   int units, head_lanes;        // a head is `units` lanes wide; head_lanes heads a block pass
+  int wide_in, wide_out;        // rows read (written) lie on 32-byte boundaries
   int rotary, interleaved, transpose;
   float m;                      // attn_factor
   float k_inv, v_inv;           // 1 / scale of an FP8 cache
   unsigned long long turn[kMaxPairs];
 };
+
+// 32 bytes a lane (aligned to 32): neighbouring lanes then fill whole sectors in one instruction,
+// where two 16-byte accesses 32 bytes apart touch each sector twice.
+__device__ __forceinline__ void load32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
+                 "=r"(b.w)
+               : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
 
 // The sequence whose rows hold row r: the last b with offsets[b] <= r, or -1 where r lies
 // before the first row or behind the last one.
@@ -118,120 +133,147 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float a, float b) {
   return u;
 }
 
-// VEC floats stored as VEC elements of C at dst[at].
+// VEC floats as VEC stored elements of C: 16 bytes (8 for E4M3), or one element.
 template <typename C, int VEC>
-__device__ __forceinline__ void store_vec(C* dst, long long at, const float* f) {
-  if constexpr (std::is_same<C, fp8e4m3>::value) {
-    uint8_t* d8 = reinterpret_cast<uint8_t*>(dst) + at;
-    if constexpr (VEC == 1) {
-      *d8 = (uint8_t)pack_e4m3x2(f[0], 0.f);
-    } else {
-      static_assert(VEC == 8, "FP8 caches have 16-bit rows");
-      uint2 w;
-      w.x = pack_e4m3x2(f[0], f[1]) | pack_e4m3x2(f[2], f[3]) << 16;
-      w.y = pack_e4m3x2(f[4], f[5]) | pack_e4m3x2(f[6], f[7]) << 16;
-      *reinterpret_cast<uint2*>(d8) = w;
-    }
-  } else if constexpr (std::is_same<C, float>::value) {
-    if constexpr (VEC == 1) dst[at] = f[0];
-    else *reinterpret_cast<float4*>(dst + at) = make_float4(f[0], f[1], f[2], f[3]);
-  } else if constexpr (VEC == 1) {
-    if constexpr (std::is_same<C, __half>::value) dst[at] = __float2half_rn(f[0]);
-    else dst[at] = __float2bfloat16_rn(f[0]);
-  } else {
-    uint4 w;
-    w.x = pack2(f[0], f[1], C());
-    w.y = pack2(f[2], f[3], C());
-    w.z = pack2(f[4], f[5], C());
-    w.w = pack2(f[6], f[7], C());
-    *reinterpret_cast<uint4*>(dst + at) = w;
+struct Packed;
+template <typename C>
+struct Packed<C, 8> {
+  using type = uint4;
+  __device__ __forceinline__ static uint4 pack(const float* f) {
+    return make_uint4(pack2(f[0], f[1], C()), pack2(f[2], f[3], C()), pack2(f[4], f[5], C()),
+                      pack2(f[6], f[7], C()));
   }
+};
+template <>
+struct Packed<float, 4> {
+  using type = uint4;
+  __device__ __forceinline__ static uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+};
+template <>
+struct Packed<fp8e4m3, 8> {
+  using type = uint2;
+  __device__ __forceinline__ static uint2 pack(const float* f) {
+    return make_uint2(pack_e4m3x2(f[0], f[1]) | pack_e4m3x2(f[2], f[3]) << 16,
+                      pack_e4m3x2(f[4], f[5]) | pack_e4m3x2(f[6], f[7]) << 16);
+  }
+};
+template <typename C>
+struct Packed<C, 1> {
+  using type = C;
+  __device__ __forceinline__ static C pack(const float* f) {
+    if constexpr (std::is_same<C, float>::value) return f[0];
+    else if constexpr (std::is_same<C, __half>::value) return __float2half_rn(f[0]);
+    else if constexpr (std::is_same<C, __nv_bfloat16>::value) return __float2bfloat16_rn(f[0]);
+    else return C{(uint8_t)pack_e4m3x2(f[0], 0.f)};
+  }
+};
+
+// A unit's two vectors to dst + a0 and dst + b0 (elements of C); `joined`: they are neighbours, and (16-byte
+// vectors) the row is aligned for one 32-byte access.
+template <typename C, typename V>
+__device__ __forceinline__ void store_unit(C* dst, int a0, int b0, bool joined, const V& a, const V& b) {
+  if constexpr (sizeof(V) == 16) {
+    if (joined) {
+      store32(dst + a0, a, b);
+      return;
+    }
+  } else if constexpr (sizeof(V) == 8) {
+    if (joined) {
+      *reinterpret_cast<uint4*>(dst + a0) = make_uint4(a.x, a.y, b.x, b.y);
+      return;
+    }
+  }
+  *reinterpret_cast<V*>(dst + a0) = a;
+  *reinterpret_cast<V*>(dst + b0) = b;
 }
 
 // One block per row (and slice of its heads). A head of d elements is d / (2 VEC) units; a unit is
 // two vectors of VEC elements, so VEC rotated pairs: with half pairs the vectors at u VEC and
 // u VEC + rotary / 2, else 2 VEC neighbours (also where nothing is rotated). A thread keeps one
-// unit position u, whose cosines and sines it holds in registers, and walks over heads.
+// unit position u and walks over heads.
 //
 // The angle of position t is t * turn mod 1 in 64-bit fixed point: exact for any 32-bit t, with
 // no 64-bit float arithmetic (an fp32 angle at t = 10^6 would be off by 0.06). Its top 32 bits,
 // as a signed half-turn count, go through sincospif.
 //
-// The first heads' vectors are loaded before the row's place in the cache is looked up, so that the
+// The first two heads' vectors are loaded before the row's place in the cache is looked up, so that the
 // lookup chain (offsets, start, table) and the loads run side by side.
 template <typename T, typename C, int VEC>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowParams p) {
-  __shared__ float s_cos[kMaxPairs], s_sin[kMaxPairs];
+__global__ void __launch_bounds__(kRowThreads, 7)
+    rows_kernel(const __grid_constant__ RowParams p) {
+  __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
   __shared__ int s_info[3];   // member, position, cache row
   using V = RowVec<T, VEC>;
   using Raw = typename V::Raw;
+  using PT = Packed<T, VEC>;
+  using PC = Packed<C, VEC>;
   const int row = blockIdx.x, tid = threadIdx.x;
   const int u = tid % p.units, lane_head = tid / p.units;
   const int heads = p.hq + 2 * p.hkv;
   const int step = p.head_lanes * gridDim.y;
   const int d = p.units * 2 * VEC;
   const bool turned = u * 2 * VEC < p.rotary;
-  const int a0 = turned && !p.interleaved ? u * VEC : u * 2 * VEC;
-  const int b0 = turned && !p.interleaved ? a0 + p.rotary / 2 : a0 + VEC;
+  const bool apart = turned && !p.interleaved;   // the two vectors lie rotary / 2 apart
+  const int a0 = apart ? u * VEC : u * 2 * VEC;
+  const int b0 = apart ? a0 + p.rotary / 2 : a0 + VEC;
   int h = lane_head < p.head_lanes ? lane_head + p.head_lanes * blockIdx.y : heads;
 
-  auto source = [&](int hh) -> const T* {
-    if (hh < p.hq) return static_cast<const T*>(p.q) + row * p.q_rs + hh * p.q_hs;
-    hh -= p.hq;
-    if (hh < p.hkv) return static_cast<const T*>(p.k) + row * p.k_rs + hh * p.k_hs;
-    return static_cast<const T*>(p.v) + row * p.v_rs + (hh - p.hkv) * p.v_hs;
+  auto load = [&](int hh, Raw& a, Raw& b) {
+    const T* x;
+    if (hh < p.hq) x = static_cast<const T*>(p.q) + row * p.q_rs + hh * p.q_hs;
+    else if (hh < p.hq + p.hkv) x = static_cast<const T*>(p.k) + row * p.k_rs + (hh - p.hq) * p.k_hs;
+    else x = static_cast<const T*>(p.v) + row * p.v_rs + (hh - p.hq - p.hkv) * p.v_hs;
+    if constexpr (VEC > 1) {
+      if (!apart && p.wide_in) {
+        load32(x + a0, a, b);
+        return;
+      }
+    }
+    a = *reinterpret_cast<const Raw*>(x + a0);
+    b = *reinterpret_cast<const Raw*>(x + b0);
   };
-  Raw ra{}, rb{};
-  if (h < heads) {
-    const T* x = source(h);
-    ra = *reinterpret_cast<const Raw*>(x + a0);
-    rb = *reinterpret_cast<const Raw*>(x + b0);
-  }
+  // two heads ahead of the one in hand
+  Raw ra[2]{}, rb[2]{};
+  if (h < heads) load(h, ra[0], rb[0]);
+  if (h + step < heads) load(h + step, ra[1], rb[1]);
 
-  if (tid == 0) {
-    int pos = 0, z = -1;
-    bool member = true;
-    if (p.row_offsets) member = locate_row(p.cache, p.row_offsets, p.start, row, pos, z);
-    if (member && p.positions) pos = __ldg(p.positions + row);
-    s_info[0] = member;
-    s_info[1] = pos;
-    s_info[2] = z;
+  long long z = -1;
+  int pos = 0;
+  if (p.row_offsets) {
+    if (tid == 0) {
+      int at = 0, zz = -1;
+      const bool member = locate_row(p.cache, p.row_offsets, p.start, row, at, zz);
+      if (member && p.positions) at = __ldg(p.positions + row);
+      s_info[0] = member;
+      s_info[1] = at;
+      s_info[2] = zz;
+    }
+    __syncthreads();
+    if (!s_info[0]) return;
+    pos = s_info[1];
+    z = s_info[2];
+  } else {
+    pos = __ldg(p.positions + row);
   }
-  __syncthreads();
-  if (!s_info[0]) return;
-  const long long z = s_info[2];
-  float cs[VEC], sn[VEC];
   if (p.rotary) {
-    const long long pos = s_info[1];
     for (int i = tid; i < p.rotary / 2; i += kRowThreads) {
-      const unsigned long long a = (unsigned long long)pos * p.turn[i];
+      const unsigned long long a = (unsigned long long)(long long)pos * p.turn[i];
       float s, c;
       sincospif((float)(int)(unsigned)(a >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
       s_cos[i] = c * p.m;
       s_sin[i] = (p.transpose ? -s : s) * p.m;
     }
     __syncthreads();
-    if (turned) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        cs[i] = s_cos[u * VEC + i];
-        sn[i] = s_sin[u * VEC + i];
-      }
-    }
   }
 
   float most_k = 0.f, most_v = 0.f;
-  while (h < heads) {
-    const int cur = h;
-    const Raw xa = ra, xb = rb;
-    h += step;
-    if (h < heads) {
-      const T* x = source(h);
-      ra = *reinterpret_cast<const Raw*>(x + a0);
-      rb = *reinterpret_cast<const Raw*>(x + b0);
-    }
+  const bool out_joined = VEC > 1 && !apart && p.wide_out;
+  auto put = [&](int cur, const Raw& xa, const Raw& xb) {
     const bool is_q = cur < p.hq, is_k = !is_q && cur < p.hq + p.hkv;
-    if (!is_q && z < 0) continue;   // no place in the cache
+    if (!is_q && z < 0) return;   // no place in the cache
     const bool rot = turned && (is_q || is_k);
     const int kvh = is_k ? cur - p.hq : cur - p.hq - p.hkv;
     const long long at = is_q ? row * p.qo_rs + cur * p.qo_hs
@@ -239,32 +281,31 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     // elements that pass unchanged move as they are
     if (!rot && !p.amax && (is_q || std::is_same<T, C>::value)) {
       T* dst = static_cast<T*>(is_q ? p.q_out : is_k ? p.k_cache : p.v_cache) + at;
-      *reinterpret_cast<Raw*>(dst + a0) = xa;
-      *reinterpret_cast<Raw*>(dst + b0) = xb;
-      continue;
+      store_unit(dst, a0, b0, out_joined, xa, xb);
+      return;
     }
     float e[2 * VEC];
     V::to_f32(xa, e);
     V::to_f32(xb, e + VEC);
     if (rot) {
+      const float* cs = s_cos + u * VEC;   // (kept in shared memory: registers bound the blocks an SM)
+      const float* sn = s_sin + u * VEC;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         if (p.interleaved) {
           const float a = e[2 * i], b = e[2 * i + 1];
-          e[2 * i] = a * cs[i] - b * sn[i];
-          e[2 * i + 1] = b * cs[i] + a * sn[i];
+          e[2 * i] = __fmaf_rn(a, cs[i], -__fmul_rn(b, sn[i]));   // the same in every instantiation
+          e[2 * i + 1] = __fmaf_rn(b, cs[i], __fmul_rn(a, sn[i]));
         } else {
           const float a = e[i], b = e[VEC + i];
-          e[i] = a * cs[i] - b * sn[i];
-          e[VEC + i] = b * cs[i] + a * sn[i];
+          e[i] = __fmaf_rn(a, cs[i], -__fmul_rn(b, sn[i]));
+          e[VEC + i] = __fmaf_rn(b, cs[i], __fmul_rn(a, sn[i]));
         }
       }
     }
     if (is_q) {
-      T* dst = static_cast<T*>(p.q_out);
-      store_vec<T, VEC>(dst, at + a0, e);
-      store_vec<T, VEC>(dst, at + b0, e + VEC);
-      continue;
+      store_unit(static_cast<T*>(p.q_out) + at, a0, b0, out_joined, PT::pack(e), PT::pack(e + VEC));
+      return;
     }
     if (p.amax) {
       float& most = is_k ? most_k : most_v;
@@ -276,9 +317,22 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
 #pragma unroll
       for (int i = 0; i < 2 * VEC; ++i) e[i] *= inv;
     }
-    C* dst = static_cast<C*>(is_k ? p.k_cache : p.v_cache);
-    store_vec<C, VEC>(dst, at + a0, e);
-    store_vec<C, VEC>(dst, at + b0, e + VEC);
+    store_unit(static_cast<C*>(is_k ? p.k_cache : p.v_cache) + at, a0, b0,
+               std::is_same<C, fp8e4m3>::value ? VEC > 1 && !apart : out_joined, PC::pack(e),
+               PC::pack(e + VEC));
+  };
+  while (h < heads) {
+    {
+      const Raw xa = ra[0], xb = rb[0];
+      if (h + 2 * step < heads) load(h + 2 * step, ra[0], rb[0]);
+      put(h, xa, xb);
+    }
+    h += step;
+    if (h >= heads) break;
+    const Raw xa = ra[1], xb = rb[1];
+    if (h + 2 * step < heads) load(h + 2 * step, ra[1], rb[1]);
+    put(h, xa, xb);
+    h += step;
   }
   if (p.amax) {
     __syncwarp();
@@ -300,9 +354,9 @@ const void* rows_kernel_for(bool vec) {
              : reinterpret_cast<const void*>(&rows_kernel<T, C, 1>);
 }
 
-// Whether a row tensor can move 16 bytes a lane.
-bool vector_ok(const void* p, long long rs, long long hs, int es) {
-  return !p || (aligned(p, 16) && rs * es % 16 == 0 && hs * es % 16 == 0);
+// Whether a row tensor can move `bytes` (16 or 32) a lane.
+bool vector_ok(const void* p, long long rs, long long hs, int es, int bytes = 16) {
+  return !p || (aligned(p, bytes) && rs * es % bytes == 0 && hs * es % bytes == 0);
 }
 
 int launch_rows(RowParams& p, int head_dim, int es, bool vec, const void* fn,
@@ -343,6 +397,7 @@ struct ReadParams {
   int row_items;                // chunks * tensors
   unsigned row_magic, chunk_magic;   // ceil(2^32 / row_items), ceil(2^32 / chunks)
   long long items;              // rows * row_items
+  int wide;                     // the outputs lie on 32-byte boundaries
 };
 
 constexpr int kReadThreads = 256;
@@ -406,8 +461,13 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
         o[2 * j + 1] = pack2(g.x * s, g.y * s, T());
       }
       uint4* d = static_cast<uint4*>(p.dst[t[k] & 1]) + 2 * at;
-      d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      const uint4 lo4 = make_uint4(o[0], o[1], o[2], o[3]), hi4 = make_uint4(o[4], o[5], o[6], o[7]);
+      if (p.wide) {
+        store32(d, lo4, hi4);
+      } else {
+        d[0] = lo4;
+        d[1] = hi4;
+      }
     }
   }
 }
@@ -540,6 +600,8 @@ int decode_attn_rope_apply(const da_rope* rope, const da_rope_args* args) {
   const bool vec = rope->cfg.head_dim % pair == 0 && rope->cfg.rotary_dim % pair == 0 &&
                    vector_ok(a.x, a.x_row_stride, a.x_head_stride, es) &&
                    vector_ok(a.out, a.out_row_stride, a.out_head_stride, es);
+  p.wide_in = vector_ok(a.x, a.x_row_stride, a.x_head_stride, es, 32);
+  p.wide_out = vector_ok(a.out, a.out_row_stride, a.out_head_stride, es, 32);
   const void* fn = a.dtype == DA_F32   ? rows_kernel_for<float, float>(vec)
                    : a.dtype == DA_F16 ? rows_kernel_for<__half, __half>(vec)
                                        : rows_kernel_for<__nv_bfloat16, __nv_bfloat16>(vec);
@@ -601,6 +663,11 @@ int decode_attn_kv_write(const da_plan* plan, const da_kv_write_args* args) {
                    vector_ok(a.q_out, a.q_out_row_stride, a.q_out_head_stride, es) &&
                    vector_ok(a.k, a.k_row_stride, a.k_head_stride, es) &&
                    vector_ok(a.v, a.v_row_stride, a.v_head_stride, es);
+  p.wide_in = vector_ok(a.q, a.q_row_stride, a.q_head_stride, es, 32) &&
+              vector_ok(a.k, a.k_row_stride, a.k_head_stride, es, 32) &&
+              vector_ok(a.v, a.v_row_stride, a.v_head_stride, es, 32);
+  p.wide_out = vector_ok(a.q_out, a.q_out_row_stride, a.q_out_head_stride, es, 32) &&
+               aligned(a.k_cache, 32) && aligned(a.v_cache, 32);
   const void* fn = pr.kv_fp8                ? rows_kernel_for<__nv_bfloat16, fp8e4m3>(vec)
                    : pr.qkv_dtype == DA_F32 ? rows_kernel_for<float, float>(vec)
                    : pr.qkv_dtype == DA_F16 ? rows_kernel_for<__half, __half>(vec)
@@ -652,6 +719,7 @@ int decode_attn_kv_read(const da_plan* plan, const da_kv_read_args* args) {
   p.row_magic = (unsigned)(((1ull << 32) + p.row_items - 1) / p.row_items);
   p.chunk_magic = (unsigned)(((1ull << 32) + p.chunks - 1) / p.chunks);
   p.items = (long long)p.rows * p.row_items;
+  p.wide = aligned(a.k_out, 32) && aligned(a.v_out, 32);
   // items a lane: more loads in flight where there are enough items to fill the GPU's warps
   const int per = p.row_items < 8 ? 2 : p.items >= (1ll << 21) ? 8 : 4;
   const long long per_block = (long long)kReadThreads * per;

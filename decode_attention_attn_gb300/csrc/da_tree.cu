@@ -23,7 +23,7 @@ struct da_tree_plan {
   int grid, stages, narrow;
   unsigned char heads[kTreeMaxRowTiles + 1];
   size_t smem_bytes;
-  size_t off_status, off_head, off_info, off_part_l, off_part_o, ws_bytes;
+  size_t off_status, off_info, off_part_l, off_part_o, ws_bytes;
 };
 
 namespace {
@@ -62,8 +62,9 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
   pdl_launch_dependents();   // the merge's launch runs beside this kernel; it waits for its end
   TreeWalk w(p, sh);
   bool first_piece = true;
+  if (sh.u1 <= sh.u0 && tid == 0) tree_record(p, sh, false, w);
   while (w.next(p, sh)) {
-    if (first_piece && tid == 0 && sh.row_tile == 0 && sh.head == 0) tree_record(p, sh, w);
+    if (first_piece && tid == 0) tree_record(p, sh, true, w);
     first_piece = false;
     const int R = w.s.T * G, r0 = sh.row_tile * kCoreRows;
     if (r0 >= R) continue;
@@ -226,8 +227,8 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
         if (p.out_lse && tx == 0) p.out_lse[row] = L * 0.69314718055994531f;
       } else {
         const long long at =
-            tree_slot(sh.owner, w.head, sh.row_tiles * sh.heads,
-                      sh.head * sh.row_tiles + sh.row_tile) * kCoreRows + 2 * ty + a;
+            (long long)tree_slot(sh.owner, w.head, sh.row_tiles * sh.heads,
+                                 sh.head * sh.row_tiles + sh.row_tile) * kCoreRows + 2 * ty + a;
         for (int c = 0; c < NC; ++c)
           for (int e = 0; e < 4; ++e)
             p.part_o[at * D + (tx + 16 * c) * 4 + e] = o[a][c][e] * inv;
@@ -238,69 +239,63 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
 }
 
 // ---- merge ----------------------------------------------------------------------------------
-// o = sum_s 2^(L_s - L) o_s, L = log2 sum_s 2^(L_s). Block (x, y): the group whose units cross the
-// start of CTA x's share, if the owner before it is the first that has units of the group; CTA x's head and
-// row tile, rows y * 8 .. + 7 of it, a warp a row, D / 32 columns a lane. A programmatic dependent of the
-// attention kernel. Bound by its chain of loads (record, L's, partials: L2 round trips), so that
-// partials are read 8 at a time.
+// o = sum_s 2^(L_s - L) o_s, L = log2 sum_s 2^(L_s). Block (x, y): what CTA x recorded (tree_record), rows
+// y * 8 .. + 7 of its row tile and head, a warp a row, D / 32 columns a lane. A programmatic dependent of
+// the attention kernel. Bound by latency, so it is two round trips to L2: the record, then a row's L's
+// and its first partials together.
 constexpr int kMergeWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(
     const __grid_constant__ TreeParams p) {
-  pdl_wait();
-  const int4 head = *p.head;
-  const int W = head.x, P = head.y, R = head.z, lanes = head.z * head.w;
-  const int next = blockIdx.x / lanes, sub = blockIdx.x % lanes;
-  if (next == 0 || next >= P) return;
-  const int4 g = p.info[2 * next], s = p.info[2 * next + 1];
-  if (g.y == 0) return;                        // its first group starts there: no crossing
-  const int at = tree_share_begin(next, W, P, p.narrow);
-  const int gs = at - g.y, ge = gs + g.z;      // the group's units
-  const int o1 = tree_owner(gs, W, P, p.narrow), o2 = tree_owner(ge - 1, W, P, p.narrow);
-  if (o1 != next - 1) return;                  // another block's
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rr = blockIdx.y * kMergeWarps + warp, r = sub % R * p.tile_rows + rr;
-  if (r >= s.y * p.group) return;
-  // partial j of the group: owner o1 + j's first piece, or o1's last
-  const bool whole_first = gs == tree_share_begin(o1, W, P, p.narrow);
-  const int n = o2 - o1 + 1;
-  const float* const part_o = p.part_o + (long long)rr * D + lane * (D / 32);
-  auto slot = [&](int j) {
-    return tree_slot(o1 + j, j > 0 || whole_first, lanes, sub) * p.tile_rows;
+  const int rr = blockIdx.y * kMergeWarps + warp;
+  pdl_wait();
+  const int4 a = p.info[2 * blockIdx.x], b = p.info[2 * blockIdx.x + 1];
+  const int n = a.x;
+  if (n == 0 || rr >= b.y) return;
+  constexpr int C = D / 32, K = 16;
+  using Vec = std::conditional_t<C == 4, float4, float2>;
+  auto slot = [&](int j) { return (long long)(a.y + (j ? a.z + (j - 1) * a.w : 0)) * p.tile_rows + rr; };
+  auto part = [&](int j) {
+    return *reinterpret_cast<const Vec*>(p.part_o + slot(j) * D + lane * C);
   };
+  Vec v[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) v[j] = j < n ? part(j) : Vec{};
   float top = -INFINITY;
-  for (int j = lane; j < n; j += 32) top = fmaxf(top, p.part_l[slot(j) + rr]);
+  for (int j = lane; j < n; j += 32) top = fmaxf(top, p.part_l[slot(j)]);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
   // a NaN among the L's passes the maximum over; it comes back through the weights
   const float ref = top == -INFINITY ? 0.f : top;
-  constexpr int C = D / 32;
   float acc[C] = {};
   float sum = 0.f;
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    const float wl = j0 + lane < n ? exp2f(p.part_l[slot(j0 + lane) + rr] - ref) : 0.f;
-    const int m = min(32, n - j0);
-#pragma unroll 8
-    for (int j = 0; j < m; ++j) {
-      const float wgt = __shfl_sync(0xffffffffu, wl, j);
-      const float* src = part_o + slot(j0 + j) * D;
-      float v[C];
-      if constexpr (C == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        v[0] = x.x; v[1] = x.y;
-      }
-      sum += wgt;
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] += wgt * v[c];
+  auto add = [&](float wgt, const Vec& x) {
+    sum += wgt;
+    acc[0] += wgt * x.x;
+    acc[1] += wgt * x.y;
+    if constexpr (C == 4) {
+      acc[2] += wgt * x.z;
+      acc[3] += wgt * x.w;
     }
+  };
+  for (int j0 = 0; j0 < n; j0 += 32) {
+    const float wl = j0 + lane < n ? exp2f(p.part_l[slot(j0 + lane)] - ref) : 0.f;
+    if (j0 == 0) {
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        const float wgt = __shfl_sync(0xffffffffu, wl, j);
+        if (j < n) add(wgt, v[j]);   // (a weight of 0 for none would make NaN of an infinite partial)
+      }
+    }
+#pragma unroll 8
+    for (int j = j0 == 0 ? K : 0; j < min(32, n - j0); ++j)
+      add(__shfl_sync(0xffffffffu, wl, j), part(j0 + j));
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int i = r / p.group, h = (g.x + sub / R) * p.group + r % p.group;
-  const long long row = (long long)(s.x + i) * p.c.hq + h;
+  const int r = b.z + rr, i = r / p.group, h = b.w * p.group + r % p.group;
+  const long long row = (long long)(b.x + i) * p.c.hq + h;
 #pragma unroll
   for (int c = 0; c < C; ++c)
     store_out(p.out, row * D + lane * C + c, p.c.out_dtype, acc[c] * inv * p.v_scale);
@@ -457,8 +452,7 @@ int decode_attn_tree_plan(const da_problem* problem, int max_tree, da_tree_plan*
   const size_t slots = 2ull * pl->grid;   // two an owner and row tile; owners x row tiles <= grid
   size_t off = 0;
   pl->off_status = off;
-  pl->off_head = off + 16;
-  off = align256(off + 64);
+  off = align256(off + 16);
   pl->off_info = off;
   off = align256(off + (size_t)pl->grid * 32);
   pl->off_part_l = off;
@@ -528,7 +522,6 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
   fill_common(pl.cache, p.c, a.block_table, nullptr, nullptr);
   char* ws = static_cast<char*>(a.workspace);
   p.c.status = reinterpret_cast<int32_t*>(ws + pl.off_status);
-  p.head = reinterpret_cast<int4*>(ws + pl.off_head);
   p.info = reinterpret_cast<int4*>(ws + pl.off_info);
   p.part_l = reinterpret_cast<float*>(ws + pl.off_part_l);
   p.part_o = reinterpret_cast<float*>(ws + pl.off_part_o);

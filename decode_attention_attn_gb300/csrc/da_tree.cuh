@@ -29,9 +29,7 @@ struct TreeParams {
   const unsigned long long* mask;   // [rows] or null (a chain)
   void* out;
   float* out_lse;
-  int4* head;                   // workspace: units W, owners P, row tiles R, heads
-  int4* info;                   // [owners][2]: {first head of its block, first unit's offset in its group, the
-                                // group's tiles, 0}, {first row, drafted tokens, 0, 0} of its first piece
+  int4* info;                   // [CTAs][2]: what the merge does for a CTA (tree_record)
   float* part_o;                // [owners][2][heads][R][tile rows][d]: 2 slots a CTA
   float* part_l;                // [owners][2][heads][R][tile rows]
   int rows, max_tree, group;
@@ -94,7 +92,7 @@ struct TreeShare {
   int u0, u1;          // units
   int base;            // first unit of sequence b0
   int b0;              // the sequence that u0 lies in
-  int row_tile, row_tiles, head, heads, owner, owners;
+  int row_tile, row_tiles, head, heads, owner, owners, units;
   int blocks;          // blocks of heads
   TreeRaw raw, ahead;  // sequences b0 and b0 + 1
 };
@@ -199,7 +197,7 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
     sh.raw = sc.raw;
     sh.ahead = sc.ahead;
   }
-  if (tid == 0 && blockIdx.x == 0) *p.head = make_int4(units, sh.owners, sh.row_tiles, sh.heads);
+  sh.units = units;
   return sh;
 }
 
@@ -245,17 +243,33 @@ struct TreeWalk {
   }
 };
 
-// What the merge has to know of an owner's first piece, in one place: it finds its work in one round
-// trip to memory.
-__device__ __forceinline__ void tree_record(const TreeParams& p, const TreeShare& sh,
-                                            const TreeWalk& w) {
-  p.info[2 * sh.owner] = make_int4(w.kvh - sh.head, w.t0, w.s.tiles, 0);
-  p.info[2 * sh.owner + 1] = make_int4(w.s.row0, w.s.T, 0, 0);
+// Slot of a partial: [owners][2][heads][row tiles]; `lane` = head * row tiles + row tile.
+__device__ __forceinline__ int tree_slot(int owner, bool head, int lanes, int lane) {
+  return (owner * 2 + (head ? 0 : 1)) * lanes + lane;
 }
 
-// Slot of a partial: [owners][2][heads][row tiles]; `lane` = head * row tiles + row tile.
-__device__ __forceinline__ long long tree_slot(int owner, bool head, int lanes, int lane) {
-  return ((long long)owner * 2 + (head ? 0 : 1)) * lanes + lane;
+// What the merge does for this CTA, written so that it learns it in one round trip to memory: the group
+// whose units cross the start of this CTA's share, if the owner before is the first with units of it.
+// {partials n (0: nothing), slot of the first, slot of the second less the first, slots from one to the
+// next}, {first row, rows of a head left of this row tile, first row of it, head}. One thread calls this.
+__device__ __forceinline__ void tree_record(const TreeParams& p, const TreeShare& sh, bool any,
+                                            const TreeWalk& w) {
+  int4 a = make_int4(0, 0, 0, 0), b = a;
+  if (any && w.t0 > 0) {
+    const int gs = sh.u0 - w.t0;   // the group's first unit
+    const int o1 = tree_owner(gs, sh.units, sh.owners, p.narrow);
+    if (o1 == sh.owner - 1) {
+      const int o2 = tree_owner(gs + w.s.tiles - 1, sh.units, sh.owners, p.narrow);
+      const int lanes = sh.row_tiles * sh.heads, lane = sh.head * sh.row_tiles + sh.row_tile;
+      const bool whole = gs == tree_share_begin(o1, sh.units, sh.owners, p.narrow);
+      const int first = tree_slot(o1, whole, lanes, lane);
+      a = make_int4(o2 - o1 + 1, first, tree_slot(o1 + 1, true, lanes, lane) - first, 2 * lanes);
+      b = make_int4(w.s.row0, w.s.T * p.group - sh.row_tile * p.tile_rows,
+                    sh.row_tile * p.tile_rows, w.kvh);
+    }
+  }
+  p.info[2 * blockIdx.x] = a;
+  p.info[2 * blockIdx.x + 1] = b;
 }
 
 }  // namespace da

@@ -386,7 +386,10 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   {
     const TreeShare mine = tree_schedule<kThreadsT>(p, *reinterpret_cast<TreeScratch*>(exch));
     pdl_launch_dependents();   // the merge's launch runs beside this kernel; it waits for its end
-    if (mine.u1 <= mine.u0) return;   // the whole CTA
+    if (mine.u1 <= mine.u0) {   // the whole CTA
+      if (tid == 0) tree_record(p, mine, false, TreeWalk(p, mine));
+      return;
+    }
     if (tid == 0) sh = mine;
   }
   if (tid == 0) {
@@ -682,8 +685,8 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
           // the row of out (and lse), or of the partials
           const long long at =
               whole ? (long long)(c.w.s.row0 + r / p.group) * p.c.hq + c.w.kvh * p.group + r % p.group
-                    : tree_slot(sh.owner, c.w.head, sh.row_tiles * sh.heads,
-                              sh.head * sh.row_tiles + sh.row_tile) * kTreeRows + row;
+                    : (long long)tree_slot(sh.owner, c.w.head, sh.row_tiles * sh.heads,
+                                           sh.head * sh.row_tiles + sh.row_tile) * kTreeRows + row;
           if (team == 0 && r >= 0) {
             const float lg = total == 0.f ? -INFINITY : m + log2f(total);
             if (!whole) p.part_l[at] = lg;
@@ -817,10 +820,10 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
     const bool issuer = elect_one();
     uint32_t it = 0, k_slot = 0, k_par = 0;
     TileSlot<NS> sl;
-    // the merge reads the first piece of every owner, whether this row tile has rows in it or not
     {
-      TreeWalk w(p, sh);
-      if (w.next(p, sh) && sh.row_tile == 0 && sh.head == 0 && issuer) tree_record(p, sh, w);
+      TreeWalk w(p, sh);   // (the cursor passes over pieces without rows in this row tile)
+      const bool any = w.next(p, sh);
+      if (issuer) tree_record(p, sh, any, w);
     }
     while (c.advance(p, sh)) {
       const uint32_t qb = c.piece & 1, buf = sl.buf;

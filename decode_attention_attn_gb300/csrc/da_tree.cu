@@ -558,7 +558,7 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
     int rc = q_map(pl, a.q, a.rows, &tmq);
     if (rc == DA_OK) rc = kv_map(pl, a.k_cache, p.c.box_tokens, &tmk);
     if (rc == DA_OK) rc = kv_map(pl, a.v_cache, p.c.box_tokens, &tmv);
-    if (rc == DA_OK) rc = raise_smem(fn, pl.smem_bytes, tree_launch_regs(pr.kv_fp8 != 0));
+    if (rc == DA_OK) rc = raise_smem(fn, pl.smem_bytes, pr.kv_fp8 ? 0 : kTreeLaunchRegs);
     if (rc != DA_OK) return rc;
     const void* vc = a.v_cache;
     void* kargs[5] = {&p, &tmq, &tmk, &tmv, &vc};

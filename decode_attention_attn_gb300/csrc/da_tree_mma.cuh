@@ -18,20 +18,12 @@ __host__ __device__ constexpr int tree_threads(bool fp8) {
   return (kTreeSoftmaxWarps + 4 + (fp8 ? kTreeConvertWarps : 0)) * 32;
 }
 
-// The softmax warps take registers from the others; all are launched with tree_launch_regs.
-__host__ __device__ constexpr int tree_launch_regs(bool fp8) { return fp8 ? 128 : 168; }
-__host__ __device__ constexpr int tree_softmax_regs(bool fp8, bool split) {
-  return !fp8 ? 192 : split ? 168 : 152;
-}
-__host__ __device__ constexpr int tree_other_regs(bool fp8, bool split) {
-  return !fp8 ? 120 : split ? 88 : 104;
-}
-__host__ __device__ constexpr bool tree_regs_fit(bool fp8, bool split) {
-  return kTreeSoftmaxWarps * tree_softmax_regs(fp8, split) +
-             (tree_threads(fp8) / 32 - kTreeSoftmaxWarps) * tree_other_regs(fp8, split) <=
-         tree_threads(fp8) / 32 * tree_launch_regs(fp8);
-}
-static_assert(tree_regs_fit(false, true) && tree_regs_fit(true, true) && tree_regs_fit(true, false),
+// 16-bit caches: launched with kTreeLaunchRegs a thread; the softmax warps then take registers from the
+// others. (FP8: 16 warps of 128 each.)
+constexpr int kTreeLaunchRegs = 168, kTreeSoftmaxRegs = 192, kTreeOtherRegs = 120;
+static_assert(kTreeSoftmaxWarps * kTreeSoftmaxRegs +
+                      (tree_threads(false) / 32 - kTreeSoftmaxWarps) * kTreeOtherRegs <=
+                  tree_threads(false) / 32 * kTreeLaunchRegs,
               "the register split must fit the launch allocation");
 
 // A 16-bit tile of 128 rows (tokens or query rows) of D elements in shared memory, as tcgen05.mma

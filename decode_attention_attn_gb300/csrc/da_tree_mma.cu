@@ -376,23 +376,12 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  if (tid == 0) {   // first use of a map would wait for its fetch
+  // Before the kernel ahead in the stream has finished (this is its programmatic dependent): barriers,
+  // TMEM, the tensor maps, whose first use would wait for their fetch.
+  if (tid == 0) {
     if (!kFp8) prefetch_tensormap(&tmq);
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
-  }
-  // the share lies in shared memory: it is looked at once a piece, and registers are short
-  TreeShare& sh = *reinterpret_cast<TreeShare*>(smem + L.misc_off + 16);
-  {
-    const TreeShare mine = tree_schedule<kThreadsT>(p, *reinterpret_cast<TreeScratch*>(exch));
-    pdl_launch_dependents();   // the merge's launch runs beside this kernel; it waits for its end
-    if (mine.u1 <= mine.u0) {   // the whole CTA
-      if (tid == 0) tree_record(p, mine, false, TreeWalk(p, mine));
-      return;
-    }
-    if (tid == 0) sh = mine;
-  }
-  if (tid == 0) {
     for (int i = 0; i < L.nk; ++i) {
       mbar_init(&k_full[i], kFp8 ? kTreeConvertWarps : 1);
       mbar_init(&k_empty[i], 1);
@@ -418,17 +407,35 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
       mbar_init(&rv_full[i], 1);
       mbar_init(&rv_empty[i], kTreeConvertWarps);
     }
-    // the swizzled tiles need a 1 KB boundary; elsewhere nothing may run
-    *abort_flag = (smem_u32(smem) & 1023u) ? 1 : 0;
-    if (*abort_flag) atomicOr(p.c.status, kStatusTimeout);
+    *abort_flag = 0;
     *odd = 0;
     fence_mbar_init();
   }
   if (warp == kTreeSoftmaxWarps + 2) tmem_alloc(tmem_slot, kTmemCols);
   tc_fence_before();
+  pdl_wait();
+  pdl_launch_dependents();   // the merge's launch runs beside this kernel; it waits for its end
+  // the share lies in shared memory: it is looked at once a piece, and registers are short
+  TreeShare& sh = *reinterpret_cast<TreeShare*>(smem + L.misc_off + 16);
+  bool any;
+  {
+    const TreeShare mine = tree_schedule<kThreadsT>(p, *reinterpret_cast<TreeScratch*>(exch));
+    any = mine.u1 > mine.u0;
+    if (tid == 0) sh = mine;
+    if (tid == 0 && !any) tree_record(p, mine, false, TreeWalk(p, mine));
+  }
+  // the swizzled tiles need a 1 KB boundary; elsewhere nothing may run
+  if (tid == 0 && any && (smem_u32(smem) & 1023u)) {
+    *abort_flag = 1;
+    atomicOr(p.c.status, kStatusTimeout);
+  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (!any) {   // the whole CTA
+    if (warp == kTreeSoftmaxWarps + 2) tmem_free(tmem, kTmemCols);
+    return;
+  }
   // K and V tiles: distance between 64-element blocks and between 8-row groups
   const bool paired = !kFp8 && p.c.paged;
   const uint32_t blk_bytes = paired ? 1024u : 16384u, grp_bytes = paired ? CH * 1024u : 1024u;

@@ -9,6 +9,7 @@
 #include <cstring>
 #include <new>
 #include <type_traits>
+#include <utility>
 
 #include "da_plan.h"
 
@@ -359,6 +360,16 @@ bool vector_ok(const void* p, long long rs, long long hs, int es, int bytes = 16
   return !p || (aligned(p, bytes) && rs * es % bytes == 0 && hs * es % bytes == 0);
 }
 
+// Whether rows written with these strides (elements) lie apart.
+bool lie_apart(long long rows, long long rs, long long heads, long long hs, long long d) {
+  if (rows > 1 && (heads == 1 || rs < hs)) {   // the smaller stride first
+    std::swap(rows, heads);
+    std::swap(rs, hs);
+  }
+  if (heads > 1 && hs < d) return false;
+  return rows <= 1 || rs >= (heads - 1) * hs + d;
+}
+
 int launch_rows(RowParams& p, int head_dim, int es, bool vec, const void* fn,
                 cudaStream_t stream) {
   const int v = vec ? 16 / es : 1;
@@ -581,6 +592,8 @@ int decode_attn_rope_apply(const da_rope* rope, const da_rope_args* args) {
   if (!a.x || !a.out || !a.positions || !aligned(a.x, es) || !aligned(a.out, es) ||
       !aligned(a.positions, 4))
     return DA_ERR_INVALID_ARG;
+  if (!lie_apart(a.rows, a.out_row_stride, a.heads, a.out_head_stride, rope->cfg.head_dim))
+    return DA_ERR_INVALID_ARG;
   if (a.x == a.out && (a.x_row_stride != a.out_row_stride || a.x_head_stride != a.out_head_stride))
     return DA_ERR_INVALID_ARG;
   RowParams p;
@@ -624,6 +637,8 @@ int decode_attn_kv_write(const da_plan* plan, const da_kv_write_args* args) {
   if (!a.k || !a.v || !a.k_cache || !a.v_cache || !aligned(a.k, es) || !aligned(a.v, es) ||
       !aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) || !aligned(a.positions, 4) ||
       !aligned(a.q, es) || !aligned(a.q_out, es) || !aligned(a.amax, 4))
+    return DA_ERR_INVALID_ARG;
+  if (a.q && !lie_apart(a.rows, a.q_out_row_stride, pr.num_q_heads, a.q_out_head_stride, pr.head_dim))
     return DA_ERR_INVALID_ARG;
   if (a.q && a.q == a.q_out &&
       (a.q_row_stride != a.q_out_row_stride || a.q_head_stride != a.q_out_head_stride))

@@ -429,9 +429,9 @@ void decode_attn_rope_destroy(da_rope* rope);
  * x of a forward call given the gradient with respect to its output (and, with m = 1, its
  * inverse). phi is reduced exactly in 64-bit fixed point whatever the position; the arithmetic is
  * fp32, rounded once to the storage type.
- *   x, out      device, [rows, heads, head_dim] of `dtype` with the given strides (elements;
- *               heads of a row and rows must not overlap in out). out may be x with equal
- *               strides (in place); any other overlap is not allowed.
+ *   x, out      device, [rows, heads, head_dim] of `dtype` with the given strides (elements; out's
+ *               heads and rows must lie apart: overlapping strides are refused). out may be x
+ *               with equal strides (in place); any other overlap is not allowed.
  *   positions   device int32 [rows]; negative positions rotate backwards.
  * Aligned to 16 bytes, with strides that are multiples of 16 bytes and rotary_dim and head_dim
  * multiples of 32 bytes, rows move 16 bytes a lane; any other case takes one pair a lane.
@@ -465,8 +465,8 @@ int decode_attn_rope_apply(const da_rope* rope, const da_rope_args* args);
  *               of the pool (of two rows written to one token, either may stay, in parts).
  *   rope        nullable. With it k is rotated by its row's position, and q, when given, is
  *               rotated into q_out: [rows, H_q, d] in qkv_dtype, both with strides; q_out may be
- *               q with equal strides. Without it q and q_out must be NULL. rope's head_dim must
- *               be the plan's.
+ *               q with equal strides, and its heads and rows must lie apart (else refused).
+ *               Without it q and q_out must be NULL. rope's head_dim must be the plan's.
  *   positions   nullable device int32 [rows]: the rotary positions where they are not the cache
  *               positions (drafted trees: a node's depth). Needs rope.
  *   amax        nullable device float [2]: amax[0] = max(amax[0], |k| as written before scaling),

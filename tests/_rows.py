@@ -15,7 +15,7 @@ class Layout:
 
     def __init__(self, held, new, hkv, d, page=0, capacity=None, before=0, behind=0, spare=2, seed=0,
                  hq=None, dtype="bf16", kv=None, k_scale=0.0125, v_scale=0.0075, out_dtype=None,
-                 validate=False):
+                 validate=False, num_sms=0):
         g = torch.Generator().manual_seed(seed)
         self.held, self.new, self.hkv, self.d, self.page = list(held), list(new), hkv, d, page
         self.hq, self.dtype, self.kv = hq or hkv, dtype, kv or dtype
@@ -55,7 +55,7 @@ class Layout:
             max_blocks_per_seq=self.table.shape[1] if page else 0,
             num_physical_blocks=self.pool if page else 0, max_seq_len=0 if page else cap,
             kv_dtype=self.kv, k_scale=self.k_scale, v_scale=self.v_scale, validate=validate,
-            num_sms=0 if torch.cuda.is_available() else 152)
+            num_sms=num_sms or (0 if torch.cuda.is_available() else 152))
         self.gen = g
 
     def normal(self, *shape):

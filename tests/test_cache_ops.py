@@ -87,6 +87,9 @@ def test_rope_apply_refuses_bad_arguments():
     assert call(dtype=3) == -2 and call(dtype=-1) == -2
     assert call(x=A + 1) == -1 and call(out=A + 3) == -1 and call(positions=A + 2) == -1
     assert call(out=A, out_row_stride=2048) == -1          # in place with other strides
+    assert call(out_head_stride=127) == -1 and call(out_head_stride=0) == -1    # rows on one another
+    assert call(out_row_stride=1023) == -1 and call(out_row_stride=128) == -1
+    assert call(out_row_stride=0) == -1 and call(out_row_stride=-1024) == -1
     # no rows: nothing is enqueued, no pointer is looked at
     args = binding.da_rope_args(None, None, 2, 0, 8, 1024, 128, 1024, 128, None, 0, None)
     binding.decode_attn_rope_apply(r.handle, args)
@@ -119,6 +122,7 @@ def test_kv_write_refuses_bad_arguments():
     assert call(rope=None, positions=None) == -1
     assert call(rope=short.handle) == -1                     # another head_dim
     assert call(q_out=A, q_out_row_stride=8192) == -1        # in place with other strides
+    assert call(q_out_row_stride=4095) == -1 and call(q_out_head_stride=64) == -1
     assert call(workspace=A + 16) == -1 and call(workspace_bytes=ws - 1) == -3
     contiguous, _ = _plan(paged=False, max_seq_len=64)
     assert call(contiguous) == -1                            # a table for a contiguous cache
@@ -236,6 +240,20 @@ def test_rope_strided_unaligned_and_in_place(offset, gap, rows):
     back = dev.cpu()
     view(back).copy_(view(base))          # nothing but the rotated heads changed
     assert torch.equal(back, base)
+
+
+@pytest.mark.gpu
+def test_rope_broadcast_rows_and_heads_first():
+    """One row read for all positions, and a [heads, rows, d] output."""
+    d = 128
+    pos = torch.arange(50, dtype=torch.int32)
+    x = torch.randn(1, 3, d, generator=torch.Generator().manual_seed(0)).half()
+    r = binding.Rope(d)
+    theta = torch.tensor(r.frequencies(), dtype=torch.float64)
+    out = torch.zeros(3, 50, d, dtype=torch.float16, device="cuda").transpose(0, 1)
+    got = r.apply(x.cuda().expand(50, 3, d), pos.cuda(), out=out)
+    assert got.stride() == (d, 50 * d, 1)
+    _check_rotated(got, x.expand(50, 3, d), pos, theta, d, False, 1.0)
 
 
 @pytest.mark.gpu

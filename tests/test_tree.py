@@ -213,6 +213,74 @@ def test_tree(dtype, kv, hq, hkv, d, page, name):
         check(lay, out, lse, reference(lay, q, kc, vc, None, scale))
 
 
+def fill_normal(lay):
+    """K and V rows of N(0, 1) in the cache's storage."""
+    if lay.kv != "e4m3":
+        return lay.normal(*lay.shape), lay.normal(*lay.shape)
+    return tuple((torch.randn(lay.shape, generator=lay.gen) / s).clamp(-448, 448).to(torch.float8_e4m3fn)
+                 .view(torch.uint8) for s in (lay.k_scale, lay.v_scale))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,kv", KINDS)
+@pytest.mark.parametrize("sms", [1, 3, 7, 40])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 8, 64), (32, 4, 128), (12, 3, 128)])
+def test_tree_on_few_ctas(dtype, kv, sms, hq, hkv, d):
+    """Plans for few SMs: many pieces a CTA, groups that start, end and cross in every way, row tiles and heads
+    that do not divide the CTAs."""
+    lay = Layout([700, 0, 129, 5, 1300, 64, 2], [9, 33, 0, 64, 1, 20, 7], hkv, d, page=16, hq=hq, dtype=dtype,
+                 kv=kv, num_sms=sms, seed=sms)
+    kc, vc = fill_normal(lay)
+    q, words = lay.normal(lay.rows, hq, d), random_trees(lay, lay.gen, hide=0.1)
+    out, lse, t = run(lay, q, kc, vc, words, 0.1)
+    check(lay, out, lse, reference(lay, q, kc, vc, words, 0.1))
+    t.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(kv):
+    """A pool of more than 2^31 elements: pages at its far end."""
+    page, hkv, d, hq = 64, 8, 128, 32
+    pool = 2 ** 31 // (page * hkv * d) + 7
+    fp8 = kv == "e4m3"
+    prob = binding.make_problem(batch=2, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, qkv_dtype="bf16",
+                                out_dtype="f32", paged=True, page_size=page, max_blocks_per_seq=3,
+                                num_physical_blocks=pool, kv_dtype=kv, k_scale=0.0125, v_scale=0.0125)
+    kc, vc = (torch.zeros((pool, page, hkv, d), dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+              for _ in range(2))
+    pages = torch.tensor([[pool - 1, pool - 3, 0], [pool - 2, 1, pool - 4]])
+    small = Layout([150, 70], [6, 3], hkv, d, page=page, hq=hq, kv=kv, capacity=192, spare=0, k_scale=0.0125,
+                   v_scale=0.0125, out_dtype="f32")
+    sk, sv = fill_normal(small)
+    for b in range(2):
+        for i in range(3):
+            if small.table[b, i] >= 0:
+                kc[pages[b, i]], vc[pages[b, i]] = sk[small.table[b, i]].cuda(), sv[small.table[b, i]].cuda()
+    q = small.normal(small.rows, hq, d)
+    out, lse = binding.TreeAttention(prob, 6).run(q.cuda(), kc, vc, pages.int().cuda(), small.row_offsets.cuda(),
+                                                  small.start.cuda(), None, 0.1)
+    check(small, out.cpu(), lse.cpu(), reference(small, q, sk, sv, None, 0.1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,kv", KINDS)
+def test_a_chain_is_a_lower_triangular_mask_and_streams_are_taken(dtype, kv):
+    lay = Layout([260, 3], [64, 11], 2, 64, page=8, hq=8, dtype=dtype, kv=kv)
+    kc, vc = fill_normal(lay)
+    q = lay.normal(lay.rows, 8, 64).cuda()
+    words = [(1 << i + 1) - 1 for n in lay.new for i in range(n)]
+    words = torch.tensor([w - (1 << 64) if w >> 63 else w for w in words]).cuda()
+    t = binding.TreeAttention(lay.problem, 64)
+    place = (kc.cuda(), vc.cuda(), lay.table.cuda(), lay.row_offsets.cuda(), lay.start.cuda())
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    a = t.run(q, *place, None, 0.1, stream=side)
+    b = t.run(q, *place, words, 0.1, stream=side)
+    side.synchronize()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype,kv", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "e4m3")])
 @pytest.mark.parametrize("d", [64, 128])

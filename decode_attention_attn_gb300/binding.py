@@ -588,6 +588,26 @@ def _int32(name, t, numel):
         raise ValueError(f"{name} must be a contiguous int32 tensor of {numel} elements")
 
 
+def _empty(shape, dtype, device, stream):
+    """A result's memory, from the pool of the stream that writes it: memory of another stream's pool may
+    still be in use there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(size, device):
+    """A zero-filled workspace, which needs no init call, ready for any stream."""
+    import torch
+    device = torch.device("cuda") if device is None else torch.device(device)
+    ws = torch.zeros(size, dtype=torch.uint8, device=device)
+    if not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(ws.device).synchronize()
+    return ws
+
+
 def _launch(fn, handle, args, index, stream):
     """Call fn on the given stream (the device's current one unless given), with the tensors' device
     current."""
@@ -640,16 +660,16 @@ class Rope:
 
     def apply(self, x, positions, out=None, transpose: bool = False, stream=None):
         """Rows of x (fp32, fp16 or bf16; rows and heads may be strided) rotated by `positions`
-        (int32 [rows]), into `out` (x itself: in place). transpose: the transposed map, which takes
-        the gradient of the output to the gradient of x."""
+        (int32 [rows]), into `out` (x itself: in place; allocated on the call's stream when None).
+        transpose: the transposed map, which takes the gradient of the output to the gradient of x;
+        autograd does not record the call, so a backward pass calls it itself."""
         code = self._codes.get(x.dtype)
         if code is None:
             raise ValueError("x must be fp32, fp16 or bf16")
         if x.dim() != 3:
             raise ValueError("x must be a [rows, heads, head_dim] tensor")
         if out is None:
-            import torch
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = _empty(x.shape, x.dtype, x.device, stream)
         rows, heads = x.shape[0], x.shape[1]
         x_row, x_head = _rows_tensor("x", x, x.dtype, heads, self.head_dim)
         out_row, out_head = _rows_tensor("out", out, x.dtype, heads, self.head_dim)
@@ -709,9 +729,7 @@ class KVCacheIO:
         self._cache = _Cache(problem)
         self.workspace = None
         if findings or problem.validate:
-            import torch
-            device = torch.device(device) if device is not None else torch.device("cuda")
-            self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=device)
+            self.workspace = _workspace(self.workspace_bytes, device)
 
     def __del__(self):
         plan = getattr(self, "plan", None)
@@ -737,7 +755,7 @@ class KVCacheIO:
         if q is not None:
             q_row, q_head = _rows_tensor("q", q, c.dtype, c.hq, c.d)
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                q_out = _empty(q.shape, q.dtype, q.device, stream)
             out_row, out_head = _rows_tensor("q_out", q_out, c.dtype, c.hq, c.d)
             if q.shape[0] != rows or q_out.shape[0] != rows:
                 raise ValueError("q and q_out must have as many rows as k")
@@ -811,14 +829,12 @@ class TreeAttention:
     must not overlap on the GPU."""
 
     def __init__(self, problem: da_problem, max_tree: int = MAX_TREE, device=None):
-        import torch
         self.problem = problem
         self.plan, self.workspace_bytes = decode_attn_tree_plan(problem, max_tree)
         self.info = decode_attn_tree_plan_info(self.plan)
         self._cache = _Cache(problem)
-        self.device = torch.device(device) if device is not None else torch.device("cuda")
-        # a zero-filled workspace needs no decode_attn_tree_workspace_init call
-        self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+        self.workspace = _workspace(self.workspace_bytes, device)
+        self.device = self.workspace.device
         self._address = self.workspace.data_ptr()
 
     def __del__(self):
@@ -841,9 +857,9 @@ class TreeAttention:
         _rows_tensor("q", q, c.dtype, c.hq, c.d)
         rows = q.shape[0]
         if out is None:
-            out = torch.empty(q.shape, dtype=c.out_dtype, device=q.device)
+            out = _empty(q.shape, c.out_dtype, q.device, stream)
         if out_lse is None:
-            out_lse = torch.empty((rows, c.hq), dtype=torch.float32, device=q.device)
+            out_lse = _empty((rows, c.hq), torch.float32, q.device, stream)
         _rows_tensor("out", out, c.out_dtype, c.hq, c.d)
         if not q.is_contiguous() or not out.is_contiguous() or out.shape[0] != rows:
             raise ValueError("q and out must be contiguous, with as many rows")

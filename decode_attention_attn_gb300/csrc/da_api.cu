@@ -455,8 +455,19 @@ namespace da {
 
 thread_local std::string g_cuda_error;
 
-int cuda_fail(cudaError_t e, const char* what) {
-  g_cuda_error = std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")";
+int cuda_fail(cudaError_t e, const char* what) noexcept {
+  try {
+    g_cuda_error = std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")";
+  } catch (...) {
+  }
+  return DA_ERR_CUDA;
+}
+
+int text_fail(const char* text, const char* more) noexcept {
+  try {
+    g_cuda_error = std::string(text) + more;
+  } catch (...) {
+  }
   return DA_ERR_CUDA;
 }
 

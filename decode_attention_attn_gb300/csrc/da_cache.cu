@@ -519,7 +519,7 @@ int decode_attn_rope_create(const da_rope_config* config, da_rope** rope_out) {
   if (c.head_dim < 2 || c.head_dim > 2 * kMaxPairs || c.head_dim % 2) return DA_ERR_UNSUPPORTED;
   if (c.rotary_dim < 2 || c.rotary_dim > c.head_dim || c.rotary_dim % 2) return DA_ERR_UNSUPPORTED;
   if (c.interleaved != 0 && c.interleaved != 1) return DA_ERR_INVALID_ARG;
-  if (!std::isfinite(c.base) || !(c.base > 1.0) || !std::isfinite(c.attn_factor))
+  if (!std::isfinite(c.base) || !(c.base > 1.0) || !std::isfinite((float)c.attn_factor))
     return DA_ERR_INVALID_ARG;
   const bool ramp = c.scaling == DA_ROPE_BY_PARTS || c.scaling == DA_ROPE_BY_INDEX;
   if (c.scaling < DA_ROPE_NONE || c.scaling > DA_ROPE_BY_INDEX) return DA_ERR_INVALID_ARG;
@@ -586,7 +586,8 @@ int decode_attn_rope_apply(const da_rope* rope, const da_rope_args* args) {
   const da_rope_args& a = *args;
   if (a.rows < 0 || a.heads < 1 || (a.transpose != 0 && a.transpose != 1))
     return DA_ERR_INVALID_ARG;
-  if (a.dtype < DA_F32 || a.dtype > DA_BF16) return DA_ERR_UNSUPPORTED;
+  if (a.dtype < DA_F32 || a.dtype > DA_BF16 || a.heads > DECODE_ATTN_ROPE_MAX_HEADS)
+    return DA_ERR_UNSUPPORTED;
   if (a.rows == 0) return DA_OK;
   const int es = elem_size(a.dtype);
   if (!a.x || !a.out || !a.positions || !aligned(a.x, es) || !aligned(a.out, es) ||
@@ -709,6 +710,8 @@ int decode_attn_kv_read(const da_plan* plan, const da_kv_read_args* args) {
   if (!aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) || !aligned(a.k_out, 16) ||
       !aligned(a.v_out, 16))
     return DA_ERR_INVALID_ARG;
+  const long long bytes = (long long)a.rows * pr.num_kv_heads * pr.head_dim * pl.es;
+  if (overlap(a.k_out, bytes, a.v_out, bytes)) return DA_ERR_INVALID_ARG;
   ReadParams p;
   std::memset(&p, 0, sizeof p);
   fill_common(pl, p.cache, a.block_table, nullptr, a.workspace);

@@ -33,8 +33,10 @@ namespace da {
 
 extern thread_local std::string g_cuda_error;   // text behind DA_ERR_CUDA
 
-// Records the CUDA error's text for decode_attn_strerror and returns DA_ERR_CUDA.
-int cuda_fail(cudaError_t e, const char* what);
+// Records the CUDA error's text for decode_attn_strerror and returns DA_ERR_CUDA. No exception leaves
+// them: without memory for the text the last one stays.
+int cuda_fail(cudaError_t e, const char* what) noexcept;
+int text_fail(const char* text, const char* more = "") noexcept;
 
 int validate_problem(const da_problem& p);
 
@@ -54,6 +56,11 @@ inline int elem_size(int dt) { return dt == DA_F32 ? 4 : 2; }
 
 inline bool aligned(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
+}
+
+inline bool overlap(const void* a, long long na, const void* b, long long nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
 }  // namespace da

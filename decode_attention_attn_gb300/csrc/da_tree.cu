@@ -328,11 +328,7 @@ int raise_smem(const void* fn, size_t smem, int regs) {
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, fn);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
-    if (fa.numRegs != regs) {
-      g_cuda_error = "tree kernel built with " + std::to_string(fa.numRegs) +
-                     " registers per thread; the register split needs " + std::to_string(regs);
-      return DA_ERR_CUDA;
-    }
+    if (fa.numRegs != regs) return text_fail("tree kernel not built to the registers of its split");
   }
   try {
     done.insert({dev, fn});
@@ -345,20 +341,13 @@ int encode(CUtensorMap* map, int es, int rank, const void* base, const cuuint64_
            const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle,
            CUtensorMapL2promotion promote) {
   auto fn = encode_fn();
-  if (!fn) {
-    g_cuda_error = "cuTensorMapEncodeTiled is not available from the driver";
-    return DA_ERR_CUDA;
-  }
+  if (!fn) return text_fail("cuTensorMapEncodeTiled is not available from the driver");
   const cuuint32_t ones[5] = {1u, 1u, 1u, 1u, 1u};
   const CUresult r =
       fn(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
          (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    g_cuda_error = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
-    return DA_ERR_CUDA;
-  }
-  return DA_OK;
+  return r == CUDA_SUCCESS ? DA_OK : text_fail("cuTensorMapEncodeTiled refused a tensor map");
 }
 
 // [tokens, Hkv, D] cache, one box = `box` tokens of one KV head. FP8 caches: rows of codes, swizzled
@@ -522,6 +511,9 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
   if (!a.q || !a.k_cache || !a.v_cache || !a.out || !aligned(a.q, 16) || !aligned(a.k_cache, 16) ||
       !aligned(a.v_cache, 16) || !aligned(a.out, 16))
     return DA_ERR_INVALID_ARG;
+  const long long elems = (long long)a.rows * pr.num_q_heads * pr.head_dim;
+  if (overlap(a.q, elems * elem_size(pr.qkv_dtype), a.out, elems * elem_size(pr.out_dtype)))
+    return DA_ERR_INVALID_ARG;
   TreeParams p;
   std::memset(&p, 0, sizeof p);
   fill_common(pl.cache, p.c, a.block_table, nullptr, nullptr);
@@ -546,6 +538,7 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
   std::memcpy(p.heads, pl.heads, sizeof p.heads);
   p.qscale = (float)((double)a.scale * 1.4426950408889634 * (pr.kv_fp8 ? (double)pr.k_scale : 1.0));
   p.v_scale = pr.kv_fp8 ? pr.v_scale : 1.f;
+  if (!std::isfinite(p.qscale)) return DA_ERR_INVALID_ARG;
   cudaStream_t stream = static_cast<cudaStream_t>(a.cuda_stream);
   cudaError_t e;
   if (pr.validate) {

@@ -408,7 +408,7 @@ typedef struct {
   double factor;             /* s > 0, finite; every scaling but NONE */
   double original_max_position; /* L0 > 0; BY_PARTS, BY_INDEX */
   double low, high;          /* 0 < low < high; BY_PARTS, BY_INDEX */
-  double attn_factor;        /* m, finite: both elements of a rotated pair are multiplied by m */
+  double attn_factor;        /* m, finite as a float: both elements of a rotated pair are multiplied by m */
 } da_rope_config;
 
 typedef struct da_rope da_rope;   /* opaque, host-owned, immutable after creation */
@@ -423,6 +423,8 @@ int decode_attn_rope_frequencies(const da_rope* rope, double* theta);
 
 void decode_attn_rope_destroy(da_rope* rope);
 
+#define DECODE_ATTN_ROPE_MAX_HEADS (1 << 20)
+
 /* Rotate rows: for every row r, head h and pair (a, b) with angle phi = positions[r] theta_i,
  *   out_a = m (x_a cos phi - x_b sin phi),  out_b = m (x_b cos phi + x_a sin phi);
  * transpose = 1: sin phi is negated, which is the transposed map, so the gradient with respect to
@@ -435,7 +437,8 @@ void decode_attn_rope_destroy(da_rope* rope);
  *   positions   device int32 [rows]; negative positions rotate backwards.
  * Aligned to 16 bytes, with strides that are multiples of 16 bytes and rotary_dim and head_dim
  * multiples of 32 bytes, rows move 16 bytes a lane; any other case takes one pair a lane.
- * Enqueued on cuda_stream. Errors: INVALID_ARG, UNSUPPORTED (dtype), CUDA. */
+ * Enqueued on cuda_stream. Errors: INVALID_ARG, UNSUPPORTED (dtype; more than
+ * DECODE_ATTN_ROPE_MAX_HEADS heads), CUDA. */
 typedef struct {
   const void* x;
   void* out;
@@ -506,8 +509,8 @@ int decode_attn_kv_write(const da_plan* plan, const da_kv_write_args* args);
 
 /* Read rows back from the cache: k_out[r], v_out[r] = the K and V of row r's position, codes of an
  * FP8 cache times k_scale or v_scale, rounded once to qkv_dtype (to nearest even).
- *   k_out, v_out  device, [rows, H_kv, d] contiguous, qkv_dtype, 16-byte aligned; either may be
- *                 NULL (not both), and its cache then too.
+ *   k_out, v_out  device, [rows, H_kv, d] contiguous, qkv_dtype, 16-byte aligned, apart (else
+ *                 refused); either may be NULL (not both), and its cache then too.
  * Rows at a position outside [0, capacity) or on a bad block-table entry read as zeros and are
  * recorded as in decode_attn_kv_write; rows of no sequence are left as they were.
  * Writing rows read from an FP8 cache back with the same scales reproduces their codes (a NaN
@@ -577,7 +580,7 @@ int decode_attn_tree_workspace_init(const da_tree_plan* plan, void* workspace,
  *               attends to drafted token j of its sequence (its own bit too, where it should
  *               see itself). Bits at or past T_b are ignored. NULL: a chain, j <= i.
  *   out         device, [rows, H_q, d] in out_dtype, 16-byte aligned. A row that attends to
- *               nothing (no context, mask 0) gets 0. out must not overlap q.
+ *               nothing (no context, mask 0) gets 0. out that overlaps q is refused.
  *   out_lse     nullable device float [rows, H_q]: natural-log log-sum-exp (-inf: nothing).
  *   workspace   device, 256-byte aligned, at least the plan's workspace_bytes.
  * Masked drafted tokens and cache slots past a sequence's end add nothing, whatever they hold

@@ -41,7 +41,7 @@ def test_frequencies(kw):
     (dict(head_dim=0), -2), (dict(head_dim=258), -2), (dict(head_dim=127), -2),
     (dict(rotary_dim=0), -2), (dict(rotary_dim=130), -2), (dict(rotary_dim=63), -2),
     (dict(base=1.0), -1), (dict(base=math.inf), -1), (dict(base=math.nan), -1),
-    (dict(attn_factor=math.nan), -1), (dict(scaling="linear", factor=0.0), -1),
+    (dict(attn_factor=math.nan), -1), (dict(attn_factor=1e300), -1), (dict(scaling="linear", factor=0.0), -1),
     (dict(scaling="ntk", factor=-2.0), -1), (dict(scaling="linear", factor=math.inf), -1),
     (dict(scaling="by_parts", factor=2.0), -1),                     # no original length
     (dict(scaling="by_parts", factor=2.0, original_max_position=64, low=4.0, high=4.0), -1),
@@ -84,7 +84,7 @@ def test_rope_apply_refuses_bad_arguments():
 
     assert call(x=None) == -1 and call(out=None) == -1 and call(positions=None) == -1
     assert call(rows=-1) == -1 and call(heads=0) == -1 and call(transpose=2) == -1
-    assert call(dtype=3) == -2 and call(dtype=-1) == -2
+    assert call(dtype=3) == -2 and call(dtype=-1) == -2 and call(heads=(1 << 20) + 1) == -2
     assert call(x=A + 1) == -1 and call(out=A + 3) == -1 and call(positions=A + 2) == -1
     assert call(out=A, out_row_stride=2048) == -1          # in place with other strides
     assert call(out_head_stride=127) == -1 and call(out_head_stride=0) == -1    # rows on one another
@@ -138,13 +138,14 @@ def test_kv_read_refuses_bad_arguments():
     plan, ws = _plan()
 
     def call(plan=plan, **kw):
-        args = binding.da_kv_read_args(A, A, A, A, A, 4, A, A, A, ws, None)
+        args = binding.da_kv_read_args(A, A, A, A, A, 4, A, A + 65536, A, ws, None)
         return _refused(binding.decode_attn_kv_read, plan, args, **kw)
 
     for name in ("k_cache", "v_cache", "block_table", "row_offsets", "start", "k_out", "v_out"):
         assert call(**{name: None}) == -1, name
     assert call(k_cache=None, k_out=None, v_cache=None, v_out=None) == -1
     assert call(rows=-1) == -1 and call(k_out=A + 8) == -1 and call(v_cache=A + 4) == -1
+    assert call(v_out=A) == -1 and call(v_out=A + 16) == -1       # results on one another
     assert call(workspace=A + 16) == -1 and call(workspace_bytes=ws - 1) == -3
     binding.decode_attn_destroy(plan)
 

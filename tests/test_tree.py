@@ -161,6 +161,8 @@ def test_run_refuses_bad_arguments():
     for name, off in (("q", 8), ("k_cache", 8), ("v_cache", 2), ("out", 8), ("out_lse", 2), ("tree_mask", 4),
                       ("row_offsets", 2), ("ctx_lens", 1), ("block_table", 2), ("workspace", 128)):
         assert call(**{name: A + off}) == -1, name
+    assert call(out=A) == -1 and call(out=A + 4 * 32 * 128 * 2 - 16) == -1      # over q
+    assert call(scale=3e38) == -1                            # times log2(e): no float
     assert call(workspace_bytes=ws - 1) == -3
     assert call(flat) == -1                                  # a table for a contiguous cache
     L = binding.lib()
@@ -273,7 +275,7 @@ def test_a_chain_is_a_lower_triangular_mask_and_streams_are_taken(dtype, kv):
     words = torch.tensor([w - (1 << 64) if w >> 63 else w for w in words]).cuda()
     t = binding.TreeAttention(lay.problem, 64)
     place = (kc.cuda(), vc.cuda(), lay.table.cuda(), lay.row_offsets.cuda(), lay.start.cuda())
-    torch.cuda.synchronize()
+    torch.cuda.synchronize()      # inputs of another stream: theirs to wait for; results are made on `side`
     side = torch.cuda.Stream()
     a = t.run(q, *place, None, 0.1, stream=side)
     b = t.run(q, *place, words, 0.1, stream=side)

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from typing import Optional
 
 from . import build as _build
@@ -555,77 +556,100 @@ class DecodeAttention:
         return out, out_lse, row_flags
 
 
-def _device_index(names: str, *tensors) -> int:
-    """The index of the one CUDA device that the tensors (named in `names`; None is passed over) are on."""
-    index = None
-    for i, t in enumerate(tensors):
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
-            raise ValueError(f"{names.split()[i]} must be a CUDA tensor")
-        if index is None:
-            index = d
-        elif d != index:
-            raise ValueError(f"{names.split()[i]} is on cuda:{d}, other tensors on cuda:{index}")
-    return index
+# What a call of the wrappers below costs on the host is of the order of the kernel it launches, so torch is
+# imported once, checks look at an attribute at a time, and the argument structures are packed in one go.
+_torch = None
+
+
+def _use_torch():
+    global _torch
+    import torch
+    _torch = torch
+
+
+class _Entry:
+    """A C entry point that takes (handle, structure of `args`, whose last field is the stream)."""
+
+    FORMATS = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int: "i", ctypes.c_float: "f",
+               ctypes.c_size_t: "N"}
+
+    def __init__(self, name, args):
+        packer = struct.Struct("@" + "".join(self.FORMATS[t] for _, t in args._fields_) + "0P")
+        if packer.size != ctypes.sizeof(args):
+            raise RuntimeError(f"{args.__name__} has no packed form")
+        self.name, self.pack = name, packer.pack
+        self.fn = ctypes.CFUNCTYPE(ctypes.c_int, P, ctypes.c_char_p)((name, lib()))
+
+    def __call__(self, handle, index, stream, *values):
+        """Call with the structure's other fields `values` (0: a null pointer) on the given stream (the
+        device's current one unless given), with device `index` current."""
+        if stream is not None:
+            s = stream.cuda_stream
+        else:
+            s = _torch._C._cuda_getCurrentRawStream(index)   # current_stream() without its objects
+        args = self.pack(*values, s)
+        if _torch._C._cuda_getDevice() == index:
+            rc = self.fn(handle, args)
+        else:
+            with _torch.cuda.device(index):
+                rc = self.fn(handle, args)
+        if rc:
+            raise DecodeAttnError(rc, self.name)
+
+
+_entries = {}
+
+
+def _entry(name, args):
+    _use_torch()
+    if name not in _entries:
+        _entries[name] = _Entry(name, args)
+    return _entries[name]
+
+
+def _refuse_devices(index, **tensors):
+    """Says which of the tensors is not on one CUDA device with the others."""
+    for name, t in tensors.items():
+        if t is not None and t.get_device() < 0:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, other tensors on cuda:{index}")
 
 
 def _rows_tensor(name, t, dtype, heads, d):
     """A [rows, heads, d] tensor whose heads are contiguous (rows and heads may be strided). Returns its
-    row and head strides."""
-    if t.dtype != dtype or t.dim() != 3 or t.shape[1:] != (heads, d):
+    rows, and the strides of rows and heads."""
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 3 or shape[1] != heads or shape[2] != d:
         raise ValueError(f"{name} must be a [rows, {heads}, {d}] tensor of {dtype}")
     row, head, one = t.stride()
     if one != 1 and t.numel():
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return row, head
+    return shape[0], row, head
 
 
 def _int32(name, t, numel):
-    import torch
-    if t.dtype != torch.int32 or t.numel() != numel or not t.is_contiguous():
+    if t.dtype is not _torch.int32 or t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of {numel} elements")
 
 
 def _empty(shape, dtype, device, stream):
     """A result's memory, from the pool of the stream that writes it: memory of another stream's pool may
     still be in use there."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 def _workspace(size, device):
     """A zero-filled workspace, which needs no init call, ready for any stream."""
-    import torch
-    device = torch.device("cuda") if device is None else torch.device(device)
-    ws = torch.zeros(size, dtype=torch.uint8, device=device)
-    if not torch.cuda.is_current_stream_capturing():
-        torch.cuda.current_stream(ws.device).synchronize()
+    device = _torch.device("cuda") if device is None else _torch.device(device)
+    ws = _torch.zeros(size, dtype=_torch.uint8, device=device)
+    if not _torch.cuda.is_current_stream_capturing():
+        _torch.cuda.current_stream(ws.device).synchronize()
     return ws
-
-
-def _launch(fn, handle, args, index, stream):
-    """Call fn on the given stream (the device's current one unless given), with the tensors' device
-    current."""
-    import torch
-    if stream is not None:
-        s = stream.cuda_stream
-    else:
-        s = torch._C._cuda_getCurrentRawStream(index)   # current_stream() without its objects
-    args.cuda_stream = s or None
-    if torch._C._cuda_getDevice() == index:
-        fn(handle, args)
-    else:
-        with torch.cuda.device(index):
-            fn(handle, args)
-
-
-def _address(t):
-    return None if t is None else t.data_ptr()
 
 
 class Rope:
@@ -641,6 +665,7 @@ class Rope:
                  attn_factor: float = 1.0):
         if scaling not in ROPE_CODES:
             raise ValueError(f"scaling must be one of {sorted(ROPE_CODES)}")
+        self._apply = _entry("decode_attn_rope_apply", da_rope_args)
         self.head_dim = head_dim
         self.rotary_dim = head_dim if rotary_dim is None else rotary_dim
         self.handle = decode_attn_rope_create(da_rope_config(
@@ -663,25 +688,26 @@ class Rope:
         (int32 [rows]), into `out` (x itself: in place; allocated on the call's stream when None).
         transpose: the transposed map, which takes the gradient of the output to the gradient of x;
         autograd does not record the call, so a backward pass calls it itself."""
-        code = self._codes.get(x.dtype)
+        dtype, shape = x.dtype, x.shape
+        code = self._codes.get(dtype)
         if code is None:
             raise ValueError("x must be fp32, fp16 or bf16")
-        if x.dim() != 3:
+        if len(shape) != 3:
             raise ValueError("x must be a [rows, heads, head_dim] tensor")
         if out is None:
-            out = _empty(x.shape, x.dtype, x.device, stream)
-        rows, heads = x.shape[0], x.shape[1]
-        x_row, x_head = _rows_tensor("x", x, x.dtype, heads, self.head_dim)
-        out_row, out_head = _rows_tensor("out", out, x.dtype, heads, self.head_dim)
-        if out.shape[0] != rows:
+            out = _empty(shape, dtype, x.device, stream)
+        heads = shape[1]
+        rows, x_row, x_head = _rows_tensor("x", x, dtype, heads, self.head_dim)
+        out_rows, out_row, out_head = _rows_tensor("out", out, dtype, heads, self.head_dim)
+        if out_rows != rows:
             raise ValueError("out must have as many rows as x")
         _int32("positions", positions, rows)
-        index = _device_index("x positions out", x, positions, out)
-        if rows == 0 or heads == 0:
-            return out
-        args = da_rope_args(x.data_ptr(), out.data_ptr(), code, rows, heads, x_row, x_head, out_row,
-                            out_head, positions.data_ptr(), int(bool(transpose)))
-        _launch(decode_attn_rope_apply, self.handle, args, index, stream)
+        index = x.get_device()
+        if index < 0 or positions.get_device() != index or out.get_device() != index:
+            _refuse_devices(index, x=x, positions=positions, out=out)
+        if rows and heads:
+            self._apply(self.handle, index, stream, x.data_ptr(), out.data_ptr(), code, rows, heads,
+                        x_row, x_head, out_row, out_head, positions.data_ptr(), 1 if transpose else 0)
         return out
 
 
@@ -702,17 +728,27 @@ class _Cache:
                       (pr.batch, pr.max_seq_len, self.hkv, self.d))
 
     def check(self, k_cache, v_cache, block_table, row_offsets, start):
-        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-            if t is not None and (t.dtype not in self.kv_dtypes or t.shape != self.shape or
+        """Returns the device's index and the block table's address (0: none)."""
+        for t in (k_cache, v_cache):
+            if t is not None and (t.shape != self.shape or t.dtype not in self.kv_dtypes or
                                   not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous {self.shape} tensor of "
-                                 f"{self.kv_dtypes}")
+                raise ValueError(f"{'k_cache' if t is k_cache else 'v_cache'} must be a contiguous "
+                                 f"{self.shape} tensor of {self.kv_dtypes}")
         if (block_table is None) == self.paged:
             raise ValueError("a paged cache takes a block_table, a contiguous one none")
-        if block_table is not None:
-            _int32("block_table", block_table, self.table)
         _int32("row_offsets", row_offsets, self.batch + 1)
         _int32("the sequences' lengths", start, self.batch)
+        index, table = row_offsets.get_device(), 0
+        if block_table is not None:
+            _int32("block_table", block_table, self.table)
+            table = block_table.data_ptr()
+        if index < 0 or start.get_device() != index or \
+                (k_cache is not None and k_cache.get_device() != index) or \
+                (v_cache is not None and v_cache.get_device() != index) or \
+                (block_table is not None and block_table.get_device() != index):
+            _refuse_devices(index, row_offsets=row_offsets, start=start, k_cache=k_cache, v_cache=v_cache,
+                            block_table=block_table)
+        return index, table
 
 
 class KVCacheIO:
@@ -724,6 +760,8 @@ class KVCacheIO:
     without a place in the cache, which check_status() reports."""
 
     def __init__(self, problem: da_problem, findings: bool = False, device=None):
+        self._write = _entry("decode_attn_kv_write", da_kv_write_args)
+        self._read = _entry("decode_attn_kv_read", da_kv_read_args)
         self.problem = problem
         self.plan, self.workspace_bytes = decode_attn_plan(problem, 0)
         self._cache = _Cache(problem)
@@ -743,70 +781,77 @@ class KVCacheIO:
         rotate k, and q into q_out (allocated when None, q itself: in place). `positions`: rotary
         positions other than the cache positions. `amax`: a float32 [2] tensor that takes the
         running largest |k| and |v|. Returns q_out (None without q)."""
-        import torch
-        c = self._cache
-        c.check(k_cache, v_cache, block_table, row_offsets, start)
+        c, ws = self._cache, self.workspace
+        index, table = c.check(k_cache, v_cache, block_table, row_offsets, start)
         if k_cache is None or v_cache is None:
             raise ValueError("k_cache and v_cache must both be given")
-        rows = k.shape[0]
-        k_row, k_head = _rows_tensor("k", k, c.dtype, c.hkv, c.d)
-        v_row, v_head = _rows_tensor("v", v, c.dtype, c.hkv, c.d)
-        q_row = q_head = out_row = out_head = 0
+        rows, k_row, k_head = _rows_tensor("k", k, c.dtype, c.hkv, c.d)
+        v_rows, v_row, v_head = _rows_tensor("v", v, c.dtype, c.hkv, c.d)
+        if v_rows != rows:
+            raise ValueError("v must have as many rows as k")
+        away = k.get_device() != index or v.get_device() != index
+        q_row = q_head = out_row = out_head = q_at = out_at = at = most = 0
         if q is not None:
-            q_row, q_head = _rows_tensor("q", q, c.dtype, c.hq, c.d)
+            q_rows, q_row, q_head = _rows_tensor("q", q, c.dtype, c.hq, c.d)
             if q_out is None:
-                q_out = _empty(q.shape, q.dtype, q.device, stream)
-            out_row, out_head = _rows_tensor("q_out", q_out, c.dtype, c.hq, c.d)
-            if q.shape[0] != rows or q_out.shape[0] != rows:
+                q_out = _empty(q.shape, c.dtype, q.device, stream)
+            out_rows, out_row, out_head = _rows_tensor("q_out", q_out, c.dtype, c.hq, c.d)
+            if q_rows != rows or out_rows != rows:
                 raise ValueError("q and q_out must have as many rows as k")
+            q_at, out_at = q.data_ptr(), q_out.data_ptr()
+            away = away or q.get_device() != index or q_out.get_device() != index
         elif q_out is not None:
             raise ValueError("q_out without q")
-        if v.shape[0] != rows:
-            raise ValueError("v must have as many rows as k")
-        if positions is not None:
-            _int32("positions", positions, rows)
         if rope is None and (q is not None or positions is not None):
             raise ValueError("q and positions need a rope")
-        if amax is not None and (amax.dtype != torch.float32 or amax.numel() != 2 or
-                                 not amax.is_contiguous()):
-            raise ValueError("amax must be a contiguous float32 tensor of 2 elements")
-        index = _device_index("k v k_cache v_cache block_table row_offsets start positions q q_out amax "
-                              "workspace", k, v, k_cache, v_cache, block_table, row_offsets, start,
-                              positions, q, q_out, amax, self.workspace)
-        if rows == 0:
-            return q_out
-        args = da_kv_write_args(k.data_ptr(), v.data_ptr(), k_row, k_head, v_row, v_head, rows,
-                                k_cache.data_ptr(), v_cache.data_ptr(), _address(block_table),
-                                row_offsets.data_ptr(), start.data_ptr(),
-                                None if rope is None else rope.handle, _address(positions),
-                                _address(q), _address(q_out), q_row, q_head, out_row, out_head,
-                                _address(amax), _address(self.workspace), self.workspace_bytes)
-        _launch(decode_attn_kv_write, self.plan, args, index, stream)
+        if positions is not None:
+            _int32("positions", positions, rows)
+            at = positions.data_ptr()
+            away = away or positions.get_device() != index
+        if amax is not None:
+            if amax.dtype is not _torch.float32 or amax.numel() != 2 or not amax.is_contiguous():
+                raise ValueError("amax must be a contiguous float32 tensor of 2 elements")
+            most = amax.data_ptr()
+            away = away or amax.get_device() != index
+        if away or (ws is not None and ws.get_device() != index):
+            _refuse_devices(index, k=k, v=v, q=q, q_out=q_out, positions=positions, amax=amax,
+                            workspace=ws)
+        if rows:
+            self._write(self.plan, index, stream, k.data_ptr(), v.data_ptr(), k_row, k_head, v_row,
+                        v_head, rows, k_cache.data_ptr(), v_cache.data_ptr(), table,
+                        row_offsets.data_ptr(), start.data_ptr(),
+                        0 if rope is None else rope.handle.value, at, q_at, out_at, q_row, q_head,
+                        out_row, out_head, most, 0 if ws is None else ws.data_ptr(),
+                        self.workspace_bytes)
         return q_out
 
     def read(self, k_cache, v_cache, block_table, row_offsets, start, k_out, v_out, stream=None):
         """Fill k_out and v_out (contiguous [rows, H_kv, d]; either may be None, its cache too) with
         the rows' K and V. Returns (k_out, v_out)."""
-        c = self._cache
-        c.check(k_cache, v_cache, block_table, row_offsets, start)
-        outs = [t for t in (k_out, v_out) if t is not None]
-        if not outs or (k_out is None) != (k_cache is None) or \
-                (v_out is None) != (v_cache is None) or outs[0].shape != outs[-1].shape:
+        c, ws = self._cache, self.workspace
+        index, table = c.check(k_cache, v_cache, block_table, row_offsets, start)
+        if (k_out is None) != (k_cache is None) or (v_out is None) != (v_cache is None) or \
+                (k_out is None and v_out is None):
             raise ValueError("give k_out with k_cache, v_out with v_cache, or all four")
-        for t in outs:
-            _rows_tensor("k_out / v_out", t, c.dtype, c.hkv, c.d)
-            if not t.is_contiguous():
-                raise ValueError("k_out and v_out must be contiguous")
-        index = _device_index("k_cache v_cache block_table row_offsets start k_out v_out workspace",
-                              k_cache, v_cache, block_table, row_offsets, start, k_out, v_out,
-                              self.workspace)
-        rows = outs[0].shape[0]
-        if rows == 0:
-            return k_out, v_out
-        args = da_kv_read_args(_address(k_cache), _address(v_cache), _address(block_table),
-                               row_offsets.data_ptr(), start.data_ptr(), rows, _address(k_out),
-                               _address(v_out), _address(self.workspace), self.workspace_bytes)
-        _launch(decode_attn_kv_read, self.plan, args, index, stream)
+        rows, places = -1, []
+        for t in (k_out, v_out):
+            if t is None:
+                places.append(0)
+                continue
+            n, _, _ = _rows_tensor("k_out / v_out", t, c.dtype, c.hkv, c.d)
+            if not t.is_contiguous() or (rows >= 0 and n != rows):
+                raise ValueError("k_out and v_out must be contiguous, with as many rows")
+            if t.get_device() != index:
+                _refuse_devices(index, k_out=k_out, v_out=v_out)
+            rows = n
+            places.append(t.data_ptr())
+        if ws is not None and ws.get_device() != index:
+            _refuse_devices(index, workspace=ws)
+        if rows:
+            self._read(self.plan, index, stream, 0 if k_cache is None else k_cache.data_ptr(),
+                       0 if v_cache is None else v_cache.data_ptr(), table, row_offsets.data_ptr(),
+                       start.data_ptr(), rows, places[0], places[1], 0 if ws is None else ws.data_ptr(),
+                       self.workspace_bytes)
         return k_out, v_out
 
     def check_status(self, stream=None):
@@ -817,9 +862,8 @@ class KVCacheIO:
 
 
 def _check_workspace(fn, plan, workspace, stream):
-    import torch
-    with torch.cuda.device(workspace.device):
-        s = stream if stream is not None else torch.cuda.current_stream()
+    with _torch.cuda.device(workspace.device):
+        s = stream if stream is not None else _torch.cuda.current_stream()
         fn(plan, workspace.data_ptr(), s.cuda_stream)
 
 
@@ -829,13 +873,13 @@ class TreeAttention:
     must not overlap on the GPU."""
 
     def __init__(self, problem: da_problem, max_tree: int = MAX_TREE, device=None):
+        self._run = _entry("decode_attn_tree_run", da_tree_args)
         self.problem = problem
         self.plan, self.workspace_bytes = decode_attn_tree_plan(problem, max_tree)
         self.info = decode_attn_tree_plan_info(self.plan)
         self._cache = _Cache(problem)
         self.workspace = _workspace(self.workspace_bytes, device)
         self.device = self.workspace.device
-        self._address = self.workspace.data_ptr()
 
     def __del__(self):
         plan = getattr(self, "plan", None)
@@ -849,37 +893,35 @@ class TreeAttention:
         and V lie in the cache from position ctx_lens[b] on. tree_mask: int64 (or uint64) [rows],
         bit j of a row's word set iff it attends to its sequence's drafted token j; None: a chain.
         Returns (out, lse)."""
-        import torch
-        c = self._cache
-        c.check(k_cache, v_cache, block_table, row_offsets, ctx_lens)
+        c, ws, mask = self._cache, self.workspace, 0
+        index, table = c.check(k_cache, v_cache, block_table, row_offsets, ctx_lens)
         if k_cache is None or v_cache is None:
             raise ValueError("k_cache and v_cache must both be given")
-        _rows_tensor("q", q, c.dtype, c.hq, c.d)
-        rows = q.shape[0]
+        rows, _, _ = _rows_tensor("q", q, c.dtype, c.hq, c.d)
         if out is None:
             out = _empty(q.shape, c.out_dtype, q.device, stream)
         if out_lse is None:
-            out_lse = _empty((rows, c.hq), torch.float32, q.device, stream)
-        _rows_tensor("out", out, c.out_dtype, c.hq, c.d)
-        if not q.is_contiguous() or not out.is_contiguous() or out.shape[0] != rows:
+            out_lse = _empty((rows, c.hq), _torch.float32, q.device, stream)
+        out_rows, _, _ = _rows_tensor("out", out, c.out_dtype, c.hq, c.d)
+        if out_rows != rows or not q.is_contiguous() or not out.is_contiguous():
             raise ValueError("q and out must be contiguous, with as many rows")
-        if out_lse.dtype != torch.float32 or out_lse.shape != (rows, c.hq) or \
+        if out_lse.dtype is not _torch.float32 or out_lse.shape != (rows, c.hq) or \
                 not out_lse.is_contiguous():
             raise ValueError("out_lse must be a contiguous float32 [rows, H_q] tensor")
-        if tree_mask is not None and (tree_mask.dtype not in (torch.int64, torch.uint64) or
-                                      tree_mask.shape != (rows,) or
-                                      not tree_mask.is_contiguous()):
-            raise ValueError("tree_mask must be a contiguous int64 [rows] tensor")
-        index = _device_index("q k_cache v_cache block_table row_offsets ctx_lens tree_mask out out_lse "
-                              "workspace", q, k_cache, v_cache, block_table, row_offsets, ctx_lens,
-                              tree_mask, out, out_lse, self.workspace)
-        if rows == 0:
-            return out, out_lse
-        args = da_tree_args(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                            _address(block_table), row_offsets.data_ptr(), ctx_lens.data_ptr(),
-                            _address(tree_mask), rows, scale, out.data_ptr(), out_lse.data_ptr(),
-                            self._address, self.workspace_bytes)
-        _launch(decode_attn_tree_run, self.plan, args, index, stream)
+        away = q.get_device() != index or out.get_device() != index or \
+            out_lse.get_device() != index or ws.get_device() != index
+        if tree_mask is not None:
+            if tree_mask.dtype not in (_torch.int64, _torch.uint64) or tree_mask.shape != (rows,) or \
+                    not tree_mask.is_contiguous():
+                raise ValueError("tree_mask must be a contiguous int64 [rows] tensor")
+            mask = tree_mask.data_ptr()
+            away = away or tree_mask.get_device() != index
+        if away:
+            _refuse_devices(index, q=q, out=out, out_lse=out_lse, tree_mask=tree_mask, workspace=ws)
+        if rows:
+            self._run(self.plan, index, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                      table, row_offsets.data_ptr(), ctx_lens.data_ptr(), mask, rows, scale,
+                      out.data_ptr(), out_lse.data_ptr(), ws.data_ptr(), self.workspace_bytes)
         return out, out_lse
 
     def check_status(self, stream=None):

@@ -47,6 +47,8 @@ struct CoreSmem {
 // A 32 x 64 tile of logits by 256 threads: thread (ty, tx) holds rows 2 ty, 2 ty + 1 and tokens tx
 // + 16 j; then the same rows of O, columns 4 tx + 64 j. fp32 throughout. K and V rows past the
 // sequence's end or on bad pages are zero in shared memory.
+// Bound by fp32 FMAs and the shared-memory reads that feed them (an operand pair a load serves 8 products);
+// an fp32 cache has no tensor-core form that keeps its 24 bits.
 template <int D>
 __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_constant__ TreeParams p,
                                                                  const void* __restrict__ kc,

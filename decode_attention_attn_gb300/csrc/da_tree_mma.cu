@@ -3,13 +3,14 @@
 //
 // One CTA an SM walks its share of 128-token KV tiles for one tile of 128 query rows (rows =
 // drafted tokens x heads of the group):
-//   S = Q K^T     tcgen05.mma 128 x 128 x D, both operands in shared memory, into TMEM (two buffers)
-//   P = 2^(S c - m)  8 warps: a thread holds one row's 64 columns of a tile, exchanges the row maximum
-//                 with the thread of the other 64, and writes P back over S in TMEM
+//   S = Q K^T     tcgen05.mma 128 x 128 x D into TMEM; K in shared memory, q there too (16-bit) or in TMEM
+//   P = 2^(S c - m)  two teams of 4 warps, a thread a row, take the tiles in turn and write P over S
 //   O += P V      tcgen05.mma 128 x D x 128 with P from TMEM and V from shared memory, O in TMEM
-// While the softmax of tile i runs, the tensor core does S of tile i + 1 and O of tile i - 1.
+// S has three buffers in TMEM (16-bit caches) or two (FP8, whose q takes the columns of the third), so that
+// the tensor core does S of later tiles and O of earlier ones while two tiles are in the softmax.
 // The maximum m is a reference that only moves when a tile exceeds it by more than 2^8, so O is
-// rescaled (a TMEM round trip) once or twice a sequence, not per tile.
+// rescaled (a TMEM round trip) once or twice a sequence, not per tile. Two teams cost one hand-over of m a
+// tile and need no exchange within a row; one team of 8 warps, two threads a row, was 14 % slower (32k).
 //
 // P enters O += P V as hi + lo, two 16-bit parts (2^-17 of a weight is lost, as in the decode step):
 // a bf16 P alone would cost as much accuracy as the bf16 output. The second product costs tensor
@@ -18,9 +19,14 @@
 // step. q enters f16 scaled by a power of two per row, exact for every element above 2^-29 of the
 // row's largest.
 //
-// What bounds it: up to 128 rows the KV stream (a 16-bit tile pair of 64 KB takes an SM 2800 cycles at
-// the HBM rate, its MMAs 1536 and its softmax about as much); above, with R row tiles the SMs read
-// every tile R times (once from HBM, then L2) and the tensor core is the bound.
+// What bounds it. 16-bit, up to 128 rows: the KV stream (64 KB of K and V a tile take an SM 2800 cycles at
+// the HBM rate, the MMAs 1536): 64 paged sequences of 512 to 8192 tokens with 3 to 12 drafted, 193 us, 6.0
+// TB/s, 90 % of a copy. With R row tiles every tile is read R times (once from HBM, then L2) and softmax and
+// MMAs are even: 64 drafted tokens over 4350 cost 356 us, 825 TFLOP/s. FP8: the chain S, softmax, O over
+// two buffers (4800 cycles for two tiles) and the conversion (2100 a tile, 192 KB through shared memory)
+// are even, whatever the rows: 8 drafted tokens 192 us (2.97 TB/s), 64 drafted tokens 356 us. A single long
+// sequence (32768 tokens, 16 drafted) takes 35 us: 20 of stream, about 6 until the first tile is there (the
+// schedule 2), the rest O's way out and the merge.
 #include <type_traits>
 
 #include "da_tree_mma.cuh"
@@ -958,18 +964,16 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
       }
     };
     // K of tile n and V of tile n - 1, which the MMAs take at about the same time, in one pass: the
-    // waits, the fence and the arrivals cost more than a tile's conversion.
+    // waits, the fence and the arrivals cost more than a tile's conversion. There is one copy of the pass and
+    // of the conversion: the warps' roles together run from more code than the instruction cache holds.
     auto pass = [&](bool k, bool v, uint32_t n, uint32_t rk, uint32_t rk_par) {
       const uint32_t i = n - 1, rv = rk ? rk - 1 : L.raw - 1, rv_par = rk ? rk_par : rk_par ^ 1;
-      if (k) {
-        wait(&rk_full[rk], rk_par);
-        wait(&k_empty[n & 1], ((n >> 1) & 1) ^ 1);
-        convert(L.rawk_off + rk * kCode, L.k_off + (n & 1) * kTile);
-      }
-      if (v) {
-        wait(&rv_full[rv], rv_par);
-        wait(&v_empty[i & 1], ((i >> 1) & 1) ^ 1);
-        convert(L.rawv_off + rv * kCode, L.v_off + (i & 1) * kTile);
+#pragma unroll 1
+      for (int s = k ? 0 : 1; s < (v ? 2 : 1); ++s) {
+        wait(s ? &rv_full[rv] : &rk_full[rk], s ? rv_par : rk_par);
+        wait(s ? &v_empty[i & 1] : &k_empty[n & 1], (((s ? i : n) >> 1) & 1) ^ 1);
+        convert(s ? L.rawv_off + rv * kCode : L.rawk_off + rk * kCode,
+                s ? L.v_off + (i & 1) * kTile : L.k_off + (n & 1) * kTile);
       }
       fence_async_smem();
       __syncwarp();
@@ -986,9 +990,11 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
     };
     static_assert(!kFp8 || (L.nk == 2 && L.nv == 2), "");
     uint32_t n = 0, rk = 0, rk_par = 0;
-    while (c.advance(p, sh)) {
-      if (c.first()) {
-        if (n) pass(false, true, n, rk, rk_par);   // the piece before is done with first
+    bool more = c.advance(p, sh), left = false;   // left: V of tile n - 1 is to come
+    while (more || left) {
+      // a piece's first tile: the V that is left goes ahead, alone, then q
+      const bool take = more && !(left && c.first());
+      if (take && c.first()) {
         // q: a thread's row as f16 times a power of two, so that its largest element lies in
         // [2^14, 2^15), into TMEM
         const int qb = c.piece & 1, rr = cw * 32 + lane, r = sh.row_tile * kTreeRows + rr;
@@ -1047,14 +1053,15 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[qb]);
-        pass(true, false, n, rk, rk_par);
-      } else {
-        pass(true, true, n, rk, rk_par);
       }
-      if (++rk == (uint32_t)L.raw) rk = 0, rk_par ^= 1;
-      ++n;
+      pass(take, left, n, rk, rk_par);
+      left = take;
+      if (take) {
+        if (++rk == (uint32_t)L.raw) rk = 0, rk_par ^= 1;
+        ++n;
+        more = c.advance(p, sh);
+      }
     }
-    if (n) pass(false, true, n, rk, rk_par);
   }
   __syncwarp();
   tc_fence_before();

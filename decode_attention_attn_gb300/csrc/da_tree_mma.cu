@@ -607,27 +607,12 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
               if constexpr (kSplit) tmem_st32(s_addr + h * 32, pk);
               else tmem_st16(s_addr + h * 32, pk);
             };
-            float xa[32];
-            if constexpr (kFp8) {   // (loading ahead measured 6 % slower beside the converters)
 #pragma unroll 1
-              for (int h = 0; h < 4; ++h) {
-                tmem_ld32(s_addr + h * 32, reinterpret_cast<uint32_t*>(xa));
-                tmem_ready(xa);
-                weigh(xa, h);
-              }
-            } else {
-              float xb[32];   // the next 32 columns are on their way while these are weighed
-              tmem_ld32(s_addr, reinterpret_cast<uint32_t*>(xa));
-              tmem_ready(xa);
-#pragma unroll 1
-              for (int h = 0; h < 4; h += 2) {
-                tmem_ld32(s_addr + (h + 1) * 32, reinterpret_cast<uint32_t*>(xb));
-                weigh(xa, h);
-                tmem_ready(xb);
-                if (h == 0) tmem_ld32(s_addr + 64, reinterpret_cast<uint32_t*>(xa));
-                weigh(xb, h + 1);
-                tmem_ready(xa);
-              }
+            for (int h = 0; h < 4; ++h) {   // (columns loaded ahead, in two copies of this, were no faster)
+              float x[32];
+              tmem_ld32(s_addr + h * 32, reinterpret_cast<uint32_t*>(x));
+              tmem_ready(x);
+              weigh(x, h);
             }
             float a, b;
             f2_unpack(f2_add(sum[0], sum[1]), a, b);

@@ -9,8 +9,8 @@
 // S has three buffers in TMEM (16-bit caches) or two (FP8, whose q takes the columns of the third), so that
 // the tensor core does S of later tiles and O of earlier ones while two tiles are in the softmax.
 // The maximum m is a reference that only moves when a tile exceeds it by more than 2^8, so O is
-// rescaled (a TMEM round trip) once or twice a sequence, not per tile. Two teams cost one hand-over of m a
-// tile and need no exchange within a row; one team of 8 warps, two threads a row, was 14 % slower (32k).
+// rescaled (a TMEM round trip) once or twice a sequence, not per tile. A thread holds a whole row, so a tile
+// needs no exchange within a row, only the hand-over of m from team to team.
 //
 // P enters O += P V as hi + lo, two 16-bit parts (2^-17 of a weight is lost, as in the decode step):
 // a bf16 P alone would cost as much accuracy as the bf16 output. The second product costs tensor
@@ -20,13 +20,13 @@
 // row's largest.
 //
 // What bounds it. 16-bit, up to 128 rows: the KV stream (64 KB of K and V a tile take an SM 2800 cycles at
-// the HBM rate, the MMAs 1536): 64 paged sequences of 512 to 8192 tokens with 3 to 12 drafted, 193 us, 6.0
-// TB/s, 90 % of a copy. With R row tiles every tile is read R times (once from HBM, then L2) and softmax and
-// MMAs are even: 64 drafted tokens over 4350 cost 356 us, 825 TFLOP/s. FP8: the chain S, softmax, O over
-// two buffers (4800 cycles for two tiles) and the conversion (2100 a tile, 192 KB through shared memory)
-// are even, whatever the rows: 8 drafted tokens 192 us (2.97 TB/s), 64 drafted tokens 356 us. A single long
-// sequence (32768 tokens, 16 drafted) takes 35 us: 20 of stream, about 6 until the first tile is there (the
-// schedule 2), the rest O's way out and the merge.
+// the HBM rate, the MMAs 1536): 64 paged sequences of 512 to 8192 tokens with 3 to 12 drafted, 196 us, 5.9
+// TB/s, 88 % of a copy. With R row tiles every tile is read R times (once from HBM, then L2) and softmax and
+// MMAs are even: 64 drafted tokens over 64 x 4350 cost 352 us, 836 TFLOP/s. FP8: the chain S, softmax, O over
+// two buffers (4800 cycles for two tiles), the conversion (192 KB a tile through shared memory) and the
+// fetching of instructions for the many roles are even, whatever the rows: 8 drafted tokens 170 us (3.4
+// TB/s), 64 drafted tokens 335 us (879 TFLOP/s). A single long sequence (32768 tokens, 16 drafted) takes 35
+// us: 20 of stream, about 6 until the first tile is there (the schedule 2), the rest O's way out and the merge.
 #include <type_traits>
 
 #include "da_tree_mma.cuh"

@@ -75,10 +75,6 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, const TreeRaw& 
   return s;
 }
 
-__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
-  return tree_seq(p, tree_raw(p, b));
-}
-
 // The drafted tokens that drafted token i of T attends to, from its mask word (no mask: a chain).
 __device__ __forceinline__ unsigned long long tree_clip(const TreeParams& p, unsigned long long word,
                                                         int i, int T) {
@@ -94,14 +90,14 @@ struct TreeShare {
   int b0;              // the sequence that u0 lies in
   int row_tile, row_tiles, head, heads, owner, owners, units;
   int blocks;          // blocks of heads
-  TreeRaw raw, ahead;  // sequences b0 and b0 + 1
+  TreeRaw raw;         // sequence b0
 };
 
 struct TreeScratch {   // shared memory of tree_schedule
   int warp_sum[32];
   int warp_max[32];
   int base, b0;
-  TreeRaw raw, ahead;
+  TreeRaw raw;
 };
 
 __device__ __forceinline__ int tree_share_begin(int o, int W, int P, int narrow) {
@@ -131,8 +127,10 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
   const int first = min(tid * per, p.c.batch), last = min(first + per, p.c.batch);
   int sum = 0, most = 1;
   bool bad = false;
+  TreeRaw raw{};   // of the run's last sequence, mostly its only one
   for (int b = first; b < last; ++b) {
-    const TreeSeq s = tree_seq(p, b);
+    raw = tree_raw(p, b);
+    const TreeSeq s = tree_seq(p, raw);
     sum += s.tiles;
     most = max(most, (s.T * p.group + p.tile_rows - 1) / p.tile_rows);
     bad |= s.bad;
@@ -177,13 +175,12 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
     if (pre * blocks <= sh.u0 && sh.u0 < (pre + sum) * blocks) {   // exactly one thread
       int at = pre;
       for (int b = first; b < last; ++b) {
-        const TreeRaw raw = tree_raw(p, b);
+        if (per > 1) raw = tree_raw(p, b);
         const int t = tree_seq(p, raw).tiles;
         if (sh.u0 < (at + t) * blocks) {
           sc.b0 = b;
           sc.base = at * blocks;
           sc.raw = raw;
-          sc.ahead = tree_raw(p, min(b + 1, p.c.batch - 1));
           break;
         }
         at += t;
@@ -195,7 +192,6 @@ __device__ __forceinline__ TreeShare tree_schedule(const TreeParams& p, TreeScra
     sh.b0 = sc.b0;
     sh.base = sc.base;
     sh.raw = sc.raw;
-    sh.ahead = sc.ahead;
   }
   sh.units = units;
   return sh;
@@ -218,7 +214,7 @@ struct TreeWalk {
       : u(sh.u0), base(sh.base), b(sh.b0) {
     if (sh.u1 > sh.u0) {
       s = tree_seq(p, sh.raw);
-      ahead = sh.ahead;
+      ahead = tree_raw(p, min(b + 1, p.c.batch - 1));
     }
   }
   __device__ __forceinline__ bool next(const TreeParams& p, const TreeShare& sh) {

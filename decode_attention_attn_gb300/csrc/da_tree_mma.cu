@@ -24,8 +24,8 @@
 // TB/s, 88 % of a copy. With R row tiles every tile is read R times (once from HBM, then L2) and softmax and
 // MMAs are even: 64 drafted tokens over 64 x 4350 cost 352 us, 836 TFLOP/s. FP8: the chain S, softmax, O over
 // two buffers (4800 cycles for two tiles), the conversion (192 KB a tile through shared memory) and the
-// fetching of instructions for the many roles are even, whatever the rows: 8 drafted tokens 170 us (3.4
-// TB/s), 64 drafted tokens 335 us (879 TFLOP/s). A single long sequence (32768 tokens, 16 drafted) takes 35
+// fetching of instructions for the many roles are even, whatever the rows: 8 drafted tokens 167 us (3.4
+// TB/s), 64 drafted tokens 332 us (886 TFLOP/s). A single long sequence (32768 tokens, 16 drafted) takes 35
 // us: 20 of stream, about 6 until the first tile is there (the schedule 2), the rest O's way out and the merge.
 #include <type_traits>
 

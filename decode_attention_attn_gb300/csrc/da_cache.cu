@@ -50,7 +50,8 @@ struct RowParams {
 };
 
 // 32 bytes a lane (aligned to 32): neighbouring lanes then fill whole sectors in one instruction,
-// where two 16-byte accesses 32 bytes apart touch each sector twice.
+// where two 16-byte accesses 32 bytes apart touch each sector twice (1.7 GB read back from FP8, 8 items a lane:
+// 266 us, 340 with 16-byte stores; a rotary gradient 26.7, 27.4; a plain write of 134 MB 23.1, 24.0).
 __device__ __forceinline__ void load32(const void* p, uint4& a, uint4& b) {
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
@@ -382,7 +383,7 @@ int launch_rows(RowParams& p, int head_dim, int es, bool vec, const void* fn,
   p.head_lanes = kRowThreads / p.units;
   const int heads = p.hq + 2 * p.hkv;
   // A block per row; where rows are few, a row's heads are spread over more blocks (at least one
-  // pass of heads each), up to two blocks an SM.
+  // pass of heads each), up to two blocks an SM (64 rows of 64 heads, or 1 of 128: 4.1 us, one block a row 6.2).
   const int passes = (heads + p.head_lanes - 1) / p.head_lanes;
   int slices = 1;
   while (slices < passes && (long long)p.rows * slices < 2 * 152) ++slices;
@@ -423,8 +424,8 @@ constexpr int kReadThreads = 256;
 // rows these touch, one row a lane, and pass the cache rows on by shuffles. They are at most 32: a
 // row of 8 items divides the 256 of PER = 8, one of 9 and more spans at most 30 rows, and shorter
 // ones (4 items: one tensor, one head of 64 codes) take PER = 2.
-// Bound by HBM: 64 sequences of 512 to 8192 FP8 tokens to bf16 (1.7 GB) 267 us, 6.4 TB/s; a warp a row,
-// with its lookup ahead of its loads, took 346.
+// Bound by HBM: 64 sequences of 512 to 8192 FP8 tokens to bf16 (1.7 GB) 244 us, 7.0 TB/s (rows that repeat
+// across calls stay in L2 in part); a warp a row, with its lookup ahead of its loads, took 346.
 template <typename T, typename C, int PER>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
   constexpr bool kFp8 = std::is_same<C, fp8e4m3>::value;
@@ -492,9 +493,10 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
 
 template <typename T, typename C>
 const void* read_kernel_for(int per) {
-  return per == 2   ? reinterpret_cast<const void*>(&read_kernel<T, C, 2>)
-         : per == 4 ? reinterpret_cast<const void*>(&read_kernel<T, C, 4>)
-                    : reinterpret_cast<const void*>(&read_kernel<T, C, 8>);
+  if (per == 2) return reinterpret_cast<const void*>(&read_kernel<T, C, 2>);
+  if constexpr (!std::is_same<C, fp8e4m3>::value)
+    if (per == 8) return reinterpret_cast<const void*>(&read_kernel<T, C, 8>);
+  return reinterpret_cast<const void*>(&read_kernel<T, C, 4>);
 }
 
 // Checks that the write and the read share; the status word when a workspace is given.
@@ -745,8 +747,10 @@ int decode_attn_kv_read(const da_plan* plan, const da_kv_read_args* args) {
   p.chunk_magic = (unsigned)(((1ull << 32) + p.chunks - 1) / p.chunks);
   p.items = (long long)p.rows * p.row_items;
   p.wide = aligned(a.k_out, 32) && aligned(a.v_out, 32);
-  // items a lane: more loads in flight where there are enough items to fill the GPU's warps
-  const int per = p.row_items < 8 ? 2 : p.items >= (1ll << 21) ? 8 : 4;
+  // Items a lane. FP8: 4 (1.7 GB to bf16: 244 us, with 8, whose results take twice the registers, 266).
+  // Plain copies: 8 where there are enough items to fill the GPU's warps (2.1 GB of bf16: 325 us, with 4
+  // 331; 33 MB: 8.2 us, with 4 6.2).
+  const int per = p.row_items < 8 ? 2 : !pr.kv_fp8 && p.items >= (1ll << 21) ? 8 : 4;
   const long long per_block = (long long)kReadThreads * per;
   const long long blocks = (p.items + per_block - 1) / per_block;
   if (blocks >= (1ll << 31)) return DA_ERR_UNSUPPORTED;

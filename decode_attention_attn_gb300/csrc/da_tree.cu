@@ -48,7 +48,8 @@ struct CoreSmem {
 // + 16 j; then the same rows of O, columns 4 tx + 64 j. fp32 throughout. K and V rows past the
 // sequence's end or on bad pages are zero in shared memory.
 // Bound by fp32 FMAs and the shared-memory reads that feed them (an operand pair a load serves 8 products);
-// an fp32 cache has no tensor-core form that keeps its 24 bits.
+// an fp32 cache has no tensor-core form that keeps its 24 bits. 8 sequences of 4350 tokens with 8 drafted: 270
+// us, 17 TFLOP/s, 1.1 TB/s; with 1 drafted token (4 of the tile's 32 rows) 263.
 template <int D>
 __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_constant__ TreeParams p,
                                                                  const void* __restrict__ kc,

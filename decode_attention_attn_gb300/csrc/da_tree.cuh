@@ -109,7 +109,8 @@ __device__ __forceinline__ int tree_owner(int u, int W, int P, int narrow) {
                 : (int)((((long long)u + 1) * P - 1) / W);
 }
 
-// Heads that an owner takes side by side: as many as leave at most 5 % of the CTAs without an owner.
+// Heads that an owner takes side by side: as many as leave at most 5 % of the CTAs without an owner (64
+// sequences of 4350 FP8 tokens, 8 drafted: 168 us with 8 heads, 189 with one; bf16 the same within 1 %).
 inline int tree_heads(int ctas, int row_tiles, int hkv) {
   for (int h = hkv; h > 1; --h)
     if (h < 256 && hkv % h == 0 && ctas / (row_tiles * h) * (row_tiles * h) * 20 >= ctas * 19)

@@ -424,8 +424,8 @@ constexpr int kReadThreads = 256;
 // rows these touch, one row a lane, and pass the cache rows on by shuffles. They are at most 32: a
 // row of 8 items divides the 256 of PER = 8, one of 9 and more spans at most 30 rows, and shorter
 // ones (4 items: one tensor, one head of 64 codes) take PER = 2.
-// Bound by HBM: 64 sequences of 512 to 8192 FP8 tokens to bf16 (1.7 GB) 244 us, 7.0 TB/s (rows that repeat
-// across calls stay in L2 in part); a warp a row, with its lookup ahead of its loads, took 346.
+// Bound by HBM: 64 sequences of 512 to 8192 FP8 tokens to bf16 (1.7 GB) 244 us, 7.0 TB/s (a plain
+// copy: 6.7); a warp a row, with its lookup ahead of its loads, took 346.
 template <typename T, typename C, int PER>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
   constexpr bool kFp8 = std::is_same<C, fp8e4m3>::value;

@@ -44,6 +44,19 @@ struct CoreSmem {
   TreeScratch sched;
 };
 
+// 16 bytes from global to shared memory, in the background; zeros where `valid` is false (src is then not
+// read).
+__device__ __forceinline__ void copy16_async(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {   // all but the N youngest groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // A 32 x 64 tile of logits by 256 threads: thread (ty, tx) holds rows 2 ty, 2 ty + 1 and tokens tx
 // + 16 j; then the same rows of O, columns 4 tx + 64 j. fp32 throughout. K and V rows past the
 // sequence's end or on bad pages are zero in shared memory.
@@ -92,57 +105,54 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
       const int i = rr / G;
       word[a] = rr < R ? tree_clip(p, p.mask ? __ldg(p.mask + w.s.row0 + i) : 0ull, i, w.s.T) : 0ull;
     }
+    const bool busy = r0 + 4 * (tid >> 5) < R;   // the warp's four rows: where there are none it only copies
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float o[2][NC][4] = {};
-    for (int kt = w.t0; kt < w.t1; ++kt) {
-      __syncthreads();
-      // K and V tile: 16-byte chunks of a cache row; a quarter of the block takes a row at a time
-      constexpr int EPC = 4;
-      constexpr int CH = D / EPC;
-      for (int i = tid; i < kCoreTokens * CH; i += kCoreThreads) {
-        const int j = i / CH, c = i % CH;
-        const int t = kt * kCoreTokens + j;
-        int z = -1;
-        if (t < w.s.n) {
-          const int entry = p.c.paged ? __ldg(p.c.block_table + (long long)w.b * p.c.max_blocks +
-                                              t / p.c.page_size)
-                                      : 0;
-          z = token_row(p.c, w.b, t, entry);
-          if (z < 0) atomicOr(p.c.status, kStatusBadBlockTable);
-        }
-        uint4 ck = make_uint4(0u, 0u, 0u, 0u), cv = ck;
-        if (z >= 0) {
-          const long long at = ((long long)z * p.c.hkv + w.kvh) * CH + c;
-          ck = __ldg(reinterpret_cast<const uint4*>(kc) + at);
-          cv = __ldg(reinterpret_cast<const uint4*>(vc) + at);
-        }
-        float fk[EPC], fv[EPC];
-        Elem<float>::to_f32(ck, fk);
-        Elem<float>::to_f32(cv, fv);
-        if (t >= w.s.ctx) {
-          // a drafted token may be hidden from some rows: its infinities and NaN must not reach
-          // them as 0 * inf; they are set aside and added to the rows that see the token
-          bool odd = false;
-#pragma unroll
-          for (int e = 0; e < EPC; ++e)
-            if (!isfinite(fv[e])) {
-              odd = true;
-              fv[e] = 0.f;
-            }
-          if (odd) atomicOr(&sm.odd, 1ull << ((t - w.s.ctx) & 63));
-        }
-#pragma unroll
-        for (int e = 0; e < EPC; ++e) {
-          sm.k[j * QS + c * EPC + e] = fk[e];
-          sm.v[j * D + c * EPC + e] = fv[e];
-        }
+    // A warp copies kCoreTokens / 8 rows of a tile; a lane looks one of them up. K of the next tile is on
+    // its way from the end of S on, V from the end of O on.
+    constexpr int kRows = kCoreTokens / 8, CH = D / 4;
+    const int lane = tid & 31, j0 = (tid >> 5) * kRows;
+    int z = -1;   // cache row of tile row j0 + lane
+    auto lookup = [&](int kt) {
+      const int t = kt * kCoreTokens + j0 + lane;
+      z = -1;
+      if (lane < kRows && t < w.s.n) {
+        const int entry = p.c.paged ? __ldg(p.c.block_table + (long long)w.b * p.c.max_blocks +
+                                            t / p.c.page_size)
+                                    : 0;
+        z = token_row(p.c, w.b, t, entry);
+        if (z < 0) atomicOr(p.c.status, kStatusBadBlockTable);
       }
+    };
+    // calls f(tile row, 16-byte chunk, cache row) for what this thread copies
+    auto mine_of_tile = [&](auto f) {
+#pragma unroll
+      for (int n = 0; n < kRows * CH / 32; ++n) {
+        const int r = n * 32 / CH + lane / CH;
+        f(j0 + r, lane % CH, __shfl_sync(0xffffffffu, z, r));
+      }
+    };
+    auto load = [&](const void* src, float* dst, int stride) {
+      mine_of_tile([&](int jr, int c, int zr) {
+        copy16_async(dst + jr * stride + c * 4,
+                     static_cast<const uint4*>(src) + (zr < 0 ? 0ll : ((long long)zr * p.c.hkv + w.kvh) * CH + c),
+                     zr >= 0);
+      });
+    };
+    lookup(w.t0);
+    __syncthreads();   // the piece before has been read
+    load(kc, sm.k, QS);
+    copies_commit();
+    load(vc, sm.v, D);
+    copies_commit();
+    for (int kt = w.t0; kt < w.t1; ++kt) {
+      copies_wait<1>();   // K
       __syncthreads();
       float s[2][4] = {};
       const float4* q0 = reinterpret_cast<const float4*>(sm.q + (2 * ty) * QS);
       const float4* q1 = reinterpret_cast<const float4*>(sm.q + (2 * ty + 1) * QS);
 #pragma unroll 4
-      for (int c = 0; c < D / 4; ++c) {
+      for (int c = 0; c < (busy ? D / 4 : 0); ++c) {
         const float4 a = q0[c], b = q1[c];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -151,39 +161,69 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
           s[1][j] += b.x * k.x + b.y * k.y + b.z * k.z + b.w * k.w;
         }
       }
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        float mx = m[a];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = kt * kCoreTokens + tx + 16 * j;
-          const bool seen = t < w.s.ctx || (t < w.s.n && (word[a] >> (t - w.s.ctx) & 1ull));
-          s[a][j] = seen ? s[a][j] * p.qscale : -INFINITY;
-          mx = fmaxf(mx, s[a][j]);
-        }
-#pragma unroll
-        for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        const float f = exp2f(m[a] - ref);
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float e = exp2f(s[a][j] - ref);
-          sum += e;
-          sm.p[(2 * ty + a) * PS + tx + 16 * j] = e;
-        }
-#pragma unroll
-        for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        l[a] = l[a] * f + sum;
-        m[a] = mx;
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[a][c][e] *= f;
+      __syncthreads();
+      const int z_now = z;
+      if (kt + 1 < w.t1) {
+        lookup(kt + 1);
+        load(kc, sm.k, QS);
       }
-      __syncwarp();   // a row's 16 threads are in one warp
+      copies_commit();
+      if (busy) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          float mx = m[a];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int t = kt * kCoreTokens + tx + 16 * j;
+            const bool seen = t < w.s.ctx || (t < w.s.n && (word[a] >> (t - w.s.ctx) & 1ull));
+            s[a][j] = seen ? s[a][j] * p.qscale : -INFINITY;
+            mx = fmaxf(mx, s[a][j]);
+          }
+#pragma unroll
+          for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+          const float ref = mx == -INFINITY ? 0.f : mx;
+          const float f = exp2f(m[a] - ref);
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float e = exp2f(s[a][j] - ref);
+            sum += e;
+            sm.p[(2 * ty + a) * PS + tx + 16 * j] = e;
+          }
+#pragma unroll
+          for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          l[a] = l[a] * f + sum;
+          m[a] = mx;
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[a][c][e] *= f;
+        }
+      }
+      copies_wait<1>();   // V
+      if ((kt + 1) * kCoreTokens > w.s.ctx) {
+        // a drafted token may be hidden from some rows: its infinities and NaN must not reach
+        // them as 0 * inf; they are set aside and added to the rows that see the token
+        const int z_next = z;
+        z = z_now;
+        mine_of_tile([&](int jr, int c, int zr) {
+          const int t = kt * kCoreTokens + jr;
+          if (zr < 0 || t < w.s.ctx) return;
+          float* const at = sm.v + jr * D + c * 4;
+          bool odd = false;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k)
+            if (!isfinite(at[k])) {
+              odd = true;
+              at[k] = 0.f;
+            }
+          if (odd) atomicOr(&sm.odd, 1ull << ((t - w.s.ctx) & 63));
+        });
+        z = z_next;
+      }
+      __syncthreads();   // V is there, and P (a row's 16 threads are in one warp)
 #pragma unroll 2
-      for (int t = 0; t < kCoreTokens; t += 4) {
+      for (int t = 0; t < (busy ? kCoreTokens : 0); t += 4) {
         const float4 pa = *reinterpret_cast<const float4*>(sm.p + (2 * ty) * PS + t);
         const float4 pb = *reinterpret_cast<const float4*>(sm.p + (2 * ty + 1) * PS + t);
         const float a4[4] = {pa.x, pa.y, pa.z, pa.w}, b4[4] = {pb.x, pb.y, pb.z, pb.w};
@@ -202,6 +242,9 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
             o[1][c][3] += b4[e] * v.w;
           }
       }
+      __syncthreads();
+      if (kt + 1 < w.t1) load(vc, sm.v, D);
+      copies_commit();
     }
 #pragma unroll
     for (int a = 0; a < 2; ++a) {

@@ -57,12 +57,14 @@ __device__ __forceinline__ void copies_wait() {   // all but the N youngest grou
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A 32 x 64 tile of logits by 256 threads: thread (ty, tx) holds rows 2 ty, 2 ty + 1 and tokens tx
-// + 16 j; then the same rows of O, columns 4 tx + 64 j. fp32 throughout. K and V rows past the
+// A 32 x 64 tile of logits by 8 warps of 4 rows each: a lane holds its warp's rows at tokens lane and lane +
+// 32 (what is read of q is the same for all lanes, what is read of K serves 4 rows); then the same rows of O at
+// D / 32 columns. fp32 throughout. K and V rows past the
 // sequence's end or on bad pages are zero in shared memory.
-// Bound by fp32 FMAs and the shared-memory reads that feed them (an operand pair a load serves 8 products);
-// an fp32 cache has no tensor-core form that keeps its 24 bits. 8 sequences of 4350 tokens with 8 drafted: 270
-// us, 17 TFLOP/s, 1.1 TB/s; with 1 drafted token (4 of the tile's 32 rows) 263.
+// Bound by the shared-memory reads that feed the FMAs (16-byte reads, 4 wavefronts each: S takes 6 for 32 packed
+// FMAs, O 8 for 32); an fp32 cache has no tensor-core form that keeps its 24 bits. 8 sequences of 4350 tokens,
+// 32/8 heads, 8 drafted (32 rows): 184 us, 25 TFLOP/s, 1.6 TB/s; with 1 drafted token (4 rows) 98 us, 2.9 TB/s.
+// Lanes of 2 rows x 4 tokens, with twice the reads of K: 205 and 92.
 template <int D>
 __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_constant__ TreeParams p,
                                                                  const void* __restrict__ kc,
@@ -71,8 +73,9 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
   using Smem = CoreSmem<D>;
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   constexpr int QS = Smem::kStride, PS = kCoreTokens + 4;
-  constexpr int NC = D / 64;                   // float4 columns of O per row
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  constexpr int NR = 4, NC = D / 32;           // rows a warp, columns of O a lane
+  using Vec = std::conditional_t<NC == 4, ulonglong2, f32x2>;
+  const int tid = threadIdx.x, lane = tid & 31, row0 = (tid >> 5) * NR;
   const int G = p.group;
   pdl_wait();
   pdl_launch_dependents();   // the merge's launch runs beside this kernel; it waits for its end
@@ -96,22 +99,21 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
       }
       sm.q[r * QS + d] = x;
     }
-    unsigned long long word[2];
-    int mine[2];
+    unsigned long long word[NR];
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      const int rr = r0 + 2 * ty + a;
-      mine[a] = rr < R ? rr : -1;
-      const int i = rr / G;
+    for (int a = 0; a < NR; ++a) {
+      const int rr = r0 + row0 + a, i = rr / G;
       word[a] = rr < R ? tree_clip(p, p.mask ? __ldg(p.mask + w.s.row0 + i) : 0ull, i, w.s.T) : 0ull;
     }
-    const bool busy = r0 + 4 * (tid >> 5) < R;   // the warp's four rows: where there are none it only copies
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[2][NC][4] = {};
+    const bool busy = r0 + row0 < R;   // a warp without rows only copies
+    float m[NR], l[NR];
+    f32x2 o2[NR][NC / 2] = {};   // pairs of columns
+#pragma unroll
+    for (int a = 0; a < NR; ++a) m[a] = -INFINITY, l[a] = 0.f;
     // A warp copies kCoreTokens / 8 rows of a tile; a lane looks one of them up. K of the next tile is on
     // its way from the end of S on, V from the end of O on.
     constexpr int kRows = kCoreTokens / 8, CH = D / 4;
-    const int lane = tid & 31, j0 = (tid >> 5) * kRows;
+    const int j0 = (tid >> 5) * kRows;
     int z = -1;   // cache row of tile row j0 + lane
     auto lookup = [&](int kt) {
       const int t = kt * kCoreTokens + j0 + lane;
@@ -148,17 +150,18 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
     for (int kt = w.t0; kt < w.t1; ++kt) {
       copies_wait<1>();   // K
       __syncthreads();
-      float s[2][4] = {};
-      const float4* q0 = reinterpret_cast<const float4*>(sm.q + (2 * ty) * QS);
-      const float4* q1 = reinterpret_cast<const float4*>(sm.q + (2 * ty + 1) * QS);
+      f32x2 s2[NR][2] = {};   // sums over even and over odd d
 #pragma unroll 4
       for (int c = 0; c < (busy ? D / 4 : 0); ++c) {
-        const float4 a = q0[c], b = q1[c];
+        const ulonglong2 k0 = reinterpret_cast<const ulonglong2*>(sm.k + lane * QS)[c];
+        const ulonglong2 k1 = reinterpret_cast<const ulonglong2*>(sm.k + (lane + 32) * QS)[c];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 k = reinterpret_cast<const float4*>(sm.k + (tx + 16 * j) * QS)[c];
-          s[0][j] += a.x * k.x + a.y * k.y + a.z * k.z + a.w * k.w;
-          s[1][j] += b.x * k.x + b.y * k.y + b.z * k.z + b.w * k.w;
+        for (int a = 0; a < NR; ++a) {
+          const ulonglong2 q = reinterpret_cast<const ulonglong2*>(sm.q + (row0 + a) * QS)[c];
+          f2_fma(s2[a][0], q.x, k0.x);
+          f2_fma(s2[a][1], q.x, k1.x);
+          f2_fma(s2[a][0], q.y, k0.y);
+          f2_fma(s2[a][1], q.y, k1.y);
         }
       }
       __syncthreads();
@@ -170,34 +173,34 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
       copies_commit();
       if (busy) {
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          float mx = m[a];
+        for (int a = 0; a < NR; ++a) {
+          float mx = m[a], s[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int t = kt * kCoreTokens + tx + 16 * j;
+          for (int j = 0; j < 2; ++j) {
+            float even, odd;
+            f2_unpack(s2[a][j], even, odd);
+            const int t = kt * kCoreTokens + lane + 32 * j;
             const bool seen = t < w.s.ctx || (t < w.s.n && (word[a] >> (t - w.s.ctx) & 1ull));
-            s[a][j] = seen ? s[a][j] * p.qscale : -INFINITY;
-            mx = fmaxf(mx, s[a][j]);
+            s[j] = seen ? (even + odd) * p.qscale : -INFINITY;
+            mx = fmaxf(mx, s[j]);
           }
 #pragma unroll
-          for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+          for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
           const float ref = mx == -INFINITY ? 0.f : mx;
           const float f = exp2f(m[a] - ref);
           float sum = 0.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float e = exp2f(s[a][j] - ref);
+          for (int j = 0; j < 2; ++j) {
+            const float e = exp2f(s[j] - ref);
             sum += e;
-            sm.p[(2 * ty + a) * PS + tx + 16 * j] = e;
+            sm.p[(row0 + a) * PS + lane + 32 * j] = e;
           }
 #pragma unroll
-          for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
           l[a] = l[a] * f + sum;
           m[a] = mx;
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[a][c][e] *= f;
+          for (int c = 0; c < NC / 2; ++c) o2[a][c] = f2_mul(o2[a][c], f2_pack(f, f));
         }
       }
       copies_wait<1>();   // V
@@ -221,65 +224,60 @@ __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_co
         });
         z = z_next;
       }
-      __syncthreads();   // V is there, and P (a row's 16 threads are in one warp)
+      __syncthreads();   // V is there, and the warp's P
 #pragma unroll 2
       for (int t = 0; t < (busy ? kCoreTokens : 0); t += 4) {
-        const float4 pa = *reinterpret_cast<const float4*>(sm.p + (2 * ty) * PS + t);
-        const float4 pb = *reinterpret_cast<const float4*>(sm.p + (2 * ty + 1) * PS + t);
-        const float a4[4] = {pa.x, pa.y, pa.z, pa.w}, b4[4] = {pb.x, pb.y, pb.z, pb.w};
+        float pr[NR][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int a = 0; a < NR; ++a)
+          *reinterpret_cast<float4*>(pr[a]) =
+              *reinterpret_cast<const float4*>(sm.p + (row0 + a) * PS + t);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float4 v = reinterpret_cast<const float4*>(sm.v + (t + e) * D)[tx + 16 * c];
-            o[0][c][0] += a4[e] * v.x;
-            o[0][c][1] += a4[e] * v.y;
-            o[0][c][2] += a4[e] * v.z;
-            o[0][c][3] += a4[e] * v.w;
-            o[1][c][0] += b4[e] * v.x;
-            o[1][c][1] += b4[e] * v.y;
-            o[1][c][2] += b4[e] * v.z;
-            o[1][c][3] += b4[e] * v.w;
-          }
+        for (int e = 0; e < 4; ++e) {
+          f32x2 v[NC / 2];
+          *reinterpret_cast<Vec*>(v) = *reinterpret_cast<const Vec*>(sm.v + (t + e) * D + lane * NC);
+#pragma unroll
+          for (int a = 0; a < NR; ++a)
+#pragma unroll
+            for (int c = 0; c < NC / 2; ++c) f2_fma(o2[a][c], f2_pack(pr[a][e], pr[a][e]), v[c]);
+        }
       }
       __syncthreads();
       if (kt + 1 < w.t1) load(vc, sm.v, D);
       copies_commit();
     }
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      if (mine[a] < 0) continue;
+    for (int a = 0; a < NR; ++a) {
+      const int rr = r0 + row0 + a;
+      if (rr >= R) continue;
+      float o[NC];
+#pragma unroll
+      for (int c = 0; c < NC / 2; ++c) f2_unpack(o2[a][c], o[2 * c], o[2 * c + 1]);
       for (unsigned long long rest = sm.odd & word[a]; rest; rest &= rest - 1) {   // rare
         const int t = w.s.ctx + __ffsll((long long)rest) - 1;
         const int entry = p.c.paged ? __ldg(p.c.block_table + (long long)w.b * p.c.max_blocks +
                                             t / p.c.page_size)
                                     : 0;
         const int z = token_row(p.c, w.b, t, entry);
-        for (int c = 0; c < NC; ++c)
-          for (int e = 0; e < 4; ++e) {
-            const long long at = ((long long)z * p.c.hkv + w.kvh) * D + (tx + 16 * c) * 4 + e;
-            const float v = static_cast<const float*>(vc)[at];
-            if (!isfinite(v)) o[a][c][e] += v;
-          }
+        for (int c = 0; c < NC; ++c) {
+          const long long at = ((long long)z * p.c.hkv + w.kvh) * D + lane * NC + c;
+          const float v = static_cast<const float*>(vc)[at];
+          if (!isfinite(v)) o[c] += v;
+        }
       }
       const float inv = l[a] == 0.f ? 0.f : 1.f / l[a];
       const float L = l[a] == 0.f ? -INFINITY : m[a] + log2f(l[a]);
       if (w.whole) {
-        const int i = mine[a] / G, h = w.kvh * G + mine[a] % G;
-        const long long row = (long long)(w.s.row0 + i) * p.c.hq + h;
+        const long long row = (long long)(w.s.row0 + rr / G) * p.c.hq + w.kvh * G + rr % G;
         for (int c = 0; c < NC; ++c)
-          for (int e = 0; e < 4; ++e)
-            store_out(p.out, row * D + (tx + 16 * c) * 4 + e, p.c.out_dtype,
-                      o[a][c][e] * inv * p.v_scale);
-        if (p.out_lse && tx == 0) p.out_lse[row] = L * 0.69314718055994531f;
+          store_out(p.out, row * D + lane * NC + c, p.c.out_dtype, o[c] * inv * p.v_scale);
+        if (p.out_lse && lane == 0) p.out_lse[row] = L * 0.69314718055994531f;
       } else {
         const long long at =
             (long long)tree_slot(sh.owner, w.head, sh.row_tiles * sh.heads,
-                                 sh.head * sh.row_tiles + sh.row_tile) * kCoreRows + 2 * ty + a;
-        for (int c = 0; c < NC; ++c)
-          for (int e = 0; e < 4; ++e)
-            p.part_o[at * D + (tx + 16 * c) * 4 + e] = o[a][c][e] * inv;
-        if (tx == 0) p.part_l[at] = L;
+                                 sh.head * sh.row_tiles + sh.row_tile) * kCoreRows + row0 + a;
+        for (int c = 0; c < NC; ++c) p.part_o[at * D + lane * NC + c] = o[c] * inv;
+        if (lane == 0) p.part_l[at] = L;
       }
     }
   }

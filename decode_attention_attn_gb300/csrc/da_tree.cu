@@ -61,9 +61,10 @@ __device__ __forceinline__ void copies_wait() {   // all but the N youngest grou
 // 32 (what is read of q is the same for all lanes, what is read of K serves 4 rows); then the same rows of O at
 // D / 32 columns. fp32 throughout. K and V rows past the
 // sequence's end or on bad pages are zero in shared memory.
-// Bound by the shared-memory reads that feed the FMAs (16-byte reads, 4 wavefronts each: S takes 6 for 32 packed
-// FMAs, O 8 for 32); an fp32 cache has no tensor-core form that keeps its 24 bits. 8 sequences of 4350 tokens,
-// 32/8 heads, 8 drafted (32 rows): 184 us, 25 TFLOP/s, 1.6 TB/s; with 1 drafted token (4 rows) 98 us, 2.9 TB/s.
+// Bound by the shared-memory reads that feed the FMAs (7800 wavefronts in the 11500 cycles of a tile; the FMAs
+// take 4100, packed half) and the barriers between the phases; an fp32 cache has no tensor-core form that keeps
+// its 24 bits. 8 sequences of 4350 tokens, 32/8 heads, 8 drafted (32 rows): 184 us, 25 TFLOP/s, 1.6 TB/s; with 1
+// drafted token (4 rows) 98 us, 2.9 TB/s.
 // Lanes of 2 rows x 4 tokens, with twice the reads of K: 205 and 92.
 template <int D>
 __global__ void __launch_bounds__(kCoreThreads) tree_core_kernel(const __grid_constant__ TreeParams p,
@@ -591,9 +592,9 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
   }
   // Programmatic dependents of what is ahead of them set themselves up while it ends, and wait for its end
   // before they read or write anything of it. The merge is one; so is the attention kernel where a
-  // sequence's rows fit one row tile (short tree, 640 tokens: 14.3 to 11.9 us a run in a row of runs). With
-  // more row tiles the CTAs that share KV tiles have to start as neighbours, which an early launch, as SMs
-  // fall free, undoes (64 drafted tokens over FP8 pages: 430 us against 370).
+  // sequence's rows fit one row tile (short tree, 640 tokens, a run in a row of runs: 17 % less time, 11.5 us
+  // now). With more row tiles the CTAs that share KV tiles have to start as neighbours, which an early launch, as
+  // SMs fall free, undoes (64 drafted tokens over FP8 pages: 16 % more time).
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;

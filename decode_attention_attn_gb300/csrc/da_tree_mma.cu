@@ -214,7 +214,10 @@ struct Waiter {
   bool dead;
   // warp-uniform
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    if (dead) return;
+    if (dead) {
+      __syncwarp();   // (what follows a wait may need a converged warp)
+      return;
+    }
     bool ok = mbar_try_wait(bar, parity);
     if (!__all_sync(0xffffffffu, ok)) {
       const unsigned long long t0 = global_timer_ns();
@@ -685,6 +688,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
           }
           float* const l_row = exch + 256 + row;
           l_row[team * 128] = l;
+          __syncwarp();
           named_bar_sync(9 + quarter, 64);
           const float total = l_row[0] + l_row[128];
           const float inv = total == 0.f ? 0.f : 1.f / total;
@@ -706,10 +710,12 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
 #pragma unroll 1
           for (int col = team * (D / 2); col < (team + 1) * (D / 2); col += 32) {
             float o[32];
+            __syncwarp();   // rows that end in this warp's 32 leave some lanes without a store
             tmem_ld32(lane_addr + kColO + col, reinterpret_cast<uint32_t*>(o));
             tmem_ready(o);
-            if (r < 0) continue;
-            if (!whole || p.c.out_dtype == kOutF32) {
+            if (r < 0) {
+              // nothing to store
+            } else if (!whole || p.c.out_dtype == kOutF32) {
               float4* dst = reinterpret_cast<float4*>(
                   (whole ? static_cast<float*>(p.out) : p.part_o) + at * D + col);
 #pragma unroll
@@ -729,15 +735,17 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
                 dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
               }
             }
-            if (strange)   // (r >= 0)
+            if (strange && r >= 0)
               add_odd<T, D>(p, c.w.b, c.w.s.ctx, c.w.kvh, strange, v_cache, col,
                             whole ? p.out : p.part_o, at, whole ? p.c.out_dtype : (int)kOutF32);
           }
+          __syncwarp();
           tc_fence_before();
         }
         // O and `odd` have been read by everyone: the next piece may write them
         named_bar_sync(13, kTreeSoftmaxWarps * 32);
         if (tid == 0) *odd = 0;
+        __syncwarp();
         named_bar_sync(13, kTreeSoftmaxWarps * 32);
       }
       ++it;
@@ -1031,6 +1039,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
               w[4 * k + e] = pack_pair<__half>(f.x * mul, f.y * mul);
             }
           }
+          __syncwarp();   // (rows without a query load nothing)
           tmem_st32(q_addr + j * 32, w);
         }
         qexp[qb * 128 + rr] = (signed char)-s;

@@ -565,3 +565,25 @@ def test_a_speculative_step(kv):
         src = k_rows[int(lay.row_offsets[b]) + torch.tensor(keep[b])].cpu().double()
         moved = old[0][rows[first:]]
         assert ((moved - src).abs() <= src.abs() * 2.0 ** -8).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,kv", KINDS)
+@pytest.mark.parametrize("out_dtype", ["f32", None])
+@pytest.mark.parametrize("hq,new", [(4, [3, 9, 17]), (8, [1, 11, 33]), (1, [31, 47, 1])])
+def test_rows_that_fill_a_warp_in_part(dtype, kv, out_dtype, hq, new):
+    """T G off the multiples of 32, over 128 columns (several a lane to store), with drafted V values that are not
+    finite: some lanes of a warp store, some store and add, some do neither."""
+    lay = Layout([200, 0, 640], new, 1, 128, page=16, hq=hq, dtype=dtype, kv=kv, out_dtype=out_dtype)
+    kc, vc = fill_normal(lay)
+    q, words = lay.normal(lay.rows, hq, 128), random_trees(lay, lay.gen, hide=0.2)
+    clean, clean_lse, _ = run(lay, q, kc, vc, words, 0.09)
+    check(lay, clean, clean_lse, reference(lay, q, kc, vc, words, 0.09))
+    for b in range(3):
+        vc.view(-1, 1, 128)[lay.cache_row(b, lay.held[b]), 0, 70] = 0x7F if kv == "e4m3" else math.nan
+    got, lse, t = run(lay, q, kc, vc, words, 0.09)
+    sees = torch.tensor([bool(int(w) & 1) for w in words])
+    assert torch.isnan(got[sees][..., 70]).all() and torch.equal(got[~sees], clean[~sees])
+    rest = [i for i in range(128) if i != 70]
+    assert torch.equal(got[..., rest], clean[..., rest]) and torch.equal(lse, clean_lse)
+    t.check_status()

@@ -385,8 +385,9 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  // Before the kernel ahead in the stream has finished (this is its programmatic dependent): barriers,
-  // TMEM, the tensor maps, whose first use would wait for their fetch.
+  // Before the kernel ahead in the stream has finished (this may be its programmatic dependent): barriers
+  // and the tensor maps, whose first use would wait for their fetch. No TMEM: a kernel ahead that takes its
+  // own after letting its dependents go, on the same SM, would wait for this CTA's, and this CTA for its end.
   if (tid == 0) {
     if (!kFp8) prefetch_tensormap(&tmq);
     prefetch_tensormap(&tmk);
@@ -420,10 +421,9 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
     *odd = 0;
     fence_mbar_init();
   }
-  if (warp == kTreeSoftmaxWarps + 2) tmem_alloc(tmem_slot, kTmemCols);
-  tc_fence_before();
   pdl_wait();
-  pdl_launch_dependents();   // the merge's launch runs beside this kernel; it waits for its end
+  if (warp == kTreeSoftmaxWarps + 2) tmem_alloc(tmem_slot, kTmemCols);   // (beside the schedule's loads)
+  tc_fence_before();
   // the share lies in shared memory: it is looked at once a piece, and registers are short
   TreeShare& sh = *reinterpret_cast<TreeShare*>(smem + L.misc_off + 16);
   bool any;
@@ -440,6 +440,9 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   }
   __syncthreads();
   tc_fence_after();
+  // The merge's launch runs beside this kernel; it waits for its end. Only now that the CTA has its TMEM: with
+  // no merge (one CTA) the dependent is the caller's next kernel, which may take TMEM of its own.
+  pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   if (!any) {   // the whole CTA
     if (warp == kTreeSoftmaxWarps + 2) tmem_free(tmem, kTmemCols);

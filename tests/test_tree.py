@@ -587,3 +587,41 @@ def test_rows_that_fill_a_warp_in_part(dtype, kv, out_dtype, hq, new):
     rest = [i for i in range(128) if i != 70]
     assert torch.equal(got[..., rest], clean[..., rest]) and torch.equal(lse, clean_lse)
     t.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,kv", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("sms", [1, 40])
+def test_runs_among_other_tensor_core_kernels(dtype, kv, sms):
+    """Runs and matrix products in turn on one stream, called and captured: each kernel takes its tensor memory
+    once what is ahead of it has ended (with one CTA the product follows the attention kernel itself)."""
+    lay = Layout([700, 90], [8, 5], 2, 128, page=16, hq=8, dtype=dtype, kv=kv, num_sms=sms)
+    kc, vc = (c.cuda() for c in fill_normal(lay))
+    q = lay.normal(lay.rows, 8, 128).cuda()
+    place = (lay.table.cuda(), lay.row_offsets.cuda(), lay.start.cuda())
+    t = binding.TreeAttention(lay.problem, 8)
+    a = torch.randint(-2, 3, (512, 512), device="cuda").to(TORCH[dtype])
+    ref, ref_lse = t.run(q, kc, vc, *place, None, 0.1)
+    prod = a @ a
+    outs = []
+
+    def turns(n):
+        for _ in range(n):
+            outs.append((a @ a, *t.run(q, kc, vc, *place, None, 0.1)))
+
+    turns(30)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        turns(2)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        turns(4)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for p, out, lse in outs:
+        assert torch.equal(p, prod)
+        assert torch.equal(out.view(torch.int16), ref.view(torch.int16)) and torch.equal(lse, ref_lse)
+    t.check_status()

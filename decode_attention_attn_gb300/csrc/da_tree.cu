@@ -605,10 +605,7 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
   cfg.attrs = pdl;
   cfg.numAttrs = pl.max_row_tiles == 1 ? 1 : 0;
   if (uses_mma(pr)) {
-    // P as two parts: always for bf16 and f16 caches; for FP8 caches, whose P is f16, where the
-    // output is fp32
-    const void* fn = tree_mma_kernel(pr.qkv_dtype, pr.kv_fp8 != 0, pr.head_dim,
-                                     !pr.kv_fp8 || pr.out_dtype == DA_F32);
+    const void* fn = tree_mma_kernel(pr.qkv_dtype, pr.kv_fp8 != 0, pr.head_dim);
     if (!fn) return DA_ERR_UNSUPPORTED;
     p.c.box_tokens = pr.paged ? std::min(pr.page_size, kTreeTokens) : kTreeTokens;
     CUtensorMap tmq, tmk, tmv;

@@ -15,8 +15,9 @@
 // P enters O += P V as hi + lo, two 16-bit parts (2^-17 of a weight is lost, as in the decode step):
 // a bf16 P alone would cost as much accuracy as the bf16 output. The second product costs tensor
 // time only where the step is not bound by memory. FP8 caches run on f16 operands (E4M3 codes are f16
-// numbers) and take P as one f16 (2^-12) where the output is 16-bit: an eighth of a bf16 output's half
-// step. q enters f16 scaled by a power of two per row, exact for every element above 2^-29 of the
+// numbers); one f16 a weight would take 336 instead of 397 us (64 drafted, 64 x 4350 tokens; 8 drafted 167
+// instead of 222), but answer a drafted token less exactly than the decode step over the same cache, and cost
+// an f16 result as much as its own rounding. q enters f16 scaled by a power of two per row, exact for every element above 2^-29 of the
 // row's largest.
 //
 // What bounds it. 16-bit, up to 128 rows: the KV stream (64 KB of K and V a tile take an SM 2800 cycles at
@@ -144,15 +145,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 
@@ -347,7 +339,7 @@ __device__ __noinline__ void add_odd(const TreeParams& p, int b, int ctx, int kv
   }
 }
 
-template <typename T, int D, bool kSplit>
+template <typename T, int D>
 __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value), 1)
     tree_mma_kernel_t(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ CUtensorMap tmk,
@@ -584,7 +576,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
             const f32x2 f2 = f2_pack(factor, factor), neg = f2_pack(-ref, -ref);
             f32x2 sum[2] = {0ull, 0ull};
             auto weigh = [&](float* x, int h) {
-              uint32_t pk[kSplit ? 32 : 16];
+              uint32_t pk[32];
               uint32_t vis = ~0u;
               if constexpr (kTail) vis = visible(c.w.s.ctx - tok0 - h * 32, word);
 #pragma unroll
@@ -603,15 +595,12 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
                 sum[k >> 1 & 1] = f2_add(sum[k >> 1 & 1], e);
                 const uint32_t hi = pack_pair<M>(a, b);
                 pk[k / 2] = hi;
-                if constexpr (kSplit) {
-                  const float2 hf = unpack_pair<M>(hi);
-                  float da, db;
-                  f2_unpack(f2_add(e, f2_pack(-hf.x, -hf.y)), da, db);
-                  pk[16 + k / 2] = pack_pair<M>(da, db);
-                }
+                const float2 hf = unpack_pair<M>(hi);
+                float da, db;
+                f2_unpack(f2_add(e, f2_pack(-hf.x, -hf.y)), da, db);
+                pk[16 + k / 2] = pack_pair<M>(da, db);
               }
-              if constexpr (kSplit) tmem_st32(s_addr + h * 32, pk);
-              else tmem_st16(s_addr + h * 32, pk);
+              tmem_st32(s_addr + h * 32, pk);
             };
 #pragma unroll 1
             for (int h = 0; h < 4; ++h) {   // (columns loaded ahead, in two copies of this, were no faster)
@@ -904,17 +893,15 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             mma_ts(oc, pa + p_col(k), vd + k * v_step, kDescO, k != 0 || !fresh);
-          if constexpr (kSplit) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_ts(oc, pa + 16u + p_col(k), vd + k * v_step, kDescO, true);
-          }
+          for (int k = 0; k < 8; ++k)
+            mma_ts(oc, pa + 16u + p_col(k), vd + k * v_step, kDescO, true);
         } else {   // the sequence ends in this tile
           const int steps = (valid + 15) / 16;
 #pragma unroll 1
           for (int k = 0; k < steps; ++k) {
             mma_ts(oc, pa + p_col(k), vd + k * v_step, kDescO, k != 0 || !fresh);
-            if constexpr (kSplit) mma_ts(oc, pa + 16u + p_col(k), vd + k * v_step, kDescO, true);
+            mma_ts(oc, pa + 16u + p_col(k), vd + k * v_step, kDescO, true);
           }
         }
         tc_commit(&o_full[buf]);
@@ -1067,20 +1054,19 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   if (warp == kTreeSoftmaxWarps + 2) tmem_free(tmem, kTmemCols);
 }
 
-template <typename T, bool kSplit>
+template <typename T>
 const void* for_d(int D) {
-  return D == 64    ? reinterpret_cast<const void*>(&tree_mma_kernel_t<T, 64, kSplit>)
-         : D == 128 ? reinterpret_cast<const void*>(&tree_mma_kernel_t<T, 128, kSplit>)
+  return D == 64    ? reinterpret_cast<const void*>(&tree_mma_kernel_t<T, 64>)
+         : D == 128 ? reinterpret_cast<const void*>(&tree_mma_kernel_t<T, 128>)
                     : nullptr;
 }
 
 }  // namespace
 
-const void* tree_mma_kernel(int dtype, bool fp8, int head_dim, bool split) {
-  if (fp8) return split ? for_d<fp8e4m3, true>(head_dim) : for_d<fp8e4m3, false>(head_dim);
-  if (!split) return nullptr;
-  if (dtype == kOutF16) return for_d<__half, true>(head_dim);
-  if (dtype == kOutBF16) return for_d<__nv_bfloat16, true>(head_dim);
+const void* tree_mma_kernel(int dtype, bool fp8, int head_dim) {
+  if (fp8) return for_d<fp8e4m3>(head_dim);
+  if (dtype == kOutF16) return for_d<__half>(head_dim);
+  if (dtype == kOutBF16) return for_d<__nv_bfloat16>(head_dim);
   return nullptr;
 }
 

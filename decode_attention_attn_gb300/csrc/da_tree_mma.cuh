@@ -75,8 +75,7 @@ static_assert(tree_layout(64, false).total <= kSmemLimit, "");
 static_assert(tree_layout(64, true).total <= kSmemLimit, "");
 static_assert(sizeof(TreeScratch) <= 4 * 128 * 4, "the schedule's scratch lies there first");
 
-// The kernel of a cache type (da_dtype, or FP8), head_dim and output; null: not built.
-// split: P enters as the sum of two 16-bit parts.
-const void* tree_mma_kernel(int dtype, bool fp8, int head_dim, bool split);
+// The kernel of a cache type (da_dtype, or FP8) and head_dim; null: not built.
+const void* tree_mma_kernel(int dtype, bool fp8, int head_dim);
 
 }  // namespace da

@@ -625,3 +625,35 @@ def test_runs_among_other_tensor_core_kernels(dtype, kv, sms):
         assert torch.equal(p, prod)
         assert torch.equal(out.view(torch.int16), ref.view(torch.int16)) and torch.equal(lse, ref_lse)
     t.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("out_dtype", ["f16", "bf16"])
+def test_fp8_weights_keep_their_bits_under_16_bit_results(out_dtype, d):
+    """A 16-bit result over an FP8 cache is held to the fp32 bound and one rounding, as over a 16-bit cache. A few
+    tokens a row, so that the roundings of weights do not average out: where terms cancel, weights of 11 bits
+    (2^-11 of sum p |v|, 16 times REL) would show."""
+    lay = Layout([2, 3, 1, 4, 6, 0, 9, 2], [2, 3, 5, 2, 4, 3, 1, 6], 4, d, page=8, hq=16, dtype="bf16", kv="e4m3",
+                 out_dtype=out_dtype, seed=9)
+    kc, vc = fill_normal(lay)
+    q = lay.normal(lay.rows, 16, d)
+    wide = Layout(lay.held, lay.new, 4, d, page=8, hq=16, dtype="bf16", kv="e4m3", out_dtype="f32", seed=9)
+    exact, _, mag = reference(wide, q, kc, vc, None, 0.1)
+    got, _, _ = run(lay, q, kc, vc, None, 0.1)
+    tol = mag * REL
+    tol = tol + (exact.abs() + tol) * half_step(TORCH[out_dtype]) + (2.0 ** -25 if out_dtype == "f16" else 0)
+    assert ((got.double() - exact).abs() <= tol).all()
+    # (the oracle with weights rounded to one f16 breaks it)
+    G, worst = 4, 0.0
+    k_all, v_all = lay.values(kc, lay.k_scale), lay.values(vc, lay.v_scale)
+    for b, (ctx, n) in enumerate(zip(lay.held, lay.new)):
+        at = torch.tensor([lay.cache_row(b, t) for t in range(ctx + n)])
+        i = n - 1
+        r = int(lay.row_offsets[b]) + i
+        x = torch.einsum("hd,thd->ht", q[r].double(), k_all[at].repeat_interleave(G, 1)) * 0.1
+        p = (x - x.amax(-1, keepdim=True)).exp()
+        o = torch.einsum("ht,thd->hd", p.half().double(), v_all[at].repeat_interleave(G, 1)) / p.sum(-1)[:, None]
+        o = o.to(TORCH[out_dtype]).double()
+        worst = max(worst, float(((o - exact[r]).abs() / tol[r]).max()))
+    assert worst > 1

@@ -8,11 +8,12 @@
 //   O += P V      tcgen05.mma 128 x D x 128 with P from TMEM and V from shared memory, O in TMEM
 // S has three buffers in TMEM (16-bit caches) or two (FP8, whose q takes the columns of the third), so that
 // the tensor core does S of later tiles and O of earlier ones while two tiles are in the softmax.
-// The maximum m is a reference that only moves when a tile exceeds it by more than 2^8, so O is
-// rescaled (a TMEM round trip) once or twice a sequence, not per tile. A thread holds a whole row, so a tile
+// The maximum m is a reference that only moves when a tile exceeds it by a few powers of two (Reference), so O
+// is rescaled (a TMEM round trip) once or twice a sequence, not per tile. A thread holds a whole row, so a tile
 // needs no exchange within a row, only the hand-over of m from team to team.
 //
-// P enters O += P V as hi + lo, two 16-bit parts (2^-17 of a weight is lost, as in the decode step):
+// P enters O += P V as hi + lo, two 16-bit parts. bf16 loses 2^-17 of a weight, as in the decode step; f16
+// 2^-23 of it or 2^-36 of the row's largest, whichever is more:
 // a bf16 P alone would cost as much accuracy as the bf16 output. The second product costs tensor
 // time only where the step is not bound by memory. FP8 caches run on f16 operands (E4M3 codes are f16
 // numbers); one f16 a weight would take 336 instead of 397 us (64 drafted, 64 x 4350 tokens; 8 drafted 167
@@ -40,7 +41,16 @@ constexpr uint32_t kColO = 0;      // O: D columns
 constexpr uint32_t kColS = 128;    // S / P buffers of 128 columns: 3, or 2 and
 constexpr uint32_t kColQ = 384;    // FP8: two q tiles of D / 2 columns
 __host__ __device__ constexpr uint32_t s_buffers(bool fp8) { return fp8 ? 2 : 3; }
-constexpr float kRescale = 8.f;    // log2: P <= 2^8 before the reference moves
+// The reference that a row's weights are formed against, 2^(x - m): m lies kHead below the largest logit when
+// it is set, and moves when a tile exceeds that by more than kMove (both log2). bf16's exponents reach as far as
+// fp32's; f16 ends at 2^16 above and, hi and lo alike, at half a step of 2^-25 below, so its weights start at
+// 2^11 and may grow to 2^15: what a weight loses is then at most 2^-36 of the row's largest. (8 and no headroom,
+// as for bf16, would lose 2^-25: a 2^-12 of all weights 9 below one sink's logit, and all of those 18 below.)
+template <typename M>
+struct Reference {
+  static constexpr float kHead = std::is_same<M, __half>::value ? 11.f : 0.f;
+  static constexpr float kMove = std::is_same<M, __half>::value ? 4.f : 8.f;
+};
 
 // ---- TMA and tcgen05 -----------------------------------------------------------------------------
 // 5-D tiled TMA load (a cache's [heads, tokens / 8, d / 64, 8, 64] view).
@@ -456,7 +466,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
     // exponentiates one the other team reads the next. Both weigh against one reference per row, m in
     // shared memory, which belongs to O: before a tile's weights are formed its team learns that the tile
     // before has settled m (a barrier between the two warps of 32 rows, `settled`), moves it where the
-    // tile exceeds it by more than kRescale, and passes on. Row sums are kept per team, relative to the
+    // tile exceeds it by too much, and passes on. Row sums are kept per team, relative to the
     // reference its thread saw last.
     Cursor c(p, sh);
     const int team = warp >> 2, quarter = warp & 3;
@@ -534,7 +544,8 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
             }
             top = top == none ? -INFINITY : top * factor;
             if (due) named_bar_sync(settled + (team ^ 1), 64);   // the tile before has settled m
-            float now = top;
+            constexpr float kHead = Reference<M>::kHead, kMove = Reference<M>::kMove;
+            float now = top - kHead;
             if (!c.first()) {
               now = *m_row;
               if (now != m) {   // the other team moved it, or this is the team's first tile of the piece
@@ -543,9 +554,9 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
                 m = now;
               }
               float f = 1.f;
-              if (top > now + kRescale) {
-                f = fast_exp2(now - top);
-                now = top;
+              if (top > now + (kHead + kMove)) {
+                f = fast_exp2(now - (top - kHead));
+                now = top - kHead;
                 l *= f;
                 *m_row = now;
               }

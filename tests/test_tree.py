@@ -657,3 +657,40 @@ def test_fp8_weights_keep_their_bits_under_16_bit_results(out_dtype, d):
         o = o.to(TORCH[out_dtype]).double()
         worst = max(worst, float(((o - exact[r]).abs() / tol[r]).max()))
     assert worst > 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,kv", KINDS)
+@pytest.mark.parametrize("place", [0, 5000, 19999])
+@pytest.mark.parametrize("depth", [2.25, 9.0, 12.0, 18.0])
+def test_weights_far_below_a_sink(dtype, kv, place, depth):
+    """One token with V = 0 holds nearly all of the weight, 20000 others lie `depth` nats below it, in one piece:
+    their small weights make up the whole result. All are equal, so that roundings add up. f16 operands lose up to
+    half of f16's smallest step, 2^-25, of a weight that is scaled so that the row's largest is at least 2^11:
+    2^-36 of it, times sum |v|. The fp32 accumulator is rounded once for every 16 tokens and part of a weight,
+    2 n / 16 times, each time by up to 2^-23 (an accumulation may cut off) of a partial sum, which with V > 0 and
+    equal weights is at most sum p |v|: n / 8 * 2^-23 of it."""
+    n = 20000
+    lay = Layout([n - 2], [2], 1, 64, page=16, hq=2, dtype=dtype, kv=kv, k_scale=1.0, v_scale=1.0, out_dtype="f32",
+                 num_sms=1)
+    rows = torch.tensor([lay.cache_row(0, t) for t in range(n)])
+    k, v = torch.zeros(lay.shape).view(-1, 1, 64), torch.zeros(lay.shape).view(-1, 1, 64)
+    k[rows, :, 0] = -depth / 8
+    v[rows] = torch.rand(n, 1, 64, generator=lay.gen) + 0.5
+    k[rows[place], :, 0] = 0.0
+    v[rows[place]] = 0.0
+    store = torch.float8_e4m3fn if kv == "e4m3" else TORCH[dtype]
+    kc, vc = (c.to(store).view(lay.shape) for c in (k, v))
+    if kv == "e4m3":
+        kc, vc = kc.view(torch.uint8), vc.view(torch.uint8)
+    assert (k.view(-1, 64) == lay.values(kc, 1.0).view(-1, 64)).all()          # the logits are exact
+    q = torch.zeros(2, 2, 64).to(TORCH[dtype])
+    q[:, :, 0] = 8.0
+    words = torch.tensor([3, 3], dtype=torch.int64)
+    out, lse, _ = run(lay, q, kc, vc, words, 1.0)
+    ref, ref_lse, mag = reference(lay, q, kc, vc, words, 1.0)
+    mag = mag * (1 + n / 8 * 2.0 ** -23 / REL)
+    if dtype == "f16" or kv == "e4m3":
+        largest = math.exp(0.0 - float(ref_lse[0, 0]))
+        mag = mag + 2.0 ** -36 / REL * largest * lay.values(vc, 1.0).abs().sum(0)
+    check(lay, out, lse, (ref, ref_lse, mag))

@@ -549,8 +549,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
             if (!c.first()) {
               now = *m_row;
               if (now != m) {   // the other team moved it, or this is the team's first tile of the piece
-                l *= fast_exp2(m - now);
-                if (l != l) l = m == -INFINITY ? 0.f : l;
+                l *= fast_exp2(m - now);   // (0 where m was -inf: a sum of 0 stays 0, and NaN stays NaN)
                 m = now;
               }
               float f = 1.f;
@@ -686,7 +685,6 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
           const float last = *m_row;
           if (last != m) {
             l *= fast_exp2(m - last);
-            if (l != l) l = m == -INFINITY ? 0.f : l;
             m = last;
           }
           float* const l_row = exch + 256 + row;

@@ -694,3 +694,22 @@ def test_weights_far_below_a_sink(dtype, kv, place, depth):
         largest = math.exp(0.0 - float(ref_lse[0, 0]))
         mag = mag + 2.0 ** -36 / REL * largest * lay.values(vc, 1.0).abs().sum(0)
     check(lay, out, lse, (ref, ref_lse, mag))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,kv", KINDS)
+@pytest.mark.parametrize("sms", [1, 40])
+@pytest.mark.parametrize("first,last", [(0, 128), (128, 256), (300, 301), (0, 900)])
+def test_nan_in_the_context_reaches_result_and_lse(dtype, kv, sms, first, last):
+    """Keys of NaN at positions first..last - 1, a whole first tile among them: every row's out and lse are NaN,
+    however the reference moves afterwards, and another sequence's are untouched."""
+    lay = Layout([1000, 1000], [3, 3], 2, 64, page=16, hq=4, dtype=dtype, kv=kv, num_sms=sms)
+    kc, vc = fill_normal(lay)
+    q = lay.normal(lay.rows, 4, 64)
+    clean = run(lay, q, kc, vc, None, 0.3)
+    z = torch.tensor([lay.cache_row(0, t) for t in range(first, last)])
+    kc.view(-1, 2, 64)[z] = 0x7F if kv == "e4m3" else math.nan
+    out, lse, t = run(lay, q, kc, vc, None, 0.3)
+    assert torch.isnan(out[:3]).all() and torch.isnan(lse[:3]).all()
+    assert torch.equal(out[3:], clean[0][3:]) and torch.equal(lse[3:], clean[1][3:])
+    t.check_status()

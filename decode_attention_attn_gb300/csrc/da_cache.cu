@@ -45,7 +45,7 @@ struct RowParams {
   int wide_in, wide_out;        // rows read (written) lie on 32-byte boundaries
   int rotary, interleaved, transpose;
   float m;                      // attn_factor
-  float k_inv, v_inv;           // 1 / scale of an FP8 cache
+  float k_scale, v_scale;       // of an FP8 cache
   unsigned long long turn[kMaxPairs];
 };
 
@@ -205,7 +205,7 @@ __device__ __forceinline__ void store_unit(C* dst, int a0, int b0, bool joined, 
 // lookup chain (offsets, start, table) and the loads run side by side.
 //
 // Bound by HBM: the rotary of q and k with the FP8 write of 64 prompts (19k rows of 32 + 2 x 8 heads, 441 MB)
-// 78 us, 5.6 TB/s; a plain f16 write of 4096 rows of 32 heads 24.6 us, 5.5 TB/s; half-rotated interleaved
+// 86 us, 5.1 TB/s; a plain f16 write of 4096 rows of 32 heads 24.6 us, 5.5 TB/s; half-rotated interleaved
 // f16 in a gradient (8191 x 32 heads) 26.8 us, 5.0 TB/s, where 134 MB are still short beside the ramp. With
 // one row a sequence (64 rows) it is a launch: 4 to 6 us back to back.
 template <typename T, typename C, int VEC>
@@ -320,9 +320,12 @@ __global__ void __launch_bounds__(kRowThreads, 7)
       for (int i = 0; i < 2 * VEC; ++i) most = fmaxf(most, fabsf(e[i]));   // NaN passes over
     }
     if constexpr (std::is_same<C, fp8e4m3>::value) {
-      const float inv = is_k ? p.k_inv : p.v_inv;
+      // A division: next to a tie between two codes a product with 1 / scale, rounded twice, falls to the
+      // other side (30 of the 65280 bf16 values at scale 0.0075). It costs 8 of the 86 us of 64 prompts. (Products,
+      // and a division only where one lies within its error of a tie: 89 us.)
+      const float scale = is_k ? p.k_scale : p.v_scale;
 #pragma unroll
-      for (int i = 0; i < 2 * VEC; ++i) e[i] *= inv;
+      for (int i = 0; i < 2 * VEC; ++i) e[i] = __fdiv_rn(e[i], scale);
     }
     store_unit(static_cast<C*>(is_k ? p.k_cache : p.v_cache) + at, a0, b0,
                std::is_same<C, fp8e4m3>::value ? VEC > 1 && !apart : out_joined, PC::pack(e),
@@ -679,9 +682,12 @@ int decode_attn_kv_write(const da_plan* plan, const da_kv_write_args* args) {
   p.hq = a.q ? pr.num_q_heads : 0;
   p.hkv = pr.num_kv_heads;
   if (pr.kv_fp8) {
-    p.k_inv = (float)(1.0 / (double)pr.k_scale);
-    p.v_inv = (float)(1.0 / (double)pr.v_scale);
-    if (!std::isfinite(p.k_inv) || !std::isfinite(p.v_inv)) return DA_ERR_INVALID_ARG;
+    p.k_scale = pr.k_scale;
+    p.v_scale = pr.v_scale;
+    // (so small a scale stands for no stored row: its codes end below fp32's normal range)
+    if (!std::isfinite((float)(1.0 / (double)pr.k_scale)) ||
+        !std::isfinite((float)(1.0 / (double)pr.v_scale)))
+      return DA_ERR_INVALID_ARG;
   }
   const bool vec = (!a.rope || a.rope->cfg.rotary_dim % (32 / es) == 0) &&
                    vector_ok(a.q, a.q_row_stride, a.q_head_stride, es) &&

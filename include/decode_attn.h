@@ -461,9 +461,10 @@ int decode_attn_rope_apply(const da_rope* rope, const da_rope_args* args);
  *               projection's rows, for instance).
  *   k_cache,    device, as for decode_attn_run. A 16-bit or fp32 cache takes the values as
  *   v_cache     they are (a rotated k rounded once to nearest even). An FP8 cache takes E4M3
- *               codes of x * (1 / k_scale) or x * (1 / v_scale) in fp32, rounded to nearest
+ *               codes of x / k_scale or x / v_scale, an fp32 quotient rounded to nearest
  *               even, values beyond +-448 to +-448, NaN to the NaN code; a rotated k is not
- *               rounded to qkv_dtype in between.
+ *               rounded to qkv_dtype in between. (A scale whose reciprocal is no fp32 number
+ *               is refused.)
  *   block_table as for decode_attn_run. Rows of two sequences must not fall on the same token
  *               of the pool (of two rows written to one token, either may stay, in parts).
  *   rope        nullable. With it k is rotated by its row's position, and q, when given, is

@@ -577,3 +577,23 @@ def test_captured_write_and_read_follow_their_inputs():
         torch.cuda.synchronize()
         for a, b in zip((q_out, k_out, v_out, kc, vc), (*ref, ref_kc, ref_vc)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k_scale,v_scale", [(0.01171875, 0.0087890625), (0.0125, 0.0075), (3.1, 1e-20), (7e20, 1 / 3), (0.25, 2e38)])
+@pytest.mark.parametrize("aligned", [True, False])
+def test_codes_are_those_of_the_fp32_quotient(k_scale, v_scale, aligned):
+    """Every bf16 value of +-480 scales and less: the codes of x / scale in fp32, next to ties between two codes
+    too, where a product with the rounded reciprocal falls to the other side."""
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).float()
+    x = x[torch.isfinite(x)]
+    lay = Layout([0], [len(x) // 128], 1, 128, kv="e4m3", k_scale=k_scale, v_scale=v_scale)
+    x = x[:lay.rows * 128].view(lay.rows, 1, 128)
+    x = x.bfloat16()
+    rows = torch.zeros(lay.rows * 129 + 1, dtype=torch.bfloat16, device="cuda")
+    k = (x.cuda() if aligned else rows[1:].view(lay.rows, 1, 129)[:, :, :128].copy_(x))
+    kc, vc = (torch.zeros(lay.shape, dtype=torch.uint8, device="cuda") for _ in range(2))
+    binding.KVCacheIO(lay.problem).write(k, k, kc, vc, None, lay.row_offsets.cuda(), lay.start.cuda())
+    for c, scale in ((kc, k_scale), (vc, v_scale)):
+        want = (x.float() / torch.tensor(scale)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        assert torch.equal(c.cpu().view(want.shape), want)

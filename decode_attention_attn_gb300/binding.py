@@ -491,14 +491,49 @@ def make_problem(*, batch, num_q_heads, num_kv_heads, head_dim, qkv_dtype, out_d
 
 
 # ---- torch-facing convenience (marshalling only) -------------------------------------------
-class DecodeAttention:
+_torch = None
+
+
+def _use_torch():
+    global _torch
+    import torch
+    _torch = torch
+
+
+class _Workspace:
+    """An object with a workspace. Its memory belongs to the stream that was current when it was made; a call on
+    another stream is noted with the allocator, so that the memory goes to nobody else before that call's
+    kernels have ended, whenever the object is dropped."""
+
+    workspace = None
+
+    def _make_workspace(self, size, device):
+        """Zero-filled, which needs no init call, and ready for any stream."""
+        device = _torch.device("cuda") if device is None else _torch.device(device)
+        self.workspace = self._noted = _torch.zeros(size, dtype=_torch.uint8, device=device)
+        stream = _torch.cuda.current_stream(self.workspace.device)
+        self._noted_stream = stream.cuda_stream
+        if not _torch.cuda.is_current_stream_capturing():
+            stream.synchronize()
+
+    def _workspace_on(self, index, stream):
+        """Its address, for a call on `stream` (None: device `index`'s current one)."""
+        ws = self.workspace
+        raw = _torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+        if raw != self._noted_stream or ws is not self._noted:
+            ws.record_stream(_torch.cuda.current_stream(index) if stream is None else stream)
+            self._noted, self._noted_stream = ws, raw
+        return ws.data_ptr()
+
+
+class DecodeAttention(_Workspace):
     """A plan plus its workspace on the current CUDA device.
 
     run() takes torch tensors already on the device, passes their addresses and the
     current stream to decode_attn_run, and returns (out, lse, row_flags)."""
 
     def __init__(self, problem: da_problem, num_splits: int = 0, device=None):
-        import torch
+        _use_torch()
         self.problem = problem
         self.plan, self.workspace_bytes = decode_attn_plan(problem, num_splits)
         self.info = decode_attn_plan_info(self.plan)
@@ -506,9 +541,8 @@ class DecodeAttention:
         names = {v: k for k, v in DTYPE_CODES.items()}
         self._qkv_dtype = TORCH_DTYPES[names[problem.qkv_dtype]]
         self._out_dtype = TORCH_DTYPES[names[problem.out_dtype]]
-        self.device = torch.device(device) if device is not None else torch.device("cuda")
-        # a zero-filled workspace needs no decode_attn_workspace_init call
-        self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+        self.device = _torch.device(device) if device is not None else _torch.device("cuda")
+        self._make_workspace(self.workspace_bytes, self.device)
 
     def __del__(self):
         plan = getattr(self, "plan", None)
@@ -545,7 +579,8 @@ class DecodeAttention:
         args = da_run_args(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                            None if block_table is None else block_table.data_ptr(),
                            seq_lens.data_ptr(), float(scale), num_splits, out.data_ptr(),
-                           out_lse.data_ptr(), row_flags.data_ptr(), self.workspace.data_ptr(),
+                           out_lse.data_ptr(), row_flags.data_ptr(),
+                           self._workspace_on(q.get_device(), s),
                            self.workspace_bytes, s.cuda_stream or None,
                            ctypes.pointer(st) if st is not None else None,
                            split_events[0].cuda_event if split_events else None,
@@ -558,15 +593,6 @@ class DecodeAttention:
 
 # What a call of the wrappers below costs on the host is of the order of the kernel it launches, so torch is
 # imported once, checks look at an attribute at a time, and the argument structures are packed in one go.
-_torch = None
-
-
-def _use_torch():
-    global _torch
-    import torch
-    _torch = torch
-
-
 class _Entry:
     """A C entry point that takes (handle, structure of `args`, whose last field is the stream)."""
 
@@ -641,15 +667,6 @@ def _empty(shape, dtype, device, stream):
         return _torch.empty(shape, dtype=dtype, device=device)
     with _torch.cuda.stream(stream):
         return _torch.empty(shape, dtype=dtype, device=device)
-
-
-def _workspace(size, device):
-    """A zero-filled workspace, which needs no init call, ready for any stream."""
-    device = _torch.device("cuda") if device is None else _torch.device(device)
-    ws = _torch.zeros(size, dtype=_torch.uint8, device=device)
-    if not _torch.cuda.is_current_stream_capturing():
-        _torch.cuda.current_stream(ws.device).synchronize()
-    return ws
 
 
 class Rope:
@@ -751,7 +768,7 @@ class _Cache:
         return index, table
 
 
-class KVCacheIO:
+class KVCacheIO(_Workspace):
     """Writes rows of K and V into a cache of the problem's shape and storage, and reads them back.
 
     The rows of a step lie one after another, sequence by sequence: row_offsets (int32
@@ -765,9 +782,8 @@ class KVCacheIO:
         self.problem = problem
         self.plan, self.workspace_bytes = decode_attn_plan(problem, 0)
         self._cache = _Cache(problem)
-        self.workspace = None
         if findings or problem.validate:
-            self.workspace = _workspace(self.workspace_bytes, device)
+            self._make_workspace(self.workspace_bytes, device)
 
     def __del__(self):
         plan = getattr(self, "plan", None)
@@ -821,8 +837,8 @@ class KVCacheIO:
                         v_head, rows, k_cache.data_ptr(), v_cache.data_ptr(), table,
                         row_offsets.data_ptr(), start.data_ptr(),
                         0 if rope is None else rope.handle.value, at, q_at, out_at, q_row, q_head,
-                        out_row, out_head, most, 0 if ws is None else ws.data_ptr(),
-                        self.workspace_bytes)
+                        out_row, out_head, most,
+                        0 if ws is None else self._workspace_on(index, stream), self.workspace_bytes)
         return q_out
 
     def read(self, k_cache, v_cache, block_table, row_offsets, start, k_out, v_out, stream=None):
@@ -850,27 +866,27 @@ class KVCacheIO:
         if rows:
             self._read(self.plan, index, stream, 0 if k_cache is None else k_cache.data_ptr(),
                        0 if v_cache is None else v_cache.data_ptr(), table, row_offsets.data_ptr(),
-                       start.data_ptr(), rows, places[0], places[1], 0 if ws is None else ws.data_ptr(),
-                       self.workspace_bytes)
+                       start.data_ptr(), rows, places[0], places[1],
+                       0 if ws is None else self._workspace_on(index, stream), self.workspace_bytes)
         return k_out, v_out
 
     def check_status(self, stream=None):
         """Synchronise, then raise the first finding recorded since the last call."""
         if self.workspace is None:
             raise ValueError("made without findings")
-        _check_workspace(decode_attn_check_status, self.plan, self.workspace, stream)
+        _check_workspace(decode_attn_check_status, self, stream)
 
 
-def _check_workspace(fn, plan, workspace, stream):
-    with _torch.cuda.device(workspace.device):
+def _check_workspace(fn, of, stream):
+    with _torch.cuda.device(of.workspace.device):
         s = stream if stream is not None else _torch.cuda.current_stream()
-        fn(plan, workspace.data_ptr(), s.cuda_stream)
+        fn(of.plan, of._workspace_on(of.workspace.get_device(), s), s.cuda_stream)
 
 
-class TreeAttention:
+class TreeAttention(_Workspace):
     """Attention of drafted tokens over a cache that already holds their K and V, one tree (or
     chain) of up to max_tree tokens a sequence: a plan plus its workspace. Two runs of one object
-    must not overlap on the GPU."""
+    must not overlap on the GPU, and a captured graph needs the object as long as it is replayed."""
 
     def __init__(self, problem: da_problem, max_tree: int = MAX_TREE, device=None):
         self._run = _entry("decode_attn_tree_run", da_tree_args)
@@ -878,7 +894,7 @@ class TreeAttention:
         self.plan, self.workspace_bytes = decode_attn_tree_plan(problem, max_tree)
         self.info = decode_attn_tree_plan_info(self.plan)
         self._cache = _Cache(problem)
-        self.workspace = _workspace(self.workspace_bytes, device)
+        self._make_workspace(self.workspace_bytes, device)
         self.device = self.workspace.device
 
     def __del__(self):
@@ -921,9 +937,10 @@ class TreeAttention:
         if rows:
             self._run(self.plan, index, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                       table, row_offsets.data_ptr(), ctx_lens.data_ptr(), mask, rows, scale,
-                      out.data_ptr(), out_lse.data_ptr(), ws.data_ptr(), self.workspace_bytes)
+                      out.data_ptr(), out_lse.data_ptr(), self._workspace_on(index, stream),
+                      self.workspace_bytes)
         return out, out_lse
 
     def check_status(self, stream=None):
         """Synchronise, then raise the first finding recorded since the last call."""
-        _check_workspace(decode_attn_tree_check_status, self.plan, self.workspace, stream)
+        _check_workspace(decode_attn_tree_check_status, self, stream)

@@ -713,3 +713,45 @@ def test_nan_in_the_context_reaches_result_and_lse(dtype, kv, sms, first, last):
     assert torch.isnan(out[:3]).all() and torch.isnan(lse[:3]).all()
     assert torch.equal(out[3:], clean[0][3:]) and torch.equal(lse[3:], clean[1][3:])
     t.check_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["tree", "io", "step"])
+@pytest.mark.parametrize("given", [True, False])
+def test_a_dropped_objects_workspace_waits_for_its_last_stream(what, given):
+    """Run on a busy side stream (given, or current), then drop the object: its workspace's memory goes to nobody
+    else while the run is pending."""
+    lay = Layout([600, 70], [4, 3], 2, 64, page=16, hq=8)
+    kc, vc, q = lay.cache().cuda(), lay.cache().cuda(), lay.normal(lay.rows, 8, 64).cuda()
+    table, offs, start = lay.table.cuda(), lay.row_offsets.cuda(), lay.start.cuda()
+    rows = torch.empty(lay.rows, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q2 = q[:2].contiguous()
+    make = {"tree": lambda: binding.TreeAttention(lay.problem, 4),
+            "io": lambda: binding.KVCacheIO(lay.problem, findings=True),
+            "step": lambda: binding.DecodeAttention(lay.problem)}[what]
+
+    def call(obj, stream):
+        if what == "tree":
+            obj.run(q, kc, vc, table, offs, start, None, 0.1, stream=stream)
+        elif what == "io":
+            obj.read(kc, vc, table, offs, start, rows, rows.clone(), stream=stream)
+        else:
+            obj.run(q2, kc, vc, table, start, 0.1, stream=stream)
+
+    side = torch.cuda.Stream()
+    call(make(), side)                       # modules loaded
+    torch.cuda.synchronize()
+    for _ in range(2):                       # the second object on a stream that the first has used
+        obj = make()
+        address, size = obj.workspace.data_ptr(), obj.workspace.numel()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400_000_000)   # a fifth of a second
+            if not given:
+                call(obj, None)
+        if given:
+            call(obj, side)
+        del obj
+        taken = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        assert not side.query() and all(t.data_ptr() != address for t in taken)
+        torch.cuda.synchronize()
+        del taken

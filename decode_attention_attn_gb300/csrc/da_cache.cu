@@ -12,6 +12,7 @@
 #include <utility>
 
 #include "da_plan.h"
+#include "da_rows.h"
 
 using namespace da;
 
@@ -369,14 +370,14 @@ bool vector_ok(const void* p, long long rs, long long hs, int es, int bytes = 16
   return !p || (aligned(p, bytes) && rs * es % bytes == 0 && hs * es % bytes == 0);
 }
 
-// Whether rows written with these strides (elements) lie apart.
-bool lie_apart(long long rows, long long rs, long long heads, long long hs, long long d) {
-  if (rows > 1 && (heads == 1 || rs < hs)) {   // the smaller stride first
-    std::swap(rows, heads);
-    std::swap(rs, hs);
-  }
-  if (heads > 1 && hs < d) return false;
-  return rows <= 1 || rs >= (heads - 1) * hs + d;
+// A row tensor's places in memory, from its strides in elements (of which a byte's are a few bits more: larger
+// ones than memory has are as good as the largest).
+RowRuns runs(const void* p, long long rows, long long rs, long long heads, long long hs, int d, int es) {
+  auto bytes = [es](long long s) {
+    const long long most = INT64_MAX / 8;
+    return std::min(std::max(s, -most), most) * es;
+  };
+  return {(uint64_t)(uintptr_t)p, rows, bytes(rs), heads, bytes(hs), (int64_t)d * es};
 }
 
 int launch_rows(RowParams& p, int head_dim, int es, bool vec, const void* fn,
@@ -605,10 +606,10 @@ int decode_attn_rope_apply(const da_rope* rope, const da_rope_args* args) {
   if (!a.x || !a.out || !a.positions || !aligned(a.x, es) || !aligned(a.out, es) ||
       !aligned(a.positions, 4))
     return DA_ERR_INVALID_ARG;
-  if (!lie_apart(a.rows, a.out_row_stride, a.heads, a.out_head_stride, rope->cfg.head_dim))
-    return DA_ERR_INVALID_ARG;
-  if (a.x == a.out && (a.x_row_stride != a.out_row_stride || a.x_head_stride != a.out_head_stride))
-    return DA_ERR_INVALID_ARG;
+  const int d = rope->cfg.head_dim;
+  const RowRuns in = runs(a.x, a.rows, a.x_row_stride, a.heads, a.x_head_stride, d, es);
+  const RowRuns result = runs(a.out, a.rows, a.out_row_stride, a.heads, a.out_head_stride, d, es);
+  if (!lie_apart(result) || !result_ok(in, result)) return DA_ERR_INVALID_ARG;
   RowParams p;
   std::memset(&p, 0, sizeof p);
   set_rope(p, rope);
@@ -651,11 +652,19 @@ int decode_attn_kv_write(const da_plan* plan, const da_kv_write_args* args) {
       !aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) || !aligned(a.positions, 4) ||
       !aligned(a.q, es) || !aligned(a.q_out, es) || !aligned(a.amax, 4))
     return DA_ERR_INVALID_ARG;
-  if (a.q && !lie_apart(a.rows, a.q_out_row_stride, pr.num_q_heads, a.q_out_head_stride, pr.head_dim))
-    return DA_ERR_INVALID_ARG;
-  if (a.q && a.q == a.q_out &&
-      (a.q_row_stride != a.q_out_row_stride || a.q_head_stride != a.q_out_head_stride))
-    return DA_ERR_INVALID_ARG;
+  const int d = pr.head_dim;
+  if (a.q) {
+    const RowRuns q = runs(a.q, a.rows, a.q_row_stride, pr.num_q_heads, a.q_head_stride, d, es);
+    const RowRuns k = runs(a.k, a.rows, a.k_row_stride, pr.num_kv_heads, a.k_head_stride, d, es);
+    const RowRuns v = runs(a.v, a.rows, a.v_row_stride, pr.num_kv_heads, a.v_head_stride, d, es);
+    const RowRuns out = runs(a.q_out, a.rows, a.q_out_row_stride, pr.num_q_heads, a.q_out_head_stride, d, es);
+    if (!lie_apart(out) || !result_ok(q, out) || may_share(k, out) || may_share(v, out))
+      return DA_ERR_INVALID_ARG;
+  }
+  const long long tokens = pr.paged ? (long long)pr.num_physical_blocks * pr.page_size
+                                    : (long long)pr.batch * pr.max_seq_len;
+  const long long cache_bytes = tokens * pr.num_kv_heads * d * pl.kv_es;
+  if (overlap(a.k_cache, cache_bytes, a.v_cache, cache_bytes)) return DA_ERR_INVALID_ARG;
   RowParams p;
   std::memset(&p, 0, sizeof p);
   fill_common(pl, p.cache, a.block_table, nullptr, a.workspace);

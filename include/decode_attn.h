@@ -433,7 +433,9 @@ void decode_attn_rope_destroy(da_rope* rope);
  * fp32, rounded once to the storage type.
  *   x, out      device, [rows, heads, head_dim] of `dtype` with the given strides (elements; out's
  *               heads and rows must lie apart: overlapping strides are refused). out may be x
- *               with equal strides (in place); any other overlap is not allowed.
+ *               with equal strides (in place), or other rows or heads of the same tensor; any
+ *               other overlap is refused, and tensors of one memory that are interleaved some
+ *               other way with it.
  *   positions   device int32 [rows]; negative positions rotate backwards.
  * Aligned to 16 bytes, with strides that are multiples of 16 bytes and rotary_dim and head_dim
  * multiples of 32 bytes, rows move 16 bytes a lane; any other case takes one pair a lane.
@@ -459,8 +461,8 @@ int decode_attn_rope_apply(const da_rope* rope, const da_rope_args* args);
  *   plan: any plan of the problem shape; its softmax mode and split choice are not used.
  *   k, v        device, [rows, H_kv, d] in qkv_dtype with the given strides (parts of one
  *               projection's rows, for instance).
- *   k_cache,    device, as for decode_attn_run. A 16-bit or fp32 cache takes the values as
- *   v_cache     they are (a rotated k rounded once to nearest even). An FP8 cache takes E4M3
+ *   k_cache,    device, as for decode_attn_run, apart (else refused); k and v must not lie where
+ *   v_cache     rows are written. A 16-bit or fp32 cache takes the values as they are (a rotated k rounded once to nearest even). An FP8 cache takes E4M3
  *               codes of x / k_scale or x / v_scale, an fp32 quotient rounded to nearest
  *               even, values beyond +-448 to +-448, NaN to the NaN code; a rotated k is not
  *               rounded to qkv_dtype in between. (A scale whose reciprocal is no fp32 number
@@ -469,7 +471,8 @@ int decode_attn_rope_apply(const da_rope* rope, const da_rope_args* args);
  *               of the pool (of two rows written to one token, either may stay, in parts).
  *   rope        nullable. With it k is rotated by its row's position, and q, when given, is
  *               rotated into q_out: [rows, H_q, d] in qkv_dtype, both with strides; q_out may be
- *               q with equal strides, and its heads and rows must lie apart (else refused).
+ *               q with equal strides, and its heads and rows must lie apart, and apart from
+ *               those of k and v (else refused, as in decode_attn_rope_apply).
  *               Without it q and q_out must be NULL. rope's head_dim must be the plan's.
  *   positions   nullable device int32 [rows]: the rotary positions where they are not the cache
  *               positions (drafted trees: a node's depth). Needs rope.
@@ -511,7 +514,8 @@ int decode_attn_kv_write(const da_plan* plan, const da_kv_write_args* args);
 /* Read rows back from the cache: k_out[r], v_out[r] = the K and V of row r's position, codes of an
  * FP8 cache times k_scale or v_scale, rounded once to qkv_dtype (to nearest even).
  *   k_out, v_out  device, [rows, H_kv, d] contiguous, qkv_dtype, 16-byte aligned, apart (else
- *                 refused); either may be NULL (not both), and its cache then too.
+ *                 refused), and not where rows are read; either may be NULL (not both), and its
+ *                 cache then too.
  * Rows at a position outside [0, capacity) or on a bad block-table entry read as zeros and are
  * recorded as in decode_attn_kv_write; rows of no sequence are left as they were.
  * Writing rows read from an FP8 cache back with the same scales reproduces their codes (a NaN

@@ -2,6 +2,9 @@
 frequencies on the CPU, results on the GPU against plain float64 forms."""
 import ctypes
 import math
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -597,3 +600,71 @@ def test_codes_are_those_of_the_fp32_quotient(k_scale, v_scale, aligned):
     for c, scale in ((kc, k_scale), (vc, v_scale)):
         want = (x.float() / torch.tensor(scale)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
         assert torch.equal(c.cpu().view(want.shape), want)
+
+
+# ---- results over inputs ----------------------------------------------------------------------
+def test_where_rows_lie(tmp_path):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = tmp_path / "row_rules"
+    subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", "-Werror",
+                    "-I" + os.path.join(root, "decode_attention_attn_gb300", "csrc"),
+                    os.path.join(root, "tests", "c_row_rules.cpp"), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+def test_rope_apply_refuses_results_over_inputs():
+    r = binding.Rope(128)
+
+    def call(**kw):   # 8 rows of 4 heads, bf16: rows of 1024 bytes, heads of 256
+        args = binding.da_rope_args(A, A + 65536, 2, 8, 4, 512, 128, 512, 128, A, 0, None)
+        return _refused(binding.decode_attn_rope_apply, r.handle, args, **kw)
+
+    assert call(out=A + 1024) == -1 and call(out=A - 1024) == -1       # a row on, a row back
+    assert call(out=A + 256) == -1 and call(out=A + 2) == -1           # a head on, an element on
+    assert call(out=A + 7 * 1024) == -1 and call(x=A + 7 * 1024, out=A) == -1
+    assert call(out=A + 4096, out_row_stride=1024) == -1               # other strides of one memory
+    assert call(x_row_stride=0, x=A + 65536 + 3 * 1024) == -1          # one row for all, among the results
+    assert call(out_row_stride=2 ** 62, out_head_stride=2 ** 61) == -1
+
+
+def test_kv_write_refuses_results_over_inputs():
+    plan, ws = _plan()
+    r = binding.Rope(128)
+    far = 1 << 24
+
+    def call(**kw):
+        args = binding.da_kv_write_args(A, A + far, 1024, 128, 1024, 128, 4, A + 2 * far, A + 3 * far, A, A, A,
+                                        r.handle, None, A + 4 * far, A + 5 * far, 4096, 128, 4096, 128, None, None,
+                                        0, None)
+        return _refused(binding.decode_attn_kv_write, plan, args, **kw)
+
+    assert call(q_out=A + 4 * far + 8192) == -1                        # q, a row on
+    assert call(q_out=A + 2048) == -1 and call(q_out=A + far - 16384) == -1   # over k, over v
+    assert call(v_cache=A + 2 * far) == -1 and call(v_cache=A + 2 * far + 4096) == -1
+    binding.decode_attn_destroy(plan)
+
+
+@pytest.mark.gpu
+def test_parts_of_one_tensor_are_rotated_beside_one_another():
+    """Results in other heads, every other head, or other rows of the input's own tensor."""
+    d = 64
+    base = torch.randn(40, 12, d, generator=torch.Generator().manual_seed(2)).bfloat16()
+    pos = torch.arange(40, dtype=torch.int32)
+    r = binding.Rope(d)
+    theta = torch.tensor(r.frequencies(), dtype=torch.float64)
+    for x, out in ((lambda t: t[:, :5], lambda t: t[:, 7:]), (lambda t: t[:, ::2], lambda t: t[:, 1::2]),
+                   (lambda t: t[:20], lambda t: t[20:]), (lambda t: t[::2], lambda t: t[1::2]),
+                   (lambda t: t.transpose(0, 1)[:, :7], lambda t: t.transpose(0, 1)[:, 9:16])):
+        dev = base.cuda()
+        p = pos[:x(base).shape[0]]
+        r.apply(x(dev), p.cuda(), out=out(dev))
+        _check_rotated(out(dev), x(base), p, theta, d, False, 1.0)
+        want = base.clone()
+        out(want).copy_(out(dev).cpu())
+        assert torch.equal(dev.cpu(), want)
+        with pytest.raises(binding.DecodeAttnError):
+            r.apply(dev[1:], pos[1:].cuda(), out=dev[:-1])

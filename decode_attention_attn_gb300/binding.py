@@ -669,6 +669,29 @@ def _empty(shape, dtype, device, stream):
         return _torch.empty(shape, dtype=dtype, device=device)
 
 
+def _rotation():
+    """The autograd function of Rope.apply, made once torch is there."""
+    class Rotation(_torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, rope, positions, transpose, stream):
+            ctx.save_for_backward(positions)
+            ctx.rope, ctx.transpose = rope, transpose
+            return rope._rotate(x, positions, None, transpose, stream)
+
+        @staticmethod
+        def backward(ctx, grad):
+            (positions,) = ctx.saved_tensors
+            if grad.stride(-1) != 1:
+                grad = grad.contiguous()
+            # on the stream that autograd runs this on: the one that was current in the forward call
+            return ctx.rope.apply(grad, positions, transpose=not ctx.transpose), None, None, None, None
+
+    return Rotation
+
+
+_Rotation = None
+
+
 class Rope:
     """A rotary embedding: its frequencies, scaled for long contexts by `scaling` ("none", "linear",
     "ntk", "by_parts", "by_index"; see da_rope_scaling), and its layout.
@@ -703,8 +726,18 @@ class Rope:
     def apply(self, x, positions, out=None, transpose: bool = False, stream=None):
         """Rows of x (fp32, fp16 or bf16; rows and heads may be strided) rotated by `positions`
         (int32 [rows]), into `out` (x itself: in place; allocated on the call's stream when None).
-        transpose: the transposed map, which takes the gradient of the output to the gradient of x;
-        autograd does not record the call, so a backward pass calls it itself."""
+        transpose: the transposed map, which takes the gradient of the output to the gradient of x.
+        Autograd records the call where x requires a gradient; `out` cannot be given then."""
+        if (x.requires_grad or (out is not None and out.requires_grad)) and _torch.is_grad_enabled():
+            if out is not None:
+                raise ValueError("autograd cannot record a call with an out")
+            global _Rotation
+            if _Rotation is None:
+                _Rotation = _rotation()
+            return _Rotation.apply(x, self, positions, transpose, stream)
+        return self._rotate(x, positions, out, transpose, stream)
+
+    def _rotate(self, x, positions, out, transpose, stream):
         dtype, shape = x.dtype, x.shape
         code = self._codes.get(dtype)
         if code is None:
@@ -774,7 +807,7 @@ class KVCacheIO(_Workspace):
     The rows of a step lie one after another, sequence by sequence: row_offsets (int32
     [batch + 1]) says which rows are whose, start (int32 [batch]) the cache position of each
     sequence's first row. With findings=True (or the problem's validate) the device records rows
-    without a place in the cache, which check_status() reports."""
+    without a place in the cache, which check_status() reports. Autograd records neither call."""
 
     def __init__(self, problem: da_problem, findings: bool = False, device=None):
         self._write = _entry("decode_attn_kv_write", da_kv_write_args)

@@ -668,3 +668,97 @@ def test_parts_of_one_tensor_are_rotated_beside_one_another():
         assert torch.equal(dev.cpu(), want)
         with pytest.raises(binding.DecodeAttnError):
             r.apply(dev[1:], pos[1:].cuda(), out=dev[:-1])
+
+
+# ---- gradients --------------------------------------------------------------------------------
+def test_rope_apply_refuses_an_out_that_autograd_would_lose():
+    r = binding.Rope(64)
+    x, pos = torch.zeros(3, 2, 64, requires_grad=True), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="autograd"):
+        r.apply(x, pos, out=torch.zeros(3, 2, 64))
+    with pytest.raises(ValueError, match="autograd"):
+        r.apply(x.detach(), pos, out=x)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):     # not recorded, so not refused for it
+        r.apply(x, pos, out=torch.zeros(3, 2, 64))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_autograd_records_a_rotation(dtype, interleaved, transpose):
+    """backward() through apply: the transposed map of the output's gradient, for a leaf, a strided part of one, a
+    row broadcast to all, and an expanded gradient; and through the backward pass itself."""
+    rows, heads, d, rotary = 21, 3, 64, 32
+    g = torch.Generator().manual_seed(5)
+    r = binding.Rope(d, rotary, interleaved, attn_factor=0.75)
+    theta = torch.tensor(r.frequencies(), dtype=torch.float64)
+    pos = torch.randint(0, 9000, (rows,), generator=g, dtype=torch.int32)
+    dy = torch.randn(rows, heads, d, generator=g).to(TORCH[dtype])
+
+    x = torch.randn(rows, 2 * heads, d, generator=g).to(TORCH[dtype]).cuda().requires_grad_()
+    y = r.apply(x[:, heads:], pos.cuda(), transpose=transpose)
+    assert y.requires_grad and torch.equal(y, r.apply(x.detach()[:, heads:], pos.cuda(), transpose=transpose))
+    y.backward(dy.cuda())
+    want = rotate(dy.double(), pos, theta, rotary, interleaved, 0.75, not transpose)
+    err = rotate_bound(dy.double(), pos, theta, rotary, interleaved, 0.75)
+    got = x.grad.cpu().double()
+    assert (got[:, :heads] == 0).all()
+    assert ((got[:, heads:] - want).abs() <= err + want.abs() * half_step(TORCH[dtype]) * 1.001 + 6e-8).all()
+    # one row for all positions: its gradient is the sum of theirs
+    one = torch.randn(1, heads, d, generator=g).to(TORCH[dtype]).cuda().requires_grad_()
+    r.apply(one.expand(rows, heads, d), pos.cuda(), transpose=transpose).backward(dy.cuda())
+    each = want.abs() * half_step(TORCH[dtype]) * 1.001 + err + 6e-8
+    total = want.sum(0, keepdim=True)
+    tol = each.sum(0, keepdim=True) + want.abs().sum(0, keepdim=True) * 21 * 2.0 ** -23 + \
+        total.abs() * half_step(TORCH[dtype]) * 1.001 + 6e-8
+    assert ((one.grad.cpu().double() - total).abs() <= tol * 1.01).all()
+    # a gradient with no strides, and a gradient of a gradient
+    leaf = torch.randn(rows, heads, d, generator=g).to(TORCH[dtype]).cuda().requires_grad_()
+    r.apply(leaf, pos.cuda(), transpose=transpose).sum().backward()
+    ones = torch.ones(rows, heads, d, dtype=torch.float64)
+    want = rotate(ones, pos, theta, rotary, interleaved, 0.75, not transpose)
+    err = rotate_bound(ones, pos, theta, rotary, interleaved, 0.75)
+    assert ((leaf.grad.cpu().double() - want).abs() <= err + want.abs() * half_step(TORCH[dtype]) * 1.001 + 6e-8).all()
+    w = dy.cuda().requires_grad_()
+    (gx,) = torch.autograd.grad(r.apply(leaf, pos.cuda(), transpose=transpose), leaf, w, create_graph=True)
+    (gw,) = torch.autograd.grad(gx, w, torch.ones_like(gx))
+    assert torch.equal(gw, r.apply(torch.ones_like(leaf), pos.cuda(), transpose=transpose))
+    with torch.no_grad():
+        assert not r.apply(leaf, pos.cuda()).requires_grad
+
+
+@pytest.mark.gpu
+def test_a_recorded_rotation_on_another_stream_and_captured():
+    d = 64
+    r = binding.Rope(d)
+    pos = torch.arange(300, dtype=torch.int32, device="cuda")
+    x = torch.randn(300, 4, d, device="cuda")
+    dy = torch.randn(300, 4, d, device="cuda")
+    want = r.apply(dy, pos, transpose=True)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        leaf = x.clone().requires_grad_()
+        r.apply(leaf, pos).backward(dy)
+    side.synchronize()
+    assert torch.equal(leaf.grad, want)
+    static = x.clone().requires_grad_()
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            static.grad = None
+            r.apply(static, pos).backward(dy)
+    torch.cuda.current_stream().wait_stream(side)
+    static.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = r.apply(static, pos)
+        y.backward(dy)
+    for _ in range(2):
+        with torch.no_grad():
+            static.mul_(1.5)
+            dy.mul_(0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y.detach(), r.apply(static.detach(), pos))
+        assert torch.equal(static.grad, r.apply(dy, pos, transpose=True))

@@ -80,19 +80,19 @@ __device__ __forceinline__ int find_sequence(const int32_t* offsets, int batch, 
 // Where row r goes: its cache position (pos) and cache row (z; -1: none, recorded).
 // Returns false for a row of no sequence.
 __device__ __forceinline__ bool locate_row(const Params& c, const int32_t* offsets,
-                                           const int32_t* start, int r, int& pos, int& z) {
+                                           const int32_t* start, int r, long long& pos, int& z) {
   const int b = find_sequence(offsets, c.batch, r);
   if (b < 0) return false;
-  const long long t = (long long)__ldg(start + b) + (r - __ldg(offsets + b));
-  pos = (int)t;
+  const long long t = (long long)__ldg(start + b) + ((long long)r - __ldg(offsets + b));
+  pos = t;
   z = -1;
   if (t < 0 || t >= c.capacity) {
     if (c.status) atomicOr(c.status, kStatusBadSeqLen);
     return true;
   }
   const int entry =
-      c.paged ? __ldg(c.block_table + (long long)b * c.max_blocks + pos / c.page_size) : 0;
-  z = token_row(c, b, pos, entry);
+      c.paged ? __ldg(c.block_table + (long long)b * c.max_blocks + (int)t / c.page_size) : 0;
+  z = token_row(c, b, (int)t, entry);
   if (z < 0 && c.status) atomicOr(c.status, kStatusBadBlockTable);
   return true;
 }
@@ -198,7 +198,7 @@ __device__ __forceinline__ void store_unit(C* dst, int a0, int b0, bool joined, 
 // u VEC + rotary / 2, else 2 VEC neighbours (also where nothing is rotated). A thread keeps one
 // unit position u and walks over heads.
 //
-// The angle of position t is t * turn mod 1 in 64-bit fixed point: exact for any 32-bit t, with
+// The angle of position t is t * turn mod 1 in 64-bit fixed point: exact for any t, with
 // no 64-bit float arithmetic (an fp32 angle at t = 10^6 would be off by 0.06). Its top 32 bits,
 // as a signed half-turn count, go through sincospif.
 //
@@ -213,7 +213,8 @@ template <typename T, typename C, int VEC>
 __global__ void __launch_bounds__(kRowThreads, 7)
     rows_kernel(const __grid_constant__ RowParams p) {
   __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
-  __shared__ int s_info[3];   // member, position, cache row
+  __shared__ int s_info[2];   // member, cache row
+  __shared__ long long s_pos;
   using V = RowVec<T, VEC>;
   using Raw = typename V::Raw;
   using PT = Packed<T, VEC>;
@@ -249,26 +250,27 @@ __global__ void __launch_bounds__(kRowThreads, 7)
   if (h + step < heads) load(h + step, ra[1], rb[1]);
 
   long long z = -1;
-  int pos = 0;
+  long long pos = 0;   // (past 2^31 where a row lies far behind its cache: its q is rotated all the same)
   if (p.row_offsets) {
     if (tid == 0) {
-      int at = 0, zz = -1;
+      long long at = 0;
+      int zz = -1;
       const bool member = locate_row(p.cache, p.row_offsets, p.start, row, at, zz);
       if (member && p.positions) at = __ldg(p.positions + row);
       s_info[0] = member;
-      s_info[1] = at;
-      s_info[2] = zz;
+      s_info[1] = zz;
+      s_pos = at;
     }
     __syncthreads();
     if (!s_info[0]) return;
-    pos = s_info[1];
-    z = s_info[2];
+    pos = s_pos;
+    z = s_info[1];
   } else {
     pos = __ldg(p.positions + row);
   }
   if (p.rotary) {
     for (int i = tid; i < p.rotary / 2; i += kRowThreads) {
-      const unsigned long long a = (unsigned long long)(long long)pos * p.turn[i];
+      const unsigned long long a = (unsigned long long)pos * p.turn[i];
       float s, c;
       sincospif((float)(int)(unsigned)(a >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
       s_cos[i] = c * p.m;
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
   // rows row0 + lane: -2 none or of no sequence, -1 no place, else the cache row
   int z = -2;
   if (lane * p.row_items < off0 + 32 * PER && row0 + lane < p.rows) {
-    int pos;
+    long long pos;
     if (!locate_row(p.cache, p.row_offsets, p.start, row0 + lane, pos, z)) z = -2;
   }
   uint4 c[PER];

@@ -5,6 +5,7 @@ import math
 import os
 import shutil
 import subprocess
+from fractions import Fraction
 
 import pytest
 import torch
@@ -762,3 +763,35 @@ def test_a_recorded_rotation_on_another_stream_and_captured():
         torch.cuda.synchronize()
         assert torch.equal(y.detach(), r.apply(static.detach(), pos))
         assert torch.equal(static.grad, r.apply(dy, pos, transpose=True))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_positions_past_31_bits_rotate_q(dtype):
+    """start + i of rows that have no place may pass 2^31: q is rotated by the sum, not by what 32 bits leave of
+    it. The reference's angle, position times theta in float64, is off by 2^-21 at theta = 1; here the turns are
+    reduced in integers of 2^-64."""
+    lay = Layout([0], [6], 1, 64, dtype=dtype, hq=2)
+    io = binding.KVCacheIO(lay.problem)
+    r = binding.Rope(64)
+    start = 2 ** 31 - 3
+    q, k = lay.normal(6, 2, 64), lay.normal(6, 1, 64)
+    kc = lay.cache().cuda()
+    before = kc.clone()
+    out = io.write(k.cuda(), k.cuda(), kc, kc.clone(), None, lay.row_offsets.cuda(),
+                   torch.tensor([start], dtype=torch.int32, device="cuda"), rope=r, q=q.cuda())
+    assert torch.equal(kc, before)
+    theta = r.frequencies()
+    c, s = torch.zeros(6, 1, 32, dtype=torch.float64), torch.zeros(6, 1, 32, dtype=torch.float64)
+    for i in range(6):
+        for j, t in enumerate(theta):
+            turn = Fraction(t) / Fraction(2 * math.pi)
+            # theta / (2 pi) in double is off by 2^-53 of itself, 2 pi by 2^-53: times 2^31 turns, 2^-21
+            a = float(((start + i) * turn) % 1) * 2 * math.pi
+            c[i, 0, j], s[i, 0, j] = math.cos(a), math.sin(a)
+    x = q.double()
+    want = torch.cat([c * x[..., :32] - s * x[..., 32:], s * x[..., :32] + c * x[..., 32:]], -1)
+    size = (x[..., :32].abs() + x[..., 32:].abs()).repeat(1, 1, 2)
+    tol = size * (4e-7 + 3 * 2.0 ** -24 + 2.0 ** 31 * 2 * math.pi * 2.0 ** -51) + want.abs() * half_step(x.dtype)
+    tol = tol + want.abs() * half_step(TORCH[dtype]) * 1.001
+    assert ((out.cpu().double() - want).abs() <= tol).all()

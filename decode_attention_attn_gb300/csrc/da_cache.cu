@@ -5,6 +5,7 @@
 // arithmetic (two products and an add per element, a conversion) is small beside it. At a decode
 // step's size (one row a sequence) the time is the launch and a chain of dependent loads.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -382,17 +383,31 @@ RowRuns runs(const void* p, long long rows, long long rs, long long heads, long 
   return {(uint64_t)(uintptr_t)p, rows, bytes(rs), heads, bytes(hs), (int64_t)d * es};
 }
 
-int launch_rows(RowParams& p, int head_dim, int es, bool vec, const void* fn,
+// SMs of the current device, asked for once; 0: not known (cuda_fail has the reason).
+int device_sms() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0, n = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < kDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) {
+    cuda_fail(e, "asking for the device's SMs");
+    return 0;
+  }
+  if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+int launch_rows(RowParams& p, int head_dim, int es, bool vec, int sms, const void* fn,
                 cudaStream_t stream) {
   const int v = vec ? 16 / es : 1;
   p.units = head_dim / (2 * v);
   p.head_lanes = kRowThreads / p.units;
   const int heads = p.hq + 2 * p.hkv;
-  // A block per row; where rows are few, a row's heads are spread over more blocks (at least one
-  // pass of heads each), up to two blocks an SM (64 rows of 64 heads, or 1 of 128: 4.1 us, one block a row 6.2).
+  // A block per row, or several (64 rows of 64 heads, or 1 of 128: 4.1 us, one block a row 6.2).
   const int passes = (heads + p.head_lanes - 1) / p.head_lanes;
-  int slices = 1;
-  while (slices < passes && (long long)p.rows * slices < 2 * 152) ++slices;
+  const int slices = row_slices(p.rows, passes, sms);
   void* args[1] = {&p};
   const cudaError_t e = cudaLaunchKernel(fn, dim3((unsigned)p.rows, (unsigned)slices),
                                          dim3(kRowThreads), args, 0, stream);
@@ -634,7 +649,9 @@ int decode_attn_rope_apply(const da_rope* rope, const da_rope_args* args) {
   const void* fn = a.dtype == DA_F32   ? rows_kernel_for<float, float>(vec)
                    : a.dtype == DA_F16 ? rows_kernel_for<__half, __half>(vec)
                                        : rows_kernel_for<__nv_bfloat16, __nv_bfloat16>(vec);
-  return launch_rows(p, rope->cfg.head_dim, es, vec, fn, static_cast<cudaStream_t>(a.cuda_stream));
+  const int sms = device_sms();
+  if (sms <= 0) return DA_ERR_CUDA;
+  return launch_rows(p, rope->cfg.head_dim, es, vec, sms, fn, static_cast<cudaStream_t>(a.cuda_stream));
 }
 
 int decode_attn_kv_write(const da_plan* plan, const da_kv_write_args* args) {
@@ -716,7 +733,7 @@ int decode_attn_kv_write(const da_plan* plan, const da_kv_write_args* args) {
                                             : rows_kernel_for<__nv_bfloat16, __nv_bfloat16>(vec);
   cudaStream_t stream = static_cast<cudaStream_t>(a.cuda_stream);
   rc = clear_status(pl, a.workspace, stream);
-  if (rc == DA_OK) rc = launch_rows(p, pr.head_dim, es, vec, fn, stream);
+  if (rc == DA_OK) rc = launch_rows(p, pr.head_dim, es, vec, pl.num_sms, fn, stream);
   if (rc == DA_OK && pr.validate) rc = decode_attn_check_status(plan, a.workspace, stream);
   return rc;
 }

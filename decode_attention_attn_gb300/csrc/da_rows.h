@@ -1,5 +1,6 @@
 // da_rows.h -- host-side rules of the row operators' launches (host code only; no CUDA types):
-// where strided row tensors lie, so that results over inputs are refused.
+// where strided row tensors lie, so that results over inputs are refused, and how many blocks share
+// a row.
 #pragma once
 
 #include <cstdint>
@@ -86,6 +87,14 @@ inline bool may_share(const RowRuns& a, const RowRuns& b) {
 inline bool result_ok(const RowRuns& in, const RowRuns& out) {
   if (in.address == out.address) return in.row == out.row && in.head == out.head;
   return !may_share(in, out);
+}
+
+// Blocks that a row's `passes` (of as many heads as a block takes at once) are spread over: where rows are few,
+// as many as two blocks an SM allow.
+inline int row_slices(int64_t rows, int passes, int sms) {
+  const int64_t blocks = 2 * (int64_t)sms;
+  const int64_t n = rows >= blocks ? 1 : (blocks + rows - 1) / rows;
+  return n < passes ? (int)n : passes;
 }
 
 }  // namespace da

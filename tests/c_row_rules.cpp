@@ -1,4 +1,5 @@
-// Host-side check of where strided row tensors lie (plain C++, no CUDA), against every byte's owner.
+// Host-side check of the row operators' rules (plain C++, no CUDA): where strided row tensors lie, against every
+// byte's owner, and how many blocks share a row.
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -86,6 +87,15 @@ int main() {
   RowRuns low = part(0, 2, 256, 1, 256);
   low.address = 4096;
   CHECK(!da::may_share(low, part(0, 2, INT64_MAX, 1 << 20, INT64_MAX)));
+  // blocks a row: enough for two an SM, by the SMs at hand, and a pass of heads each
+  for (int sms : {1, 2, 40, 132, 152, 160})
+    for (int64_t rows : {1, 2, 3, 5, 64, 79, 80, 263, 264, 303, 304, 305, 5000, 2147483647})
+      for (int passes : {1, 2, 5, 64, 1000}) {
+        const int n = da::row_slices(rows, passes, sms);
+        int want = 1;
+        while (want < passes && rows * want < 2 * sms) ++want;
+        CHECK(n == want);
+      }
   if (fails == 0) std::printf("ok\n");
   return fails ? 1 : 0;
 }

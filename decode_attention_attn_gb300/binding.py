@@ -264,6 +264,7 @@ def lib():
         L.decode_attn_tree_plan.argtypes = [ctypes.POINTER(da_problem), ctypes.c_int,
                                             ctypes.POINTER(P), ctypes.POINTER(ctypes.c_size_t)]
         L.decode_attn_tree_plan_info.argtypes = [P, ctypes.POINTER(da_tree_plan_info)]
+        L.decode_attn_tree_debug_stall.argtypes = [P, ctypes.c_int]
         L.decode_attn_tree_workspace_init.argtypes = [P, P, ctypes.c_size_t, P]
         L.decode_attn_tree_run.argtypes = [P, ctypes.POINTER(da_tree_args)]
         L.decode_attn_tree_check_status.argtypes = [P, P, P]
@@ -284,6 +285,7 @@ def lib():
                      "decode_attn_rope_create", "decode_attn_rope_frequencies",
                      "decode_attn_rope_apply", "decode_attn_kv_write", "decode_attn_kv_read",
                      "decode_attn_tree_plan", "decode_attn_tree_plan_info",
+                     "decode_attn_tree_debug_stall",
                      "decode_attn_tree_workspace_init", "decode_attn_tree_run",
                      "decode_attn_tree_check_status", "decode_attn_abi_version"):
             getattr(L, name).restype = ctypes.c_int
@@ -449,6 +451,10 @@ def decode_attn_tree_plan_info(plan) -> da_tree_plan_info:
     _check(lib().decode_attn_tree_plan_info(plan, ctypes.byref(info)),
            "decode_attn_tree_plan_info")
     return info
+
+
+def decode_attn_tree_debug_stall(plan, tensor: int):
+    _check(lib().decode_attn_tree_debug_stall(plan, tensor), "decode_attn_tree_debug_stall")
 
 
 def decode_attn_tree_workspace_init(plan, workspace: int, workspace_bytes: int, stream: int = 0):

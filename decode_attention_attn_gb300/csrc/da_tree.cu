@@ -21,6 +21,7 @@ struct da_tree_plan {
   int max_tree, num_sms;
   int tile_rows, tile_tokens, max_row_tiles;
   int grid, stages, narrow;
+  int stall;                    // test hook, see TreeParams
   unsigned char heads[kTreeMaxRowTiles + 1];
   size_t smem_bytes;
   size_t off_status, off_info, off_part_l, off_part_o, ws_bytes;
@@ -517,6 +518,13 @@ int decode_attn_tree_plan_info(const da_tree_plan* plan, da_tree_plan_info* info
   return DA_OK;
 }
 
+int decode_attn_tree_debug_stall(da_tree_plan* plan, int tensor) {
+  if (!plan || tensor < 0 || tensor > 2) return DA_ERR_INVALID_ARG;
+  if (plan->stages == 0) return DA_ERR_UNSUPPORTED;   // the fp32 kernel waits for its own copies alone
+  plan->stall = tensor;
+  return DA_OK;
+}
+
 void decode_attn_tree_destroy(da_tree_plan* plan) { delete plan; }
 
 int decode_attn_tree_workspace_init(const da_tree_plan* plan, void* workspace,
@@ -580,6 +588,8 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args) {
   p.tile_tokens = pl.tile_tokens;
   p.max_row_tiles = pl.max_row_tiles;
   p.narrow = pl.narrow;
+  p.stall = pl.stall;
+  if (pl.stall) p.c.wait_limit_ns = kTestWaitLimitNs;
   std::memcpy(p.heads, pl.heads, sizeof p.heads);
   p.qscale = (float)((double)a.scale * 1.4426950408889634 * (pr.kv_fp8 ? (double)pr.k_scale : 1.0));
   p.v_scale = pr.kv_fp8 ? pr.v_scale : 1.f;

@@ -36,6 +36,7 @@ struct TreeParams {
   int tile_rows, tile_tokens;
   int max_row_tiles;            // R's bound, from max_tree
   int narrow;                   // owners x units fits 32 bits: short divisions
+  int stall;                    // test hook: 0, or 1 (2): CTA 0's loader of K (V) leaves out its second tile
   unsigned char heads[kTreeMaxRowTiles + 1];   // heads side by side, by R (tree_heads)
   float qscale, v_scale;
 };

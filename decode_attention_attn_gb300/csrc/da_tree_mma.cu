@@ -331,7 +331,9 @@ __device__ __noinline__ void add_odd(const TreeParams& p, int b, int ctx, int kv
       const int entry = p.c.paged ? __ldg(p.c.block_table + (long long)b * p.c.max_blocks +
                                           t / p.c.page_size)
                                   : 0;
-      const long long at = ((long long)token_row(p.c, b, t, entry) * p.c.hkv + kvh) * D + col;
+      const int z = token_row(p.c, b, t, entry);
+      if (z < 0) continue;   // (a bad page holds zeros, unless the loads were given up)
+      const long long at = ((long long)z * p.c.hkv + kvh) * D + col;
       float v;
       if constexpr (kFp8)
         v = unpack_pair<__half>(e4m3x2_to_f16x2(static_cast<const uint8_t*>(v_cache)[at])).x;
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
   // K and V tiles: distance between 64-element blocks and between 8-row groups
   const bool paired = !kFp8 && p.c.paged;
   const uint32_t blk_bytes = paired ? 1024u : 16384u, grp_bytes = paired ? CH * 1024u : 1024u;
-  Waiter wait{abort_flag, p.c.status, kWaitLimitNs, *abort_flag != 0};
+  Waiter wait{abort_flag, p.c.status, p.c.wait_limit_ns, *abort_flag != 0};
   if constexpr (!kFp8) {
     if (warp < kTreeSoftmaxWarps)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeSoftmaxRegs));
@@ -804,7 +806,11 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
         }
       }
       wait(&empty[slot], par);
-      if (!wait.dead) {
+      // A converter that has given up frees tiles that it did not wait for: no copy may be armed on a barrier
+      // whose last one is still under way. (What it arrived after, the flag, is seen once the wait has ended.)
+      if (kFp8) wait.dead |= __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(abort_flag));
+      const bool left_out = p.stall == 1 + (int)is_v && blockIdx.x == 0 && it == 1;
+      if (!wait.dead && !left_out) {
         const int boxes = __popc(__ballot_sync(0xffffffffu, z_now != -2));
         if (lane == 0) mbar_arrive_expect_tx(&full[slot], boxes * lane_bytes);
         __syncwarp();
@@ -825,9 +831,9 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
     }
     // never leave with copies in flight
     for (uint32_t k = issued > slots ? issued - slots : 0; k < issued; ++k)
-      mbar_wait(&full[k % slots], (k / slots) & 1, kWaitLimitNs);
+      mbar_wait(&full[k % slots], (k / slots) & 1, p.c.wait_limit_ns);
     for (int k = loaded > L.nq ? loaded - L.nq : 0; k < loaded; ++k)
-      mbar_wait(&q_full[k & 1], (k >> 1) & 1, kWaitLimitNs);
+      mbar_wait(&q_full[k & 1], (k >> 1) & 1, p.c.wait_limit_ns);
   } else if (warp == kTreeSoftmaxWarps + 2) {
     // ---- S = Q K^T issuer ------------------------------------------------------------------
     Cursor c(p, sh);
@@ -875,7 +881,7 @@ __global__ void __launch_bounds__(tree_threads(std::is_same<T, fp8e4m3>::value),
       sl.next();
     }
     if (issuer) tc_commit(&drained[0]);   // nothing leaves before the last MMA has completed
-    mbar_wait(&drained[0], 0, kWaitLimitNs);
+    mbar_wait(&drained[0], 0, kWaitLimitNs);   // (issued MMAs end; no test hook holds them up)
   } else if (warp == kTreeSoftmaxWarps + 3) {
     // ---- O += P V issuer -------------------------------------------------------------------
     Cursor c(p, sh);

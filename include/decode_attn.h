@@ -570,6 +570,15 @@ int decode_attn_tree_plan(const da_problem* problem, int max_tree, da_tree_plan*
 
 int decode_attn_tree_plan_info(const da_tree_plan* plan, da_tree_plan_info* info);
 
+/* Test hook, 0 in normal use. tensor = 1 (2): in the plan's later runs CTA 0 leaves out its second
+ * load of K (V) and every pipeline wait gives up after 2 ms instead of 2 s, so that the warps waiting
+ * for it run out of time: the device records DA_ERR_DEVICE_TIMEOUT, nothing more is issued, copies in
+ * flight are waited for, and the run ends with unspecified results (with validate set, the call returns
+ * DA_ERR_DEVICE_TIMEOUT). This exercises the bounded-wait path without a fault. Not to be called while
+ * another thread runs the plan. Errors: INVALID_ARG, UNSUPPORTED (fp32 caches, whose kernel has no such
+ * wait). */
+int decode_attn_tree_debug_stall(da_tree_plan* plan, int tensor);
+
 /* Clear a new workspace's status word (a zero-filled allocation needs no call). Enqueued on
  * cuda_stream. Errors: INVALID_ARG, WORKSPACE_TOO_SMALL, CUDA. */
 int decode_attn_tree_workspace_init(const da_tree_plan* plan, void* workspace,

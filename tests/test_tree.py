@@ -755,3 +755,49 @@ def test_a_dropped_objects_workspace_waits_for_its_last_stream(what, given):
         assert not side.query() and all(t.data_ptr() != address for t in taken)
         torch.cuda.synchronize()
         del taken
+
+
+# ---- waits that run out of time ---------------------------------------------------------------
+def test_debug_stall_refuses_bad_arguments():
+    plan, _ = binding.decode_attn_tree_plan(_prob(), 8)
+    plain, _ = binding.decode_attn_tree_plan(_prob(qkv_dtype="f32", out_dtype="f32"), 8)
+    for p, tensor, code in ((plan, -1, -1), (plan, 3, -1), (plain, 1, -2), (None, 0, -1)):
+        with pytest.raises(binding.DecodeAttnError) as e:
+            binding.decode_attn_tree_debug_stall(p, tensor)
+        assert e.value.code == code
+    binding.decode_attn_tree_debug_stall(plan, 2)
+    binding.decode_attn_tree_debug_stall(plan, 0)
+    for p in (plan, plain):
+        binding.decode_attn_tree_destroy(p)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,kv", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("tensor", [1, 2])
+@pytest.mark.parametrize("d,page,new", [(128, 16, [6, 5]), (64, 0, [50, 3]), (128, 0, [64, 64])])
+def test_waits_that_run_out_of_time_end_the_run(dtype, kv, tensor, d, page, new):
+    """CTA 0 leaves out a load: every role gives up in turn, the run ends with the timeout recorded, and the same
+    object's next run is the plain one's, bit for bit."""
+    lay = Layout([3000, 2500], new, 2, d, page=page, hq=8, dtype=dtype, kv=kv, num_sms=8)
+    kc, vc = (c.cuda() for c in fill_normal(lay))
+    q = lay.normal(lay.rows, 8, d).cuda()
+    place = (lay.table.cuda() if page else None, lay.row_offsets.cuda(), lay.start.cuda())
+    t = binding.TreeAttention(lay.problem, 64)
+    ref, ref_lse = t.run(q, kc, vc, *place, None, 0.1)
+    t.check_status()
+    for _ in range(2):
+        binding.decode_attn_tree_debug_stall(t.plan, tensor)
+        t.run(q, kc, vc, *place, None, 0.1)
+        with pytest.raises(binding.DecodeAttnError) as e:
+            t.check_status()
+        assert e.value.code == -6
+        binding.decode_attn_tree_debug_stall(t.plan, 0)
+        out, lse = t.run(q, kc, vc, *place, None, 0.1)
+        t.check_status()
+        assert torch.equal(out.view(torch.int16), ref.view(torch.int16)) and torch.equal(lse, ref_lse)
+    lay.problem.validate = 1
+    strict = binding.TreeAttention(lay.problem, 64)
+    binding.decode_attn_tree_debug_stall(strict.plan, tensor)
+    with pytest.raises(binding.DecodeAttnError) as e:
+        strict.run(q, kc, vc, *place, None, 0.1)
+    assert e.value.code == -6

@@ -6,6 +6,7 @@
 // step's size (one row a sequence) the time is the launch and a chain of dependent loads.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -214,8 +215,7 @@ template <typename T, typename C, int VEC>
 __global__ void __launch_bounds__(kRowThreads, 7)
     rows_kernel(const __grid_constant__ RowParams p) {
   __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
-  __shared__ int s_info[2];   // member, cache row
-  __shared__ long long s_pos;
+  __shared__ int s_info[4];   // member, position (its low 32 bits, signed; 2^32 more?), cache row
   using V = RowVec<T, VEC>;
   using Raw = typename V::Raw;
   using PT = Packed<T, VEC>;
@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(kRowThreads, 7)
   if (h + step < heads) load(h + step, ra[1], rb[1]);
 
   long long z = -1;
-  long long pos = 0;   // (past 2^31 where a row lies far behind its cache: its q is rotated all the same)
+  int pos = 0;
+  bool far = false;   // past 2^31, where a row lies far behind its cache: its q is rotated all the same
   if (p.row_offsets) {
     if (tid == 0) {
       long long at = 0;
@@ -259,19 +260,22 @@ __global__ void __launch_bounds__(kRowThreads, 7)
       const bool member = locate_row(p.cache, p.row_offsets, p.start, row, at, zz);
       if (member && p.positions) at = __ldg(p.positions + row);
       s_info[0] = member;
-      s_info[1] = zz;
-      s_pos = at;
+      s_info[1] = (int)at;
+      s_info[2] = at > INT_MAX;
+      s_info[3] = zz;
     }
     __syncthreads();
     if (!s_info[0]) return;
-    pos = s_pos;
-    z = s_info[1];
+    pos = s_info[1];
+    far = s_info[2];
+    z = s_info[3];
   } else {
     pos = __ldg(p.positions + row);
   }
   if (p.rotary) {
     for (int i = tid; i < p.rotary / 2; i += kRowThreads) {
-      const unsigned long long a = (unsigned long long)pos * p.turn[i];
+      unsigned long long a = (unsigned long long)(long long)pos * p.turn[i];
+      if (far) a += p.turn[i] << 32;
       float s, c;
       sincospif((float)(int)(unsigned)(a >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
       s_cos[i] = c * p.m;

@@ -511,7 +511,7 @@ class _Workspace:
     another stream is noted with the allocator, so that the memory goes to nobody else before that call's
     kernels have ended, whenever the object is dropped."""
 
-    workspace = None
+    workspace = _noted = _noted_stream = None
 
     def _make_workspace(self, size, device):
         """Zero-filled, which needs no init call, and ready for any stream."""

@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(kRowThreads, 7)
       most_k = fmaxf(most_k, __shfl_xor_sync(0xffffffffu, most_k, o));
       most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, o));
     }
-    // non-negative floats order as their bits; a maximum does not depend on order
+    // non-negative floats order as their bits; a maximum does not depend on order (64 prompts of 300 rows into
+    // FP8 pages, rotary: 92.5 us with the maxima, 88.4 without)
     if ((tid & 31) == 0) {
       if (most_k > 0.f) atomicMax(reinterpret_cast<int*>(p.amax), __float_as_int(most_k));
       if (most_v > 0.f) atomicMax(reinterpret_cast<int*>(p.amax) + 1, __float_as_int(most_v));
@@ -442,17 +443,19 @@ struct ReadParams {
   int wide;                     // the outputs lie on 32-byte boundaries
 };
 
-constexpr int kReadThreads = 256;
+constexpr int kReadThreads = 256, kReadItems = 4;
 
 // The step's rows as one line of items (row, tensor, 16-byte chunk of the cache row). A warp takes
-// 32 * PER neighbouring items, PER a lane with all their loads in flight; its lanes look up the
+// 128 neighbouring items, 4 a lane with all their loads in flight; its lanes look up the
 // rows these touch, one row a lane, and pass the cache rows on by shuffles. They are at most 32: a
-// row of 8 items divides the 256 of PER = 8, one of 9 and more spans at most 30 rows, and shorter
-// ones (4 items: one tensor, one head of 64 codes) take PER = 2.
+// row has a multiple of 4 items, and one of 4 (one tensor, one head of 64 codes) starts where a
+// warp does. (8 a lane: up to 4 % slower below 2e6 items, the same above, bf16 and fp32; for FP8, whose results take
+// twice the registers, 266 us instead of 244 below.)
 // Bound by HBM: 64 sequences of 512 to 8192 FP8 tokens to bf16 (1.7 GB) 244 us, 7.0 TB/s (a plain
 // copy: 6.7); a warp a row, with its lookup ahead of its loads, took 346.
-template <typename T, typename C, int PER>
+template <typename T, typename C>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
+  constexpr int PER = kReadItems;
   constexpr bool kFp8 = std::is_same<C, fp8e4m3>::value;
   const int lane = threadIdx.x & 31;
   const long long i0 =
@@ -514,14 +517,6 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
       }
     }
   }
-}
-
-template <typename T, typename C>
-const void* read_kernel_for(int per) {
-  if (per == 2) return reinterpret_cast<const void*>(&read_kernel<T, C, 2>);
-  if constexpr (!std::is_same<C, fp8e4m3>::value)
-    if (per == 8) return reinterpret_cast<const void*>(&read_kernel<T, C, 8>);
-  return reinterpret_cast<const void*>(&read_kernel<T, C, 4>);
 }
 
 // Checks that the write and the read share; the status word when a workspace is given.
@@ -778,23 +773,20 @@ int decode_attn_kv_read(const da_plan* plan, const da_kv_read_args* args) {
   p.rows = a.rows;
   p.chunks = pr.num_kv_heads * pr.head_dim * pl.kv_es / 16;
   p.row_items = p.chunks * nt;
-  // i / n = umulhi(i, ceil(2^32 / n)) for i n < 2^32: here i < row_items + 256 and n = row_items,
+  // i / n = umulhi(i, ceil(2^32 / n)) for i n < 2^32: here i < row_items + 128 and n = row_items,
   // or i < row_items and n = chunks, which caps row_items at 2^15
   if (p.row_items > (1 << 15)) return DA_ERR_UNSUPPORTED;
   p.row_magic = (unsigned)(((1ull << 32) + p.row_items - 1) / p.row_items);
   p.chunk_magic = (unsigned)(((1ull << 32) + p.chunks - 1) / p.chunks);
   p.items = (long long)p.rows * p.row_items;
   p.wide = aligned(a.k_out, 32) && aligned(a.v_out, 32);
-  // Items a lane. FP8: 4 (1.7 GB to bf16: 244 us, with 8, whose results take twice the registers, 266).
-  // Plain copies: 8 where there are enough items to fill the GPU's warps (2.1 GB of bf16: 325 us, with 4
-  // 331; 33 MB: 8.2 us, with 4 6.2).
-  const int per = p.row_items < 8 ? 2 : !pr.kv_fp8 && p.items >= (1ll << 21) ? 8 : 4;
-  const long long per_block = (long long)kReadThreads * per;
+  const long long per_block = (long long)kReadThreads * kReadItems;
   const long long blocks = (p.items + per_block - 1) / per_block;
   if (blocks >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
-  const void* fn = pr.kv_fp8                ? read_kernel_for<__nv_bfloat16, fp8e4m3>(per)
-                   : pr.qkv_dtype == DA_F32 ? read_kernel_for<float, float>(per)
-                                            : read_kernel_for<__half, __half>(per);   // moved as bits
+  const void* fn = pr.kv_fp8 ? reinterpret_cast<const void*>(&read_kernel<__nv_bfloat16, fp8e4m3>)
+                   : pr.qkv_dtype == DA_F32
+                       ? reinterpret_cast<const void*>(&read_kernel<float, float>)
+                       : reinterpret_cast<const void*>(&read_kernel<__half, __half>);   // moved as bits
   cudaStream_t stream = static_cast<cudaStream_t>(a.cuda_stream);
   rc = clear_status(pl, a.workspace, stream);
   if (rc != DA_OK) return rc;

@@ -795,3 +795,28 @@ def test_positions_past_31_bits_rotate_q(dtype):
     tol = size * (4e-7 + 3 * 2.0 ** -24 + 2.0 ** 31 * 2 * math.pi * 2.0 ** -51) + want.abs() * half_step(x.dtype)
     tol = tol + want.abs() * half_step(TORCH[dtype]) * 1.001
     assert ((out.cpu().double() - want).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,kv,hkv,d", [("bf16", "e4m3", 1, 64), ("bf16", "bf16", 1, 64), ("f32", "f32", 1, 64),
+                                            ("bf16", "e4m3", 3, 64), ("bf16", "e4m3", 5, 128)])
+def test_reads_of_short_and_odd_rows_at_every_length(dtype, kv, hkv, d):
+    """Rows of 4 items and more, one tensor and both, row counts around a warp's and a block's items."""
+    for rows in (1, 2, 31, 32, 33, 255, 256, 257, 1023, 1025):
+        lay = Layout([5, 40], [rows, 3], hkv, d, page=8, dtype=dtype, kv=kv, before=1, behind=2, seed=rows)
+        io = binding.KVCacheIO(lay.problem)
+        kc, vc = lay.cache(), lay.cache()
+        place = (lay.table.cuda(), lay.row_offsets.cuda(), lay.start.cuda())
+        member = torch.tensor([b >= 0 for b in lay.row_seq])
+        z = torch.tensor([lay.cache_row(b, t) for b, t in zip(lay.row_seq, lay.row_pos) if b >= 0])
+        for which in ((0,), (1,), (0, 1)):
+            src = [(kc, vc)[i].cuda() if i in which else None for i in range(2)]
+            out = [torch.full((lay.rows, hkv, d), 9.0, dtype=TORCH[dtype], device="cuda") if i in which else None
+                   for i in range(2)]
+            io.read(*src, *place, *out)
+            for i, scale in zip(range(2), (lay.k_scale, lay.v_scale)):
+                if i in which:
+                    want = (kc, vc)[i].reshape(-1, hkv, d)[z]
+                    if kv == "e4m3":
+                        want = (want.view(torch.float8_e4m3fn).float() * torch.tensor(scale)).to(TORCH[dtype])
+                    assert torch.equal(out[i].cpu()[member], want) and (out[i].cpu()[~member] == 9.0).all()

@@ -16,18 +16,19 @@
 // 2^-23 of it or 2^-36 of the row's largest, whichever is more:
 // a bf16 P alone would cost as much accuracy as the bf16 output. The second product costs tensor
 // time only where the step is not bound by memory. FP8 caches run on f16 operands (E4M3 codes are f16
-// numbers); one f16 a weight would take 336 instead of 397 us (64 drafted, 64 x 4350 tokens; 8 drafted 167
-// instead of 222), but answer a drafted token less exactly than the decode step over the same cache, and cost
+// numbers); one f16 a weight took 339 instead of 386 us (64 drafted, 64 x 4350 tokens; 8 drafted 181
+// instead of 195), but answered a drafted token less exactly than the decode step over the same cache, and cost
 // an f16 result as much as its own rounding. q enters f16 scaled by a power of two per row, exact for every element above 2^-29 of the
 // row's largest.
 //
 // What bounds it. 16-bit, up to 128 rows: the KV stream (64 KB of K and V a tile take an SM 2800 cycles at
-// the HBM rate, the MMAs 1536): 64 paged sequences of 512 to 8192 tokens with 3 to 12 drafted, 196 us, 5.9
-// TB/s, 88 % of a copy. With R row tiles every tile is read R times (once from HBM, then L2) and softmax and
-// MMAs are even: 64 drafted tokens over 64 x 4350 cost 352 us, 836 TFLOP/s. FP8: the chain S, softmax, O over
-// two buffers (4800 cycles for two tiles), the conversion (192 KB a tile through shared memory) and the
-// fetching of instructions for the many roles are even, whatever the rows: 8 drafted tokens 167 us (3.4
-// TB/s), 64 drafted tokens 332 us (886 TFLOP/s). A single long sequence (32768 tokens, 16 drafted) takes 35
+// the HBM rate, the MMAs 1536): 64 paged sequences of 512 to 8192 tokens with 3 to 12 drafted, 197 us, 5.8
+// TB/s, 87 % of a copy. With R row tiles every tile is read R times (once from HBM, then L2) and no part is the
+// full one: 64 drafted tokens over 64 x 4350 cost 348 us, 846 TFLOP/s; without the second product of P's parts 6 %
+// less, without forming them 6 %, without both 11 %. FP8: the chain S, softmax, O over two buffers (6300 cycles
+// for two tiles), the conversion (192 KB a tile through shared memory) and the fetching of instructions for the
+// many roles (a vote for a branch in every wait: 205 to 195 us) are even, whatever the rows: 8 drafted tokens 195
+// us (2.9 TB/s), 64 drafted tokens 386 us (762 TFLOP/s). A single long sequence (32768 tokens, 16 drafted) takes 35
 // us: 20 of stream, about 6 until the first tile is there (the schedule 2), the rest O's way out and the merge.
 #include <type_traits>
 
@@ -216,11 +217,7 @@ struct Waiter {
   bool dead;
   // warp-uniform
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    if (dead) {
-      __syncwarp();   // (what follows a wait may need a converged warp)
-      return;
-    }
-    bool ok = mbar_try_wait(bar, parity);
+    bool ok = dead || mbar_try_wait(bar, parity);   // (the vote converges the warp either way)
     if (!__all_sync(0xffffffffu, ok)) {
       const unsigned long long t0 = global_timer_ns();
       while (!ok) {

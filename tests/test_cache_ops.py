@@ -820,3 +820,23 @@ def test_reads_of_short_and_odd_rows_at_every_length(dtype, kv, hkv, d):
                     if kv == "e4m3":
                         want = (want.view(torch.float8_e4m3fn).float() * torch.tensor(scale)).to(TORCH[dtype])
                     assert torch.equal(out[i].cpu()[member], want) and (out[i].cpu()[~member] == 9.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,kv", KINDS)
+def test_q_is_rotated_in_place_beside_k_and_v(dtype, kv):
+    """q, k and v as parts of one projection's rows, q rotated where it lies: the same as into a tensor of its own,
+    and k and v keep their values."""
+    lay = Layout([30, 4], [50, 3], 2, 64, page=16, hq=8, dtype=dtype, kv=kv)
+    io = binding.KVCacheIO(lay.problem)
+    r = binding.Rope(64)
+    wide = lay.normal(lay.rows, 12, 64).cuda()
+    kept = wide.clone()
+    place = (lay.table.cuda(), lay.row_offsets.cuda(), lay.start.cuda())
+    a, b = ([lay.cache().cuda().zero_() for _ in range(2)] for _ in range(2))
+    q = io.write(wide[:, 8:10], wide[:, 10:], *a, *place, rope=r, q=wide[:, :8])
+    same = io.write(wide[:, 8:10], wide[:, 10:], *b, *place, rope=r, q=wide[:, :8], q_out=wide[:, :8])
+    assert same.data_ptr() == wide.data_ptr() and torch.equal(same, q)
+    assert torch.equal(wide[:, 8:], kept[:, 8:]) and all(torch.equal(x, y) for x, y in zip(a, b))
+    with pytest.raises(binding.DecodeAttnError):
+        io.write(wide[:, 8:10], wide[:, 10:], *b, *place, rope=r, q=kept[:, :8], q_out=wide[:, 2:10])

@@ -20,12 +20,15 @@ DA_SOFTMAX_SYNC, DA_SOFTMAX_UNIFIED, DA_SOFTMAX_UNIFIED_LOCAL = 0, 1, 2
 ERRORS = {0: "DA_OK", -1: "DA_ERR_INVALID_ARG", -2: "DA_ERR_UNSUPPORTED",
           -3: "DA_ERR_WORKSPACE_TOO_SMALL", -4: "DA_ERR_BAD_BLOCK_TABLE", -5: "DA_ERR_CUDA",
           -6: "DA_ERR_DEVICE_TIMEOUT", -7: "DA_ERR_BAD_SEQ_LEN", -8: "DA_ERR_HISTOGRAM_RANGE",
-          -9: "DA_ERR_RANGE_TOO_WIDE"}
+          -9: "DA_ERR_RANGE_TOO_WIDE", -10: "DA_ERR_NO_PAGES"}
 DA_ERR_RANGE_TOO_WIDE = -9
 MAX_HIST_BINS = 32768
 MAX_TREE = 64
+POOL_HEAD = 4
+ADAPTER_PARTS = 4
 DTYPE_CODES = {"f32": DA_F32, "f16": DA_F16, "bf16": DA_BF16}
 ROPE_CODES = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "by_index": 4}
+SCALING_CODES = {"tensor": 1, "row": 2, "group": 3}
 MODE_CODES = {"sync": DA_SOFTMAX_SYNC, "unified": DA_SOFTMAX_UNIFIED,
               "unified_local": DA_SOFTMAX_UNIFIED_LOCAL}
 
@@ -221,6 +224,101 @@ class da_tree_args(ctypes.Structure):
     ]
 
 
+class da_pages_reserve_args(ctypes.Structure):
+    _fields_ = [
+        ("pool", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("row_offsets", ctypes.c_void_p),
+        ("ctx_lens", ctypes.c_void_p),
+        ("rows", ctypes.c_int),
+        ("seq_lens", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("cuda_stream", ctypes.c_void_p),
+    ]
+
+
+class da_pages_release_args(ctypes.Structure):
+    _fields_ = [
+        ("pool", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
+        ("keep_lens", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("cuda_stream", ctypes.c_void_p),
+    ]
+
+
+class da_norm_config(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int),
+        ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+    ]
+
+
+class da_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("residual_out", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("dtype", ctypes.c_int),
+        ("weight_f32", ctypes.c_int),
+        ("scaling", ctypes.c_int),
+        ("group", ctypes.c_int),
+        ("rows", ctypes.c_int),
+        ("heads", ctypes.c_int),
+        ("x_row_stride", ctypes.c_int64),
+        ("x_head_stride", ctypes.c_int64),
+        ("residual_row_stride", ctypes.c_int64),
+        ("residual_head_stride", ctypes.c_int64),
+        ("residual_out_row_stride", ctypes.c_int64),
+        ("residual_out_head_stride", ctypes.c_int64),
+        ("out_row_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("codes_row_stride", ctypes.c_int64),
+        ("codes_head_stride", ctypes.c_int64),
+        ("cuda_stream", ctypes.c_void_p),
+    ]
+
+
+class da_adapter_config(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("width", ctypes.c_int),
+        ("parts", ctypes.c_int),
+        ("out_sizes", ctypes.c_int * ADAPTER_PARTS),
+        ("rank", ctypes.c_int),
+    ]
+
+
+class da_adapter_args(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("a", ctypes.c_void_p),
+        ("b", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("row_offsets", ctypes.c_void_p),
+        ("adapter_ids", ctypes.c_void_p),
+        ("rows", ctypes.c_int),
+        ("batch", ctypes.c_int),
+        ("adapters", ctypes.c_int),
+        ("x_row_stride", ctypes.c_int64),
+        ("y_row_stride", ctypes.c_int64),
+        ("out_row_stride", ctypes.c_int64),
+        ("cuda_stream", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 P = ctypes.c_void_p
 
@@ -270,6 +368,12 @@ def lib():
         L.decode_attn_tree_check_status.argtypes = [P, P, P]
         L.decode_attn_tree_destroy.argtypes = [P]
         L.decode_attn_tree_destroy.restype = None
+        L.decode_attn_pages_init.argtypes = [P, P, P]
+        L.decode_attn_pages_reserve.argtypes = [P, ctypes.POINTER(da_pages_reserve_args)]
+        L.decode_attn_pages_release.argtypes = [P, ctypes.POINTER(da_pages_release_args)]
+        L.decode_attn_norm_apply.argtypes = [ctypes.POINTER(da_norm_config), ctypes.POINTER(da_norm_args)]
+        L.decode_attn_adapters_apply.argtypes = [ctypes.POINTER(da_adapter_config),
+                                                 ctypes.POINTER(da_adapter_args)]
         L.decode_attn_rope_destroy.argtypes = [P]
         L.decode_attn_rope_destroy.restype = None
         L.decode_attn_destroy.argtypes = [P]
@@ -287,7 +391,10 @@ def lib():
                      "decode_attn_tree_plan", "decode_attn_tree_plan_info",
                      "decode_attn_tree_debug_stall",
                      "decode_attn_tree_workspace_init", "decode_attn_tree_run",
-                     "decode_attn_tree_check_status", "decode_attn_abi_version"):
+                     "decode_attn_tree_check_status", "decode_attn_pages_init",
+                     "decode_attn_pages_reserve", "decode_attn_pages_release",
+                     "decode_attn_norm_apply", "decode_attn_adapters_apply",
+                     "decode_attn_abi_version"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -473,6 +580,28 @@ def decode_attn_tree_check_status(plan, workspace: int, stream: int = 0):
 
 def decode_attn_tree_destroy(plan):
     lib().decode_attn_tree_destroy(plan)
+
+
+def decode_attn_pages_init(plan, pool: int, stream: int = 0):
+    _check(lib().decode_attn_pages_init(plan, pool, stream or None), "decode_attn_pages_init")
+
+
+def decode_attn_pages_reserve(plan, args: da_pages_reserve_args):
+    _check(lib().decode_attn_pages_reserve(plan, ctypes.byref(args)), "decode_attn_pages_reserve")
+
+
+def decode_attn_pages_release(plan, args: da_pages_release_args):
+    _check(lib().decode_attn_pages_release(plan, ctypes.byref(args)), "decode_attn_pages_release")
+
+
+def decode_attn_norm_apply(config: da_norm_config, args: da_norm_args):
+    _check(lib().decode_attn_norm_apply(ctypes.byref(config), ctypes.byref(args)),
+           "decode_attn_norm_apply")
+
+
+def decode_attn_adapters_apply(config: da_adapter_config, args: da_adapter_args):
+    _check(lib().decode_attn_adapters_apply(ctypes.byref(config), ctypes.byref(args)),
+           "decode_attn_adapters_apply")
 
 
 def decode_attn_destroy(plan):
@@ -983,3 +1112,277 @@ class TreeAttention(_Workspace):
     def check_status(self, stream=None):
         """Synchronise, then raise the first finding recorded since the last call."""
         _check_workspace(decode_attn_tree_check_status, self, stream)
+
+
+class PageTables(_Workspace):
+    """Pages of the problem's paged cache: new_pool() makes a pool with every page free, reserve() takes a
+    step's pages off it and enters them in the block table, release() gives back what sequences lose.
+
+    A pool is an int32 tensor [POOL_HEAD + num_physical_blocks] (the C header says what is in it). Calls on
+    one pool must not overlap on the GPU. With findings=True (or the problem's validate) the device records
+    bad lengths and entries, and steps that the pool had too few pages for, which check_status() reports."""
+
+    def __init__(self, problem: da_problem, findings: bool = False, device=None):
+        self._reserve = _entry("decode_attn_pages_reserve", da_pages_reserve_args)
+        self._release = _entry("decode_attn_pages_release", da_pages_release_args)
+        self.problem = problem
+        self.plan, self.workspace_bytes = decode_attn_plan(problem, 0)
+        if not problem.paged:
+            raise ValueError("a contiguous cache has no pages")
+        self._batch, self._table = problem.batch, problem.batch * problem.max_blocks_per_seq
+        self._pool = POOL_HEAD + problem.num_physical_blocks
+        if findings or problem.validate:
+            self._make_workspace(self.workspace_bytes, device)
+
+    def __del__(self):
+        plan = getattr(self, "plan", None)
+        if plan is not None and _lib is not None:
+            decode_attn_destroy(plan)
+            self.plan = None
+
+    def new_pool(self, device=None, stream=None):
+        """A pool whose pages are all free, page 0 on top."""
+        device = _torch.device("cuda") if device is None else _torch.device(device)
+        pool = _empty((self._pool,), _torch.int32, device, stream)
+        with _torch.cuda.device(pool.device):
+            s = stream if stream is not None else _torch.cuda.current_stream()
+            decode_attn_pages_init(self.plan, pool.data_ptr(), s.cuda_stream)
+        return pool
+
+    def _places(self, pool, block_table, lens, others):
+        _int32("pool", pool, self._pool)
+        _int32("block_table", block_table, self._table)
+        _int32("the sequences' lengths", lens, self._batch)
+        index, ws = pool.get_device(), self.workspace
+        away = index < 0 or block_table.get_device() != index or lens.get_device() != index or \
+            (ws is not None and ws.get_device() != index)
+        for t in others:
+            away = away or t.get_device() != index
+        if away:
+            _refuse_devices(index, pool=pool, block_table=block_table, lengths=lens, workspace=ws,
+                            **{f"tensor {i}": t for i, t in enumerate(others)})
+        return index
+
+    def reserve(self, pool, block_table, row_offsets, ctx_lens, rows: int, seq_lens=None, slots=None,
+                positions=None, stream=None):
+        """Pages for a step of `rows` rows: sequence b holds ctx_lens[b] tokens and gets the rows row_offsets[b]
+        to row_offsets[b + 1]. Returns (seq_lens, slots, positions): the lengths then (ctx_lens itself: in
+        place), each row's cache row (-1: none) and position; allocated when None. Where the pool has too few
+        pages nothing is taken, every slot is -1 and pool[1] says how many were missing."""
+        _int32("row_offsets", row_offsets, self._batch + 1)
+        if rows < 0:
+            raise ValueError("rows must not be negative")
+        if seq_lens is None:
+            seq_lens = _empty((self._batch,), _torch.int32, pool.device, stream)
+        if slots is None:
+            slots = _empty((rows,), _torch.int32, pool.device, stream)
+        if positions is None:
+            positions = _empty((rows,), _torch.int32, pool.device, stream)
+        _int32("seq_lens", seq_lens, self._batch)
+        _int32("slots", slots, rows)
+        _int32("positions", positions, rows)
+        index = self._places(pool, block_table, ctx_lens, (row_offsets, seq_lens, slots, positions))
+        self._reserve(self.plan, index, stream, pool.data_ptr(), block_table.data_ptr(), row_offsets.data_ptr(),
+                      ctx_lens.data_ptr(), rows, seq_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+                      0 if self.workspace is None else self._workspace_on(index, stream), self.workspace_bytes)
+        return seq_lens, slots, positions
+
+    def release(self, pool, block_table, seq_lens, keep_lens, stream=None):
+        """Cut sequences back from seq_lens[b] to keep_lens[b] tokens (0: it has ended): the pages they lose
+        go back to the pool, and their entries become -1."""
+        _int32("keep_lens", keep_lens, self._batch)
+        index = self._places(pool, block_table, seq_lens, (keep_lens,))
+        self._release(self.plan, index, stream, pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                      keep_lens.data_ptr(), 0 if self.workspace is None else self._workspace_on(index, stream),
+                      self.workspace_bytes)
+
+    def check_status(self, stream=None):
+        """Synchronise, then raise the first finding recorded since the last call."""
+        if self.workspace is None:
+            raise ValueError("made without findings")
+        _check_workspace(decode_attn_check_status, self, stream)
+
+
+def _refuse_autograd(**tensors):
+    if _torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name} requires a gradient, which this call has none of: use no_grad()")
+
+
+class RMSNorm:
+    """A root-mean-square norm of rows of n elements: y = u (weight + weight_offset) / sqrt(mean(u^2) + eps),
+    u = x + residual where one is given, rounded to the type.
+
+    x is [rows, n], or [rows, heads, n] (q or k heads), fp32, fp16 or bf16; rows and heads may be strided.
+    The weight ([n], None: without one) is of x's type or fp32. Autograd records neither call; tensors that
+    require a gradient are refused outside no_grad()."""
+
+    def __init__(self, n: int, eps: float = 1e-6, weight_offset: float = 0.0):
+        self._apply = _entry("decode_attn_norm_apply", da_norm_args)
+        if not 1 <= n <= 32768:
+            raise ValueError("n must be 1 to 32768")
+        self.n, self.config = n, da_norm_config(n, eps, weight_offset)
+        self._at = ctypes.addressof(self.config)
+        from .workloads import TORCH_DTYPES
+        self._codes = {TORCH_DTYPES[k]: v for k, v in DTYPE_CODES.items()}
+
+    def apply(self, x, weight=None, residual=None, out=None, residual_out=None, stream=None):
+        """y in x's type, into `out` (x itself: in place; allocated when None). With a residual returns
+        (out, u): u goes into residual_out (x or residual itself: in place; allocated when None)."""
+        if out is None:
+            out = _empty(x.shape, x.dtype, x.device, stream)
+        total = self._call(x, weight, residual, out, residual_out, None, None, 0, 0, stream)
+        return out if residual is None else (out, total)
+
+    def quantise(self, x, weight=None, residual=None, scaling: str = "row", group: int = 128, codes=None,
+                 scales=None, out=None, residual_out=None, stream=None):
+        """E4M3 codes of y / scale (float8_e4m3fn, or their bytes where `codes` is uint8). scaling "tensor":
+        `scales` is a float32 tensor of one element; "row": one found for each row (and head); "group": one for
+        each `group` (32, 64 or 128) elements. Where `out` is given it takes y too. Returns
+        (codes, scales, u), u as in apply() and None without a residual."""
+        kind = SCALING_CODES.get(scaling)
+        if kind is None:
+            raise ValueError(f"scaling must be one of {sorted(SCALING_CODES)}")
+        if kind == 3 and group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        if codes is None:
+            codes = _empty(x.shape, _torch.float8_e4m3fn, x.device, stream)
+        elif codes.dtype is not _torch.float8_e4m3fn and codes.dtype is not _torch.uint8:
+            raise ValueError("codes must be float8_e4m3fn or uint8")
+        shape = (1,) if kind == 1 else x.shape[:-1] if kind == 2 else \
+            (*x.shape[:-1], -(-self.n // group))
+        if scales is None:
+            if kind == 1:
+                raise ValueError("scaling by tensor takes scales")
+            scales = _empty(shape, _torch.float32, x.device, stream)
+        elif scales.dtype is not _torch.float32 or not scales.is_contiguous() or \
+                (scales.numel() != 1 if kind == 1 else scales.shape != shape):
+            raise ValueError(f"scales must be a contiguous float32 tensor {list(shape)}")
+        total = self._call(x, weight, residual, out, residual_out, codes, scales, kind, group, stream)
+        return codes, scales, total
+
+    def _rows(self, name, t, shape, dtype):
+        if t.shape != shape or t.dtype is not dtype:
+            raise ValueError(f"{name} must be a {list(shape)} tensor of {dtype}")
+        st = t.stride()
+        if st[-1] != 1 and self.n > 1 and t.numel():
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+        return (st[0], 0) if len(st) == 2 else (st[0], st[1])
+
+    def _call(self, x, weight, residual, out, residual_out, codes, scales, kind, group, stream):
+        shape, dtype = x.shape, x.dtype
+        code = self._codes.get(dtype)
+        if code is None:
+            raise ValueError("x must be fp32, fp16 or bf16")
+        if not 2 <= len(shape) <= 3 or shape[-1] != self.n:
+            raise ValueError(f"x must be a [rows, {self.n}] or [rows, heads, {self.n}] tensor")
+        if _torch.is_grad_enabled():
+            _refuse_autograd(x=x, weight=weight, residual=residual, out=out, residual_out=residual_out)
+        xs, index = self._rows("x", x, shape, dtype), x.get_device()
+        rs = us = os_ = cs = (0, 0)
+        res_at = u_at = out_at = code_at = scale_at = weight_at = wide = 0
+        away = index < 0
+        if residual is not None:
+            if residual_out is None:
+                residual_out = _empty(shape, dtype, x.device, stream)
+            rs, us = self._rows("residual", residual, shape, dtype), self._rows("residual_out", residual_out, shape, dtype)
+            res_at, u_at = residual.data_ptr(), residual_out.data_ptr()
+            away = away or residual.get_device() != index or residual_out.get_device() != index
+        elif residual_out is not None:
+            raise ValueError("residual_out without a residual")
+        if weight is not None:
+            wide = weight.dtype is _torch.float32
+            if (not wide and weight.dtype is not dtype) or weight.shape != (self.n,) or not weight.is_contiguous():
+                raise ValueError(f"weight must be a contiguous [{self.n}] tensor of {dtype} or float32")
+            weight_at = weight.data_ptr()
+            away = away or weight.get_device() != index
+        if out is not None:
+            os_, out_at = self._rows("out", out, shape, dtype), out.data_ptr()
+            away = away or out.get_device() != index
+        if codes is not None:
+            cs, code_at, scale_at = self._rows("codes", codes, shape, codes.dtype), codes.data_ptr(), scales.data_ptr()
+            away = away or codes.get_device() != index or scales.get_device() != index
+        if away:
+            _refuse_devices(index, x=x, residual=residual, residual_out=residual_out, weight=weight, out=out,
+                            codes=codes, scales=scales)
+        rows, heads = shape[0], 1 if len(shape) == 2 else shape[1]
+        if rows and heads:
+            self._apply(self._at, index, stream, x.data_ptr(), res_at, weight_at, u_at, out_at, code_at, scale_at,
+                        code, 1 if wide else 0, kind, group, rows, heads, *xs, *rs, *us, *os_, *cs)
+        return residual_out
+
+
+class Adapters:
+    """Low-rank adapters of many requests beside a shared projection of rows of `width` to columns in parts
+    of out_sizes (q, k and v, for instance): out = y + scales[a] (x A_a^T) B_a^T, part by part.
+
+    a: [adapters, parts * rank, width] (or [adapters, parts, rank, width]), b: [adapters, columns, rank],
+    contiguous, of `dtype` ("f32", "f16", "bf16") as x and y are. Autograd does not record the call; tensors
+    that require a gradient are refused outside no_grad()."""
+
+    def __init__(self, width: int, out_sizes, rank: int, dtype: str = "bf16"):
+        self._apply = _entry("decode_attn_adapters_apply", da_adapter_args)
+        out_sizes = [int(n) for n in out_sizes]
+        if not 1 <= len(out_sizes) <= ADAPTER_PARTS or min(out_sizes) < 1 or width < 1:
+            raise ValueError(f"a projection has 1 to {ADAPTER_PARTS} parts, of at least a column each")
+        if rank not in (8, 16, 32, 64, 128):
+            raise ValueError("rank must be 8, 16, 32, 64 or 128")
+        if dtype not in DTYPE_CODES:
+            raise ValueError(f"dtype must be one of {sorted(DTYPE_CODES)}")
+        from .workloads import TORCH_DTYPES
+        self.width, self.out_sizes, self.rank, self.dtype = width, out_sizes, rank, TORCH_DTYPES[dtype]
+        self.columns = sum(out_sizes)
+        self.config = da_adapter_config(DTYPE_CODES[dtype], width, len(out_sizes),
+                                        (ctypes.c_int * ADAPTER_PARTS)(*out_sizes), rank)
+        self._at = ctypes.addressof(self.config)
+        self._one = (len(out_sizes) * rank * width, self.columns * rank)
+
+    def _rows(self, name, t, n):
+        if t.dtype is not self.dtype or len(t.shape) != 2 or t.shape[1] != n:
+            raise ValueError(f"{name} must be a [rows, {n}] tensor of {self.dtype}")
+        row, one = t.stride()
+        if one != 1 and n > 1 and t.numel():
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+        return row
+
+    def apply(self, x, y, a, b, scales, row_offsets, adapter_ids, out=None, stream=None):
+        """x [rows, width] and y [rows, columns] (rows may be strided), rows by request (row_offsets int32
+        [batch + 1]), adapter_ids int32 [batch] (-1: none), scales float32 [adapters] or None. Returns out
+        (y itself: in place; allocated when None)."""
+        if _torch.is_grad_enabled():
+            _refuse_autograd(x=x, y=y, a=a, b=b, scales=scales, out=out)
+        if out is None:
+            out = _empty(y.shape, self.dtype, y.device, stream)
+        x_row, y_row, out_row = self._rows("x", x, self.width), self._rows("y", y, self.columns), \
+            self._rows("out", out, self.columns)
+        rows, n = x.shape[0], a.shape[0]
+        if y.shape[0] != rows or out.shape[0] != rows:
+            raise ValueError("x, y and out must have as many rows")
+        if a.dtype is not self.dtype or n < 1 or a.numel() != n * self._one[0] or a.shape[-1] != self.width or \
+                not a.is_contiguous():
+            raise ValueError(f"a must be a contiguous [adapters, {len(self.out_sizes) * self.rank}, {self.width}] "
+                             f"tensor of {self.dtype}")
+        if b.dtype is not self.dtype or b.shape != (n, self.columns, self.rank) or not b.is_contiguous():
+            raise ValueError(f"b must be a contiguous [{n}, {self.columns}, {self.rank}] tensor of {self.dtype}")
+        batch = adapter_ids.numel()
+        _int32("adapter_ids", adapter_ids, batch)
+        _int32("row_offsets", row_offsets, batch + 1)
+        if batch < 1:
+            raise ValueError("a step has at least one request")
+        scale_at, index = 0, x.get_device()
+        away = index < 0 or y.get_device() != index or out.get_device() != index or a.get_device() != index or \
+            b.get_device() != index or row_offsets.get_device() != index or adapter_ids.get_device() != index
+        if scales is not None:
+            if scales.dtype is not _torch.float32 or scales.numel() != n or not scales.is_contiguous():
+                raise ValueError(f"scales must be a contiguous float32 tensor of {n} elements")
+            scale_at = scales.data_ptr()
+            away = away or scales.get_device() != index
+        if away:
+            _refuse_devices(index, x=x, y=y, out=out, a=a, b=b, scales=scales, row_offsets=row_offsets,
+                            adapter_ids=adapter_ids)
+        if rows:
+            self._apply(self._at, index, stream, x.data_ptr(), y.data_ptr(), out.data_ptr(), a.data_ptr(),
+                        b.data_ptr(), scale_at, row_offsets.data_ptr(), adapter_ids.data_ptr(), rows, batch, n,
+                        x_row, y_row, out_row)
+        return out

@@ -1,0 +1,121 @@
+// da_adapters.cu -- low-rank adapters of many requests beside a shared projection: checks and launch.
+#include <algorithm>
+#include <climits>
+
+#include "da_adapters.cuh"
+#include "da_plan.h"
+
+using namespace da;
+
+namespace {
+
+bool begins_on_16(const void* p, long long stride, int es) { return aligned(p, 16) && stride * es % 16 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter_args* args) {
+  if (!config || !args) return DA_ERR_INVALID_ARG;
+  const da_adapter_config& c = *config;
+  const da_adapter_args& a = *args;
+  if (c.width < 1 || c.parts < 1 || a.rows < 0 || a.batch < 1 || a.adapters < 1) return DA_ERR_INVALID_ARG;
+  if (c.dtype < DA_F32 || c.dtype > DA_BF16 || c.parts > DECODE_ATTN_ADAPTER_PARTS ||
+      (c.rank != 8 && c.rank != 16 && c.rank != 32 && c.rank != 64 && c.rank != 128) ||
+      c.width > DECODE_ATTN_ADAPTER_MAX_WIDTH || a.adapters > DECODE_ATTN_MAX_ADAPTERS ||
+      a.batch > DECODE_ATTN_MAX_PAGED_BATCH)
+    return DA_ERR_UNSUPPORTED;
+  AdapterParams p = {};
+  long long columns = 0;
+  for (int s = 0; s < c.parts; ++s) {
+    if (c.out_sizes[s] < 1) return DA_ERR_INVALID_ARG;
+    if (c.out_sizes[s] > DECODE_ATTN_ADAPTER_MAX_WIDTH) return DA_ERR_UNSUPPORTED;
+    p.starts[s] = (int)columns;
+    columns += c.out_sizes[s];
+    p.chunks[s + 1] = p.chunks[s] + (c.out_sizes[s] + 31) / 32;
+  }
+  p.starts[c.parts] = (int)columns;
+  if (a.rows == 0) return DA_OK;
+  const int es = elem_size(c.dtype);
+  if (!a.x || !a.y || !a.out || !a.a || !a.b || !a.row_offsets || !a.adapter_ids || !aligned(a.x, es) ||
+      !aligned(a.y, es) || !aligned(a.out, es) || !aligned(a.a, 16) || !aligned(a.b, 16) || !aligned(a.scales, 4) ||
+      !aligned(a.row_offsets, 4) || !aligned(a.adapter_ids, 4))
+    return DA_ERR_INVALID_ARG;
+  const int low = c.parts * c.rank;
+  const RowRuns x = runs(a.x, a.rows, a.x_row_stride, 1, 0, c.width, es);
+  const RowRuns y = runs(a.y, a.rows, a.y_row_stride, 1, 0, (int)columns, es);
+  const RowRuns out = runs(a.out, a.rows, a.out_row_stride, 1, 0, (int)columns, es);
+  auto flat = [](const void* at, long long bytes) { return RowRuns{(uint64_t)(uintptr_t)at, 1, 0, 1, 0, bytes}; };
+  if (!lie_apart(out) || !result_ok(y, out) || may_share(x, out) ||
+      may_share(flat(a.a, (long long)a.adapters * low * c.width * es), out) ||
+      may_share(flat(a.b, (long long)a.adapters * columns * c.rank * es), out) ||
+      (a.scales && may_share(flat(a.scales, 4ll * a.adapters), out)) ||
+      may_share(flat(a.row_offsets, 4ll * (a.batch + 1)), out) || may_share(flat(a.adapter_ids, 4ll * a.batch), out))
+    return DA_ERR_INVALID_ARG;
+  p.x = a.x;
+  p.y = a.y;
+  p.out = a.out;
+  p.a = a.a;
+  p.b = a.b;
+  p.scales = a.scales;
+  p.row_offsets = a.row_offsets;
+  p.ids = a.adapter_ids;
+  p.x_rs = a.x_row_stride;
+  p.y_rs = a.y_row_stride;
+  p.out_rs = a.out_row_stride;
+  p.rows = a.rows;
+  p.batch = a.batch;
+  p.adapters = a.adapters;
+  p.width = c.width;
+  p.parts = c.parts;
+  p.copy = a.out != a.y;
+  p.x_wide = begins_on_16(a.x, a.x_row_stride, es) && (long long)c.width * es % 16 == 0;
+  p.y_wide = begins_on_16(a.y, a.y_row_stride, es) && begins_on_16(a.out, a.out_row_stride, es);
+  for (int s = 0; s <= c.parts; ++s) p.y_wide = p.y_wide && (long long)p.starts[s] * es % 16 == 0;
+  const bool vec = p.x_wide && p.y_wide;
+  const int sms = device_sms();
+  if (sms <= 0) return DA_ERR_CUDA;
+
+  // Tiles of 16 rows where an adapter has few, of 64 where it has many (the weights come from L2 once a tile).
+  const int groups = std::min(a.batch, a.adapters);
+  const long long each = a.rows / groups;
+  int mt = !vec || c.dtype == DA_F32 || each < 20 ? 1 : each < 48 ? 2 : 4;
+  const int column_tiles = low / 8;
+  if (mt == 4 && column_tiles > 32) mt = 2;
+  if (mt == 2 && column_tiles > 48) mt = 1;
+  const int most = mt == 1 ? 8 : mt == 2 ? 6 : 4;
+  p.n_groups = 1;
+  while ((column_tiles + p.n_groups - 1) / p.n_groups > most) p.n_groups *= 2;
+  p.n_tiles = (column_tiles + p.n_groups - 1) / p.n_groups;
+  p.pitch = low + ((8 - low) & 31);   // (8 mod 32: the accumulators' pairs of eight rows on different banks)
+  const int m = 16 * mt;
+  const long long tiles = a.rows / m + std::min({(long long)a.batch, (long long)a.adapters + p.copy, (long long)a.rows});
+  // CTAs a tile: as many as two an SM allow
+  int ranks = 8;
+  while (ranks > 1 && tiles * ranks > 2ll * sms) ranks /= 2;
+  const size_t smem = adapter_smem(a.adapters, mt, c.parts, c.rank, es, p.n_groups, p.pitch);
+  if (smem + 4096 > kSmemLimit || tiles * ranks > INT_MAX) return DA_ERR_UNSUPPORTED;
+  const void* fn = c.dtype == DA_F32   ? adapter_kernel_f32(c.rank, mt, vec)
+                   : c.dtype == DA_F16 ? adapter_kernel_f16(c.rank, mt, vec)
+                                       : adapter_kernel_bf16(c.rank, mt, vec);
+  if (!fn) return DA_ERR_UNSUPPORTED;
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return cuda_fail(e, "preparing the adapter kernel");
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)ranks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * ranks));
+  cfg.blockDim = dim3(kAdapterThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(a.cuda_stream);
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  void* kargs[1] = {&p};
+  e = cudaLaunchKernelExC(&cfg, fn, kargs);
+  return e == cudaSuccess ? DA_OK : cuda_fail(e, "launching the adapter kernel");
+}
+
+}  // extern "C"

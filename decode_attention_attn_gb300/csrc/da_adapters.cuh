@@ -1,0 +1,607 @@
+// da_adapters.cuh -- low-rank adapters of many requests beside a shared projection: the kernel.
+//
+//     out[r, part s] = y[r, part s] + c_a (x[r] A_{a,s}^T) B_{a,s}^T,   a the adapter of row r's request,
+//
+// A_{a,s} [rank, width], B_{a,s} [width of part s, rank], s over the projection's parts (q, k and v).
+//
+// A step reads the weights of the adapters in use once, x and y once, and writes out once; at 2 rank products a
+// number read or written this is bound by memory (few rows: the weights; prompts: x, y and out), so the legacy
+// tensor path is enough, and its operands can come straight from memory into registers: an order of the
+// contraction's index is free, so a lane takes 16 neighbouring bytes of a row and a weight as what two
+// instructions want of it, with no transpose and nothing staged.
+//
+// One launch. A tile is up to 16 MT rows of one adapter, wherever they lie, and a cluster of CTAs takes it: each
+// CTA contracts a share of x's width, the cluster's CTAs exchange their partial sums through distributed shared
+// memory, and each then expands a share of the columns. Which rows are a tile's, every CTA finds for itself from
+// the requests' offsets and adapters (a few KB), so that no schedule has to be launched ahead.
+#pragma once
+
+#include <cstring>
+#include <type_traits>
+
+#include "da_device.cuh"
+#include "da_rowvec.cuh"
+
+namespace da {
+
+constexpr int kAdapterThreads = 256, kAdapterWarps = kAdapterThreads / 32;
+constexpr int kMaxParts = 4;
+
+struct AdapterParams {
+  const void *x, *y, *a, *b;
+  void* out;
+  const float* scales;          // of each adapter, or null
+  const int32_t* row_offsets;
+  const int32_t* ids;
+  long long x_rs, y_rs, out_rs;
+  int rows, batch, adapters, width, parts;
+  int starts[kMaxParts + 1];    // columns of the parts
+  int chunks[kMaxParts + 1];    // chunks of 32 columns ahead of each part
+  int n_groups, n_tiles;        // warps that share the low-rank columns, 8-column tiles of each
+  int pitch;                    // floats of a row of partial sums
+  int copy;                     // rows without an adapter are copied (out is not y)
+  int x_wide, y_wide;           // (of the kernel for odd shapes) x and weights / y and out by 16 bytes
+};
+
+// Bytes of dynamic shared memory: the partial sums of every group of warps (where the counts of rows lay before),
+// the sums over the cluster, and them as operands.
+inline size_t adapter_smem(int adapters, int mt, int parts, int rank, int es, int n_groups, int pitch) {
+  const size_t rows = 16 * (size_t)mt;
+  const size_t counts = 4 * ((size_t)adapters + 1), sums = rows * pitch * 4 * (kAdapterWarps / n_groups);
+  const size_t steps = es == 4 ? rank / 8 : rank < 16 ? 1 : rank / 16;
+  return std::max((counts + 15) / 16 * 16, sums) + rows * pitch * 4 + (size_t)parts * mt * steps * 2 * 512;
+}
+
+// The contraction of 16 rows with 8 columns, 16 (8 for fp32, as tf32) deep.
+template <typename T>
+__device__ __forceinline__ void mma16x8(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, float>::value)
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else if constexpr (std::is_same<T, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An fp32 number as two tf32 ones: what is left is 2^-22 of it (nothing of an infinity or NaN).
+__device__ __forceinline__ uint32_t tf32(float x) {
+  uint32_t u;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(u) : "f"(x));
+  return u;
+}
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = tf32(x);
+  const float h = __uint_as_float(hi);
+  lo = fabsf(h) <= 3.4028235e38f ? tf32(x - h) : 0u;
+}
+// Two fp32 numbers as two pairs of T: what is left is 2^-18 (bf16) or 2^-24 (f16) of them.
+template <typename T>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack2(x, y, T());
+  float hx, hy;
+  if constexpr (std::is_same<T, __half>::value) {
+    __half2 h;
+    memcpy(&h, &hi, 4);
+    const float2 f = __half22float2(h);
+    hx = f.x;
+    hy = f.y;
+  } else {
+    hx = __uint_as_float(hi << 16);
+    hy = __uint_as_float(hi & 0xffff0000u);
+  }
+  lo = pack2(fabsf(hx) <= 3.4028235e38f ? x - hx : 0.f, fabsf(hy) <= 3.4028235e38f ? y - hy : 0.f, T());
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// (aligned: by whole warps)
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 load_of_rank(const float* p, uint32_t rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
+// 16 bytes of T at row + k, of which the first `left` elements are there (none: zeros); elements one by one unless
+// `wide`.
+template <typename T>
+__device__ __forceinline__ uint4 load16(const T* row, int k, int left, bool wide) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (wide) return left > 0 ? __ldg(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0u, 0u, 0u, 0u);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (i < left) {
+      if constexpr (sizeof(T) == 4) {
+        w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + k) + i);
+      } else {
+        w[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(row + k) + i) << (16 * (i & 1));
+      }
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct AdapterShared {
+  int sums[kAdapterWarps];
+  int adapter, first, count, chunk_total;
+};
+
+// Sum over the threads before this one; the sum over all in sh.chunk_total. Two barriers.
+__device__ __forceinline__ int block_prefix(int mine, AdapterShared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int below = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += below;
+  }
+  if (lane == 31) sh.sums[warp] = upto;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kAdapterWarps; ++w) {
+    const int v = sh.sums[w];
+    before += w < warp ? v : 0;
+    all += v;
+  }
+  if (threadIdx.x == 0) sh.chunk_total = all;
+  __syncthreads();
+  return before + upto - mine;
+}
+
+// Rows of request b, and the adapter they take (`adapters`: none).
+__device__ __forceinline__ int rows_of(const AdapterParams& p, int b, int& first) {
+  first = min(max(__ldg(p.row_offsets + b), 0), p.rows);
+  return max(min(max(__ldg(p.row_offsets + b + 1), 0), p.rows) - first, 0);
+}
+__device__ __forceinline__ int adapter_of(const AdapterParams& p, int b) {
+  const int id = __ldg(p.ids + b);
+  return id >= 0 && id < p.adapters ? id : p.adapters;
+}
+
+// Tile t: its adapter in sh (-1: there are fewer tiles), its rows in s_row (-1 behind them). Tiles go by adapter,
+// an adapter's rows by request.
+template <int M>
+__device__ void find_tile(const AdapterParams& p, int t, int* s_count, int* s_row, AdapterShared& sh) {
+  const int tid = threadIdx.x, buckets = p.adapters + (p.copy ? 1 : 0);
+  for (int i = tid; i < p.adapters + 1; i += kAdapterThreads) s_count[i] = 0;
+  if (tid < M) s_row[tid] = -1;
+  if (tid == 0) sh.adapter = -1;
+  __syncthreads();
+  for (int b = tid; b < p.batch; b += kAdapterThreads) {
+    int first;
+    const int n = rows_of(p, b, first);
+    if (n) atomicAdd(s_count + adapter_of(p, b), n);
+  }
+  __syncthreads();
+  for (int i0 = 0, base = 0; i0 < buckets; i0 += kAdapterThreads) {
+    const int i = i0 + tid, n = i < buckets ? s_count[i] : 0, tiles = (n + M - 1) / M;
+    const int before = base + block_prefix(tiles, sh);
+    if (before <= t && t < before + tiles) {
+      sh.adapter = i;
+      sh.first = (t - before) * M;
+      sh.count = n;
+    }
+    base += sh.chunk_total;
+    __syncthreads();
+    if (sh.adapter >= 0 || base > t) break;
+  }
+  const int adapter = sh.adapter;
+  if (adapter < 0) return;
+  const int first = sh.first, end = min(first + M, sh.count);
+  for (int b0 = 0, base = 0; b0 < p.batch && base < end; b0 += kAdapterThreads) {
+    const int b = b0 + tid;
+    int row = 0, n = 0;
+    if (b < p.batch && adapter_of(p, b) == adapter) n = rows_of(p, b, row);
+    const int before = base + block_prefix(n, sh);
+    for (int i = max(first - before, 0); i < n && before + i < end; ++i) s_row[before + i - first] = row + i;
+    base += sh.chunk_total;
+    __syncthreads();
+  }
+}
+
+// VEC: rows and weights lie on 16-byte boundaries, parts and the width are multiples of 16 bytes.
+template <typename T, int MT, int R, bool VEC>
+__global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_constant__ AdapterParams p) {
+  constexpr int M = 16 * MT;                       // rows of a tile
+  constexpr bool F32 = std::is_same<T, float>::value;
+  constexpr int V = 16 / (int)sizeof(T);           // elements of 16 bytes
+  constexpr int KB = 4 * V;                        // of the contraction a warp takes at once: 16 bytes a lane
+  constexpr int NT = MT == 1 ? 8 : MT == 2 ? 6 : 4;   // 8-column tiles a warp holds
+  constexpr int STEPS = F32 ? R / 8 : R < 16 ? 1 : R / 16;   // instructions deep, of the expansion
+  extern __shared__ __align__(16) char smem[];
+  __shared__ AdapterShared sh;
+  __shared__ int s_row[M];
+  __shared__ int s_from[M];                        // rows to read: places without one read the tile's first
+  __shared__ float s_scale[M * kMaxParts];         // f16: of a row's low-rank numbers, and back
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const uint32_t rank = cluster_rank(), ranks = cluster_size();
+  const int tile = (int)(blockIdx.x / ranks);
+  const int low = p.parts * R, pitch = p.pitch;    // low-rank columns
+
+  find_tile<M>(p, tile, reinterpret_cast<int*>(smem), s_row, sh);
+  const int adapter = min(sh.adapter, p.adapters);
+  if (adapter < 0) return;                          // (the whole cluster)
+  __syncthreads();
+  if (tid < M) s_from[tid] = min(max(s_row[tid] < 0 ? s_row[0] : s_row[tid], 0), p.rows - 1);
+  __syncthreads();
+
+  // the cluster's shares: of the width in blocks of KB, of the columns in chunks of 32
+  const int blocks = (p.width + KB - 1) / KB, chunks = p.chunks[p.parts];
+  const int k0 = (int)((long long)blocks * rank / ranks), k1 = (int)((long long)blocks * (rank + 1) / ranks);
+  const int h0 = (int)((long long)chunks * rank / ranks), h1 = (int)((long long)chunks * (rank + 1) / ranks);
+  auto part_of = [&](int h) {
+    int s = 0;
+    while (s + 1 < p.parts && h >= p.chunks[s + 1]) ++s;
+    return s;
+  };
+
+  const T* y = static_cast<const T*>(p.y);
+  T* out = static_cast<T*>(p.out);
+  if (adapter == p.adapters) {   // no adapter: the rows as they are
+    for (int m = warp; m < M && s_row[m] >= 0; m += kAdapterWarps) {
+      const T* from = y + s_row[m] * p.y_rs;
+      T* to = out + s_row[m] * p.out_rs;
+      const int c1 = p.starts[p.parts];
+      for (int c = ((int)rank * 32 + lane) * V; c < c1; c += 32 * V * (int)ranks) {
+        if (VEC || p.y_wide) {
+          *reinterpret_cast<uint4*>(to + c) = __ldg(reinterpret_cast<const uint4*>(from + c));
+        } else {
+          for (int i = c; i < min(c + V, c1); ++i) to[i] = from[i];
+        }
+      }
+    }
+    return;
+  }
+  const T* a = static_cast<const T*>(p.a) + (long long)adapter * low * p.width;
+  const T* b = static_cast<const T*>(p.b) + (long long)adapter * p.starts[p.parts] * R;
+
+  float* s_part = reinterpret_cast<float*>(smem);
+  const int k_groups = kAdapterWarps / p.n_groups;
+  const size_t head = max(((size_t)(p.adapters + 1) * 4 + 15) / 16 * 16, (size_t)k_groups * M * pitch * 4);
+  float* s_sum = reinterpret_cast<float*>(smem + head);
+  uint4* s_frag = reinterpret_cast<uint4*>(s_sum + M * pitch);
+
+  // ---- contraction: low[m][n] = sum over k of x[m][k] a[n][k]
+  {
+    const int kg = warp / p.n_groups, ng = warp % p.n_groups;
+    float acc[MT][NT][4] = {};
+    // (what places behind the tile's rows and low-rank columns hold is never looked at: they read others')
+    const T* xr[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int o = 0; o < 2; ++o) xr[i][o] = static_cast<const T*>(p.x) + s_from[i * 16 + 8 * o + g] * p.x_rs;
+    const int n0 = ng * p.n_tiles * 8 + g;
+#pragma unroll MT == 1 ? 2 : 1
+    for (int kb = k0 + kg; kb < k1; kb += k_groups) {
+      const int k = kb * KB + q * V, left = p.width - k;
+      uint4 xv[MT][2], av[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        if (j < p.n_tiles)
+          av[j] = load16<T>(a + (long long)min(n0 + j * 8, low - 1) * p.width, k, left, VEC || p.x_wide);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int o = 0; o < 2; ++o) xv[i][o] = load16<T>(xr[i][o], k, left, VEC || p.x_wide);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if constexpr (!F32) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            const uint32_t f[4] = {s ? xv[i][0].z : xv[i][0].x, s ? xv[i][1].z : xv[i][1].x,
+                                   s ? xv[i][0].w : xv[i][0].y, s ? xv[i][1].w : xv[i][1].y};
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              if (j < p.n_tiles) mma16x8<T>(acc[i][j], f, s ? av[j].z : av[j].x, s ? av[j].w : av[j].y);
+          }
+        } else {
+          // each factor as two tf32 numbers, three of the four products (the last is 2^-22 of the first)
+          uint32_t ah[NT][2], al[NT][2];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            split_tf32(__uint_as_float(s ? av[j].z : av[j].x), ah[j][0], al[j][0]);
+            split_tf32(__uint_as_float(s ? av[j].w : av[j].y), ah[j][1], al[j][1]);
+          }
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            uint32_t hi[4], lo[4];
+            split_tf32(__uint_as_float(s ? xv[i][0].z : xv[i][0].x), hi[0], lo[0]);
+            split_tf32(__uint_as_float(s ? xv[i][1].z : xv[i][1].x), hi[1], lo[1]);
+            split_tf32(__uint_as_float(s ? xv[i][0].w : xv[i][0].y), hi[2], lo[2]);
+            split_tf32(__uint_as_float(s ? xv[i][1].w : xv[i][1].y), hi[3], lo[3]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              if (j >= p.n_tiles) continue;
+              mma16x8<T>(acc[i][j], lo, ah[j][0], ah[j][1]);
+              mma16x8<T>(acc[i][j], hi, al[j][0], al[j][1]);
+              mma16x8<T>(acc[i][j], hi, ah[j][0], ah[j][1]);
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int n = (ng * p.n_tiles + j) * 8 + 2 * q;
+        if (j >= p.n_tiles || n >= low) continue;
+        float* to = s_part + ((size_t)kg * M + i * 16 + g) * pitch + n;
+        *reinterpret_cast<float2*>(to) = make_float2(acc[i][j][0], acc[i][j][1]);
+        *reinterpret_cast<float2*>(to + 8 * pitch) = make_float2(acc[i][j][2], acc[i][j][3]);
+      }
+  }
+  __syncthreads();
+  if (k_groups > 1) {
+    for (int i = tid; i < M * (low / 4); i += kAdapterThreads) {
+      const int m = i / (low / 4), n = (i - m * (low / 4)) * 4;
+      float4* at = reinterpret_cast<float4*>(s_part + (size_t)m * pitch + n);
+      float4 v = *at;
+      for (int k = 1; k < k_groups; ++k) {
+        const float4 w = *reinterpret_cast<const float4*>(s_part + ((size_t)k * M + m) * pitch + n);
+        v.x += w.x;
+        v.y += w.y;
+        v.z += w.z;
+        v.w += w.w;
+      }
+      *at = v;
+    }
+  }
+  if (ranks > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+
+  // ---- the sums over the cluster, of the parts that this CTA's columns lie in
+  const int part0 = h0 < h1 ? part_of(h0) : 0, part1 = h0 < h1 ? part_of(h1 - 1) + 1 : 0;
+  const int wide4 = (part1 - part0) * R / 4;
+  for (int i = tid; i < M * wide4; i += kAdapterThreads) {
+    const int m = i / wide4, n = part0 * R + (i - m * wide4) * 4;
+    const float* at = s_part + (size_t)m * pitch + n;
+    float4 v = ranks > 1 ? load_of_rank(at, 0) : *reinterpret_cast<const float4*>(at);
+    for (uint32_t r = 1; r < ranks; ++r) {
+      const float4 w = load_of_rank(at, r);
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    *reinterpret_cast<float4*>(s_sum + (size_t)m * pitch + n) = v;
+  }
+  if (ranks > 1) cluster_arrive();   // (waited for at the end: nobody leaves while its sums are read)
+  __syncthreads();
+  if constexpr (std::is_same<T, __half>::value) {
+    // f16 ends at 65504: a row's numbers are taken by a power of two to at most 2^8 and less than 2^-24 below that
+    // is lost; the product is taken back by it. (Rows with nothing finite to scale by stay as they are.)
+    for (int i = warp; i < M * (part1 - part0); i += kAdapterWarps) {
+      const int m = i / (part1 - part0), s = part0 + i - m * (part1 - part0);
+      float most = 0.f;
+      for (int n = lane; n < R; n += 32) most = fmaxf(most, fabsf(s_sum[(size_t)m * pitch + s * R + n]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      int e = most > 0.f && most <= 3.4028235e38f ? ilogbf(most) - 7 : 0;
+      e = min(max(e, -120), 120);
+      if (lane == 0) s_scale[m * kMaxParts + s] = ldexpf(1.f, -e);
+    }
+    __syncthreads();
+  }
+  // as operands: what each lane holds of 16 rows and a step, the large parts and the small ones
+  for (int i = tid; i < (part1 - part0) * MT * STEPS * 32; i += kAdapterThreads) {
+    const int l = i & 31, step = (i >> 5) % STEPS, ms = (i >> 5) / STEPS, m16 = ms % MT, s = part0 + ms / MT;
+    const int lg = l >> 2, lq = l & 3;
+    const float* v0 = s_sum + (size_t)(m16 * 16 + lg) * pitch + s * R;
+    const float* v1 = v0 + 8 * pitch;
+    uint32_t hi[4], lo[4];
+    if constexpr (F32) {
+      const int k = R < 16 ? lq * 2 : (step >> 1) * 16 + lq * 4 + (step & 1) * 2;
+      split_tf32(v0[k], hi[0], lo[0]);
+      split_tf32(v1[k], hi[1], lo[1]);
+      split_tf32(v0[k + 1], hi[2], lo[2]);
+      split_tf32(v1[k + 1], hi[3], lo[3]);
+    } else {
+      float c0 = 1.f, c1 = 1.f;
+      if constexpr (std::is_same<T, __half>::value) {
+        c0 = s_scale[(m16 * 16 + lg) * kMaxParts + s];
+        c1 = s_scale[(m16 * 16 + lg + 8) * kMaxParts + s];
+      }
+      if constexpr (R < 16) {
+        split_pair<T>(v0[lq * 2] * c0, v0[lq * 2 + 1] * c0, hi[0], lo[0]);
+        split_pair<T>(v1[lq * 2] * c1, v1[lq * 2 + 1] * c1, hi[1], lo[1]);
+        hi[2] = hi[3] = lo[2] = lo[3] = 0u;
+      } else {
+        const int k = R < 32 ? lq * 4 : (step >> 1) * 32 + lq * 8 + (step & 1) * 4;
+        split_pair<T>(v0[k] * c0, v0[k + 1] * c0, hi[0], lo[0]);
+        split_pair<T>(v1[k] * c1, v1[k + 1] * c1, hi[1], lo[1]);
+        split_pair<T>(v0[k + 2] * c0, v0[k + 3] * c0, hi[2], lo[2]);
+        split_pair<T>(v1[k + 2] * c1, v1[k + 3] * c1, hi[3], lo[3]);
+      }
+    }
+    uint4* to = s_frag + (((size_t)(s - part0) * MT + m16) * STEPS + step) * 64 + l;
+    to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    to[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  __syncthreads();
+
+  // ---- expansion: a warp 32 columns at once. Of 8-column tile j a lane holds columns 8 q + 2 j, 2 j + 1 of its
+  // rows, so that its columns of the four tiles are neighbours.
+  const float c_a = p.scales ? __ldg(p.scales + adapter) : 1.f;
+  for (int h = h0 + warp; h < h1; h += kAdapterWarps) {
+    const int s = part_of(h), col0 = p.starts[s] + (h - p.chunks[s]) * 32, end = p.starts[s + 1];
+    const int mine = col0 + q * 8, n_mine = min(end - mine, 8);   // (none there: below 1)
+    constexpr int YV = 8 / V;            // 16-byte pieces of 8 columns
+    uint4 yv[MT][2][YV];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const T* from = y + s_from[i * 16 + 8 * o + g] * p.y_rs;
+#pragma unroll
+        for (int w = 0; w < YV; ++w) yv[i][o][w] = load16<T>(from, mine + w * V, n_mine - w * V, VEC || p.y_wide);
+      }
+    float acc[MT][4][4] = {};
+    const T* bc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      bc[j] = b + (long long)min(col0 + (g >> 1) * 8 + 2 * j + (g & 1), end - 1) * R;
+    }
+    const uint4* frag = s_frag + (size_t)(s - part0) * MT * STEPS * 64 + lane;
+    constexpr int BLK = R < KB ? 1 : R / KB;      // of 16 bytes a lane
+    constexpr int PER = STEPS / BLK;              // steps of a block
+#pragma unroll
+    for (int blk = 0; blk < BLK; ++blk) {
+      uint32_t bw[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bw[j][1] = bw[j][2] = bw[j][3] = 0u;
+        if constexpr (R * (int)sizeof(T) >= 64) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(bc[j] + blk * KB) + q);
+          bw[j][0] = v.x, bw[j][1] = v.y, bw[j][2] = v.z, bw[j][3] = v.w;
+        } else if constexpr (R * (int)sizeof(T) == 32) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(bc[j]) + q);
+          bw[j][0] = v.x, bw[j][1] = v.y;
+        } else {
+          bw[j][0] = __ldg(reinterpret_cast<const uint32_t*>(bc[j]) + q);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < PER; ++t) {
+        uint32_t bl[4][2];
+        if constexpr (F32) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            split_tf32(__uint_as_float(bw[j][2 * t]), bw[j][2 * t], bl[j][0]);
+            split_tf32(__uint_as_float(bw[j][2 * t + 1]), bw[j][2 * t + 1], bl[j][1]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const uint4* f = frag + (i * STEPS + blk * PER + t) * 64;
+          const uint4 fh = f[0], fl = f[32];
+          const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mma16x8<T>(acc[i][j], lo, bw[j][2 * t], bw[j][2 * t + 1]);
+            if constexpr (F32) mma16x8<T>(acc[i][j], hi, bl[j][0], bl[j][1]);
+            mma16x8<T>(acc[i][j], hi, bw[j][2 * t], bw[j][2 * t + 1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const int m = i * 16 + 8 * o + g, r = s_row[m];
+        if (r < 0 || n_mine <= 0) continue;
+        float c = c_a;
+        if constexpr (std::is_same<T, __half>::value) c = c_a / s_scale[m * kMaxParts + s];
+        T* to = out + r * p.out_rs + mine;
+        if constexpr (F32) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint4 w = yv[i][o][e / 4];
+            v[e] = __uint_as_float(e % 4 == 0 ? w.x : e % 4 == 1 ? w.y : e % 4 == 2 ? w.z : w.w) +
+                   c * acc[i][e / 2][2 * o + (e & 1)];
+          }
+          if (VEC || p.y_wide) {
+            *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+            if (n_mine > 4) *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e < n_mine) to[e] = v[e];
+          }
+        } else {
+          const uint32_t in[4] = {yv[i][o][0].x, yv[i][o][0].y, yv[i][o][0].z, yv[i][o][0].w};
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float y0, y1;
+            if constexpr (std::is_same<T, __half>::value) {
+              __half2 hv;
+              memcpy(&hv, &in[j], 4);
+              const float2 f = __half22float2(hv);
+              y0 = f.x;
+              y1 = f.y;
+            } else {
+              y0 = __uint_as_float(in[j] << 16);
+              y1 = __uint_as_float(in[j] & 0xffff0000u);
+            }
+            w[j] = pack2(y0 + c * acc[i][j][2 * o], y1 + c * acc[i][j][2 * o + 1], T());
+          }
+          if (VEC || p.y_wide) {
+            *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e < n_mine) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+          }
+        }
+      }
+  }
+  if (ranks > 1) cluster_wait();
+}
+
+// The kernel for tiles of 16 mt rows (null: not built).
+template <typename T, int R>
+const void* adapter_kernel_of(int mt, bool vec) {
+  if (!vec) return mt == 1 ? reinterpret_cast<const void*>(&adapter_kernel<T, 1, R, false>) : nullptr;
+  if (mt == 1) return reinterpret_cast<const void*>(&adapter_kernel<T, 1, R, true>);
+  if constexpr (!std::is_same<T, float>::value) {
+    if (mt == 2) return reinterpret_cast<const void*>(&adapter_kernel<T, 2, R, true>);
+    if (mt == 4) return reinterpret_cast<const void*>(&adapter_kernel<T, 4, R, true>);
+  }
+  return nullptr;
+}
+template <typename T>
+const void* adapter_kernel_for(int rank, int mt, bool vec) {
+  switch (rank) {
+    case 8: return adapter_kernel_of<T, 8>(mt, vec);
+    case 16: return adapter_kernel_of<T, 16>(mt, vec);
+    case 32: return adapter_kernel_of<T, 32>(mt, vec);
+    case 64: return adapter_kernel_of<T, 64>(mt, vec);
+    case 128: return adapter_kernel_of<T, 128>(mt, vec);
+    default: return nullptr;
+  }
+}
+
+const void* adapter_kernel_bf16(int rank, int mt, bool vec);
+const void* adapter_kernel_f16(int rank, int mt, bool vec);
+const void* adapter_kernel_f32(int rank, int mt, bool vec);
+
+}  // namespace da

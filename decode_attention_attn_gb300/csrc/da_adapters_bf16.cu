@@ -1,0 +1,8 @@
+// da_adapters_bf16.cu -- adapter kernels for bf16 rows.
+#include "da_adapters.cuh"
+
+namespace da {
+
+const void* adapter_kernel_bf16(int rank, int mt, bool vec) { return adapter_kernel_for<__nv_bfloat16>(rank, mt, vec); }
+
+}  // namespace da

@@ -1,0 +1,8 @@
+// da_adapters_f32.cu -- adapter kernels for f32 rows.
+#include "da_adapters.cuh"
+
+namespace da {
+
+const void* adapter_kernel_f32(int rank, int mt, bool vec) { return adapter_kernel_for<float>(rank, mt, vec); }
+
+}  // namespace da

@@ -698,6 +698,7 @@ int status_to_error(int s) {
   if (s & kStatusBadBlockTable) return DA_ERR_BAD_BLOCK_TABLE;
   if (s & kStatusBadSeqLen) return DA_ERR_BAD_SEQ_LEN;
   if (s & kStatusTimeout) return DA_ERR_DEVICE_TIMEOUT;
+  if (s & kStatusNoPages) return DA_ERR_NO_PAGES;
   return DA_OK;
 }
 
@@ -721,6 +722,7 @@ const char* decode_attn_strerror(int code) {
       return "a tail of the requested coverage lies outside the histogram's range";
     case DA_ERR_RANGE_TOO_WIDE:
       return "the covered logit range is wider than allowed: use DA_SOFTMAX_SYNC";
+    case DA_ERR_NO_PAGES: return "the pool has fewer free pages than the step takes";
     default: return "unknown error code";
   }
 }

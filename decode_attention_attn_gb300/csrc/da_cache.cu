@@ -14,7 +14,7 @@
 #include <utility>
 
 #include "da_plan.h"
-#include "da_rows.h"
+#include "da_rowvec.cuh"
 
 using namespace da;
 
@@ -23,6 +23,26 @@ struct da_rope {
   double theta[128];        // radians per position
   unsigned long long turn[128];   // turns per position, 0.64 fixed point (mod 1)
 };
+
+namespace da {
+
+// SMs of the current device, asked for once; 0: not known (cuda_fail has the reason).
+int device_sms() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0, n = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < kDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) {
+    cuda_fail(e, "asking for the device's SMs");
+    return 0;
+  }
+  if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+}  // namespace da
 
 namespace {
 
@@ -51,21 +71,6 @@ struct RowParams {
   float k_scale, v_scale;       // of an FP8 cache
   unsigned long long turn[kMaxPairs];
 };
-
-// 32 bytes a lane (aligned to 32): neighbouring lanes then fill whole sectors in one instruction,
-// where two 16-byte accesses 32 bytes apart touch each sector twice (1.7 GB read back from FP8, 8 items a lane:
-// 266 us, 340 with 16-byte stores; a rotary gradient 26.7, 27.4; a plain write of 134 MB 23.1, 24.0).
-__device__ __forceinline__ void load32(const void* p, uint4& a, uint4& b) {
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
-                 "=r"(b.w)
-               : "l"(p));
-}
-__device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
-               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-               : "memory");
-}
 
 // The sequence whose rows hold row r: the last b with offsets[b] <= r, or -1 where r lies
 // before the first row or behind the last one.
@@ -116,27 +121,6 @@ struct RowVec<T, 1> {
     else f[0] = __bfloat162float(r);
   }
 };
-
-__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  uint32_t u;
-  memcpy(&u, &h, 4);
-  return u;
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
-  const __half2 h = __floats2half2_rn(a, b);
-  uint32_t u;
-  memcpy(&u, &h, 4);
-  return u;
-}
-// Two E4M3 codes, nearest even, |x| > 448 to +-448; `a` in the low byte.
-__device__ __forceinline__ uint32_t pack_e4m3x2(float a, float b) {
-  uint32_t u;
-  asm("{\n\t.reg .b16 c;\n\tcvt.rn.satfinite.e4m3x2.f32 c, %2, %1;\n\tcvt.u32.u16 %0, c;\n\t}"
-      : "=r"(u)
-      : "f"(a), "f"(b));
-  return u;
-}
 
 // VEC floats as VEC stored elements of C: 16 bytes (8 for E4M3), or one element.
 template <typename C, int VEC>
@@ -376,32 +360,6 @@ const void* rows_kernel_for(bool vec) {
 // Whether a row tensor can move `bytes` (16 or 32) a lane.
 bool vector_ok(const void* p, long long rs, long long hs, int es, int bytes = 16) {
   return !p || (aligned(p, bytes) && rs * es % bytes == 0 && hs * es % bytes == 0);
-}
-
-// A row tensor's places in memory, from its strides in elements (of which a byte's are a few bits more: larger
-// ones than memory has are as good as the largest).
-RowRuns runs(const void* p, long long rows, long long rs, long long heads, long long hs, int d, int es) {
-  auto bytes = [es](long long s) {
-    const long long most = INT64_MAX / 8;
-    return std::min(std::max(s, -most), most) * es;
-  };
-  return {(uint64_t)(uintptr_t)p, rows, bytes(rs), heads, bytes(hs), (int64_t)d * es};
-}
-
-// SMs of the current device, asked for once; 0: not known (cuda_fail has the reason).
-int device_sms() {
-  constexpr int kDevices = 64;
-  static std::atomic<int> known[kDevices];
-  int dev = 0, n = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && dev < kDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) {
-    cuda_fail(e, "asking for the device's SMs");
-    return 0;
-  }
-  if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
-  return n;
 }
 
 int launch_rows(RowParams& p, int head_dim, int es, bool vec, int sms, const void* fn,

@@ -36,6 +36,7 @@ constexpr int kPieceCostBytes = 96 * 1024;
 constexpr int kStatusBadBlockTable = 1;
 constexpr int kStatusBadSeqLen = 2;
 constexpr int kStatusTimeout = 4;
+constexpr int kStatusNoPages = 8;
 
 // bound on any pipeline wait (ns); a healthy wait lasts microseconds
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;

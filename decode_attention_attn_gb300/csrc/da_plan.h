@@ -40,6 +40,9 @@ int text_fail(const char* text, const char* more = "") noexcept;
 
 int validate_problem(const da_problem& p);
 
+// SMs of the current device; 0: not known (cuda_fail has the reason).
+int device_sms();
+
 // Launch parameters of a plan's problem; the workspace's pointers when ws is given.
 void fill_common(const da_plan& pl, Params& k, const int32_t* block_table,
                  const int32_t* seq_lens, void* ws);

@@ -83,7 +83,8 @@ enum {
   DA_ERR_DEVICE_TIMEOUT = -6,       /* validate: a device pipeline wait ran out of time */
   DA_ERR_BAD_SEQ_LEN = -7,          /* validate: seq_lens[b] < 0 or above the capacity */
   DA_ERR_HISTOGRAM_RANGE = -8,      /* choose_phi: a coverage tail lies outside [lo, hi) */
-  DA_ERR_RANGE_TOO_WIDE = -9        /* choose_phi: covered range wider than max_width */
+  DA_ERR_RANGE_TOO_WIDE = -9,       /* choose_phi: covered range wider than max_width */
+  DA_ERR_NO_PAGES = -10             /* validate: a step needs more pages than its pool has free */
 };
 
 typedef struct {
@@ -625,6 +626,193 @@ int decode_attn_tree_run(const da_tree_plan* plan, const da_tree_args* args);
 int decode_attn_tree_check_status(const da_tree_plan* plan, void* workspace, void* cuda_stream);
 
 void decode_attn_tree_destroy(da_tree_plan* plan);
+
+/* ---- Pages: block tables and slots from the sequences' lengths --------------------------------
+ * A pool is a device array of DECODE_ATTN_POOL_HEAD + num_physical_blocks int32, 16-byte aligned:
+ *   pool[0]  the number of free pages, F (taken as 0 .. num_physical_blocks where it lies outside);
+ *   pool[1]  the pages that the last reservation lacked (0: it had them);
+ *   pool[2]  the library's, pool[3] unused; both 0 at the start;
+ *   pool[DECODE_ATTN_POOL_HEAD + i], i < F: the free pages, a stack whose top is the last.
+ * The caller may fill it by itself (in any order of pages), or by decode_attn_pages_init. Each page is on the
+ * stack or in one place of one sequence's row of the block table; a page that sequences share is the caller's
+ * to keep out. Calls on one pool must not overlap on the GPU; they may be captured into a graph.
+ * `plan` is any plan of the (paged) problem shape; batch may be at most DECODE_ATTN_MAX_PAGED_BATCH
+ * (else UNSUPPORTED). Results must lie apart from inputs and from one another (else INVALID_ARG). */
+
+#define DECODE_ATTN_POOL_HEAD 4
+#define DECODE_ATTN_MAX_PAGED_BATCH 16384
+
+/* Every page free, page 0 on top. Enqueued on cuda_stream. Errors: INVALID_ARG, UNSUPPORTED (not paged), CUDA. */
+int decode_attn_pages_init(const da_plan* plan, int32_t* pool, void* cuda_stream);
+
+/* Pages for a step's rows, and where each row goes. Sequence b holds ctx_lens[b] tokens, in the first
+ * ceil(ctx_lens[b] / page_size) entries of its block-table row, and gets T_b rows (row_offsets as above; those
+ * past `rows` do not count), so it takes ceil((ctx_lens[b] + T_b) / page_size) - ceil(ctx_lens[b] / page_size)
+ * pages. They come off the top of the stack, sequence by sequence, and are entered in block_table, whose other
+ * entries stay as they are.
+ *   seq_lens    nullable device int32 [batch]: ctx_lens[b] + T_b (what decode_attn_run takes). May be ctx_lens.
+ *   slots       nullable device int32 [rows]: the cache row block_table[b][t / page_size] * page_size +
+ *               t % page_size of each row's position t = ctx_lens[b] + r - row_offsets[b] (row z of a cache
+ *               seen as [tokens, H_kv, d]); -1 for a row without a place: one of no sequence, one at a
+ *               position outside [0, capacity), one on an entry outside the pool.
+ *   positions   nullable device int32 [rows]: t; 0 for rows of no sequence.
+ * The pool has fewer pages than the step takes: it takes none. The tables and the stack stay as they are, every
+ * slot is -1, seq_lens[b] = ctx_lens[b], pool[1] says how many pages were missing (0 otherwise), and NO_PAGES
+ * is recorded. A length that is negative or would pass the capacity is recorded (BAD_SEQ_LEN) and clamped, as
+ * are entries outside the pool (BAD_BLOCK_TABLE; one of the stack is entered as -1).
+ *   workspace   nullable, the plan's workspace: takes the findings (decode_attn_check_status); required when
+ *               the problem's validate is set: the call then synchronises and returns them.
+ * Enqueued on cuda_stream. Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA; with validate the
+ * findings. */
+typedef struct {
+  int32_t* pool;
+  int32_t* block_table;
+  const int32_t* row_offsets;
+  const int32_t* ctx_lens;
+  int rows;
+  int32_t* seq_lens;
+  int32_t* slots;
+  int32_t* positions;
+  void* workspace;
+  size_t workspace_bytes;
+  void* cuda_stream;
+} da_pages_reserve_args;
+
+int decode_attn_pages_reserve(const da_plan* plan, const da_pages_reserve_args* args);
+
+/* Cut sequences back from seq_lens[b] to keep_lens[b] tokens (0: the sequence has ended; a step's drafted tokens
+ * that were turned down): pages past ceil(keep_lens[b] / page_size) go onto the stack, and their entries of
+ * block_table become -1. The last sequence's last page goes first, so that a reservation given back whole leaves
+ * the stack as it was. keep_lens[b] outside [0, seq_lens[b]], and seq_lens[b] outside [0, capacity], are
+ * recorded (BAD_SEQ_LEN) and clamped. An entry outside the pool is pushed as -1 and recorded (BAD_BLOCK_TABLE).
+ * More pages than the pool has room for (some come back twice): none is taken back, and BAD_BLOCK_TABLE is
+ * recorded. keep_lens may be seq_lens. workspace, errors: as above. */
+typedef struct {
+  int32_t* pool;
+  int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* keep_lens;
+  void* workspace;
+  size_t workspace_bytes;
+  void* cuda_stream;
+} da_pages_release_args;
+
+int decode_attn_pages_release(const da_plan* plan, const da_pages_release_args* args);
+
+/* ---- Root-mean-square norm ----------------------------------------------------------------------
+ * Of every row r and head h of x, over its n elements:
+ *     u = x + residual, rounded to the type (u = x without a residual),
+ *     y = u (weight + weight_offset) / sqrt(mean(u^2) + eps),
+ * hidden rows (heads = 1) with the residual's addition, or q and k heads ahead of a rotary. Statistics, products
+ * and y are fp32; each result is rounded once. y goes out in x's type, as E4M3 codes of y / scale (an fp32
+ * quotient, rounded to nearest even, values beyond +-448 to +-448, NaN to the NaN code), or both. */
+
+/* Where the codes' scales come from. Found ones are s = max(max |y| / 448, 2^-126), NaNs passed over:
+ * DA_SCALE_NONE    no codes.
+ * DA_SCALE_TENSOR  scales[0], read by the call (a device float, finite and > 0).
+ * DA_SCALE_ROW     one for each row and head: scales [rows, heads], written.
+ * DA_SCALE_GROUP   one for each `group` (32, 64 or 128) neighbouring elements, the last group of a row as long
+ *                  as n leaves it: scales [rows, heads, ceil(n / group)], written. */
+typedef enum { DA_SCALE_NONE = 0, DA_SCALE_TENSOR = 1, DA_SCALE_ROW = 2, DA_SCALE_GROUP = 3 } da_scaling;
+
+#define DECODE_ATTN_NORM_MAX 32768
+
+typedef struct {
+  int n;                    /* 1 to DECODE_ATTN_NORM_MAX (else UNSUPPORTED) */
+  float eps;                /* finite, >= 0 (0: a row of zeros gives NaN) */
+  float weight_offset;      /* finite; 1 for weights stored as their distance from 1 */
+} da_norm_config;
+
+/* One call.
+ *   x             device, [rows, heads, n] of `dtype` with strides in elements (any, 0 among them).
+ *   residual      nullable, likewise. residual_out: nullable, takes u; needs a residual; may be x or
+ *                 residual with its strides.
+ *   weight        nullable device [n] (null: y = u / sqrt(...), weight_offset is not used), of `dtype`, or
+ *                 fp32 where weight_f32 is set.
+ *   out           nullable, takes y in `dtype`; may be x or residual with its strides.
+ *   codes, scales nullable, one byte an element, and as da_scaling says (contiguous); given where scaling is
+ *                 not NONE. out or codes must be given.
+ * Results' rows and heads must lie apart from one another, from other results and from inputs, except as said
+ * (else INVALID_ARG). Rows of 32-byte multiples on 32-byte boundaries (codes: 16 or, for fp32, 8) move 32 bytes
+ * a lane, others an element a lane. rows = 0: nothing is enqueued. Enqueued on cuda_stream.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, n, group, more than DECODE_ATTN_ROPE_MAX_HEADS heads), CUDA. */
+typedef struct {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  void* residual_out;
+  void* out;
+  void* codes;
+  float* scales;
+  da_dtype dtype;
+  int weight_f32;
+  da_scaling scaling;
+  int group;
+  int rows;
+  int heads;
+  int64_t x_row_stride, x_head_stride;
+  int64_t residual_row_stride, residual_head_stride;
+  int64_t residual_out_row_stride, residual_out_head_stride;
+  int64_t out_row_stride, out_head_stride;
+  int64_t codes_row_stride, codes_head_stride;
+  void* cuda_stream;
+} da_norm_args;
+
+int decode_attn_norm_apply(const da_norm_config* config, const da_norm_args* args);
+
+/* ---- Low-rank adapters of many requests beside a shared projection -------------------------------
+ * Rows x [rows, width] of a batch of requests went through one projection, to y [rows, columns]; the columns
+ * are `parts` side by side (q, k and v). Request b's rows (row_offsets as above) take adapter a =
+ * adapter_ids[b]:
+ *     out[r, part s] = y[r, part s] + scales[a] (x[r] A_{a,s}^T) B_{a,s}^T,
+ * A_{a,s} [rank, width], B_{a,s} [out_sizes[s], rank]. A request whose id lies outside [0, adapters) (-1 by
+ * convention) has none: out = y. An adapter of a smaller rank has zeros in the rest.
+ * Products are exact to fp32's order and sums are fp32: the low-rank numbers are not rounded to the type in
+ * between; out is rounded once. */
+
+#define DECODE_ATTN_ADAPTER_PARTS 4
+#define DECODE_ATTN_ADAPTER_MAX_WIDTH (1 << 20)
+#define DECODE_ATTN_MAX_ADAPTERS 8192
+
+typedef struct {
+  da_dtype dtype;           /* of x, y, a, b and out */
+  int width;                /* 1 to DECODE_ATTN_ADAPTER_MAX_WIDTH */
+  int parts;                /* 1 to DECODE_ATTN_ADAPTER_PARTS */
+  int out_sizes[DECODE_ATTN_ADAPTER_PARTS];   /* columns of each part, 1 to DECODE_ATTN_ADAPTER_MAX_WIDTH */
+  int rank;                 /* 8, 16, 32, 64 or 128 */
+} da_adapter_config;
+
+/* One call.
+ *   x, y, out     device, rows with strides in elements (x's and y's any, 0 among them); out may be y with its
+ *                 stride, and lies apart from everything else (else INVALID_ARG).
+ *   a             device [adapters, parts, rank, width], contiguous, 16-byte aligned.
+ *   b             device [adapters, columns, rank], contiguous, 16-byte aligned (column by column, the parts
+ *                 one after another).
+ *   scales        nullable device float [adapters] (null: 1).
+ *   row_offsets, adapter_ids   device int32 [batch + 1] and [batch].
+ * Rows of no request are left as they were. Results do not depend on the order of execution. Rows and parts of
+ * 16-byte multiples on 16-byte boundaries move 16 bytes a lane, others an element. Enqueued on cuda_stream, one
+ * launch, no workspace. Errors: INVALID_ARG, UNSUPPORTED (dtype, rank, parts, sizes; more than
+ * DECODE_ATTN_MAX_ADAPTERS adapters or DECODE_ATTN_MAX_PAGED_BATCH requests), CUDA. */
+typedef struct {
+  const void* x;
+  const void* y;
+  void* out;
+  const void* a;
+  const void* b;
+  const float* scales;
+  const int32_t* row_offsets;
+  const int32_t* adapter_ids;
+  int rows;
+  int batch;
+  int adapters;
+  int64_t x_row_stride;
+  int64_t y_row_stride;
+  int64_t out_row_stride;
+  void* cuda_stream;
+} da_adapter_args;
+
+int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter_args* args);
 
 void decode_attn_destroy(da_plan* plan);
 

@@ -1,0 +1,300 @@
+"""Low-rank adapters of many requests: refusals on the CPU, results on the GPU against plain float64 forms."""
+import pytest
+import torch
+
+from _rows import TORCH, half_step
+from decode_attention_attn_gb300 import binding, build as lib_build
+
+A = 0x10000000   # an aligned address that no refused call dereferences
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    lib_build.build()
+
+
+# ---- CPU: refusals --------------------------------------------------------------------------
+def test_apply_refuses_bad_arguments():
+    P = 1 << 24
+
+    def call(cfg=(), **kw):
+        config = binding.da_adapter_config(2, 256, 2, (binding.ctypes.c_int * 4)(128, 64, 0, 0), 16)
+        for k, v in dict(cfg).items():
+            setattr(config, k, v if k != "out_sizes" else (binding.ctypes.c_int * 4)(*v))
+        args = binding.da_adapter_args(A, A + P, A + 2 * P, A + 3 * P, A + 4 * P, A + 5 * P, A + 6 * P, A + 7 * P, 9, 4, 3,
+                                       256, 192, 192, None)
+        for k, v in kw.items():
+            assert hasattr(args, k)
+            setattr(args, k, v)
+        with pytest.raises(binding.DecodeAttnError) as e:
+            binding.decode_attn_adapters_apply(config, args)
+        return e.value.code
+
+    for cfg, code in ((dict(dtype=3), -2), (dict(dtype=-1), -2), (dict(width=0), -1), (dict(width=(1 << 20) + 1), -2),
+                      (dict(parts=0), -1), (dict(parts=5), -2), (dict(rank=12), -2), (dict(rank=256), -2), (dict(rank=0), -2),
+                      (dict(out_sizes=(128, 0, 0, 0)), -1), (dict(out_sizes=(128, (1 << 20) + 1, 0, 0)), -2)):
+        assert call(cfg) == code, cfg
+    for name in ("x", "y", "out", "a", "b", "row_offsets", "adapter_ids"):
+        assert call(**{name: None}) == -1, name
+    assert call(rows=-1) == -1 and call(batch=0) == -1 and call(adapters=0) == -1
+    assert call(batch=16385) == -2 and call(adapters=8193) == -2
+    for name, by in (("x", 1), ("y", 1), ("out", 1), ("a", 8), ("b", 2), ("scales", 2), ("row_offsets", 1), ("adapter_ids", 2)):
+        assert call(**{name: A + 9 * P + by}) == -1, name
+    # rows on one another, results over inputs
+    assert call(out_row_stride=191) == -1 and call(out_row_stride=0) == -1 and call(out_row_stride=-192) == -1
+    assert call(out=A + P, out_row_stride=384) == -1 and call(out=A + P + 64) == -1
+    for i in (0, 3, 4, 5, 6, 7):
+        assert call(out=A + i * P) == -1, i
+    # no rows: nothing is enqueued, no pointer is looked at
+    config = binding.da_adapter_config(2, 256, 1, (binding.ctypes.c_int * 4)(128, 0, 0, 0), 16)
+    binding.decode_attn_adapters_apply(config, binding.da_adapter_args(*[None] * 8, 0, 1, 1))
+    with pytest.raises(binding.DecodeAttnError):
+        binding._check(binding.lib().decode_attn_adapters_apply(None, None), "adapters")
+
+
+def test_wrapper_refuses_bad_tensors():
+    for args in ((0, [8], 8), (64, [], 8), (64, [8] * 5, 8), (64, [8, 0], 8), (64, [8], 12)):
+        with pytest.raises(ValueError):
+            binding.Adapters(*args)
+    with pytest.raises(ValueError):
+        binding.Adapters(64, [8], 8, "f64")
+    ad = binding.Adapters(64, [24, 8], 8, "f32")
+    ok = dict(x=torch.zeros(5, 64), y=torch.zeros(5, 32), a=torch.zeros(3, 16, 64), b=torch.zeros(3, 32, 8),
+              scales=torch.zeros(3), row_offsets=torch.zeros(3, dtype=torch.int32), adapter_ids=torch.zeros(2, dtype=torch.int32))
+    bad = [dict(x=torch.zeros(5, 65)), dict(x=torch.zeros(4, 64)), dict(x=torch.zeros(5, 64).half()), dict(x=torch.zeros(64, 5).t()),
+           dict(y=torch.zeros(5, 31)), dict(out=torch.zeros(4, 32)), dict(out=torch.zeros(5, 32).half()),
+           dict(a=torch.zeros(3, 8, 64)), dict(a=torch.zeros(3, 16, 64).half()), dict(a=torch.zeros(3, 16, 128)[..., ::2]),
+           dict(b=torch.zeros(2, 32, 8)), dict(b=torch.zeros(3, 32, 16)), dict(scales=torch.zeros(2)),
+           dict(scales=torch.zeros(3).half()), dict(row_offsets=torch.zeros(4, dtype=torch.int32)),
+           dict(adapter_ids=torch.zeros(2)), dict(adapter_ids=torch.zeros(0, dtype=torch.int32), row_offsets=torch.zeros(1, dtype=torch.int32))]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            ad.apply(**{**ok, **kw})
+    with pytest.raises(ValueError, match="CUDA"):
+        ad.apply(**ok)
+    for name in ("x", "y", "a", "b"):
+        with pytest.raises(ValueError, match="gradient"):
+            ad.apply(**{**ok, name: ok[name].clone().requires_grad_()})
+
+
+# ---- the plain form -------------------------------------------------------------------------
+class Step:
+    """Requests' rows and adapters, what the product is in 64 bits, and what a result may be off by."""
+
+    def __init__(self, lens, ids, width, outs, rank, adapters, dtype, before=0, behind=0, seed=0, x_gain=1.0, x_pad=0,
+                 y_pad=0, shift=0):
+        g = torch.Generator().manual_seed(seed + width + rank)
+        self.t, self.outs, self.rank = TORCH[dtype], outs, rank
+        rows, columns = before + sum(lens) + behind, sum(outs)
+
+        def strided(rows, n, pad, gain=1.0):
+            flat = torch.zeros(shift + rows * (n + pad), dtype=self.t)
+            flat[shift:].view(rows, n + pad).copy_(gain * torch.randn(rows, n + pad, generator=g))
+            return flat.cuda()[shift:].view(rows, n + pad)[:, :n]
+
+        self.x, self.y = strided(rows, width, x_pad, x_gain), strided(rows, columns, y_pad)
+        self.a = (torch.randn(adapters, len(outs) * rank, width, generator=g) / width ** 0.5).to(self.t).cuda()
+        self.b = (0.5 * torch.randn(adapters, columns, rank, generator=g) / rank ** 0.5).to(self.t).cuda()
+        self.scales = (0.5 + torch.rand(adapters, generator=g)).cuda()
+        offs = [before]
+        for n in lens:
+            offs.append(offs[-1] + n)
+        self.offsets = torch.tensor(offs, dtype=torch.int32).cuda()
+        self.ids = torch.tensor(ids, dtype=torch.int32).cuda()
+        self.of = [-1] * rows
+        self.member = torch.zeros(rows, dtype=torch.bool)
+        for b, n in enumerate(lens):
+            for r in range(offs[b], offs[b + 1]):
+                self.of[r] = ids[b] if 0 <= ids[b] < adapters else -1
+                self.member[r] = True
+        self.handle = binding.Adapters(width, outs, rank, dtype)
+
+    def apply(self, out=None, **kw):
+        return self.handle.apply(self.x, self.y, self.a, self.b, self.scales, self.offsets, self.ids, out=out, **kw)
+
+    def want(self):
+        """(result, bound). Of a low-rank number: a sum of width products, each exact (fp32: within 2^-20, two tf32
+        parts of each factor without their smallest product), added 8 or 16 at a time, each addition within 2^-23 of
+        the sum of magnitudes, then 8 warps and 8 CTAs. As an operand within 2^-17 (bf16 pairs) or 2^-20 (f16, tf32
+        pairs); rank more products, added twice or three times 8 at a time."""
+        width, rank = self.x.shape[1], self.rank
+        f32 = self.t is torch.float32
+        e1 = (3 * (width // 8 + 1) + 16 if f32 else width // 16 + 17) * 2.0 ** -23 + (2.0 ** -20 if f32 else 0)
+        e2 = (3 * (rank // 8 + 1)) * 2.0 ** -23 + (2.0 ** -17 if self.t is torch.bfloat16 else 2.0 ** -20)
+        want, off = self.y.double().clone(), torch.zeros_like(self.y, dtype=torch.float64)
+        of = torch.tensor(self.of, device="cuda")
+        for a in set(self.of) - {-1}:
+            rows = (of == a).nonzero()[:, 0]
+            x, at = self.x[rows].double(), 0
+            for k, w in enumerate(self.outs):
+                down = self.a[a, k * rank:(k + 1) * rank].double()
+                up = self.b[a, at:at + w].double()
+                low, mag = x @ down.T, x.abs() @ down.abs().T
+                c = float(self.scales[a])
+                want[rows, at:at + w] += c * (low @ up.T)
+                most = low.abs().amax(1, keepdim=True)        # (f16: less than 2^-32 of the row's largest is cut off)
+                off[rows, at:at + w] = c * ((e1 * mag + e2 * low.abs() + 2.0 ** -32 * most) @ up.abs().T)
+                at += w
+        fused = 2.0 ** -23 * (want.abs() + self.y.double().abs())
+        bound = off * 1.01 + fused + want.abs() * half_step(self.t) + (2.0 ** -25 if self.t is torch.float16 else 0)
+        return want, bound
+
+    def check(self, got, before=None):
+        want, bound = self.want()
+        err = (got.double() - want).abs()
+        m = self.member.cuda()
+        assert (err[m] <= bound[m]).all(), float((err[m] / bound[m]).max())
+        if before is not None:
+            assert torch.equal(got[~m], before[~m])
+
+
+CASES = {   # lens, ids
+    "one": ([1], [0]),
+    "each": ([1] * 7, [3, 0, 4, 1, 2, 5, 6]),
+    "shared": ([1, 3, 2, 1, 40, 1], [2, 2, 2, 2, 2, 2]),
+    "bare": ([4, 1, 0, 2, 5], [-1, 1, 1, 7, 900]),
+    "ragged": ([0, 17, 0, 0, 1, 33, 16, 64, 2], [1, 0, 1, 2, 1, 0, -1, 1, 0]),
+    "prompts": ([300, 77, 129], [1, 0, 1]),
+    "none": ([3, 2], [-1, -2]),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("name", list(CASES))
+@pytest.mark.parametrize("width,outs,rank", [(256, [128, 64], 16), (4096, [512, 128, 128], 8), (64, [8], 64), (1000, [40, 8, 16, 104], 32),
+                                             (512, [96, 32], 128)])
+def test_adapters(dtype, name, width, outs, rank):
+    lens, ids = CASES[name]
+    s = Step(lens, ids, width, outs, rank, 7, dtype, before=2, behind=3)
+    before = torch.randn_like(s.y)
+    out = before.clone()
+    assert s.apply(out) is out
+    s.check(out, before)
+    # in place
+    y0 = s.y.clone()
+    want, bound = s.want()
+    s.apply(s.y)
+    m = s.member.cuda()
+    assert ((s.y.double() - want).abs()[m] <= bound[m]).all() and torch.equal(s.y[~m], y0[~m])
+    assert torch.equal(s.y[m], out[m])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("name", ["ragged", "prompts"])
+@pytest.mark.parametrize("width,outs,rank,x_pad,y_pad,shift", [
+    (1001, [99, 7], 16, 0, 0, 0), (64, [5, 1, 1, 3], 8, 3, 1, 1), (256, [64, 65], 64, 0, 8, 0), (255, [64, 64], 32, 0, 0, 0),
+    (256, [128], 16, 8, 16, 8), (256, [128], 16, 8, 16, 3), (1, [1], 128, 0, 0, 0), (7, [33], 32, 1, 0, 0)])
+def test_odd_sizes_strides_and_alignment(dtype, name, width, outs, rank, x_pad, y_pad, shift):
+    lens, ids = CASES[name]
+    s = Step(lens, ids, width, outs, rank, 3, dtype, before=1, behind=1, x_pad=x_pad, y_pad=y_pad, shift=shift)
+    out = torch.randn_like(s.y)
+    before = out.clone()
+    s.check(s.apply(out), before)
+    wide = s.y._base.clone()
+    s.apply(s.y)
+    rows, n = s.y.shape
+    same = torch.ones(rows, n + y_pad, dtype=torch.bool, device="cuda")
+    same[s.member.cuda(), :n] = False
+    assert torch.equal(s.y._base[shift:].view(rows, -1)[same], wide[shift:].view(rows, -1)[same])
+    assert torch.equal(s.y._base[:shift], wide[:shift])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("parts,rank", [(1, 8), (4, 128), (3, 64), (4, 64), (3, 128), (4, 8)])
+@pytest.mark.parametrize("each", [1, 30, 200])
+def test_every_tile_height_and_share(dtype, parts, rank, each):
+    """Few, some and many rows an adapter, and low-rank columns for every split over the warps."""
+    s = Step([each] * 3, [0, 1, 0], 320, [64 * (k + 1) for k in range(parts)], rank, 2, dtype)
+    s.check(s.apply())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_many_requests_and_adapters(dtype):
+    for batch, adapters, most in ((3000, 500, 3), (1, 8192, 40), (700, 3, 9), (16384, 2, 1)):
+        g = torch.Generator().manual_seed(batch)
+        lens = torch.randint(0, most + 1, (batch,), generator=g).tolist()
+        ids = torch.randint(-1, adapters, (batch,), generator=g).tolist()
+        lens[0], ids[0] = 2, adapters - 1
+        s = Step(lens, ids, 64, [32], 8, adapters, dtype)
+        s.check(s.apply())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_values_at_the_types_ends(dtype):
+    """Low-rank numbers past f16's range, small ones beside them, rows of zeros, and rows that are not finite."""
+    s = Step([5, 4], [0, 1], 512, [64, 32], 16, 2, dtype, x_gain=1000.0)
+    s.b[0] *= 2.0 ** -9
+    s.b[1] *= 2.0 ** -9
+    s.a[0, :16] *= 512
+    s.a[1, 3] *= 2.0 ** -12
+    s.x[2] = 0
+    out = s.apply()
+    s.check(out)
+    assert torch.equal(out[2], s.y[2])
+    s.x[4, 7], s.x[7, 500] = float("inf"), float("nan")
+    out2 = s.apply()
+    assert not out2[4].isfinite().all() and out2[7].isnan().all()
+    keep = [0, 1, 2, 3, 5, 6, 8]
+    assert torch.equal(out2[keep], out[keep])
+
+
+@pytest.mark.gpu
+def test_broadcast_rows_no_scales_and_four_dimensions():
+    s = Step([30, 1], [1, 0], 128, [64], 8, 2, "bf16")
+    s.x = s.x[:1].expand(31, 128)
+    s.check(s.apply())
+    s.scales[:] = 1
+    got = s.handle.apply(s.x, s.y, s.a.view(2, 1, 8, 128), s.b, None, s.offsets, s.ids)
+    s.check(got)
+    empty = s.handle.apply(s.x[:0], s.y[:0], s.a, s.b, None, s.offsets, s.ids)
+    assert empty.shape == (0, 64)
+    # offsets that reach past the rows there are
+    got = s.handle.apply(s.x[:9], s.y[:9], s.a, s.b, None, s.offsets, s.ids)
+    want, bound = s.want()
+    assert ((got.double() - want[:9]).abs() <= bound[:9]).all()
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Adapters more than 2^31 elements in, rows as far apart."""
+    width, rank, adapters = 1 << 20, 128, 18
+    handle = binding.Adapters(width, [32], rank, "bf16")
+    a = torch.zeros(adapters, rank, width, dtype=torch.bfloat16, device="cuda")
+    a[17, 127, 1048570], a[16, 0, 3] = 2.0, 3.0
+    b = torch.zeros(adapters, 32, rank, dtype=torch.bfloat16, device="cuda")
+    b[17, 31, 127], b[16, 0, 0] = 0.5, 4.0
+    far = torch.zeros((1 << 31) + 64 + width, dtype=torch.bfloat16, device="cuda")
+    x = far.as_strided((2, width), ((1 << 31) + 64, 1))
+    x[0, 3], x[1, 1048570] = 1.5, 7.0
+    y = torch.zeros(2, 32, dtype=torch.bfloat16, device="cuda")
+    out = handle.apply(x, y, a, b, None, torch.tensor([0, 1, 2], dtype=torch.int32).cuda(),
+                       torch.tensor([16, 17], dtype=torch.int32).cuda())
+    want = torch.zeros(2, 32)
+    want[0, 0], want[1, 31] = 18.0, 7.0
+    assert torch.equal(out.cpu().float(), want)
+
+
+@pytest.mark.gpu
+def test_streams_graphs_and_repeats():
+    s = Step([3, 1, 20, 6], [1, 0, 2, 1], 1024, [256, 64], 16, 3, "bf16")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = s.apply(stream=side)
+    side.synchronize()
+    s.check(out)
+    assert all(torch.equal(s.apply(), out) for _ in range(3))
+    graph = torch.cuda.CUDAGraph()
+    held = torch.empty_like(s.y)
+    with torch.cuda.graph(graph):
+        s.apply(held)
+    for ids in ([0, 0, 0, 0], [2, -1, 1, 0], [1, 2, 2, 2]):
+        s.ids.copy_(torch.tensor(ids, dtype=torch.int32))
+        s.x.copy_(torch.randn(s.x.shape))
+        s.of = [a for n, a in zip([3, 1, 20, 6], ids) for _ in range(n)]
+        graph.replay()
+        s.check(held)

@@ -1149,18 +1149,15 @@ class PageTables(_Workspace):
             decode_attn_pages_init(self.plan, pool.data_ptr(), s.cuda_stream)
         return pool
 
-    def _places(self, pool, block_table, lens, others):
+    def _checked(self, pool, block_table, lens):
+        """The device's index, once the three are what they should be."""
         _int32("pool", pool, self._pool)
         _int32("block_table", block_table, self._table)
         _int32("the sequences' lengths", lens, self._batch)
         index, ws = pool.get_device(), self.workspace
-        away = index < 0 or block_table.get_device() != index or lens.get_device() != index or \
-            (ws is not None and ws.get_device() != index)
-        for t in others:
-            away = away or t.get_device() != index
-        if away:
-            _refuse_devices(index, pool=pool, block_table=block_table, lengths=lens, workspace=ws,
-                            **{f"tensor {i}": t for i, t in enumerate(others)})
+        if index < 0 or block_table.get_device() != index or lens.get_device() != index or \
+                (ws is not None and ws.get_device() != index):
+            _refuse_devices(index, pool=pool, block_table=block_table, lengths=lens, workspace=ws)
         return index
 
     def reserve(self, pool, block_table, row_offsets, ctx_lens, rows: int, seq_lens=None, slots=None,
@@ -1168,20 +1165,31 @@ class PageTables(_Workspace):
         """Pages for a step of `rows` rows: sequence b holds ctx_lens[b] tokens and gets the rows row_offsets[b]
         to row_offsets[b + 1]. Returns (seq_lens, slots, positions): the lengths then (ctx_lens itself: in
         place), each row's cache row (-1: none) and position; allocated when None. Where the pool has too few
-        pages nothing is taken, every slot is -1 and pool[1] says how many were missing."""
-        _int32("row_offsets", row_offsets, self._batch + 1)
+        pages nothing is taken, every slot is -1 and pool[1] says how many
+        were missing."""
+        index, batch = self._checked(pool, block_table, ctx_lens), self._batch
+        _int32("row_offsets", row_offsets, batch + 1)
         if rows < 0:
             raise ValueError("rows must not be negative")
+        away = row_offsets.get_device() != index
         if seq_lens is None:
-            seq_lens = _empty((self._batch,), _torch.int32, pool.device, stream)
+            seq_lens = _empty((batch,), _torch.int32, pool.device, stream)
+        else:
+            _int32("seq_lens", seq_lens, batch)
+            away = away or seq_lens.get_device() != index
         if slots is None:
             slots = _empty((rows,), _torch.int32, pool.device, stream)
+        else:
+            _int32("slots", slots, rows)
+            away = away or slots.get_device() != index
         if positions is None:
             positions = _empty((rows,), _torch.int32, pool.device, stream)
-        _int32("seq_lens", seq_lens, self._batch)
-        _int32("slots", slots, rows)
-        _int32("positions", positions, rows)
-        index = self._places(pool, block_table, ctx_lens, (row_offsets, seq_lens, slots, positions))
+        else:
+            _int32("positions", positions, rows)
+            away = away or positions.get_device() != index
+        if away:
+            _refuse_devices(index, pool=pool, row_offsets=row_offsets, seq_lens=seq_lens, slots=slots,
+                            positions=positions)
         self._reserve(self.plan, index, stream, pool.data_ptr(), block_table.data_ptr(), row_offsets.data_ptr(),
                       ctx_lens.data_ptr(), rows, seq_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(),
                       0 if self.workspace is None else self._workspace_on(index, stream), self.workspace_bytes)
@@ -1190,8 +1198,10 @@ class PageTables(_Workspace):
     def release(self, pool, block_table, seq_lens, keep_lens, stream=None):
         """Cut sequences back from seq_lens[b] to keep_lens[b] tokens (0: it has ended): the pages they lose
         go back to the pool, and their entries become -1."""
+        index = self._checked(pool, block_table, seq_lens)
         _int32("keep_lens", keep_lens, self._batch)
-        index = self._places(pool, block_table, seq_lens, (keep_lens,))
+        if keep_lens.get_device() != index:
+            _refuse_devices(index, pool=pool, keep_lens=keep_lens)
         self._release(self.plan, index, stream, pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
                       keep_lens.data_ptr(), 0 if self.workspace is None else self._workspace_on(index, stream),
                       self.workspace_bytes)
@@ -1230,9 +1240,7 @@ class RMSNorm:
     def apply(self, x, weight=None, residual=None, out=None, residual_out=None, stream=None):
         """y in x's type, into `out` (x itself: in place; allocated when None). With a residual returns
         (out, u): u goes into residual_out (x or residual itself: in place; allocated when None)."""
-        if out is None:
-            out = _empty(x.shape, x.dtype, x.device, stream)
-        total = self._call(x, weight, residual, out, residual_out, None, None, 0, 0, stream)
+        out, total, _, _ = self._call(x, weight, residual, out, residual_out, None, None, 0, 0, True, stream)
         return out if residual is None else (out, total)
 
     def quantise(self, x, weight=None, residual=None, scaling: str = "row", group: int = 128, codes=None,
@@ -1246,71 +1254,89 @@ class RMSNorm:
             raise ValueError(f"scaling must be one of {sorted(SCALING_CODES)}")
         if kind == 3 and group not in (32, 64, 128):
             raise ValueError("group must be 32, 64 or 128")
-        if codes is None:
-            codes = _empty(x.shape, _torch.float8_e4m3fn, x.device, stream)
-        elif codes.dtype is not _torch.float8_e4m3fn and codes.dtype is not _torch.uint8:
-            raise ValueError("codes must be float8_e4m3fn or uint8")
-        shape = (1,) if kind == 1 else x.shape[:-1] if kind == 2 else \
-            (*x.shape[:-1], -(-self.n // group))
-        if scales is None:
-            if kind == 1:
-                raise ValueError("scaling by tensor takes scales")
-            scales = _empty(shape, _torch.float32, x.device, stream)
-        elif scales.dtype is not _torch.float32 or not scales.is_contiguous() or \
-                (scales.numel() != 1 if kind == 1 else scales.shape != shape):
-            raise ValueError(f"scales must be a contiguous float32 tensor {list(shape)}")
-        total = self._call(x, weight, residual, out, residual_out, codes, scales, kind, group, stream)
+        _, total, codes, scales = self._call(x, weight, residual, out, residual_out, codes, scales, kind, group, False,
+                                             stream)
         return codes, scales, total
 
-    def _rows(self, name, t, shape, dtype):
+    def _strides(self, name, t, shape, dtype, index):
+        """Strides of rows and heads of a tensor that has to be like x."""
         if t.shape != shape or t.dtype is not dtype:
             raise ValueError(f"{name} must be a {list(shape)} tensor of {dtype}")
         st = t.stride()
         if st[-1] != 1 and self.n > 1 and t.numel():
             raise ValueError(f"the last dimension of {name} must be contiguous")
-        return (st[0], 0) if len(st) == 2 else (st[0], st[1])
+        if t.get_device() != index:
+            _refuse_devices(index, **{name: t})
+        return st[0], 0 if len(st) == 2 else st[1]
 
-    def _call(self, x, weight, residual, out, residual_out, codes, scales, kind, group, stream):
-        shape, dtype = x.shape, x.dtype
-        code = self._codes.get(dtype)
+    def _call(self, x, weight, residual, out, residual_out, codes, scales, kind, group, want_out, stream):
+        shape, dtype, n = x.shape, x.dtype, self.n
+        code, dims = self._codes.get(dtype), len(shape)
         if code is None:
             raise ValueError("x must be fp32, fp16 or bf16")
-        if not 2 <= len(shape) <= 3 or shape[-1] != self.n:
-            raise ValueError(f"x must be a [rows, {self.n}] or [rows, heads, {self.n}] tensor")
-        if _torch.is_grad_enabled():
+        if (dims != 2 and dims != 3) or shape[-1] != n:
+            raise ValueError(f"x must be a [rows, {n}] or [rows, heads, {n}] tensor")
+        if _torch.is_grad_enabled() and (
+                x.requires_grad or (weight is not None and weight.requires_grad) or
+                (residual is not None and residual.requires_grad) or (out is not None and out.requires_grad) or
+                (residual_out is not None and residual_out.requires_grad)):
             _refuse_autograd(x=x, weight=weight, residual=residual, out=out, residual_out=residual_out)
-        xs, index = self._rows("x", x, shape, dtype), x.get_device()
-        rs = us = os_ = cs = (0, 0)
-        res_at = u_at = out_at = code_at = scale_at = weight_at = wide = 0
-        away = index < 0
+        rows, heads, index = shape[0], 1 if dims == 2 else shape[1], x.get_device()
+        x_row, x_head = self._strides("x", x, shape, dtype, index)
+        plain = heads * n     # strides of what is allocated here: plain, n
+        r_row = r_head = u_row = u_head = o_row = o_head = c_row = c_head = 0
+        r_at = u_at = o_at = c_at = s_at = w_at = wide = 0
+        if weight is not None:
+            wide = 1 if weight.dtype is _torch.float32 else 0
+            if (not wide and weight.dtype is not dtype) or weight.shape != (n,) or not weight.is_contiguous():
+                raise ValueError(f"weight must be a contiguous [{n}] tensor of {dtype} or float32")
+            w_at = weight.data_ptr()
+            if weight.get_device() != index:
+                _refuse_devices(index, weight=weight)
         if residual is not None:
-            if residual_out is None:
-                residual_out = _empty(shape, dtype, x.device, stream)
-            rs, us = self._rows("residual", residual, shape, dtype), self._rows("residual_out", residual_out, shape, dtype)
-            res_at, u_at = residual.data_ptr(), residual_out.data_ptr()
-            away = away or residual.get_device() != index or residual_out.get_device() != index
+            r_row, r_head = self._strides("residual", residual, shape, dtype, index)
+            r_at = residual.data_ptr()
         elif residual_out is not None:
             raise ValueError("residual_out without a residual")
-        if weight is not None:
-            wide = weight.dtype is _torch.float32
-            if (not wide and weight.dtype is not dtype) or weight.shape != (self.n,) or not weight.is_contiguous():
-                raise ValueError(f"weight must be a contiguous [{self.n}] tensor of {dtype} or float32")
-            weight_at = weight.data_ptr()
-            away = away or weight.get_device() != index
+        if residual_out is not None:
+            u_row, u_head = self._strides("residual_out", residual_out, shape, dtype, index)
         if out is not None:
-            os_, out_at = self._rows("out", out, shape, dtype), out.data_ptr()
-            away = away or out.get_device() != index
+            o_row, o_head = self._strides("out", out, shape, dtype, index)
         if codes is not None:
-            cs, code_at, scale_at = self._rows("codes", codes, shape, codes.dtype), codes.data_ptr(), scales.data_ptr()
-            away = away or codes.get_device() != index or scales.get_device() != index
-        if away:
-            _refuse_devices(index, x=x, residual=residual, residual_out=residual_out, weight=weight, out=out,
-                            codes=codes, scales=scales)
-        rows, heads = shape[0], 1 if len(shape) == 2 else shape[1]
+            if codes.dtype is not _torch.float8_e4m3fn and codes.dtype is not _torch.uint8:
+                raise ValueError("codes must be float8_e4m3fn or uint8")
+            c_row, c_head = self._strides("codes", codes, shape, codes.dtype, index)
+        if kind:
+            many = (1,) if kind == 1 else shape[:-1] if kind == 2 else (*shape[:-1], -(-n // group))
+            if scales is None:
+                if kind == 1:
+                    raise ValueError("scaling by tensor takes scales")
+            elif scales.dtype is not _torch.float32 or not scales.is_contiguous() or \
+                    (scales.numel() != 1 if kind == 1 else scales.shape != many):
+                raise ValueError(f"scales must be a contiguous float32 tensor {list(many)}")
+            elif scales.get_device() != index:
+                _refuse_devices(index, scales=scales)
+        if index < 0:
+            _refuse_devices(index, x=x)
+        # results that are not given
+        if residual is not None:
+            if residual_out is None:
+                residual_out, u_row, u_head = _empty(shape, dtype, x.device, stream), plain, n
+            u_at = residual_out.data_ptr()
+        if want_out and out is None:
+            out, o_row, o_head = _empty(shape, dtype, x.device, stream), plain, n
+        if out is not None:
+            o_at = out.data_ptr()
+        if kind:
+            if codes is None:
+                codes, c_row, c_head = _empty(shape, _torch.float8_e4m3fn, x.device, stream), plain, n
+            if scales is None:
+                scales = _empty(many, _torch.float32, x.device, stream)
+            c_at, s_at = codes.data_ptr(), scales.data_ptr()
         if rows and heads:
-            self._apply(self._at, index, stream, x.data_ptr(), res_at, weight_at, u_at, out_at, code_at, scale_at,
-                        code, 1 if wide else 0, kind, group, rows, heads, *xs, *rs, *us, *os_, *cs)
-        return residual_out
+            self._apply(self._at, index, stream, x.data_ptr(), r_at, w_at, u_at, o_at, c_at, s_at, code, wide, kind,
+                        group, rows, heads, x_row, x_head, r_row, r_head, u_row, u_head, o_row, o_head, c_row, c_head)
+        return out, residual_out, codes, scales
 
 
 class Adapters:
@@ -1350,12 +1376,14 @@ class Adapters:
         """x [rows, width] and y [rows, columns] (rows may be strided), rows by request (row_offsets int32
         [batch + 1]), adapter_ids int32 [batch] (-1: none), scales float32 [adapters] or None. Returns out
         (y itself: in place; allocated when None)."""
-        if _torch.is_grad_enabled():
+        if _torch.is_grad_enabled() and (x.requires_grad or y.requires_grad or a.requires_grad or b.requires_grad or
+                                         (scales is not None and scales.requires_grad) or
+                                         (out is not None and out.requires_grad)):
             _refuse_autograd(x=x, y=y, a=a, b=b, scales=scales, out=out)
+        x_row, y_row = self._rows("x", x, self.width), self._rows("y", y, self.columns)
         if out is None:
             out = _empty(y.shape, self.dtype, y.device, stream)
-        x_row, y_row, out_row = self._rows("x", x, self.width), self._rows("y", y, self.columns), \
-            self._rows("out", out, self.columns)
+        out_row = self._rows("out", out, self.columns)
         rows, n = x.shape[0], a.shape[0]
         if y.shape[0] != rows or out.shape[0] != rows:
             raise ValueError("x, y and out must have as many rows")

@@ -315,6 +315,8 @@ class da_adapter_args(ctypes.Structure):
         ("x_row_stride", ctypes.c_int64),
         ("y_row_stride", ctypes.c_int64),
         ("out_row_stride", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
         ("cuda_stream", ctypes.c_void_p),
     ]
 
@@ -374,6 +376,9 @@ def lib():
         L.decode_attn_norm_apply.argtypes = [ctypes.POINTER(da_norm_config), ctypes.POINTER(da_norm_args)]
         L.decode_attn_adapters_apply.argtypes = [ctypes.POINTER(da_adapter_config),
                                                  ctypes.POINTER(da_adapter_args)]
+        L.decode_attn_adapters_workspace.argtypes = [ctypes.POINTER(da_adapter_config), ctypes.c_int,
+                                                     ctypes.POINTER(ctypes.c_size_t)]
+        L.decode_attn_adapters_check_status.argtypes = [P, P]
         L.decode_attn_rope_destroy.argtypes = [P]
         L.decode_attn_rope_destroy.restype = None
         L.decode_attn_destroy.argtypes = [P]
@@ -394,6 +399,7 @@ def lib():
                      "decode_attn_tree_check_status", "decode_attn_pages_init",
                      "decode_attn_pages_reserve", "decode_attn_pages_release",
                      "decode_attn_norm_apply", "decode_attn_adapters_apply",
+                     "decode_attn_adapters_workspace", "decode_attn_adapters_check_status",
                      "decode_attn_abi_version"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -602,6 +608,19 @@ def decode_attn_norm_apply(config: da_norm_config, args: da_norm_args):
 def decode_attn_adapters_apply(config: da_adapter_config, args: da_adapter_args):
     _check(lib().decode_attn_adapters_apply(ctypes.byref(config), ctypes.byref(args)),
            "decode_attn_adapters_apply")
+
+
+def decode_attn_adapters_workspace(config: da_adapter_config, rows: int) -> int:
+    """Bytes of the workspace with which a call over `rows` rows is fastest."""
+    n = ctypes.c_size_t()
+    _check(lib().decode_attn_adapters_workspace(ctypes.byref(config), rows, ctypes.byref(n)),
+           "decode_attn_adapters_workspace")
+    return n.value
+
+
+def decode_attn_adapters_check_status(workspace: int, stream: int = 0):
+    _check(lib().decode_attn_adapters_check_status(workspace, stream or None),
+           "decode_attn_adapters_check_status")
 
 
 def decode_attn_destroy(plan):
@@ -1347,6 +1366,8 @@ class Adapters:
     contiguous, of `dtype` ("f32", "f16", "bf16") as x and y are. Autograd does not record the call; tensors
     that require a gradient are refused outside no_grad()."""
 
+    LONG = 1024   # rows from which a step may use a workspace
+
     def __init__(self, width: int, out_sizes, rank: int, dtype: str = "bf16"):
         self._apply = _entry("decode_attn_adapters_apply", da_adapter_args)
         out_sizes = [int(n) for n in out_sizes]
@@ -1410,7 +1431,14 @@ class Adapters:
             _refuse_devices(index, x=x, y=y, out=out, a=a, b=b, scales=scales, row_offsets=row_offsets,
                             adapter_ids=adapter_ids)
         if rows:
+            # long steps' low-rank sums, from the pool of the call's stream and its again after the call
+            ws, size = None, 0
+            if rows >= self.LONG and self.dtype is not _torch.float32:
+                with _torch.cuda.device(index):
+                    size = decode_attn_adapters_workspace(self.config, rows)
+                if size:
+                    ws = _empty((size,), _torch.uint8, x.device, stream)
             self._apply(self._at, index, stream, x.data_ptr(), y.data_ptr(), out.data_ptr(), a.data_ptr(),
                         b.data_ptr(), scale_at, row_offsets.data_ptr(), adapter_ids.data_ptr(), rows, batch, n,
-                        x_row, y_row, out_row)
+                        x_row, y_row, out_row, 0 if ws is None else ws.data_ptr(), size)
         return out

@@ -9,6 +9,10 @@ using namespace da;
 
 namespace {
 
+// Rows of a step from which the tall kernels are launched. They cost two launches where no request is long (4 us),
+// and a request of 1024 rows 60 us without them.
+constexpr int kTallStep = 1024;
+
 bool begins_on_16(const void* p, long long stride, int es) { return aligned(p, 16) && stride * es % 16 == 0; }
 
 }  // namespace
@@ -50,8 +54,16 @@ int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter
       may_share(flat(a.a, (long long)a.adapters * low * c.width * es), out) ||
       may_share(flat(a.b, (long long)a.adapters * columns * c.rank * es), out) ||
       (a.scales && may_share(flat(a.scales, 4ll * a.adapters), out)) ||
-      may_share(flat(a.row_offsets, 4ll * (a.batch + 1)), out) || may_share(flat(a.adapter_ids, 4ll * a.batch), out))
+      may_share(flat(a.row_offsets, 4ll * (a.batch + 1)), out) || may_share(flat(a.adapter_ids, 4ll * a.batch), out) ||
+      !aligned(a.workspace, 256))
     return DA_ERR_INVALID_ARG;
+  if (a.workspace && a.workspace_bytes) {   // the sums are results too
+    const RowRuns ws = flat(a.workspace, (long long)a.workspace_bytes);
+    if (may_share(ws, out) || may_share(ws, x) || may_share(ws, y) ||
+        may_share(ws, flat(a.a, (long long)a.adapters * low * c.width * es)) ||
+        may_share(ws, flat(a.b, (long long)a.adapters * columns * c.rank * es)))
+      return DA_ERR_INVALID_ARG;
+  }
   p.x = a.x;
   p.y = a.y;
   p.out = a.out;
@@ -76,9 +88,17 @@ int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter
   const int sms = device_sms();
   if (sms <= 0) return DA_ERR_CUDA;
 
+  // Requests of many rows go to the tensor cores' two launches, where the step has enough of them to be worth it
+  // and a workspace for their sums is there.
+  const int shares = tall_shares(a.rows, c.width, sms);
+  const bool tall = vec && c.dtype != DA_F32 && a.rows >= kTallStep && a.workspace && tall_fits(p, c.rank, sms);
+  p.tall = tall ? kTallRows : INT_MAX;
+  if (tall && a.workspace_bytes < tall_workspace(a.rows, low, shares)) return DA_ERR_WORKSPACE_TOO_SMALL;
+
   // Tiles of 16 rows where an adapter has few, of 64 where it has many (the weights come from L2 once a tile).
   const int groups = std::min(a.batch, a.adapters);
-  const long long each = a.rows / groups;
+  const long long most_rows = tall ? std::min((long long)a.rows, (kTallRows - 1ll) * a.batch) : a.rows;
+  const long long each = most_rows / groups;
   int mt = !vec || c.dtype == DA_F32 || each < 20 ? 1 : each < 48 ? 2 : 4;
   const int column_tiles = low / 8;
   if (mt == 4 && column_tiles > 32) mt = 2;
@@ -89,19 +109,22 @@ int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter
   p.n_tiles = (column_tiles + p.n_groups - 1) / p.n_groups;
   p.pitch = low + ((8 - low) & 31);   // (8 mod 32: the accumulators' pairs of eight rows on different banks)
   const int m = 16 * mt;
-  const long long tiles = a.rows / m + std::min({(long long)a.batch, (long long)a.adapters + p.copy, (long long)a.rows});
-  // CTAs a tile: as many as two an SM allow
+  // (rows without an adapter are copied whatever their number)
+  const long long tiles = (p.copy ? a.rows : most_rows) / m +
+                          std::min({(long long)a.batch, (long long)a.adapters + p.copy, (long long)a.rows});
+  // CTAs a tile: as many as two an SM allow (by a count that is the same in place, as the sums' order is then)
   int ranks = 8;
-  while (ranks > 1 && tiles * ranks > 2ll * sms) ranks /= 2;
+  while (ranks > 1 && (a.rows / m + groups) * ranks > 2ll * sms) ranks /= 2;
   const size_t smem = adapter_smem(a.adapters, mt, c.parts, c.rank, es, p.n_groups, p.pitch);
   if (smem + 4096 > kSmemLimit || tiles * ranks > INT_MAX) return DA_ERR_UNSUPPORTED;
   const void* fn = c.dtype == DA_F32   ? adapter_kernel_f32(c.rank, mt, vec)
                    : c.dtype == DA_F16 ? adapter_kernel_f16(c.rank, mt, vec)
                                        : adapter_kernel_bf16(c.rank, mt, vec);
   if (!fn) return DA_ERR_UNSUPPORTED;
-  cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return cuda_fail(e, "preparing the adapter kernel");
+  if (smem > 40 * 1024) {
+    const int rc = raise_smem(fn, kSmemLimit - 4096, 0);
+    if (rc != DA_OK) return rc;
+  }
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)ranks;
@@ -114,8 +137,31 @@ int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter
   cfg.attrs = at;
   cfg.numAttrs = 1;
   void* kargs[1] = {&p};
-  e = cudaLaunchKernelExC(&cfg, fn, kargs);
-  return e == cudaSuccess ? DA_OK : cuda_fail(e, "launching the adapter kernel");
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, kargs);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the adapter kernel");
+  return tall ? launch_tall(p, c.rank, c.dtype == DA_BF16, shares, sms, a.workspace, cfg.stream) : DA_OK;
+}
+
+int decode_attn_adapters_workspace(const da_adapter_config* config, int rows, size_t* bytes) {
+  if (!config || !bytes || rows < 0 || config->width < 1 || config->parts < 1) return DA_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (rows < kTallStep || config->dtype == DA_F32) return DA_OK;
+  const int sms = device_sms();
+  if (sms <= 0) return DA_ERR_CUDA;
+  const long long low = (long long)config->parts * config->rank;
+  if (low <= 256) *bytes = tall_workspace(rows, (int)low, tall_shares(rows, config->width, sms));
+  return DA_OK;
+}
+
+int decode_attn_adapters_check_status(void* workspace, void* cuda_stream) {
+  if (!workspace) return DA_ERR_INVALID_ARG;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  int32_t st = 0;
+  cudaError_t e = cudaMemcpyAsync(&st, workspace, 4, cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, 4, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "reading the device status");
+  return status_to_error(st);
 }
 
 }  // extern "C"

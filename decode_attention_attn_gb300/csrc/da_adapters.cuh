@@ -41,7 +41,25 @@ struct AdapterParams {
   int pitch;                    // floats of a row of partial sums
   int copy;                     // rows without an adapter are copied (out is not y)
   int x_wide, y_wide;           // (of the kernel for odd shapes) x and weights / y and out by 16 bytes
+  int tall;                     // requests of as many rows with an adapter are left to the tall kernels
 };
+
+// Requests of many rows: what their kernels take beside AdapterParams, in da_adapters_tall.cu.
+constexpr int kTallRows = 32;           // rows from which a request is theirs, where they are launched
+constexpr size_t kTallStatusBytes = 256;
+struct TallParams {
+  float4* sums;                 // [shares, low / 4, rows]: low-rank sums, four columns of a row
+  int32_t* status;
+  int rank, shares, stages, most_tiles;
+  int n;                        // low-rank columns, to a multiple of 16
+  uint32_t tmem_cols;
+  int blocks[kMaxParts + 1];    // blocks of 128 columns ahead of each part; all of them
+};
+long long most_tall_tiles(const AdapterParams& p);
+bool tall_fits(const AdapterParams& p, int rank, int sms);
+int tall_shares(int rows, int width, int sms);
+size_t tall_workspace(int rows, int low, int shares);
+int launch_tall(const AdapterParams& p, int rank, bool bf16, int shares, int sms, void* workspace, cudaStream_t stream);
 
 // Bytes of dynamic shared memory: the partial sums of every group of warps (where the counts of rows lay before),
 // the sums over the cluster, and them as operands.
@@ -99,6 +117,12 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
     hy = __uint_as_float(hi & 0xffff0000u);
   }
   lo = pack2(fabsf(hx) <= 3.4028235e38f ? x - hx : 0.f, fabsf(hy) <= 3.4028235e38f ? y - hy : 0.f, T());
+}
+
+// The power of two that takes numbers of up to `most` below 2^8 (1: there is nothing finite to go by).
+__device__ __forceinline__ float low_rank_scale(float most) {
+  const int e = most > 0.f && most <= 3.4028235e38f ? (int)(__float_as_uint(most) >> 23) - 127 - 7 : 0;
+  return __uint_as_float((uint32_t)(127 - min(max(e, -120), 120)) << 23);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -179,6 +203,14 @@ __device__ __forceinline__ int block_prefix(int mine, AdapterShared& sh) {
   return before + upto - mine;
 }
 
+// The same in a wider block, of whose threads only the first kAdapterThreads bring anything.
+__device__ __forceinline__ int wide_prefix(int mine, AdapterShared& sh) {
+  if (threadIdx.x < kAdapterThreads) return block_prefix(mine, sh);
+  __syncthreads();
+  __syncthreads();
+  return 0;
+}
+
 // Rows of request b, and the adapter they take (`adapters`: none).
 __device__ __forceinline__ int rows_of(const AdapterParams& p, int b, int& first) {
   first = min(max(__ldg(p.row_offsets + b), 0), p.rows);
@@ -201,7 +233,8 @@ __device__ void find_tile(const AdapterParams& p, int t, int* s_count, int* s_ro
   for (int b = tid; b < p.batch; b += kAdapterThreads) {
     int first;
     const int n = rows_of(p, b, first);
-    if (n) atomicAdd(s_count + adapter_of(p, b), n);
+    const int a = adapter_of(p, b);
+    if (n && (n < p.tall || a == p.adapters)) atomicAdd(s_count + a, n);
   }
   __syncthreads();
   for (int i0 = 0, base = 0; i0 < buckets; i0 += kAdapterThreads) {
@@ -223,6 +256,7 @@ __device__ void find_tile(const AdapterParams& p, int t, int* s_count, int* s_ro
     const int b = b0 + tid;
     int row = 0, n = 0;
     if (b < p.batch && adapter_of(p, b) == adapter) n = rows_of(p, b, row);
+    if (n >= p.tall && adapter < p.adapters) n = 0;
     const int before = base + block_prefix(n, sh);
     for (int i = max(first - before, 0); i < n && before + i < end; ++i) s_row[before + i - first] = row + i;
     base += sh.chunk_total;
@@ -248,6 +282,7 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
   const int tile = (int)(blockIdx.x / ranks);
   const int low = p.parts * R, pitch = p.pitch;    // low-rank columns
+  pdl_launch_dependents();                         // (the tall kernels' rows are others)
 
   find_tile<M>(p, tile, reinterpret_cast<int*>(smem), s_row, sh);
   const int adapter = min(sh.adapter, p.adapters);
@@ -405,17 +440,15 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
   if (ranks > 1) cluster_arrive();   // (waited for at the end: nobody leaves while its sums are read)
   __syncthreads();
   if constexpr (std::is_same<T, __half>::value) {
-    // f16 ends at 65504: a row's numbers are taken by a power of two to at most 2^8 and less than 2^-24 below that
-    // is lost; the product is taken back by it. (Rows with nothing finite to scale by stay as they are.)
+    // f16 ends at 65504: a row's numbers are taken by a power of two to below 2^8, and less than 2^-32 of the
+    // largest is lost; the product is taken back by it.
     for (int i = warp; i < M * (part1 - part0); i += kAdapterWarps) {
       const int m = i / (part1 - part0), s = part0 + i - m * (part1 - part0);
       float most = 0.f;
       for (int n = lane; n < R; n += 32) most = fmaxf(most, fabsf(s_sum[(size_t)m * pitch + s * R + n]));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-      int e = most > 0.f && most <= 3.4028235e38f ? ilogbf(most) - 7 : 0;
-      e = min(max(e, -120), 120);
-      if (lane == 0) s_scale[m * kMaxParts + s] = ldexpf(1.f, -e);
+      if (lane == 0) s_scale[m * kMaxParts + s] = low_rank_scale(most);
     }
     __syncthreads();
   }

@@ -53,6 +53,15 @@ int status_to_error(int s);
 // The driver's cuTensorMapEncodeTiled, or null.
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
+// A kernel's shared-memory limit, raised once per device and kernel. regs: the registers that it must have
+// been compiled to (its register split draws on them), or 0.
+int raise_smem(const void* fn, size_t smem, int regs);
+
+// A tensor map of 1- or 2-byte elements, zeros outside it.
+int encode_map(CUtensorMap* map, int es, int rank, const void* base, const cuuint64_t* dims,
+               const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle,
+               CUtensorMapL2promotion promote);
+
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 inline int elem_size(int dt) { return dt == DA_F32 ? 4 : 2; }

@@ -27,6 +27,46 @@ struct da_tree_plan {
   size_t off_status, off_info, off_part_l, off_part_o, ws_bytes;
 };
 
+namespace da {
+
+int raise_smem(const void* fn, size_t smem, int regs) {
+  static std::mutex mu;
+  static std::set<std::pair<int, const void*>> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  std::lock_guard<std::mutex> lk(mu);
+  if (done.count({dev, fn})) return DA_OK;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(shared memory)");
+  if (regs) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, fn);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
+    if (fa.numRegs != regs) return text_fail("kernel not built to the registers of its split");
+  }
+  try {
+    done.insert({dev, fn});
+  } catch (...) {   // out of host memory: asked again next time
+  }
+  return DA_OK;
+}
+
+int encode_map(CUtensorMap* map, int es, int rank, const void* base, const cuuint64_t* dims,
+           const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle,
+           CUtensorMapL2promotion promote) {
+  auto fn = encode_fn();
+  if (!fn) return text_fail("cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint32_t ones[5] = {1u, 1u, 1u, 1u, 1u};
+  const CUresult r =
+      fn(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+         (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DA_OK : text_fail("cuTensorMapEncodeTiled refused a tensor map");
+}
+
+}  // namespace da
+
 namespace {
 
 // ---- fp32 caches: CUDA cores ------------------------------------------------------------------
@@ -358,44 +398,6 @@ const void* core_kernel(int D) {
 
 bool uses_mma(const da_problem& p) { return p.kv_fp8 || p.qkv_dtype != DA_F32; }
 
-// The kernel's shared-memory limit, raised once per device and kernel. regs: the registers that the
-// kernel must have been compiled to (its register split draws on them), or 0.
-int raise_smem(const void* fn, size_t smem, int regs) {
-  static std::mutex mu;
-  static std::set<std::pair<int, const void*>> done;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  std::lock_guard<std::mutex> lk(mu);
-  if (done.count({dev, fn})) return DA_OK;
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(tree kernel)");
-  if (regs) {
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, fn);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
-    if (fa.numRegs != regs) return text_fail("tree kernel not built to the registers of its split");
-  }
-  try {
-    done.insert({dev, fn});
-  } catch (...) {   // out of host memory: asked again next time
-  }
-  return DA_OK;
-}
-
-int encode(CUtensorMap* map, int es, int rank, const void* base, const cuuint64_t* dims,
-           const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle,
-           CUtensorMapL2promotion promote) {
-  auto fn = encode_fn();
-  if (!fn) return text_fail("cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint32_t ones[5] = {1u, 1u, 1u, 1u, 1u};
-  const CUresult r =
-      fn(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
-         (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? DA_OK : text_fail("cuTensorMapEncodeTiled refused a tensor map");
-}
-
 // [tokens, Hkv, D] cache, one box = `box` tokens of one KV head. FP8 caches: rows of codes, swizzled
 // as wide as they are. 16-bit
 // caches in 128-byte-swizzled blocks of 64 elements: contiguous ones as [Hkv, D / 64, tokens, 64], a
@@ -408,7 +410,7 @@ int kv_map(const da_tree_plan& pl, const void* base, int box, CUtensorMap* map) 
   if (p.kv_fp8) {
     const cuuint64_t dims[3] = {D, tokens, H}, strides[2] = {H * D, D};
     const cuuint32_t b[3] = {(cuuint32_t)D, (cuuint32_t)box, 1u};
-    return encode(map, 1, 3, base, dims, strides, b,
+    return encode_map(map, 1, 3, base, dims, strides, b,
                   D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
   }
@@ -418,11 +420,11 @@ int kv_map(const da_tree_plan& pl, const void* base, int box, CUtensorMap* map) 
     const cuuint64_t dims[5] = {64, 8, D / 64, tokens / 8, H};
     const cuuint64_t strides[4] = {H * D * 2, 128, H * D * 16, D * 2};
     const cuuint32_t b[5] = {64u, 8u, (cuuint32_t)D / 64, (cuuint32_t)box / 8, 1u};
-    return encode(map, 2, 5, base, dims, strides, b, CU_TENSOR_MAP_SWIZZLE_128B, promote);
+    return encode_map(map, 2, 5, base, dims, strides, b, CU_TENSOR_MAP_SWIZZLE_128B, promote);
   }
   const cuuint64_t dims[4] = {64, tokens, D / 64, H}, strides[3] = {H * D * 2, 128, D * 2};
   const cuuint32_t b[4] = {64u, (cuuint32_t)box, 1u, 1u};
-  return encode(map, 2, 4, base, dims, strides, b, CU_TENSOR_MAP_SWIZZLE_128B, promote);
+  return encode_map(map, 2, 4, base, dims, strides, b, CU_TENSOR_MAP_SWIZZLE_128B, promote);
 }
 
 // [rows, Hq, D] q, one box = the G heads of a KV head of 128 / G drafted tokens, one 64-element block.
@@ -431,7 +433,7 @@ int q_map(const da_tree_plan& pl, const void* base, int rows, CUtensorMap* map) 
   const cuuint32_t G = (cuuint32_t)pl.cache.group;
   const cuuint64_t dims[4] = {64, H, (cuuint64_t)rows, D / 64}, strides[3] = {D * 2, H * D * 2, 128};
   const cuuint32_t b[4] = {64u, G, (cuuint32_t)kTreeRows / G, 1u};
-  return encode(map, 2, 4, base, dims, strides, b, CU_TENSOR_MAP_SWIZZLE_128B,
+  return encode_map(map, 2, 4, base, dims, strides, b, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 

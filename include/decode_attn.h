@@ -790,9 +790,14 @@ typedef struct {
  *                 one after another).
  *   scales        nullable device float [adapters] (null: 1).
  *   row_offsets, adapter_ids   device int32 [batch + 1] and [batch].
+ *   workspace     nullable device memory, 256-byte aligned, of decode_attn_adapters_workspace bytes, which lies
+ *                 apart from everything else: 16-bit steps of 1024 rows and more then take requests of 32 rows
+ *                 and more in two further launches on the tensor cores (tcgen05). Its first word takes
+ *                 DEVICE_TIMEOUT, cleared by the caller ahead of the first call; the rest need not be. Two calls
+ *                 that can overlap on the GPU need workspaces of their own.
  * Rows of no request are left as they were. Results do not depend on the order of execution. Rows and parts of
- * 16-byte multiples on 16-byte boundaries move 16 bytes a lane, others an element. Enqueued on cuda_stream, one
- * launch, no workspace. Errors: INVALID_ARG, UNSUPPORTED (dtype, rank, parts, sizes; more than
+ * 16-byte multiples on 16-byte boundaries move 16 bytes a lane, others an element. Enqueued on cuda_stream. Errors:
+ * INVALID_ARG, WORKSPACE_TOO_SMALL, UNSUPPORTED (dtype, rank, parts, sizes; more than
  * DECODE_ATTN_MAX_ADAPTERS adapters or DECODE_ATTN_MAX_PAGED_BATCH requests), CUDA. */
 typedef struct {
   const void* x;
@@ -809,8 +814,17 @@ typedef struct {
   int64_t x_row_stride;
   int64_t y_row_stride;
   int64_t out_row_stride;
+  void* workspace;
+  size_t workspace_bytes;
   void* cuda_stream;
 } da_adapter_args;
+
+/* The workspace with which a call over `rows` rows is fastest (0: it uses none). Errors: INVALID_ARG, CUDA. */
+int decode_attn_adapters_workspace(const da_adapter_config* config, int rows, size_t* bytes);
+
+/* Synchronise `stream`, then read and clear the finding that calls with this workspace left in its first word:
+ * DA_OK or DEVICE_TIMEOUT. */
+int decode_attn_adapters_check_status(void* workspace, void* cuda_stream);
 
 int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter_args* args);
 

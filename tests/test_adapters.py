@@ -45,6 +45,8 @@ def test_apply_refuses_bad_arguments():
     assert call(out=A + P, out_row_stride=384) == -1 and call(out=A + P + 64) == -1
     for i in (0, 3, 4, 5, 6, 7):
         assert call(out=A + i * P) == -1, i
+    assert call(workspace=A + 9 * P + 16, workspace_bytes=4096) == -1
+    assert call(workspace=A + 2 * P + 256, workspace_bytes=4096) == -1      # over the results
     # no rows: nothing is enqueued, no pointer is looked at
     config = binding.da_adapter_config(2, 256, 1, (binding.ctypes.c_int * 4)(128, 0, 0, 0), 16)
     binding.decode_attn_adapters_apply(config, binding.da_adapter_args(*[None] * 8, 0, 1, 1))
@@ -241,6 +243,109 @@ def test_values_at_the_types_ends(dtype):
     assert not out2[4].isfinite().all() and out2[7].isnan().all()
     keep = [0, 1, 2, 3, 5, 6, 8]
     assert torch.equal(out2[keep], out[keep])
+
+
+TALL = {   # lens, ids
+    "prompts": ([1000, 1, 129, 128, 33], [1, 0, 2, 0, 1]),
+    "mixed": ([1] * 40 + [31, 32, 64, 900, 0, 5, 300], [i % 3 for i in range(45)] + [-1, 1]),
+    "bare": ([700, 600, 40, 10], [-1, 2, 9, 0]),
+    "many": ([40] * 60, [i % 3 for i in range(60)]),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("name", list(TALL))
+@pytest.mark.parametrize("width,outs,rank", [(256, [128, 64], 16), (1000, [520, 8, 136], 64), (520, [256], 8), (192, [40, 8, 16, 104], 32),
+                                             (512, [96, 200], 128), (64, [8], 128), (2048, [384, 128], 32)])
+def test_long_requests(dtype, name, width, outs, rank):
+    """Steps that the tensor-core launches take a part of: tiles and blocks that end inside, every rank."""
+    lens, ids = TALL[name]
+    s = Step(lens, ids, width, outs, rank, 3, dtype, before=3, behind=60)
+    before = torch.randn_like(s.y)
+    out = before.clone()
+    s.check(s.apply(out), before)
+    m = s.member.cuda()
+    y0 = s.y.clone()
+    s.apply(s.y)
+    assert torch.equal(s.y[m], out[m]) and torch.equal(s.y[~m], y0[~m])
+
+
+@pytest.mark.gpu
+def test_long_requests_of_strided_rows_repeat_on_streams_and_in_graphs():
+    s = Step([700, 400, 3], [1, 0, 1], 264, [96, 64], 16, 2, "bf16", before=1, behind=1, x_pad=8, y_pad=16, shift=8)
+    wide = s.y._base.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = s.apply(stream=side)
+    side.synchronize()
+    s.check(out)
+    m = s.member.cuda()
+    assert all(torch.equal(s.apply()[m], out[m]) for _ in range(3))
+    # two at once
+    for _ in range(4):
+        a = s.apply(stream=side)
+        b = s.apply()
+        torch.cuda.synchronize()
+        assert torch.equal(a[m], out[m]) and torch.equal(b[m], out[m])
+    graph = torch.cuda.CUDAGraph()
+    held = torch.empty_like(out)
+    with torch.cuda.graph(graph):
+        s.apply(held)
+    for ids in ([0, 0, 0], [-1, 1, 0], [1, 1, 1]):
+        s.ids.copy_(torch.tensor(ids, dtype=torch.int32))
+        s.x.copy_(torch.randn(s.x.shape))
+        s.of = [-1] + [a for n, a in zip([700, 400, 3], ids) for _ in range(n)] + [-1]
+        graph.replay()
+        s.check(held)
+    rows, n = s.y.shape
+    s.apply(s.y)
+    same = torch.ones(rows, n + 16, dtype=torch.bool, device="cuda")
+    same[m, :n] = False
+    assert torch.equal(s.y._base[8:].view(rows, -1)[same], wide[8:].view(rows, -1)[same])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_long_requests_with_values_at_the_types_ends(dtype):
+    s = Step([1100, 60], [0, 1], 512, [64, 32], 16, 2, dtype, x_gain=1000.0)
+    s.b[:] *= 2.0 ** -9
+    s.a[0, :16] *= 512
+    s.a[1, 3] *= 2.0 ** -12
+    s.x[2] = 0
+    out = s.apply()
+    s.check(out)
+    assert torch.equal(out[2], s.y[2])
+    s.x[4, 7], s.x[1130, 500] = float("inf"), float("nan")
+    out2 = s.apply()
+    assert not out2[4].isfinite().all() and out2[1130].isnan().all()
+    keep = torch.ones(1160, dtype=torch.bool)
+    keep[[4, 1130]] = False
+    assert torch.equal(out2[keep.cuda()], out[keep.cuda()])
+
+
+@pytest.mark.gpu
+def test_workspaces_of_long_steps():
+    """Without one a long step is answered all the same, a short one is refused, and nothing is found."""
+    s = Step([1200, 90], [1, 0], 256, [64, 64], 32, 2, "bf16")
+    size = binding.decode_attn_adapters_workspace(s.handle.config, 1290)
+    assert size > 256 and binding.decode_attn_adapters_workspace(s.handle.config, 1023) == 0
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(s.y)
+    args = binding.da_adapter_args(s.x.data_ptr(), s.y.data_ptr(), out.data_ptr(), s.a.data_ptr(), s.b.data_ptr(),
+                                   s.scales.data_ptr(), s.offsets.data_ptr(), s.ids.data_ptr(), 1290, 2, 2, 256, 128, 128,
+                                   ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
+    binding.decode_attn_adapters_apply(s.handle.config, args)
+    s.check(out)
+    binding.decode_attn_adapters_check_status(ws.data_ptr())
+    args.workspace_bytes = size - 1
+    with pytest.raises(binding.DecodeAttnError) as e:
+        binding.decode_attn_adapters_apply(s.handle.config, args)
+    assert e.value.code == -3
+    args.workspace, args.workspace_bytes = None, 0
+    out.zero_()
+    binding.decode_attn_adapters_apply(s.handle.config, args)
+    s.check(out)
 
 
 @pytest.mark.gpu

@@ -99,27 +99,26 @@ int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter
   const int groups = std::min(a.batch, a.adapters);
   const long long most_rows = tall ? std::min((long long)a.rows, (kTallRows - 1ll) * a.batch) : a.rows;
   const long long each = most_rows / groups;
-  int mt = !vec || c.dtype == DA_F32 || each < 20 ? 1 : each < 48 ? 2 : 4;
+  int mt = !vec || c.dtype == DA_F32 || each < 40 ? 1 : each < 64 ? 2 : 4;
   const int column_tiles = low / 8;
   if (mt == 4 && column_tiles > 32) mt = 2;
   if (mt == 2 && column_tiles > 48) mt = 1;
-  const int most = mt == 1 ? 8 : mt == 2 ? 6 : 4;
-  p.n_groups = 1;
-  while ((column_tiles + p.n_groups - 1) / p.n_groups > most) p.n_groups *= 2;
-  p.n_tiles = (column_tiles + p.n_groups - 1) / p.n_groups;
+  const int tiles_of_warp = adapter_tiles(mt, column_tiles, p.n_groups);
   p.pitch = low + ((8 - low) & 31);   // (8 mod 32: the accumulators' pairs of eight rows on different banks)
   const int m = 16 * mt;
   // (rows without an adapter are copied whatever their number)
   const long long tiles = (p.copy ? a.rows : most_rows) / m +
                           std::min({(long long)a.batch, (long long)a.adapters + p.copy, (long long)a.rows});
-  // CTAs a tile: as many as two an SM allow (by a count that is the same in place, as the sums' order is then)
-  int ranks = 8;
-  while (ranks > 1 && (a.rows / m + groups) * ranks > 2ll * sms) ranks /= 2;
+  // CTAs a tile, where an SM holds two at once (by a count that is the same in place, as the sums' order is then;
+  // it is a bound, so that up to three an SM are let in).
+  p.log_ranks = 3;
+  while (p.log_ranks > 0 && (a.rows / m + groups) << p.log_ranks > 3ll * sms) --p.log_ranks;
+  const int ranks = 1 << p.log_ranks;
   const size_t smem = adapter_smem(a.adapters, mt, c.parts, c.rank, es, p.n_groups, p.pitch);
   if (smem + 4096 > kSmemLimit || tiles * ranks > INT_MAX) return DA_ERR_UNSUPPORTED;
-  const void* fn = c.dtype == DA_F32   ? adapter_kernel_f32(c.rank, mt, vec)
-                   : c.dtype == DA_F16 ? adapter_kernel_f16(c.rank, mt, vec)
-                                       : adapter_kernel_bf16(c.rank, mt, vec);
+  const void* fn = c.dtype == DA_F32   ? adapter_kernel_f32(c.rank, mt, tiles_of_warp, vec)
+                   : c.dtype == DA_F16 ? adapter_kernel_f16(c.rank, mt, tiles_of_warp, vec)
+                                       : adapter_kernel_bf16(c.rank, mt, tiles_of_warp, vec);
   if (!fn) return DA_ERR_UNSUPPORTED;
   if (smem > 40 * 1024) {
     const int rc = raise_smem(fn, kSmemLimit - 4096, 0);

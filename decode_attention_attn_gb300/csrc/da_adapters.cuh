@@ -37,7 +37,8 @@ struct AdapterParams {
   int rows, batch, adapters, width, parts;
   int starts[kMaxParts + 1];    // columns of the parts
   int chunks[kMaxParts + 1];    // chunks of 32 columns ahead of each part
-  int n_groups, n_tiles;        // warps that share the low-rank columns, 8-column tiles of each
+  int n_groups;                 // warps that share the low-rank columns
+  int log_ranks;                // CTAs that share a tile
   int pitch;                    // floats of a row of partial sums
   int copy;                     // rows without an adapter are copied (out is not y)
   int x_wide, y_wide;           // (of the kernel for odd shapes) x and weights / y and out by 16 bytes
@@ -100,6 +101,17 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
   hi = tf32(x);
   const float h = __uint_as_float(hi);
   lo = fabsf(h) <= 3.4028235e38f ? tf32(x - h) : 0u;
+}
+// c += a b of fp32 numbers in two tf32 parts: three of the four products (the last is 2^-22 of the first). They are
+// added up from zero and then to c, as the instruction cuts off what it adds to a larger sum.
+__device__ __forceinline__ void add_products(float* c, const uint32_t* hi, const uint32_t* lo, const uint32_t* bh,
+                                             const uint32_t* bl) {
+  float t[4] = {0.f, 0.f, 0.f, 0.f};
+  mma16x8<float>(t, lo, bh[0], bh[1]);
+  mma16x8<float>(t, hi, bl[0], bl[1]);
+  mma16x8<float>(t, hi, bh[0], bh[1]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c[e] += t[e];
 }
 // Two fp32 numbers as two pairs of T: what is left is 2^-18 (bf16) or 2^-24 (f16) of them.
 template <typename T>
@@ -230,11 +242,14 @@ __device__ void find_tile(const AdapterParams& p, int t, int* s_count, int* s_ro
   if (tid < M) s_row[tid] = -1;
   if (tid == 0) sh.adapter = -1;
   __syncthreads();
+  int first0 = 0, n0 = 0, adapter0 = -1;   // of the request that is the thread's first
   for (int b = tid; b < p.batch; b += kAdapterThreads) {
-    int first;
-    const int n = rows_of(p, b, first);
+    int first_row;
+    int n = rows_of(p, b, first_row);
     const int a = adapter_of(p, b);
-    if (n && (n < p.tall || a == p.adapters)) atomicAdd(s_count + a, n);
+    if (n >= p.tall && a < p.adapters) n = 0;
+    if (n) atomicAdd(s_count + a, n);
+    if (b == tid) first0 = first_row, n0 = n, adapter0 = a;
   }
   __syncthreads();
   for (int i0 = 0, base = 0; i0 < buckets; i0 += kAdapterThreads) {
@@ -255,8 +270,13 @@ __device__ void find_tile(const AdapterParams& p, int t, int* s_count, int* s_ro
   for (int b0 = 0, base = 0; b0 < p.batch && base < end; b0 += kAdapterThreads) {
     const int b = b0 + tid;
     int row = 0, n = 0;
-    if (b < p.batch && adapter_of(p, b) == adapter) n = rows_of(p, b, row);
-    if (n >= p.tall && adapter < p.adapters) n = 0;
+    if (b0 == 0) {
+      row = first0;
+      n = adapter0 == adapter ? n0 : 0;
+    } else if (b < p.batch && adapter_of(p, b) == adapter) {
+      n = rows_of(p, b, row);
+      if (n >= p.tall && adapter < p.adapters) n = 0;
+    }
     const int before = base + block_prefix(n, sh);
     for (int i = max(first - before, 0); i < n && before + i < end; ++i) s_row[before + i - first] = row + i;
     base += sh.chunk_total;
@@ -265,13 +285,13 @@ __device__ void find_tile(const AdapterParams& p, int t, int* s_count, int* s_ro
 }
 
 // VEC: rows and weights lie on 16-byte boundaries, parts and the width are multiples of 16 bytes.
-template <typename T, int MT, int R, bool VEC>
-__global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_constant__ AdapterParams p) {
+// NT: 8-column tiles of low-rank columns that a warp holds (those behind the last repeat it).
+template <typename T, int MT, int R, int NT, bool VEC>
+__global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kernel(const __grid_constant__ AdapterParams p) {
   constexpr int M = 16 * MT;                       // rows of a tile
   constexpr bool F32 = std::is_same<T, float>::value;
   constexpr int V = 16 / (int)sizeof(T);           // elements of 16 bytes
   constexpr int KB = 4 * V;                        // of the contraction a warp takes at once: 16 bytes a lane
-  constexpr int NT = MT == 1 ? 8 : MT == 2 ? 6 : 4;   // 8-column tiles a warp holds
   constexpr int STEPS = F32 ? R / 8 : R < 16 ? 1 : R / 16;   // instructions deep, of the expansion
   extern __shared__ __align__(16) char smem[];
   __shared__ AdapterShared sh;
@@ -279,8 +299,8 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
   __shared__ int s_from[M];                        // rows to read: places without one read the tile's first
   __shared__ float s_scale[M * kMaxParts];         // f16: of a row's low-rank numbers, and back
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  const uint32_t rank = cluster_rank(), ranks = cluster_size();
-  const int tile = (int)(blockIdx.x / ranks);
+  const int rank = (int)cluster_rank(), log_ranks = p.log_ranks, ranks = 1 << log_ranks;
+  const int tile = (int)(blockIdx.x >> log_ranks);
   const int low = p.parts * R, pitch = p.pitch;    // low-rank columns
   pdl_launch_dependents();                         // (the tall kernels' rows are others)
 
@@ -293,8 +313,8 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
 
   // the cluster's shares: of the width in blocks of KB, of the columns in chunks of 32
   const int blocks = (p.width + KB - 1) / KB, chunks = p.chunks[p.parts];
-  const int k0 = (int)((long long)blocks * rank / ranks), k1 = (int)((long long)blocks * (rank + 1) / ranks);
-  const int h0 = (int)((long long)chunks * rank / ranks), h1 = (int)((long long)chunks * (rank + 1) / ranks);
+  const int k0 = blocks * rank >> log_ranks, k1 = blocks * (rank + 1) >> log_ranks;
+  const int h0 = chunks * rank >> log_ranks, h1 = chunks * (rank + 1) >> log_ranks;
   auto part_of = [&](int h) {
     int s = 0;
     while (s + 1 < p.parts && h >= p.chunks[s + 1]) ++s;
@@ -308,7 +328,7 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
       const T* from = y + s_row[m] * p.y_rs;
       T* to = out + s_row[m] * p.out_rs;
       const int c1 = p.starts[p.parts];
-      for (int c = ((int)rank * 32 + lane) * V; c < c1; c += 32 * V * (int)ranks) {
+      for (int c = (rank * 32 + lane) * V; c < c1; c += 32 * V * ranks) {
         if (VEC || p.y_wide) {
           *reinterpret_cast<uint4*>(to + c) = __ldg(reinterpret_cast<const uint4*>(from + c));
         } else {
@@ -337,15 +357,14 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int o = 0; o < 2; ++o) xr[i][o] = static_cast<const T*>(p.x) + s_from[i * 16 + 8 * o + g] * p.x_rs;
-    const int n0 = ng * p.n_tiles * 8 + g;
+    const int n0 = ng * NT * 8 + g;
 #pragma unroll MT == 1 ? 2 : 1
     for (int kb = k0 + kg; kb < k1; kb += k_groups) {
       const int k = kb * KB + q * V, left = p.width - k;
       uint4 xv[MT][2], av[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        if (j < p.n_tiles)
-          av[j] = load16<T>(a + (long long)min(n0 + j * 8, low - 1) * p.width, k, left, VEC || p.x_wide);
+        av[j] = load16<T>(a + (long long)min(n0 + j * 8, low - 1) * p.width, k, left, VEC || p.x_wide);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -359,10 +378,10 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
                                    s ? xv[i][0].w : xv[i][0].y, s ? xv[i][1].w : xv[i][1].y};
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-              if (j < p.n_tiles) mma16x8<T>(acc[i][j], f, s ? av[j].z : av[j].x, s ? av[j].w : av[j].y);
+              mma16x8<T>(acc[i][j], f, s ? av[j].z : av[j].x, s ? av[j].w : av[j].y);
           }
         } else {
-          // each factor as two tf32 numbers, three of the four products (the last is 2^-22 of the first)
+          // each factor as two tf32 numbers
           uint32_t ah[NT][2], al[NT][2];
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
@@ -378,10 +397,7 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
             split_tf32(__uint_as_float(s ? xv[i][1].w : xv[i][1].y), hi[3], lo[3]);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-              if (j >= p.n_tiles) continue;
-              mma16x8<T>(acc[i][j], lo, ah[j][0], ah[j][1]);
-              mma16x8<T>(acc[i][j], hi, al[j][0], al[j][1]);
-              mma16x8<T>(acc[i][j], hi, ah[j][0], ah[j][1]);
+              add_products(acc[i][j], hi, lo, ah[j], al[j]);
             }
           }
         }
@@ -391,8 +407,8 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const int n = (ng * p.n_tiles + j) * 8 + 2 * q;
-        if (j >= p.n_tiles || n >= low) continue;
+        const int n = (ng * NT + j) * 8 + 2 * q;
+        if (n >= low) continue;
         float* to = s_part + ((size_t)kg * M + i * 16 + g) * pitch + n;
         *reinterpret_cast<float2*>(to) = make_float2(acc[i][j][0], acc[i][j][1]);
         *reinterpret_cast<float2*>(to + 8 * pitch) = make_float2(acc[i][j][2], acc[i][j][3]);
@@ -414,6 +430,56 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
       *at = v;
     }
   }
+  // The expansion's chunks of 32 columns, as a lane holds them: y of its rows, and weights where they are few. AHEAD
+  // of them are on their way, the first from here on.
+  constexpr int YV = 8 / V;                     // 16-byte pieces of 8 columns
+  constexpr int BLK = R < KB ? 1 : R / KB;      // weights: blocks of 16 bytes a lane,
+  constexpr int PER = STEPS / BLK;              // of as many steps,
+  constexpr int BW = R * (int)sizeof(T) >= 64 ? 4 : R * (int)sizeof(T) / 16;   // of as many words
+  constexpr bool B_TOO = 4 * BLK * BW <= 32;
+  constexpr int REGS = MT * 2 * YV * 4 + (B_TOO ? 4 * BLK * BW : 0), ROOM = MT == 4 ? 96 : MT == 2 ? 32 : F32 ? 24 : 56;
+  constexpr int AHEAD = ROOM / REGS < 1 ? 1 : ROOM / REGS > 3 ? 3 : ROOM / REGS;
+  struct Chunk {
+    uint4 y[MT][2][YV];
+    uint32_t b[B_TOO ? BLK : 1][4][BW];
+  };
+  auto load_b = [&](int col0, int end, int blk, uint32_t (*bw)[BW]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // (columns behind the part's end read its last one's)
+      const T* bc = b + (long long)min(col0 + (g >> 1) * 8 + 2 * j + (g & 1), end - 1) * R;
+      if constexpr (BW == 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(bc + blk * KB) + q);
+        bw[j][0] = v.x, bw[j][1] = v.y, bw[j][2] = v.z, bw[j][3] = v.w;
+      } else if constexpr (BW == 2) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(bc) + q);
+        bw[j][0] = v.x, bw[j][1] = v.y;
+      } else {
+        bw[j][0] = __ldg(reinterpret_cast<const uint32_t*>(bc) + q);
+      }
+    }
+  };
+  auto load_chunk = [&](int h, Chunk& c) {
+    const int s = part_of(h), col0 = p.starts[s] + (h - p.chunks[s]) * 32, end = p.starts[s + 1];
+    const int mine = col0 + q * 8;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const T* from = y + s_from[i * 16 + 8 * o + g] * p.y_rs;
+#pragma unroll
+        for (int w = 0; w < YV; ++w) c.y[i][o][w] = load16<T>(from, mine + w * V, end - mine - w * V, VEC || p.y_wide);
+      }
+    if constexpr (B_TOO) {
+#pragma unroll
+      for (int blk = 0; blk < BLK; ++blk) load_b(col0, end, blk, c.b[blk]);
+    }
+  };
+  Chunk chunk[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (h0 + warp + i * kAdapterWarps < h1) load_chunk(h0 + warp + i * kAdapterWarps, chunk[i]);
+
   if (ranks > 1) {
     cluster_arrive();
     cluster_wait();
@@ -427,13 +493,19 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
   for (int i = tid; i < M * wide4; i += kAdapterThreads) {
     const int m = i / wide4, n = part0 * R + (i - m * wide4) * 4;
     const float* at = s_part + (size_t)m * pitch + n;
-    float4 v = ranks > 1 ? load_of_rank(at, 0) : *reinterpret_cast<const float4*>(at);
-    for (uint32_t r = 1; r < ranks; ++r) {
-      const float4 w = load_of_rank(at, r);
-      v.x += w.x;
-      v.y += w.y;
-      v.z += w.z;
-      v.w += w.w;
+    float4 v = *reinterpret_cast<const float4*>(at);
+    if (ranks > 1) {
+      float4 w[8];   // all on their way before the first is added
+#pragma unroll
+      for (int r = 0; r < 8; ++r) w[r] = r < ranks ? load_of_rank(at, r) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v = w[0];
+#pragma unroll
+      for (int r = 1; r < 8; ++r) {
+        v.x += w[r].x;
+        v.y += w[r].y;
+        v.z += w[r].z;
+        v.w += w[r].w;
+      }
     }
     *reinterpret_cast<float4*>(s_sum + (size_t)m * pitch + n) = v;
   }
@@ -492,54 +564,27 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
   // ---- expansion: a warp 32 columns at once. Of 8-column tile j a lane holds columns 8 q + 2 j, 2 j + 1 of its
   // rows, so that its columns of the four tiles are neighbours.
   const float c_a = p.scales ? __ldg(p.scales + adapter) : 1.f;
-  for (int h = h0 + warp; h < h1; h += kAdapterWarps) {
+  auto finish = [&](int h, const Chunk& now) {
     const int s = part_of(h), col0 = p.starts[s] + (h - p.chunks[s]) * 32, end = p.starts[s + 1];
     const int mine = col0 + q * 8, n_mine = min(end - mine, 8);   // (none there: below 1)
-    constexpr int YV = 8 / V;            // 16-byte pieces of 8 columns
-    uint4 yv[MT][2][YV];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const T* from = y + s_from[i * 16 + 8 * o + g] * p.y_rs;
-#pragma unroll
-        for (int w = 0; w < YV; ++w) yv[i][o][w] = load16<T>(from, mine + w * V, n_mine - w * V, VEC || p.y_wide);
-      }
     float acc[MT][4][4] = {};
-    const T* bc[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      bc[j] = b + (long long)min(col0 + (g >> 1) * 8 + 2 * j + (g & 1), end - 1) * R;
-    }
     const uint4* frag = s_frag + (size_t)(s - part0) * MT * STEPS * 64 + lane;
-    constexpr int BLK = R < KB ? 1 : R / KB;      // of 16 bytes a lane
-    constexpr int PER = STEPS / BLK;              // steps of a block
 #pragma unroll
     for (int blk = 0; blk < BLK; ++blk) {
-      uint32_t bw[4][4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bw[j][1] = bw[j][2] = bw[j][3] = 0u;
-        if constexpr (R * (int)sizeof(T) >= 64) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(bc[j] + blk * KB) + q);
-          bw[j][0] = v.x, bw[j][1] = v.y, bw[j][2] = v.z, bw[j][3] = v.w;
-        } else if constexpr (R * (int)sizeof(T) == 32) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(bc[j]) + q);
-          bw[j][0] = v.x, bw[j][1] = v.y;
-        } else {
-          bw[j][0] = __ldg(reinterpret_cast<const uint32_t*>(bc[j]) + q);
-        }
-      }
+      uint32_t bw[4][BW];
+      if constexpr (!B_TOO) load_b(col0, end, blk, bw);
+      else memcpy(bw, now.b[blk], sizeof bw);
 #pragma unroll
       for (int t = 0; t < PER; ++t) {
-        uint32_t bl[4][2];
-        if constexpr (F32) {
+        uint32_t bh[4][2], bl[4][2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            split_tf32(__uint_as_float(bw[j][2 * t]), bw[j][2 * t], bl[j][0]);
-            split_tf32(__uint_as_float(bw[j][2 * t + 1]), bw[j][2 * t + 1], bl[j][1]);
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t w = 2 * t + e < BW ? bw[j][2 * t + e] : 0u;
+            if constexpr (F32) split_tf32(__uint_as_float(w), bh[j][e], bl[j][e]);
+            else bh[j][e] = w;
           }
-        }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           const uint4* f = frag + (i * STEPS + blk * PER + t) * 64;
@@ -547,9 +592,12 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
           const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            mma16x8<T>(acc[i][j], lo, bw[j][2 * t], bw[j][2 * t + 1]);
-            if constexpr (F32) mma16x8<T>(acc[i][j], hi, bl[j][0], bl[j][1]);
-            mma16x8<T>(acc[i][j], hi, bw[j][2 * t], bw[j][2 * t + 1]);
+            if constexpr (F32) {
+              add_products(acc[i][j], hi, lo, bh[j], bl[j]);
+            } else {
+              mma16x8<T>(acc[i][j], lo, bh[j][0], bh[j][1]);
+              mma16x8<T>(acc[i][j], hi, bh[j][0], bh[j][1]);
+            }
           }
         }
       }
@@ -567,7 +615,7 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
           float v[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const uint4 w = yv[i][o][e / 4];
+            const uint4 w = now.y[i][o][e / 4];
             v[e] = __uint_as_float(e % 4 == 0 ? w.x : e % 4 == 1 ? w.y : e % 4 == 2 ? w.z : w.w) +
                    c * acc[i][e / 2][2 * o + (e & 1)];
           }
@@ -580,7 +628,7 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
               if (e < n_mine) to[e] = v[e];
           }
         } else {
-          const uint32_t in[4] = {yv[i][o][0].x, yv[i][o][0].y, yv[i][o][0].z, yv[i][o][0].w};
+          const uint32_t in[4] = {now.y[i][o][0].x, now.y[i][o][0].y, now.y[i][o][0].z, now.y[i][o][0].w};
           uint32_t w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -606,35 +654,67 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_kernel(const __grid_c
           }
         }
       }
+  };
+#pragma unroll 1
+  for (int h = h0 + warp; h < h1; h += AHEAD * kAdapterWarps) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int hh = h + i * kAdapterWarps;
+      if (hh >= h1) break;
+      const Chunk now = chunk[i];
+      if (hh + AHEAD * kAdapterWarps < h1) load_chunk(hh + AHEAD * kAdapterWarps, chunk[i]);
+      finish(hh, now);
+    }
   }
   if (ranks > 1) cluster_wait();
 }
 
+// The 8-column tiles of a warp, of `columns` of them in all: the fewest built that take them with 1, 2, 4 or 8 warps
+// side by side (`groups`).
+inline int adapter_tiles(int mt, int columns, int& groups) {
+  const int most = mt == 1 ? 8 : mt == 2 ? 6 : 4;
+  groups = 1;
+  while ((columns + groups - 1) / groups > most) groups *= 2;
+  const int each = (columns + groups - 1) / groups;
+  return each <= 4 ? 4 : each <= 6 ? 6 : 8;
+}
+
 // The kernel for tiles of 16 mt rows (null: not built).
-template <typename T, int R>
+template <typename T, int R, int NT>
 const void* adapter_kernel_of(int mt, bool vec) {
-  if (!vec) return mt == 1 ? reinterpret_cast<const void*>(&adapter_kernel<T, 1, R, false>) : nullptr;
-  if (mt == 1) return reinterpret_cast<const void*>(&adapter_kernel<T, 1, R, true>);
-  if constexpr (!std::is_same<T, float>::value) {
-    if (mt == 2) return reinterpret_cast<const void*>(&adapter_kernel<T, 2, R, true>);
-    if (mt == 4) return reinterpret_cast<const void*>(&adapter_kernel<T, 4, R, true>);
+  if (mt == 1)
+    return vec ? reinterpret_cast<const void*>(&adapter_kernel<T, 1, R, NT, true>)
+               : reinterpret_cast<const void*>(&adapter_kernel<T, 1, R, NT, false>);
+  if constexpr (!std::is_same<T, float>::value && NT <= 6) {
+    if (mt == 2 && vec) return reinterpret_cast<const void*>(&adapter_kernel<T, 2, R, NT, true>);
+    if constexpr (NT == 4)
+      if (mt == 4 && vec) return reinterpret_cast<const void*>(&adapter_kernel<T, 4, R, NT, true>);
+  }
+  return nullptr;
+}
+template <typename T, int R>
+const void* adapter_kernel_of(int mt, int tiles, bool vec) {
+  if (tiles == 4) return adapter_kernel_of<T, R, 4>(mt, vec);
+  if constexpr (R >= 16) {   // (rank 8: at most 4 tiles in all)
+    if (tiles == 6) return adapter_kernel_of<T, R, 6>(mt, vec);
+    if (tiles == 8) return adapter_kernel_of<T, R, 8>(mt, vec);
   }
   return nullptr;
 }
 template <typename T>
-const void* adapter_kernel_for(int rank, int mt, bool vec) {
+const void* adapter_kernel_for(int rank, int mt, int tiles, bool vec) {
   switch (rank) {
-    case 8: return adapter_kernel_of<T, 8>(mt, vec);
-    case 16: return adapter_kernel_of<T, 16>(mt, vec);
-    case 32: return adapter_kernel_of<T, 32>(mt, vec);
-    case 64: return adapter_kernel_of<T, 64>(mt, vec);
-    case 128: return adapter_kernel_of<T, 128>(mt, vec);
+    case 8: return adapter_kernel_of<T, 8>(mt, tiles, vec);
+    case 16: return adapter_kernel_of<T, 16>(mt, tiles, vec);
+    case 32: return adapter_kernel_of<T, 32>(mt, tiles, vec);
+    case 64: return adapter_kernel_of<T, 64>(mt, tiles, vec);
+    case 128: return adapter_kernel_of<T, 128>(mt, tiles, vec);
     default: return nullptr;
   }
 }
 
-const void* adapter_kernel_bf16(int rank, int mt, bool vec);
-const void* adapter_kernel_f16(int rank, int mt, bool vec);
-const void* adapter_kernel_f32(int rank, int mt, bool vec);
+const void* adapter_kernel_bf16(int rank, int mt, int tiles, bool vec);
+const void* adapter_kernel_f16(int rank, int mt, int tiles, bool vec);
+const void* adapter_kernel_f32(int rank, int mt, int tiles, bool vec);
 
 }  // namespace da

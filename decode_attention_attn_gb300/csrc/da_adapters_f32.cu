@@ -3,6 +3,8 @@
 
 namespace da {
 
-const void* adapter_kernel_f32(int rank, int mt, bool vec) { return adapter_kernel_for<float>(rank, mt, vec); }
+const void* adapter_kernel_f32(int rank, int mt, int tiles, bool vec) {
+  return adapter_kernel_for<float>(rank, mt, tiles, vec);
+}
 
 }  // namespace da

@@ -386,25 +386,24 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       const TileInfo t = sh.tiles[w.tile];
       const uint32_t vb = w.seg & 1, vpar = (w.seg >> 1) & 1;
       const float4* from = q.sums + (long long)(w.part * R / 4) * p.rows + t.row0 + row;
-      float v[R];
+      // (a share's numbers all on their way before the next is added)
+      float v[R] = {};
+      if (row < t.rows) {
+#pragma unroll 1
+        for (int k = 0; k < q.shares; ++k, from += (long long)(low / 4) * p.rows) {
+          float4 m[R / 4];
 #pragma unroll
-      for (int c = 0; c < R / 4; ++c) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row < t.rows) {
-          s = from[(long long)c * p.rows];
-          for (int k = 1; k < q.shares; ++k) {
-            const float4 m = from[((long long)k * (low / 4) + c) * p.rows];
-            s.x += m.x;
-            s.y += m.y;
-            s.z += m.z;
-            s.w += m.w;
+          for (int c = 0; c < R / 4; ++c) m[c] = from[(long long)c * p.rows];
+#pragma unroll
+          for (int c = 0; c < R / 4; ++c) {
+            v[4 * c] += m[c].x;
+            v[4 * c + 1] += m[c].y;
+            v[4 * c + 2] += m[c].z;
+            v[4 * c + 3] += m[c].w;
           }
         }
-        v[4 * c] = s.x;
-        v[4 * c + 1] = s.y;
-        v[4 * c + 2] = s.z;
-        v[4 * c + 3] = s.w;
       }
+      __syncwarp();
       if constexpr (std::is_same<T, __half>::value) {
         // f16 ends at 65504: by a power of two to below 2^8, and back in the product
         float most = 0.f;
@@ -508,10 +507,10 @@ const void* expand_for(int rank) {
 }
 
 int map_2d(CUtensorMap* map, const void* base, long long inner, long long outer, long long stride_bytes, int box_inner,
-           int box_outer, CUtensorMapSwizzle swizzle) {
+           int box_outer, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promote) {
   const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer}, strides[1] = {(cuuint64_t)stride_bytes};
   const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer};
-  return encode_map(map, 2, 2, base, dims, strides, box, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+  return encode_map(map, 2, 2, base, dims, strides, box, swizzle, promote);
 }
 
 int launch_with(const void* fn, int grid, int threads, size_t smem, bool dependent, cudaStream_t stream, void** args) {
@@ -563,15 +562,18 @@ int launch_tall(const AdapterParams& p, int rank, bool bf16, int shares, int sms
   for (int s = p.parts; s < kMaxParts; ++s) q.blocks[s] = q.blocks[kMaxParts];   // (no part begins there)
   CUtensorMap tmx, tma, tmy, tmb;
   const int rb = std::max(rank, 16);
-  int rc = map_2d(&tmx, p.x, p.width, p.rows, p.x_rs * 2, 64, kTallTile, CU_TENSOR_MAP_SWIZZLE_128B);
+  const CUtensorMapL2promotion next = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+  int rc = map_2d(&tmx, p.x, p.width, p.rows, p.x_rs * 2, 64, kTallTile, CU_TENSOR_MAP_SWIZZLE_128B, next);
   if (rc == DA_OK)
-    rc = map_2d(&tma, p.a, p.width, (long long)p.adapters * low, p.width * 2ll, 64, q.n, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (rc == DA_OK) rc = map_2d(&tmy, p.y, columns, p.rows, p.y_rs * 2, 64, kTallTile, CU_TENSOR_MAP_SWIZZLE_128B);
+    rc = map_2d(&tma, p.a, p.width, (long long)p.adapters * low, p.width * 2ll, 64, q.n, CU_TENSOR_MAP_SWIZZLE_128B,
+                next);
+  if (rc == DA_OK) rc = map_2d(&tmy, p.y, columns, p.rows, p.y_rs * 2, 64, kTallTile, CU_TENSOR_MAP_SWIZZLE_128B, next);
   if (rc == DA_OK)
     rc = map_2d(&tmb, p.b, rank, (long long)p.adapters * columns, rank * 2ll, std::min(rb, 64), 128,
                 rb >= 64   ? CU_TENSOR_MAP_SWIZZLE_128B
                 : rb == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
-                           : CU_TENSOR_MAP_SWIZZLE_32B);
+                           : CU_TENSOR_MAP_SWIZZLE_32B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
   if (rc != DA_OK) return rc;
   const void* contract = bf16 ? reinterpret_cast<const void*>(&contract_kernel<__nv_bfloat16>)
                               : reinterpret_cast<const void*>(&contract_kernel<__half>);

@@ -1434,8 +1434,7 @@ class Adapters:
             # long steps' low-rank sums, from the pool of the call's stream and its again after the call
             ws, size = None, 0
             if rows >= self.LONG and self.dtype is not _torch.float32:
-                with _torch.cuda.device(index):
-                    size = decode_attn_adapters_workspace(self.config, rows)
+                size = decode_attn_adapters_workspace(self.config, rows)
                 if size:
                     ws = _empty((size,), _torch.uint8, x.device, stream)
             self._apply(self._at, index, stream, x.data_ptr(), y.data_ptr(), out.data_ptr(), a.data_ptr(),

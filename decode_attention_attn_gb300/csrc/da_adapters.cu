@@ -90,10 +90,9 @@ int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter
 
   // Requests of many rows go to the tensor cores' two launches, where the step has enough of them to be worth it
   // and a workspace for their sums is there.
-  const int shares = tall_shares(a.rows, c.width, sms);
   const bool tall = vec && c.dtype != DA_F32 && a.rows >= kTallStep && a.workspace && tall_fits(p, c.rank, sms);
   p.tall = tall ? kTallRows : INT_MAX;
-  if (tall && a.workspace_bytes < tall_workspace(a.rows, low, shares)) return DA_ERR_WORKSPACE_TOO_SMALL;
+  if (tall && a.workspace_bytes < tall_workspace(a.rows, low)) return DA_ERR_WORKSPACE_TOO_SMALL;
 
   // Tiles of 16 rows where an adapter has few, of 64 where it has many (the weights come from L2 once a tile).
   const int groups = std::min(a.batch, a.adapters);
@@ -138,17 +137,15 @@ int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter
   void* kargs[1] = {&p};
   const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, kargs);
   if (e != cudaSuccess) return cuda_fail(e, "launching the adapter kernel");
-  return tall ? launch_tall(p, c.rank, c.dtype == DA_BF16, shares, sms, a.workspace, cfg.stream) : DA_OK;
+  return tall ? launch_tall(p, c.rank, c.dtype == DA_BF16, sms, a.workspace, cfg.stream) : DA_OK;
 }
 
 int decode_attn_adapters_workspace(const da_adapter_config* config, int rows, size_t* bytes) {
   if (!config || !bytes || rows < 0 || config->width < 1 || config->parts < 1) return DA_ERR_INVALID_ARG;
   *bytes = 0;
   if (rows < kTallStep || config->dtype == DA_F32) return DA_OK;
-  const int sms = device_sms();
-  if (sms <= 0) return DA_ERR_CUDA;
   const long long low = (long long)config->parts * config->rank;
-  if (low <= 256) *bytes = tall_workspace(rows, (int)low, tall_shares(rows, config->width, sms));
+  if (low <= 256) *bytes = tall_workspace(rows, (int)low);
   return DA_OK;
 }
 

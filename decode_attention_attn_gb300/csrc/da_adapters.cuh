@@ -47,20 +47,19 @@ struct AdapterParams {
 
 // Requests of many rows: what their kernels take beside AdapterParams, in da_adapters_tall.cu.
 constexpr int kTallRows = 32;           // rows from which a request is theirs, where they are launched
+constexpr int kTallPieces = 8;          // sums of a tile, from as many CTAs at most
 constexpr size_t kTallStatusBytes = 256;
 struct TallParams {
-  float4* sums;                 // [shares, low / 4, rows]: low-rank sums, four columns of a row
+  float4* sums;                 // [kTallPieces, low / 4, rows]: low-rank sums, four columns of a row
   int32_t* status;
-  int rank, shares, stages, most_tiles;
+  int rank, stages, most_tiles;
   int n;                        // low-rank columns, to a multiple of 16
-  uint32_t tmem_cols;
   int blocks[kMaxParts + 1];    // blocks of 128 columns ahead of each part; all of them
 };
 long long most_tall_tiles(const AdapterParams& p);
 bool tall_fits(const AdapterParams& p, int rank, int sms);
-int tall_shares(int rows, int width, int sms);
-size_t tall_workspace(int rows, int low, int shares);
-int launch_tall(const AdapterParams& p, int rank, bool bf16, int shares, int sms, void* workspace, cudaStream_t stream);
+size_t tall_workspace(int rows, int low);
+int launch_tall(const AdapterParams& p, int rank, bool bf16, int sms, void* workspace, cudaStream_t stream);
 
 // Bytes of dynamic shared memory: the partial sums of every group of warps (where the counts of rows lay before),
 // the sums over the cluster, and them as operands.

@@ -1,9 +1,9 @@
 // da_adapters_tall.cu -- adapters of requests with many rows (prompts), 16-bit types, on the 5th-generation
 // tensor cores: two launches over tiles of 128 rows of one request.
 //
-//   contract   low[r] = x[r] A_a^T: tcgen05.mma 128 x (parts * rank) x 64, x and A by TMA into a ring, a share of the
-//              width a CTA; fp32 sums of every share into the workspace.
-//   expand     out[r, c..c+127] = y + c_a low[r] B_a^T: the shares' sums as 16-bit operands in tensor memory (two
+//   contract   low[r] = x[r] A_a^T: tcgen05.mma 128 x (parts * rank) x 64, x and A by TMA into a ring, an even run of
+//              the tiles' widths a CTA; its fp32 sums into the workspace.
+//   expand     out[r, c..c+127] = y + c_a low[r] B_a^T: the CTAs' sums as 16-bit operands in tensor memory (two
 //              parts, so that nothing of fp32's order is lost), B and y by TMA. A CTA walks a run of column blocks,
 //              tile by tile: one warp loads, one issues, four put the next rows' operand together, and two teams of
 //              four finish blocks in turn (a thread a row) and write them row by row.
@@ -25,10 +25,10 @@ constexpr int kTallTile = 128;
 constexpr int kContractThreads = 256;
 constexpr int kMaxTileList = 1024;    // tiles of a CTA's run
 
-// Tiles of request b: as many as its rows fill, if they are many and it has an adapter.
-__device__ __forceinline__ int tall_tiles(const AdapterParams& p, int b, int& first, int& n) {
-  n = rows_of(p, b, first);
-  return n >= p.tall && adapter_of(p, b) < p.adapters ? (n + kTallTile - 1) / kTallTile : 0;
+// Rows of request b, if they are many and it has an adapter; else 0.
+__device__ __forceinline__ int tall_rows(const AdapterParams& p, int b, int& first) {
+  const int n = rows_of(p, b, first);
+  return n >= p.tall && adapter_of(p, b) < p.adapters ? n : 0;
 }
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
@@ -39,16 +39,101 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// ---- contract ----------------------------------------------------------------------------------
-struct ContractShared {
-  uint64_t full[8], empty[8], done;
-  uint32_t tmem;
-  int abort_flag;
+struct TileInfo {
   int row0, rows, adapter;
-  AdapterShared scan;
 };
 
-// grid: tile bound * shares. Dynamic shared memory: stages of [128 rows | n columns] x 64, 1 KB aligned.
+// A CTA's run of `per_tile` items a tile, [i0, i1) of n_tiles * per_tile, and its tiles (from t0 on) in list; `ctas`
+// share the items evenly, at most `spread` a tile (0: all of them). False: it has none. By every thread of a block
+// whose first 256 look through the requests.
+struct Run {
+  long long i0, i1, items;
+  int t0, n_tiles, ctas;
+};
+// (no more CTAs than items, so that each one between a tile's first and last has some of it)
+__device__ __forceinline__ int ctas_of(long long items, int n_tiles, int spread) {
+  return (int)min((long long)gridDim.x, min((long long)spread * n_tiles, items));
+}
+// a / b, short where both are
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+template <int THREADS>
+__device__ bool find_run(const AdapterParams& p, const TallParams& q, int per_tile, int spread, AdapterShared& scan,
+                         TileInfo* list, Run& r) {
+  const int tid = threadIdx.x;
+  int first0 = 0, n0 = 0, a0 = 0, before0 = 0;   // of the request that is the thread's first
+  r.n_tiles = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kAdapterThreads) {
+    const int b = b0 + tid;
+    int first = 0, n = 0;
+    if (tid < kAdapterThreads && b < p.batch) {
+      n = tall_rows(p, b, first);
+      if (b0 == 0) a0 = adapter_of(p, b);
+    }
+    const int before = wide_prefix((n + kTallTile - 1) / kTallTile, scan);
+    r.n_tiles += scan.chunk_total;
+    __syncthreads();
+    if (b0 == 0) first0 = first, n0 = n, before0 = before;
+  }
+  // (more than offsets in order allow: nothing is done)
+  if (r.n_tiles < 0 || r.n_tiles > q.most_tiles) r.n_tiles = 0;
+  r.items = (long long)r.n_tiles * per_tile;
+  r.ctas = spread ? ctas_of(r.items, r.n_tiles, spread) : (int)gridDim.x;
+  if ((int)blockIdx.x >= r.ctas) return false;
+  r.i0 = divide(r.items * blockIdx.x, r.ctas);
+  r.i1 = divide(r.items * (blockIdx.x + 1), r.ctas);
+  if (r.i0 == r.i1) return false;
+  r.t0 = (int)divide(r.i0, per_tile);
+  const int t1 = (int)divide(r.i1 - 1, per_tile);   // t1 - t0 < kMaxTileList: tall_fits
+  for (int t = tid; t <= t1 - r.t0; t += THREADS) list[t] = TileInfo{0, 0, 0};
+  __syncthreads();
+  for (int b0 = 0, base = 0; b0 < p.batch && base <= t1; b0 += kAdapterThreads) {
+    const int b = b0 + tid;
+    int first = first0, n = n0, adapter = a0, before = before0;
+    if (p.batch > kAdapterThreads) {
+      n = 0;
+      if (tid < kAdapterThreads && b < p.batch) {
+        n = tall_rows(p, b, first);
+        adapter = adapter_of(p, b);
+      }
+      before = base + wide_prefix((n + kTallTile - 1) / kTallTile, scan);
+      base += scan.chunk_total;
+      __syncthreads();
+    }
+    const int end = before + (n + kTallTile - 1) / kTallTile;
+    for (int t = max(before, r.t0); t <= t1 && t < end; ++t) {
+      const int at = (t - before) * kTallTile;
+      list[t - r.t0] = TileInfo{first + at, min(n - at, kTallTile), adapter};
+    }
+  }
+  return true;
+}
+
+// The CTA whose run holds item u.
+__device__ __forceinline__ int owner(const Run& r, long long u) {
+  return (int)divide((u + 1) * r.ctas + r.items - 1, r.items) - 1;
+}
+
+// ---- contract ----------------------------------------------------------------------------------
+// Runs of 64-wide blocks of the tiles' widths, evenly over the CTAs wherever a tile ends, so that a tile's sums come
+// from up to kTallPieces of them. What bounds it is the way from L2: 40 KB a block of rank 64's three parts, of which 24
+// are weights, at 87 GB/s an SM (13 TB/s in all); 8800 rows 24 us. (Whole tiles split in shares, two CTAs an SM: 25 us;
+// 256 rows beside one tile of weights, 56 KB a block, three in flight: 27 us.)
+constexpr int kContractSpread = 6;    // CTAs a tile at most: a tile then meets at most 6 + 2 runs
+constexpr uint32_t kContractCols = 512;
+static_assert(kContractSpread + 2 <= kTallPieces, "");
+
+struct ContractShared {
+  uint64_t full[8], empty[8], acc_full[2], acc_empty[2], done;
+  uint32_t tmem;
+  int abort_flag;
+  AdapterShared scan;
+  TileInfo tiles[kMaxTileList];
+};
+
+// Dynamic shared memory: stages of [128 rows | n columns] x 64, 1 KB aligned; more than half of an SM's, so that a
+// CTA has its tensor memory to itself.
 template <typename T>
 __global__ void __launch_bounds__(kContractThreads, 1)
     contract_kernel(const __grid_constant__ AdapterParams p, const __grid_constant__ TallParams q,
@@ -58,38 +143,26 @@ __global__ void __launch_bounds__(kContractThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   pdl_launch_dependents();
-  const int tile = blockIdx.x / q.shares, share = blockIdx.x % q.shares;
   if (tid == 0) {
-    sh.adapter = -1;
     sh.abort_flag = 0;
     for (int i = 0; i < q.stages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.acc_full[i], 1);
+      mbar_init(&sh.acc_empty[i], 4);
+    }
     mbar_init(&sh.done, 1);
     fence_mbar_init();
   }
-  __syncthreads();
-  for (int b0 = 0, base = 0; b0 < p.batch; b0 += kContractThreads) {
-    const int b = b0 + tid;
-    int first = 0, n = 0;
-    const int tiles = b < p.batch ? tall_tiles(p, b, first, n) : 0;
-    const int before = base + block_prefix(tiles, sh.scan);
-    if (before <= tile && tile < before + tiles) {
-      sh.row0 = first + (tile - before) * kTallTile;
-      sh.rows = min(n - (tile - before) * kTallTile, kTallTile);
-      sh.adapter = adapter_of(p, b);
-    }
-    base += sh.scan.chunk_total;
-    __syncthreads();
-    if (base > tile) break;
-  }
-  const int adapter = sh.adapter;
-  if (adapter < 0) {   // fewer tiles: nothing here may end before the launch ahead has
-    pdl_wait();
+  const int blocks = (p.width + 63) / 64;
+  Run run;
+  if (!find_run<kContractThreads>(p, q, blocks, kContractSpread, sh.scan, sh.tiles, run)) {
+    pdl_wait();   // (its end stands for that of the launch ahead too)
     return;
   }
-  if (warp == 5) tmem_alloc(&sh.tmem, q.tmem_cols);
+  if (warp == 5) tmem_alloc(&sh.tmem, kContractCols);
   if (tid == 0 && (smem_u32(smem) & 1023u)) {   // the swizzled tiles need it: nothing may run elsewhere
     sh.abort_flag = 1;
     atomicOr(q.status, kStatusTimeout);
@@ -99,79 +172,99 @@ __global__ void __launch_bounds__(kContractThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const int low = p.parts * q.rank;
-  const int blocks = (p.width + 63) / 64;
-  const int k0 = (int)((long long)blocks * share / q.shares), k1 = (int)((long long)blocks * (share + 1) / q.shares);
-  const uint32_t stage_bytes = 16384u + (uint32_t)q.n * 128u;
+  const uint32_t x_bytes = kTallTile * 128u, stage_bytes = x_bytes + (uint32_t)q.n * 128u;
   Waiter wait{&sh.abort_flag, q.status, kWaitLimitNs, sh.abort_flag != 0};
+  const int units = (int)(run.i1 - run.i0);
+  int k = (int)(run.i0 % blocks), tile = 0;          // of the unit at hand
   if (warp == 4) {
     const bool issuer = elect_one();
     int slot = 0, issued = 0;
     uint32_t par = 1;
-    for (int k = k0; k < k1; ++k) {
+    for (int u = 0; u < units; ++u) {
       wait(&sh.empty[slot], par);
       if (!wait.dead) {
         if (issuer) {
+          const TileInfo t = sh.tiles[tile];
           uint8_t* at = smem + slot * stage_bytes;
           mbar_arrive_expect_tx(&sh.full[slot], stage_bytes);
-          tma_load_2d(at, &tmx, &sh.full[slot], k * 64, sh.row0);
-          tma_load_2d(at + 16384, &tma, &sh.full[slot], k * 64, adapter * low);
+          tma_load_2d(at, &tmx, &sh.full[slot], k * 64, t.row0);
+          tma_load_2d(at + x_bytes, &tma, &sh.full[slot], k * 64, t.adapter * low);
         }
         ++issued;
       }
       __syncwarp();
       if (++slot == q.stages) slot = 0, par ^= 1;
+      if (++k == blocks) k = 0, ++tile;
     }
     // never leave with copies in flight
-    for (int k = max(issued - q.stages, 0); k < issued; ++k)
-      mbar_wait(&sh.full[k % q.stages], (k / q.stages) & 1, kWaitLimitNs);
+    for (int i = max(issued - q.stages, 0); i < issued; ++i)
+      mbar_wait(&sh.full[i % q.stages], (i / q.stages) & 1, kWaitLimitNs);
   } else if (warp == 5) {
     const bool issuer = elect_one();
     const uint32_t desc = mma_desc(std::is_same<T, __nv_bfloat16>::value, q.n, false);
-    const uint64_t xd = tile_desc(smem_u32(smem), 16, 1024), ad = tile_desc(smem_u32(smem + 16384), 16, 1024);
+    const uint64_t xd = tile_desc(smem_u32(smem), 16, 1024), ad = tile_desc(smem_u32(smem + x_bytes), 16, 1024);
     int slot = 0;
     uint32_t par = 0;
-    for (int k = k0; k < k1; ++k) {
+    bool fresh = true;
+    for (int u = 0; u < units; ++u) {
+      const uint32_t buf = tile & 1, bpar = (tile >> 1) & 1;
+      if (fresh) wait(&sh.acc_empty[buf], bpar ^ 1);
       wait(&sh.full[slot], par);
       tc_fence_after();
+      const bool last = k + 1 == blocks || u + 1 == units;
       if (!wait.dead && issuer) {
         const uint32_t off = slot * (stage_bytes >> 4);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) mma_ss(tmem, xd + off + 2 * s, ad + off + 2 * s, desc, k != k0 || s != 0);
+        for (int s = 0; s < 4; ++s)
+          mma_ss(tmem + buf * 256u, xd + off + 2 * s, ad + off + 2 * s, desc, !fresh || s != 0);
         tc_commit(&sh.empty[slot]);
+        if (last) tc_commit(&sh.acc_full[buf]);
       }
       __syncwarp();
+      fresh = last;
       if (++slot == q.stages) slot = 0, par ^= 1;
+      if (++k == blocks) k = 0, ++tile;
     }
     if (issuer) tc_commit(&sh.done);
     mbar_wait(&sh.done, 0, kWaitLimitNs);
   } else if (warp < 4) {
-    wait(&sh.done, 0);
-    tc_fence_after();
     const int row = warp * 32 + lane;
-    float4* to = q.sums + (long long)share * (low / 4) * p.rows + sh.row0 + row;
+    const int n_tiles = (k + units + blocks - 1) / blocks;
+    for (; tile < n_tiles; ++tile) {
+      const TileInfo t = sh.tiles[tile];
+      const uint32_t buf = tile & 1, bpar = (tile >> 1) & 1;
+      // whose run the tile's first block is in says which piece this is
+      const int piece = (int)blockIdx.x - owner(run, (long long)(run.t0 + tile) * blocks);
+      wait(&sh.acc_full[buf], bpar);
+      tc_fence_after();
+      float4* to = q.sums + (long long)piece * (low / 4) * p.rows + t.row0 + row;
+      const bool there = row < t.rows && !wait.dead && piece >= 0 && piece < kTallPieces;
 #pragma unroll 1
-    for (int c = 0; c < low; c += 32) {
-      uint32_t v[32];
-      __syncwarp();
-      tmem_ld32(tmem + ((uint32_t)warp << 21) + c, v);
-      tmem_ready(v);
-      if (row < sh.rows && !wait.dead) {
+      for (int c = 0; c < low; c += 32) {
+        uint32_t v[32];
+        __syncwarp();
+        tmem_ld32(tmem + ((uint32_t)warp << 21) + buf * 256u + c, v);
+        tmem_ready(v);
+        if (there) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + 4 * k < low)
-            to[(long long)(c / 4 + k) * p.rows] =
-                make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]),
-                            __uint_as_float(v[4 * k + 3]));
+          for (int e = 0; e < 8; ++e)
+            if (c + 4 * e < low)
+              to[(long long)(c / 4 + e) * p.rows] =
+                  make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
+                              __uint_as_float(v[4 * e + 3]));
+        }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
     }
-    __syncwarp();
-    tc_fence_before();
   }
   __syncwarp();
+  tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_free(tmem, q.tmem_cols);
-  pdl_wait();   // (its end stands for that of the launch ahead too)
+  if (warp == 5) tmem_free(tmem, kContractCols);
+  pdl_wait();
 }
 
 // ---- expand --------------------------------------------------------------------------------------
@@ -179,9 +272,6 @@ constexpr int kExpandTeams = 2;                       // of 4 warps, that finish
 constexpr int kExpandThreads = (kExpandTeams * 4 + 4 + 2) * 32;
 constexpr uint32_t kExpandCols = 512, kColD = 0, kColV = 256;
 
-struct TileInfo {
-  int row0, rows, adapter;
-};
 struct ExpandShared {
   uint64_t y_full[4], y_empty[4], b_full[4], b_empty[4], d_full[2], d_empty[2], v_full[2], v_empty[2], drained;
   uint32_t tmem;
@@ -258,36 +348,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
   }
-  // how many tiles there are, and those of this CTA's run (inputs of the launches ahead, not theirs to write)
-  int n_tiles = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += kAdapterThreads) {   // (256 threads' prefix: the others bring nothing)
-    const int b = b0 + tid;
-    int first, n;
-    const int tiles = tid < kAdapterThreads && b < p.batch ? tall_tiles(p, b, first, n) : 0;
-    wide_prefix(tiles, sh.scan);
-    n_tiles += sh.scan.chunk_total;
-    __syncthreads();
-  }
-  // (more than offsets in order allow: nothing is done)
-  const long long items = n_tiles < 0 || n_tiles > q.most_tiles ? 0 : (long long)n_tiles * q.blocks[kMaxParts];
-  const long long i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
-  if (i0 == i1) {
+  // (the requests are no result of the launch ahead)
+  Run run;
+  if (!find_run<kExpandThreads>(p, q, q.blocks[kMaxParts], 0, sh.scan, sh.tiles, run)) {
     pdl_wait();
     return;
-  }
-  for (int t = tid; t < kMaxTileList; t += kExpandThreads) sh.tiles[t] = TileInfo{0, 0, 0};
-  __syncthreads();
-  const int t0 = (int)(i0 / q.blocks[kMaxParts]), t1 = (int)((i1 - 1) / q.blocks[kMaxParts]);
-  for (int b0 = 0, base = 0; b0 < p.batch && base <= t1; b0 += kAdapterThreads) {
-    const int b = b0 + tid;
-    int first = 0, n = 0;
-    const int tiles = tid < kAdapterThreads && b < p.batch ? tall_tiles(p, b, first, n) : 0;
-    const int before = base + wide_prefix(tiles, sh.scan);
-    for (int t = max(before, t0); t <= t1 && t < before + tiles; ++t)   // (t1 - t0 < kMaxTileList: tall_fits)
-      sh.tiles[t - t0] = TileInfo{first + (t - before) * kTallTile, min(n - (t - before) * kTallTile, kTallTile),
-                                  adapter_of(p, b)};
-    base += sh.scan.chunk_total;
-    __syncthreads();
   }
   if (tid == 0 && (smem_u32(smem) & 1023u)) {
     sh.abort_flag = 1;
@@ -295,7 +360,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   }
   __syncthreads();
   Waiter wait{&sh.abort_flag, q.status, kWaitLimitNs, sh.abort_flag != 0};
-  BlockWalk w(q, i0, i1);
+  BlockWalk w(q, run.i0, run.i1);
   const int low = p.parts * R;
 
   if (warp == 12) {
@@ -379,18 +444,24 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     if (issuer) tc_commit(&sh.drained);
     mbar_wait(&sh.drained, 0, kWaitLimitNs);
   } else if (warp >= 8) {
-    // ---- the rows' operand: the shares' sums, in two 16-bit parts, large ones first ---------------------
+    // ---- the rows' operand: the contraction's sums, in two 16-bit parts, large ones first ---------------------
     const int row = (warp - 8) * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(warp - 8) << 21) + kColV;
+    const int per_tile = (p.width + 63) / 64;      // the contraction's run, as its CTAs had it
+    Run sums;
+    sums.items = (long long)run.n_tiles * per_tile;
+    sums.ctas = ctas_of(sums.items, run.n_tiles, kContractSpread);
     while (w.more()) {
       const TileInfo t = sh.tiles[w.tile];
       const uint32_t vb = w.seg & 1, vpar = (w.seg >> 1) & 1;
+      // the tile's pieces, in order (one's numbers all on their way before the next is added)
+      const long long u0 = (long long)(run.t0 + w.tile) * per_tile;
+      const int pieces = min(owner(sums, u0 + per_tile - 1) - owner(sums, u0) + 1, kTallPieces);
       const float4* from = q.sums + (long long)(w.part * R / 4) * p.rows + t.row0 + row;
-      // (a share's numbers all on their way before the next is added)
       float v[R] = {};
       if (row < t.rows) {
 #pragma unroll 1
-        for (int k = 0; k < q.shares; ++k, from += (long long)(low / 4) * p.rows) {
+        for (int k = 0; k < pieces; ++k, from += (long long)(low / 4) * p.rows) {
           float4 m[R / 4];
 #pragma unroll
           for (int c = 0; c < R / 4; ++c) m[c] = from[(long long)c * p.rows];
@@ -535,28 +606,19 @@ long long most_tall_tiles(const AdapterParams& p) {
   return p.rows / kTallTile + std::min(p.batch, p.rows / kTallRows);
 }
 
-size_t tall_workspace(int rows, int low, int shares) {
-  return kTallStatusBytes + (size_t)shares * low * rows * sizeof(float);
+size_t tall_workspace(int rows, int low) {
+  return kTallStatusBytes + (size_t)kTallPieces * low * rows * sizeof(float);
 }
 
-int tall_shares(int rows, int width, int sms) {
-  // CTAs for two an SM, a share at least 4 blocks of the width
-  const int tiles = std::max(1, rows / kTallTile);
-  return std::max(1, std::min({2 * sms / tiles, 8, (width + 255) / 256}));
-}
-
-int launch_tall(const AdapterParams& p, int rank, bool bf16, int shares, int sms, void* workspace, cudaStream_t stream) {
+int launch_tall(const AdapterParams& p, int rank, bool bf16, int sms, void* workspace, cudaStream_t stream) {
   const int low = p.parts * rank, columns = p.starts[p.parts];
   TallParams q = {};
   q.rank = rank;
-  q.shares = shares;
   q.status = static_cast<int32_t*>(workspace);
   q.sums = reinterpret_cast<float4*>(static_cast<char*>(workspace) + kTallStatusBytes);
   q.n = (low + 15) / 16 * 16;
-  const int stage = 16384 + q.n * 128;
-  q.stages = std::max(2, std::min(8, 106 * 1024 / stage));
-  q.tmem_cols = 32;
-  while ((int)q.tmem_cols < q.n) q.tmem_cols *= 2;
+  const int stage = kTallTile * 128 + q.n * 128;
+  q.stages = std::min(8, 200 * 1024 / stage);   // 147 KB and more
   for (int s = 0; s < kMaxParts; ++s)
     q.blocks[s + 1] = q.blocks[s] + (s < p.parts ? (p.starts[s + 1] - p.starts[s] + 127) / 128 : 0);
   for (int s = p.parts; s < kMaxParts; ++s) q.blocks[s] = q.blocks[kMaxParts];   // (no part begins there)
@@ -580,14 +642,13 @@ int launch_tall(const AdapterParams& p, int rank, bool bf16, int shares, int sms
   const void* expand = bf16 ? expand_for<__nv_bfloat16>(rank) : expand_for<__half>(rank);
   const size_t contract_smem = (size_t)q.stages * stage;
   const size_t expand_smem = 4 * 32768 + (rank == 128 ? 2 : 4) * (size_t)128 * rb * 2;
-  rc = raise_smem(contract, 112 * 1024, 0);
+  rc = raise_smem(contract, 200 * 1024, 0);
   if (rc == DA_OK) rc = raise_smem(expand, expand_smem, 0);
   if (rc != DA_OK) return rc;
-  const long long tiles = most_tall_tiles(p);
-  q.most_tiles = (int)tiles;
+  q.most_tiles = (int)most_tall_tiles(p);
   AdapterParams pp = p;
   void* cargs[4] = {&pp, &q, &tmx, &tma};
-  rc = launch_with(contract, (int)(tiles * shares), kContractThreads, contract_smem, true, stream, cargs);
+  rc = launch_with(contract, sms, kContractThreads, contract_smem, true, stream, cargs);
   if (rc != DA_OK) return rc;
   void* eargs[4] = {&pp, &q, &tmy, &tmb};
   return launch_with(expand, sms, kExpandThreads, expand_smem, true, stream, eargs);
@@ -595,12 +656,10 @@ int launch_tall(const AdapterParams& p, int rank, bool bf16, int shares, int sms
 
 bool tall_fits(const AdapterParams& p, int rank, int sms) {
   const int low = p.parts * rank, columns = p.starts[p.parts];
-  long long blocks = 0;
-  for (int s = 0; s < p.parts; ++s) blocks += (p.starts[s + 1] - p.starts[s] + 127) / 128;
   const long long tiles = most_tall_tiles(p);
   return low <= 256 && p.x_rs >= p.width && p.y_rs >= columns && p.x_rs < (1ll << 38) && p.y_rs < (1ll << 38) &&
          (long long)p.adapters * columns < INT_MAX - 256 && (long long)p.adapters * low < INT_MAX - 256 &&
-         tiles * 8 < INT_MAX && tiles / sms + 2 < kMaxTileList && tiles * blocks < (1ll << 40);
+         tiles < (1 << 24) && tiles / sms + 2 < kMaxTileList;
 }
 
 }  // namespace da

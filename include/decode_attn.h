@@ -819,7 +819,7 @@ typedef struct {
   void* cuda_stream;
 } da_adapter_args;
 
-/* The workspace with which a call over `rows` rows is fastest (0: it uses none). Errors: INVALID_ARG, CUDA. */
+/* The workspace with which a call over `rows` rows is fastest (0: it uses none). Host only. Errors: INVALID_ARG. */
 int decode_attn_adapters_workspace(const da_adapter_config* config, int rows, size_t* bytes);
 
 /* Synchronise `stream`, then read and clear the finding that calls with this workspace left in its first word:

@@ -1358,17 +1358,21 @@ class RMSNorm:
         return out, residual_out, codes, scales
 
 
-class Adapters:
+class Adapters(_Workspace):
     """Low-rank adapters of many requests beside a shared projection of rows of `width` to columns in parts
     of out_sizes (q, k and v, for instance): out = y + scales[a] (x A_a^T) B_a^T, part by part.
 
     a: [adapters, parts * rank, width] (or [adapters, parts, rank, width]), b: [adapters, columns, rank],
     contiguous, of `dtype` ("f32", "f16", "bf16") as x and y are. Autograd does not record the call; tensors
-    that require a gradient are refused outside no_grad()."""
+    that require a gradient are refused outside no_grad().
+
+    Long steps take a workspace for their low-rank sums, from the allocator for each call. With findings=True
+    the object keeps one, whose findings check_status() reports; two such calls must not overlap on the GPU, and a
+    captured graph needs the object (and the longest step made ahead of it) as long as it is replayed."""
 
     LONG = 1024   # rows from which a step may use a workspace
 
-    def __init__(self, width: int, out_sizes, rank: int, dtype: str = "bf16"):
+    def __init__(self, width: int, out_sizes, rank: int, dtype: str = "bf16", findings: bool = False):
         self._apply = _entry("decode_attn_adapters_apply", da_adapter_args)
         out_sizes = [int(n) for n in out_sizes]
         if not 1 <= len(out_sizes) <= ADAPTER_PARTS or min(out_sizes) < 1 or width < 1:
@@ -1384,6 +1388,7 @@ class Adapters:
                                         (ctypes.c_int * ADAPTER_PARTS)(*out_sizes), rank)
         self._at = ctypes.addressof(self.config)
         self._one = (len(out_sizes) * rank * width, self.columns * rank)
+        self._findings, self.workspace_bytes = findings, 0
 
     def _rows(self, name, t, n):
         if t.dtype is not self.dtype or len(t.shape) != 2 or t.shape[1] != n:
@@ -1432,12 +1437,31 @@ class Adapters:
                             adapter_ids=adapter_ids)
         if rows:
             # long steps' low-rank sums, from the pool of the call's stream and its again after the call
-            ws, size = None, 0
+            ws = at = size = 0
             if rows >= self.LONG and self.dtype is not _torch.float32:
                 size = decode_attn_adapters_workspace(self.config, rows)
-                if size:
+                if size and self._findings:
+                    if size > self.workspace_bytes:
+                        if self.workspace is not None:
+                            self.check_status(stream)      # (its findings are not lost with it)
+                        self._make_workspace(size, x.device)
+                        self.workspace_bytes = size
+                    if self.workspace.get_device() != index:
+                        _refuse_devices(index, workspace=self.workspace)
+                    at, size = self._workspace_on(index, stream), self.workspace_bytes
+                elif size:
                     ws = _empty((size,), _torch.uint8, x.device, stream)
+                    at = ws.data_ptr()
             self._apply(self._at, index, stream, x.data_ptr(), y.data_ptr(), out.data_ptr(), a.data_ptr(),
                         b.data_ptr(), scale_at, row_offsets.data_ptr(), adapter_ids.data_ptr(), rows, batch, n,
-                        x_row, y_row, out_row, 0 if ws is None else ws.data_ptr(), size)
+                        x_row, y_row, out_row, at, size)
         return out
+
+    def check_status(self, stream=None):
+        """Synchronise, then raise the finding recorded since the last call, if there is one."""
+        if not self._findings:
+            raise ValueError("made without findings")
+        if self.workspace is not None:
+            with _torch.cuda.device(self.workspace.device):
+                s = stream if stream is not None else _torch.cuda.current_stream()
+                decode_attn_adapters_check_status(self._workspace_on(self.workspace.get_device(), s), s.cuda_stream)

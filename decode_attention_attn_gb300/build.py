@@ -17,7 +17,8 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libdecode_attn.so")
 SOURCES = ["da_api.cu", "da_kernels_f32.cu", "da_kernels_f16.cu", "da_kernels_bf16.cu",
            "da_kernels_fp8.cu", "da_cache.cu", "da_tree.cu",
-           "da_tree_mma.cu", "da_pages.cu", "da_norm.cu", "da_adapters.cu",
+           "da_tree_mma.cu", "da_pages.cu", "da_norm.cu",
+           "da_norm_f32.cu", "da_norm_f16.cu", "da_norm_bf16.cu", "da_adapters.cu",
            "da_adapters_tall.cu", "da_adapters_bf16.cu", "da_adapters_f16.cu", "da_adapters_f32.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

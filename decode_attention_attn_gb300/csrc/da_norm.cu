@@ -1,523 +1,17 @@
-// da_norm.cu -- root-mean-square norm of rows, with the residual's addition ahead of it and an output in 8 bits
-// behind it:
-//     h = x + residual (rounded to the type: what the next block adds to),
-//     y = h (w + o) / sqrt(mean(h^2) + eps),   code = E4M3(y / scale),
-// scale given, or max |y| / 448 over the row or over groups of 32, 64 or 128 elements.
-//
-// Bound by HBM: every element is read once and written once, about 10 operations between. A row stays in registers
-// from the loads to the stores; what the row's threads exchange is one sum and one maximum, together. The maximum
-// needs no second pass over y: rounding is monotone, so max |y| = round(max |h (w + o)| r) with y = round(h (w + o) r).
+// da_norm.cu -- root-mean-square norms: checks and launch.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <map>
 #include <mutex>
 #include <tuple>
-#include <type_traits>
 
+#include "da_norm.cuh"
 #include "da_plan.h"
-#include "da_rowvec.cuh"
 
 using namespace da;
 
 namespace {
-
-constexpr float kE4M3Max = 448.f;
-constexpr float kFarScale = 5.421010862e-20f;    // 2^-64
-constexpr float kLeastScale = 1.17549435e-38f;   // 2^-126: of a row of zeros; no scale is subnormal
-
-struct NormParams {
-  const void *x, *residual, *weight;
-  void *total, *out;
-  uint8_t* codes;
-  float* scales;
-  // strides in elements, of rows and heads
-  long long x_rs, x_hs, res_rs, res_hs, tot_rs, tot_hs, out_rs, out_hs, code_rs, code_hs;
-  long long items;              // rows * heads
-  int heads, n, units;          // units: of E elements, or (not VEC) of 32 E elements a warp
-  int lanes;                    // lanes a row takes (a power of two; a warp's or more: BLOCK)
-  int weight_f32, scaling, group, groups;
-  float eps, offset;
-};
-
-template <typename T>
-struct Unit {   // elements a lane holds of a row, side by side: 32 bytes
-  static constexpr int E = 32 / (int)sizeof(T);
-};
-
-template <typename T>
-__device__ __forceinline__ float widen(T x) {
-  if constexpr (std::is_same<T, float>::value) return x;
-  else if constexpr (std::is_same<T, __half>::value) return __half2float(x);
-  else return __bfloat162float(x);
-}
-template <typename T>
-__device__ __forceinline__ T narrow(float x) {
-  if constexpr (std::is_same<T, float>::value) return x;
-  else if constexpr (std::is_same<T, __half>::value) return __float2half_rn(x);
-  else return __float2bfloat16_rn(x);
-}
-
-// Pairs of floats, two of them to an instruction: what bounds the kernel beside HBM is the instructions it issues
-// (8192 rows of 8192 bf16 with groups: 17 an element 122 us, 8 an element 85).
-__device__ __forceinline__ float2 both(f32x2 x) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
-  return f;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-// max(m, |x|, |y|); a NaN passes over
-__device__ __forceinline__ float most_of(float m, f32x2 x) {
-  const float2 f = both(x);
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(f.x)), "f"(fabsf(f.y)));
-  return r;
-}
-
-// 8 words of T as floats, and back (rounded to nearest even).
-template <typename T>
-__device__ __forceinline__ void unpack(const uint32_t* w, f32x2* f) {
-  if constexpr (std::is_same<T, float>::value) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (std::is_same<T, __half>::value) {
-        __half2 h;
-        memcpy(&h, &w[i], 4);
-        const float2 g = __half22float2(h);
-        f[i] = f2_pack(g.x, g.y);
-      } else {
-        f[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-      }
-    }
-  }
-}
-template <typename T>
-__device__ __forceinline__ void pack(const f32x2* f, uint32_t* w) {
-  if constexpr (std::is_same<T, float>::value) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 g = both(f[i]);
-      w[2 * i] = __float_as_uint(g.x);
-      w[2 * i + 1] = __float_as_uint(g.y);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 g = both(f[i]);
-      w[i] = pack2(g.x, g.y, T());
-    }
-  }
-}
-// 8 words of x + residual, rounded once. (fp32 has 24 bits, at least 2 p + 2 of a type of p: the sum rounded to fp32
-// and then to the type is the same.)
-template <typename T>
-__device__ __forceinline__ void add_words(uint32_t* x, const uint32_t* r) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if constexpr (std::is_same<T, float>::value)
-      x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(r[i]));
-    else if constexpr (std::is_same<T, __half>::value)
-      asm("add.rn.f16x2 %0, %1, %2;" : "=r"(x[i]) : "r"(x[i]), "r"(r[i]));
-    else
-      asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(x[i]) : "r"(x[i]), "r"(r[i]));
-  }
-}
-__device__ __forceinline__ void load8(const void* p, uint32_t* w) {
-  uint4 a, b;
-  load32(p, a, b);
-  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-}
-__device__ __forceinline__ void store8(void* p, const uint32_t* w) {
-  store32(p, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
-}
-
-// y / s rounded to nearest, for a scale that the row shares: the product with the reciprocal, corrected once by
-// its remainder (Markstein 1990: correctly rounded where the reciprocal is, short of under- and overflow), and the
-// plain division for scales near the ends of the range. `given`: a scale that was not found from y, whose
-// quotients may be infinite or far past E4M3's largest: those stay as they are.
-struct Divider {
-  float s;
-  f32x2 inverse, minus;
-  bool middling, given;
-  __device__ __forceinline__ Divider(float scale, bool from_caller) {
-    s = scale;
-    given = from_caller;
-    const float r = __fdiv_rn(1.f, scale);
-    inverse = f2_pack(r, r);
-    minus = f2_pack(-scale, -scale);
-    middling = scale > 8.2718061e-25f && scale < 1.2089258e24f;   // 2^+-80
-  }
-  __device__ __forceinline__ float2 operator()(f32x2 y) const {
-    if (!middling) {
-      const float2 f = both(y);
-      return make_float2(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
-    }
-    const f32x2 q = f2_mul(y, inverse);
-    float2 better = both(fma2(fma2(q, minus, y), inverse, q));
-    if (given) {
-      const float2 f = both(q);
-      if (!(fabsf(f.x) < 1048576.f)) better.x = f.x;
-      if (!(fabsf(f.y) < 1048576.f)) better.y = f.y;
-    }
-    return better;
-  }
-};
-
-// The sum of v over a row's threads, by its block or `lanes` lanes.
-template <bool BLOCK>
-__device__ __forceinline__ float row_sum(float v, int lanes, float* s_part) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    if (!BLOCK && o >= lanes) continue;
-    v += __shfl_xor_sync(0xffffffffu, v, o);
-  }
-  if constexpr (BLOCK) {
-    const int warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-    for (int w = 0; w < warps; ++w) v += s_part[w];
-    __syncthreads();
-  }
-  return v;
-}
-
-// A row's threads: a block (BLOCK), or `lanes` lanes of a warp, several rows a warp. A thread holds ITEMS units of E
-// elements. VEC: a unit is 32 bytes of the row, loaded at once, and the row's units go round the threads. Otherwise
-// (an odd width, rows that lie anywhere) a warp holds 32 E elements, a lane every 32nd of them, so that each
-// load of a warp is of neighbours. In both a group's elements are in one warp: in VEC, neighbouring lanes' units;
-// else, group / 32 of each lane's elements.
-template <typename T, int ITEMS, bool VEC, bool BLOCK, bool RES>
-__global__ void __launch_bounds__(BLOCK ? 512 : 128, BLOCK ? 1 : RES ? 6 : 8)
-    norm_kernel(const __grid_constant__ NormParams p) {
-  constexpr int E = Unit<T>::E;
-  __shared__ float2 s_part[2][16];
-  __shared__ float s_far[16];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int lanes = BLOCK ? (int)blockDim.x : p.lanes;
-  const int me = BLOCK ? tid : tid & (lanes - 1);
-  const int per_block = BLOCK ? 1 : (int)blockDim.x / lanes;
-  // the element e of item i
-  auto place = [&](int i, int e) {
-    return VEC ? (i * lanes + me) * E + e : (i * (lanes / 32) + (BLOCK ? warp : 0)) * 32 * E + e * 32 + lane;
-  };
-  auto there = [&](int i) { return VEC ? i * lanes + me < p.units : true; };
-
-  // where an item (a row's head) lies
-  auto find = [&](long long item, long long& row, long long& head) {
-    row = p.heads == 1            ? item
-          : p.items < (1ll << 31) ? (unsigned)item / (unsigned)p.heads
-                                  : item / p.heads;
-    head = item - row * p.heads;
-  };
-  uint32_t wx[VEC ? ITEMS : 1][8], wr[VEC ? ITEMS : 1][8];
-  auto load = [&](long long item) {   // VEC
-    if (item >= p.items) return;
-    long long row, head;
-    find(item, row, head);
-    const T* x = static_cast<const T*>(p.x) + row * p.x_rs + head * p.x_hs;
-    const T* res = static_cast<const T*>(p.residual) + row * p.res_rs + head * p.res_hs;
-#pragma unroll
-    for (int i = 0; i < (VEC ? ITEMS : 1); ++i) {
-      if (!there(i)) continue;
-      load8(x + place(i, 0), wx[i]);
-      if constexpr (RES) load8(res + place(i, 0), wr[i]);
-    }
-  };
-  const long long step = (long long)gridDim.x * per_block;
-  if constexpr (VEC) {
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) wx[i][j] = wr[i][j] = 0u;
-    load((long long)blockIdx.x * per_block + (BLOCK ? 0 : tid / lanes));
-  }
-
-  int flip = 0;
-  for (long long item0 = (long long)blockIdx.x * per_block; item0 < p.items; item0 += step, flip ^= 1) {
-    const long long item = item0 + (BLOCK ? 0 : tid / lanes);
-    const bool live = item < p.items;
-    long long row, head;
-    find(item, row, head);
-    T* tot = static_cast<T*>(p.total) + row * p.tot_rs + head * p.tot_hs;
-    T* out = static_cast<T*>(p.out) + row * p.out_rs + head * p.out_hs;
-    uint8_t* codes = p.codes + row * p.code_rs + head * p.code_hs;
-
-    f32x2 h[ITEMS][E / 2];
-    if constexpr (VEC) {
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        if constexpr (RES) {
-          add_words<T>(wx[i], wr[i]);
-          if (p.total && live && there(i)) store8(tot + place(i, 0), wx[i]);
-        }
-        unpack<T>(wx[i], h[i]);
-      }
-      load(item + step);   // the next row's, on their way while this one is worked on
-    } else {
-      const T* x = static_cast<const T*>(p.x) + row * p.x_rs + head * p.x_hs;
-      const T* res = static_cast<const T*>(p.residual) + row * p.res_rs + head * p.res_hs;
-      float v[ITEMS][E];
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int at = place(i, e);
-          v[i][e] = live && at < p.n ? widen(x[at]) : 0.f;
-        }
-      if constexpr (RES) {
-        float r[ITEMS][E];
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int at = place(i, e);
-            r[i][e] = live && at < p.n ? widen(res[at]) : 0.f;
-          }
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int at = place(i, e);
-            const T sum = narrow<T>(v[i][e] + r[i][e]);
-            v[i][e] = widen(sum);
-            if (p.total && live && at < p.n) tot[at] = sum;
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) h[i][e] = f2_pack(v[i][2 * e], v[i][2 * e + 1]);
-    }
-
-    f32x2 sum2 = f2_pack(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      f32x2 part = f2_mul(h[i][0], h[i][0]);   // (shorter chains, and sums of like size)
-#pragma unroll
-      for (int e = 1; e < E / 2; ++e) part = fma2(h[i][e], h[i][e], part);
-      sum2 = add2(sum2, part);
-    }
-    float sum = both(sum2).x + both(sum2).y;
-    // The same of h 2^-64, for rows whose squares pass fp32: a thread whose own do not adds what is left of them.
-    float far = sum * kFarScale * kFarScale;
-    if (!(sum <= 1.2676506e30f)) {   // 2^100
-      const f32x2 c = f2_pack(kFarScale, kFarScale);
-      f32x2 part = f2_pack(0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) part = fma2(f2_mul(h[i][e], c), f2_mul(h[i][e], c), part);
-      far = both(part).x + both(part).y;
-    }
-    // h becomes h (w + o)
-    if (p.weight) {
-      const f32x2 o = f2_pack(p.offset, p.offset);
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        f32x2 w[E / 2];
-        if constexpr (VEC) {
-          if (!there(i)) continue;
-          if (std::is_same<T, float>::value || !p.weight_f32) {
-            uint32_t u[8];
-            load8(static_cast<const T*>(p.weight) + place(i, 0), u);
-            unpack<T>(u, w);
-          } else {
-#pragma unroll
-            for (int k = 0; k < E / 8; ++k) {
-              uint32_t u[8];
-              load8(static_cast<const float*>(p.weight) + place(i, 8 * k), u);
-              unpack<float>(u, w + 4 * k);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            float v[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int at = place(i, e + k);
-              v[k] = at >= p.n      ? 0.f
-                     : p.weight_f32 ? __ldg(static_cast<const float*>(p.weight) + at)
-                                    : widen(static_cast<const T*>(p.weight)[at]);
-            }
-            w[e / 2] = f2_pack(v[0], v[1]);
-          }
-        }
-        if (p.offset != 0.f) {
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) w[e] = add2(w[e], o);
-        }
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) h[i][e] = f2_mul(h[i][e], w[e]);
-      }
-    }
-    float most = 0.f;
-    if (p.scaling == DA_SCALE_ROW) {
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) most = most_of(most, h[i][e]);
-    }
-    // the row's sum and maximum, in an order that the width alone sets
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      if (!BLOCK && o >= lanes) continue;
-      sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    }
-    if constexpr (BLOCK) {
-      // (two places in turn: a warp may be a row ahead, not two)
-      if (lane == 0) s_part[flip][warp] = make_float2(sum, most);
-      __syncthreads();
-      const int warps = blockDim.x >> 5;
-      const float2 v = lane < warps ? s_part[flip][lane] : make_float2(0.f, 0.f);
-      sum = v.x;
-      most = v.y;
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-      }
-      sum = __shfl_sync(0xffffffffu, sum, 0);
-      most = __shfl_sync(0xffffffffu, most, 0);
-    }
-    const float n = (float)p.n;
-    float r = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(sum, n) + p.eps));
-    const bool passed = sum > 3.4028235e38f;
-    if (BLOCK ? passed : __any_sync(0xffffffffu, passed)) {
-      far = row_sum<BLOCK>(far, lanes, s_far);
-      if (passed) r = __fdiv_rn(kFarScale, __fsqrt_rn(__fdiv_rn(far, n) + p.eps * kFarScale * kFarScale));
-    }
-    const f32x2 r2 = f2_pack(r, r);
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) h[i][e] = f2_mul(h[i][e], r2);
-    auto value = [&](int i, int e) { return e & 1 ? both(h[i][e / 2]).y : both(h[i][e / 2]).x; };
-
-    if (p.out) {
-      if constexpr (VEC) {
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-          uint32_t w[8];
-          pack<T>(h[i], w);
-          if (live && there(i)) store8(out + place(i, 0), w);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int at = place(i, e);
-            if (live && at < p.n) out[at] = narrow<T>(value(i, e));
-          }
-      }
-    }
-    if (!p.codes) continue;
-    float scale = 1.f;
-    if (p.scaling == DA_SCALE_TENSOR) scale = __ldg(p.scales);
-    if (p.scaling == DA_SCALE_ROW) {
-      scale = fmaxf(__fdiv_rn(most * r, kE4M3Max), kLeastScale);
-      if (me == 0 && live) p.scales[item] = scale;
-    }
-    Divider over(scale, p.scaling == DA_SCALE_TENSOR);
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      if constexpr (VEC) {
-        if (p.scaling == DA_SCALE_GROUP) {
-          float m = 0.f;
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) m = most_of(m, h[i][e]);
-#pragma unroll
-          for (int o = 1; o < 16; o <<= 1) {
-            if (o * E >= p.group) continue;
-            const float other = __shfl_xor_sync(0xffffffffu, m, o);
-            if (BLOCK || o < lanes) m = fmaxf(m, other);
-          }
-          const float s = fmaxf(__fdiv_rn(m, kE4M3Max), kLeastScale);
-          const int at = place(i, 0);
-          if (live && there(i) && (at & (p.group - 1)) == 0) p.scales[item * p.groups + at / p.group] = s;
-          over = Divider(s, false);
-        }
-        uint32_t w[E / 4];
-#pragma unroll
-        for (int k = 0; k < E / 4; ++k) {
-          const float2 a = over(h[i][2 * k]), b = over(h[i][2 * k + 1]);
-          w[k] = pack_e4m3x2(a.x, a.y) | pack_e4m3x2(b.x, b.y) << 16;
-        }
-        if (live && there(i)) {
-          if constexpr (E == 16)
-            *reinterpret_cast<uint4*>(codes + place(i, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
-          else
-            *reinterpret_cast<uint2*>(codes + place(i, 0)) = make_uint2(w[0], w[1]);
-        }
-      } else if (p.scaling != DA_SCALE_GROUP) {
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 q = over(h[i][e / 2]);
-          const uint32_t w = pack_e4m3x2(q.x, q.y);
-          const int a0 = place(i, e), a1 = place(i, e + 1);
-          if (live && a0 < p.n) codes[a0] = (uint8_t)w;
-          if (live && a1 < p.n) codes[a1] = (uint8_t)(w >> 8);
-        }
-      } else {
-        // a group is group / 32 of every lane's elements
-        float m[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          m[e] = fabsf(value(i, e));
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], o));
-        }
-#pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          const float a = fmaxf(m[e], m[e + 1]), b = fmaxf(m[e + 2], m[e + 3]), c = fmaxf(a, b);
-          if (p.group == 64) {
-            m[e] = m[e + 1] = a;
-            m[e + 2] = m[e + 3] = b;
-          } else if (p.group == 128) {
-            m[e] = m[e + 1] = m[e + 2] = m[e + 3] = c;
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float s = fmaxf(__fdiv_rn(m[e], kE4M3Max), kLeastScale);
-          const int at = place(i, e);
-          if (live && lane == 0 && at < p.n && (at & (p.group - 1)) == 0)
-            p.scales[item * p.groups + at / p.group] = s;
-          if (live && at < p.n) codes[at] = (uint8_t)pack_e4m3x2(__fdiv_rn(value(i, e), s), 0.f);
-        }
-      }
-    }
-  }
-}
-
-template <typename T, bool VEC, bool RES>
-const void* kernel_of(int items, bool block) {
-  if (!block) return reinterpret_cast<const void*>(&norm_kernel<T, 1, VEC, false, RES>);
-  return items <= 1   ? reinterpret_cast<const void*>(&norm_kernel<T, 1, VEC, true, RES>)
-         : items <= 2 ? reinterpret_cast<const void*>(&norm_kernel<T, 2, VEC, true, RES>)
-         : items <= 4 ? reinterpret_cast<const void*>(&norm_kernel<T, 4, VEC, true, RES>)
-                      : reinterpret_cast<const void*>(&norm_kernel<T, std::is_same<T, float>::value ? 8 : 4, VEC, true, RES>);
-}
-template <typename T>
-const void* kernel_of(int items, bool vec, bool block, bool residual) {
-  if (vec) return residual ? kernel_of<T, true, true>(items, block) : kernel_of<T, true, false>(items, block);
-  return residual ? kernel_of<T, false, true>(items, block) : kernel_of<T, false, false>(items, block);
-}
 
 // Whether a row tensor's runs begin on multiples of `bytes`.
 bool begins_on(const void* p, long long rs, long long hs, int es, int bytes) {
@@ -633,38 +127,50 @@ int decode_attn_norm_apply(const da_norm_config* config, const da_norm_args* arg
                    begins_on(a.codes, p.code_rs, p.code_hs, 1, E) && aligned(a.weight, 32);
   const int sms = device_sms();
   if (sms <= 0) return DA_ERR_CUDA;
+  // Rows that begin anywhere, but alike in every tensor (see NormLayout), where a row takes a block.
+  const int V = E / 2;
+  auto alike = [&](const void* at, long long rs, int bytes) {
+    return !at || (aligned(at, bytes) && (((unsigned long long)rs - (unsigned long long)p.x_rs) & (V - 1)) == 0);
+  };
+  const bool shifted = !vec && a.heads == 1 && a.scaling != DA_SCALE_GROUP && c.n > 32 * E &&
+                       c.n <= DECODE_ATTN_NORM_MAX - V && alike(a.x, p.x_rs, 16) &&
+                       alike(a.residual, p.res_rs, 16) && alike(a.residual_out, p.tot_rs, 16) &&
+                       alike(a.out, p.out_rs, 16) && alike(a.codes, p.code_rs, V);
+  const int layout = vec ? kWide : shifted ? kShifted : kScattered;
   // Threads of a row: one for each of its units up to a warp; then whole warps, of two units a thread where there
-  // are more than 256.
-  p.units = vec ? c.n / E : (c.n + 32 * E - 1) / (32 * E);
+  // are more than 256. (A scattered row's: whole warps throughout.)
+  const int units = vec ? c.n / E : shifted ? (c.n + V - 1 + E - 1) / E : (c.n + 32 * E - 1) / (32 * E);
+  p.units = units;
   int threads, per = 1, items_each;
   bool block = false;
-  if (vec && p.units <= 32) {
+  if (vec && units <= 32) {
     p.lanes = 1;
-    while (p.lanes < p.units) p.lanes *= 2;
+    while (p.lanes < units) p.lanes *= 2;
     threads = 128;
     per = threads / p.lanes;
     items_each = 1;
-  } else if (!vec && p.units <= 1) {
+  } else if (!vec && !shifted && units <= 1) {
     p.lanes = 32;
     threads = 128;
     per = 4;
     items_each = 1;
   } else {
     block = true;
-    const int warps = vec ? (p.units + 31) / 32 : p.units;   // at a unit a thread
-    items_each = warps <= 8 ? 1 : warps <= 16 ? 2 : warps <= 32 ? 2 : warps <= 64 ? 4 : 8;
+    const int warps = vec || shifted ? (units + 31) / 32 : units;   // at a unit a thread
+    items_each = warps <= 8 ? 1 : warps <= 32 ? 2 : warps <= 64 ? 4 : 8;
     threads = 32 * ((warps + items_each - 1) / items_each);
     p.lanes = threads;
   }
   const bool residual = a.residual != nullptr;
-  const void* fn = a.dtype == DA_F32   ? kernel_of<float>(items_each, vec, block, residual)
-                   : a.dtype == DA_F16 ? kernel_of<__half>(items_each, vec, block, residual)
-                                       : kernel_of<__nv_bfloat16>(items_each, vec, block, residual);
+  const void* fn = a.dtype == DA_F32   ? norm_kernel_f32(layout, items_each, block, residual)
+                   : a.dtype == DA_F16 ? norm_kernel_f16(layout, items_each, block, residual)
+                                       : norm_kernel_bf16(layout, items_each, block, residual);
   // as many blocks as run at once: a thread loads its next row's share while it works on one
   int resident = 0;
   const int rc = resident_blocks(fn, threads, resident);
   if (rc != DA_OK) return rc;
-  const long long blocks = std::min((items + per - 1) / per, (long long)sms * resident);
+  long long blocks = std::min((items + per - 1) / per, (long long)sms * resident);
+  if (shifted && blocks < items) blocks = std::max<long long>(V, blocks / V * V);   // (a block's rows begin alike)
   void* kargs[1] = {&p};
   const cudaError_t e = cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(threads), kargs, 0,
                                          static_cast<cudaStream_t>(a.cuda_stream));

@@ -342,6 +342,14 @@ def test_workspaces_of_long_steps():
     with pytest.raises(binding.DecodeAttnError) as e:
         binding.decode_attn_adapters_apply(s.handle.config, args)
     assert e.value.code == -3
+    kept = binding.Adapters(256, [64, 64], 32, findings=True)
+    for n in (1290, 1200, 9):
+        got = kept.apply(s.x[:n], s.y[:n], s.a, s.b, s.scales, s.offsets, s.ids)
+        assert torch.equal(got, out[:n]) or n == 9
+        kept.check_status()
+    assert kept.workspace_bytes == size
+    with pytest.raises(ValueError):
+        s.handle.check_status()
     args.workspace, args.workspace_bytes = None, 0
     out.zero_()
     binding.decode_attn_adapters_apply(s.handle.config, args)

@@ -186,9 +186,10 @@ def test_norm(dtype, rows, heads, n, residual, wide_weight, offset):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("rows,heads,n,gap,shift", [(40, 5, 128, 3, 0), (40, 5, 128, 3, 1), (300, 1, 4096, 1, 8),
-                                                    (17, 3, 96, 2, 5), (6, 2, 1000, 1, 16)])
+                                                    (17, 3, 96, 2, 5), (6, 2, 1000, 1, 16),
+                                                    (700, 1, 4099, 0, 8), (700, 1, 1030, 0, 3), (90, 1, 5001, 1, 16)])
 def test_strides_alignment_and_in_place(dtype, rows, heads, n, gap, shift):
-    """Wide and narrow accesses, results over their inputs: the same numbers, and nothing else written."""
+    """Wide and narrow accesses, results over their inputs, and nothing else written."""
     x = _make(rows, heads, n, dtype, gap, shift)
     res = _make(rows, heads, n, dtype, gap, shift, seed=2)
     w = torch.randn(n, generator=torch.Generator().manual_seed(3)).to(TORCH[dtype]).cuda()
@@ -204,7 +205,9 @@ def test_strides_alignment_and_in_place(dtype, rows, heads, n, gap, shift):
     others[shift:].view(rows, heads + gap, n)[:, :heads] = False
     x0, r0 = wide_x[others].clone(), wide_r[others].clone()
     again, total = norm.apply(x, w, residual=res, out=x, residual_out=res)
-    assert again is x and total is res and torch.equal(x, got) and torch.equal(res, u)
+    # (a row's sum goes by how its elements are spread over the threads, which in place may be otherwise)
+    assert again is x and total is res and torch.equal(res, u)
+    near(x, want, "in place")
     assert torch.equal(wide_x[others], x0) and torch.equal(wide_r[others], r0)
     codes = torch.full((shift + rows * (heads + gap) * n,), 0x55, dtype=torch.uint8, device="cuda")
     view = codes[shift:].view(rows, heads + gap, n)[:, :heads]

@@ -79,6 +79,13 @@ __device__ __forceinline__ float most_of(float m, f32x2 x) {
   return r;
 }
 
+// the largest of the warp's m >= 0; a NaN passes over
+__device__ __forceinline__ float warp_most(float m) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
+  return r;
+}
+
 // 8 words of T as floats, and back (rounded to nearest even).
 template <typename T>
 __device__ __forceinline__ void unpack(const uint32_t* w, f32x2* f) {
@@ -139,6 +146,12 @@ __device__ __forceinline__ void store8(void* p, const uint32_t* w) {
   store32(p, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
 }
 
+// y / s by s's reciprocal, and that corrected.
+__device__ __forceinline__ f32x2 divided(f32x2 y, f32x2 minus_s, f32x2 inverse) {
+  const f32x2 q = f2_mul(y, inverse);
+  return fma2(fma2(q, minus_s, y), inverse, q);
+}
+
 // y / s rounded to nearest, for a scale that the row shares: the product with the reciprocal, corrected once by
 // its remainder (Markstein 1990: correctly rounded where the reciprocal is, short of under- and overflow), and the
 // plain division for scales near the ends of the range. `given`: a scale that was not found from y, whose
@@ -160,10 +173,9 @@ struct Divider {
       const float2 f = both(y);
       return make_float2(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
     }
-    const f32x2 q = f2_mul(y, inverse);
-    float2 better = both(fma2(fma2(q, minus, y), inverse, q));
+    float2 better = both(divided(y, minus, inverse));
     if (given) {
-      const float2 f = both(q);
+      const float2 f = both(f2_mul(y, inverse));
       if (!(fabsf(f.x) < 1048576.f)) better.x = f.x;
       if (!(fabsf(f.y) < 1048576.f)) better.y = f.y;
     }
@@ -201,9 +213,19 @@ __device__ __forceinline__ float row_sum(float v, int lanes, float* s_part) {
 // elements; kShifted has none.
 enum NormLayout { kScattered = 0, kWide = 1, kShifted = 2 };
 
+// Registers of a block's thread: 128; with a residual and at most two units 96 (by 640 threads), for 5 blocks an SM of
+// 4 warps in place of 4 (8192 rows of bf16 with groups: width 4096 48 to 44 us, 6144 82 to 67, 8192 alike; without
+// groups 4096 alike, 6144 64 to 68). kScattered with one unit 64, for two blocks an SM or more, as it loads nothing
+// ahead (4000 rows of 4107 bf16 with residual and groups: 159 to 75 us).
+template <int ITEMS, int LAYOUT, bool BLOCK, bool RES>
+constexpr int kMostThreads = !BLOCK ? 128 : LAYOUT == kWide && RES && ITEMS <= 2 ? 640 : 512;
+
 // A row's threads: a block (BLOCK), or `lanes` lanes of a warp, several rows a warp.
 template <typename T, int ITEMS, int LAYOUT, bool BLOCK, bool RES>
-__global__ void __launch_bounds__(BLOCK ? 512 : 128, BLOCK ? 1 : RES ? 6 : 8)
+__global__ void __launch_bounds__(kMostThreads<ITEMS, LAYOUT, BLOCK, RES>,
+                                  !BLOCK                               ? (RES ? 6 : 8)
+                                  : LAYOUT == kScattered && ITEMS == 1 ? 2
+                                                                       : 1)
     norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int E = Unit<T>::E, V = E / 2;
   constexpr bool VEC = LAYOUT != kScattered, SHIFTED = LAYOUT == kShifted;
@@ -515,7 +537,8 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128, BLOCK ? 1 : RES ? 6 : 8)
             const float other = __shfl_xor_sync(0xffffffffu, m, o);
             if (BLOCK || o < lanes) m = fmaxf(m, other);
           }
-          const float s = fmaxf(__fdiv_rn(m, kE4M3Max), kLeastScale);
+          // (lanes without a unit: no scale that would take the warp to the plain division)
+          const float s = there(i) ? fmaxf(__fdiv_rn(m, kE4M3Max), kLeastScale) : 1.f;
           const int at = place(i, 0);
           if (live && there(i) && (at & (p.group - 1)) == 0) p.scales[item * p.groups + at / p.group] = s;
           over = Divider(s, false);
@@ -558,32 +581,48 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128, BLOCK ? 1 : RES ? 6 : 8)
           if (live && a1 < p.n) codes[a1] = (uint8_t)(w >> 8);
         }
       } else {
-        // a group is group / 32 of every lane's elements
-        float m[E];
+        // A group is K = group / 32 of every lane's elements; lane g finds the scale of the unit's group g and its
+        // reciprocal, for all (4000 rows of 4107 fp32, groups of 64: 86 us with every lane finding every scale
+        // and dividing by it, 49 so).
+        auto groups_of = [&](auto k) {
+          constexpr int K = decltype(k)::value, G = E / K;
+          float mine = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          m[e] = fabsf(value(i, e));
+          for (int g = 0; g < G; ++g) {
+            float m = 0.f;
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], o));
-        }
-#pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          const float a = fmaxf(m[e], m[e + 1]), b = fmaxf(m[e + 2], m[e + 3]), c = fmaxf(a, b);
-          if (p.group == 64) {
-            m[e] = m[e + 1] = a;
-            m[e + 2] = m[e + 3] = b;
-          } else if (p.group == 128) {
-            m[e] = m[e + 1] = m[e + 2] = m[e + 3] = c;
+            for (int e = 0; e < K; ++e) m = fmaxf(m, fabsf(value(i, g * K + e)));
+            m = warp_most(m);
+            if (lane == g) mine = m;
           }
-        }
+          const int first = place(i, 0) - lane + lane * 32 * K;   // of lane's group
+          const bool has = lane < G && first < p.n;
+          const float s = has ? fmaxf(__fdiv_rn(mine, kE4M3Max), kLeastScale) : 1.f;
+          if (live && has) p.scales[item * p.groups + first / (32 * K)] = s;
+          const Divider by(s, false);
+          const bool middling = !__any_sync(0xffffffffu, !by.middling);
+          const float inverse = both(by.inverse).x;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float s = fmaxf(__fdiv_rn(m[e], kE4M3Max), kLeastScale);
-          const int at = place(i, e);
-          if (live && lane == 0 && at < p.n && (at & (p.group - 1)) == 0)
-            p.scales[item * p.groups + at / p.group] = s;
-          if (live && at < p.n) codes[at] = (uint8_t)pack_e4m3x2(__fdiv_rn(value(i, e), s), 0.f);
-        }
+          for (int e = 0; e < E; e += 2) {
+            const f32x2 y = h[i][e / 2];
+            const float2 t = make_float2(__shfl_sync(0xffffffffu, s, e / K), __shfl_sync(0xffffffffu, s, (e + 1) / K));
+            float2 q;
+            if (middling) {
+              const f32x2 r2 = f2_pack(__shfl_sync(0xffffffffu, inverse, e / K),
+                                       __shfl_sync(0xffffffffu, inverse, (e + 1) / K));
+              q = both(divided(y, f2_pack(-t.x, -t.y), r2));
+            } else {
+              q = make_float2(__fdiv_rn(both(y).x, t.x), __fdiv_rn(both(y).y, t.y));
+            }
+            const uint32_t w = pack_e4m3x2(q.x, q.y);
+            const int a0 = place(i, e), a1 = place(i, e + 1);
+            if (live && a0 < p.n) codes[a0] = (uint8_t)w;
+            if (live && a1 < p.n) codes[a1] = (uint8_t)(w >> 8);
+          }
+        };
+        if (p.group == 32) groups_of(std::integral_constant<int, 1>());
+        else if (p.group == 64) groups_of(std::integral_constant<int, 2>());
+        else groups_of(std::integral_constant<int, 4>());
       }
     }
   }

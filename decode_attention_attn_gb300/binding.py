@@ -1366,9 +1366,10 @@ class Adapters(_Workspace):
     contiguous, of `dtype` ("f32", "f16", "bf16") as x and y are. Autograd does not record the call; tensors
     that require a gradient are refused outside no_grad().
 
-    Long steps take a workspace for their low-rank sums, from the allocator for each call. With findings=True
-    the object keeps one, whose findings check_status() reports; two such calls must not overlap on the GPU, and a
-    captured graph needs the object (and the longest step made ahead of it) as long as it is replayed."""
+    Long steps for which it pays take a workspace for their low-rank sums, from the allocator for each call. With
+    findings=True the object keeps one, whose findings check_status() reports; two such calls must not overlap on
+    the GPU, and a captured graph needs the object (and the longest step made ahead of it) as long as it is
+    replayed."""
 
     LONG = 1024   # rows from which a step may use a workspace
 

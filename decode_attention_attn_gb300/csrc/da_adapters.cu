@@ -9,9 +9,20 @@ using namespace da;
 
 namespace {
 
-// Rows of a step from which the tall kernels are launched. They cost two launches where no request is long (4 us),
-// and a request of 1024 rows 60 us without them.
+// Rows of a step from which the tall kernels may be launched.
 constexpr int kTallStep = 1024;
+
+// Whether they are worth it. The short kernel takes, in effect, x, y and out at 4 TB/s and an adapter's weights once
+// for 16 rows at 12 (they come from L2); the tall ones x, y and out at 4.8, with 11 us more of launches and first
+// operands (rank 64: 17, as the products weigh; rank 128: 47, as its operands fill the registers). bf16, 4096 wide, short and
+// tall in us: to 6144 columns, 8000 rows of rank 64 183 and 87, of rank 16 95 and 74, 2000 rows 50 and 36, 24 and 26; to
+// 4096 columns, 2000 rows of rank 64 24 and 27, 3200 of rank 128 71 and 81, 8000 148 and 102.
+bool tall_pays(const da_adapter_config& c, long long rows, long long columns) {
+  const long long low = (long long)c.parts * c.rank;
+  const double weights = 2.0 * (rows / kAdapterTile) * (low * c.width + columns * c.rank);
+  const double others = 2.0 * rows * (c.width + 2 * columns);
+  return weights + 0.4 * others > 130e6 + (c.rank < 64 ? 0.0 : c.rank == 64 ? 72e6 : 432e6);
+}
 
 bool begins_on_16(const void* p, long long stride, int es) { return aligned(p, 16) && stride * es % 16 == 0; }
 
@@ -94,31 +105,28 @@ int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter
   p.tall = tall ? kTallRows : INT_MAX;
   if (tall && a.workspace_bytes < tall_workspace(a.rows, low)) return DA_ERR_WORKSPACE_TOO_SMALL;
 
-  // Tiles of 16 rows where an adapter has few, of 64 where it has many (the weights come from L2 once a tile).
   const int groups = std::min(a.batch, a.adapters);
   const long long most_rows = tall ? std::min((long long)a.rows, (kTallRows - 1ll) * a.batch) : a.rows;
-  const long long each = most_rows / groups;
-  int mt = !vec || c.dtype == DA_F32 || each < 40 ? 1 : each < 64 ? 2 : 4;
-  const int column_tiles = low / 8;
-  if (mt == 4 && column_tiles > 32) mt = 2;
-  if (mt == 2 && column_tiles > 48) mt = 1;
-  const int tiles_of_warp = adapter_tiles(mt, column_tiles, p.n_groups);
+  const int tiles_of_warp = adapter_tiles(low / 8, p.n_groups);
   p.pitch = low + ((8 - low) & 31);   // (8 mod 32: the accumulators' pairs of eight rows on different banks)
-  const int m = 16 * mt;
-  // (rows without an adapter are copied whatever their number)
-  const long long tiles = (p.copy ? a.rows : most_rows) / m +
-                          std::min({(long long)a.batch, (long long)a.adapters + p.copy, (long long)a.rows});
-  // CTAs a tile, where an SM holds two at once (by a count that is the same in place, as the sums' order is then;
-  // it is a bound, so that up to three an SM are let in).
-  p.log_ranks = 3;
-  while (p.log_ranks > 0 && (a.rows / m + groups) << p.log_ranks > 3ll * sms) --p.log_ranks;
+  // CTAs a tile: as many as run at once, two an SM (by a count of tiles that is the same in place, as the sums'
+  // order is then), by the tiles that are likely: a half full one an adapter; beside the tall kernels few. More
+  // than run at once begin over: 26 requests of 33 rows 15.9 us with 4 a tile, 25 with 8; 62 of 2 rows, 2176 wide, 12.1
+  // with 4 and 21.7 with 8. (Beside the tall kernels 4 at most, as their tiles may be many all the same: 4 requests of
+  // 900 rows and 60 of one 60 us with 8, 68 with 4, 122 with 1; 64 of 20 to 40 rows 85, 63 and 83.)
+  p.log_ranks = tall ? 2 : 3;
+  const long long likely = tall ? std::max(groups, a.batch / 4)
+                                : std::max((long long)groups, most_rows / kAdapterTile + groups / 2);
+  while (p.log_ranks > 0 && likely << p.log_ranks > 2ll * sms) --p.log_ranks;
   const int ranks = 1 << p.log_ranks;
-  const size_t smem = adapter_smem(a.adapters, mt, c.parts, c.rank, es, p.n_groups, p.pitch);
+  // one cluster for each tile there can be, and what copies rows without an adapter (however many)
+  const long long tiles = most_rows / kAdapterTile + std::min(groups, a.rows) +
+                          (p.copy ? std::min<long long>(a.rows / kAdapterTile + 1, std::max(2 * sms >> p.log_ranks, 1)) : 0);
+  const size_t smem = adapter_smem(a.adapters, c.parts, c.rank, es, p.n_groups, p.pitch);
   if (smem + 4096 > kSmemLimit || tiles * ranks > INT_MAX) return DA_ERR_UNSUPPORTED;
-  const void* fn = c.dtype == DA_F32   ? adapter_kernel_f32(c.rank, mt, tiles_of_warp, vec)
-                   : c.dtype == DA_F16 ? adapter_kernel_f16(c.rank, mt, tiles_of_warp, vec)
-                                       : adapter_kernel_bf16(c.rank, mt, tiles_of_warp, vec);
-  if (!fn) return DA_ERR_UNSUPPORTED;
+  const void* fn = c.dtype == DA_F32   ? adapter_kernel_f32(c.rank, tiles_of_warp, vec)
+                   : c.dtype == DA_F16 ? adapter_kernel_f16(c.rank, tiles_of_warp, vec)
+                                       : adapter_kernel_bf16(c.rank, tiles_of_warp, vec);
   if (smem > 40 * 1024) {
     const int rc = raise_smem(fn, kSmemLimit - 4096, 0);
     if (rc != DA_OK) return rc;
@@ -145,7 +153,9 @@ int decode_attn_adapters_workspace(const da_adapter_config* config, int rows, si
   *bytes = 0;
   if (rows < kTallStep || config->dtype == DA_F32) return DA_OK;
   const long long low = (long long)config->parts * config->rank;
-  if (low <= 256) *bytes = tall_workspace(rows, (int)low);
+  long long columns = 0;
+  for (int s = 0; s < config->parts && s < DECODE_ATTN_ADAPTER_PARTS; ++s) columns += config->out_sizes[s];
+  if (low <= 256 && tall_pays(*config, rows, columns)) *bytes = tall_workspace(rows, (int)low);
   return DA_OK;
 }
 

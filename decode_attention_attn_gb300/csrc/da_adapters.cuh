@@ -10,7 +10,7 @@
 // contraction's index is free, so a lane takes 16 neighbouring bytes of a row and a weight as what two
 // instructions want of it, with no transpose and nothing staged.
 //
-// One launch. A tile is up to 16 MT rows of one adapter, wherever they lie, and a cluster of CTAs takes it: each
+// One launch. A tile is up to 16 rows of one adapter, wherever they lie, and a cluster of CTAs takes it: each
 // CTA contracts a share of x's width, the cluster's CTAs exchange their partial sums through distributed shared
 // memory, and each then expands a share of the columns. Which rows are a tile's, every CTA finds for itself from
 // the requests' offsets and adapters (a few KB), so that no schedule has to be launched ahead.
@@ -26,6 +26,8 @@ namespace da {
 
 constexpr int kAdapterThreads = 256, kAdapterWarps = kAdapterThreads / 32;
 constexpr int kMaxParts = 4;
+constexpr int kAdapterTile = 16;   // rows of a tile: more, the weights' share of the traffic falls, and so do the tiles
+                                   // at work (2000 rows, rank 64, 6144 columns: 47 us with 16, 82 with 32, 88 with 64)
 
 struct AdapterParams {
   const void *x, *y, *a, *b;
@@ -46,7 +48,7 @@ struct AdapterParams {
 };
 
 // Requests of many rows: what their kernels take beside AdapterParams, in da_adapters_tall.cu.
-constexpr int kTallRows = 32;           // rows from which a request is theirs, where they are launched
+constexpr int kTallRows = 64;           // rows from which a request is theirs, where they are launched
 constexpr int kTallPieces = 8;          // sums of a tile, from as many CTAs at most
 constexpr size_t kTallStatusBytes = 256;
 struct TallParams {
@@ -63,11 +65,11 @@ int launch_tall(const AdapterParams& p, int rank, bool bf16, int sms, void* work
 
 // Bytes of dynamic shared memory: the partial sums of every group of warps (where the counts of rows lay before),
 // the sums over the cluster, and them as operands.
-inline size_t adapter_smem(int adapters, int mt, int parts, int rank, int es, int n_groups, int pitch) {
-  const size_t rows = 16 * (size_t)mt;
+inline size_t adapter_smem(int adapters, int parts, int rank, int es, int n_groups, int pitch) {
+  const size_t rows = kAdapterTile;
   const size_t counts = 4 * ((size_t)adapters + 1), sums = rows * pitch * 4 * (kAdapterWarps / n_groups);
   const size_t steps = es == 4 ? rank / 8 : rank < 16 ? 1 : rank / 16;
-  return std::max((counts + 15) / 16 * 16, sums) + rows * pitch * 4 + (size_t)parts * mt * steps * 2 * 512;
+  return std::max((counts + 15) / 16 * 16, sums) + rows * pitch * 4 + (size_t)parts * steps * 2 * 512;
 }
 
 // The contraction of 16 rows with 8 columns, 16 (8 for fp32, as tf32) deep.
@@ -232,27 +234,34 @@ __device__ __forceinline__ int adapter_of(const AdapterParams& p, int b) {
   return id >= 0 && id < p.adapters ? id : p.adapters;
 }
 
-// Tile t: its adapter in sh (-1: there are fewer tiles), its rows in s_row (-1 behind them). Tiles go by adapter,
-// an adapter's rows by request.
-template <int M>
-__device__ void find_tile(const AdapterParams& p, int t, int* s_count, int* s_row, AdapterShared& sh) {
-  const int tid = threadIdx.x, buckets = p.adapters + (p.copy ? 1 : 0);
+// A request ahead of the block's loops, of each thread: its first row, rows and adapter.
+struct AdapterRequest {
+  int row, n, adapter;
+};
+
+// Tile t in sh: its adapter, its first row's place among the adapter's rows and their count. Tiles go by adapter, an
+// adapter's rows by request. Tiles behind the last: sh.adapter is p.adapters (rows without one), and sh.first which of
+// them.
+__device__ __forceinline__ void find_tile(const AdapterParams& p, int t, int* s_count, AdapterRequest& own, AdapterShared& sh) {
+  constexpr int M = kAdapterTile;
+  const int tid = threadIdx.x;
   for (int i = tid; i < p.adapters + 1; i += kAdapterThreads) s_count[i] = 0;
-  if (tid < M) s_row[tid] = -1;
   if (tid == 0) sh.adapter = -1;
   __syncthreads();
-  int first0 = 0, n0 = 0, adapter0 = -1;   // of the request that is the thread's first
+  own.row = own.n = 0;
+  own.adapter = -1;
   for (int b = tid; b < p.batch; b += kAdapterThreads) {
     int first_row;
     int n = rows_of(p, b, first_row);
     const int a = adapter_of(p, b);
     if (n >= p.tall && a < p.adapters) n = 0;
     if (n) atomicAdd(s_count + a, n);
-    if (b == tid) first0 = first_row, n0 = n, adapter0 = a;
+    if (b == tid) own.row = first_row, own.n = n, own.adapter = a;
   }
   __syncthreads();
-  for (int i0 = 0, base = 0; i0 < buckets; i0 += kAdapterThreads) {
-    const int i = i0 + tid, n = i < buckets ? s_count[i] : 0, tiles = (n + M - 1) / M;
+  int base = 0;
+  for (int i0 = 0; i0 < p.adapters; i0 += kAdapterThreads) {
+    const int i = i0 + tid, n = i < p.adapters ? s_count[i] : 0, tiles = (n + M - 1) / M;
     const int before = base + block_prefix(tiles, sh);
     if (before <= t && t < before + tiles) {
       sh.adapter = i;
@@ -261,17 +270,27 @@ __device__ void find_tile(const AdapterParams& p, int t, int* s_count, int* s_ro
     }
     base += sh.chunk_total;
     __syncthreads();
-    if (sh.adapter >= 0 || base > t) break;
+    if (base > t) return;
   }
-  const int adapter = sh.adapter;
-  if (adapter < 0) return;
-  const int first = sh.first, end = min(first + M, sh.count);
+  if (tid == 0) {
+    sh.adapter = p.adapters;
+    sh.first = t - base;
+    sh.count = s_count[p.adapters];
+  }
+  __syncthreads();
+}
+
+// The rows of the tile of `adapter` that begins at `first` of its `count` rows, in s_row (which was all -1).
+__device__ __forceinline__ void rows_of_tile(const AdapterParams& p, int adapter, int first, int count, const AdapterRequest& own,
+                             int* s_row, AdapterShared& sh) {
+  constexpr int M = kAdapterTile;
+  const int tid = threadIdx.x, end = first + min(M, count - first);
   for (int b0 = 0, base = 0; b0 < p.batch && base < end; b0 += kAdapterThreads) {
     const int b = b0 + tid;
     int row = 0, n = 0;
     if (b0 == 0) {
-      row = first0;
-      n = adapter0 == adapter ? n0 : 0;
+      row = own.row;
+      n = own.adapter == adapter ? own.n : 0;
     } else if (b < p.batch && adapter_of(p, b) == adapter) {
       n = rows_of(p, b, row);
       if (n >= p.tall && adapter < p.adapters) n = 0;
@@ -285,9 +304,9 @@ __device__ void find_tile(const AdapterParams& p, int t, int* s_count, int* s_ro
 
 // VEC: rows and weights lie on 16-byte boundaries, parts and the width are multiples of 16 bytes.
 // NT: 8-column tiles of low-rank columns that a warp holds (those behind the last repeat it).
-template <typename T, int MT, int R, int NT, bool VEC>
-__global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kernel(const __grid_constant__ AdapterParams p) {
-  constexpr int M = 16 * MT;                       // rows of a tile
+template <typename T, int R, int NT, bool VEC>
+__global__ void __launch_bounds__(kAdapterThreads, 2) adapter_kernel(const __grid_constant__ AdapterParams p) {
+  constexpr int M = kAdapterTile;
   constexpr bool F32 = std::is_same<T, float>::value;
   constexpr int V = 16 / (int)sizeof(T);           // elements of 16 bytes
   constexpr int KB = 4 * V;                        // of the contraction a warp takes at once: 16 bytes a lane
@@ -303,10 +322,36 @@ __global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kern
   const int low = p.parts * R, pitch = p.pitch;    // low-rank columns
   pdl_launch_dependents();                         // (the tall kernels' rows are others)
 
-  find_tile<M>(p, tile, reinterpret_cast<int*>(smem), s_row, sh);
-  const int adapter = min(sh.adapter, p.adapters);
-  if (adapter < 0) return;                          // (the whole cluster)
-  __syncthreads();
+  const T* y = static_cast<const T*>(p.y);
+  T* out = static_cast<T*>(p.out);
+  AdapterRequest own;
+  if (tid < M) s_row[tid] = -1;
+  find_tile(p, tile, reinterpret_cast<int*>(smem), own, sh);
+  const int adapter = min(max(sh.adapter, 0), p.adapters);
+  if (adapter == p.adapters) {
+    // no adapter: the clusters behind the last tile copy such rows, 16 at a time in turn
+    const int copiers = (int)(gridDim.x >> log_ranks) - tile + sh.first;   // (tiles ahead: tile - sh.first)
+    for (long long first = (long long)sh.first * M; p.copy && first < sh.count; first += (long long)copiers * M) {
+      rows_of_tile(p, adapter, (int)first, sh.count, own, s_row, sh);
+      for (int m = warp; m < M && s_row[m] >= 0; m += kAdapterWarps) {
+        const T* from = y + s_row[m] * p.y_rs;
+        T* to = out + s_row[m] * p.out_rs;
+        const int c1 = p.starts[p.parts];
+        for (int c = (rank * 32 + lane) * V; c < c1; c += 32 * V * ranks) {
+          if (VEC || p.y_wide) {
+            *reinterpret_cast<uint4*>(to + c) = __ldg(reinterpret_cast<const uint4*>(from + c));
+          } else {
+            for (int i = c; i < min(c + V, c1); ++i) to[i] = from[i];
+          }
+        }
+      }
+      __syncthreads();
+      if (tid < M) s_row[tid] = -1;
+      __syncthreads();
+    }
+    return;   // (the whole cluster)
+  }
+  rows_of_tile(p, adapter, sh.first, sh.count, own, s_row, sh);
   if (tid < M) s_from[tid] = min(max(s_row[tid] < 0 ? s_row[0] : s_row[tid], 0), p.rows - 1);
   __syncthreads();
 
@@ -320,23 +365,6 @@ __global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kern
     return s;
   };
 
-  const T* y = static_cast<const T*>(p.y);
-  T* out = static_cast<T*>(p.out);
-  if (adapter == p.adapters) {   // no adapter: the rows as they are
-    for (int m = warp; m < M && s_row[m] >= 0; m += kAdapterWarps) {
-      const T* from = y + s_row[m] * p.y_rs;
-      T* to = out + s_row[m] * p.out_rs;
-      const int c1 = p.starts[p.parts];
-      for (int c = (rank * 32 + lane) * V; c < c1; c += 32 * V * ranks) {
-        if (VEC || p.y_wide) {
-          *reinterpret_cast<uint4*>(to + c) = __ldg(reinterpret_cast<const uint4*>(from + c));
-        } else {
-          for (int i = c; i < min(c + V, c1); ++i) to[i] = from[i];
-        }
-      }
-    }
-    return;
-  }
   const T* a = static_cast<const T*>(p.a) + (long long)adapter * low * p.width;
   const T* b = static_cast<const T*>(p.b) + (long long)adapter * p.starts[p.parts] * R;
 
@@ -349,36 +377,28 @@ __global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kern
   // ---- contraction: low[m][n] = sum over k of x[m][k] a[n][k]
   {
     const int kg = warp / p.n_groups, ng = warp % p.n_groups;
-    float acc[MT][NT][4] = {};
+    float acc[NT][4] = {};
     // (what places behind the tile's rows and low-rank columns hold is never looked at: they read others')
-    const T* xr[MT][2];
+    const T* xr[2];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int o = 0; o < 2; ++o) xr[i][o] = static_cast<const T*>(p.x) + s_from[i * 16 + 8 * o + g] * p.x_rs;
+    for (int o = 0; o < 2; ++o) xr[o] = static_cast<const T*>(p.x) + s_from[8 * o + g] * p.x_rs;
     const int n0 = ng * NT * 8 + g;
-#pragma unroll MT == 1 ? 2 : 1
+#pragma unroll 2
     for (int kb = k0 + kg; kb < k1; kb += k_groups) {
       const int k = kb * KB + q * V, left = p.width - k;
-      uint4 xv[MT][2], av[NT];
+      uint4 xv[2], av[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
         av[j] = load16<T>(a + (long long)min(n0 + j * 8, low - 1) * p.width, k, left, VEC || p.x_wide);
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int o = 0; o < 2; ++o) xv[i][o] = load16<T>(xr[i][o], k, left, VEC || p.x_wide);
+      for (int o = 0; o < 2; ++o) xv[o] = load16<T>(xr[o], k, left, VEC || p.x_wide);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if constexpr (!F32) {
+          const uint32_t f[4] = {s ? xv[0].z : xv[0].x, s ? xv[1].z : xv[1].x, s ? xv[0].w : xv[0].y,
+                                 s ? xv[1].w : xv[1].y};
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            const uint32_t f[4] = {s ? xv[i][0].z : xv[i][0].x, s ? xv[i][1].z : xv[i][1].x,
-                                   s ? xv[i][0].w : xv[i][0].y, s ? xv[i][1].w : xv[i][1].y};
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-              mma16x8<T>(acc[i][j], f, s ? av[j].z : av[j].x, s ? av[j].w : av[j].y);
-          }
+          for (int j = 0; j < NT; ++j) mma16x8<T>(acc[j], f, s ? av[j].z : av[j].x, s ? av[j].w : av[j].y);
         } else {
           // each factor as two tf32 numbers
           uint32_t ah[NT][2], al[NT][2];
@@ -387,31 +407,24 @@ __global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kern
             split_tf32(__uint_as_float(s ? av[j].z : av[j].x), ah[j][0], al[j][0]);
             split_tf32(__uint_as_float(s ? av[j].w : av[j].y), ah[j][1], al[j][1]);
           }
+          uint32_t hi[4], lo[4];
+          split_tf32(__uint_as_float(s ? xv[0].z : xv[0].x), hi[0], lo[0]);
+          split_tf32(__uint_as_float(s ? xv[1].z : xv[1].x), hi[1], lo[1]);
+          split_tf32(__uint_as_float(s ? xv[0].w : xv[0].y), hi[2], lo[2]);
+          split_tf32(__uint_as_float(s ? xv[1].w : xv[1].y), hi[3], lo[3]);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            uint32_t hi[4], lo[4];
-            split_tf32(__uint_as_float(s ? xv[i][0].z : xv[i][0].x), hi[0], lo[0]);
-            split_tf32(__uint_as_float(s ? xv[i][1].z : xv[i][1].x), hi[1], lo[1]);
-            split_tf32(__uint_as_float(s ? xv[i][0].w : xv[i][0].y), hi[2], lo[2]);
-            split_tf32(__uint_as_float(s ? xv[i][1].w : xv[i][1].y), hi[3], lo[3]);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              add_products(acc[i][j], hi, lo, ah[j], al[j]);
-            }
-          }
+          for (int j = 0; j < NT; ++j) add_products(acc[j], hi, lo, ah[j], al[j]);
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int n = (ng * NT + j) * 8 + 2 * q;
-        if (n >= low) continue;
-        float* to = s_part + ((size_t)kg * M + i * 16 + g) * pitch + n;
-        *reinterpret_cast<float2*>(to) = make_float2(acc[i][j][0], acc[i][j][1]);
-        *reinterpret_cast<float2*>(to + 8 * pitch) = make_float2(acc[i][j][2], acc[i][j][3]);
-      }
+    for (int j = 0; j < NT; ++j) {
+      const int n = (ng * NT + j) * 8 + 2 * q;
+      if (n >= low) continue;
+      float* to = s_part + ((size_t)kg * M + g) * pitch + n;
+      *reinterpret_cast<float2*>(to) = make_float2(acc[j][0], acc[j][1]);
+      *reinterpret_cast<float2*>(to + 8 * pitch) = make_float2(acc[j][2], acc[j][3]);
+    }
   }
   __syncthreads();
   if (k_groups > 1) {
@@ -436,10 +449,10 @@ __global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kern
   constexpr int PER = STEPS / BLK;              // of as many steps,
   constexpr int BW = R * (int)sizeof(T) >= 64 ? 4 : R * (int)sizeof(T) / 16;   // of as many words
   constexpr bool B_TOO = 4 * BLK * BW <= 32;
-  constexpr int REGS = MT * 2 * YV * 4 + (B_TOO ? 4 * BLK * BW : 0), ROOM = MT == 4 ? 96 : MT == 2 ? 32 : F32 ? 24 : 56;
+  constexpr int REGS = 2 * YV * 4 + (B_TOO ? 4 * BLK * BW : 0), ROOM = F32 ? 24 : 56;
   constexpr int AHEAD = ROOM / REGS < 1 ? 1 : ROOM / REGS > 3 ? 3 : ROOM / REGS;
   struct Chunk {
-    uint4 y[MT][2][YV];
+    uint4 y[2][YV];
     uint32_t b[B_TOO ? BLK : 1][4][BW];
   };
   auto load_b = [&](int col0, int end, int blk, uint32_t (*bw)[BW]) {
@@ -462,13 +475,11 @@ __global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kern
     const int s = part_of(h), col0 = p.starts[s] + (h - p.chunks[s]) * 32, end = p.starts[s + 1];
     const int mine = col0 + q * 8;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int o = 0; o < 2; ++o) {
+      const T* from = y + s_from[8 * o + g] * p.y_rs;
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const T* from = y + s_from[i * 16 + 8 * o + g] * p.y_rs;
-#pragma unroll
-        for (int w = 0; w < YV; ++w) c.y[i][o][w] = load16<T>(from, mine + w * V, end - mine - w * V, VEC || p.y_wide);
-      }
+      for (int w = 0; w < YV; ++w) c.y[o][w] = load16<T>(from, mine + w * V, end - mine - w * V, VEC || p.y_wide);
+    }
     if constexpr (B_TOO) {
 #pragma unroll
       for (int blk = 0; blk < BLK; ++blk) load_b(col0, end, blk, c.b[blk]);
@@ -524,10 +535,10 @@ __global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kern
     __syncthreads();
   }
   // as operands: what each lane holds of 16 rows and a step, the large parts and the small ones
-  for (int i = tid; i < (part1 - part0) * MT * STEPS * 32; i += kAdapterThreads) {
-    const int l = i & 31, step = (i >> 5) % STEPS, ms = (i >> 5) / STEPS, m16 = ms % MT, s = part0 + ms / MT;
+  for (int i = tid; i < (part1 - part0) * STEPS * 32; i += kAdapterThreads) {
+    const int l = i & 31, step = (i >> 5) % STEPS, s = part0 + (i >> 5) / STEPS;
     const int lg = l >> 2, lq = l & 3;
-    const float* v0 = s_sum + (size_t)(m16 * 16 + lg) * pitch + s * R;
+    const float* v0 = s_sum + (size_t)lg * pitch + s * R;
     const float* v1 = v0 + 8 * pitch;
     uint32_t hi[4], lo[4];
     if constexpr (F32) {
@@ -539,8 +550,8 @@ __global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kern
     } else {
       float c0 = 1.f, c1 = 1.f;
       if constexpr (std::is_same<T, __half>::value) {
-        c0 = s_scale[(m16 * 16 + lg) * kMaxParts + s];
-        c1 = s_scale[(m16 * 16 + lg + 8) * kMaxParts + s];
+        c0 = s_scale[lg * kMaxParts + s];
+        c1 = s_scale[(lg + 8) * kMaxParts + s];
       }
       if constexpr (R < 16) {
         split_pair<T>(v0[lq * 2] * c0, v0[lq * 2 + 1] * c0, hi[0], lo[0]);
@@ -554,7 +565,7 @@ __global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kern
         split_pair<T>(v1[k + 2] * c1, v1[k + 3] * c1, hi[3], lo[3]);
       }
     }
-    uint4* to = s_frag + (((size_t)(s - part0) * MT + m16) * STEPS + step) * 64 + l;
+    uint4* to = s_frag + ((size_t)(s - part0) * STEPS + step) * 64 + l;
     to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     to[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
@@ -566,8 +577,8 @@ __global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kern
   auto finish = [&](int h, const Chunk& now) {
     const int s = part_of(h), col0 = p.starts[s] + (h - p.chunks[s]) * 32, end = p.starts[s + 1];
     const int mine = col0 + q * 8, n_mine = min(end - mine, 8);   // (none there: below 1)
-    float acc[MT][4][4] = {};
-    const uint4* frag = s_frag + (size_t)(s - part0) * MT * STEPS * 64 + lane;
+    float acc[4][4] = {};
+    const uint4* frag = s_frag + (size_t)(s - part0) * STEPS * 64 + lane;
 #pragma unroll
     for (int blk = 0; blk < BLK; ++blk) {
       uint32_t bw[4][BW];
@@ -584,75 +595,70 @@ __global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kern
             if constexpr (F32) split_tf32(__uint_as_float(w), bh[j][e], bl[j][e]);
             else bh[j][e] = w;
           }
+        const uint4* f = frag + (blk * PER + t) * 64;
+        const uint4 fh = f[0], fl = f[32];
+        const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const uint4* f = frag + (i * STEPS + blk * PER + t) * 64;
-          const uint4 fh = f[0], fl = f[32];
-          const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (F32) {
-              add_products(acc[i][j], hi, lo, bh[j], bl[j]);
-            } else {
-              mma16x8<T>(acc[i][j], lo, bh[j][0], bh[j][1]);
-              mma16x8<T>(acc[i][j], hi, bh[j][0], bh[j][1]);
-            }
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (F32) {
+            add_products(acc[j], hi, lo, bh[j], bl[j]);
+          } else {
+            mma16x8<T>(acc[j], lo, bh[j][0], bh[j][1]);
+            mma16x8<T>(acc[j], hi, bh[j][0], bh[j][1]);
           }
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int o = 0; o < 2; ++o) {
+      const int m = 8 * o + g, r = s_row[m];
+      if (r < 0 || n_mine <= 0) continue;
+      float c = c_a;
+      if constexpr (std::is_same<T, __half>::value) c = c_a / s_scale[m * kMaxParts + s];
+      T* to = out + r * p.out_rs + mine;
+      if constexpr (F32) {
+        float v[8];
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const int m = i * 16 + 8 * o + g, r = s_row[m];
-        if (r < 0 || n_mine <= 0) continue;
-        float c = c_a;
-        if constexpr (std::is_same<T, __half>::value) c = c_a / s_scale[m * kMaxParts + s];
-        T* to = out + r * p.out_rs + mine;
-        if constexpr (F32) {
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint4 w = now.y[i][o][e / 4];
-            v[e] = __uint_as_float(e % 4 == 0 ? w.x : e % 4 == 1 ? w.y : e % 4 == 2 ? w.z : w.w) +
-                   c * acc[i][e / 2][2 * o + (e & 1)];
-          }
-          if (VEC || p.y_wide) {
-            *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
-            if (n_mine > 4) *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (e < n_mine) to[e] = v[e];
-          }
+        for (int e = 0; e < 8; ++e) {
+          const uint4 w = now.y[o][e / 4];
+          v[e] = __uint_as_float(e % 4 == 0 ? w.x : e % 4 == 1 ? w.y : e % 4 == 2 ? w.z : w.w) +
+                 c * acc[e / 2][2 * o + (e & 1)];
+        }
+        if (VEC || p.y_wide) {
+          *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+          if (n_mine > 4) *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
         } else {
-          const uint32_t in[4] = {now.y[i][o][0].x, now.y[i][o][0].y, now.y[i][o][0].z, now.y[i][o][0].w};
-          uint32_t w[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float y0, y1;
-            if constexpr (std::is_same<T, __half>::value) {
-              __half2 hv;
-              memcpy(&hv, &in[j], 4);
-              const float2 f = __half22float2(hv);
-              y0 = f.x;
-              y1 = f.y;
-            } else {
-              y0 = __uint_as_float(in[j] << 16);
-              y1 = __uint_as_float(in[j] & 0xffff0000u);
-            }
-            w[j] = pack2(y0 + c * acc[i][j][2 * o], y1 + c * acc[i][j][2 * o + 1], T());
-          }
-          if (VEC || p.y_wide) {
-            *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int e = 0; e < 8; ++e)
+            if (e < n_mine) to[e] = v[e];
+        }
+      } else {
+        const uint32_t in[4] = {now.y[o][0].x, now.y[o][0].y, now.y[o][0].z, now.y[o][0].w};
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float y0, y1;
+          if constexpr (std::is_same<T, __half>::value) {
+            __half2 hv;
+            memcpy(&hv, &in[j], 4);
+            const float2 f = __half22float2(hv);
+            y0 = f.x;
+            y1 = f.y;
           } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (e < n_mine) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            y0 = __uint_as_float(in[j] << 16);
+            y1 = __uint_as_float(in[j] & 0xffff0000u);
           }
+          w[j] = pack2(y0 + c * acc[j][2 * o], y1 + c * acc[j][2 * o + 1], T());
+        }
+        if (VEC || p.y_wide) {
+          *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < n_mine) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
         }
       }
+    }
   };
 #pragma unroll 1
   for (int h = h0 + warp; h < h1; h += AHEAD * kAdapterWarps) {
@@ -670,50 +676,38 @@ __global__ void __launch_bounds__(kAdapterThreads, MT == 4 ? 1 : 2) adapter_kern
 
 // The 8-column tiles of a warp, of `columns` of them in all: the fewest built that take them with 1, 2, 4 or 8 warps
 // side by side (`groups`).
-inline int adapter_tiles(int mt, int columns, int& groups) {
-  const int most = mt == 1 ? 8 : mt == 2 ? 6 : 4;
+inline int adapter_tiles(int columns, int& groups) {
   groups = 1;
-  while ((columns + groups - 1) / groups > most) groups *= 2;
+  while ((columns + groups - 1) / groups > 8) groups *= 2;
   const int each = (columns + groups - 1) / groups;
   return each <= 4 ? 4 : each <= 6 ? 6 : 8;
 }
 
-// The kernel for tiles of 16 mt rows (null: not built).
+// The kernel of a rank and of `tiles` 8-column tiles a warp.
 template <typename T, int R, int NT>
-const void* adapter_kernel_of(int mt, bool vec) {
-  if (mt == 1)
-    return vec ? reinterpret_cast<const void*>(&adapter_kernel<T, 1, R, NT, true>)
-               : reinterpret_cast<const void*>(&adapter_kernel<T, 1, R, NT, false>);
-  if constexpr (!std::is_same<T, float>::value && NT <= 6) {
-    if (mt == 2 && vec) return reinterpret_cast<const void*>(&adapter_kernel<T, 2, R, NT, true>);
-    if constexpr (NT == 4)
-      if (mt == 4 && vec) return reinterpret_cast<const void*>(&adapter_kernel<T, 4, R, NT, true>);
-  }
-  return nullptr;
+const void* adapter_kernel_of(bool vec) {
+  return vec ? reinterpret_cast<const void*>(&adapter_kernel<T, R, NT, true>)
+             : reinterpret_cast<const void*>(&adapter_kernel<T, R, NT, false>);
 }
 template <typename T, int R>
-const void* adapter_kernel_of(int mt, int tiles, bool vec) {
-  if (tiles == 4) return adapter_kernel_of<T, R, 4>(mt, vec);
+const void* adapter_kernel_of(int tiles, bool vec) {
   if constexpr (R >= 16) {   // (rank 8: at most 4 tiles in all)
-    if (tiles == 6) return adapter_kernel_of<T, R, 6>(mt, vec);
-    if (tiles == 8) return adapter_kernel_of<T, R, 8>(mt, vec);
+    if (tiles == 6) return adapter_kernel_of<T, R, 6>(vec);
+    if (tiles == 8) return adapter_kernel_of<T, R, 8>(vec);
   }
-  return nullptr;
+  return adapter_kernel_of<T, R, 4>(vec);
 }
 template <typename T>
-const void* adapter_kernel_for(int rank, int mt, int tiles, bool vec) {
-  switch (rank) {
-    case 8: return adapter_kernel_of<T, 8>(mt, tiles, vec);
-    case 16: return adapter_kernel_of<T, 16>(mt, tiles, vec);
-    case 32: return adapter_kernel_of<T, 32>(mt, tiles, vec);
-    case 64: return adapter_kernel_of<T, 64>(mt, tiles, vec);
-    case 128: return adapter_kernel_of<T, 128>(mt, tiles, vec);
-    default: return nullptr;
-  }
+const void* adapter_kernel_for(int rank, int tiles, bool vec) {
+  return rank == 8    ? adapter_kernel_of<T, 8>(tiles, vec)
+         : rank == 16 ? adapter_kernel_of<T, 16>(tiles, vec)
+         : rank == 32 ? adapter_kernel_of<T, 32>(tiles, vec)
+         : rank == 64 ? adapter_kernel_of<T, 64>(tiles, vec)
+                      : adapter_kernel_of<T, 128>(tiles, vec);
 }
 
-const void* adapter_kernel_bf16(int rank, int mt, int tiles, bool vec);
-const void* adapter_kernel_f16(int rank, int mt, int tiles, bool vec);
-const void* adapter_kernel_f32(int rank, int mt, int tiles, bool vec);
+const void* adapter_kernel_bf16(int rank, int tiles, bool vec);
+const void* adapter_kernel_f16(int rank, int tiles, bool vec);
+const void* adapter_kernel_f32(int rank, int tiles, bool vec);
 
 }  // namespace da

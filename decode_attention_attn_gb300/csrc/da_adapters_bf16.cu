@@ -3,8 +3,8 @@
 
 namespace da {
 
-const void* adapter_kernel_bf16(int rank, int mt, int tiles, bool vec) {
-  return adapter_kernel_for<__nv_bfloat16>(rank, mt, tiles, vec);
+const void* adapter_kernel_bf16(int rank, int tiles, bool vec) {
+  return adapter_kernel_for<__nv_bfloat16>(rank, tiles, vec);
 }
 
 }  // namespace da

@@ -3,8 +3,8 @@
 
 namespace da {
 
-const void* adapter_kernel_f32(int rank, int mt, int tiles, bool vec) {
-  return adapter_kernel_for<float>(rank, mt, tiles, vec);
+const void* adapter_kernel_f32(int rank, int tiles, bool vec) {
+  return adapter_kernel_for<float>(rank, tiles, vec);
 }
 
 }  // namespace da

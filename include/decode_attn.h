@@ -791,7 +791,7 @@ typedef struct {
  *   scales        nullable device float [adapters] (null: 1).
  *   row_offsets, adapter_ids   device int32 [batch + 1] and [batch].
  *   workspace     nullable device memory, 256-byte aligned, of decode_attn_adapters_workspace bytes, which lies
- *                 apart from everything else: 16-bit steps of 1024 rows and more then take requests of 32 rows
+ *                 apart from everything else: 16-bit steps of 1024 rows and more then take requests of 64 rows
  *                 and more in two further launches on the tensor cores (tcgen05). Its first word takes
  *                 DEVICE_TIMEOUT, cleared by the caller ahead of the first call; the rest need not be. Two calls
  *                 that can overlap on the GPU need workspaces of their own.
@@ -819,7 +819,8 @@ typedef struct {
   void* cuda_stream;
 } da_adapter_args;
 
-/* The workspace with which a call over `rows` rows is fastest (0: it uses none). Host only. Errors: INVALID_ARG. */
+/* The workspace with which a call over `rows` rows is fastest (0: without one; the size depends on rows, parts and rank
+ * alone, whether there is one on the widths too). Host only. Errors: INVALID_ARG. */
 int decode_attn_adapters_workspace(const da_adapter_config* config, int rows, size_t* bytes);
 
 /* Synchronise `stream`, then read and clear the finding that calls with this workspace left in its first word:

@@ -14,9 +14,9 @@ constexpr int kTallStep = 1024;
 
 // Whether they are worth it. The short kernel takes, in effect, x, y and out at 4 TB/s and an adapter's weights once
 // for 16 rows at 12 (they come from L2); the tall ones x, y and out at 4.8, with 11 us more of launches and first
-// operands (rank 64: 17, as the products weigh; rank 128: 47, as its operands fill the registers). bf16, 4096 wide, short and
-// tall in us: to 6144 columns, 8000 rows of rank 64 183 and 87, of rank 16 95 and 74, 2000 rows 50 and 36, 24 and 26; to
-// 4096 columns, 2000 rows of rank 64 24 and 27, 3200 of rank 128 71 and 81, 8000 148 and 102.
+// operands (rank 64: 17, as the products weigh; rank 128: 47, as its operands fill the registers). bf16, 4096 wide,
+// short and tall in us: to 6144 columns, 8000 rows of rank 64 183 and 83, of rank 16 95 and 71, 2000 rows 50 and 36, 24
+// and 26; to 4096 columns, 2000 rows of rank 64 23 and 27, 3200 of rank 128 71 and 81, 8000 147 and 102.
 bool tall_pays(const da_adapter_config& c, long long rows, long long columns) {
   const long long low = (long long)c.parts * c.rank;
   const double weights = 2.0 * (rows / kAdapterTile) * (low * c.width + columns * c.rank);
@@ -120,8 +120,8 @@ int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter
   while (p.log_ranks > 0 && likely << p.log_ranks > 2ll * sms) --p.log_ranks;
   const int ranks = 1 << p.log_ranks;
   // one cluster for each tile there can be, and what copies rows without an adapter (however many)
-  const long long tiles = most_rows / kAdapterTile + std::min(groups, a.rows) +
-                          (p.copy ? std::min<long long>(a.rows / kAdapterTile + 1, std::max(2 * sms >> p.log_ranks, 1)) : 0);
+  const int copiers = p.copy ? std::min(a.rows / kAdapterTile + 1, std::max(2 * sms >> p.log_ranks, 1)) : 0;
+  const long long tiles = most_rows / kAdapterTile + std::min(groups, a.rows) + copiers;
   const size_t smem = adapter_smem(a.adapters, c.parts, c.rank, es, p.n_groups, p.pitch);
   if (smem + 4096 > kSmemLimit || tiles * ranks > INT_MAX) return DA_ERR_UNSUPPORTED;
   const void* fn = c.dtype == DA_F32   ? adapter_kernel_f32(c.rank, tiles_of_warp, vec)
@@ -149,12 +149,14 @@ int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter
 }
 
 int decode_attn_adapters_workspace(const da_adapter_config* config, int rows, size_t* bytes) {
-  if (!config || !bytes || rows < 0 || config->width < 1 || config->parts < 1) return DA_ERR_INVALID_ARG;
+  if (!config || !bytes || rows < 0 || config->width < 1 || config->parts < 1 || config->rank < 1 ||
+      config->parts > DECODE_ATTN_ADAPTER_PARTS)
+    return DA_ERR_INVALID_ARG;
   *bytes = 0;
   if (rows < kTallStep || config->dtype == DA_F32) return DA_OK;
   const long long low = (long long)config->parts * config->rank;
   long long columns = 0;
-  for (int s = 0; s < config->parts && s < DECODE_ATTN_ADAPTER_PARTS; ++s) columns += config->out_sizes[s];
+  for (int s = 0; s < config->parts; ++s) columns += config->out_sizes[s];
   if (low <= 256 && tall_pays(*config, rows, columns)) *bytes = tall_workspace(rows, (int)low);
   return DA_OK;
 }

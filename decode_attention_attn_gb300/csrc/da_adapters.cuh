@@ -26,8 +26,10 @@ namespace da {
 
 constexpr int kAdapterThreads = 256, kAdapterWarps = kAdapterThreads / 32;
 constexpr int kMaxParts = 4;
-constexpr int kAdapterTile = 16;   // rows of a tile: more, the weights' share of the traffic falls, and so do the tiles
-                                   // at work (2000 rows, rank 64, 6144 columns: 47 us with 16, 82 with 32, 88 with 64)
+// Rows of a tile. With more of them weights are read less often, but fewer CTAs are at work, one an SM from 64 rows on
+// (at the best number of CTAs a tile: 2000 rows, rank 64, 4096 to 6144: 47 us with 16, 60 with 32, 89 with 64; 2300
+// rows, rank 8: 14, 17 and 21).
+constexpr int kAdapterTile = 16;
 
 struct AdapterParams {
   const void *x, *y, *a, *b;
@@ -242,7 +244,8 @@ struct AdapterRequest {
 // Tile t in sh: its adapter, its first row's place among the adapter's rows and their count. Tiles go by adapter, an
 // adapter's rows by request. Tiles behind the last: sh.adapter is p.adapters (rows without one), and sh.first which of
 // them.
-__device__ __forceinline__ void find_tile(const AdapterParams& p, int t, int* s_count, AdapterRequest& own, AdapterShared& sh) {
+__device__ __forceinline__ void find_tile(const AdapterParams& p, int t, int* s_count, AdapterRequest& own,
+                                          AdapterShared& sh) {
   constexpr int M = kAdapterTile;
   const int tid = threadIdx.x;
   for (int i = tid; i < p.adapters + 1; i += kAdapterThreads) s_count[i] = 0;
@@ -281,8 +284,8 @@ __device__ __forceinline__ void find_tile(const AdapterParams& p, int t, int* s_
 }
 
 // The rows of the tile of `adapter` that begins at `first` of its `count` rows, in s_row (which was all -1).
-__device__ __forceinline__ void rows_of_tile(const AdapterParams& p, int adapter, int first, int count, const AdapterRequest& own,
-                             int* s_row, AdapterShared& sh) {
+__device__ __forceinline__ void rows_of_tile(const AdapterParams& p, int adapter, int first, int count,
+                                             const AdapterRequest& own, int* s_row, AdapterShared& sh) {
   constexpr int M = kAdapterTile;
   const int tid = threadIdx.x, end = first + min(M, count - first);
   for (int b0 = 0, base = 0; b0 < p.batch && base < end; b0 += kAdapterThreads) {
@@ -296,7 +299,11 @@ __device__ __forceinline__ void rows_of_tile(const AdapterParams& p, int adapter
       if (n >= p.tall && adapter < p.adapters) n = 0;
     }
     const int before = base + block_prefix(n, sh);
-    for (int i = max(first - before, 0); i < n && before + i < end; ++i) s_row[before + i - first] = row + i;
+    for (int i = max(first - before, 0); i < n && before + i < end; ++i) {
+      const unsigned at = before + i - first;
+      if (at >= M) break;   // (counts of offsets out of order may pass 32 bits)
+      s_row[at] = row + i;
+    }
     base += sh.chunk_total;
     __syncthreads();
   }

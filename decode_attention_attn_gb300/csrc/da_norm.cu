@@ -122,9 +122,11 @@ int decode_attn_norm_apply(const da_norm_config* config, const da_norm_args* arg
   p.eps = c.eps;
   p.offset = c.weight_offset;
   const int E = 32 / es;
-  const bool vec = c.n % E == 0 && begins_on(a.x, p.x_rs, p.x_hs, es, 32) && begins_on(a.residual, p.res_rs, p.res_hs, es, 32) &&
-                   begins_on(a.residual_out, p.tot_rs, p.tot_hs, es, 32) && begins_on(a.out, p.out_rs, p.out_hs, es, 32) &&
-                   begins_on(a.codes, p.code_rs, p.code_hs, 1, E) && aligned(a.weight, 32);
+  const bool vec = c.n % E == 0 && begins_on(a.x, p.x_rs, p.x_hs, es, 32) &&
+                   begins_on(a.residual, p.res_rs, p.res_hs, es, 32) &&
+                   begins_on(a.residual_out, p.tot_rs, p.tot_hs, es, 32) &&
+                   begins_on(a.out, p.out_rs, p.out_hs, es, 32) && begins_on(a.codes, p.code_rs, p.code_hs, 1, E) &&
+                   aligned(a.weight, 32);
   const int sms = device_sms();
   if (sms <= 0) return DA_ERR_CUDA;
   // Rows that begin anywhere, but alike in every tensor (see NormLayout), where a row takes a block.

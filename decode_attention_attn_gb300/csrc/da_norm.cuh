@@ -641,7 +641,8 @@ const void* norm_kernel_of(int items, bool block) {
 }
 template <typename T>
 const void* norm_kernel_for(int layout, int items, bool block, bool residual) {
-  if (layout == kWide) return residual ? norm_kernel_of<T, kWide, true>(items, block) : norm_kernel_of<T, kWide, false>(items, block);
+  if (layout == kWide)
+    return residual ? norm_kernel_of<T, kWide, true>(items, block) : norm_kernel_of<T, kWide, false>(items, block);
   if (layout == kShifted)
     return residual ? norm_kernel_of<T, kShifted, true>(items, block) : norm_kernel_of<T, kShifted, false>(items, block);
   return residual ? norm_kernel_of<T, kScattered, true>(items, block)

@@ -1,7 +1,8 @@
 /*
  * decode_attn.h -- C ABI of the GB300 (sm_103a) decode-attention library: single-query decode
- * attention over a KV cache, attention for trees of drafted tokens over the same cache, and the
- * operators that fill and read it (rotary positions, quantising writes, reads).
+ * attention over a KV cache, attention for trees of drafted tokens over the same cache, the
+ * operators that fill and read it (rotary positions, quantising writes, reads), and what a serving
+ * loop runs beside them: pages from lengths, norms, and requests' adapters.
  *
  * Computes, for every sequence b and query head h of a decode step,
  *     o[b,h] = softmax(scale * q[b,h] . K_b^T) V_b          (natural exp)

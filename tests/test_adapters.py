@@ -54,6 +54,21 @@ def test_apply_refuses_bad_arguments():
         binding._check(binding.lib().decode_attn_adapters_apply(None, None), "adapters")
 
 
+def test_the_workspace_by_widths_rows_and_rank():
+    def size(rows, dtype=2, width=4096, sizes=(4096, 1024, 1024, 0), parts=3, rank=64):
+        config = binding.da_adapter_config(dtype, width, parts, (binding.ctypes.c_int * 4)(*sizes), rank)
+        return binding.decode_attn_adapters_workspace(config, rows)
+
+    assert size(8000) == size(8000, width=8192) > size(4000) > 256       # by rows, parts and rank
+    assert size(8000, sizes=(8192, 8192, 8192, 0)) == size(8000) == size(8000, dtype=1)
+    assert size(1023) == size(0) == size(8000, dtype=0) == size(8000, rank=128) == 0
+    assert size(1100, width=256, sizes=(64, 64, 64, 0)) == size(2000, rank=8) == 0   # few weights: short launches
+    for kw in (dict(rows=-1), dict(width=0), dict(parts=0), dict(parts=5), dict(rank=0), dict(rank=-8)):
+        with pytest.raises(binding.DecodeAttnError) as e:
+            size(**{"rows": 8000, **kw})
+        assert e.value.code == -1
+
+
 def test_wrapper_refuses_bad_tensors():
     for args in ((0, [8], 8), (64, [], 8), (64, [8] * 5, 8), (64, [8, 0], 8), (64, [8], 12)):
         with pytest.raises(ValueError):

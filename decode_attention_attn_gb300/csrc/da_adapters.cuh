@@ -45,7 +45,7 @@ struct AdapterParams {
   int log_ranks;                // CTAs that share a tile
   int pitch;                    // floats of a row of partial sums
   int copy;                     // rows without an adapter are copied (out is not y)
-  int x_wide, y_wide;           // (of the kernel for odd shapes) x and weights / y and out by 16 bytes
+  int x_unit, y_unit;           // bytes that x and A / y and out move by: 16, 8, 4 or an element's
   int tall;                     // requests of as many rows with an adapter are left to the tall kernels
 };
 
@@ -170,24 +170,53 @@ __device__ __forceinline__ float4 load_of_rank(const float* p, uint32_t rank) {
   return v;
 }
 
-// 16 bytes of T at row + k, of which the first `left` elements are there (none: zeros); elements one by one unless
-// `wide`.
+// 16 bytes of T at row + k, of which the first `left` elements are there (none: zeros), `unit` bytes at a time:
+// 16, an element's, or between them 8 or 4 (fp32: none between).
 template <typename T>
-__device__ __forceinline__ uint4 load16(const T* row, int k, int left, bool wide) {
+__device__ __forceinline__ uint4 load16(const T* row, int k, int left, int unit) {
   constexpr int V = 16 / (int)sizeof(T);
-  if (wide) return left > 0 ? __ldg(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0u, 0u, 0u, 0u);
+  if (unit == 16) return left > 0 ? __ldg(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0u, 0u, 0u, 0u);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if (sizeof(T) == 2 && unit == 8) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (i < left) {
-      if constexpr (sizeof(T) == 4) {
-        w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + k) + i);
-      } else {
-        w[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(row + k) + i) << (16 * (i & 1));
+    for (int i = 0; i < 2; ++i) {
+      if (i * (V / 2) < left) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + k) + i);
+        w[2 * i] = v.x;
+        w[2 * i + 1] = v.y;
       }
     }
+  } else if (sizeof(T) == 4 || unit == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i * (V / 4) < left) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + k) + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < left) w[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(row + k) + i) << (16 * (i & 1));
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The first `left` elements of 16 bytes of T to `to`, in the same way.
+template <typename T>
+__device__ __forceinline__ void store16(T* to, int left, int unit, const uint32_t* w) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (unit == 16) {
+    if (left > 0) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if (sizeof(T) == 2 && unit == 8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (i * (V / 2) < left) reinterpret_cast<uint2*>(to)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
+  } else if (sizeof(T) == 4 || unit == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i * (V / 4) < left) reinterpret_cast<uint32_t*>(to)[i] = w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < left) reinterpret_cast<uint16_t*>(to)[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+  }
 }
 
 struct AdapterShared {
@@ -345,11 +374,9 @@ __global__ void __launch_bounds__(kAdapterThreads, 2) adapter_kernel(const __gri
         T* to = out + s_row[m] * p.out_rs;
         const int c1 = p.starts[p.parts];
         for (int c = (rank * 32 + lane) * V; c < c1; c += 32 * V * ranks) {
-          if (VEC || p.y_wide) {
-            *reinterpret_cast<uint4*>(to + c) = __ldg(reinterpret_cast<const uint4*>(from + c));
-          } else {
-            for (int i = c; i < min(c + V, c1); ++i) to[i] = from[i];
-          }
+          const uint4 v = load16<T>(from, c, c1 - c, VEC ? 16 : p.y_unit);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          store16<T>(to + c, c1 - c, VEC ? 16 : p.y_unit, w);
         }
       }
       __syncthreads();
@@ -396,9 +423,9 @@ __global__ void __launch_bounds__(kAdapterThreads, 2) adapter_kernel(const __gri
       uint4 xv[2], av[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        av[j] = load16<T>(a + (long long)min(n0 + j * 8, low - 1) * p.width, k, left, VEC || p.x_wide);
+        av[j] = load16<T>(a + (long long)min(n0 + j * 8, low - 1) * p.width, k, left, VEC ? 16 : p.x_unit);
 #pragma unroll
-      for (int o = 0; o < 2; ++o) xv[o] = load16<T>(xr[o], k, left, VEC || p.x_wide);
+      for (int o = 0; o < 2; ++o) xv[o] = load16<T>(xr[o], k, left, VEC ? 16 : p.x_unit);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if constexpr (!F32) {
@@ -485,7 +512,7 @@ __global__ void __launch_bounds__(kAdapterThreads, 2) adapter_kernel(const __gri
     for (int o = 0; o < 2; ++o) {
       const T* from = y + s_from[8 * o + g] * p.y_rs;
 #pragma unroll
-      for (int w = 0; w < YV; ++w) c.y[o][w] = load16<T>(from, mine + w * V, end - mine - w * V, VEC || p.y_wide);
+      for (int w = 0; w < YV; ++w) c.y[o][w] = load16<T>(from, mine + w * V, end - mine - w * V, VEC ? 16 : p.y_unit);
     }
     if constexpr (B_TOO) {
 #pragma unroll
@@ -624,21 +651,15 @@ __global__ void __launch_bounds__(kAdapterThreads, 2) adapter_kernel(const __gri
       if constexpr (std::is_same<T, __half>::value) c = c_a / s_scale[m * kMaxParts + s];
       T* to = out + r * p.out_rs + mine;
       if constexpr (F32) {
-        float v[8];
+        uint32_t v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const uint4 w = now.y[o][e / 4];
-          v[e] = __uint_as_float(e % 4 == 0 ? w.x : e % 4 == 1 ? w.y : e % 4 == 2 ? w.z : w.w) +
-                 c * acc[e / 2][2 * o + (e & 1)];
+          v[e] = __float_as_uint(__uint_as_float(e % 4 == 0 ? w.x : e % 4 == 1 ? w.y : e % 4 == 2 ? w.z : w.w) +
+                                 c * acc[e / 2][2 * o + (e & 1)]);
         }
-        if (VEC || p.y_wide) {
-          *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
-          if (n_mine > 4) *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < n_mine) to[e] = v[e];
-        }
+        store16<T>(to, n_mine, VEC ? 16 : p.y_unit, v);
+        store16<T>(to + 4, n_mine - 4, VEC ? 16 : p.y_unit, v + 4);
       } else {
         const uint32_t in[4] = {now.y[o][0].x, now.y[o][0].y, now.y[o][0].z, now.y[o][0].w};
         uint32_t w[4];
@@ -657,13 +678,7 @@ __global__ void __launch_bounds__(kAdapterThreads, 2) adapter_kernel(const __gri
           }
           w[j] = pack2(y0 + c * acc[j][2 * o], y1 + c * acc[j][2 * o + 1], T());
         }
-        if (VEC || p.y_wide) {
-          *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < n_mine) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
-        }
+        store16<T>(to, n_mine, VEC ? 16 : p.y_unit, w);
       }
     }
   };

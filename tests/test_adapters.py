@@ -222,7 +222,9 @@ def test_adapters(dtype, name, width, outs, rank):
 @pytest.mark.parametrize("name", ["ragged", "prompts"])
 @pytest.mark.parametrize("width,outs,rank,x_pad,y_pad,shift", [
     (1001, [99, 7], 16, 0, 0, 0), (64, [5, 1, 1, 3], 8, 3, 1, 1), (256, [64, 65], 64, 0, 8, 0), (255, [64, 64], 32, 0, 0, 0),
-    (256, [128], 16, 8, 16, 8), (256, [128], 16, 8, 16, 3), (1, [1], 128, 0, 0, 0), (7, [33], 32, 1, 0, 0)])
+    (256, [128], 16, 8, 16, 8), (256, [128], 16, 8, 16, 3), (1, [1], 128, 0, 0, 0), (7, [33], 32, 1, 0, 0),
+    (1002, [34, 6], 16, 0, 0, 0), (1004, [36, 4], 8, 0, 4, 0), (100, [36, 52], 64, 4, 8, 4), (130, [64, 2], 32, 6, 2, 2),
+    (256, [60], 16, 0, 4, 0), (252, [64], 16, 4, 0, 0)])
 def test_odd_sizes_strides_and_alignment(dtype, name, width, outs, rank, x_pad, y_pad, shift):
     lens, ids = CASES[name]
     s = Step(lens, ids, width, outs, rank, 3, dtype, before=1, behind=1, x_pad=x_pad, y_pad=y_pad, shift=shift)

@@ -797,8 +797,8 @@ typedef struct {
  *                 DEVICE_TIMEOUT, cleared by the caller ahead of the first call; the rest need not be. Two calls
  *                 that can overlap on the GPU need workspaces of their own.
  * Rows of no request are left as they were. Results do not depend on the order of execution. Rows and parts of
- * 16-byte multiples on 16-byte boundaries move 16 bytes a lane, others 8, 4 or an element. Enqueued on cuda_stream. Errors:
- * INVALID_ARG, WORKSPACE_TOO_SMALL, UNSUPPORTED (dtype, rank, parts, sizes; more than
+ * 16-byte multiples on 16-byte boundaries move 16 bytes a lane, others 8, 4 or an element. Enqueued on
+ * cuda_stream. Errors: INVALID_ARG, WORKSPACE_TOO_SMALL, UNSUPPORTED (dtype, rank, parts, sizes; more than
  * DECODE_ATTN_MAX_ADAPTERS adapters or DECODE_ATTN_MAX_PAGED_BATCH requests), CUDA. */
 typedef struct {
   const void* x;

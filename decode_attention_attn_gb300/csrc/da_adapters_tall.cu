@@ -475,20 +475,25 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         }
       }
       __syncwarp();
+      float s = 1.f;
       if constexpr (std::is_same<T, __half>::value) {
         // f16 ends at 65504: by a power of two to below 2^8, and back in the product
         float most = 0.f;
 #pragma unroll
         for (int k = 0; k < R; ++k) most = fmaxf(most, fabsf(v[k]));
-        const float s = low_rank_scale(most);
+        s = low_rank_scale(most);
 #pragma unroll
         for (int k = 0; k < R; ++k) v[k] *= s;
-        sh.scale[w.seg & 3][row] = s;
       }
       uint32_t o[V_COLS] = {};
 #pragma unroll
       for (int k = 0; k < R / 2; ++k) split_pair<T>(v[2 * k], v[2 * k + 1], o[k], o[RB / 2 + k]);
       wait(&sh.v_empty[vb], vpar ^ 1);
+      // The scale's place was segment seg - 4's, and is free only now: seg - 2's products are done, the last of them two
+      // blocks or more behind seg - 4's last one, and a block's product waits (d_empty) until the block two before it
+      // has been finished. Before the wait seg - 3's alone are known to be, which may be a single block, with seg - 4's
+      // last one still waiting for its y.
+      if constexpr (std::is_same<T, __half>::value) sh.scale[w.seg & 3][row] = s;
       tc_fence_after();
 #pragma unroll
       for (uint32_t c = 0; c < V_COLS; c += 32) tmem_st32(lane_addr + vb * V_COLS + c, o + c);

@@ -466,3 +466,36 @@ def test_streams_graphs_and_repeats():
         s.of = [a for n, a in zip([3, 1, 20, 6], ids) for _ in range(n)]
         graph.replay()
         s.check(held)
+
+
+LONG_RUNS = [   # width, outs, rank, rows: what a CTA of 152 has, of blocks of 128 columns, of segments (blocks of one
+                # tile and part) and of units of the contraction (64 of a tile's width)
+    (64, [128, 64, 128, 64], 8, 40000),     # 7.5 blocks, as many segments; 1.9 units, 1 a tile
+    (192, [128, 64, 64, 64], 64, 26000),    # 5.1 blocks, as many segments; 3.8 units, 3 a tile
+    (1000, [2048, 128, 128], 64, 6400),     # 7.1 blocks, 1.2 segments; 6.3 units, 16 a tile
+    (520, [64], 128, 100000),               # 4.7 blocks, as many segments; 42.5 units, 9 a tile
+    (328, [136, 1000], 32, 16000),          # 7.4 blocks, 1.5 segments; 4.4 units, 6 a tile
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("width,outs,rank,rows", LONG_RUNS)
+def test_long_runs_of_the_tensor_core_launches(dtype, width, outs, rank, rows):
+    """A CTA's run goes through its rings, accumulators and operands several times, over tiles and parts whose
+    numbers are of other sizes (f16: with powers of two of their own), single blocks among them."""
+    lens, sizes = [], [1000, 77, 640, 129, 64, 333, 1500, 63, 0, 200]
+    while sum(lens) < rows:
+        lens.append(sizes[len(lens) % len(sizes)])
+    s = Step(lens, [i % 4 - (i % 7 == 6) for i in range(len(lens))], width, outs, rank, 3, dtype, before=5, behind=9)
+    s.x.mul_(2.0 ** (torch.arange(s.x.shape[0], device="cuda") * 7 % 9 - 4)[:, None].to(s.t))
+    for k in range(len(outs)):
+        s.a[:, k * rank:(k + 1) * rank] *= 2.0 ** (3 * (k % 3) - 3)
+    before = torch.randn_like(s.y)
+    out = before.clone()
+    s.check(s.apply(out, long=True), before)
+    m = s.member.cuda()
+    for _ in range(3):
+        assert torch.equal(s.apply(long=True)[m], out[m])
+    s.apply(s.y, long=True)
+    assert torch.equal(s.y[m], out[m])

@@ -16,7 +16,8 @@ namespace {
 
 constexpr int kPageThreads = 512;
 constexpr int kPageRows = 4;        // rows (or entries) a thread has in flight
-static_assert(DECODE_ATTN_MAX_PAGED_BATCH * 12 + 1024 <= kSmemLimit, "the lengths fit shared memory");
+constexpr size_t kMostSmem = 4 * (3 * (size_t)DECODE_ATTN_MAX_PAGED_BATCH + 1);   // of any plan's call
+static_assert(kMostSmem + 1024 <= kSmemLimit, "the lengths fit shared memory");
 
 struct PageParams {
   int32_t* pool;                // head, then the stack
@@ -312,9 +313,11 @@ int launch(const da_plan& pl, const PageParams& p, const void* fn, long long ite
   cudaError_t e = cudaSuccess;
   if (pl.prob.validate)
     e = cudaMemsetAsync(static_cast<char*>(workspace) + pl.off_status, 0, 4, stream);
-  if (e == cudaSuccess && smem > 48 * 1024)
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return cuda_fail(e, "preparing the page kernel");
+  if (smem > 40 * 1024) {   // to the most that any call takes: the limit is the kernel's, which other threads launch too
+    const int rc = raise_smem(fn, kMostSmem, 0);
+    if (rc != DA_OK) return rc;
+  }
   const long long per = (long long)kPageThreads * kPageRows;
   const int grid = (int)std::max(1ll, std::min((items + per - 1) / per, 2ll * pl.num_sms));
   void* args[1] = {const_cast<PageParams*>(&p)};

@@ -1,5 +1,10 @@
 """Pages and slots from the sequences' lengths: refusals on the CPU, results on the GPU against a model in
 plain integers."""
+import ctypes
+import os
+import shutil
+import subprocess
+
 import pytest
 import torch
 
@@ -405,3 +410,35 @@ def test_validate_returns_the_findings():
     pages.reserve(pool, table, _i32([0, 8, 16]), lens, 16)
     assert _code(pages.reserve, pool, table, _i32([0, 8, 16]), _i32([8, 8]), 16) == -10
     assert _code(pages.release, pool, table, _i32([8, 8]), _i32([0, 9])) == -7
+
+
+@pytest.mark.gpu
+def test_plans_of_different_batches_from_threads_at_once(tmp_path):
+    """Their launches take different amounts of shared memory, of which one call must not withhold another's."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    subprocess.run([cxx, "-std=c++17", "-O2", "-Wall", "-Werror", "-shared", "-fPIC", "-pthread",
+                    os.path.join(os.path.dirname(__file__), "c_call_threads.cpp"), "-o", str(tmp_path / "threads.so")], check=True)
+    call = ctypes.CDLL(str(tmp_path / "threads.so")).call_at_once
+    entry = {n: ctypes.cast(getattr(binding.lib(), "decode_attn_pages_" + n), ctypes.c_void_p).value for n in ("reserve", "release")}
+    for name in ("reserve", "release"):
+        fns, handles, args, keep = [], [], [], []
+        for batch in (16384, 8300, 6500, 9):
+            pages = binding.PageTables(_problem(batch, 16, 2, 64))
+            stream = torch.cuda.Stream()
+            pool, table = pages.new_pool(), torch.full((batch, 2), -1, dtype=torch.int32, device="cuda")
+            offsets, lens, then = (torch.zeros(batch + k, dtype=torch.int32, device="cuda") for k in (1, 0, 0))
+            at = stream.cuda_stream
+            a = (binding.da_pages_reserve_args(pool.data_ptr(), table.data_ptr(), offsets.data_ptr(), lens.data_ptr(), 0,
+                                               then.data_ptr(), None, None, None, 0, at) if name == "reserve" else
+                 binding.da_pages_release_args(pool.data_ptr(), table.data_ptr(), then.data_ptr(), lens.data_ptr(), None, 0, at))
+            keep.append((pages, stream, pool, table, offsets, lens, then, a))
+            fns.append(entry[name])
+            handles.append(pages.plan if isinstance(pages.plan, int) else pages.plan.value)
+            args.append(ctypes.addressof(a))
+        torch.cuda.synchronize()
+        many = ctypes.c_void_p * 4
+        assert call(4, 3000, many(*fns), many(*handles), many(*args)) == 0, name
+        torch.cuda.synchronize()
+        assert all(k[2][0] == 64 and not k[6].any() for k in keep)

@@ -1184,8 +1184,8 @@ class PageTables(_Workspace):
         """Pages for a step of `rows` rows: sequence b holds ctx_lens[b] tokens and gets the rows row_offsets[b]
         to row_offsets[b + 1]. Returns (seq_lens, slots, positions): the lengths then (ctx_lens itself: in
         place), each row's cache row (-1: none) and position; allocated when None. Where the pool has too few
-        pages nothing is taken, every slot is -1 and pool[1] says how many
-        were missing."""
+        pages nothing is taken, every slot is -1 and pool[1] says how many were missing; nor where row_offsets
+        fall anywhere, which is a bad length."""
         index, batch = self._checked(pool, block_table, ctx_lens), self._batch
         _int32("row_offsets", row_offsets, batch + 1)
         if rows < 0:

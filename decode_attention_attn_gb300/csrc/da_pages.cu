@@ -145,15 +145,20 @@ __global__ void __launch_bounds__(kPageThreads) reserve_kernel(const __grid_cons
   for (int b = tid; b < p.batch; b += kPageThreads) s_ctx[b] = p.ctx_lens[b];
   __syncthreads();
   int found = 0;
+  bool falls = false;
   for (int b = tid; b < p.batch; b += kPageThreads) {
     const int t = max(s_off[b + 1] - s_off[b], 0), ctx = s_ctx[b];
+    falls |= s_off[b + 1] < s_off[b];
     if (ctx < 0 || (long long)ctx + t > p.capacity) found = kStatusBadSeqLen;
     s_before[b] = growth(p, ctx, t).need;
   }
-  __syncthreads();
+  // Where offsets fall, rows are two sequences' at once, and pages would be counted for both that one of them enters:
+  // no row is anybody's then, and nothing is taken.
+  const bool in_order = !__syncthreads_or(falls);
   const int total = prefix_sums(s_before, p.batch, sh);
-  const bool fits = total <= free;
-  if (blockIdx.x == 0) find(p, found | (!fits && tid == 0 ? kStatusNoPages : 0));
+  const bool fits = in_order && total <= free;
+  if (blockIdx.x == 0)
+    find(p, found | (falls ? kStatusBadSeqLen : 0) | (in_order && !fits && tid == 0 ? kStatusNoPages : 0));
   found = 0;
 
   const int warps = gridDim.x * (kPageThreads / 32), warp = blockIdx.x * (kPageThreads / 32) + (tid >> 5);
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(kPageThreads) reserve_kernel(const __grid_cons
       to[k] = -1;
       in_page[k] = pos[k] = 0;
       const int r = (int)min(rr + 32 * k, (long long)INT_MAX);
-      if (r >= r1 || r < first_row || r >= end_row) continue;
+      if (r >= r1 || r < first_row || r >= end_row || !in_order) continue;
       if (!(s_off[b] <= r && r < s_off[b + 1])) b = last_at_or_below(s_off, s_off[b] <= r ? b : 0, p.batch, r);
       const long long t = (long long)s_ctx[b] + (r - s_off[b]);
       pos[k] = (int)min(t, (long long)INT_MAX);
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(kPageThreads) reserve_kernel(const __grid_cons
                            : clamp_len(s_ctx[i], p.capacity);
   if (tid == 0) {
     p.pool[0] = fits ? free - total : free;
-    p.pool[1] = fits ? 0 : total - free;
+    p.pool[1] = fits || !in_order ? 0 : total - free;
   }
 }
 

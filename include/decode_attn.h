@@ -659,8 +659,9 @@ int decode_attn_pages_init(const da_plan* plan, int32_t* pool, void* cuda_stream
  *   positions   nullable device int32 [rows]: t; 0 for rows of no sequence.
  * The pool has fewer pages than the step takes: it takes none. The tables and the stack stay as they are, every
  * slot is -1, seq_lens[b] = ctx_lens[b], pool[1] says how many pages were missing (0 otherwise), and NO_PAGES
- * is recorded. A length that is negative or would pass the capacity is recorded (BAD_SEQ_LEN) and clamped, as
- * are entries outside the pool (BAD_BLOCK_TABLE; one of the stack is entered as -1).
+ * is recorded. Nor does it where row_offsets fall anywhere up to `rows`: every slot is -1 and every position 0 then,
+ * pool[1] is 0, and BAD_SEQ_LEN is recorded. A length that is negative or would pass the capacity is recorded
+ * (BAD_SEQ_LEN) and clamped, as are entries outside the pool (BAD_BLOCK_TABLE; one of the stack is entered as -1).
  *   workspace   nullable, the plan's workspace: takes the findings (decode_attn_check_status); required when
  *               the problem's validate is set: the call then synchronises and returns them.
  * Enqueued on cuda_stream. Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA; with validate the

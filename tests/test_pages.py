@@ -442,3 +442,24 @@ def test_plans_of_different_batches_from_threads_at_once(tmp_path):
         assert call(4, 3000, many(*fns), many(*handles), many(*args)) == 0, name
         torch.cuda.synchronize()
         assert all(k[2][0] == 64 and not k[6].any() for k in keep)
+
+
+@pytest.mark.gpu
+def test_offsets_that_fall_take_nothing():
+    """Rows of two sequences at once: no pages leave the stack, nothing is entered, and the finding says so."""
+    m = Model(5, 8, 10, 60)
+    pages = binding.PageTables(_problem(5, 8, 10, 60), findings=True)
+    first = m.reserve(_offsets([20, 8, 0, 31, 5]), m.lens, 64)[0]
+    pool, table = m.tensors()
+    for offsets, rows in (([0, 30, 10, 40, 50, 60], 60), ([0, 9, 20, 21, 22, 21], 30), ([40, 0, 1, 2, 3, 4], 64)):
+        got = pages.reserve(pool, table, _i32(offsets), _i32(first), rows)
+        assert [x.tolist() for x in got] == [first, [-1] * rows, [0] * rows]
+        m.check(pool, table)
+        assert _code(pages.check_status) == -7
+    # ones that fall past the rows there are do not: no row counts there
+    offsets = [0, 3, 40, 20, 30, 25]
+    got = pages.reserve(pool, table, _i32(offsets), _i32(first), 12)
+    want = m.reserve(offsets, first, 12)
+    assert [x.tolist() for x in got] == list(want[:3]) and want[0][1] == first[1] + 9
+    m.check(pool, table)
+    pages.check_status()

@@ -94,27 +94,51 @@ __device__ __forceinline__ void mma16x8(float* c, const uint32_t* a, uint32_t b0
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// An fp32 number as two tf32 ones: what is left is 2^-22 of it (nothing of an infinity or NaN).
+// An fp32 number as two tf32 ones: what is left is 2^-22 of it. An infinity, or what rounds to one, has no such parts
+// unless CAREFUL: then an infinity or NaN is its first part alone, and tf32's largest number the first part of what is
+// larger.
 __device__ __forceinline__ uint32_t tf32(float x) {
   uint32_t u;
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(u) : "f"(x));
   return u;
 }
+template <bool CAREFUL>
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = tf32(x);
-  const float h = __uint_as_float(hi);
-  lo = fabsf(h) <= 3.4028235e38f ? tf32(x - h) : 0u;
+  constexpr float kMost = 3.40116213421e38f;   // (2 - 2^-10) 2^127
+  const bool finite = !CAREFUL || fabsf(x) <= 3.4028235e38f;
+  hi = tf32(CAREFUL && finite ? fminf(fmaxf(x, -kMost), kMost) : x);
+  lo = finite ? tf32(x - __uint_as_float(hi)) : 0u;
 }
 // c += a b of fp32 numbers in two tf32 parts: three of the four products (the last is 2^-22 of the first). They are
-// added up from zero and then to c, as the instruction cuts off what it adds to a larger sum.
+// added up from zero and then to c, as the instruction cuts off what it adds to a larger sum. An infinite part times
+// the other number's rest is no share of the product (0 times it is NaN, a rest may have either sign): CAREFUL takes
+// the large products alone where the small ones are not finite.
+// The hot loops are not careful: a factor that is not finite leaves them a sum that is not either, and such sums are
+// formed again, carefully (5 prompts of up to 300 rows, 1001 to 1076: 15.3 us; careful throughout 16.1; 700 rows of
+// rank 128, 2048 wide to three parts, 90 and 129).
+template <bool CAREFUL>
 __device__ __forceinline__ void add_products(float* c, const uint32_t* hi, const uint32_t* lo, const uint32_t* bh,
                                              const uint32_t* bl) {
   float t[4] = {0.f, 0.f, 0.f, 0.f};
   mma16x8<float>(t, lo, bh[0], bh[1]);
   mma16x8<float>(t, hi, bl[0], bl[1]);
+  if constexpr (CAREFUL) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = fabsf(t[e]) <= 3.4028235e38f ? t[e] : 0.f;
+  }
   mma16x8<float>(t, hi, bh[0], bh[1]);
 #pragma unroll
   for (int e = 0; e < 4; ++e) c[e] += t[e];
+}
+// Whether one of the warp's sums is not finite (0 times it is not 0).
+template <int N>
+__device__ __forceinline__ bool any_not_finite(const float (*c)[4]) {
+  float z = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z = fmaf(c[j][e], 0.f, z);
+  return __any_sync(0xffffffffu, z != 0.f);
 }
 // Two fp32 numbers as two pairs of T: what is left is 2^-18 (bf16) or 2^-24 (f16) of them.
 template <typename T>
@@ -411,45 +435,54 @@ __global__ void __launch_bounds__(kAdapterThreads, 2) adapter_kernel(const __gri
   // ---- contraction: low[m][n] = sum over k of x[m][k] a[n][k]
   {
     const int kg = warp / p.n_groups, ng = warp % p.n_groups;
-    float acc[NT][4] = {};
+    float acc[NT][4];
     // (what places behind the tile's rows and low-rank columns hold is never looked at: they read others')
     const T* xr[2];
 #pragma unroll
     for (int o = 0; o < 2; ++o) xr[o] = static_cast<const T*>(p.x) + s_from[8 * o + g] * p.x_rs;
     const int n0 = ng * NT * 8 + g;
-#pragma unroll 2
-    for (int kb = k0 + kg; kb < k1; kb += k_groups) {
-      const int k = kb * KB + q * V, left = p.width - k;
-      uint4 xv[2], av[NT];
+    auto contract = [&](auto careful) {
+      constexpr bool CAREFUL = decltype(careful)::value;
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        av[j] = load16<T>(a + (long long)min(n0 + j * 8, low - 1) * p.width, k, left, VEC ? 16 : p.x_unit);
+      for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll(CAREFUL ? 1 : 2)
+      for (int kb = k0 + kg; kb < k1; kb += k_groups) {
+        const int k = kb * KB + q * V, left = p.width - k;
+        uint4 xv[2], av[NT];
 #pragma unroll
-      for (int o = 0; o < 2; ++o) xv[o] = load16<T>(xr[o], k, left, VEC ? 16 : p.x_unit);
+        for (int j = 0; j < NT; ++j)
+          av[j] = load16<T>(a + (long long)min(n0 + j * 8, low - 1) * p.width, k, left, VEC ? 16 : p.x_unit);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if constexpr (!F32) {
-          const uint32_t f[4] = {s ? xv[0].z : xv[0].x, s ? xv[1].z : xv[1].x, s ? xv[0].w : xv[0].y,
-                                 s ? xv[1].w : xv[1].y};
+        for (int o = 0; o < 2; ++o) xv[o] = load16<T>(xr[o], k, left, VEC ? 16 : p.x_unit);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma16x8<T>(acc[j], f, s ? av[j].z : av[j].x, s ? av[j].w : av[j].y);
-        } else {
-          // each factor as two tf32 numbers
-          uint32_t ah[NT][2], al[NT][2];
+        for (int s = 0; s < 2; ++s) {
+          if constexpr (!F32) {
+            const uint32_t f[4] = {s ? xv[0].z : xv[0].x, s ? xv[1].z : xv[1].x, s ? xv[0].w : xv[0].y,
+                                   s ? xv[1].w : xv[1].y};
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            split_tf32(__uint_as_float(s ? av[j].z : av[j].x), ah[j][0], al[j][0]);
-            split_tf32(__uint_as_float(s ? av[j].w : av[j].y), ah[j][1], al[j][1]);
+            for (int j = 0; j < NT; ++j) mma16x8<T>(acc[j], f, s ? av[j].z : av[j].x, s ? av[j].w : av[j].y);
+          } else {
+            // each factor as two tf32 numbers
+            uint32_t ah[NT][2], al[NT][2];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              split_tf32<CAREFUL>(__uint_as_float(s ? av[j].z : av[j].x), ah[j][0], al[j][0]);
+              split_tf32<CAREFUL>(__uint_as_float(s ? av[j].w : av[j].y), ah[j][1], al[j][1]);
+            }
+            uint32_t hi[4], lo[4];
+            split_tf32<CAREFUL>(__uint_as_float(s ? xv[0].z : xv[0].x), hi[0], lo[0]);
+            split_tf32<CAREFUL>(__uint_as_float(s ? xv[1].z : xv[1].x), hi[1], lo[1]);
+            split_tf32<CAREFUL>(__uint_as_float(s ? xv[0].w : xv[0].y), hi[2], lo[2]);
+            split_tf32<CAREFUL>(__uint_as_float(s ? xv[1].w : xv[1].y), hi[3], lo[3]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) add_products<CAREFUL>(acc[j], hi, lo, ah[j], al[j]);
           }
-          uint32_t hi[4], lo[4];
-          split_tf32(__uint_as_float(s ? xv[0].z : xv[0].x), hi[0], lo[0]);
-          split_tf32(__uint_as_float(s ? xv[1].z : xv[1].x), hi[1], lo[1]);
-          split_tf32(__uint_as_float(s ? xv[0].w : xv[0].y), hi[2], lo[2]);
-          split_tf32(__uint_as_float(s ? xv[1].w : xv[1].y), hi[3], lo[3]);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) add_products(acc[j], hi, lo, ah[j], al[j]);
         }
       }
+    };
+    contract(std::false_type());
+    if constexpr (F32) {
+      if (any_not_finite<NT>(acc)) contract(std::true_type());
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -489,7 +522,7 @@ __global__ void __launch_bounds__(kAdapterThreads, 2) adapter_kernel(const __gri
     uint4 y[2][YV];
     uint32_t b[B_TOO ? BLK : 1][4][BW];
   };
-  auto load_b = [&](int col0, int end, int blk, uint32_t (*bw)[BW]) {
+  auto load_b = [&](const T* b, int col0, int end, int blk, uint32_t (*bw)[BW]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       // (columns behind the part's end read its last one's)
@@ -516,7 +549,7 @@ __global__ void __launch_bounds__(kAdapterThreads, 2) adapter_kernel(const __gri
     }
     if constexpr (B_TOO) {
 #pragma unroll
-      for (int blk = 0; blk < BLK; ++blk) load_b(col0, end, blk, c.b[blk]);
+      for (int blk = 0; blk < BLK; ++blk) load_b(b, col0, end, blk, c.b[blk]);
     }
   };
   Chunk chunk[AHEAD];
@@ -577,10 +610,10 @@ __global__ void __launch_bounds__(kAdapterThreads, 2) adapter_kernel(const __gri
     uint32_t hi[4], lo[4];
     if constexpr (F32) {
       const int k = R < 16 ? lq * 2 : (step >> 1) * 16 + lq * 4 + (step & 1) * 2;
-      split_tf32(v0[k], hi[0], lo[0]);
-      split_tf32(v1[k], hi[1], lo[1]);
-      split_tf32(v0[k + 1], hi[2], lo[2]);
-      split_tf32(v1[k + 1], hi[3], lo[3]);
+      split_tf32<true>(v0[k], hi[0], lo[0]);
+      split_tf32<true>(v1[k], hi[1], lo[1]);
+      split_tf32<true>(v0[k + 1], hi[2], lo[2]);
+      split_tf32<true>(v1[k + 1], hi[3], lo[3]);
     } else {
       float c0 = 1.f, c1 = 1.f;
       if constexpr (std::is_same<T, __half>::value) {
@@ -611,37 +644,50 @@ __global__ void __launch_bounds__(kAdapterThreads, 2) adapter_kernel(const __gri
   auto finish = [&](int h, const Chunk& now) {
     const int s = part_of(h), col0 = p.starts[s] + (h - p.chunks[s]) * 32, end = p.starts[s + 1];
     const int mine = col0 + q * 8, n_mine = min(end - mine, 8);   // (none there: below 1)
-    float acc[4][4] = {};
+    float acc[4][4];
     const uint4* frag = s_frag + (size_t)(s - part0) * STEPS * 64 + lane;
+    auto expand = [&](auto careful) {
+      constexpr bool CAREFUL = decltype(careful)::value;
+      const T* weights = b;
+      const uint4* operand = frag;
+      // (loaded again, then: kept from the first time they would fill the registers)
+      if constexpr (CAREFUL) asm volatile("" : "+l"(weights), "+l"(operand));
 #pragma unroll
-    for (int blk = 0; blk < BLK; ++blk) {
-      uint32_t bw[4][BW];
-      if constexpr (!B_TOO) load_b(col0, end, blk, bw);
-      else memcpy(bw, now.b[blk], sizeof bw);
+      for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 #pragma unroll
-      for (int t = 0; t < PER; ++t) {
-        uint32_t bh[4][2], bl[4][2];
+      for (int blk = 0; blk < BLK; ++blk) {
+        uint32_t bw[4][BW];
+        if constexpr (!B_TOO) load_b(weights, col0, end, blk, bw);
+        else memcpy(bw, now.b[blk], sizeof bw);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int t = 0; t < PER; ++t) {
+          uint32_t bh[4][2], bl[4][2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t w = 2 * t + e < BW ? bw[j][2 * t + e] : 0u;
-            if constexpr (F32) split_tf32(__uint_as_float(w), bh[j][e], bl[j][e]);
-            else bh[j][e] = w;
-          }
-        const uint4* f = frag + (blk * PER + t) * 64;
-        const uint4 fh = f[0], fl = f[32];
-        const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (F32) {
-            add_products(acc[j], hi, lo, bh[j], bl[j]);
-          } else {
-            mma16x8<T>(acc[j], lo, bh[j][0], bh[j][1]);
-            mma16x8<T>(acc[j], hi, bh[j][0], bh[j][1]);
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t w = 2 * t + e < BW ? bw[j][2 * t + e] : 0u;
+              if constexpr (F32) split_tf32<CAREFUL>(__uint_as_float(w), bh[j][e], bl[j][e]);
+              else bh[j][e] = w;
+            }
+          const uint4* f = operand + (blk * PER + t) * 64;
+          const uint4 fh = f[0], fl = f[32];
+          const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (F32) {
+              add_products<CAREFUL>(acc[j], hi, lo, bh[j], bl[j]);
+            } else {
+              mma16x8<T>(acc[j], lo, bh[j][0], bh[j][1]);
+              mma16x8<T>(acc[j], hi, bh[j][0], bh[j][1]);
+            }
           }
         }
       }
+    };
+    expand(std::false_type());
+    if constexpr (F32) {
+      if (any_not_finite<4>(acc)) expand(std::true_type());
     }
 #pragma unroll
     for (int o = 0; o < 2; ++o) {

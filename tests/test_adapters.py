@@ -499,3 +499,31 @@ def test_long_runs_of_the_tensor_core_launches(dtype, width, outs, rank, rows):
         assert torch.equal(s.apply(long=True)[m], out[m])
     s.apply(s.y, long=True)
     assert torch.equal(s.y[m], out[m])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("where", ["x", "a", "b", "far"])
+@pytest.mark.parametrize("width,outs,rank", [(64, [40, 24], 16), (257, [33], 8), (128, [64], 128)])
+def test_infinities_in_fp32(width, outs, rank, where):
+    """An infinity times a number that is exact in a part of it, or whose rest has the other sign, is an infinity."""
+    s = Step([3, 20, 1], [0, 1, 0], width, outs, rank, 2, "f32")
+    s.x.abs_()
+    s.a.abs_()
+    s.b.abs_().add_(2.0 ** -10)
+    s.x[:, ::2] = 1.0                                   # (nothing left behind its first part)
+    s.b[:, ::3] = 0.5
+    for v in (float("inf"), -float("inf")):
+        if where == "x":
+            s.x[1, 5], s.x[7, 6] = v, -v
+        elif where == "a":
+            s.a[0, 3, 2], s.a[1, 1, 5] = v, -v
+        elif where == "b":
+            s.b[0, 4, 1], s.b[1, 7, rank - 1] = v, -v
+        else:                                           # 2^-14 below the largest number there is, and small weights
+            s.x[1, 5], s.a[:] = 3.4027e38 if v > 0 else -3.4027e38, 2.0 ** -100
+        got, want = s.apply(), s.want()[0].float()
+        assert not want.isnan().any() and (where == "far" or want.isinf().any())
+        assert torch.equal(got.isinf(), want.isinf()) and torch.equal(got.sign()[want.isinf()], want.sign()[want.isinf()])
+        assert not got.isnan().any()
+        if where == "far":
+            s.check(got)

@@ -158,9 +158,13 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
   lo = pack2(fabsf(hx) <= 3.4028235e38f ? x - hx : 0.f, fabsf(hy) <= 3.4028235e38f ? y - hy : 0.f, T());
 }
 
-// The power of two that takes numbers of up to `most` below 2^8 (1: there is nothing finite to go by).
+// The larger of `most` and |v|, if v is finite.
+__device__ __forceinline__ float most_finite(float most, float v) {
+  return fabsf(v) <= 3.4028235e38f ? fmaxf(most, fabsf(v)) : most;
+}
+// The power of two that takes finite numbers of up to `most` below 2^8 (1: there are none but zeros).
 __device__ __forceinline__ float low_rank_scale(float most) {
-  const int e = most > 0.f && most <= 3.4028235e38f ? (int)(__float_as_uint(most) >> 23) - 127 - 7 : 0;
+  const int e = most > 0.f ? (int)(__float_as_uint(most) >> 23) - 127 - 7 : 0;
   return __uint_as_float((uint32_t)(127 - min(max(e, -120), 120)) << 23);
 }
 
@@ -594,7 +598,7 @@ __global__ void __launch_bounds__(kAdapterThreads, 2) adapter_kernel(const __gri
     for (int i = warp; i < M * (part1 - part0); i += kAdapterWarps) {
       const int m = i / (part1 - part0), s = part0 + i - m * (part1 - part0);
       float most = 0.f;
-      for (int n = lane; n < R; n += 32) most = fmaxf(most, fabsf(s_sum[(size_t)m * pitch + s * R + n]));
+      for (int n = lane; n < R; n += 32) most = most_finite(most, s_sum[(size_t)m * pitch + s * R + n]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
       if (lane == 0) s_scale[m * kMaxParts + s] = low_rank_scale(most);

@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         // f16 ends at 65504: by a power of two to below 2^8, and back in the product
         float most = 0.f;
 #pragma unroll
-        for (int k = 0; k < R; ++k) most = fmaxf(most, fabsf(v[k]));
+        for (int k = 0; k < R; ++k) most = most_finite(most, v[k]);
         s = low_rank_scale(most);
 #pragma unroll
         for (int k = 0; k < R; ++k) v[k] *= s;

@@ -527,3 +527,25 @@ def test_infinities_in_fp32(width, outs, rank, where):
         assert not got.isnan().any()
         if where == "far":
             s.check(got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("long", [False, True])
+def test_an_infinite_low_rank_number_beside_large_ones(dtype, long):
+    """Its columns are infinite, whatever the row's others are (which in f16 pass the operand's range unless they are
+    taken by a power of two)."""
+    s = Step([1100, 60] if long else [9, 3], [0, 1], 256, [64, 32], 16, 2, dtype, x_gain=1000.0)
+    n = 1100 if long else 9
+    s.b[:] *= 2.0 ** -9
+    s.a[0] *= 512                                       # numbers up to 10^6
+    s.x[:n, 7] = 1.0
+    s.a[0, ::16, 7] = float("inf")                      # each part's first one
+    s.b[0, :, 0] = s.b[0, :, 0].abs() + 0.5
+    s.b[0, ::2, 0] *= -1
+    got = s.apply(long=long)
+    sign = torch.tensor([-1.0, 1.0], device="cuda").repeat(48)
+    assert torch.equal(got[:n].float(), (sign * float("inf")).expand(n, 96))
+    want, bound = s.want()
+    assert torch.equal(want[:n].float(), got[:n].float())
+    assert ((got.double() - want).abs() <= bound)[n:].all()

@@ -19,7 +19,8 @@
 namespace da {
 
 constexpr float kE4M3Max = 448.f;
-constexpr float kFarScale = 5.421010862e-20f;    // 2^-64
+constexpr float kFarSum = 1.2676506e30f;         // 2^100: larger sums of squares are formed again,
+constexpr float kFarScale = 8.2718061e-25f;      // 2^-80: of h taken by that
 constexpr float kLeastScale = 1.17549435e-38f;   // 2^-126: of a row of zeros; no scale is subnormal
 
 struct NormParams {
@@ -183,20 +184,36 @@ struct Divider {
   }
 };
 
-// The sum of v over a row's threads, by its block or `lanes` lanes.
-template <bool BLOCK>
-__device__ __forceinline__ float row_sum(float v, int lanes, float* s_part) {
+// The sum (MOST: the largest) of v over a row's threads, by its block or `lanes` lanes. Of rows that hardly ever come,
+// but what it is made of is felt in all: with a loop over the warps' values in place of the shuffles (STRAIGHT), what
+// is loaded ahead is waited for too early (8192 rows of 6464 bf16 with residual and groups: 109 us in place of 85);
+// where several units a thread are not loaded ahead, the loop leaves more registers (4000 rows of 4107 fp32: 79 us
+// without it, 49 with).
+template <bool BLOCK, bool MOST, bool STRAIGHT>
+__device__ __forceinline__ float over_row(float v, int lanes, float* s_part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     if (!BLOCK && o >= lanes) continue;
-    v += __shfl_xor_sync(0xffffffffu, v, o);
+    const float other = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MOST ? fmaxf(v, other) : v + other;
   }
   if constexpr (BLOCK) {
-    const int warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0) s_part[threadIdx.x >> 5] = v;
     __syncthreads();
     v = 0.f;
-    for (int w = 0; w < warps; ++w) v += s_part[w];
+    if constexpr (STRAIGHT) {
+      if (lane < warps) v = s_part[lane];
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, v, o);
+        v = MOST ? fmaxf(v, other) : v + other;
+      }
+      v = __shfl_sync(0xffffffffu, v, 0);
+    } else {
+#pragma unroll 1
+      for (int w = 0; w < warps; ++w) v = MOST ? fmaxf(v, s_part[w]) : v + s_part[w];
+    }
     __syncthreads();
   }
   return v;
@@ -228,7 +245,7 @@ __global__ void __launch_bounds__(kMostThreads<ITEMS, LAYOUT, BLOCK, RES>,
                                                                        : 1)
     norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int E = Unit<T>::E, V = E / 2;
-  constexpr bool VEC = LAYOUT != kScattered, SHIFTED = LAYOUT == kShifted;
+  constexpr bool VEC = LAYOUT != kScattered, SHIFTED = LAYOUT == kShifted, STRAIGHT = VEC || ITEMS == 1;
   static_assert(BLOCK || !SHIFTED, "");
   __shared__ float2 s_part[2][16];
   __shared__ float s_far[16];
@@ -398,15 +415,20 @@ __global__ void __launch_bounds__(kMostThreads<ITEMS, LAYOUT, BLOCK, RES>,
       sum2 = add2(sum2, part);
     }
     float sum = both(sum2).x + both(sum2).y;
-    // The same of h 2^-64, for rows whose squares pass fp32: a thread whose own do not adds what is left of them.
+    // Squares, and products with the weights, pass fp32 where h does not. A thread whose sum is that large takes its h by
+    // a power of two and sums again; where a row's is, the others add what is left of theirs.
     float far = sum * kFarScale * kFarScale;
-    if (!(sum <= 1.2676506e30f)) {   // 2^100
+    const bool taken = !(sum <= kFarSum);
+    if (taken) {
       const f32x2 c = f2_pack(kFarScale, kFarScale);
       f32x2 part = f2_pack(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) part = fma2(f2_mul(h[i][e], c), f2_mul(h[i][e], c), part);
+        for (int e = 0; e < E / 2; ++e) {
+          h[i][e] = f2_mul(h[i][e], c);
+          part = fma2(h[i][e], h[i][e], part);
+        }
       far = both(part).x + both(part).y;
     }
     // h becomes h (w + o)
@@ -486,10 +508,11 @@ __global__ void __launch_bounds__(kMostThreads<ITEMS, LAYOUT, BLOCK, RES>,
     }
     const float n = (float)p.n;
     float r = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(sum, n) + p.eps));
-    const bool passed = sum > 3.4028235e38f;
+    const bool passed = sum > kFarSum;
     if (BLOCK ? passed : __any_sync(0xffffffffu, passed)) {
-      far = row_sum<BLOCK>(far, lanes, s_far);
-      if (passed) r = __fdiv_rn(kFarScale, __fsqrt_rn(__fdiv_rn(far, n) + p.eps * kFarScale * kFarScale));
+      far = over_row<BLOCK, false, STRAIGHT>(far, lanes, s_far);
+      if (passed)
+        r = __fdiv_rn(taken ? 1.f : kFarScale, __fsqrt_rn(__fdiv_rn(far, n) + p.eps * kFarScale * kFarScale));
     }
     const f32x2 r2 = f2_pack(r, r);
 #pragma unroll
@@ -520,7 +543,17 @@ __global__ void __launch_bounds__(kMostThreads<ITEMS, LAYOUT, BLOCK, RES>,
     float scale = 1.f;
     if (p.scaling == DA_SCALE_TENSOR) scale = __ldg(p.scales);
     if (p.scaling == DA_SCALE_ROW) {
-      scale = fmaxf(__fdiv_rn(most * r, kE4M3Max), kLeastScale);
+      most *= r;
+      if (BLOCK ? passed : __any_sync(0xffffffffu, passed)) {
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) y = most_of(y, h[i][e]);
+        y = over_row<BLOCK, true, STRAIGHT>(y, lanes, s_far);
+        if (passed) most = y;   // (its threads' products are not alike: y itself)
+      }
+      scale = fmaxf(__fdiv_rn(most, kE4M3Max), kLeastScale);
       if (me == 0 && live) p.scales[item] = scale;
     }
     Divider over(scale, p.scaling == DA_SCALE_TENSOR);

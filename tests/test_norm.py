@@ -326,3 +326,33 @@ def test_streams_and_graphs():
     # leaves that require a gradient are taken under no_grad
     with torch.no_grad():
         norm.apply(x.clone().requires_grad_(), w)
+
+
+FAR = [(5, 1, 24), (9, 2, 100), (40, 3, 128), (300, 1, 4096), (3, 1, 513), (700, 1, 4099), (2, 1, 16384)]   # every layout
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,heads,n", FAR)
+def test_products_with_the_weight_past_fp32(dtype, rows, heads, n):
+    """Rows near the type's end under weights above 1: the products pass fp32, what they are divided by too."""
+    x = _make(rows, heads, n, dtype)
+    x.clamp_(-4, 4)
+    x[::2] *= 2.0 ** 125                                # up to 2^127
+    x[1::4, :, ::7] *= 2.0 ** 60                        # squares past fp32 beside small numbers
+    w = (1 + torch.rand(n, generator=torch.Generator().manual_seed(n)) * 60).to(TORCH[dtype]).cuda()
+    norm = binding.RMSNorm(n, eps=1e-5)
+    want, _ = plain(x, w, None, 1e-5, 0.0)
+    near(norm.apply(x, w), want, "y")
+    near(norm.apply(x, w, residual=torch.zeros_like(x))[0], want, "with a residual")
+    given = torch.full((1,), 0.5, device="cuda")
+    for scaling, group in (("row", 0), ("group", 32), ("group", 128), ("tensor", 0)):
+        codes, scales, _ = norm.quantise(x, w, scaling=scaling, group=group or 128, scales=given if scaling == "tensor" else None)
+        size = n if scaling != "group" else group
+        parts = -(-n // size)
+        padded = torch.nn.functional.pad(want, (0, parts * size - n)).unflatten(-1, (parts, size))
+        most = padded.abs().amax(-1) / 448
+        if scaling != "tensor":
+            assert ((scales.view(most.shape).double() - most).abs() <= most * (Y_ERR + 2.0 ** -23)).all(), (scaling, group)
+        each = (scales if scaling == "tensor" else scales.view(most.shape)[..., None].expand(-1, -1, -1, size).flatten(-2)[..., :n])
+        check_codes(codes, each.expand(want.shape), want, (scaling, group))

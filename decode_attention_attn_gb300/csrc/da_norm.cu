@@ -129,6 +129,14 @@ int decode_attn_norm_apply(const da_norm_config* config, const da_norm_args* arg
                    aligned(a.weight, 32);
   const int sms = device_sms();
   if (sms <= 0) return DA_ERR_CUDA;
+  if (c.eps < kLeastEps && a.dtype != DA_F16) {   // (f16's squares are 2^-48 and more)
+    const int threads = std::min(kCarefulThreads, (c.n + 31) / 32 * 32);
+    const void* fn = a.dtype == DA_F32 ? careful_norm_kernel_f32() : careful_norm_kernel_bf16();
+    void* kargs[1] = {&p};
+    const cudaError_t e = cudaLaunchKernel(fn, dim3((unsigned)std::min(items, 8ll * sms)), dim3(threads), kargs, 0,
+                                           static_cast<cudaStream_t>(a.cuda_stream));
+    return e == cudaSuccess ? DA_OK : cuda_fail(e, "launching the norm kernel");
+  }
   // Rows that begin anywhere, but alike in every tensor (see NormLayout), where a row takes a block.
   const int V = E / 2;
   auto alike = [&](const void* at, long long rs, int bytes) {

@@ -415,8 +415,8 @@ __global__ void __launch_bounds__(kMostThreads<ITEMS, LAYOUT, BLOCK, RES>,
       sum2 = add2(sum2, part);
     }
     float sum = both(sum2).x + both(sum2).y;
-    // Squares, and products with the weights, pass fp32 where h does not. A thread whose sum is that large takes its h by
-    // a power of two and sums again; where a row's is, the others add what is left of theirs.
+    // Squares, and products with the weights, pass fp32 where h does not. A thread whose sum is that large takes its h
+    // by a power of two and sums again; where a row's is, the others add what is left of theirs.
     float far = sum * kFarScale * kFarScale;
     const bool taken = !(sum <= kFarSum);
     if (taken) {
@@ -661,6 +661,102 @@ __global__ void __launch_bounds__(kMostThreads<ITEMS, LAYOUT, BLOCK, RES>,
   }
 }
 
+// ---- an eps that small rows' squares do not reach --------------------------------------------------------------
+// Squares of numbers below 2^-63 vanish in fp32, and with them a row's size, unless eps covers it. Under an eps of less
+// than kLeastEps rows are taken by a power of two that brings their largest number to 1, which takes another reading of
+// them: a block a row, an element a lane, three times over the row (the last two from L1 or L2). Zero is the only such
+// eps that is met, and rarely, so this is not made fast: 8192 rows of 8192 bf16 with a residual and codes by rows 511
+// us, where the kernel above takes 77.
+constexpr float kLeastEps = 8.2718061e-25f;   // 2^-80
+constexpr int kCarefulThreads = 256;
+
+// The sum (MOST: the largest) of v over the block.
+template <bool MOST, typename V>
+__device__ __forceinline__ V over_block(V v, V* s_part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const V other = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MOST ? max(v, other) : v + other;
+  }
+  __syncthreads();   // (what was there has been read)
+  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = s_part[0];
+  for (int w = 1; w < (int)(blockDim.x >> 5); ++w) v = MOST ? max(v, s_part[w]) : v + s_part[w];
+  return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kCarefulThreads) careful_norm_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float s_most[kCarefulThreads / 32];
+  __shared__ double s_sum[kCarefulThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
+  for (long long item = blockIdx.x; item < p.items; item += gridDim.x) {
+    const long long row = item / p.heads, head = item - row * p.heads;
+    const T* x = static_cast<const T*>(p.x) + row * p.x_rs + head * p.x_hs;
+    const T* res = static_cast<const T*>(p.residual) + row * p.res_rs + head * p.res_hs;
+    T* tot = static_cast<T*>(p.total) + row * p.tot_rs + head * p.tot_hs;
+    T* out = static_cast<T*>(p.out) + row * p.out_rs + head * p.out_hs;
+    uint8_t* codes = p.codes + row * p.code_rs + head * p.code_hs;
+    auto sum_at = [&](int e) { return p.residual ? narrow<T>(widen(x[e]) + widen(res[e])) : x[e]; };
+    auto weight = [&](int e) {
+      if (!p.weight) return 1.f;
+      const float w = p.weight_f32 ? static_cast<const float*>(p.weight)[e] : widen(static_cast<const T*>(p.weight)[e]);
+      return w + p.offset;
+    };
+    float most = 0.f;
+    for (int e = tid; e < p.n; e += threads) {
+      const T h = sum_at(e);
+      if (p.total) tot[e] = h;
+      most = fmaxf(most, fabsf(widen(h)));
+    }
+    most = over_block<true>(most, s_most);
+    // 2^-e of the largest number's 2^e (of a subnormal one 2^126, which brings it above 2^-24; else 1)
+    const int bits = (int)(__float_as_uint(most) >> 23);
+    const int up = most > 0.f && bits < 255 ? min(127 - bits, 126) : 0;
+    const float c0 = __uint_as_float((uint32_t)(127 + up / 2) << 23);                // (2^-127 is not normal)
+    const float c1 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
+    auto taken = [&](int e) { return (p.total ? widen(tot[e]) : widen(sum_at(e))) * c0 * c1; };
+    double sum = 0.;
+    most = 0.f;
+    for (int e0 = tid; e0 < p.n; e0 += 16 * threads) {
+      float part = 0.f;
+      for (int k = 0; k < 16 && e0 + k * threads < p.n; ++k) {
+        const float h = taken(e0 + k * threads);
+        part = fmaf(h, h, part);
+        most = fmaxf(most, fabsf(h * weight(e0 + k * threads)));
+      }
+      sum += part;
+    }
+    sum = over_block<false>(sum, s_sum);
+    // (eps taken as the squares are, which fp32 may not hold; the quotient it does)
+    const double c = (double)c0 * c1;
+    const float r = (float)(1. / sqrt(sum / p.n + p.eps * c * c));
+    float scale = p.scaling == DA_SCALE_TENSOR ? __ldg(p.scales) : 1.f;
+    if (p.scaling == DA_SCALE_ROW) {
+      scale = fmaxf(__fdiv_rn(over_block<true>(most, s_most) * r, kE4M3Max), kLeastScale);
+      if (tid == 0) p.scales[item] = scale;
+    }
+    // A warp takes a group (or 128 elements); out may be x, whose elements only their own lane reads from here on.
+    const int size = p.scaling == DA_SCALE_GROUP ? p.group : 128;
+    for (int g = tid >> 5; g * size < p.n; g += threads >> 5) {
+      const int end = min(p.n, (g + 1) * size);
+      if (p.scaling == DA_SCALE_GROUP) {
+        float m = 0.f;
+        for (int e = g * size + lane; e < end; e += 32) m = fmaxf(m, fabsf(taken(e) * weight(e) * r));
+        scale = fmaxf(__fdiv_rn(warp_most(m), kE4M3Max), kLeastScale);
+        if (lane == 0) p.scales[item * p.groups + g] = scale;
+      }
+      for (int e = g * size + lane; e < end; e += 32) {
+        const float y = taken(e) * weight(e) * r;
+        if (p.out) out[e] = narrow<T>(y);
+        if (p.codes) codes[e] = (uint8_t)pack_e4m3x2(__fdiv_rn(y, scale), 0.f);
+      }
+    }
+    __syncthreads();   // (the next row's sums may go where this one's are read)
+  }
+}
+
 // The kernel of a layout: ITEMS units a thread (1, 2, 4 or, fp32, 8), a block a row or not.
 template <typename T, int LAYOUT, bool RES>
 const void* norm_kernel_of(int items, bool block) {
@@ -685,5 +781,7 @@ const void* norm_kernel_for(int layout, int items, bool block, bool residual) {
 const void* norm_kernel_f32(int layout, int items, bool block, bool residual);
 const void* norm_kernel_f16(int layout, int items, bool block, bool residual);
 const void* norm_kernel_bf16(int layout, int items, bool block, bool residual);
+const void* careful_norm_kernel_f32();
+const void* careful_norm_kernel_bf16();
 
 }  // namespace da

@@ -6,5 +6,6 @@ namespace da {
 const void* norm_kernel_bf16(int layout, int items, bool block, bool residual) {
   return norm_kernel_for<__nv_bfloat16>(layout, items, block, residual);
 }
+const void* careful_norm_kernel_bf16() { return reinterpret_cast<const void*>(&careful_norm_kernel<__nv_bfloat16>); }
 
 }  // namespace da

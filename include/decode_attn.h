@@ -721,7 +721,7 @@ typedef enum { DA_SCALE_NONE = 0, DA_SCALE_TENSOR = 1, DA_SCALE_ROW = 2, DA_SCAL
 
 typedef struct {
   int n;                    /* 1 to DECODE_ATTN_NORM_MAX (else UNSUPPORTED) */
-  float eps;                /* finite, >= 0 (0: a row of zeros gives NaN) */
+  float eps;                /* finite, >= 0 (0: a row of zeros gives NaN; fp32 and bf16 below 2^-80: slower) */
   float weight_offset;      /* finite; 1 for weights stored as their distance from 1 */
 } da_norm_config;
 

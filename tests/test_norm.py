@@ -356,3 +356,34 @@ def test_products_with_the_weight_past_fp32(dtype, rows, heads, n):
             assert ((scales.view(most.shape).double() - most).abs() <= most * (Y_ERR + 2.0 ** -23)).all(), (scaling, group)
         each = (scales if scaling == "tensor" else scales.view(most.shape)[..., None].expand(-1, -1, -1, size).flatten(-2)[..., :n])
         check_codes(codes, each.expand(want.shape), want, (scaling, group))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-36])
+@pytest.mark.parametrize("rows,heads,n", FAR)
+def test_rows_whose_squares_vanish(dtype, eps, rows, heads, n):
+    """Under an eps that does not cover them, rows of small numbers are normed as others are."""
+    x = _make(rows, heads, n, dtype)
+    for i, e in enumerate((0, -60, -76, -100, -126, -135 if dtype == "f32" else -130)):      # (the last ones subnormal)
+        x[i::6] *= 2.0 ** e
+    x[:, :, ::5] *= 2.0 ** -20                          # smaller numbers beside larger ones
+    w = (0.5 + torch.rand(n, generator=torch.Generator().manual_seed(n))).to(TORCH[dtype]).cuda()
+    norm = binding.RMSNorm(n, eps=eps)
+    want, _ = plain(x, w, None, float(torch.tensor(eps)), 0.0)
+    y = norm.apply(x, w)
+    near(y, want, "y")
+    near(norm.apply(x, w, residual=torch.zeros_like(x))[0], want, "with a residual")
+    for scaling, group in (("row", 0), ("group", 64)):
+        codes, scales, _ = norm.quantise(x, w, scaling=scaling, group=group or 128)
+        size = group or n
+        parts = -(-n // size)
+        padded = torch.nn.functional.pad(want, (0, parts * size - n)).unflatten(-1, (parts, size))
+        most = (padded.abs().amax(-1) / 448).clamp(min=2.0 ** -126)
+        off = most * (Y_ERR + 2.0 ** -23) + 2.0 ** -149
+        assert ((scales.view(most.shape).double() - most).abs() <= off).all(), (scaling, group)
+        each = scales.view(most.shape)[..., None].expand(-1, -1, -1, size).flatten(-2)[..., :n]
+        check_codes(codes, each, want, (scaling, group))
+    # a row of zeros has no direction: NaN without eps, as with every other size
+    x[0] = 0
+    assert norm.apply(x, w)[0].isnan().all() == (float(torch.tensor(eps)) == 0)

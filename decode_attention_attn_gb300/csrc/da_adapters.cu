@@ -151,10 +151,10 @@ int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter
   cfg.stream = static_cast<cudaStream_t>(a.cuda_stream);
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  if (tall) return launch_tall(p, c.rank, c.dtype == DA_BF16, sms, a.workspace, cfg, fn);
   void* kargs[1] = {&p};
   const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, kargs);
-  if (e != cudaSuccess) return cuda_fail(e, "launching the adapter kernel");
-  return tall ? launch_tall(p, c.rank, c.dtype == DA_BF16, sms, a.workspace, cfg.stream) : DA_OK;
+  return e == cudaSuccess ? DA_OK : cuda_fail(e, "launching the adapter kernel");
 }
 
 int decode_attn_adapters_workspace(const da_adapter_config* config, int rows, size_t* bytes) {

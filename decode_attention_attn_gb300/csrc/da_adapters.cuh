@@ -63,7 +63,9 @@ struct TallParams {
 long long most_tall_tiles(const AdapterParams& p);
 bool tall_fits(const AdapterParams& p, int rank, int sms);
 size_t tall_workspace(int rows, int low);
-int launch_tall(const AdapterParams& p, int rank, bool bf16, int sms, void* workspace, cudaStream_t stream);
+// The three launches, the short kernel's (`first` of `fn`) ahead.
+int launch_tall(const AdapterParams& p, int rank, bool bf16, int sms, void* workspace, const cudaLaunchConfig_t& first,
+                const void* fn);
 
 // Bytes of dynamic shared memory: the partial sums of every group of warps (where the counts of rows lay before),
 // the sums over the cluster, and them as operands.

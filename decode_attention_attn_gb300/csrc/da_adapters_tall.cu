@@ -615,7 +615,8 @@ size_t tall_workspace(int rows, int low) {
   return kTallStatusBytes + (size_t)kTallPieces * low * rows * sizeof(float);
 }
 
-int launch_tall(const AdapterParams& p, int rank, bool bf16, int sms, void* workspace, cudaStream_t stream) {
+int launch_tall(const AdapterParams& p, int rank, bool bf16, int sms, void* workspace, const cudaLaunchConfig_t& first,
+                const void* fn) {
   const int low = p.parts * rank, columns = p.starts[p.parts];
   TallParams q = {};
   q.rank = rank;
@@ -652,6 +653,11 @@ int launch_tall(const AdapterParams& p, int rank, bool bf16, int sms, void* work
   if (rc != DA_OK) return rc;
   q.most_tiles = (int)most_tall_tiles(p);
   AdapterParams pp = p;
+  // (nothing is enqueued before all that can fail has been prepared)
+  void* fargs[1] = {&pp};
+  const cudaError_t e = cudaLaunchKernelExC(&first, fn, fargs);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the adapter kernel");
+  const cudaStream_t stream = first.stream;
   void* cargs[4] = {&pp, &q, &tmx, &tma};
   rc = launch_with(contract, sms, kContractThreads, contract_smem, true, stream, cargs);
   if (rc != DA_OK) return rc;

@@ -1368,8 +1368,8 @@ class Adapters(_Workspace):
 
     Long steps for which it pays take a workspace for their low-rank sums, from the allocator for each call. With
     findings=True the object keeps one, whose findings check_status() reports; two such calls must not overlap on
-    the GPU, and a captured graph needs the object (and the longest step made ahead of it) as long as it is
-    replayed."""
+    the GPU. A captured graph needs the object as long as it is replayed, and a step as long as its own made ahead of
+    the capture; a longer one later leaves it what it has."""
 
     LONG = 1024   # rows from which a step may use a workspace
 
@@ -1389,7 +1389,7 @@ class Adapters(_Workspace):
                                         (ctypes.c_int * ADAPTER_PARTS)(*out_sizes), rank)
         self._at = ctypes.addressof(self.config)
         self._one = (len(out_sizes) * rank * width, self.columns * rank)
-        self._findings, self.workspace_bytes = findings, 0
+        self._findings, self.workspace_bytes, self._outgrown = findings, 0, []
 
     def _rows(self, name, t, n):
         if t.dtype is not self.dtype or len(t.shape) != 2 or t.shape[1] != n:
@@ -1443,8 +1443,9 @@ class Adapters(_Workspace):
                 size = decode_attn_adapters_workspace(self.config, rows)
                 if size and self._findings:
                     if size > self.workspace_bytes:
-                        if self.workspace is not None:
-                            self.check_status(stream)      # (its findings are not lost with it)
+                        if self.workspace is not None:     # graphs may hold its address: kept, and twice as large
+                            self._outgrown.append(self.workspace)      # from then on, so that they stay few
+                            size = max(size, 2 * self.workspace_bytes)
                         self._make_workspace(size, x.device)
                         self.workspace_bytes = size
                     if self.workspace.get_device() != index:
@@ -1462,7 +1463,7 @@ class Adapters(_Workspace):
         """Synchronise, then raise the finding recorded since the last call, if there is one."""
         if not self._findings:
             raise ValueError("made without findings")
-        if self.workspace is not None:
-            with _torch.cuda.device(self.workspace.device):
+        for ws in self._outgrown + ([self.workspace] if self.workspace is not None else []):
+            with _torch.cuda.device(ws.device):
                 s = stream if stream is not None else _torch.cuda.current_stream()
-                decode_attn_adapters_check_status(self._workspace_on(self.workspace.get_device(), s), s.cuda_stream)
+                decode_attn_adapters_check_status(ws.data_ptr(), s.cuda_stream)

@@ -1,4 +1,6 @@
 """Low-rank adapters of many requests: refusals on the CPU, results on the GPU against plain float64 forms."""
+import weakref
+
 import pytest
 import torch
 
@@ -549,3 +551,31 @@ def test_an_infinite_low_rank_number_beside_large_ones(dtype, long):
     want, bound = s.want()
     assert torch.equal(want[:n].float(), got[:n].float())
     assert ((got.double() - want).abs() <= bound)[n:].all()
+
+
+@pytest.mark.gpu
+def test_a_captured_step_keeps_its_workspace_when_longer_ones_come():
+    """Findings are kept of each; what the allocator gives out later is not the graph's."""
+    s = Step([1200, 1400, 90], [1, 0, 1], 4096, [2048] * 4, 64, 2, "bf16")
+    kept = binding.Adapters(4096, [2048] * 4, 64, findings=True)
+    first = Step([1200, 90], [1, 0], 4096, [2048] * 4, 64, 2, "bf16")
+    call = lambda t, **kw: kept.apply(t.x, t.y, t.a, t.b, t.scales, t.offsets, t.ids, **kw)
+    first.check(call(first))
+    held = torch.zeros_like(first.y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(first, out=held)
+    ws = weakref.ref(kept.workspace)
+    size = kept.workspace_bytes
+    s.check(call(s))
+    assert ws() is not None and kept.workspace is not ws() and kept.workspace_bytes >= 2 * size
+    others = [torch.full((size,), 0x55, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    graph.replay()
+    first.check(held)
+    assert all((o == 0x55).all() for o in others)
+    kept.check_status()
+    ws()[:4] = torch.tensor([4, 0, 0, 0], dtype=torch.uint8)        # (what a wait that ran out leaves)
+    with pytest.raises(binding.DecodeAttnError) as e:
+        kept.check_status()
+    assert e.value.code == -6
+    kept.check_status()

@@ -78,7 +78,9 @@ int decode_attn_adapters_apply(const da_adapter_config* config, const da_adapter
     const RowRuns ws = flat(a.workspace, (long long)a.workspace_bytes);
     if (may_share(ws, out) || may_share(ws, x) || may_share(ws, y) ||
         may_share(ws, flat(a.a, (long long)a.adapters * low * c.width * es)) ||
-        may_share(ws, flat(a.b, (long long)a.adapters * columns * c.rank * es)))
+        may_share(ws, flat(a.b, (long long)a.adapters * columns * c.rank * es)) ||
+        (a.scales && may_share(ws, flat(a.scales, 4ll * a.adapters))) ||
+        may_share(ws, flat(a.row_offsets, 4ll * (a.batch + 1))) || may_share(ws, flat(a.adapter_ids, 4ll * a.batch)))
       return DA_ERR_INVALID_ARG;
   }
   p.x = a.x;

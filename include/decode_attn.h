@@ -793,10 +793,10 @@ typedef struct {
  *   scales        nullable device float [adapters] (null: 1).
  *   row_offsets, adapter_ids   device int32 [batch + 1] and [batch].
  *   workspace     nullable device memory, 256-byte aligned, of decode_attn_adapters_workspace bytes, which lies
- *                 apart from everything else: 16-bit steps of 1024 rows and more then take requests of 64 rows
- *                 and more in two further launches on the tensor cores (tcgen05). Its first word takes
- *                 DEVICE_TIMEOUT, cleared by the caller ahead of the first call; the rest need not be. Two calls
- *                 that can overlap on the GPU need workspaces of their own.
+ *                 apart from everything else (else INVALID_ARG): 16-bit steps of 1024 rows and more then take
+ *                 requests of 64 rows and more in two further launches on the tensor cores (tcgen05). Its first
+ *                 word takes DEVICE_TIMEOUT, cleared by the caller ahead of the first call; the rest need not be.
+ *                 Two calls that can overlap on the GPU need workspaces of their own.
  * Rows of no request are left as they were. Results do not depend on the order of execution. Rows and parts of
  * 16-byte multiples on 16-byte boundaries move 16 bytes a lane, others 8, 4 or an element. Enqueued on
  * cuda_stream. Errors: INVALID_ARG, WORKSPACE_TOO_SMALL, UNSUPPORTED (dtype, rank, parts, sizes; more than

@@ -579,3 +579,14 @@ def test_a_captured_step_keeps_its_workspace_when_longer_ones_come():
         kept.check_status()
     assert e.value.code == -6
     kept.check_status()
+
+
+def test_a_workspace_over_other_arguments_is_refused():
+    P = 1 << 24
+    config = binding.da_adapter_config(2, 256, 2, (binding.ctypes.c_int * 4)(128, 64, 0, 0), 16)
+    for i in range(8):     # x, y, out, a, b, scales, row_offsets, adapter_ids
+        args = binding.da_adapter_args(A, A + P, A + 2 * P, A + 3 * P, A + 4 * P, A + 5 * P, A + 6 * P, A + 7 * P, 2000, 4, 3,
+                                       256, 192, 192, A + i * P, 1 << 20, None)
+        with pytest.raises(binding.DecodeAttnError) as e:
+            binding.decode_attn_adapters_apply(config, args)
+        assert e.value.code == -1, i

@@ -14,7 +14,7 @@ namespace {
 constexpr int kTallStep = 1024;
 
 // Whether they are worth it. The short kernel takes, in effect, x, y and out at 4 TB/s and an adapter's weights once
-// for 16 rows at 12 (they come from L2); the tall ones x, y and out at 4.8, with 11 us more of launches and first
+// for 16 rows at 12 (they come from L2); the tall ones x, y and out at 4.6, with 11 us more of launches and first
 // operands (rank 64: 17, as the products weigh; rank 128: 47, as its operands fill the registers). bf16, 4096 wide,
 // short and tall in us: to 6144 columns, 8000 rows of rank 64 183 and 83, of rank 16 95 and 71, 2000 rows 50 and 36, 24
 // and 26; to 4096 columns, 2000 rows of rank 64 23 and 27, 3200 of rank 128 71 and 81, 8000 147 and 102.

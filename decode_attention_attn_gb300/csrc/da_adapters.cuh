@@ -142,7 +142,7 @@ __device__ __forceinline__ bool any_not_finite(const float (*c)[4]) {
     for (int e = 0; e < 4; ++e) z = fmaf(c[j][e], 0.f, z);
   return __any_sync(0xffffffffu, z != 0.f);
 }
-// Two fp32 numbers as two pairs of T: what is left is 2^-18 (bf16) or 2^-24 (f16) of them.
+// Two fp32 numbers as two pairs of T: what is left is at most 2^-17 (bf16) or 2^-23 (f16) of them.
 template <typename T>
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = pack2(x, y, T());

@@ -4,9 +4,9 @@
 //   contract   low[r] = x[r] A_a^T: tcgen05.mma 128 x (parts * rank) x 64, x and A by TMA into a ring, an even run of
 //              the tiles' widths a CTA; its fp32 sums into the workspace.
 //   expand     out[r, c..c+127] = y + c_a low[r] B_a^T: the CTAs' sums as 16-bit operands in tensor memory (two
-//              parts, so that nothing of fp32's order is lost), B and y by TMA. A CTA walks a run of column blocks,
-//              tile by tile: one warp loads, one issues, four put the next rows' operand together, and two teams of
-//              four finish blocks in turn (a thread a row) and write them row by row.
+//              parts: at most 2^-17 of a number is lost in bf16, 2^-23 in f16), B and y by TMA. A CTA walks a run
+//              of column blocks, tile by tile: one warp loads, one issues, four put the next rows' operand together,
+//              and two teams of four finish blocks in turn (a thread a row) and write them row by row.
 //
 // Bound by HBM: x is read once, y once, out written once (the weights and the low-rank sums stay in L2). 8800 rows
 // in 16 prompts, 4096 to 6144 columns, rank 64: the bytes are 47 us at a copy's rate.
@@ -489,10 +489,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 #pragma unroll
       for (int k = 0; k < R / 2; ++k) split_pair<T>(v[2 * k], v[2 * k + 1], o[k], o[RB / 2 + k]);
       wait(&sh.v_empty[vb], vpar ^ 1);
-      // The scale's place was segment seg - 4's, and is free only now: seg - 2's products are done, the last of them two
-      // blocks or more behind seg - 4's last one, and a block's product waits (d_empty) until the block two before it
-      // has been finished. Before the wait seg - 3's alone are known to be, which may be a single block, with seg - 4's
-      // last one still waiting for its y.
+      // The scale's place was segment seg - 4's, and is free only now: seg - 2's products are done, the last of them
+      // two blocks or more behind seg - 4's last one, and a block's product waits (d_empty) until the block two before
+      // it has been finished. Before the wait seg - 3's alone are known to be, which may be a single block, with
+      // seg - 4's last one still waiting for its y.
       if constexpr (std::is_same<T, __half>::value) sh.scale[w.seg & 3][row] = s;
       tc_fence_after();
 #pragma unroll

@@ -168,8 +168,8 @@ int decode_attn_norm_apply(const da_norm_config* config, const da_norm_args* arg
     block = true;
     const int warps = vec || shifted ? (units + 31) / 32 : units;   // at a unit a thread
     // kWide, many rows: two units a thread from 4 warps on, as that has more on its way for the registers (8192 rows
-    // of 4096 bf16 with residual and groups: 58 us with one, 44 with two; 620 rows 7.5 and 5.9). kScattered: one as
-    // long as a block holds it (4000 rows of 4107 bf16 with residual and groups: 75 us with one, 179 with two).
+    // of 4096 bf16 with residual and groups: 56 us with one, 44 with two; 620 rows 7.3 and 5.5). kScattered: one as
+    // long as a block holds it (4000 rows of 4107 bf16 with residual and groups: 59 us with one, 181 with two).
     const int ones = vec ? (items >= 4ll * sms ? 3 : 8) : shifted ? 8 : 16;
     items_each = warps <= ones ? 1 : warps <= 32 ? 2 : warps <= 64 ? 4 : 8;
     threads = 32 * ((warps + items_each - 1) / items_each);

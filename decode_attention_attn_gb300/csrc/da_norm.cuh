@@ -5,8 +5,10 @@
 // scale given, or max |y| / 448 over the row or over groups of 32, 64 or 128 elements.
 //
 // Bound by HBM: every element is read once and written once, about 10 operations between. A row stays in registers
-// from the loads to the stores; what the row's threads exchange is one sum and one maximum, together. The maximum
-// needs no second pass over y: rounding is monotone, so max |y| = round(max |h (w + o)| r) with y = round(h (w + o) r).
+// from the loads to the stores (past 16384 elements not all of it: kWide with a residual spills 0.5 KB a thread in 16
+// bits and 1.4 KB in fp32, kShifted 0.8 and 2.3); what the row's threads exchange is one sum and one maximum,
+// together. The maximum needs no second pass over y: rounding is monotone, so max |y| = round(max |h (w + o)| r) with
+// y = round(h (w + o) r).
 #pragma once
 
 #include <cstring>
@@ -224,16 +226,16 @@ __device__ __forceinline__ float over_row(float v, int lanes, float* s_part) {
 // kShifted  the same for rows of any width that begin anywhere, but all tensors' alike (one block a row): units lie on
 //           16-byte boundaries, so a row begins and ends inside one, whose elements are moved one by one. Rows that are
 //           a multiple of 8 (fp32: 4) apart begin alike, so a block keeps to such rows, with its weights in registers.
-//           (2002 rows of 5119 bf16 to 8 bits: 104 us element by element, 33 so; 1001 of fp32 23 and 20.)
+//           (2002 rows of 5119 bf16 to 8 bits: 34 us element by element, 30 so; 1001 of fp32 19 both ways.)
 // kScattered a warp holds 32 E elements, a lane every 32nd of them, so that each load of a warp is of neighbours.
 // A group's elements are in one warp: in kWide, neighbouring lanes' units; in kScattered, group / 32 of each lane's
 // elements; kShifted has none.
 enum NormLayout { kScattered = 0, kWide = 1, kShifted = 2 };
 
 // Registers of a block's thread: 128; with a residual and at most two units 96 (by 640 threads), for 5 blocks an SM of
-// 4 warps in place of 4 (8192 rows of bf16 with groups: width 4096 48 to 44 us, 6144 82 to 67, 8192 alike; without
-// groups 4096 alike, 6144 64 to 68). kScattered with one unit 64, for two blocks an SM or more, as it loads nothing
-// ahead (4000 rows of 4107 bf16 with residual and groups: 159 to 75 us).
+// 4 warps in place of 4 (8192 rows of bf16 with groups: width 4096 47 to 44 us, 6144 80 to 65, 8192 alike; without
+// groups alike). kScattered with one unit 64, for two blocks an SM or more, as it loads nothing ahead (4000 rows of
+// 4107 bf16 with residual and groups: 147 to 59 us).
 template <int ITEMS, int LAYOUT, bool BLOCK, bool RES>
 constexpr int kMostThreads = !BLOCK ? 128 : LAYOUT == kWide && RES && ITEMS <= 2 ? 640 : 512;
 
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kMostThreads<ITEMS, LAYOUT, BLOCK, RES>,
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) most = most_of(most, h[i][e]);
     }
-    // the row's sum and maximum, in an order that the width alone sets
+    // the row's sum and maximum, in an order that goes by the threads a row has (its width, and whether rows are many)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       if (!BLOCK && o >= lanes) continue;

@@ -769,8 +769,10 @@ int decode_attn_norm_apply(const da_norm_config* config, const da_norm_args* arg
  *     out[r, part s] = y[r, part s] + scales[a] (x[r] A_{a,s}^T) B_{a,s}^T,
  * A_{a,s} [rank, width], B_{a,s} [out_sizes[s], rank]. A request whose id lies outside [0, adapters) (-1 by
  * convention) has none: out = y. An adapter of a smaller rank has zeros in the rest.
- * Products are exact to fp32's order and sums are fp32: the low-rank numbers are not rounded to the type in
- * between; out is rounded once. */
+ * Sums are fp32, and the low-rank numbers x A^T are not rounded to the type in between: they enter the second
+ * product as two parts, which keep all but 2^-17 (bf16) or 2^-23 (f16, and 2^-32 of the row's largest) of them. fp32
+ * products are formed of two tf32 parts of each factor, within 2^-20. out is rounded once. An infinite number gives
+ * what the formula gives, but that one of b in 16 bits may come out as NaN. */
 
 #define DECODE_ATTN_ADAPTER_PARTS 4
 #define DECODE_ATTN_ADAPTER_MAX_WIDTH (1 << 20)
@@ -822,7 +824,8 @@ typedef struct {
 } da_adapter_args;
 
 /* The workspace with which a call over `rows` rows is fastest (0: without one; the size depends on rows, parts and rank
- * alone, whether there is one on the widths too). Host only. Errors: INVALID_ARG. */
+ * alone, whether there is one on the widths too: none for fp32, for few rows or weights, nor where parts * rank passes
+ * 256). Host only. Errors: INVALID_ARG. */
 int decode_attn_adapters_workspace(const da_adapter_config* config, int rows, size_t* bytes);
 
 /* Synchronise `stream`, then read and clear the finding that calls with this workspace left in its first word:

@@ -1369,7 +1369,7 @@ class Adapters(_Workspace):
     Long steps for which it pays take a workspace for their low-rank sums, from the allocator for each call. With
     findings=True the object keeps one, whose findings check_status() reports; two such calls must not overlap on
     the GPU. A captured graph needs the object as long as it is replayed, and a step as long as its own made ahead of
-    the capture; a longer one later leaves it what it has."""
+    the capture (a ValueError without); a longer one later leaves it what it has."""
 
     LONG = 1024   # rows from which a step may use a workspace
 
@@ -1443,6 +1443,10 @@ class Adapters(_Workspace):
                 size = decode_attn_adapters_workspace(self.config, rows)
                 if size and self._findings:
                     if size > self.workspace_bytes:
+                        with _torch.cuda.stream(stream):
+                            if _torch.cuda.is_current_stream_capturing():
+                                raise ValueError("a captured step needs one as long made ahead of the capture: its "
+                                                 "workspace would be cleared by each replay, and by nothing before")
                         if self.workspace is not None:     # graphs may hold its address: kept, and twice as large
                             self._outgrown.append(self.workspace)      # from then on, so that they stay few
                             size = max(size, 2 * self.workspace_bytes)

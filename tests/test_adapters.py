@@ -590,3 +590,25 @@ def test_a_workspace_over_other_arguments_is_refused():
         with pytest.raises(binding.DecodeAttnError) as e:
             binding.decode_attn_adapters_apply(config, args)
         assert e.value.code == -1, i
+
+
+@pytest.mark.gpu
+def test_a_workspace_is_not_made_inside_a_capture():
+    s = Step([1200, 90], [1, 0], 4096, [2048] * 4, 64, 2, "bf16")
+    kept = binding.Adapters(4096, [2048] * 4, 64, findings=True)
+    call = lambda **kw: kept.apply(s.x, s.y, s.a, s.b, s.scales, s.offsets, s.ids, **kw)
+    held, side = torch.zeros_like(s.y), torch.cuda.Stream()
+    for kw in ({}, {"stream": side}):
+        graph = torch.cuda.CUDAGraph()
+        with pytest.raises(ValueError, match="capture"):
+            with torch.cuda.graph(graph, **kw):
+                held.zero_()
+                call(out=held, **kw)
+        assert kept.workspace is None
+    s.check(call())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out=held)
+    graph.replay()
+    s.check(held)
+    kept.check_status()
